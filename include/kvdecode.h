@@ -24,7 +24,7 @@
  *    too small). KVD_ERR_CUDA reports a launch failure (cudaGetLastError).
  *  - Device errors: conditions only visible on the device (a length past the
  *    capacity, a parent outside its window, a draft id outside the vocabulary, a
- *    NaN logit) are written to `*dev_err` with an atomic compare-and-swap from 0, so
+ *    NaN logit, a sampling parameter out of range) are written to `*dev_err` with an atomic compare-and-swap from 0, so
  *    the first code wins; the offending unit of work is skipped, nothing traps and
  *    nothing spins. `dev_err` (device int32) may be NULL to ignore them. The caller
  *    reads and clears it when it chooses.
@@ -79,8 +79,9 @@ typedef enum kvd_status {
     KVD_ERR_BAD_INDEX = 17,    /* a beam parent outside its window's block */
     KVD_ERR_BAD_TOKEN = 18,    /* a draft id outside [0, vocab) */
     KVD_ERR_NAN = 19,          /* a NaN among the logits */
-    KVD_ERR_TIMEOUT = 20       /* a bounded wait for a shared-memory copy gave up; the
+    KVD_ERR_TIMEOUT = 20,      /* a bounded wait for a shared-memory copy gave up; the
                                   workspace counters may be left non-zero: re-zero them */
+    KVD_ERR_BAD_PARAM = 21     /* a per-row sampling parameter out of range */
 } kvd_status;
 
 typedef enum kvd_dtype { KVD_F16 = 0, KVD_BF16 = 1 } kvd_dtype;
@@ -89,7 +90,9 @@ typedef enum kvd_op {
     KVD_OP_DECODE_ATTN = 0,
     KVD_OP_VERIFY_ATTN = 1,
     KVD_OP_GREEDY_ACCEPT = 2,
-    KVD_OP_SAMPLE_ACCEPT = 3
+    KVD_OP_SAMPLE_ACCEPT = 3,
+    KVD_OP_WINDOW_ATTN = 4,
+    KVD_OP_Q4_ATTN = 5
 } kvd_op;
 
 enum {
@@ -350,6 +353,174 @@ kvd_status kvd_rope(kvd_dtype dtype, int32_t batch, int32_t n, void *q, int32_t 
                     void *k, int32_t n_k_heads, const int32_t *pos0, float base, uint32_t flags,
                     int32_t *dev_err, kvd_stream_t stream);
 
+/* One tensor of head rows for kvd_qk_norm_rope: where its rows are read and written. */
+typedef struct kvd_head_rows {
+    const void *x;      /* device, rows of 64 values; row (b, h, j) starts at          */
+                        /* x + b*stride_b + h*stride_h + j*stride_t elements           */
+    int64_t stride_b;   /* strides in elements, >= 0 and multiples of 8: a view of a   */
+    int64_t stride_h;   /* fused projection [batch, n, heads, 64] is read where it is  */
+    int64_t stride_t;
+    const void *weight; /* device [64] of the call's type, or NULL (ones)              */
+    void *out;          /* device [batch, n_heads, n, 64], contiguous                  */
+    int32_t n_heads;
+} kvd_head_rows;
+
+/*
+ * kvd_qk_norm_rope -- RMS norm of every query and key head, then the rotation, one pass.
+ *
+ * No counterpart on the pages: models that normalise queries and keys per head do this
+ * between the QKV projection and kvd_decode_attn / kvd_prefill_attn / kvd_q4_append.
+ *
+ *   y = x * weight / sqrt(sum(x^2)/64 + eps), rotated (kvd_rope's pairs and angles) at
+ *   position pos0[b] + j; fp32 arithmetic, one rounding to the storage type
+ *
+ * q, k  : either may be NULL. All pointers 16-byte aligned. out may equal x when x has
+ *         out's layout (in place); otherwise they must not overlap, and neither tensor's
+ *         output may overlap the other's input.
+ * pos0  : device int32 [batch] or NULL (0); any value. base 0: norm only, no rotation.
+ *         The angle is exact modulo a turn (64-bit fixed point) at every position, where
+ *         kvd_rope forms it in fp32: at far positions the two differ by kvd_rope's
+ *         rounding of the angle, so encode all keys of a cache with the same one.
+ * eps >= 0 and finite; eps 0 makes a row of zeros NaN. No device errors; dev_err is
+ * accepted for symmetry.
+ */
+kvd_status kvd_qk_norm_rope(kvd_dtype dtype, int32_t batch, int32_t n, const kvd_head_rows *q,
+                            const kvd_head_rows *k, const int32_t *pos0, float eps, float base,
+                            uint32_t flags, int32_t *dev_err, kvd_stream_t stream);
+
+/*
+ * kvd_window_attn -- qlen query tokens per row over the cache, through a sliding window
+ * with sinks.
+ *
+ * No counterpart on the pages: layers that see only the last `window` positions, and the
+ * first `n_sinks` ones, which stay visible. With the block appended first (kvd_kv_append,
+ * or `append`), query i sits at position p_i = len - qlen + i and sees
+ *   t <= p_i  with  t < n_sinks or t > p_i - window
+ * Everything else is kvd_decode_attn (qlen 1) and kvd_verify_attn with causal = 1: arguments,
+ * fused append, workspace (KVD_OP_WINDOW_ATTN), flags, errors; rows_per_kv is 1. Only the
+ * 64-position tiles some query of the block sees are read, and what lies elsewhere in the
+ * cache, infinities and NaN included, does not reach a query that does not see it.
+ *
+ * 1 <= qlen <= KVD_MAX_QLEN; window >= 1; n_sinks >= 0.
+ */
+kvd_status kvd_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads, int32_t qlen,
+                           const void *q, const kvd_cache *kv, const int32_t *lens,
+                           int32_t fixed_len, const kvd_new_tokens *append, int32_t window,
+                           int32_t n_sinks, float scale, void *out, void *workspace,
+                           size_t workspace_bytes, uint32_t flags, int32_t *dev_err,
+                           kvd_stream_t stream);
+
+/*
+ * kvd_prefill_window_attn -- kvd_prefill_attn through a sliding window with sinks.
+ *
+ * Prompt token j, at position p = lens_in[b] + j, sees t <= p with t < n_sinks or
+ * t > p - window; everything else is kvd_prefill_attn. window >= 1; n_sinks >= 0.
+ * Cached positions that no token of the prompt sees do not reach the outputs, whatever
+ * they hold.
+ */
+kvd_status kvd_prefill_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads,
+                                   int32_t max_len, const void *q, const kvd_cache *kv,
+                                   const void *k_new, const void *v_new, const int32_t *lens_in,
+                                   const int32_t *plens, int32_t *lens_out, int32_t window,
+                                   int32_t n_sinks, float scale, float rope_base, void *out,
+                                   uint32_t flags, int32_t *dev_err, kvd_stream_t stream);
+
+/*
+ * A layer's cache held in 4 bits.
+ *
+ * No counterpart on the pages: 72 bytes per position and head instead of the 16-bit cache's
+ * 256, for long contexts. A row is the 64 values of one head at one position. It is stored as
+ *   32 bytes: byte j holds dims 2j (low 4 bits) and 2j+1 (high 4 bits), n in 0..15;
+ *   a step (bfloat16) and a zero point z (binary16): the row's values are step * (n - z).
+ * With the row's least and greatest value lo and hi, every operation rounded to fp32:
+ *   step = bf16((hi/2 - lo/2) / 7.5),  z = f16(-lo / step),
+ *   n    = clamp(rint(x / step + z), 0, 15)      (rint: ties to even)
+ * A row whose step comes out 0 (equal values) has step = bf16(|lo| / 15) (1 when that is 0)
+ * and z = 0, or 15 for lo < 0. A value is off by at most half a step, more at the row's ends
+ * by what rounding the step and the zero point moved the grid (at most 15 * 2^-9 + |z| *
+ * 2^-11 steps). A row with an infinity or a NaN is stored as n = 0, step = NaN, z = 0: it
+ * reads back as NaN. Steps are >= 0.
+ */
+typedef struct kvd_q4_cache {
+    void *k;            /* device, 32 bytes per row, 16-byte aligned                  */
+    void *v;            /* the same layout                                            */
+    void *params;       /* device, 8 bytes per row of K and V: step of K, zero point  */
+                        /* of K, step of V, zero point of V; 8-byte aligned           */
+    int64_t stride_b;   /* rows between consecutive batch rows                        */
+    int64_t stride_h;   /* rows between consecutive heads; positions are consecutive  */
+    int32_t batch;
+    int32_t n_kv_heads;
+    int32_t head_dim;   /* must be 64                                                 */
+    int32_t capacity;   /* positions allocated per (batch row, head), <= 2^30         */
+} kvd_q4_cache;
+
+/*
+ * kvd_q4_append -- quantise new tokens' K/V and write them into a 4-bit cache.
+ *
+ * As kvd_kv_append, into a kvd_q4_cache; with `counts`, row b appends its first counts[b]
+ * tokens only (a ragged prompt):
+ *   row (b, h, lens_in[b] + j) = quantised k_new[b, h, j], v_new[b, h, j]   j < counts[b]
+ *   lens_out[b] = lens_in[b] + counts[b]
+ *
+ * k_new, v_new : device [batch, n_kv_heads, q, 64], contiguous, 16-byte aligned
+ * lens_in : device int32 [batch] or NULL (every row starts empty)
+ * counts  : device int32 [batch] in [0, q], or NULL (q for every row)
+ * lens_out: device int32 [batch] or NULL; must not alias lens_in or counts
+ * Device errors: lens_in + counts outside [0, capacity] or counts outside [0, q] ->
+ * KVD_ERR_LEN_OVERFLOW (row b not written, lens_out[b] = lens_in[b]); an infinity or a NaN
+ * -> KVD_ERR_NAN (its 64 values are stored as NaN).
+ */
+kvd_status kvd_q4_append(kvd_dtype dtype, const kvd_q4_cache *cache, int32_t batch, int32_t q,
+                         const void *k_new, const void *v_new, const int32_t *lens_in,
+                         const int32_t *counts, int32_t *lens_out, uint32_t flags,
+                         int32_t *dev_err, kvd_stream_t stream);
+
+/*
+ * kvd_q4_dequant -- read rows of a 4-bit cache back into 16 bits.
+ *
+ *   k_out[b, h, j] = K row (b, h, pos0[b] + j), the same for V, j < n
+ * (for a chunked prefill over a cached prefix, which runs on a 16-bit cache). The values
+ * step * (n - z) are formed in fp32 and rounded to `dtype`.
+ *
+ * k_out, v_out : device [batch, n_kv_heads, n, 64], contiguous, 16-byte aligned; either
+ *                may be NULL
+ * pos0 : device int32 [batch] or NULL (0)
+ * Device error: pos0[b] < 0 or pos0[b] + n > capacity -> KVD_ERR_LEN_OVERFLOW, row b's
+ * outputs are not written.
+ */
+kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache *cache, int32_t batch, int32_t n,
+                          void *k_out, void *v_out, const int32_t *pos0, uint32_t flags,
+                          int32_t *dev_err, kvd_stream_t stream);
+
+/*
+ * kvd_q4_attn -- qlen query tokens per row attend over a 4-bit cache.
+ *
+ * The block's K/V are already appended (kvd_q4_append), so query i sits at position
+ * p_i = len - qlen + i, len = lens ? lens[b] : fixed_len, and sees
+ *   causal != 0, window == 0:  t <= p_i
+ *   causal != 0, window > 0 :  t <= p_i with t < n_sinks or t > p_i - window
+ *   causal == 0            :  t < len (window must be 0: cross-attention)
+ *   out[b,hq,i,:] = sum_t softmax_t(scale * q[b,hq,i] . K[b,h,t]) V[b,h,t] over those t,
+ *   h = hq / (n_q_heads / cache->n_kv_heads); a query that sees nothing gets zeros
+ *
+ * q, out : device [batch, n_q_heads, qlen, 64], contiguous, 16-byte aligned; 1 <= qlen <=
+ *          KVD_MAX_QLEN; batch <= cache->batch
+ * window, n_sinks >= 0; n_sinks is ignored without a window
+ * workspace : kvd_workspace_size(KVD_OP_Q4_ATTN, batch, n_q_heads, n_kv_heads, 1, qlen,
+ *          max_len) bytes with max_len = the capacity (or fixed_len); used only by few long
+ *          rows, under the rules of the other attention calls
+ * Products run on the tensor cores with fp32 accumulation; the softmax is fp32.
+ * Flags: KVD_FLAG_PDL; KVD_FLAG_EARLY_KV gives what KVD_FLAG_PDL gives (nothing is read
+ * before the wait).
+ * Device error: len < 0 or len > capacity -> KVD_ERR_LEN_OVERFLOW, the row's output is
+ * left as is.
+ */
+kvd_status kvd_q4_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads, int32_t qlen,
+                       const void *q, const kvd_q4_cache *cache, const int32_t *lens,
+                       int32_t fixed_len, int32_t causal, int32_t window, int32_t n_sinks,
+                       float scale, void *out, void *workspace, size_t workspace_bytes,
+                       uint32_t flags, int32_t *dev_err, kvd_stream_t stream);
+
 /*
  * kvd_greedy_accept -- greedy verification of k draft tokens.
  *
@@ -416,6 +587,43 @@ kvd_status kvd_sample_accept(const float *target, const float *draft, const int3
                              const float *r, const float *u, int32_t *n_accepted,
                              int32_t *next_token, void *workspace, size_t workspace_bytes,
                              uint32_t flags, int32_t *dev_err, kvd_stream_t stream);
+
+/*
+ * kvd_sample_filtered -- draw one token per row after temperature, top-k, top-p and min-p.
+ *
+ * Beside kvd_sample_accept's plain temperature sampling ([W] "Inference 抽象と KV キャッシュ":
+ * Categorical(logits / T)); the filters have no counterpart on the pages. Every row (a
+ * request) has its own values. The ids of a row are ordered by logit, ties lower id first;
+ * with w_t = exp((x_t - max x) / T) the row keeps the longest prefix of that order that
+ *   1. has at most top_k ids                                       (top_k <= 0: all)
+ *   2. ends at the latest with the id at which the prefix's mass reaches top_p times the
+ *      mass of what step 1 left                                    (top_p >= 1: all)
+ *   3. has w_t >= min_p for every id                               (min_p <= 0: all)
+ * and at least one id. Ids with logit -inf are never kept. Then, over the kept ids,
+ *   token   = the smallest id whose running sum of w, in id order, exceeds u * sum(w)
+ *             (the last kept id with w > 0 if rounding leaves none)
+ *   logprob = log(w_token / sum(w))
+ * T = 0 takes the largest logit (kept: that id). Masses are integers in units of 2^-44 (the
+ * largest w is 1; w is formed to a relative 2^-32): the same bits on every run and batch.
+ *
+ * logits      : device fp32, row r at logits + r * row_stride; vocab <= KVD_MAX_VOCAB;
+ *               row_stride >= vocab. A NaN counts as -inf. With +inf logits those ids alone
+ *               have mass.
+ * temperature, top_p, min_p : device fp32 [batch] or NULL (1, 1, 0)
+ * top_k       : device int32 [batch] or NULL (all)
+ * u           : device fp32 [batch], uniform in [0, 1)
+ * token       : device int32 [batch]; logprob: device fp32 [batch] or NULL; n_kept: device
+ *               int32 [batch] or NULL (how many ids the row kept)
+ * A row without any logit above -inf gets token -1, logprob -inf, n_kept 0.
+ * Device errors: a NaN logit -> KVD_ERR_NAN; T < 0, or a NaN or infinite T, NaN top_p,
+ * NaN min_p or NaN u -> KVD_ERR_BAD_PARAM, the row's outputs are left as they are. No
+ * workspace: one thread-block cluster per row. batch <= 65535.
+ */
+kvd_status kvd_sample_filtered(const float *logits, int64_t row_stride, int32_t batch,
+                               int32_t vocab, const float *temperature, const int32_t *top_k,
+                               const float *top_p, const float *min_p, const float *u,
+                               int32_t *token, float *logprob, int32_t *n_kept, uint32_t flags,
+                               int32_t *dev_err, kvd_stream_t stream);
 
 /*
  * kvd_beam_reorder_kv -- reorder the self-attention caches of all layers.
@@ -494,6 +702,8 @@ kvd_status kvd_beam_select(const float *logits, int32_t windows, int32_t beam, i
  *   KVD_OP_VERIFY_ATTN : the same plus qlen
  *   KVD_OP_GREEDY_ACCEPT: batch, qlen = k, vocab
  *   KVD_OP_SAMPLE_ACCEPT: batch, qlen = k, vocab
+ *   KVD_OP_WINDOW_ATTN : batch, n_q_heads, n_kv_heads, qlen, max_len (rows_per_kv 1)
+ *   KVD_OP_Q4_ATTN     : the same
  * max_len is an upper bound of the attended length (the capacity, or fixed_len).
  * Returns 0 for invalid arguments.
  */

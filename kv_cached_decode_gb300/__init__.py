@@ -10,7 +10,9 @@ Tensors: caches are ``[batch, n_kv_heads, capacity, 64]`` fp16/bf16 CUDA tensors
 the last axis contiguous; queries/outputs are contiguous ``[batch, n_q_heads, qlen, 64]``;
 lengths, drafts, parents and outputs of ``kvd_greedy_accept`` are int32 CUDA tensors;
 logits are contiguous fp32 ``[batch, k+1, vocab]`` (``kvd_greedy_accept``) or
-``[windows*beam, vocab]`` (``kvd_beam_select``).
+``[windows*beam, vocab]`` (``kvd_beam_select``). ``kvd_qk_norm_rope`` reads strided head
+rows and ``kvd_sample_filtered`` strided logit rows. A 4-bit cache is a ``Q4Cache`` over
+``[batch, n_kv_heads, capacity, 32]`` uint8 data and ``[..., 4]`` int16 parameters.
 """
 
 from __future__ import annotations
@@ -28,9 +30,10 @@ KVD_OK = 0
 STATUS_NAMES = {0: "KVD_OK", 1: "KVD_ERR_INVALID_ARG", 2: "KVD_ERR_UNSUPPORTED",
                 3: "KVD_ERR_WORKSPACE", 4: "KVD_ERR_CUDA", 16: "KVD_ERR_LEN_OVERFLOW",
                 17: "KVD_ERR_BAD_INDEX", 18: "KVD_ERR_BAD_TOKEN", 19: "KVD_ERR_NAN",
-                20: "KVD_ERR_TIMEOUT"}
+                20: "KVD_ERR_TIMEOUT", 21: "KVD_ERR_BAD_PARAM"}
 KVD_F16, KVD_BF16 = 0, 1
 KVD_OP_DECODE_ATTN, KVD_OP_VERIFY_ATTN, KVD_OP_GREEDY_ACCEPT, KVD_OP_SAMPLE_ACCEPT = 0, 1, 2, 3
+KVD_OP_WINDOW_ATTN, KVD_OP_Q4_ATTN = 4, 5
 KVD_FLAG_PDL, KVD_FLAG_EARLY_KV = 1, 2
 KVD_FLAG_TEST_STALL = 1 << 8  # test only: see include/kvdecode.h
 KVD_WS_COUNTER_BYTES = 65536
@@ -39,7 +42,9 @@ HEAD_DIM = 64
 EXPORTED = ("kvd_kv_append", "kvd_decode_attn", "kvd_verify_attn", "kvd_greedy_accept",
             "kvd_beam_reorder_kv", "kvd_workspace_size", "kvd_status_string", "kvd_version",
             "kvd_decode_attn_noalloc", "kvd_prefill_attn", "kvd_rope", "kvd_beam_select",
-            "kvd_kv_append_rope", "kvd_sample_accept", "kvd_noalloc_test_fill_counters")
+            "kvd_kv_append_rope", "kvd_sample_accept", "kvd_noalloc_test_fill_counters",
+            "kvd_qk_norm_rope", "kvd_window_attn", "kvd_prefill_window_attn", "kvd_q4_append",
+            "kvd_q4_dequant", "kvd_q4_attn", "kvd_sample_filtered")
 
 
 class KvdError(RuntimeError):
@@ -65,6 +70,24 @@ class NewTokens(ctypes.Structure):
                 ("lens_out", ctypes.c_void_p), ("rope_base", ctypes.c_float)]
 
 
+class HeadRows(ctypes.Structure):
+    """Mirror of ``kvd_head_rows``: one tensor of head rows for ``kvd_qk_norm_rope``."""
+
+    _fields_ = [("x", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("n_heads", ctypes.c_int32)]
+
+
+class Q4Cache(ctypes.Structure):
+    """Mirror of ``kvd_q4_cache``: one layer's K and V held in 4 bits."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("params", ctypes.c_void_p),
+                ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("batch", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -84,6 +107,7 @@ def load_library(path: str = LIB_PATH):
                               ctypes.c_size_t)
         CP = ctypes.POINTER(Cache)
         NP = ctypes.POINTER(NewTokens)
+        QP = ctypes.POINTER(Q4Cache)
         sig = {
             "kvd_kv_append": [I32, CP, I32, I32, P, P, P, P, U32, P, P],
             "kvd_decode_attn": [I32, I32, I32, P, CP, P, I32, NP, I32, F, P, P, SZ, U32, P, P],
@@ -99,6 +123,18 @@ def load_library(path: str = LIB_PATH):
             "kvd_beam_reorder_kv": [I32, CP, I32, I32, I32, P, P, I32, U32, P, P],
             "kvd_beam_select": [P, I32, I32, I32, P, P, I32, P, I32, I32, I32, P, P, P, P, P,
                                 P, P, P, U32, P, P],
+            "kvd_qk_norm_rope": [I32, I32, I32, ctypes.POINTER(HeadRows),
+                                 ctypes.POINTER(HeadRows), P, F, F, U32, P, P],
+            "kvd_window_attn": [I32, I32, I32, I32, P, CP, P, I32, NP, I32, I32, F, P, P, SZ,
+                                U32, P, P],
+            "kvd_prefill_window_attn": [I32, I32, I32, I32, P, CP, P, P, P, P, P, I32, I32, F,
+                                        F, P, U32, P, P],
+            "kvd_q4_append": [I32, QP, I32, I32, P, P, P, P, P, U32, P, P],
+            "kvd_q4_dequant": [I32, QP, I32, I32, P, P, P, U32, P, P],
+            "kvd_q4_attn": [I32, I32, I32, I32, P, QP, P, I32, I32, I32, I32, F, P, P, SZ, U32,
+                            P, P],
+            "kvd_sample_filtered": [P, ctypes.c_int64, I32, I32, P, P, P, P, P, P, P, P, U32,
+                                    P, P],
             "kvd_workspace_size": [I32, I32, I32, I32, I32, I32, I32, I32],
             "kvd_status_string": [I32],
             "kvd_version": [],
@@ -364,3 +400,259 @@ def kvd_sample_accept(target, u, n_accepted, next_token, workspace, temperature:
                                             _dev(workspace, "workspace"), ws_bytes, flags,
                                             _i32(dev_err, "dev_err"), _stream(stream)),
            "kvd_sample_accept")
+
+
+def _at(t, dtype, shape, what, dev):
+    """The address (an int, 0 for None) of a contiguous CUDA tensor of this type and shape on
+    device ``dev``; the argument checks of the calls below."""
+    if t is None:
+        return 0
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current device (cuda:{dev})")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(workspace, dev):
+    if workspace is None:
+        return 0, 0
+    return (_at(workspace, workspace.dtype, None, "workspace", dev),
+            workspace.numel() * workspace.element_size())
+
+
+def _device_of(t, what):
+    """The tensor's device index, which must be the current device: kernels are launched
+    there."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def _on(stream, dev):
+    s = torch.cuda.current_stream() if stream is None else stream
+    if s.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{s.device_index}, the tensors on cuda:{dev}")
+    return s.cuda_stream
+
+
+def _cache_on(cache, dev, dtype=None):
+    """The cache's tensors (kept with the struct) are on the current device and of this
+    type."""
+    for t in getattr(cache, "_tensors", ()):
+        if t.get_device() != dev:
+            raise ValueError(f"cache must be on the current device (cuda:{dev})")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"cache must be {dtype}, got {t.dtype}")
+    return ctypes.byref(cache)
+
+
+def _strides(t):
+    """Element strides of the first three axes of a 4-D tensor; 0 for an axis of size 1 (its
+    stride is arbitrary and never used)."""
+    st, sh = t.stride(), t.shape
+    return tuple(0 if sh[i] == 1 else st[i] for i in range(3))
+
+
+def make_q4_cache(k: torch.Tensor, v: torch.Tensor, params: torch.Tensor) -> Q4Cache:
+    """Describe one layer's 4-bit K/V for the C ABI: ``k`` and ``v`` uint8 ``[batch, heads,
+    capacity, 32]`` (dims 2j and 2j+1 in the low and high half of byte j), ``params`` int16
+    ``[batch, heads, capacity, 4]`` (the bits of K's step and zero point, V's step and zero
+    point). Positions of a head must be consecutive; the three share their layout."""
+    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or params.dtype != torch.int16:
+        raise TypeError("k and v must be uint8, params int16")
+    if (k.dim() != 4 or k.shape[3] != HEAD_DIM // 2 or v.shape != k.shape
+            or tuple(params.shape) != (*k.shape[:3], 4)):
+        raise ValueError("k and v must be [batch, heads, capacity, 32], params [batch, heads, "
+                         "capacity, 4]")
+    if not (k.is_cuda and k.device == v.device == params.device):
+        raise ValueError("cache tensors must be CUDA tensors on one device")
+    rows = []
+    for t in (k, v, params):
+        sb, sh, st = _strides(t)
+        n = t.shape[3]
+        if t.stride(3) != 1 or (t.shape[2] > 1 and st != n) or sb % n or sh % n:
+            raise ValueError("a head's positions must be consecutive rows")
+        rows.append((sb // n, sh // n))
+    if rows[0] != rows[1] or rows[0] != rows[2]:
+        raise ValueError("k, v and params must share their strides")
+    B, H, cap, _ = k.shape
+    c = Q4Cache(k.data_ptr(), v.data_ptr(), params.data_ptr(), rows[0][0], rows[0][1], B, H,
+                HEAD_DIM, cap)
+    c._tensors = (k, v, params)  # the struct holds raw pointers: keep the tensors alive
+    return c
+
+
+def new_q4_cache(batch: int, n_kv_heads: int, capacity: int, device=None) -> Q4Cache:
+    """A zero-filled 4-bit cache (its tensors: ``cache._tensors``)."""
+    dev = device or "cuda"
+    shape = (batch, n_kv_heads, capacity)
+    return make_q4_cache(torch.zeros(*shape, HEAD_DIM // 2, dtype=torch.uint8, device=dev),
+                         torch.zeros(*shape, HEAD_DIM // 2, dtype=torch.uint8, device=dev),
+                         torch.zeros(*shape, 4, dtype=torch.int16, device=dev))
+
+
+def _head_rows(x, out, weight, dtype, n, what, dev):
+    if x is None:
+        if out is not None or weight is not None:
+            raise ValueError(f"{what}_out and {what}_weight need {what}")
+        return None
+    if not x.is_cuda or x.get_device() != dev:
+        raise ValueError(f"{what} must be on the current device (cuda:{dev})")
+    if x.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {x.dtype}")
+    if x.dim() != 4 or x.shape[3] != HEAD_DIM or x.stride(3) != 1:
+        raise ValueError(f"{what} must be [batch, heads, n, 64] with the last axis contiguous")
+    B, H = x.shape[:2]
+    sb, sh, st = _strides(x)
+    return HeadRows(x.data_ptr(), sb, sh, st,
+                    _at(weight, dtype, (HEAD_DIM,), f"{what}_weight", dev),
+                    _at(out, dtype, (B, H, n, HEAD_DIM), f"{what}_out", dev), H)
+
+
+def kvd_qk_norm_rope(q=None, k=None, q_out=None, k_out=None, q_weight=None, k_weight=None,
+                     pos0=None, eps: float = 1e-6, base: float = 10000.0, flags: int = 0,
+                     dev_err=None, stream=None):
+    """RMS norm of each query and key head, then the rotation at position ``pos0[b] + j``, in
+    one pass: ``q [batch, n_q_heads, n, 64]`` and/or ``k [batch, n_k_heads, n, 64]`` of any
+    strides (a view of a fused projection) into contiguous ``q_out`` / ``k_out`` (``q`` and
+    ``k`` themselves when contiguous). ``base`` 0: norm only."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k is needed")
+    if ref.dim() != 4:
+        raise ValueError("q and k must be [batch, heads, n, 64]")
+    dev = _device_of(ref, "q" if q is not None else "k")
+    B, _, n, _ = ref.shape
+    if q is not None and k is not None and (k.shape[0] != B or k.shape[2] != n):
+        raise ValueError("q and k must share batch and n")
+    if (q is not None and q_out is None) or (k is not None and k_out is None):
+        raise ValueError("q_out (k_out) is needed with q (k)")
+    rq = _head_rows(q, q_out, q_weight, ref.dtype, n, "q", dev)
+    rk = _head_rows(k, k_out, k_weight, ref.dtype, n, "k", dev)
+    _check(load_library().kvd_qk_norm_rope(
+        _dtype_code(ref), B, n, None if rq is None else ctypes.byref(rq),
+        None if rk is None else ctypes.byref(rk), _at(pos0, _I32, (B,), "pos0", dev), eps, base,
+        flags, _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_qk_norm_rope")
+
+
+def _query_shape(q, out, dev):
+    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
+        raise ValueError("q must be [batch, n_q_heads, qlen, 64]")
+    shape = tuple(q.shape)
+    return shape, _at(q, q.dtype, None, "q", dev), _at(out, q.dtype, shape, "out", dev)
+
+
+def kvd_window_attn(q, cache: Cache, out, workspace, window: int, n_sinks: int = 0, lens=None,
+                    fixed_len: int = 0, scale: float = 0.125, flags: int = 0, dev_err=None,
+                    stream=None, append=None):
+    """``kvd_decode_attn`` (one query token per row) or the causal ``kvd_verify_attn`` (up to
+    16) through a sliding window: the query at position p sees t <= p with t < n_sinks or
+    t > p - window. workspace: kvd_workspace_size(KVD_OP_WINDOW_ATTN, ...) bytes."""
+    dev = _device_of(q, "q")
+    (B, Hq, ql, _), qp, op = _query_shape(q, out, dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    if append is not None:
+        for t, what in zip(append[:3], ("k_new", "v_new", "lens_out")):
+            dt, sh = (_I32, (B,)) if what == "lens_out" else (
+                q.dtype, (B, cache.n_kv_heads, ql, HEAD_DIM))
+            _at(t, dt, sh, what, dev)
+    _check(load_library().kvd_window_attn(
+        _dtype_code(q), B, Hq, ql, qp, _cache_on(cache, dev, q.dtype),
+        _at(lens, _I32, (B,), "lens", dev), fixed_len, _append_arg(append), window, n_sinks, scale,
+        op, ws, ws_bytes, flags, _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)),
+        "kvd_window_attn")
+
+
+def kvd_prefill_window_attn(q, cache: Cache, k_new, v_new, plens, out, window: int,
+                            n_sinks: int = 0, lens_in=None, lens_out=None, scale: float = 0.125,
+                            rope_base: float = 0.0, flags: int = 0, dev_err=None, stream=None):
+    """``kvd_prefill_attn`` through a sliding window with sinks."""
+    dev = _device_of(q, "q")
+    (B, Hq, T, _), qp, op = _query_shape(q, out, dev)
+    kv = (B, cache.n_kv_heads, T, HEAD_DIM)
+    _check(load_library().kvd_prefill_window_attn(
+        _dtype_code(q), B, Hq, T, qp, _cache_on(cache, dev, q.dtype),
+        _at(k_new, q.dtype, kv, "k_new", dev), _at(v_new, q.dtype, kv, "v_new", dev),
+        _at(lens_in, _I32, (B,), "lens_in", dev), _at(plens, _I32, (B,), "plens", dev),
+        _at(lens_out, _I32, (B,), "lens_out", dev), window, n_sinks, scale, rope_base, op, flags,
+        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_prefill_window_attn")
+
+
+def kvd_q4_append(cache: Q4Cache, k_new, v_new, lens_in=None, lens_out=None, counts=None,
+                  flags: int = 0, dev_err=None, stream=None):
+    """Quantise ``k_new``, ``v_new`` ``[batch, n_kv_heads, q, 64]`` and write row b's first
+    ``counts[b]`` tokens (all q without ``counts``) at positions ``lens_in[b]`` on."""
+    dev = _device_of(k_new, "k_new")
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [batch, n_kv_heads, q, 64]")
+    B, _, n, _ = k_new.shape
+    shape = (B, cache.n_kv_heads, n, HEAD_DIM)
+    _check(load_library().kvd_q4_append(
+        _dtype_code(k_new), _cache_on(cache, dev), B, n,
+        _at(k_new, k_new.dtype, shape, "k_new", dev), _at(v_new, k_new.dtype, shape, "v_new", dev),
+        _at(lens_in, _I32, (B,), "lens_in", dev), _at(counts, _I32, (B,), "counts", dev),
+        _at(lens_out, _I32, (B,), "lens_out", dev), flags,
+        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_q4_append")
+
+
+def kvd_q4_dequant(cache: Q4Cache, k_out=None, v_out=None, pos0=None, flags: int = 0,
+                   dev_err=None, stream=None):
+    """Read positions ``pos0[b] ..`` of a 4-bit cache back into ``k_out`` and/or ``v_out``,
+    ``[batch, n_kv_heads, n, 64]``."""
+    ref = k_out if k_out is not None else v_out
+    if ref is None or ref.dim() != 4:
+        raise ValueError("k_out or v_out [batch, n_kv_heads, n, 64] is needed")
+    dev = _device_of(ref, "k_out" if k_out is not None else "v_out")
+    B, _, n, _ = ref.shape
+    shape = (B, cache.n_kv_heads, n, HEAD_DIM)
+    _check(load_library().kvd_q4_dequant(
+        _dtype_code(ref), _cache_on(cache, dev), B, n, _at(k_out, ref.dtype, shape, "k_out", dev),
+        _at(v_out, ref.dtype, shape, "v_out", dev), _at(pos0, _I32, (B,), "pos0", dev), flags,
+        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_q4_dequant")
+
+
+def kvd_q4_attn(q, cache: Q4Cache, out, workspace=None, lens=None, fixed_len: int = 0,
+                causal: bool = True, window: int = 0, n_sinks: int = 0, scale: float = 0.125,
+                flags: int = 0, dev_err=None, stream=None):
+    """Attention of 1..16 query tokens per row over a 4-bit cache (the block's K/V already
+    appended). ``window`` > 0: a sliding window with ``n_sinks`` sinks. workspace:
+    kvd_workspace_size(KVD_OP_Q4_ATTN, ...) bytes, used by a few long rows only."""
+    dev = _device_of(q, "q")
+    (B, Hq, ql, _), qp, op = _query_shape(q, out, dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    _check(load_library().kvd_q4_attn(
+        _dtype_code(q), B, Hq, ql, qp, _cache_on(cache, dev), _at(lens, _I32, (B,), "lens", dev),
+        fixed_len, int(bool(causal)), window, n_sinks, scale, op, ws, ws_bytes, flags,
+        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_q4_attn")
+
+
+def kvd_sample_filtered(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None,
+                        logprob=None, n_kept=None, flags: int = 0, dev_err=None, stream=None):
+    """Draw one token per row of ``logits [batch, vocab]`` (rows may be strided) after
+    temperature, top-k, top-p and min-p, each an optional ``[batch]`` tensor; ``u [batch]``
+    are the caller's uniforms in [0, 1)."""
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be [batch, vocab] with contiguous rows")
+    if logits.dtype != _F32:
+        raise TypeError(f"logits must be {_F32}, got {logits.dtype}")
+    dev = _device_of(logits, "logits")
+    B, V = logits.shape
+    row = logits.stride(0) if B > 1 else V
+    b = (B,)
+    _check(load_library().kvd_sample_filtered(
+        logits.data_ptr(), row, B, V, _at(temperature, _F32, b, "temperature", dev),
+        _at(top_k, _I32, b, "top_k", dev), _at(top_p, _F32, b, "top_p", dev),
+        _at(min_p, _F32, b, "min_p", dev), _at(u, _F32, b, "u", dev),
+        _at(token, _I32, b, "token", dev), _at(logprob, _F32, b, "logprob", dev),
+        _at(n_kept, _I32, b, "n_kept", dev), flags, _at(dev_err, _I32, None, "dev_err", dev),
+        _on(stream, dev)), "kvd_sample_filtered")

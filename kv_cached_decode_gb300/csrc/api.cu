@@ -151,6 +151,7 @@ extern "C" size_t kvd_workspace_size(kvd_op op, int32_t batch, int32_t n_q_heads
                                      int32_t max_len, int32_t vocab) {
     switch (op) {
     case KVD_OP_DECODE_ATTN:
+    case KVD_OP_WINDOW_ATTN:
     case KVD_OP_VERIFY_ATTN: {
         const int q = op == KVD_OP_DECODE_ATTN ? 1 : qlen;
         if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || rows_per_kv <= 0 ||
@@ -169,6 +170,11 @@ extern "C" size_t kvd_workspace_size(kvd_op op, int32_t batch, int32_t n_q_heads
                                           mmax, kMaxSplits, 1);
         return std::max<size_t>(P.ws_bytes, KVD_WS_COUNTER_BYTES);
     }
+    case KVD_OP_Q4_ATTN:
+        if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
+            qlen < 1 || qlen > KVD_MAX_QLEN || max_len < 0)
+            return 0;
+        return q4_workspace_bytes(batch, n_q_heads, n_kv_heads, qlen, max_len);
     case KVD_OP_GREEDY_ACCEPT: {
         if (batch <= 0 || qlen < 1 || qlen > KVD_MAX_QLEN || vocab <= 0) return 0;
         return accept_workspace_bytes(batch, qlen, vocab, kWsTargetBound);
@@ -193,6 +199,7 @@ extern "C" const char* kvd_status_string(kvd_status s) {
     case KVD_ERR_BAD_TOKEN: return "KVD_ERR_BAD_TOKEN: draft id outside the vocabulary";
     case KVD_ERR_NAN: return "KVD_ERR_NAN: NaN in the logits";
     case KVD_ERR_TIMEOUT: return "KVD_ERR_TIMEOUT: a bounded device wait gave up";
+    case KVD_ERR_BAD_PARAM: return "KVD_ERR_BAD_PARAM: sampling parameter out of range";
     }
     return "unknown kvd_status";
 }

@@ -38,6 +38,10 @@
 //    whose first CTAs' merged partials go through the workspace (or, with few enough
 //    splits, every block's partial does), and the last block to arrive (atomic
 //    ticket) merges them. Merges run in fixed split order, so results are repeatable.
+//  * With a sliding window (kvd_window_attn) the tiles of a unit are numbered over what its
+//    queries can see: the tiles of the sinks, then those from the window's first position
+//    on; the splits share that list, and nothing between is read. Compiled into builds of
+//    their own (WINDOW), so the others keep their code.
 //  * Programmatic dependent launch: every block lets the next kernel on the stream
 //    start as soon as its own copies are issued; with KVD_FLAG_EARLY_KV it also issues
 //    those copies before waiting for the previous kernel.
@@ -45,6 +49,7 @@
 #include <atomic>
 #include <climits>
 #include <mutex>
+#include <type_traits>
 #include <unordered_map>
 
 #include "kvd_common.cuh"
@@ -100,6 +105,8 @@ struct AttnParams {
     float2* ws_ml;
     int32_t* ws_cnt;
     int32_t* dev_err;
+    int32_t window;    // WINDOW builds: query at p sees t <= p, t < n_sinks or t > p - window
+    int32_t n_sinks;
 };
 
 // Shared memory: [stages x (K tile, V tile); after the tile loop the same bytes hold the
@@ -149,6 +156,9 @@ struct CtaCtx {
     // s: split of the unit; rank / grp: place in its cluster / the cluster's index
     int bk, h, sub, s, rank, grp, m0, mcount, len, new0, t_begin, t_end, n_tiles, unit;
     bool bad;
+    // WINDOW builds: the split's first tile in the unit's list of visible tiles; tiles
+    // numbered from `head` on lie `gap` further in the cache; wlo: query 0's first position
+    int vt0, head, gap, wlo;
 };
 
 // Give-up points of the block's waits. Every wait is bounded relative to its own start
@@ -175,6 +185,17 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
+// Cache position of the block's tile j.
+template <bool WINDOW>
+__device__ __forceinline__ int tile_pos(const CtaCtx& c, int j) {
+    if (WINDOW) {
+        const int v = c.vt0 + j;
+        return (v < c.head ? v : v + c.gap) * kTile;
+    }
+    return c.t_begin + j * kTile;
+}
+
+template <bool WINDOW>
 __device__ __forceinline__ void setup_ctx(const AttnParams& p, CtaCtx& c) {
     c.s = blockIdx.x;
     c.grp = p.cgroups > 1 ? c.s / p.csize : 0;
@@ -192,6 +213,20 @@ __device__ __forceinline__ void setup_ctx(const AttnParams& p, CtaCtx& c) {
     c.t_begin = c.s * p.tiles_per_split * kTile;
     c.t_end = c.bad ? c.t_begin : min(c.len, c.t_begin + p.tiles_per_split * kTile);
     c.n_tiles = c.t_end > c.t_begin ? (c.t_end - c.t_begin + kTile - 1) / kTile : 0;
+    if (WINDOW) {
+        const int len = c.bad ? 0 : c.len;
+        const int all = (len + kTile - 1) / kTile;
+        const int64_t lo = (int64_t)len - p.qlen - p.window + 1;
+        c.wlo = lo > 0 ? (int)lo : 0;
+        const int first = c.wlo / kTile;
+        const int sinks = (min(p.n_sinks, len) + kTile - 1) / kTile;
+        c.head = sinks < first ? sinks : 0;
+        c.gap = sinks < first ? first - sinks : 0;
+        c.vt0 = c.s * p.tiles_per_split;
+        c.n_tiles = max(0, min(p.tiles_per_split, all - c.gap - c.vt0));
+        c.t_end = len;
+        c.t_begin = c.n_tiles > 0 ? tile_pos<true>(c, 0) : len;
+    }
 }
 
 // Element offset of query vector m (0 <= m < M) of unit (bk, h) in q / out.
@@ -232,13 +267,13 @@ __device__ __forceinline__ void store_out(const AttnParams& p, const int64_t* qo
 // start, and waits for the previous one (before all of this unless the call was made
 // with KVD_FLAG_EARLY_KV). Returns false if the length is out of range: flagged,
 // nothing written.
-template <bool ROPE>
+template <bool ROPE, bool WINDOW>
 __device__ __forceinline__ bool prologue(const AttnParams& p, CtaCtx& c, uint8_t* smem,
                                          uint64_t* bars, int64_t* qoff, uint8_t* app,
                                          const CUtensorMap* tmk, const CUtensorMap* tmv) {
     const int tid = threadIdx.x;
     if (!p.early) pdl_wait();
-    setup_ctx(p, c);
+    setup_ctx<WINDOW>(p, c);
     if (c.bad) {
         if (p.early) pdl_wait();
         if (tid == 0 && c.s == 0 && c.h == 0 && c.sub == 0) {
@@ -264,7 +299,7 @@ __device__ __forceinline__ bool prologue(const AttnParams& p, CtaCtx& c, uint8_t
         if (p.test_stall && c.s == p.splits - 1 && first > 0)
             mbar_expect_tx_only(smem_u32(&bars[0]), 16);
         for (int j = 0; j < first; ++j)
-            issue_tile(tmk, tmv, smem, bars, j, c.t_begin + j * kTile, c.h, c.bk, tx);
+            issue_tile(tmk, tmv, smem, bars, j, tile_pos<WINDOW>(c, j), c.h, c.bk, tx);
     }
     // the last warp, clear of thread 0's copies
     const int qi = tid - (kThreads - kMmaQueryBlock);
@@ -411,7 +446,7 @@ __device__ void abort_after_timeout(const AttnParams& p, const CtaCtx& c, uint64
 // The tile loop shared by both kernels. Tiles are taken two at a time (a round); warp w
 // works on tile 2r + w/4, positions (w%4)*16 .. +15, through slab(sK, sV, tile0, slab0).
 // Returns false after a timeout (already handled: the caller just returns).
-template <typename T, bool ROPE, typename Slab>
+template <typename T, bool ROPE, bool WINDOW, typename Slab>
 __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, uint8_t* smem,
                                           uint64_t* bars, float* mrg, uint8_t* app,
                                           const CUtensorMap* tmk, const CUtensorMap* tmv,
@@ -425,7 +460,7 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
     if (p.append && c.new0 < c.t_end) {
         for (int r = 0; r < rounds; ++r)
             if (2 * r + half < c.n_tiles)
-                stage_appended(p, c, app, c.t_begin + (2 * r + half) * kTile, slab0);
+                stage_appended(p, c, app, tile_pos<WINDOW>(c, 2 * r + half), slab0);
         cp_async_commit();
     }
     for (int r = 0; r < rounds; ++r) {
@@ -439,7 +474,7 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
             if (ok) {
                 uint8_t* sK = smem + st * 2 * kTileBytes;
                 uint8_t* sV = sK + kTileBytes;
-                const int tile0 = c.t_begin + j * kTile;
+                const int tile0 = tile_pos<WINDOW>(c, j);
                 if (p.append) inject_slab<T, ROPE>(p, c, sK, sV, app, tile0, slab0);
                 slab(sK, sV, tile0, slab0);
             }
@@ -453,7 +488,7 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
                 fence_proxy_async();
                 for (int k = 0; k < 2 && 2 * r + p.stages + k < c.n_tiles; ++k) {
                     const int jn = 2 * r + p.stages + k;
-                    issue_tile(tmk, tmv, smem, bars, jn % p.stages, c.t_begin + jn * kTile, c.h,
+                    issue_tile(tmk, tmv, smem, bars, jn % p.stages, tile_pos<WINDOW>(c, jn), c.h,
                                c.bk, tx);
                 }
             }
@@ -546,7 +581,9 @@ __device__ void ws_merge_last(const AttnParams& p, const CtaCtx& c, float* red, 
 // A cluster's merge of float4 q4 of one query vector's output: the vector's slots in
 // the cluster's CS splits (at sl0 + r * stride: o[64], max, sum) combined in split order
 // into (max, sum, o), o unnormalised. Loads are unconditional (a split past CS re-reads the last slot and gets
-// weight 0) and go in batches of four, so they overlap.
+// weight 0) and go in batches of four, so they overlap. WINDOW builds, which promise what an
+// infinite value does, drop the re-read slot's values too (0 * inf would be NaN).
+template <bool WINDOW>
 __device__ __forceinline__ void merge_cluster_quad(const float* sl0, int stride, int CS, int q4,
                                                    float& mx, float& l, float4& o) {
     mx = -INFINITY;
@@ -570,6 +607,7 @@ __device__ __forceinline__ void merge_cluster_quad(const float* sl0, int stride,
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float a = r0 + j < CS ? exp2f(mv[j] - ref) : 0.f;
+            if (WINDOW && r0 + j >= CS) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
             l = fmaf(lv[j], a, l);
             o.x = fmaf(v[j].x, a, o.x);
             o.y = fmaf(v[j].y, a, o.y);
@@ -593,7 +631,7 @@ __device__ __forceinline__ void merge_cluster_quad(const float* sl0, int stride,
 // whose plan has several clusters per unit: kept out of the other builds, the code after
 // the cluster merge stays as short as the chain of every single-cluster launch needs.
 // red: o [8][RMAX][red_stride], m [8][RMAX], l [8][RMAX]; mrg: [splits][msub][kSlot].
-template <typename T, int RMAX, bool GROUPED>
+template <typename T, int RMAX, bool GROUPED, bool WINDOW>
 __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, float* mrg,
                            uint64_t* merge_bar, int* misc, const int64_t* qoff,
                            uint8_t* scratch4k) {
@@ -667,7 +705,7 @@ __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, flo
                 const int m = it >> 4, q4 = it & 15;
                 float mx, l;
                 float4 o;
-                merge_cluster_quad(mrg + m * kSlot, p.msub * kSlot, CS, q4, mx, l, o);
+                merge_cluster_quad<WINDOW>(mrg + m * kSlot, p.msub * kSlot, CS, q4, mx, l, o);
                 const size_t slot = ((size_t)c.unit * p.cgroups + c.grp) * p.msub + m;
                 *reinterpret_cast<float4*>(p.ws_part + slot * kHeadDim + 4 * q4) = o;
                 if (q4 == 0) p.ws_ml[slot] = make_float2(mx, l);
@@ -680,7 +718,7 @@ __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, flo
             const int m = it >> 4, q4 = it & 15;
             float mx, l;
             float4 o;
-            merge_cluster_quad(mrg + m * kSlot, p.msub * kSlot, CS, q4, mx, l, o);
+            merge_cluster_quad<WINDOW>(mrg + m * kSlot, p.msub * kSlot, CS, q4, mx, l, o);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             uint2 packed;
             packed.x = Half16<T>::from_f2(o.x * inv, o.y * inv);
@@ -716,7 +754,7 @@ __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, flo
 }
 
 // ------------------------------------------------- one query vector per KV head (SIMT) --
-template <typename T, bool ROPE, bool GROUPED = false>
+template <typename T, bool ROPE, bool GROUPED = false, bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per SM
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
@@ -735,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
     const int grp = lane >> 3, c8 = lane & 7;
 
     CtaCtx c;
-    if (!prologue<ROPE>(p, c, smem, bars, qoff, smem + L.app_off, &tmk, &tmv)) return;
+    if (!prologue<ROPE, WINDOW>(p, c, smem, bars, qoff, smem + L.app_off, &tmk, &tmv)) return;
 
     float qf[8];
     {
@@ -767,12 +805,15 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 
+    auto visible = [&](int t) {
+        return t < c.t_end && (!WINDOW || t >= c.wlo || t < p.n_sinks);
+    };
     auto slab = [&](const uint8_t* sK, const uint8_t* sV, int tile0, int slab0) {
         float sc[4];
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const int row = slab0 + grp * 4 + jj;
-            const bool valid = tile0 + row < c.t_end;
+            const bool valid = visible(tile0 + row);
             const uint4 kr = *reinterpret_cast<const uint4*>(sK + swz(row, c8));
             float kf[8];
             unpack8<T>(kr, kf);
@@ -801,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const int row = slab0 + grp * 4 + jj;
-            const bool valid = tile0 + row < c.t_end;
+            const bool valid = visible(tile0 + row);
             const uint4 vr = *reinterpret_cast<const uint4*>(sV + swz(row, c8));
             float vf[8];
             unpack8<T>(vr, vf);
@@ -809,7 +850,8 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(sc[jj], valid ? vf[e] : 0.f, acc[e]);
         }
     };
-    if (!run_tiles<T, ROPE>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab)) return;
+    if (!run_tiles<T, ROPE, WINDOW>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
+        return;
 
     // Merge the four 8-lane groups of each warp (they saw different positions).
 #pragma unroll
@@ -837,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
         }
     }
     __syncthreads();
-    finish_cta<T, RM, GROUPED>(p, c, red, mrg, &bars[p.stages], misc, qoff,
+    finish_cta<T, RM, GROUPED, WINDOW>(p, c, red, mrg, &bars[p.stages], misc, qoff,
                                smem + L.bar_off - 4096);
 }
 
@@ -851,7 +893,8 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
 // constant 0, their S and O accumulators are not kept, and the block needs about 30
 // fewer registers -- three blocks per SM without spilling, so that more of the next
 // launch's blocks (and its thread-block clusters) fit beside a running launch.
-template <typename T, int MINB, bool ROPE, int RM = 16, bool GROUPED = false>
+template <typename T, int MINB, bool ROPE, int RM = 16, bool GROUPED = false,
+          bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads, MINB)
     block_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
@@ -872,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     const int jm = lane >> 3, rr = lane & 7;         // ldmatrix matrix / row
 
     CtaCtx c;
-    if (!prologue<ROPE>(p, c, smem, bars, qoff, smem + L.app_off, &tmk, &tmv)) return;
+    if (!prologue<ROPE, WINDOW>(p, c, smem, bars, qoff, smem + L.app_off, &tmk, &tmv)) return;
 
     // Q as m16n8k16 A fragments for the four 16-dim k-steps (rows >= mcount are 0).
     uint32_t qa[4][4];
@@ -929,6 +972,12 @@ __global__ void __launch_bounds__(kThreads, MINB)
         return min(lim, c.t_end);
     };
     const int limA = limit_of(qr, rowA), limB = limit_of(qr + 8, rowB);
+    // WINDOW: the row's first position; query i's is i further than query 0's
+    auto first_of = [&](int r) -> int {
+        const int64_t lo = (int64_t)c.len - p.qlen - p.window + 1 + (c.m0 + r) % p.qlen;
+        return lo > 0 ? (int)lo : 0;
+    };
+    const int wloA = WINDOW ? first_of(qr) : 0, wloB = WINDOW ? first_of(qr + 8) : 0;
 
     constexpr int kAcc = kFull ? 4 : 2;  // accumulator elements kept per n8 block
     float oacc[8][kAcc];
@@ -951,6 +1000,40 @@ __global__ void __launch_bounds__(kThreads, MINB)
             fence_proxy_async();
             __syncwarp();
         }
+        // WINDOW: V rows that some queries see and others do not, or none does. 0 * inf and
+        // 0 * NaN would poison the queries that do not see them: rows of the second kind
+        // are cleared, rows of the first kind that hold such values are kept out of the
+        // product and added to the queries that see them one by one (odd).
+        uint32_t odd = 0;
+        if (WINDOW) {
+            const int ts = tile0 + slab0;
+            if (ts >= p.n_sinks && ts + 16 <= c.wlo) return;
+            const int last = (int)max((int64_t)c.len - p.window, (int64_t)0);
+            if (!(ts + 16 <= c.len - p.qlen + 1 && (ts >= last || ts + 16 <= p.n_sinks))) {
+#pragma unroll
+                for (int x = lane; x < 128; x += 32) {
+                    const int row = x >> 3, t = ts + row;
+                    uint4* v = reinterpret_cast<uint4*>(sV + swz(slab0 + row, x & 7));
+                    if (t < c.wlo && t >= p.n_sinks) {
+                        *v = make_uint4(0, 0, 0, 0);
+                    } else {
+                        constexpr uint32_t kExp =
+                            std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+                        const uint4 u = *v;
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t a = w[e] & kExp;
+                            if ((a & 0xFFFFu) == (kExp & 0xFFFFu) || (a >> 16) == (kExp >> 16))
+                                odd |= 1u << row;
+                        }
+                    }
+                }
+                odd = __reduce_or_sync(0xffffffffu, odd);
+                fence_proxy_async();
+                __syncwarp();
+            }
+        }
         const uint32_t kb = smem_u32(sK), vb = smem_u32(sV);
         float sacc[2][kAcc];
 #pragma unroll
@@ -971,7 +1054,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
             for (int e = 0; e < kAcc; ++e) {
                 const int key = tile0 + slab0 + n * 8 + qc + (e & 1);
                 const int lim = e < 2 ? limA : limB;
-                sacc[n][e] = key < lim ? sacc[n][e] * p.scale_log2 : -INFINITY;
+                const bool in = !WINDOW || key >= (e < 2 ? wloA : wloB) || key < p.n_sinks;
+                sacc[n][e] = key < lim && in ? sacc[n][e] * p.scale_log2 : -INFINITY;
             }
         uint32_t pa[4];
         if constexpr (kFull) {
@@ -1022,6 +1106,38 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 oacc[n][1] *= aA;
             }
         }
+        if (WINDOW && odd) {  // warp-uniform
+            for (uint32_t left = odd; left; left &= left - 1) {
+                const int row = __ffs(left) - 1, t = tile0 + slab0 + row;
+                const int src = (lane & 28) | ((row & 7) >> 1);
+                const uint32_t pA = __shfl_sync(0xffffffffu, row < 8 ? pa[0] : pa[2], src);
+                const uint32_t pB = __shfl_sync(0xffffffffu, row < 8 ? pa[1] : pa[3], src);
+                const float2 fA = Half16<T>::to_f2(pA), fB = Half16<T>::to_f2(pB);
+                const float wA = row & 1 ? fA.y : fA.x, wB = row & 1 ? fB.y : fB.x;
+                const bool seeA = t < limA && (t >= wloA || t < p.n_sinks);
+                const bool seeB = t < limB && (t >= wloB || t < p.n_sinks);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float2 v = Half16<T>::to_f2(*reinterpret_cast<const uint32_t*>(
+                        sV + swz(slab0 + row, n) + qc * 2));
+                    if (seeA) {
+                        oacc[n][0] = fmaf(wA, v.x, oacc[n][0]);
+                        oacc[n][1] = fmaf(wA, v.y, oacc[n][1]);
+                    }
+                    if (kFull && seeB) {
+                        oacc[n][kAcc - 2] = fmaf(wB, v.x, oacc[n][kAcc - 2]);
+                        oacc[n][kAcc - 1] = fmaf(wB, v.y, oacc[n][kAcc - 1]);
+                    }
+                }
+            }
+            __syncwarp();
+            for (int x = lane; x < 128; x += 32)
+                if (odd >> (x >> 3) & 1)
+                    *reinterpret_cast<uint4*>(sV + swz(slab0 + (x >> 3), x & 7)) =
+                        make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
+            __syncwarp();
+        }
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             const int vrow = slab0 + (jm & 1) * 8 + rr;
@@ -1031,7 +1147,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
             mma(oacc[2 * np + 1], pa, v2, v3);
         }
     };
-    if (!run_tiles<T, ROPE>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab)) return;
+    if (!run_tiles<T, ROPE, WINDOW>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
+        return;
 
     lA += __shfl_xor_sync(0xffffffffu, lA, 1);
     lA += __shfl_xor_sync(0xffffffffu, lA, 2);
@@ -1064,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
         }
     }
     __syncthreads();
-    finish_cta<T, RM, GROUPED>(p, c, red, mrg, &bars[p.stages], misc, qoff,
+    finish_cta<T, RM, GROUPED, WINDOW>(p, c, red, mrg, &bars[p.stages], misc, qoff,
                                smem + L.bar_off - 4096);
 }
 
@@ -1127,13 +1244,17 @@ int prepare_kernel(size_t smem_bytes) {
 // of the other builds, whose register budgets it would raise).
 enum Variant {
     kSimt = 1, kMma = 2, kMma3 = 3, kSimtRope = 4, kMmaRope = 5, kMma8 = 6,
-    kSimtG = 7, kMmaG = 8  // kSimt / kMma with the merge across clusters of a unit
+    kSimtG = 7, kMmaG = 8,  // kSimt / kMma with the merge across clusters of a unit
+    kSimtW = 9, kMmaW = 10, kSimtRopeW = 11, kMmaRopeW = 12  // with a sliding window
 };
 
 // Rows of the warp partials (the red area) of a variant: 16 for the tensor-core builds,
 // 8 for the 8-vector build, 1 for the CUDA-core kernel.
 constexpr int variant_rmax(int var) {
-    return (var == kSimt || var == kSimtRope || var == kSimtG) ? 1 : var == kMma8 ? 8 : 16;
+    return (var == kSimt || var == kSimtRope || var == kSimtG || var == kSimtW ||
+            var == kSimtRopeW)
+               ? 1
+               : var == kMma8 ? 8 : 16;
 }
 
 template <typename T>
@@ -1149,6 +1270,10 @@ int prepare(int var) {
     case kSimtRope: return prepare_kernel<decode_attn_kernel<T, true>>(smem);
     case kMmaG: return prepare_kernel<block_attn_kernel<T, 2, false, 16, true>>(smem);
     case kSimtG: return prepare_kernel<decode_attn_kernel<T, false, true>>(smem);
+    case kSimtW: return prepare_kernel<decode_attn_kernel<T, false, false, true>>(smem);
+    case kSimtRopeW: return prepare_kernel<decode_attn_kernel<T, true, false, true>>(smem);
+    case kMmaW: return prepare_kernel<block_attn_kernel<T, 2, false, 16, false, true>>(smem);
+    case kMmaRopeW: return prepare_kernel<block_attn_kernel<T, 2, true, 16, false, true>>(smem);
     default: return prepare_kernel<decode_attn_kernel<T, false>>(smem);
     }
 }
@@ -1163,6 +1288,13 @@ const void* kernel_of(int var) {
     case kSimtRope: return reinterpret_cast<const void*>(decode_attn_kernel<T, true>);
     case kMmaG: return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 16, true>);
     case kSimtG: return reinterpret_cast<const void*>(decode_attn_kernel<T, false, true>);
+    case kSimtW: return reinterpret_cast<const void*>(decode_attn_kernel<T, false, false, true>);
+    case kSimtRopeW:
+        return reinterpret_cast<const void*>(decode_attn_kernel<T, true, false, true>);
+    case kMmaW:
+        return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 16, false, true>);
+    case kMmaRopeW:
+        return reinterpret_cast<const void*>(block_attn_kernel<T, 2, true, 16, false, true>);
     default: return reinterpret_cast<const void*>(decode_attn_kernel<T, false>);
     }
 }
@@ -1196,6 +1328,18 @@ kvd_status launch_attn(int var, dim3 grid, cudaStream_t st, bool pdl, unsigned c
     case kSimtG:
         return launch_ex(decode_attn_kernel<T, false, true>, grid, dim3(kThreads), simt_smem, st,
                          pdl, cl, mk, mv, p);
+    case kSimtW:
+        return launch_ex(decode_attn_kernel<T, false, false, true>, grid, dim3(kThreads),
+                         simt_smem, st, pdl, cl, mk, mv, p);
+    case kSimtRopeW:
+        return launch_ex(decode_attn_kernel<T, true, false, true>, grid, dim3(kThreads),
+                         simt_smem, st, pdl, cl, mk, mv, p);
+    case kMmaW:
+        return launch_ex(block_attn_kernel<T, 2, false, 16, false, true>, grid, dim3(kThreads),
+                         mma_smem, st, pdl, cl, mk, mv, p);
+    case kMmaRopeW:
+        return launch_ex(block_attn_kernel<T, 2, true, 16, false, true>, grid, dim3(kThreads),
+                         mma_smem, st, pdl, cl, mk, mv, p);
     default:
         return launch_ex(decode_attn_kernel<T, false>, grid, dim3(kThreads), simt_smem, st, pdl,
                          cl, mk, mv, p);
@@ -1308,7 +1452,7 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
                      int32_t fixed_len, const kvd_new_tokens* app, int32_t rows_per_kv,
                      int32_t causal, float scale, void* out, void* ws, size_t ws_bytes,
                      uint32_t flags, int32_t* dev_err, cudaStream_t stream,
-                     bool noalloc = false) {
+                     bool noalloc = false, int32_t window = 0, int32_t n_sinks = 0) {
     if (dtype != KVD_F16 && dtype != KVD_BF16) return KVD_ERR_INVALID_ARG;
     if (kvd_status s = validate_cache(kv)) return s;
     if (batch < 0 || n_q_heads <= 0 || rows_per_kv <= 0) return KVD_ERR_INVALID_ARG;
@@ -1332,7 +1476,18 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
         if (kvd_status s = noalloc_scratch(&ws)) return s;
         ws_bytes = KVD_NOALLOC_SCRATCH_BYTES;
     }
-    const int len_bound = lens ? kv->capacity : fixed_len;
+    const bool windowed = window > 0;
+    int len_bound = lens ? kv->capacity : fixed_len;
+    if (windowed) {
+        // more than the cache holds sees the whole cache: the kernel's sums stay small
+        window = std::min(window, kv->capacity);
+        n_sinks = std::min(n_sinks, kv->capacity);
+        // the most positions the tiles of a unit's list hold: those of the window of all
+        // qlen queries, cut anywhere, and those of the sinks
+        const int64_t near = ((int64_t)window + qlen - 1 + 2 * (kTile - 1)) / kTile;
+        const int64_t far = ((int64_t)n_sinks + kTile - 1) / kTile;
+        len_bound = (int)std::min<int64_t>(len_bound, (near + far) * kTile);
+    }
     const bool bf = dtype == KVD_BF16;
     const int group = n_q_heads / kv->n_kv_heads;
     const int app_rows = app_units(app ? 1 : 0, rope ? 1 : 0, qlen);
@@ -1360,7 +1515,8 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
                resident(kern, var * 2 + (bf ? 1 : 0), plan_smem(Q, var, app_rows), 1, nsm);
     };
     // the builds with the rotation compiled in stand for kSimt and kMma when it is on
-    const int simt = rope ? kSimtRope : kSimt, mma = rope ? kMmaRope : kMma;
+    const int simt = windowed ? (rope ? kSimtRopeW : kSimtW) : rope ? kSimtRope : kSimt;
+    const int mma = windowed ? (rope ? kMmaRopeW : kMmaW) : rope ? kMmaRope : kMma;
     int var = (verify || (int64_t)rows_per_kv * group * qlen >= 2) ? mma : simt;
     AttnPlan P;
     if (!plan_for(var, P)) return KVD_ERR_CUDA;
@@ -1464,6 +1620,8 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
     p.ws_part = wsb ? reinterpret_cast<float*>(wsb + P.part_offset) : nullptr;
     p.ws_ml = wsb ? reinterpret_cast<float2*>(wsb + P.ml_offset) : nullptr;
     p.dev_err = dev_err;
+    p.window = window;
+    p.n_sinks = n_sinks;
 
     // The built-in scratch keeps whatever the previous call left; a plan that merges
     // through it needs its units' arrival counters at zero (a call that stopped early
@@ -1502,6 +1660,21 @@ extern "C" kvd_status kvd_verify_attn(kvd_dtype dtype, int32_t batch, int32_t n_
     return kvd::attention(true, dtype, batch, n_q_heads, qlen, q, kv, lens, fixed_len, append,
                           rows_per_kv, causal, scale, out, workspace, workspace_bytes, flags,
                           dev_err, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" kvd_status kvd_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads,
+                                      int32_t qlen, const void* q, const kvd_cache* kv,
+                                      const int32_t* lens, int32_t fixed_len,
+                                      const kvd_new_tokens* append, int32_t window,
+                                      int32_t n_sinks, float scale, void* out, void* workspace,
+                                      size_t workspace_bytes, uint32_t flags, int32_t* dev_err,
+                                      kvd_stream_t stream) {
+    if (window < 1 || n_sinks < 0) return KVD_ERR_INVALID_ARG;
+    // (qlen outside 1..KVD_MAX_QLEN is refused with the other arguments)
+    return kvd::attention(qlen > 1, dtype, batch, n_q_heads, qlen, q, kv, lens, fixed_len,
+                          append, 1, 1, scale, out, workspace, workspace_bytes, flags, dev_err,
+                          reinterpret_cast<cudaStream_t>(stream), /*noalloc=*/false, window,
+                          n_sinks);
 }
 
 // ---------------------------------------------------------------- no-allocation entry

@@ -26,6 +26,10 @@ kvd_status encode_rows_map(CUtensorMap* map, kvd_dtype dtype, void* base, int ro
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 kvd_status validate_cache(const kvd_cache* c);
+kvd_status validate_q4_cache(const kvd_q4_cache* c);
+
+// Workspace bytes of kvd_q4_attn for an attended length of at most max_len (q4_attn.cu).
+size_t q4_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int qlen, int max_len);
 
 // Launch with an optional programmatic-dependent-launch attribute; maps errors.
 // Launch with an optional programmatic-dependent-launch attribute and an optional

@@ -24,7 +24,9 @@
 // operand (two buffers) with tcgen05.st. A row's reference m moves
 // only when its maximum grows by more than 2^8; the rows then rescale their O in tensor
 // memory. Hand-offs run through mbarriers, every wait bounded. Only the tiles a block's
-// rows can see are read, and the blocks with the most tiles start first.
+// rows can see are read, and the blocks with the most tiles start first. With a sliding
+// window (kvd_prefill_window_attn, the WINDOW builds) a block's tiles are those of the sinks,
+// then those from its first row's window on; a row also masks what lies before its window.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -78,6 +80,7 @@ struct PrefillParams {
     float scale_log2;
     float rope_log2_base;     // > 0 sets the rotary variant's base (log2)
     int32_t test_stall;       // KVD_FLAG_TEST_STALL: the first K copy is never issued
+    int32_t window, n_sinks;  // WINDOW builds: position p sees t < n_sinks or t > p - window
 };
 
 // Three-input maximum and two-lane fp32 arithmetic of this architecture: one instruction
@@ -122,7 +125,7 @@ enum PfBar {
     kBarCount = kBarDrain + 1
 };
 
-template <typename T, bool ROPE>
+template <typename T, bool ROPE, bool WINDOW>
 __global__ void __launch_bounds__(kPfThreads, kPfMinBlocks)
     prefill_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv,
@@ -176,14 +179,27 @@ __global__ void __launch_bounds__(kPfThreads, kPfMinBlocks)
         return;
     }
     const int kv_end = s0 + q0 + rows_live;  // exclusive: the last live row's limit
-    const int n_tiles = (kv_end + kTile - 1) / kTile;
+    // the block's tiles: all up to kv_end, or (WINDOW) without the `gap` ones from tile
+    // `head` on, which none of its rows sees
+    int head = 0, gap = 0, wlo_block = 0;
+    if (WINDOW) {
+        wlo_block = max(s0 + q0 - p.window + 1, 0);  // the first row's first position
+        const int sinks = (min(p.n_sinks, kv_end) + kTile - 1) / kTile;
+        const int first = wlo_block / kTile;
+        if (sinks < first) {
+            head = sinks;
+            gap = first - sinks;
+        }
+    }
+    auto tile_t0 = [&](int j) { return (WINDOW && j >= head ? j + gap : j) * kTile; };
+    const int n_tiles = (kv_end + kTile - 1) / kTile - gap;
     const uint32_t tx = p.box_rows * kRowBytes;  // bytes of one K or V tile copy
     // K_j and V_j into slot j % kPfSlots, both completing on the slot's barrier
     auto load_kv = [&](int j) {
         const int s = j % kPfSlots;
         mbar_expect_tx(bar(kBarKV + s), 2 * tx);
-        tma_load_4d(smem_u32(sK + s * kTileBytes), &tmk, bar(kBarKV + s), 0, j * kTile, hk, b);
-        tma_load_4d(smem_u32(sV + s * kTileBytes), &tmv, bar(kBarKV + s), 0, j * kTile, hk, b);
+        tma_load_4d(smem_u32(sK + s * kTileBytes), &tmk, bar(kBarKV + s), 0, tile_t0(j), hk, b);
+        tma_load_4d(smem_u32(sV + s * kTileBytes), &tmv, bar(kBarKV + s), 0, tile_t0(j), hk, b);
     };
     if (producer && (tid & 31) == 0) {
         for (int i = 0; i < kBarCount; ++i)
@@ -302,10 +318,14 @@ __global__ void __launch_bounds__(kPfThreads, kPfMinBlocks)
         // the lane, so lane 0 holds the warp's smallest limit.
         const int lim = min(s0 + row + 1, kv_end);
         const int lim_warp = __shfl_sync(0xffffffffu, lim, 0);
+        // WINDOW: the row's first position before which only sinks are visible (rows past
+        // the prompt take the last live row's); lane 31 holds the warp's largest
+        const int wlo = WINDOW ? max(lim - p.window, 0) : 0;
+        const int wlo_warp = WINDOW ? __shfl_sync(0xffffffffu, wlo, 31) : 0;
         float m = -INFINITY, l = 0.f;  // the row's reference (log2 units) and normaliser
         for (int j = 0; j < n_tiles; ++j) {
             const int sb = j % kPfSBufs, pb = j % kPfPBufs;
-            const int t0 = j * kTile;
+            const int t0 = tile_t0(j);
             if (!__all_sync(0xffffffffu,
                             mbar_wait_bounded(bar(kBarS + sb), (j / kPfSBufs) & 1))) {
                 ok = false;
@@ -323,6 +343,11 @@ __global__ void __launch_bounds__(kPfThreads, kPfMinBlocks)
                 // the tile is not wholly visible to every row of the warp: mask it
 #pragma unroll
                 for (int i = 0; i < kTile; ++i) s[i] = t0 + i < lim ? s[i] : -INFINITY;
+            }
+            if (WINDOW && t0 < wlo_warp && t0 + kTile > p.n_sinks) {
+#pragma unroll
+                for (int i = 0; i < kTile; ++i)
+                    s[i] = t0 + i >= wlo || t0 + i < p.n_sinks ? s[i] : -INFINITY;
             }
             // (eight independent partial maxima over eight scores each: short chains)
             float pm[8];
@@ -383,7 +408,11 @@ __global__ void __launch_bounds__(kPfThreads, kPfMinBlocks)
             // this row of the A operand, in this thread's lane of tensor memory (its last
             // reader, P_{j-2} . V_{j-2}, completed before S_j did)
             tc_st32_u(tmem + lane_off + kPfColsP + pb * (kTile / 2), w);
-            if (t0 + kTile > kv_end) {
+            // WINDOW: the positions between the sinks and the block's first visible one, of
+            // a tile that also holds visible ones
+            const int dead0 = WINDOW ? min(max(p.n_sinks - t0, 0), kTile) : 0;
+            const int dead1 = WINDOW ? max(min(wlo_block - t0, kTile), dead0) : 0;
+            if (t0 + kTile > kv_end || (WINDOW && dead0 < dead1)) {
                 // Positions past the last visible key hold other data (or nothing): P is
                 // 0 there, but 0 * NaN would still poison P.V, so clear those V rows once
                 // the tile's copy has landed.
@@ -394,10 +423,14 @@ __global__ void __launch_bounds__(kPfThreads, kPfMinBlocks)
                     break;
                 }
                 uint8_t* vt = sV + vs * kTileBytes;
-                const int first = kv_end - t0;
+                const int first = min(kv_end - t0, kTile);
                 for (int x = tid; x < (kTile - first) * 8; x += kPfRows)
                     *reinterpret_cast<uint4*>(vt + swz(first + (x >> 3), x & 7)) =
                         make_uint4(0u, 0u, 0u, 0u);
+                if (WINDOW)
+                    for (int x = tid; x < (dead1 - dead0) * 8; x += kPfRows)
+                        *reinterpret_cast<uint4*>(vt + swz(dead0 + (x >> 3), x & 7)) =
+                            make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async();  // the cleared rows are read by the tensor cores
             }
             tc_fence_before();
@@ -448,14 +481,14 @@ __global__ void __launch_bounds__(kPfThreads, kPfMinBlocks)
 
 constexpr int kMaxDev = 64;
 
-template <typename T, bool ROPE>
+template <typename T, bool ROPE, bool WINDOW>
 bool prepare_prefill() {
     static std::once_flag once[kMaxDev];
     static bool ok[kMaxDev];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return false;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(prefill_attn_kernel<T, ROPE>,
+        ok[dev] = cudaFuncSetAttribute(prefill_attn_kernel<T, ROPE, WINDOW>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kPfSmem) == cudaSuccess;
         cudaGetLastError();
@@ -463,12 +496,12 @@ bool prepare_prefill() {
     return ok[dev];
 }
 
-template <typename T, bool ROPE>
+template <typename T, bool ROPE, bool WINDOW>
 kvd_status launch_prefill(dim3 grid, cudaStream_t st, bool pdl, const CUtensorMap& mk,
                           const CUtensorMap& mv, const CUtensorMap& mo, const PrefillParams& p) {
-    if (!prepare_prefill<T, ROPE>()) return KVD_ERR_CUDA;
-    return launch(prefill_attn_kernel<T, ROPE>, grid, dim3(kPfThreads), kPfSmem, st, pdl, mk,
-                  mv, mo, p);
+    if (!prepare_prefill<T, ROPE, WINDOW>()) return KVD_ERR_CUDA;
+    return launch(prefill_attn_kernel<T, ROPE, WINDOW>, grid, dim3(kPfThreads), kPfSmem, st,
+                  pdl, mk, mv, mo, p);
 }
 
 }  // namespace
@@ -476,13 +509,13 @@ kvd_status launch_prefill(dim3 grid, cudaStream_t st, bool pdl, const CUtensorMa
 
 using namespace kvd;
 
-extern "C" kvd_status kvd_prefill_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads,
-                                       int32_t max_len, const void* q, const kvd_cache* kv,
-                                       const void* k_new, const void* v_new,
-                                       const int32_t* lens_in, const int32_t* plens,
-                                       int32_t* lens_out, float scale, float rope_base,
-                                       void* out, uint32_t flags, int32_t* dev_err,
-                                       kvd_stream_t stream) {
+namespace {
+// window 0: causal attention without a window
+kvd_status prefill(kvd_dtype dtype, int32_t batch, int32_t n_q_heads, int32_t max_len,
+                   const void* q, const kvd_cache* kv, const void* k_new, const void* v_new,
+                   const int32_t* lens_in, const int32_t* plens, int32_t* lens_out,
+                   int32_t window, int32_t n_sinks, float scale, float rope_base, void* out,
+                   uint32_t flags, int32_t* dev_err, cudaStream_t st) {
     if (dtype != KVD_F16 && dtype != KVD_BF16) return KVD_ERR_INVALID_ARG;
     if (kvd_status s = validate_cache(kv)) return s;
     if (batch < 0 || n_q_heads <= 0 || max_len < 0 || batch > kv->batch)
@@ -497,7 +530,6 @@ extern "C" kvd_status kvd_prefill_attn(kvd_dtype dtype, int32_t batch, int32_t n
     if (!(rope_base >= 0.f) || !(rope_base < INFINITY)) return KVD_ERR_INVALID_ARG;
     const int64_t q_tiles = ((int64_t)max_len + kPfRows - 1) / kPfRows;
     if (q_tiles > 0x7fffffff || n_q_heads > 65535 || batch > 65535) return KVD_ERR_UNSUPPORTED;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // 1: the prompt's K/V into the cache (rows j < plens[b] at lens_in[b] + j)
     if (kvd_status s = launch_append(kv, batch, max_len, k_new, v_new, lens_in, plens, lens_out,
                                      dtype, rope_base, flags, dev_err, st))
@@ -528,9 +560,44 @@ extern "C" kvd_status kvd_prefill_attn(kvd_dtype dtype, int32_t batch, int32_t n
     const bool pdl = (flags & (KVD_FLAG_PDL | KVD_FLAG_EARLY_KV)) != 0;
     const bool rope = rope_base > 0.f;
     p.rope_log2_base = rope ? log2f(rope_base) : 0.f;
-    if (dtype == KVD_BF16)
-        return rope ? launch_prefill<__nv_bfloat16, true>(grid, st, pdl, mk, mv, mo, p)
-                    : launch_prefill<__nv_bfloat16, false>(grid, st, pdl, mk, mv, mo, p);
-    return rope ? launch_prefill<__half, true>(grid, st, pdl, mk, mv, mo, p)
-                : launch_prefill<__half, false>(grid, st, pdl, mk, mv, mo, p);
+    // more than the cache holds sees the whole cache: the kernel's sums stay small
+    p.window = std::min(window, kv->capacity);
+    p.n_sinks = std::min(n_sinks, kv->capacity);
+    const bool bf = dtype == KVD_BF16;
+    if (window > 0) {
+        if (bf)
+            return rope ? launch_prefill<__nv_bfloat16, true, true>(grid, st, pdl, mk, mv, mo, p)
+                        : launch_prefill<__nv_bfloat16, false, true>(grid, st, pdl, mk, mv, mo, p);
+        return rope ? launch_prefill<__half, true, true>(grid, st, pdl, mk, mv, mo, p)
+                    : launch_prefill<__half, false, true>(grid, st, pdl, mk, mv, mo, p);
+    }
+    if (bf)
+        return rope ? launch_prefill<__nv_bfloat16, true, false>(grid, st, pdl, mk, mv, mo, p)
+                    : launch_prefill<__nv_bfloat16, false, false>(grid, st, pdl, mk, mv, mo, p);
+    return rope ? launch_prefill<__half, true, false>(grid, st, pdl, mk, mv, mo, p)
+                : launch_prefill<__half, false, false>(grid, st, pdl, mk, mv, mo, p);
+}
+}  // namespace
+
+extern "C" kvd_status kvd_prefill_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads,
+                                       int32_t max_len, const void* q, const kvd_cache* kv,
+                                       const void* k_new, const void* v_new,
+                                       const int32_t* lens_in, const int32_t* plens,
+                                       int32_t* lens_out, float scale, float rope_base,
+                                       void* out, uint32_t flags, int32_t* dev_err,
+                                       kvd_stream_t stream) {
+    return prefill(dtype, batch, n_q_heads, max_len, q, kv, k_new, v_new, lens_in, plens,
+                   lens_out, 0, 0, scale, rope_base, out, flags, dev_err,
+                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" kvd_status kvd_prefill_window_attn(
+    kvd_dtype dtype, int32_t batch, int32_t n_q_heads, int32_t max_len, const void* q,
+    const kvd_cache* kv, const void* k_new, const void* v_new, const int32_t* lens_in,
+    const int32_t* plens, int32_t* lens_out, int32_t window, int32_t n_sinks, float scale,
+    float rope_base, void* out, uint32_t flags, int32_t* dev_err, kvd_stream_t stream) {
+    if (window < 1 || n_sinks < 0) return KVD_ERR_INVALID_ARG;
+    return prefill(dtype, batch, n_q_heads, max_len, q, kv, k_new, v_new, lens_in, plens,
+                   lens_out, window, n_sinks, scale, rope_base, out, flags, dev_err,
+                   reinterpret_cast<cudaStream_t>(stream));
 }

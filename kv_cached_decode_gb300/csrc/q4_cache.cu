@@ -1,0 +1,263 @@
+// q4_cache.cu -- the 4-bit cache's rows: quantise and append, and read back in 16 bits.
+//
+// A row is 64 values of one head at one position: n in 0..15 (32 bytes), a bfloat16 step
+// and a binary16 zero point z, value = step * (n - z). The step has bfloat16's exponent
+// range (any input range fits), the zero point binary16's 11 bits (|z| <= 15 * 2^11 for
+// inputs of 11 bits). Both are rounded BEFORE n is formed, so their rounding moves the
+// grid and is not an error of every value.
+//
+// Design. Both kernels are bound by HBM on a prompt (append: 128 bytes read and 36 written
+// per row; read-back the other way round) and by the launch on a step. Four lanes own a
+// row, 16 values (two 16-byte accesses) each: minimum and maximum take two shuffles, and
+// every lane packs its own 8 bytes. Division, subtraction and rounding are the IEEE
+// operations, in one fixed order, so that the stored bits follow from the definition on
+// any machine.
+#include "kvd_common.cuh"
+#include "kvd_internal.h"
+
+namespace kvd {
+namespace {
+
+constexpr int kQ4Threads = 256;
+
+struct Q4RowsParams {
+    uint8_t* data[2];     // K, V rows of the cache
+    uint8_t* params;
+    const uint8_t* in[2];  // append: the new K, V
+    uint8_t* out[2];       // read-back
+    int64_t sb, sh;        // rows
+    const int32_t* pos0;   // lens_in of the append
+    const int32_t* counts;
+    int32_t* lens_out;
+    int32_t* dev_err;
+    int32_t capacity, heads, n;
+    int64_t rows;          // batch * heads * n, per tensor
+};
+
+__device__ __forceinline__ float bf16_up(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ uint16_t f2bf(float x) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+// Quantise the 16 values of this lane (a quarter of a row; the row's lanes are lane ^ 1,
+// ^ 2, ^ 3): packed nibbles and the row's (step | zero point << 16). bad: the row holds an
+// infinity or a NaN.
+__device__ __forceinline__ uint2 quantise16(const float* x, uint32_t& par, bool& bad) {
+    float lo = x[0], hi = x[0], odd = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        lo = fminf(lo, x[e]);
+        hi = fmaxf(hi, x[e]);
+        odd = fmaf(x[e], 0.f, odd);  // 0, or NaN from an infinity or a NaN
+    }
+#pragma unroll
+    for (int off = 1; off <= 2; off <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+        odd += __shfl_xor_sync(0xffffffffu, odd, off);
+    }
+    bad = !(odd == 0.f);
+    // halves: no finite range overflows
+    uint16_t sbits =
+        f2bf(__fdiv_rn(__fsub_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo)), 7.5f));
+    float step = bf16_up(sbits), z;
+    if (step == 0.f) {
+        sbits = f2bf(__fdiv_rn(fabsf(lo), 15.f));
+        step = bf16_up(sbits);
+        if (step == 0.f) {
+            sbits = f2bf(1.f);
+            step = 1.f;
+        }
+        z = lo < 0.f ? 15.f : 0.f;
+    } else {
+        z = __half2float(__float2half_rn(__fdiv_rn(-lo, step)));
+    }
+    par = (uint32_t)sbits | ((uint32_t)__half_as_ushort(__float2half_rn(z)) << 16);
+    if (bad) {
+        par = 0x7FC0u;
+        return make_uint2(0u, 0u);
+    }
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float t = rintf(__fadd_rn(__fdiv_rn(x[e], step), z));
+        const uint32_t n = (uint32_t)fminf(fmaxf(t, 0.f), 15.f);
+        w[e >> 3] |= n << (4 * (e & 7));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+struct Q4Row {
+    int b, h, j;
+};
+__device__ __forceinline__ Q4Row split_row(const Q4RowsParams& p, int64_t row) {
+    Q4Row r;
+    r.j = (int)(row % p.n);
+    const int64_t bh = row / p.n;
+    r.h = (int)(bh % p.heads);
+    r.b = (int)(bh / p.heads);
+    return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4RowsParams p) {
+    pdl_wait();
+    const int64_t idx = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x;
+    const int l = (int)(idx & 3);
+    int64_t row = idx >> 2;
+    const int t = row >= p.rows ? 1 : 0;  // K rows, then V rows
+    row -= t ? p.rows : 0;
+    bool live = row < p.rows;
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    Q4Row r = {0, 0, 0};
+    int len = 0;
+    if (live) {
+        r = split_row(p, row);
+        len = p.pos0 ? p.pos0[r.b] : 0;
+        const int cnt = p.counts ? p.counts[r.b] : p.n;
+        const bool first = t == 0 && r.h == 0 && r.j == 0 && l == 0;
+        const bool wrong = len < 0 || cnt < 0 || cnt > p.n || (int64_t)len + cnt > p.capacity;
+        if (first && wrong) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+        if (first && p.lens_out) p.lens_out[r.b] = wrong ? len : len + cnt;
+        live = !wrong && r.j < cnt;
+    }
+    if (live) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.in[t] + row * kRowBytes + l * 32);
+        const uint4 a = src[0], b = src[1];
+        unpack8<T>(a, x);
+        unpack8<T>(b, x + 8);
+    }
+    uint32_t par;
+    bool bad;
+    const uint2 w = quantise16(x, par, bad);  // every lane: the shuffles need whole rows
+    if (live) {
+        const int64_t at = r.b * p.sb + r.h * p.sh + len + r.j;
+        *reinterpret_cast<uint2*>(p.data[t] + at * 32 + l * 8) = w;
+        if (l == 0) {
+            *reinterpret_cast<uint32_t*>(p.params + at * 8 + t * 4) = par;
+            if (bad) flag_error(p.dev_err, KVD_ERR_NAN);
+        }
+    }
+    pdl_trigger();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQ4Threads) q4_dequant_kernel(const Q4RowsParams p) {
+    pdl_wait();
+    const int64_t idx = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x;
+    const int l = (int)(idx & 3);
+    int64_t row = idx >> 2;
+    const int t = row >= p.rows ? 1 : 0;
+    row -= t ? p.rows : 0;
+    if (row < p.rows && p.out[t]) {
+        const Q4Row r = split_row(p, row);
+        const int pos = p.pos0 ? p.pos0[r.b] : 0;
+        if (pos < 0 || (int64_t)pos + p.n > p.capacity) {
+            if (r.h == 0 && r.j == 0 && l == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+        } else {
+            const int64_t at = r.b * p.sb + r.h * p.sh + pos + r.j;
+            const uint2 w = *reinterpret_cast<const uint2*>(p.data[t] + at * 32 + l * 8);
+            const uint32_t par = *reinterpret_cast<const uint32_t*>(p.params + at * 8 + t * 4);
+            const float step = bf16_up((uint16_t)par);
+            const float z = __half2float(__ushort_as_half((uint16_t)(par >> 16)));
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t v = (e < 4 ? w.x : w.y) >> (8 * (e & 3));
+                o[e] = Half16<T>::from_f2(__fmul_rn(step, (float)(v & 15u) - z),
+                                          __fmul_rn(step, (float)((v >> 4) & 15u) - z));
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.out[t] + row * kRowBytes + l * 32);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
+    pdl_trigger();
+}
+
+kvd_status rows_params(Q4RowsParams& p, const kvd_q4_cache* c, int32_t batch, int32_t n,
+                       dim3& grid) {
+    p.data[0] = static_cast<uint8_t*>(c->k);
+    p.data[1] = static_cast<uint8_t*>(c->v);
+    p.params = static_cast<uint8_t*>(c->params);
+    p.sb = c->stride_b;
+    p.sh = c->stride_h;
+    p.capacity = c->capacity;
+    p.heads = c->n_kv_heads;
+    p.n = n;
+    p.rows = (int64_t)batch * c->n_kv_heads * n;
+    const int64_t blocks = (2 * p.rows * 4 + kQ4Threads - 1) / kQ4Threads;
+    if (blocks > 0x7fffffff) return KVD_ERR_UNSUPPORTED;
+    grid = dim3((unsigned)blocks);
+    return KVD_OK;
+}
+
+}  // namespace
+
+kvd_status validate_q4_cache(const kvd_q4_cache* c) {
+    if (!c || !c->k || !c->v || !c->params) return KVD_ERR_INVALID_ARG;
+    if (c->head_dim != KVD_HEAD_DIM) return KVD_ERR_UNSUPPORTED;
+    if (c->batch <= 0 || c->n_kv_heads <= 0 || c->capacity <= 0) return KVD_ERR_INVALID_ARG;
+    if (c->capacity > (1 << 30)) return KVD_ERR_UNSUPPORTED;  // positions + a tile fit an int
+    if ((c->batch > 1 && c->stride_b < c->capacity) || c->stride_b < 0 ||
+        (c->n_kv_heads > 1 && c->stride_h < c->capacity) || c->stride_h < 0)
+        return KVD_ERR_INVALID_ARG;  // a head's positions are consecutive rows
+    if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->params) & 7))
+        return KVD_ERR_INVALID_ARG;
+    return KVD_OK;
+}
+
+}  // namespace kvd
+
+using namespace kvd;
+
+extern "C" kvd_status kvd_q4_append(kvd_dtype dtype, const kvd_q4_cache* cache, int32_t batch,
+                                    int32_t q, const void* k_new, const void* v_new,
+                                    const int32_t* lens_in, const int32_t* counts,
+                                    int32_t* lens_out, uint32_t flags, int32_t* dev_err,
+                                    kvd_stream_t stream) {
+    if (dtype != KVD_F16 && dtype != KVD_BF16) return KVD_ERR_INVALID_ARG;
+    if (kvd_status s = validate_q4_cache(cache)) return s;
+    if (batch < 0 || q < 0 || batch > cache->batch) return KVD_ERR_INVALID_ARG;
+    if (batch == 0 || q == 0) return KVD_OK;
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return KVD_ERR_INVALID_ARG;
+    if (lens_out && (lens_out == lens_in || lens_out == counts)) return KVD_ERR_INVALID_ARG;
+    Q4RowsParams p = {};
+    dim3 grid;
+    if (kvd_status s = rows_params(p, cache, batch, q, grid)) return s;
+    p.in[0] = static_cast<const uint8_t*>(k_new);
+    p.in[1] = static_cast<const uint8_t*>(v_new);
+    p.pos0 = lens_in;
+    p.counts = counts;
+    p.lens_out = lens_out;
+    p.dev_err = dev_err;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool pdl = (flags & KVD_FLAG_PDL) != 0;
+    if (dtype == KVD_BF16)
+        return launch(q4_append_kernel<__nv_bfloat16>, grid, dim3(kQ4Threads), 0, st, pdl, p);
+    return launch(q4_append_kernel<__half>, grid, dim3(kQ4Threads), 0, st, pdl, p);
+}
+
+extern "C" kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache* cache, int32_t batch,
+                                     int32_t n, void* k_out, void* v_out, const int32_t* pos0,
+                                     uint32_t flags, int32_t* dev_err, kvd_stream_t stream) {
+    if (dtype != KVD_F16 && dtype != KVD_BF16) return KVD_ERR_INVALID_ARG;
+    if (kvd_status s = validate_q4_cache(cache)) return s;
+    if (batch < 0 || n < 0 || batch > cache->batch) return KVD_ERR_INVALID_ARG;
+    if (batch == 0 || n == 0 || (!k_out && !v_out)) return KVD_OK;
+    if (!aligned16(k_out) || !aligned16(v_out)) return KVD_ERR_INVALID_ARG;
+    Q4RowsParams p = {};
+    dim3 grid;
+    if (kvd_status s = rows_params(p, cache, batch, n, grid)) return s;
+    p.out[0] = static_cast<uint8_t*>(k_out);
+    p.out[1] = static_cast<uint8_t*>(v_out);
+    p.pos0 = pos0;
+    p.dev_err = dev_err;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool pdl = (flags & KVD_FLAG_PDL) != 0;
+    if (dtype == KVD_BF16)
+        return launch(q4_dequant_kernel<__nv_bfloat16>, grid, dim3(kQ4Threads), 0, st, pdl, p);
+    return launch(q4_dequant_kernel<__half>, grid, dim3(kQ4Threads), 0, st, pdl, p);
+}
