@@ -118,3 +118,36 @@ def norm_rope(x, w, pos, eps, base):
     t = pos[:, None, :, None].astype(np.float64) * theta
     c, s = np.cos(t), np.sin(t)
     return np.concatenate([a * c - b * s, b * c + a * s], -1), mag
+
+
+def sample(x, u, T=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One row of kvd_sample_filtered in 64 bits: (token, logprob, n_kept)."""
+    x = np.asarray(x, np.float64)
+    x = np.where(np.isnan(x), -np.inf, x)
+    order = np.lexsort((np.arange(len(x)), -x))
+    order = order[x[order] > -np.inf]
+    if len(order) == 0:
+        return -1, -np.inf, 0
+    if T == 0:
+        return int(order[0]), 0.0, 1
+    y = x[order]
+    with np.errstate(invalid="ignore", over="ignore"):
+        d = np.where(y == y[0], 0.0, (y - y[0]) / np.float64(T))
+    if top_k > 0:
+        order, d = order[:top_k], d[:top_k]
+    w = np.exp(d)
+    keep = len(w)
+    if top_p < 1:
+        c = np.cumsum(w)
+        keep = min(keep, max(1, int((c - w < np.float64(top_p) * c[-1]).sum())))
+    if min_p > 0:
+        keep = min(keep, max(1, int((w >= min(1.0, np.float64(min_p))).sum())))
+    ids, w = order[:keep], w[:keep]
+    at = np.argsort(ids)
+    ids, w = ids[at], w[at]
+    c = np.cumsum(w)
+    over = np.flatnonzero(c > np.float64(u) * c[-1])
+    i = int(over[0]) if len(over) else int(np.flatnonzero(w > 0)[-1])
+    rest = np.delete(w, i).sum()
+    lp = np.log1p(-rest / c[-1]) if w[i] > c[-1] / 2 else np.log(w[i] / c[-1])
+    return int(ids[i]), float(lp), keep
