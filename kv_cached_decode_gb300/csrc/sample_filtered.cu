@@ -10,26 +10,37 @@
 //
 // Masses. A draw moves to another id when a running sum moves across u * total, so fp32
 // sums in whatever order would give other tokens run by run. Here w is an integer in units
-// of 2^-44 and sums are integers: the same on every run and for every split of the row. w
-// itself is 2^-y with y = (max - x) * log2(e) / T carried in two floats, taken apart as
-// 2^-n * 2^(-j/256) (a table) * 2^-r, |r| <= 2^-9 (a cubic): relative error below 2^-31, at
-// about thirty fp32/integer instructions -- double precision would be 30 times slower here.
-// Where w is below 2^-45.5 it is 0.
+// of 2^-44 and sums are integers: the same on every run and for every split of the row. What
+// counts is the sum of all errors against the spacing of the running sums, so w has no bias:
+// w = 2^-y, y = (max - x) * log2(e) / T carried in two floats. For y < 16 (heavy ids) y is
+// taken apart as n + j/256 + r: a table, a cubic in r, a relative 2^-29, about 30 instructions.
+// Below (light ids), fp32 rounding of y (unbiased, its constant in two floats) and the
+// hardware's 2^x, whose measured mean error of 3.47e-8 is taken off, are 2^-33 absolute at a
+// third of the price. Below 2^-45.5 w is 0. (Double precision would be 30 times slower here.)
 //
 // Design. Bound by the chain of passes and exchanges for few rows, by instruction issue (the
-// weights) for many; the logits are read from HBM once. One thread-block cluster per row;
-// CTA c keeps the ids [c * slice, (c + 1) * slice) in shared memory.
-//  1. Load, largest logit (lowest id first), number of logits above -inf: one exchange.
-//  2. select(): the k-th id (counts) or the id at which the mass reaches its target. A
-//     histogram of 2048 bins over y (bins fall with x, so they are intervals of the order;
-//     counts, and 64-bit masses in the second case), summed over the cluster through
-//     distributed shared memory (each CTA a share of the bins), names the bin. If at most
-//     kList ids are in it, every CTA gathers them and ranks them all against all; else the
-//     interval of their bit patterns is cut into 2048 again, until few are left or all are
-//     equal, when the cut falls by id.
-//  3. The kept ids' mass per 512-thread segment of the slice; one exchange; the CTA that holds
-//     u * total scans that segment and writes the row's outputs. The others have exited.
+// weights) for many. One thread-block cluster per row; CTA c has the ids [c * slice, (c + 1) *
+// slice), each warp a segment of them. Slices of at most kKeep logits stay in shared memory;
+// longer ones (many rows: fewer CTAs per row, one wave) are read again from L2, where a whole
+// batch fits, so that two CTAs fit on an SM.
+//  1. Read, largest logit (lowest id first), number of logits above -inf: one exchange.
+//  2. Every warp lists the places of the heavy ids of its segment (eight ids per lane and one
+//     warp scan: no atomics) and sums the mass of the light ones. What follows works on the
+//     lists (half of flat, a few of peaked logits), unless a cut lies among the light ids: then
+//     it takes all ids.
+//  3. select(): the k-th id (counts) or the id at which the mass reaches its target. A
+//     histogram of 1024 bins over y (bins fall with x, so they are intervals of the order;
+//     counts, or 64-bit masses as two 32-bit additions: a 64-bit one in shared memory is a
+//     loop of exchanges, measured several times slower) and the sums of every 32 bins; through
+//     distributed shared memory every CTA finds the group, then the bin (reading all bins of
+//     all CTAs instead takes longer than both). If at most kList ids are in it, every CTA
+//     gathers them and ranks them all against all; else the interval of their bit patterns is
+//     cut into 1024 again, until few are left or all are equal, when the cut falls by id.
+//  4. The kept mass per warp segment; one exchange; the CTA that holds u * total scans that
+//     segment and writes the row's outputs. The others have exited.
+// Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p.
 #include <algorithm>
+#include <cstddef>
 #include <mutex>
 
 #include "kvd_common.cuh"
@@ -41,21 +52,25 @@ namespace {
 constexpr int kSfThreads = 512;
 constexpr int kSfWarps = kSfThreads / 32;
 constexpr int kSfMaxCluster = 16;
-constexpr int kBins = 2048;
+constexpr int kGroup = 32;                           // bins per group: a lane each
+constexpr int kGroups = 32;
+constexpr int kBins = kGroup * kGroups;
 constexpr int kList = 128;
+constexpr int kKeep = 8192;                          // logits of a slice kept in shared memory
+constexpr int kMaxSlice = KVD_MAX_VOCAB / kSfMaxCluster;
 constexpr float kYMax = 45.5f;                       // 2^-y below this is 0
-constexpr float kBinScale = (kBins - 1) / kYMax;     // the last bin: weight 0
+constexpr float kHeavy = 16.f;                       // y of the listed ids is below this
 constexpr unsigned long long kOne = 1ull << 44;      // w = 1
 
-// 2^(-j/256) in units of 2^-44, j < 256, from repeated products of 2^(-1/256).
+// 2^(-j/256) in units of 2^-30, j < 256, from repeated products of 2^(-1/256).
 struct PowTable {
-    unsigned long long t[256];
+    uint32_t t[256];
 };
 constexpr PowTable make_pow_table() {
     PowTable p = {};
-    double v = 17592186044416.0;  // 2^44
+    double v = 1073741824.0;  // 2^30
     for (int j = 0; j < 256; ++j) {
-        p.t[j] = (unsigned long long)(v + 0.5);
+        p.t[j] = (uint32_t)(v + 0.5);
         v *= 0.99729605608547012625;  // 2^(-1/256)
     }
     return p;
@@ -83,30 +98,39 @@ struct Entry {
     unsigned long long w;
 };
 
-struct FilterShared {
-    unsigned long long pow[256];
-    unsigned long long mass[kBins];
-    uint32_t cnt[kBins];
-    // exchanged: written by CTA c into slot c of every CTA
-    unsigned long long ex_best[kSfMaxCluster], ex_fin[kSfMaxCluster];
-    unsigned long long ex_a[kSfMaxCluster], ex_b[kSfMaxCluster];
-    unsigned long long res_mass;         // select's result, written by one CTA into all
-    uint32_t res_cnt, res_n;
-    int32_t res_bin;
-    uint32_t n_list;
+struct alignas(16) FilterShared {
+    uint32_t pow[256];
+    // one bin: its mass (or its count), low and high half. Cleared after every use.
+    uint2 hist[kBins];
+    unsigned long long group[kGroups];                  // sums of kGroup bins
+    unsigned long long part[kSfMaxCluster][kGroup];     // one row per CTA of the cluster
     Entry list[kList];                   // this CTA's members
     Entry all[kList];                    // the cluster's
-    unsigned long long red[kSfWarps], red2[kSfWarps];
+    // exchanged: written by CTA c into slot c of every CTA, each once per use below
+    unsigned long long ex_best[kSfMaxCluster], ex_sum[kSfMaxCluster], ex_light[kSfMaxCluster],
+        ex_key[kSfMaxCluster];
+    uint32_t ex_fin[kSfMaxCluster], ex_cnt[kSfMaxCluster], ex_tie[kSfMaxCluster];
+    unsigned long long red[kSfWarps];
+    uint32_t red32[kSfWarps], red_b[kSfWarps];
+    uint32_t n_list;
     float cut_x;
     int32_t cut_id;
     int32_t found;
+    // places of the listed ids in their warp's segment, a segment's length apart
+    alignas(16) uint16_t lists[kMaxSlice];
+    // (a slice of at most kKeep logits: lists in the first quarter, logits behind it)
 };
+static_assert(kKeep * 6 <= kMaxSlice * 2 && offsetof(FilterShared, lists) % 16 == 0,
+              "kept logits, in 16-byte stores");
+static_assert(kMaxSlice / kSfWarps <= 65536, "places in a segment are 16 bits");
 
-// Total order of floats as unsigned integers (-0 below +0; both compare equal as floats, so
-// callers order by the float first).
+// Total order of finite floats and infinities as unsigned integers (no -0 reaches it).
 __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t b = __float_as_uint(x);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
 __device__ __forceinline__ void st_cluster_u64(void* local, int rank, unsigned long long v) {
@@ -125,6 +149,14 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(const void* local, 
     unsigned long long v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];"
                  : "=l"(v)
+                 : "r"(map_shared(smem_u32(local), (uint32_t)rank))
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ ulonglong2 ld_cluster_2u64(const void* local, int rank) {
+    ulonglong2 v;
+    asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];"
+                 : "=l"(v.x), "=l"(v.y)
                  : "r"(map_shared(smem_u32(local), (uint32_t)rank))
                  : "memory");
     return v;
@@ -149,34 +181,44 @@ __device__ __forceinline__ void sync_row(int cluster) {
     }
 }
 
-// The row's weights. y in two floats (p, e).
+// The row's weights, in units of 2^-44.
 struct Weights {
     float m, ch, cl;  // largest logit; log2(e) / T in two floats
-    const unsigned long long* pow;
+    const uint32_t* pow;
 
-    // y's leading part, monotone in x; 0 at the largest, inf where the weight is 0 anyway
+    // y's leading part, monotone in x; 0 at the largest (which may be infinite)
     __device__ __forceinline__ float lead(float x) const {
-        return x == m ? 0.f : (m - x) * ch;
+        return (x == m ? 0.f : m - x) * ch;
     }
-    __device__ __forceinline__ unsigned long long of(float x) const {
-        if (x == m) return kOne;
-        const float d = m - x;
+    // y < kHeavy
+    __device__ __forceinline__ unsigned long long heavy(float x) const {
+        const float d = x == m ? 0.f : m - x;
         const float p = d * ch;
-        if (!(p < kYMax)) return 0ull;
         // m - x = d + dl exactly
         const float bb = d - m;
-        const float dl = (m - (d - bb)) - (x + bb);
+        const float dl = x == m ? 0.f : (m - (d - bb)) - (x + bb);
         const float e = fmaf(d, ch, -p) + fmaf(d, cl, dl * ch);
-        const int k = __float2int_rn(p * 256.f);
-        const float r = fmaf((float)k, -0.00390625f, p) + e;  // the first part is exact
-        const float z = r * -0.693147180559945f;
-        const float q = fmaf(z * z, fmaf(z, 0.16666667f, 0.5f), z);  // 2^-r - 1
-        const unsigned long long t = pow[k & 255];
-        const int n = k >> 8;
-        const long long w =
-            (long long)t +
-            (((long long)(int32_t)(t >> 14) * (long long)__float2int_rn(q * 0x1p40f)) >> 26);
-        return ((unsigned long long)w + ((1ull << n) >> 1)) >> n;
+        // k = p * 256 rounded, in the low bits of kf + 1.5 * 2^23
+        const float ks = fmaf(p, 256.f, 12582912.f), kf = ks - 12582912.f;
+        const float r = fmaf(kf, -0.00390625f, p) + e;  // the first part is exact; |r| <= 2^-9
+        // (2^-r - 1) * 2^32: -r ln 2 + (r ln 2)^2 / 2 - (r ln 2)^3 / 6
+        const float q = r * fmaf(r, fmaf(r, -238388331.5f, 1031764992.f), -2977044471.8f);
+        const int k = __float_as_int(ks) & 0x3FFF, n = k >> 8;  // n <= 16
+        const int t = (int)pow[k & 255];
+        // * 2^(14 - n), as a 32 x 32 -> 64 bit product
+        return (unsigned long long)(uint32_t)(t + __mulhi(t, __float2int_rn(q))) *
+                   (65536u >> n) >> 2;
+    }
+    // y >= kHeavy; 0 for -inf
+    __device__ __forceinline__ uint32_t light(float x) const {
+        const float d = m - x;
+        // 2^a, at most 2^28 (far below 2^-1 the sums may overflow, or be NaN for -inf)
+        const float a = d * ch < 64.f ? 44.f - fmaf(d, ch, d * cl) : -10.f;
+        const uint32_t w = __float2uint_rn(ex2_approx(a));
+        return w - __umulhi(w, 149u);  // 149 / 2^32 = 3.47e-8
+    }
+    __device__ __forceinline__ unsigned long long of(float x) const {
+        return lead(x) < kHeavy ? heavy(x) : (unsigned long long)light(x);
     }
 };
 
@@ -208,225 +250,239 @@ struct Cut {
     }
 };
 
+// Sum over the warp, to every lane (of values whose sum is below 2^64).
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+    const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x3FFFFFu);
+    const uint32_t b = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 22) & 0x3FFFFFu);
+    const uint32_t c = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 44));
+    return a + ((unsigned long long)b << 22) + ((unsigned long long)c << 44);
 }
-// Sum over the block of two values, to every thread. Ends with the arrays free for reuse.
-__device__ __forceinline__ void block_sum2(FilterShared& S, unsigned long long& a,
-                                           unsigned long long& b) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (lane == 0) {
-        S.red[warp] = a;
-        S.red2[warp] = b;
-    }
-    __syncthreads();
-    a = b = 0;
-#pragma unroll
-    for (int w = 0; w < kSfWarps; ++w) {
-        a += S.red[w];
-        b += S.red2[w];
-    }
-    __syncthreads();
-}
-// Exclusive prefix over the block (thread order) of v.
-__device__ __forceinline__ unsigned long long block_excl(FilterShared& S, unsigned long long v) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long inc = v;
+__device__ __forceinline__ unsigned long long warp_incl(unsigned long long v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += o;
+        const unsigned long long o = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += o;
     }
+    return v;
+}
+// Exclusive prefix over the block (thread order) of v, and the block's total. `red` is free
+// for reuse only after the next block barrier.
+__device__ __forceinline__ unsigned long long block_excl(FilterShared& S, unsigned long long v,
+                                                         unsigned long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned long long inc = warp_incl(v);
     if (lane == 31) S.red[warp] = inc;
     __syncthreads();
-    unsigned long long base = 0;
-#pragma unroll
-    for (int w = 0; w < kSfWarps; ++w) base += w < warp ? S.red[w] : 0ull;
-    __syncthreads();
-    return base + inc - v;
+    const unsigned long long w = lane < kSfWarps ? S.red[lane] : 0ull;
+    total = warp_sum(w);
+    return warp_sum(lane < warp ? w : 0ull) + inc - v;
 }
 
 struct Row {
-    const float* x;  // this CTA's logits in shared memory (NaN replaced by -inf)
-    int n, lo;       // how many, and the first one's id
+    const float* x;  // this CTA's logits: in shared memory, or where they were given
+    int n, lo, seg;  // logits here, the first one's id, logits per warp segment
     int rank, cluster;
+    int w0, wn, wl;  // this warp's segment: first logit, logits, listed ones
+    uint16_t* lj;    // the slice's lists, warp w's from w0 on
+
+    __device__ __forceinline__ float at(int i) const {
+        const float v = x[i];
+        return isnan(v) ? -INFINITY : v + 0.f;  // -0 and +0 are one value
+    }
 };
+// f(x, i) for the logits of this warp's segment: the listed ones, or all. The loads of several
+// go first (f's atomics would hold later ones back).
+template <typename F>
+__device__ __forceinline__ void for_ids(const Row& R, bool full, F&& f) {
+    const int lane = threadIdx.x & 31;
+    if (full) {
+        constexpr int G = 8;
+#pragma unroll 1
+        for (int j0 = lane; j0 < R.wn; j0 += 32 * G) {
+            float v[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) v[g] = R.at(R.w0 + min(j0 + 32 * g, R.wn - 1));
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (j0 + 32 * g < R.wn) f(v[g], R.w0 + j0 + 32 * g);
+        }
+    } else {
+        constexpr int G = 8;
+        const uint16_t* lj = R.lj + R.w0;
+#pragma unroll 1
+        for (int j0 = lane; j0 < R.wl; j0 += 32 * G) {
+            float v[G];
+            int i[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) i[g] = R.w0 + lj[min(j0 + 32 * g, R.wl - 1)];
+#pragma unroll
+            for (int g = 0; g < G; ++g) v[g] = R.x[i[g]] + 0.f;  // (never a NaN)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (j0 + 32 * g < R.wl) f(v[g], i[g]);
+        }
+    }
+}
+
+enum SelectResult { kCutHere, kBeyond, kAll };
 
 // The last id of the shortest prefix (within `kept`) that holds `k` ids (MASS false) or whose
-// mass reaches frac * (mass of `kept`) (MASS true; frac < 1). Returns false, leaving `kept`, when the
-// prefix ends among ids of weight 0. Every thread of the cluster calls it.
+// mass reaches frac * (mass of `kept`) (MASS true; frac < 1; `light`: this CTA's light mass, 0
+// when none of it is kept). Over the listed ids, or with `full` over all. Returns kBeyond,
+// leaving `kept`, when the cut is not among the listed ids; kAll when the prefix ends among
+// ids of weight 0. Every thread of the cluster calls it; the histogram is clear before and
+// after.
 template <bool MASS>
-__device__ bool select(FilterShared& S, const Row& R, const Weights& W, Cut& kept,
-                       unsigned long long k, float frac) {
-    const int tid = threadIdx.x;
+__device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, bool full,
+                               Cut& kept, unsigned long long k, float frac,
+                               unsigned long long light) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto clear_hist = [&]() {
+        for (int i = tid; i < kBins; i += kSfThreads) S.hist[i] = make_uint2(0u, 0u);
+        __syncthreads();
+    };
     // members of the current interval: all, then ordered keys in [klo, khi]
     bool first = true;
     uint32_t klo = 0, khi = 0;
     int shift = 0;
-    unsigned long long before_c = 0, before_m = 0;
-    unsigned long long target = k;  // the prefix is complete once its count or mass is this
+    unsigned long long before = 0;   // count or mass before the interval
+    unsigned long long target = k;   // the prefix is complete once its count or mass is this
+    const float scale = full ? kBins / kYMax : kBins / kHeavy;
     auto bin_of = [&](float x, bool& in) -> int {
         if (first) {
             const float y = W.lead(x);
-            in = y < kYMax;
-            return in ? (int)(y * kBinScale) : kBins - 1;
+            in = y < kYMax;  // (the listed ones are below kHeavy)
+            return min((int)(y * scale), kBins - 1);
         }
         const uint32_t key = ordered(x);
         in = key >= klo && key <= khi;
         return (int)((khi - key) >> shift);
     };
+    if (MASS) {
+        if (R.cluster > 1) {
+            if (tid < R.cluster) st_cluster_u64(&S.ex_light[R.rank], tid, light);
+        } else if (tid == 0) {
+            S.ex_light[0] = light;
+        }
+    }
     for (;;) {
         // ---- histogram of the members over the bins ----
-        for (int i = tid; i < kBins; i += kSfThreads) {
-            S.cnt[i] = 0;
-            if (MASS) S.mass[i] = 0;
-        }
-        __syncthreads();
-        for (int i = tid; i < R.n; i += kSfThreads) {
-            const float x = R.x[i];
+        for_ids(R, full, [&](float x, int i) {
             bool in;
             const int bin = bin_of(x, in);
             if (in && kept.keeps(x, R.lo + i)) {
-                atomicAdd(&S.cnt[bin], 1u);
-                if (MASS) atomicAdd(&S.mass[bin], W.of(x));
-            }
-        }
-        sync_row(R.cluster);
-        // ---- this CTA's share of the bins, summed over the cluster ----
-        const int share = kBins / R.cluster;  // a power of two of CTAs
-        const int per = (share + kSfThreads - 1) / kSfThreads;  // at most 4
-        unsigned long long c4[4], m4[4], cs = 0, ms = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            c4[j] = m4[j] = 0;
-            const int i = tid * per + j;
-            if (j < per && i < share) {
-                const int bin = R.rank * share + i;
-                for (int r = 0; r < R.cluster; ++r) {
-                    c4[j] += R.cluster > 1 ? ld_cluster_u32(&S.cnt[bin], r) : S.cnt[bin];
-                    if (MASS)
-                        m4[j] += R.cluster > 1 ? ld_cluster_u64(&S.mass[bin], r) : S.mass[bin];
+                if (MASS) {
+                    const unsigned long long w = full ? W.of(x) : W.heavy(x);
+                    const uint32_t lo = (uint32_t)w;
+                    const uint32_t old = atomicAdd(&S.hist[bin].x, lo);
+                    const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+                    if (hi) atomicAdd(&S.hist[bin].y, hi);
+                } else {
+                    atomicAdd(&S.hist[bin].x, 1u);
                 }
-                cs += c4[j];
-                ms += m4[j];
             }
-        }
-        unsigned long long pc = block_excl(S, cs), pm = MASS ? block_excl(S, ms) : 0ull;
-        if (tid == kSfThreads - 1) {  // the share's totals
-            S.red[0] = pc + cs;
-            S.red[1] = pm + ms;
-        }
+        });
         __syncthreads();
-        if (tid < R.cluster) {
-            if (R.cluster > 1) {
-                st_cluster_u64(&S.ex_a[R.rank], tid, S.red[0]);
-                st_cluster_u64(&S.ex_b[R.rank], tid, S.red[1]);
-            } else {
-                S.ex_a[0] = S.red[0];
-                S.ex_b[0] = S.red[1];
-            }
-        }
-        if (tid == 0) {
-            S.n_list = 0;  // (every CTA has read the last list: it has arrived above)
-            S.res_bin = -1;
-        }
-        sync_row(R.cluster);
-        unsigned long long tc = 0, tmass = 0;
-        for (int r = 0; r < R.cluster; ++r) {
-            if (r == R.rank) {
-                pc += tc;
-                pm += tmass;
-            }
-            tc += S.ex_a[r];
-            tmass += S.ex_b[r];
-        }
-        if (MASS && first) {
-            bool rest = false;
-            target = frac > 0.f ? mul_floor(frac, tmass, rest) : 0ull;
-            target = target + (rest ? 1 : 0);  // a mass reaches frac * tmass when it is >= this
-            if (target == 0) target = 1;
-        }
-        // ---- the bin at whose end the prefix is complete: one thread of the cluster has it ----
-        pc += before_c;
-        pm += before_m;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j >= per) break;
-            const bool here = MASS ? pm < target && pm + m4[j] >= target
-                                   : pc < target && pc + c4[j] >= target;
-            if (here && c4[j] > 0 && tid * per + j < share) {
-                for (int r = 0; r < R.cluster; ++r) {
-                    const int bin = R.rank * share + tid * per + j;
-                    if (R.cluster > 1) {
-                        st_cluster_u64(&S.res_mass, r, pm);
-                        st_cluster_u32(&S.res_cnt, r, (uint32_t)pc);
-                        st_cluster_u32(&S.res_n, r, (uint32_t)c4[j]);
-                        st_cluster_u32(&S.res_bin, r, (uint32_t)bin);
-                    } else {
-                        S.res_mass = pm;
-                        S.res_cnt = (uint32_t)pc;
-                        S.res_n = (uint32_t)c4[j];
-                        S.res_bin = bin;
-                    }
-                }
-            }
-            pc += c4[j];
-            pm += m4[j];
+        for (int h = 0; h < kGroups / kSfWarps; ++h) {
+            const int g = warp * (kGroups / kSfWarps) + h;
+            const uint2 v = S.hist[g * kGroup + lane];
+            const unsigned long long sum = warp_sum(((unsigned long long)v.y << 32) | v.x);
+            if (lane == 0) S.group[g] = sum;
         }
         sync_row(R.cluster);
-        const int bin = S.res_bin;
-        if (bin < 0) return false;  // it ends among ids of weight 0: nothing to cut
-        before_c = S.res_cnt;
-        before_m = S.res_mass;
-        const uint32_t n = S.res_n;
+        // ---- the group, then the bin in which the prefix becomes complete ----
+        // `from`: 32 sums in every CTA; lane l gets the cluster's l-th
+        auto sums_of = [&](const unsigned long long* from) -> unsigned long long {
+            if (R.cluster == 1) return from[lane];
+            if (warp < R.cluster) S.part[warp][lane] = ld_cluster_u64(from + lane, warp);
+            __syncthreads();
+            unsigned long long v = 0;
+#pragma unroll 4
+            for (int r = 0; r < R.cluster; ++r) v += S.part[r][lane];
+            __syncthreads();
+            return v;
+        };
+        if (tid == 0) S.n_list = 0;  // (every CTA has read the last list: it has arrived above)
+        unsigned long long v = sums_of(S.group);
+        unsigned long long inc = before + warp_incl(v);
+        if (first) {
+            const unsigned long long total = __shfl_sync(0xffffffffu, inc, 31);
+            if (MASS) {
+                bool rest = false;
+                const unsigned long long all =
+                    total + warp_sum(lane < R.cluster ? S.ex_light[lane] : 0ull);
+                target = frac > 0.f ? mul_floor(frac, all, rest) : 0ull;
+                target += rest ? 1 : 0;  // a mass reaches frac * all when it is >= this
+                if (target == 0) target = 1;
+            }
+            if (total < target) {  // the same in every CTA
+                sync_row(R.cluster);  // all have read the sums
+                clear_hist();
+                return full ? kAll : kBeyond;
+            }
+        }
+        uint32_t hit = __ballot_sync(0xffffffffu, inc >= target);
+        const int grp = hit ? __ffs(hit) - 1 : 0;
+        before = __shfl_sync(0xffffffffu, inc - v, grp);
+        v = sums_of(reinterpret_cast<const unsigned long long*>(S.hist) + grp * kGroup);
+        inc = before + warp_incl(v);
+        hit = __ballot_sync(0xffffffffu, inc >= target);
+        const int in_grp = hit ? __ffs(hit) - 1 : 0;
+        before = __shfl_sync(0xffffffffu, inc - v, in_grp);
+        const int bin = grp * kGroup + in_grp;
+        __syncthreads();  // n_list is 0
 
-        // ---- few members: gather and rank them ----
-        if (n <= kList) {
-            for (int i = tid; i < R.n; i += kSfThreads) {
-                const float x = R.x[i];
-                bool in;
-                const int mine = bin_of(x, in);
-                if (in && mine == bin && kept.keeps(x, R.lo + i)) {
-                    const uint32_t at = atomicAdd(&S.n_list, 1u);
-                    if (at < kList) {
-                        S.list[at].x = x;
-                        S.list[at].id = R.lo + i;
-                        S.list[at].w = MASS ? W.of(x) : 0ull;
-                    }
+        // ---- gather its members ----
+        for_ids(R, full, [&](float x, int i) {
+            bool in;
+            const int mine = bin_of(x, in);
+            if (in && mine == bin && kept.keeps(x, R.lo + i)) {
+                const uint32_t at = atomicAdd(&S.n_list, 1u);
+                if (at < kList) {
+                    S.list[at].x = x;
+                    S.list[at].id = R.lo + i;
+                    S.list[at].w = MASS ? W.of(x) : 1ull;
                 }
             }
-            sync_row(R.cluster);
-            if (R.cluster > 1) {
-                int base = 0;
+        });
+        sync_row(R.cluster);
+        clear_hist();  // all have read them
+        const uint32_t nr = lane < R.cluster
+                                ? (R.cluster > 1 ? ld_cluster_u32(&S.n_list, lane) : S.n_list)
+                                : 0u;
+        const uint32_t n = __reduce_add_sync(0xffffffffu, nr);
+
+        // ---- few: rank them all against all ----
+        if (n <= kList) {
+            // thread t: member t of the concatenated lists
+            if (tid < kList) {  // whole warps
+                uint32_t base = 0, off = 0;
+                int from = 0;
                 for (int r = 0; r < R.cluster; ++r) {
-                    const int nr = (int)ld_cluster_u32(&S.n_list, r);
-                    if (tid < nr && base + tid < kList) {
-                        const unsigned long long xi = ld_cluster_u64(&S.list[tid], r);
-                        S.all[base + tid].x = __uint_as_float((uint32_t)xi);
-                        S.all[base + tid].id = (int32_t)(xi >> 32);
-                        S.all[base + tid].w = ld_cluster_u64(&S.list[tid].w, r);
+                    const uint32_t c = __shfl_sync(0xffffffffu, nr, r);
+                    if ((uint32_t)tid >= base) {
+                        from = r;
+                        off = tid - base;
                     }
-                    base += nr;
+                    base += c;
                 }
-            } else if (tid < (int)n) {
-                S.all[tid] = S.list[tid];
+                if (tid < (int)n)
+                    *reinterpret_cast<ulonglong2*>(&S.all[tid]) =
+                        R.cluster > 1 ? ld_cluster_2u64(&S.list[off], from)
+                                      : *reinterpret_cast<const ulonglong2*>(&S.list[off]);
             }
             __syncthreads();
             if (tid < (int)n) {
                 const Entry me = S.all[tid];
-                unsigned long long c = before_c, mm = before_m;
+                unsigned long long sum = before;
+#pragma unroll 4
                 for (uint32_t i = 0; i < n; ++i) {
                     const Entry o = S.all[i];
-                    if (o.x > me.x || (o.x == me.x && o.id < me.id)) {
-                        ++c;
-                        mm += o.w;
-                    }
+                    sum += o.x > me.x || (o.x == me.x && o.id < me.id) ? o.w : 0ull;
                 }
-                if (MASS ? mm < target && mm + me.w >= target : c + 1 == target) {
+                if (sum < target && sum + me.w >= target) {
                     S.cut_x = me.x;
                     S.cut_id = me.id;
                 }
@@ -434,14 +490,13 @@ __device__ bool select(FilterShared& S, const Row& R, const Weights& W, Cut& kep
             __syncthreads();
             kept.x = S.cut_x;
             kept.id = S.cut_id;
-            // (every CTA has read the others' lists before the next exchange completes)
-            return true;
+            // (every CTA has read the others' lists before it arrives at the next exchange)
+            return kCutHere;
         }
 
         // ---- many: the interval of their bit patterns ----
         uint32_t lo = 0xffffffffu, hi = 0;
-        for (int i = tid; i < R.n; i += kSfThreads) {
-            const float x = R.x[i];
+        for_ids(R, full, [&](float x, int i) {
             bool in;
             const int mine = bin_of(x, in);
             if (in && mine == bin && kept.keeps(x, R.lo + i)) {
@@ -449,66 +504,68 @@ __device__ bool select(FilterShared& S, const Row& R, const Weights& W, Cut& kep
                 lo = min(lo, key);
                 hi = max(hi, key);
             }
-        }
+        });
+        __syncwarp();
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
-        if ((tid & 31) == 0) S.red[tid >> 5] = ((unsigned long long)lo << 32) | hi;
-        __syncthreads();
-        lo = 0xffffffffu;
-        hi = 0;
-        for (int w = 0; w < kSfWarps; ++w) {
-            lo = min(lo, (uint32_t)(S.red[w] >> 32));
-            hi = max(hi, (uint32_t)S.red[w]);
+        if (lane == 0) {
+            S.red32[tid >> 5] = lo;
+            S.red_b[tid >> 5] = hi;
         }
+        __syncthreads();
+        lo = __reduce_min_sync(0xffffffffu, S.red32[lane & (kSfWarps - 1)]);
+        hi = __reduce_max_sync(0xffffffffu, S.red_b[lane & (kSfWarps - 1)]);
         if (R.cluster > 1) {
             if (tid < R.cluster)
-                st_cluster_u64(&S.ex_a[R.rank], tid, ((unsigned long long)lo << 32) | hi);
+                st_cluster_u64(&S.ex_key[R.rank], tid, ((unsigned long long)lo << 32) | hi);
             sync_row(R.cluster);
-            for (int r = 0; r < R.cluster; ++r) {
-                lo = min(lo, (uint32_t)(S.ex_a[r] >> 32));
-                hi = max(hi, (uint32_t)S.ex_a[r]);
-            }
+            const unsigned long long v = S.ex_key[lane & (R.cluster - 1)];
+            lo = __reduce_min_sync(0xffffffffu, (uint32_t)(v >> 32));
+            hi = __reduce_max_sync(0xffffffffu, (uint32_t)v);
         }
-        __syncthreads();
         first = false;
         klo = lo;
         khi = hi;
         if (klo < khi) {
             // cut (khi - klo + 1) patterns into at most kBins intervals
-            shift = max(0, 32 - __clz(khi - klo) - 11);
+            static_assert(kBins == 1024, "the shift below");
+            shift = max(0, 32 - __clz(khi - klo) - 10);
             continue;
         }
 
-        // ---- all equal: the cut falls by id. r: how many of them stay ----
-        unsigned long long take;
+        // ---- all equal: the cut falls by id; the take-th of them is the last to stay ----
+        const float xv = unordered(klo);
+        unsigned long long take = target - before;
         if (MASS) {
-            const float xv = __uint_as_float(klo & 0x80000000u ? klo & 0x7fffffffu : ~klo);
             const unsigned long long w = W.of(xv);
-            take = (target - before_m + w - 1) / w;  // the least r with r * w enough; w > 0
-        } else {
-            take = target - before_c;
+            take = (take + w - 1) / w;  // the least number with enough mass; w > 0
         }
         auto member = [&](int i) {
-            return ordered(R.x[i]) == klo && kept.keeps(R.x[i], R.lo + i);
+            const float x = R.at(i);
+            return ordered(x) == klo && kept.keeps(x, R.lo + i);
         };
-        unsigned long long c = 0, none = 0;
+        uint32_t c = 0;
         for (int i = tid; i < R.n; i += kSfThreads) c += member(i);
-        block_sum2(S, c, none);
+        c = __reduce_add_sync(0xffffffffu, c);
+        __syncthreads();
+        if (lane == 0) S.red32[tid >> 5] = c;
+        __syncthreads();
+        c = __reduce_add_sync(0xffffffffu, lane < kSfWarps ? S.red32[lane] : 0u);
         if (R.cluster > 1) {
-            if (tid < R.cluster) st_cluster_u64(&S.ex_b[R.rank], tid, c);
+            if (tid < R.cluster) st_cluster_u32(&S.ex_tie[R.rank], tid, c);
             sync_row(R.cluster);
         } else {
-            if (tid == 0) S.ex_b[0] = c;
+            if (tid == 0) S.ex_tie[0] = c;
             __syncthreads();
         }
         unsigned long long run = 0;
         int owner = 0;
         for (int r = 0; r < R.cluster; ++r) {
-            if (run + S.ex_b[r] >= take) {
+            if (run + S.ex_tie[r] >= take) {
                 owner = r;
                 break;
             }
-            run += S.ex_b[r];
+            run += S.ex_tie[r];
         }
         take -= run;  // the take-th member of the owner's, in id order
         if (owner == R.rank) {
@@ -517,7 +574,8 @@ __device__ bool select(FilterShared& S, const Row& R, const Weights& W, Cut& kep
             for (int i0 = 0; i0 < R.n; i0 += kSfThreads) {
                 const int i = i0 + tid;
                 const bool mine = i < R.n && member(i);
-                const unsigned long long ex = block_excl(S, mine ? 1ull : 0ull);
+                unsigned long long all;
+                const unsigned long long ex = block_excl(S, mine ? 1ull : 0ull, all);
                 if (mine && seen + ex + 1 == take) {
                     if (R.cluster > 1)
                         for (int r = 0; r < R.cluster; ++r)
@@ -525,23 +583,21 @@ __device__ bool select(FilterShared& S, const Row& R, const Weights& W, Cut& kep
                     else
                         S.cut_id = R.lo + i;
                 }
-                unsigned long long all = mine ? 1ull : 0ull, none2 = 0;
-                block_sum2(S, all, none2);
+                __syncthreads();
                 seen += all;
                 if (seen >= take) break;
             }
         }
         sync_row(R.cluster);
-        kept.x = __uint_as_float(klo & 0x80000000u ? klo & 0x7fffffffu : ~klo);
+        kept.x = xv;
         kept.id = S.cut_id;
-        return true;
+        return kCutHere;
     }
 }
 
 __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const FilterParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     FilterShared& S = *reinterpret_cast<FilterShared*>(smem_raw);
-    float* xs = reinterpret_cast<float*>(smem_raw + sizeof(FilterShared));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Row R;
     R.cluster = p.cluster;
@@ -549,8 +605,11 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     const int b = (int)(blockIdx.x / (unsigned)p.cluster);
     R.lo = R.rank * p.slice;
     R.n = max(0, min(p.slice, p.vocab - R.lo));
-    R.x = xs;
+    R.seg = p.slice / kSfWarps;
+    R.w0 = warp * R.seg;
+    R.wn = max(0, min(R.seg, R.n - R.w0));
     if (tid < 256) S.pow[tid] = g_pow.t[tid];
+    for (int i = tid; i < kBins; i += kSfThreads) S.hist[i] = make_uint2(0u, 0u);
     pdl_wait();
     pdl_trigger();
     const float T = p.temperature ? p.temperature[b] : 1.f;
@@ -564,66 +623,87 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         return;
     }
 
-    // ---- 1. load; the largest logit, lowest id first; how many are above -inf ----
+    // ---- 1. read; the largest logit, lowest id first; how many are above -inf ----
     const float* src = p.logits + (int64_t)b * p.row_stride + R.lo;
-    unsigned long long best = 0;  // (ordered x, ~id)
+    const bool keep = p.slice <= kKeep;
+    R.lj = S.lists;
+    float* xs = reinterpret_cast<float*>(S.lists + kKeep);  // (keep)
+    R.x = keep ? xs : src;
+    // 16-byte loads where the row allows (segments start at multiples of 32 ids)
+    const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+    const int whole = wide ? R.wn & ~3 : 0;
+    float top = -INFINITY;
+    int top_i = 0;
     uint32_t n_fin = 0;
     bool nan = false;
-    constexpr int G = 8;
-    for (int i0 = tid; i0 < R.n; i0 += G * kSfThreads) {
-        float v[G];
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-            const int i = i0 + j * kSfThreads;
-            v[j] = i < R.n ? __ldcs(src + i) : -INFINITY;
+    auto take = [&](float x, int i) -> float {  // ids ascend within a thread
+        nan |= isnan(x);
+        n_fin += x > -INFINITY;
+        if (x > top) {
+            top = x;
+            top_i = i;
         }
+        return x;
+    };
+    for (int j0 = lane * 4; j0 < whole; j0 += 512) {
+        float4 v[4];
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-            const int i = i0 + j * kSfThreads;
-            if (i >= R.n) break;
-            float x = v[j];
-            if (isnan(x)) {
-                nan = true;
-                x = -INFINITY;
+        for (int g = 0; g < 4; ++g)
+            v[g] = __ldg(
+                reinterpret_cast<const float4*>(src + R.w0 + min(j0 + g * 128, whole - 4)));
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int i = R.w0 + j0 + g * 128;
+            if (j0 + g * 128 < whole) {
+                take(v[g].x, i);
+                take(v[g].y, i + 1);
+                take(v[g].z, i + 2);
+                take(v[g].w, i + 3);
+                if (keep) *reinterpret_cast<float4*>(xs + i) = v[g];
             }
-            x = x == 0.f ? 0.f : x;  // -0 and +0 are one value
-            xs[i] = x;
-            n_fin += x > -INFINITY;
-            const unsigned long long key =
-                ((unsigned long long)ordered(x) << 32) | (uint32_t)~(R.lo + i);
-            best = key > best ? key : best;
+        }
+    }
+    for (int j = whole + lane; j < R.wn; j += 256) {
+        float v[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) v[g] = __ldg(src + R.w0 + min(j + 32 * g, R.wn - 1));
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+            if (j + 32 * g < R.wn) {
+                take(v[g], R.w0 + j + 32 * g);
+                if (keep) xs[R.w0 + j + 32 * g] = v[g];
+            }
+    }
+    const uint32_t fin_w = __reduce_add_sync(0xffffffffu, n_fin);
+    {
+        // the warp's largest, then the lowest id that has it (0: nothing above -inf)
+        const uint32_t key = top > -INFINITY ? ordered(top + 0.f) : 0u;
+        const uint32_t mk = __reduce_max_sync(0xffffffffu, key);
+        const uint32_t mi =
+            __reduce_min_sync(0xffffffffu, key == mk ? (uint32_t)(R.lo + top_i) : 0xffffffffu);
+        if (lane == 0) {
+            S.red[warp] = mk ? ((unsigned long long)mk << 32) | (uint32_t)~mi : 0ull;
+            S.red32[warp] = fin_w;
         }
     }
     if (__syncthreads_or(nan) && tid == 0) flag_error(p.dev_err, KVD_ERR_NAN);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, off);
-        best = o > best ? o : best;
-    }
-    n_fin = __reduce_add_sync(0xffffffffu, n_fin);
-    if (lane == 0) {
-        S.red[warp] = best;
-        S.red2[warp] = n_fin;
-    }
-    __syncthreads();
-    unsigned long long fin = 0;
-    for (int w = 0; w < kSfWarps; ++w) {
-        best = S.red[w] > best ? S.red[w] : best;
-        fin += S.red2[w];
-    }
+    auto best_of = [&](unsigned long long v) {  // the largest of the warp's
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+        const uint32_t lo =
+            __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+        return ((unsigned long long)hi << 32) | lo;
+    };
+    unsigned long long best = best_of(lane < kSfWarps ? S.red[lane] : 0ull);
+    uint32_t fin = __reduce_add_sync(0xffffffffu, lane < kSfWarps ? S.red32[lane] : 0u);
     if (R.cluster > 1) {
         if (tid < R.cluster) {
             st_cluster_u64(&S.ex_best[R.rank], tid, best);
-            st_cluster_u64(&S.ex_fin[R.rank], tid, fin);
+            st_cluster_u32(&S.ex_fin[R.rank], tid, fin);
         }
         sync_row(R.cluster);
-        best = fin = 0;
-        for (int r = 0; r < R.cluster; ++r) {
-            best = S.ex_best[r] > best ? S.ex_best[r] : best;
-            fin += S.ex_fin[r];
-        }
+        best = best_of(lane < R.cluster ? S.ex_best[lane] : 0ull);
+        fin = __reduce_add_sync(0xffffffffu, lane < R.cluster ? S.ex_fin[lane] : 0u);
     }
-    __syncthreads();
     if (fin == 0) {
         if (tid == 0 && R.rank == 0) {
             p.token[b] = -1;
@@ -642,8 +722,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         return;
     }
     Weights W;
-    const uint32_t mk = (uint32_t)(best >> 32);
-    W.m = __uint_as_float(mk & 0x80000000u ? mk & 0x7fffffffu : ~mk);
+    W.m = unordered((uint32_t)(best >> 32));
     W.pow = S.pow;
     {
         // log2(e) = 0x1.715476p0 + 0x1.4ae0cp-26, over T
@@ -653,11 +732,104 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         W.cl = q < 3e38f ? __fdiv_rn(fmaf(-q, T, h) + l, T) : 0.f;
     }
 
-    // ---- 2. the filters ----
+    // ---- 2. the heavy ids of this warp's segment; the light ones' mass ----
+    // (a top-k that cuts leaves no light id, or all ids are looked at)
+    const bool cuts = top_k > 0 && (uint32_t)top_k < fin;
+    unsigned long long light_w = 0;
+    R.wl = 0;
+    const bool finite = W.m < INFINITY;
+    if (finite) {
+        const bool quads = keep || wide;
+        // eight logits per lane of the 256 from jb on; place e of them
+        auto place = [&](int jb, int e, bool q) {
+            return q ? jb + lane * 4 + (e & 3) + 128 * (e >> 2) : jb + lane + 32 * e;
+        };
+        auto load8 = [&](int jb, float (&x)[8]) {
+            if (quads && jb + 256 <= R.wn) {
+                const float4 a = *reinterpret_cast<const float4*>(R.x + R.w0 + jb + lane * 4);
+                const float4 c =
+                    *reinterpret_cast<const float4*>(R.x + R.w0 + jb + lane * 4 + 128);
+                x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+                x[4] = c.x; x[5] = c.y; x[6] = c.z; x[7] = c.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = jb + lane + 32 * e;
+                    x[e] = j < R.wn ? R.x[R.w0 + j] : -INFINITY;
+                }
+            }
+        };
+        uint16_t* lj = R.lj + R.w0;
+        float next[8];
+        load8(0, next);
+        for (int jb = 0; jb < R.wn; jb += 256) {
+            const bool q = quads && jb + 256 <= R.wn;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = next[e];
+            load8(jb + 256, next);
+            uint32_t mine = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)  // (a NaN is neither: its lead is NaN, its weight 0)
+                mine |= (W.m - x[e]) * W.ch < kHeavy ? 1u << e : 0u;
+            if (!cuts) {
+                // two sums of four, below 2^32
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t l4 = 0;
+#pragma unroll
+                    for (int e = 4 * h; e < 4 * h + 4; ++e)
+                        l4 += mine >> e & 1 ? 0u : W.light(x[e]);
+                    light_w += l4;
+                }
+            }
+            uint32_t inc = __popc(mine);
+            const uint32_t own = inc;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += o;
+            }
+            int at = R.wl + (int)(inc - own);
+            R.wl += (int)__shfl_sync(0xffffffffu, inc, 31);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (mine >> e & 1) lj[at++] = (uint16_t)place(jb, e, q);
+        }
+    }
+    light_w = warp_sum(light_w);
+    __syncthreads();  // S.red is free
+    if (lane == 0) S.red[warp] = light_w;
+    __syncthreads();
+    const unsigned long long light_cta = warp_sum(lane < kSfWarps ? S.red[lane] : 0ull);
+    const bool plain = !cuts && !(top_p < 1.f) && !(min_p > 0.f);  // every id above -inf stays
+
+    // ---- 3. the filters ----
+    // light: what of the light ids is kept: all, none, or (all ids are to be looked at) some
+    enum { kNone, kLightAll, kSome };
+    int light = finite ? kLightAll : kSome;
     Cut kept = {-INFINITY, -1};
-    if (top_k > 0 && (unsigned long long)top_k < fin)
-        select<false>(S, R, W, kept, (unsigned long long)top_k, 0.f);
-    if (top_p < 1.f) select<true>(S, R, W, kept, 0ull, top_p);
+    if (cuts) {
+        SelectResult r = kBeyond;
+        if (light != kSome) {
+            r = select<false>(S, R, W, false, kept, (unsigned long long)top_k, 0.f, 0ull);
+        }
+        light = kNone;
+        if (r == kBeyond) {
+            select<false>(S, R, W, true, kept, (unsigned long long)top_k, 0.f, 0ull);
+            light = kSome;
+        }
+    }
+    if (top_p < 1.f) {
+        SelectResult r = kBeyond;
+        if (light != kSome) {
+            r = select<true>(S, R, W, false, kept, 0ull, top_p,
+                             light == kLightAll ? light_cta : 0ull);
+            if (r == kCutHere) light = kNone;
+        }
+        if (r == kBeyond && select<true>(S, R, W, true, kept, 0ull, top_p, 0ull) == kCutHere)
+            light = kSome;
+    }
     // min-p by the weight, or (where it is too small for the weight's unit) by y
     const bool by_w = min_p >= 0x1p-40f;
     unsigned long long w_min = 0;
@@ -667,130 +839,118 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         w_min += rest ? 1 : 0;
     }
     const float y_max = min_p > 0.f && !by_w ? -log2f(min_p) : INFINITY;
+    if (light == kLightAll && min_p > 0.f) light = w_min > (1ull << 29) ? kNone : kSome;
 
-    // ---- 3. the kept ids' mass, per segment of kSfThreads * q ids of this CTA ----
-    // warp w: segment w of the slice
-    const int seg = (p.slice / kSfThreads) * 32;  // ids per warp
-    unsigned long long sum = 0, count = 0;
-    auto weigh = [&](int i, unsigned long long& c) -> unsigned long long {
-        const float x = xs[i];
-        if (!kept.keeps(x, R.lo + i) || !(W.lead(x) <= y_max)) return 0ull;
-        const unsigned long long w = W.of(x);
-        if (w < w_min) return 0ull;
-        c += 1;
-        return w;
+    // ---- 4. the kept ids' mass, per warp segment ----
+    unsigned long long sum = 0;
+    uint32_t count = 0;
+    auto weigh = [&](float x, int i, bool listed) -> unsigned long long {
+        const unsigned long long w = listed ? W.heavy(x) : W.of(x);
+        const bool in = kept.keeps(x, R.lo + i) && W.lead(x) <= y_max && w >= w_min;
+        count += in;
+        return in ? w : 0ull;
     };
-    for (int i = warp * seg + lane; i < min(R.n, (warp + 1) * seg); i += 32) sum += weigh(i, count);
+    if (light == kSome) for_ids(R, true, [&](float x, int i) { sum += weigh(x, i, false); });
+    else for_ids(R, false, [&](float x, int i) { sum += weigh(x, i, true); });
+    __syncwarp();
     sum = warp_sum(sum);
-    count = warp_sum(count);
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (light == kLightAll) {  // every id above -inf is kept
+        sum += light_w;
+        count = 0;
+    }
     __syncthreads();
     if (lane == 0) {
         S.red[warp] = sum;
-        S.red2[warp] = count;
+        S.red32[warp] = count;
     }
+    if (tid == 0) S.found = -1;
     __syncthreads();
-    unsigned long long mine = 0, cnt = 0;
-    for (int w = 0; w < kSfWarps; ++w) {
-        mine += S.red[w];
-        cnt += S.red2[w];
-    }
+    const unsigned long long seg_sum = lane < kSfWarps ? S.red[lane] : 0ull;
+    const unsigned long long cta_sum = warp_sum(seg_sum);
+    const uint32_t cta_cnt =
+        __reduce_add_sync(0xffffffffu, lane < kSfWarps ? S.red32[lane] : 0u);
+    unsigned long long ex_sum = lane == 0 ? cta_sum : 0ull;
+    uint32_t cnt = cta_cnt;
     if (R.cluster > 1) {
         if (tid < R.cluster) {
-            st_cluster_u64(&S.ex_a[R.rank], tid, mine);
-            st_cluster_u64(&S.ex_b[R.rank], tid, cnt);
+            st_cluster_u64(&S.ex_sum[R.rank], tid, cta_sum);
+            st_cluster_u32(&S.ex_cnt[R.rank], tid, cta_cnt);
         }
         sync_row(R.cluster);  // nothing is read from another CTA after this
-    } else {
-        if (tid == 0) {
-            S.ex_a[0] = mine;
-            S.ex_b[0] = cnt;
-        }
-        __syncthreads();
+        ex_sum = lane < R.cluster ? S.ex_sum[lane] : 0ull;
+        cnt = __reduce_add_sync(0xffffffffu, lane < R.cluster ? S.ex_cnt[lane] : 0u);
     }
-    unsigned long long total = 0;
-    cnt = 0;
-    for (int r = 0; r < R.cluster; ++r) {
-        total += S.ex_a[r];
-        cnt += S.ex_b[r];
-    }
+    if (plain || light == kLightAll) cnt = fin;
+    const unsigned long long total = warp_sum(ex_sum);
     // the draw: the first id whose running mass exceeds u * total, i.e. is at least t (else the
     // last kept id of mass: u >= 1)
     bool rest;
-    const unsigned long long t = u >= 1.f ? ~0ull : mul_floor(fmaxf(u, 0.f), total, rest) + 1;
-    unsigned long long run = 0, run_owner = 0;
-    int owner = -1, last = 0;
-    for (int r = 0; r < R.cluster; ++r) {
-        if (owner < 0 && run + S.ex_a[r] >= t) {
-            owner = r;
-            run_owner = run;
-        }
-        if (S.ex_a[r] > 0) last = r;
-        run += S.ex_a[r];
-    }
-    const bool lost = owner < 0;  // u >= 1
-    if (lost) owner = last;
-    if (owner != R.rank) return;
-    // the warp segment of this CTA
-    int ow = -1, lw = 0;
-    run = run_owner;
-    unsigned long long run_w = run;
-    for (int w = 0; w < kSfWarps; ++w) {
-        if (!lost && ow < 0 && run + S.red[w] >= t) {
-            ow = w;
-            run_w = run;
-        }
-        if (S.red[w] > 0) lw = w;
-        run += S.red[w];
-    }
-    if (lost) ow = lw;
-    __syncthreads();
-    if (tid == 0) S.found = -1;
+    const bool lost = u >= 1.f;
+    const unsigned long long t = lost ? ~0ull : mul_floor(fmaxf(u, 0.f), total, rest) + 1;
+    // the first entry of v (one per lane) at which `from` + the running sum reaches t (lost:
+    // the last one with any), and the sum before it
+    auto find = [&](unsigned long long v, unsigned long long from,
+                    unsigned long long& before) -> int {
+        const unsigned long long inc = from + warp_incl(v);
+        const uint32_t hit = __ballot_sync(0xffffffffu, lost ? v > 0 : inc >= t);
+        const int l = hit ? (lost ? 31 - __clz(hit) : __ffs(hit) - 1) : 0;
+        before = __shfl_sync(0xffffffffu, inc - v, l);
+        return l;
+    };
+    unsigned long long run;
+    if (find(ex_sum, 0ull, run) != R.rank) return;
+    const int ow = find(seg_sum, run, run);
     // thread t of the block: ids [t * q, (t + 1) * q) of the segment
-    const int q = (seg + kSfThreads - 1) / kSfThreads;
-    const int s0 = ow * seg, s1 = min(R.n, s0 + seg);
-    const int i0 = min(s1, s0 + tid * q), i1 = min(s1, i0 + q);
-    unsigned long long part = 0, dummy = 0;
+    const int w0 = ow * R.seg;
+    const int len = max(0, min(R.seg, R.n - w0));
+    const int q = (len + kSfThreads - 1) / kSfThreads;
+    const int i0 = w0 + min(len, tid * q), i1 = w0 + min(len, (tid + 1) * q);
+    unsigned long long part = 0;
     int last_i = -1;
+#pragma unroll 4
     for (int i = i0; i < i1; ++i) {
-        const unsigned long long w = weigh(i, dummy);
+        const unsigned long long w = weigh(R.at(i), i, false);
         part += w;
         if (w > 0) last_i = i;
     }
-    const unsigned long long ex = run_w + block_excl(S, part);
+    __syncthreads();  // S.red is free
+    unsigned long long dummy;
+    const unsigned long long ex = run + block_excl(S, part, dummy);
     int token = -1;
     if (lost) {
         if (last_i >= 0) atomicMax(&S.found, last_i);
+        __syncthreads();
+        if (tid == 0) token = S.found;
     } else if (ex < t && ex + part >= t) {
         unsigned long long at = ex;
         for (int i = i0; i < i1; ++i) {
-            at += weigh(i, dummy);
+            at += weigh(R.at(i), i, false);
             if (at >= t) {
                 token = i;
                 break;
             }
         }
     }
-    if (lost) {
-        __syncthreads();
-        if (tid == 0) token = S.found;
-    }
     if (token >= 0) {
         p.token[b] = R.lo + token;
         if (p.logprob) {
             // near 1 from what is left over, which the integers know exactly
-            const unsigned long long w = W.of(xs[token]);
+            const unsigned long long w = W.of(R.at(token));
             const float tf = (float)total;
             p.logprob[b] = w > total / 2 ? log1pf(-((float)(total - w) / tf)) : logf((float)w / tf);
         }
-        if (p.n_kept)
-            p.n_kept[b] = (int32_t)(top_k > 0 && (unsigned long long)top_k < cnt ? top_k : cnt);
+        if (p.n_kept) p.n_kept[b] = (int32_t)(top_k > 0 ? min((uint32_t)top_k, cnt) : cnt);
     }
 }
 
 constexpr int kMaxDevF = 64;
+constexpr size_t kSfSmem = sizeof(FilterShared);
+static_assert(2 * (kSfSmem + 1024) <= 227 * 1024, "two CTAs per SM");
+static_assert(kMaxSlice / kSfWarps <= 65536, "places in a segment are 16 bits");
 
 // Once per device: shared memory and clusters of 16; the largest usable cluster.
-int prepare_filtered(size_t smem) {
+int prepare_filtered() {
     static std::once_flag once[kMaxDevF];
     static int result[kMaxDevF];
     int dev = 0;
@@ -798,7 +958,7 @@ int prepare_filtered(size_t smem) {
     std::call_once(once[dev], [&] {
         if (cudaFuncSetAttribute(sample_filtered_kernel,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem) != cudaSuccess) {
+                                 (int)kSfSmem) != cudaSuccess) {
             cudaGetLastError();
             return;
         }
@@ -811,7 +971,7 @@ int prepare_filtered(size_t smem) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(kSfMaxCluster);
             cfg.blockDim = dim3(kSfThreads);
-            cfg.dynamicSmemBytes = smem;
+            cfg.dynamicSmemBytes = kSfSmem;
             cudaLaunchAttribute a;
             a.id = cudaLaunchAttributeClusterDimension;
             a.val.clusterDim.x = kSfMaxCluster;
@@ -843,17 +1003,17 @@ extern "C" kvd_status kvd_sample_filtered(const float* logits, int64_t row_strid
     if (vocab > KVD_MAX_VOCAB || batch > 65535) return KVD_ERR_UNSUPPORTED;
     if (batch == 0) return KVD_OK;
     if (!logits || !u || !token) return KVD_ERR_INVALID_ARG;
-    constexpr int kMaxSlice = KVD_MAX_VOCAB / kSfMaxCluster;  // 128 KiB of logits
-    constexpr size_t kMost = sizeof(FilterShared) + (size_t)kMaxSlice * sizeof(float);
-    static_assert(kMost <= 227 * 1024, "shared memory");
-    const int mc = prepare_filtered(kMost);
-    if (mc <= 0) return KVD_ERR_CUDA;
-    // the fewest CTAs (a power of two) whose slices hold the row
+    const int nsm = sm_count();
+    const int mc = prepare_filtered();
+    if (nsm <= 0 || mc <= 0) return KVD_ERR_CUDA;
+    // CTAs per row, a power of two: enough for the longest slice; then more while slices stay
+    // long and all rows' CTAs are resident at once (two per SM)
     int c = 1;
-    while (c < mc && (int64_t)c * kSfThreads * 16 < vocab) c *= 2;
+    while (c < mc && ((int64_t)c * kMaxSlice < vocab ||
+                      (2ll * c * batch <= 2ll * nsm && (int64_t)c * 2048 < vocab)))
+        c *= 2;
     FilterParams p;
     p.slice = ((vocab + c - 1) / c + kSfThreads - 1) / kSfThreads * kSfThreads;
-    if (p.slice > kMaxSlice) return KVD_ERR_UNSUPPORTED;  // (clusters of 8 only)
     p.cluster = c;
     p.logits = logits;
     p.row_stride = row_stride;
@@ -867,8 +1027,8 @@ extern "C" kvd_status kvd_sample_filtered(const float* logits, int64_t row_strid
     p.n_kept = n_kept;
     p.dev_err = dev_err;
     p.vocab = vocab;
-    const size_t smem = sizeof(FilterShared) + (size_t)p.slice * sizeof(float);
-    return launch_ex(sample_filtered_kernel, dim3((unsigned)(batch * c)), dim3(kSfThreads), smem,
+    if (p.slice > kMaxSlice) return KVD_ERR_UNSUPPORTED;  // (a device without clusters of 16)
+    return launch_ex(sample_filtered_kernel, dim3((unsigned)(batch * c)), dim3(kSfThreads), kSfSmem,
                      reinterpret_cast<cudaStream_t>(stream), (flags & KVD_FLAG_PDL) != 0,
                      (unsigned)c, p);
 }
