@@ -95,6 +95,8 @@ _lib = None
 def load_library(path: str = LIB_PATH):
     """Load the CUDA library (raises if it was never built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -212,14 +214,15 @@ def _check(status: int, call: str):
 
 def make_cache(k: torch.Tensor, v: torch.Tensor) -> Cache:
     """Describe one layer's ``[batch, heads, capacity, 64]`` K/V tensors for the C ABI."""
-    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+    shape, st = k.shape, k.stride()
+    if shape != v.shape or st != v.stride() or k.dtype != v.dtype:
         raise ValueError("K and V must share shape, strides and dtype")
-    if k.dim() != 4 or k.shape[3] != HEAD_DIM or k.stride(3) != 1:
+    if len(shape) != 4 or shape[3] != HEAD_DIM or st[3] != 1:
         raise ValueError("cache must be [batch, heads, capacity, 64] with the last axis contiguous")
     if not (k.is_cuda and v.is_cuda):
         raise ValueError("cache tensors must be CUDA tensors")
-    B, H, cap, D = k.shape
-    c = Cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), B, H, D, cap)
+    B, H, cap, D = shape
+    c = Cache(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], B, H, D, cap)
     c._tensors = (k, v)  # the struct holds raw pointers: keep the tensors alive with it
     return c
 
@@ -402,11 +405,14 @@ def kvd_sample_accept(target, u, n_accepted, next_token, workspace, temperature:
            "kvd_sample_accept")
 
 
-def _at(t, dtype, shape, what, dev):
-    """The address (an int, 0 for None) of a contiguous CUDA tensor of this type and shape on
-    device ``dev``; the argument checks of the calls below."""
-    if t is None:
-        return 0
+# The current device and its current stream as plain numbers: torch.cuda.current_stream()
+# builds a Stream object, 3 us of a decode step's launch.
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _refuse(t, dtype, shape, what, dev):
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.get_device() != dev:
@@ -415,8 +421,17 @@ def _at(t, dtype, shape, what, dev):
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    raise ValueError(f"{what} must be contiguous")
+
+
+def _at(t, dtype, shape, what, dev):
+    """The address (an int, 0 for None) of a contiguous CUDA tensor of this type and shape on
+    device ``dev``; the argument checks of the calls below."""
+    if t is None:
+        return 0
+    if (t.get_device() != dev or t.dtype != dtype or (shape is not None and t.shape != shape)
+            or not t.is_contiguous()):
+        _refuse(t, dtype, shape, what, dev)
     return t.data_ptr()
 
 
@@ -430,25 +445,28 @@ def _scratch(workspace, dev):
 def _device_of(t, what):
     """The tensor's device index, which must be the current device: kernels are launched
     there."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if dev != _raw_device():
         raise ValueError(f"{what} is on cuda:{dev}, which is not the current device")
     return dev
 
 
 def _on(stream, dev):
-    s = torch.cuda.current_stream() if stream is None else stream
-    if s.device_index != dev:
-        raise ValueError(f"the stream is on cuda:{s.device_index}, the tensors on cuda:{dev}")
-    return s.cuda_stream
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _cache_on(cache, dev, dtype=None):
     """The cache's tensors (kept with the struct) are on the current device and of this
     type."""
-    for t in getattr(cache, "_tensors", ()):
+    held = getattr(cache, "_tensors", None)
+    if held is not None:  # they share device and type
+        t = held[0]
         if t.get_device() != dev:
             raise ValueError(f"cache must be on the current device (cuda:{dev})")
         if dtype is not None and t.dtype != dtype:
@@ -470,24 +488,29 @@ def make_q4_cache(k: torch.Tensor, v: torch.Tensor, params: torch.Tensor) -> Q4C
     point). Positions of a head must be consecutive; the three share their layout."""
     if k.dtype != torch.uint8 or v.dtype != torch.uint8 or params.dtype != torch.int16:
         raise TypeError("k and v must be uint8, params int16")
-    if (k.dim() != 4 or k.shape[3] != HEAD_DIM // 2 or v.shape != k.shape
-            or tuple(params.shape) != (*k.shape[:3], 4)):
+    shape = k.shape
+    if (len(shape) != 4 or shape[3] != HEAD_DIM // 2 or v.shape != shape
+            or params.shape != (*shape[:3], 4)):
         raise ValueError("k and v must be [batch, heads, capacity, 32], params [batch, heads, "
                          "capacity, 4]")
-    if not (k.is_cuda and k.device == v.device == params.device):
+    dev = k.get_device()
+    if dev < 0 or v.get_device() != dev or params.get_device() != dev:
         raise ValueError("cache tensors must be CUDA tensors on one device")
-    rows = []
-    for t in (k, v, params):
-        sb, sh, st = _strides(t)
-        n = t.shape[3]
-        if t.stride(3) != 1 or (t.shape[2] > 1 and st != n) or sb % n or sh % n:
-            raise ValueError("a head's positions must be consecutive rows")
-        rows.append((sb // n, sh // n))
-    if rows[0] != rows[1] or rows[0] != rows[2]:
-        raise ValueError("k, v and params must share their strides")
+    if k.is_contiguous() and v.is_contiguous() and params.is_contiguous():
+        row = (shape[1] * shape[2], shape[2])
+    else:
+        rows = []
+        for t in (k, v, params):
+            sb, sh, st = _strides(t)
+            n = t.shape[3]
+            if t.stride(3) != 1 or (shape[2] > 1 and st != n) or sb % n or sh % n:
+                raise ValueError("a head's positions must be consecutive rows")
+            rows.append((sb // n, sh // n))
+        if rows[0] != rows[1] or rows[0] != rows[2]:
+            raise ValueError("k, v and params must share their strides")
+        row = rows[0]
     B, H, cap, _ = k.shape
-    c = Q4Cache(k.data_ptr(), v.data_ptr(), params.data_ptr(), rows[0][0], rows[0][1], B, H,
-                HEAD_DIM, cap)
+    c = Q4Cache(k.data_ptr(), v.data_ptr(), params.data_ptr(), row[0], row[1], B, H, HEAD_DIM, cap)
     c._tensors = (k, v, params)  # the struct holds raw pointers: keep the tensors alive
     return c
 
@@ -506,17 +529,18 @@ def _head_rows(x, out, weight, dtype, n, what, dev):
         if out is not None or weight is not None:
             raise ValueError(f"{what}_out and {what}_weight need {what}")
         return None
-    if not x.is_cuda or x.get_device() != dev:
+    if x.get_device() != dev:
         raise ValueError(f"{what} must be on the current device (cuda:{dev})")
     if x.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {x.dtype}")
-    if x.dim() != 4 or x.shape[3] != HEAD_DIM or x.stride(3) != 1:
+    shape, st = x.shape, x.stride()
+    if len(shape) != 4 or shape[3] != HEAD_DIM or st[3] != 1:
         raise ValueError(f"{what} must be [batch, heads, n, 64] with the last axis contiguous")
-    B, H = x.shape[:2]
-    sb, sh, st = _strides(x)
-    return HeadRows(x.data_ptr(), sb, sh, st,
-                    _at(weight, dtype, (HEAD_DIM,), f"{what}_weight", dev),
-                    _at(out, dtype, (B, H, n, HEAD_DIM), f"{what}_out", dev), H)
+    B, H = shape[0], shape[1]
+    # (the stride of an axis of size 1 is arbitrary and never used)
+    return HeadRows(x.data_ptr(), st[0] if B > 1 else 0, st[1] if H > 1 else 0,
+                    st[2] if n > 1 else 0, _at(weight, dtype, (HEAD_DIM,), what + "_weight", dev),
+                    _at(out, dtype, (B, H, n, HEAD_DIM), what + "_out", dev), H)
 
 
 def kvd_qk_norm_rope(q=None, k=None, q_out=None, k_out=None, q_weight=None, k_weight=None,
@@ -546,9 +570,9 @@ def kvd_qk_norm_rope(q=None, k=None, q_out=None, k_out=None, q_weight=None, k_we
 
 
 def _query_shape(q, out, dev):
-    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM:
         raise ValueError("q must be [batch, n_q_heads, qlen, 64]")
-    shape = tuple(q.shape)
     return shape, _at(q, q.dtype, None, "q", dev), _at(out, q.dtype, shape, "out", dev)
 
 
