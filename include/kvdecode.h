@@ -433,7 +433,7 @@ kvd_status kvd_prefill_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_h
  *   32 bytes: byte j holds dims 2j (low 4 bits) and 2j+1 (high 4 bits), n in 0..15;
  *   a step (bfloat16) and a zero point z (binary16): the row's values are step * (n - z).
  * With the row's least and greatest value lo and hi, every operation rounded to fp32:
- *   step = bf16((hi/2 - lo/2) / 7.5),  z = f16(-lo / step),
+ *   step = bf16((hi/2 - lo/2) / 7.5),  z = f16(-lo / step) (a zero is +0),
  *   n    = clamp(rint(x / step + z), 0, 15)      (rint: ties to even)
  * A row whose step comes out 0 (equal values) has step = bf16(|lo| / 15) (1 when that is 0)
  * and z = 0, or 15 for lo < 0. A value is off by at most half a step, more at the row's ends

@@ -13,25 +13,29 @@
 //    word with 0x000F000F IS a pair of binary16 subnormals n * 2^-24 (0x00F000F0: n * 2^-20):
 //    one AND per two values instead of a conversion. Exact: the tensor cores take
 //    subnormals, q is scaled by a power of two per row, the powers are undone in fp32.
+//  * The cache is the 16-row operand of both products (16 positions x dims for the scores, 16
+//    dims x positions for the output) and the queries are the 8 columns: half the products of
+//    the other way round, and a lane prepares the parameters of 4 positions per tile instead
+//    of 8. The weights turn from score to operand layout with one movmatrix per 8 positions.
 //  * A byte holds consecutive dims. The contraction order of q.K is free, so lane c of a
 //    quad takes dims 16c..16c+15 of a K row (8 consecutive bytes) and q is loaded in the
-//    same order; in P.V the n-block of an output column is free, so lane g takes word g of
-//    a V row, dims 8g..8g+7, one per n-block. Columns 2c and 2c+1 of a score fragment are
-//    rows c and c+4, which keeps both reads free of bank conflicts. Pairs of positions for
-//    the V operand are two words merged with PRMT.
+//    same order; the row order of the output product is free, so lane g takes word g of a V
+//    row, dims 8g..8g+7. Row g of 8 positions is position g / 2 + 4 (g % 2), which keeps both
+//    reads free of bank conflicts. Pairs of positions are two words merged with PRMT.
 //  * The weights that multiply V are fp16(w * sV / 2^E), E a per-warp exponent that follows
-//    the largest step; the zero points are one more n-block of the same product, so the same
-//    rounded weights multiply n and z and their rounding is not amplified by n - z
-//    cancelling. The normaliser sums w unrounded in fp32.
-//  * Rows' references move only when a score exceeds them by 2^8, decided by one vote per
-//    tile: the usual tile has no reduction across lanes at all.
+//    the largest step; the zero points multiply the same rounded weights, so their rounding
+//    is not amplified by n - z cancelling. The normaliser sums w unrounded in fp32.
+//  * References move only when a score exceeds them by 2^8, decided by one vote per tile: the
+//    usual tile has no reduction across lanes at all.
 //  * Each warp streams its own tiles of 32 positions (2304 bytes with the parameters)
 //    through a ring of cp.async stages: no block barrier in the loop, and rows at or past
 //    the length are filled with zeros and never read.
-//  * A (row, KV head, block of <= 16 query vectors) unit is cut into splits of equal tile
-//    counts of the row's own length. Splits of a unit form a thread-block cluster and merge
-//    through distributed shared memory, every CTA a share of the outputs; for a few long
-//    units, more splits than a cluster holds merge through the workspace (last arrival).
+//  * Work. A unit is a (row, KV head, block of <= 16 query vectors). Little work in all: every
+//    unit is cut into splits of equal tile counts of the row's own length, which form a
+//    thread-block cluster and merge through distributed shared memory, every CTA a share of
+//    the outputs. Much work (STREAM): the tiles of all units form one list, every CTA of one
+//    wave takes an equal stretch of it, and units cut by a stretch's end merge through the
+//    workspace (last arrival): ragged lengths then cost nothing.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -48,7 +52,7 @@ constexpr int kT = 32;                       // positions per tile
 constexpr int kStagesQ = 4;                  // cp.async stages per warp
 constexpr int kStageBytes = kT * (32 + 32 + 8);
 constexpr int kMaxClusterQ = 16;
-constexpr int kMaxSplitsQ = 128;
+constexpr int kMaxStream = 512;              // CTAs of a STREAM launch
 constexpr float kGrowLog2 = 8.f;
 constexpr int kPart = kHeadDim + 4;          // floats per partial: o[64], max, sum, 2 pad
 
@@ -60,14 +64,14 @@ struct Q4AttnParams {
     const uint8_t* par;
     int64_t sb, sh;          // rows
     const int32_t* lens;
-    int32_t fixed_len, capacity;
+    int32_t fixed_len, capacity, batch;
     int32_t n_q_heads, n_kv_heads, group, qlen;
     int32_t M, msub, nsub;   // query vectors per (row, KV head), per block; blocks
-    int32_t splits, cluster; // splits per unit; 1: they form a cluster, 0: workspace
+    int32_t splits;          // cluster launches: splits per unit
     int32_t causal, window, n_sinks;
     float scale_log2;
-    float* ws_part;          // [units][splits][msub][kPart]
-    int32_t* ws_cnt;
+    float* ws_part;          // STREAM: [2 * CTAs][msub][kPart]
+    int32_t* ws_cnt;         // [units]
     int32_t* dev_err;
 };
 
@@ -80,6 +84,9 @@ __device__ __forceinline__ void cp_async8_zfill(uint32_t dst, const void* src, b
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
                  "r"(on ? 8 : 0)
                  : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -98,6 +105,17 @@ __device__ __forceinline__ void cluster_sync_q4() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Transpose of an 8 x 8 matrix of 16-bit values held two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 __device__ __forceinline__ float half_bits(uint32_t b) {
     return __half2float(__ushort_as_half((uint16_t)b));
@@ -130,375 +148,460 @@ __device__ __forceinline__ TileMap tile_map(const Q4AttnParams& p, int len) {
     m.total = all - m.gap;
     return m;
 }
+__device__ __forceinline__ int row_len(const Q4AttnParams& p, int b) {
+    return p.lens ? p.lens[b] : p.fixed_len;
+}
 
-template <typename T, int RM>
+// STREAM: the tiles of rows 0 .. batch-1, each row's times its units (KV heads x blocks).
+// The row that holds tile `at` of the list, and the list's tiles before that row; with at past
+// the end, `before` is the length of the list. One warp, the same in all of them.
+__device__ __forceinline__ int find_row(const Q4AttnParams& p, int64_t at, int64_t& before) {
+    const int lane = threadIdx.x & 31;
+    const int64_t units = (int64_t)p.n_kv_heads * p.nsub;
+    before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        int64_t n = 0;
+        if (b0 + lane < p.batch) {
+            const int len = row_len(p, b0 + lane);
+            if (len >= 0 && len <= p.capacity) n = tile_map(p, len).total * units;
+        }
+        int64_t inc = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += o;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > at);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            before += __shfl_sync(0xffffffffu, inc - n, l);
+            return b0 + l;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return p.batch;
+}
+
+// NT: blocks of 8 query vectors.
+template <typename T, int NT, bool STREAM>
 __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParams p) {
-    constexpr bool kFull = RM == 16;
-    constexpr int kAcc = kFull ? 4 : 2;
+    constexpr int RM = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int s = blockIdx.x, h = blockIdx.y / p.nsub, sub = blockIdx.y % p.nsub, b = blockIdx.z;
-    const int m0 = sub * p.msub, mcount = min(p.msub, p.M - m0);
+    float* red = reinterpret_cast<float*>(smem);  // after a unit's tiles: [warp][RM][kPart]
+    float* part = red + kWarpsQ * RM * kPart;     // this CTA's partial [msub][kPart]
 
     pdl_wait();
     pdl_trigger();
-    const int len = p.lens ? p.lens[b] : p.fixed_len;
-    const bool bad = len < 0 || len > p.capacity;  // the same in every CTA of a cluster
-    if (bad) {
-        if (tid == 0 && s == 0 && blockIdx.y == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
-        return;
-    }
-    const TileMap tm = tile_map(p, len);
-    const int v0 = (int)((int64_t)tm.total * s / p.splits);
-    const int v1 = (int)((int64_t)tm.total * (s + 1) / p.splits);
 
-    // ---- the warp's ring ----
-    uint8_t* ring = smem + warp * (kStagesQ * kStageBytes);
-    const int64_t row0 = b * p.sb + h * p.sh;
-    const uint8_t* kbase = p.k + row0 * 32;
-    const uint8_t* vbase = p.v + row0 * 32;
-    const uint8_t* pbase = p.par + row0 * 8;
-    auto fetch = [&](int v, int stage) {
-        if (v < v1) {
-            const int t0 = tm.pos(v);
-            const uint32_t dst = smem_u32(ring + stage * kStageBytes);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int x = lane + 32 * i;
-                const bool on = t0 + (x >> 1) < len;
-                const int64_t off = on ? (int64_t)t0 * 32 + x * 16 : 0;
-                cp_async16_zfill(dst + x * 16, kbase + off, on);
-                cp_async16_zfill(dst + kT * 32 + x * 16, vbase + off, on);
-            }
-            const bool on = t0 + lane < len;
-            cp_async8_zfill(dst + kT * 64 + lane * 8, pbase + (on ? (int64_t)(t0 + lane) * 8 : 0),
-                            on);
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStagesQ - 1; ++i) fetch(v0 + warp + i * kWarpsQ, i);
-
-    // ---- the query rows g (A) and g + 8 (B) of the block: 16 dims per lane ----
-    // fp16, scaled by 2^e so that a row's largest value lies in [2^14, 2^15)
-    uint32_t qa[4][4];
-    float rs[2], qs[2];  // score factor (log2 units) and sum of the scaled q, * 2^-24
-    int lim[2], wlo[2];  // the row sees t < lim with t >= wlo or t < n_sinks
-#pragma unroll
-    for (int r = 0; r < (kFull ? 2 : 1); ++r) {
-        const int m = g + 8 * r;
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.f;
-        lim[r] = 0;
-        wlo[r] = 0;
-        if (m < mcount) {
-            const int i = (m0 + m) % p.qlen, hq = h * p.group + (m0 + m) / p.qlen;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const T*>(p.q) +
-                (((int64_t)b * p.n_q_heads + hq) * p.qlen + i) * kHeadDim + 16 * c);
-            unpack8<T>(src[0], x);
-            unpack8<T>(src[1], x + 8);
-            const int pos = len - p.qlen + i;
-            lim[r] = p.causal ? max(pos + 1, 0) : len;
-            if (p.window > 0) wlo[r] = (int)max((int64_t)pos - p.window + 1, (int64_t)0);
-        }
-        float big = 0.f;
-        bool odd = false;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            big = fmaxf(big, fabsf(x[e]));
-            odd |= !(fabsf(x[e]) < INFINITY);
-        }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // a row with an infinity or a NaN keeps its values (its outputs are not finite)
-        const bool any_odd = ((__ballot_sync(0xffffffffu, odd) >> (lane & 28)) & 15u) != 0;
-        int e2 = 0;
-        if (big > 0.f && !any_odd) {
-            frexpf(big, &e2);  // big = f * 2^e2, f in [0.5, 1)
-            e2 = min(15 - e2, 120);
-        }
-        const float up = p.scale_log2 < 0.f ? -1.f : 1.f;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            x[e] = __half2float(__float2half_rn(up * ldexpf(x[e], e2)));
-            sum += x[e];
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[r] = sum * 0x1p-24f;
-        rs[r] = ldexpf(fabsf(p.scale_log2), 24 - e2);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                // nibbles n and n + 4 of word kk / 2; the odd ones come times 16
-                const int n = 8 * (kk >> 1) + 2 * (kk & 1) + w;
-                const float f = w ? 0.0625f : 1.f;
-                qa[kk][2 * w + r] = pack_half(x[n] * f, x[n + 4] * f);
-            }
-    }
-    if (!kFull) {
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) qa[kk][1] = qa[kk][3] = 0u;
-        rs[1] = qs[1] = 0.f;
-        lim[1] = wlo[1] = 0;
-    }
-    auto mma = [&](float* acc, const uint32_t* a, uint32_t b0, uint32_t b1) {
-        if (kFull) Mma<__half>::run(acc, a, b0, b1);
-        else Mma<__half>::run_top(acc, a[0], a[2], b0, b1);
-    };
-
-    float acc[9][kAcc];  // n-blocks 0..7: the output dims; 8: the zero points
-#pragma unroll
-    for (int n = 0; n < 9; ++n)
-#pragma unroll
-        for (int e = 0; e < kAcc; ++e) acc[n][e] = 0.f;
-    float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float vref = 0.f, vinv = 0.f;  // 2^E and 2^-E of the V steps (0: none seen yet)
-
-    // positions every row of the block sees wholly: t < seen_hi, and with a window
-    // t >= seen_lo or t < n_sinks
-    const int seen_hi = p.causal ? len - p.qlen + 1 : len;
-    const int seen_lo = p.window > 0 ? (int)max((int64_t)len - p.window, (int64_t)0) : 0;
-
-    auto tile = [&](const uint8_t* st, int t0, auto masked_) {
-        constexpr bool kMasked = decltype(masked_)::value;
-        const uint8_t* sK = st;
-        const uint8_t* sV = st + kT * 32;
-        const uint2* sP = reinterpret_cast<const uint2*>(st + kT * 64);
-        // the lane's positions: 8 nb + 4 e + c, nb 0..3, e 0..1
-        float sc[4][kAcc];
-        const int krow = (g >> 1) + 4 * (g & 1);
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-#pragma unroll
-            for (int e = 0; e < kAcc; ++e) sc[nb][e] = 0.f;
-            const uint2 w = *reinterpret_cast<const uint2*>(sK + (8 * nb + krow) * 32 + c * 8);
-            mma(sc[nb], qa[0], w.x & 0x000F000Fu, w.x & 0x00F000F0u);
-            mma(sc[nb], qa[1], (w.x >> 8) & 0x000F000Fu, (w.x >> 8) & 0x00F000F0u);
-            mma(sc[nb], qa[2], w.y & 0x000F000Fu, w.y & 0x00F000F0u);
-            mma(sc[nb], qa[3], (w.y >> 8) & 0x000F000Fu, (w.y >> 8) & 0x00F000F0u);
-        }
-        float vs[4][2];     // V steps of the lane's positions
-        uint32_t vz[4];     // zero points of V: pair (row c, row c + 4)
-        float top[2] = {-INFINITY, -INFINITY}, vtop = 0.f;
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            uint2 pr[2] = {sP[8 * nb + c], sP[8 * nb + 4 + c]};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (kMasked) {
-                    // an infinite zero point must not reach rows that do not see it
-                    if (((pr[e].y >> 16) & 0x7C00u) == 0x7C00u) pr[e].y = 0x7FC0u;
-                }
-                const float ks = __uint_as_float(pr[e].x << 16), kz = half_bits(pr[e].x >> 16);
-                vs[nb][e] = __uint_as_float(pr[e].y << 16);
-                vtop = fmaxf(vtop, vs[nb][e] < INFINITY ? vs[nb][e] : 0.f);
-#pragma unroll
-                for (int r = 0; r < kAcc / 2; ++r) {
-                    float x = fmaf(-kz, qs[r], sc[nb][2 * r + e]) * ks;
-                    if (kMasked) {
-                        const int t = t0 + 8 * nb + 4 * e + c;
-                        if (!(t < lim[r] && (t >= wlo[r] || t < p.n_sinks))) x = -INFINITY;
-                    }
-                    sc[nb][2 * r + e] = x;
-                    top[r] = fmaxf(top[r], x);
-                }
-            }
-            vz[nb] = __byte_perm(pr[0].y, pr[1].y, 0x7632);
-        }
-        // One vote: does a row's reference or the step exponent have to move?
-        bool move = vtop > 16.f * vref;
-#pragma unroll
-        for (int r = 0; r < kAcc / 2; ++r) move |= top[r] * rs[r] > ref[r] + kGrowLog2;
-        if (__any_sync(0xffffffffu, move)) {
-            const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vtop));
-            float fv = 1.f;
-            if (__uint_as_float(vb) > vref) {
-                // 2^E: the largest step's power of two (at least the smallest normal)
-                const float nv = __uint_as_float(max(vb & 0x7F800000u, 0x00800000u));
-                fv = vref * (1.f / nv);
-                vref = nv;
-                vinv = 1.f / nv;
-            }
-#pragma unroll
-            for (int r = 0; r < kAcc / 2; ++r) {
-                float t = top[r];
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                t = t == -INFINITY ? t : t * rs[r];
-                const float nref = fmaxf(ref[r], t);
-                const float f = nref == -INFINITY ? 1.f : exp2f(ref[r] - nref);
-                ref[r] = nref;
-                l[r] *= f;
-#pragma unroll
-                for (int n = 0; n < 9; ++n) {
-                    acc[n][2 * r] *= f * fv;
-                    acc[n][2 * r + 1] *= f * fv;
-                }
-            }
-        }
-        // weights, in pairs of positions (row c, row c + 4) of each n-block
-        uint32_t pw[4][2];
-        const float nr[2] = {ref[0] == -INFINITY ? 0.f : -ref[0],
-                             ref[1] == -INFINITY ? 0.f : -ref[1]};
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-            const float y[2] = {vs[nb][0] * vinv, vs[nb][1] * vinv};
-#pragma unroll
-            for (int r = 0; r < kAcc / 2; ++r) {
-                float w[2], f[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float x = sc[nb][2 * r + e];
-                    w[e] = ex2_approx(fmaf(x, rs[r], nr[r]));
-                    f[e] = w[e] * y[e];
-                    if (kMasked && x == -INFINITY) w[e] = f[e] = 0.f;
-                }
-                l[r] += w[0] + w[1];
-                pw[nb][r] = pack_half(f[0], f[1]);
-            }
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t pa[4] = {pw[2 * half][0], 0u, pw[2 * half + 1][0], 0u};
-            if (kFull) {
-                pa[1] = pw[2 * half][1];
-                pa[3] = pw[2 * half + 1][1];
-            }
-            const uint8_t* vr = sV + (16 * half + c) * 32 + g * 4;
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(vr + j * 128);
-            const uint32_t a0 = __byte_perm(w[0], w[1], 0x5410), b0 = __byte_perm(w[2], w[3], 0x5410);
-            const uint32_t a1 = __byte_perm(w[0], w[1], 0x7632), b1 = __byte_perm(w[2], w[3], 0x7632);
-            mma(acc[0], pa, a0 & 0x000F000Fu, b0 & 0x000F000Fu);
-            mma(acc[1], pa, a0 & 0x00F000F0u, b0 & 0x00F000F0u);
-            mma(acc[2], pa, (a0 >> 8) & 0x000F000Fu, (b0 >> 8) & 0x000F000Fu);
-            mma(acc[3], pa, (a0 >> 8) & 0x00F000F0u, (b0 >> 8) & 0x00F000F0u);
-            mma(acc[4], pa, a1 & 0x000F000Fu, b1 & 0x000F000Fu);
-            mma(acc[5], pa, a1 & 0x00F000F0u, b1 & 0x00F000F0u);
-            mma(acc[6], pa, (a1 >> 8) & 0x000F000Fu, (b1 >> 8) & 0x000F000Fu);
-            mma(acc[7], pa, (a1 >> 8) & 0x00F000F0u, (b1 >> 8) & 0x00F000F0u);
-            mma(acc[8], pa, vz[2 * half], vz[2 * half + 1]);
-        }
-    };
-
-    int stage = 0;
-    for (int v = v0 + warp; v < v1; v += kWarpsQ) {
-        cp_async_wait<kStagesQ - 2>();
-        __syncwarp();
-        const int t0 = tm.pos(v);
-        const uint8_t* st = ring + stage * kStageBytes;
-        // refill the stage read in the previous iteration
-        fetch(v + (kStagesQ - 1) * kWarpsQ, stage == 0 ? kStagesQ - 1 : stage - 1);
-        if (t0 + kT <= seen_hi && (t0 >= seen_lo || t0 + kT <= p.n_sinks))
-            tile(st, t0, std::false_type{});
-        else
-            tile(st, t0, std::true_type{});
-        stage = stage + 1 == kStagesQ ? 0 : stage + 1;
-        __syncwarp();  // the tile is read before its stage is refilled
-    }
-    cp_async_wait_all();
-    __syncthreads();
-
-    // ---- merge the warps: red[warp][row][kPart] over the ring ----
-    float* red = reinterpret_cast<float*>(smem);
-#pragma unroll
-    for (int r = 0; r < kAcc / 2; ++r) {
-        float t = l[r];
-        t += __shfl_xor_sync(0xffffffffu, t, 1);
-        t += __shfl_xor_sync(0xffffffffu, t, 2);
-        const int m = g + 8 * r;
-        if (m < mcount) {
-            float* o = red + (warp * RM + m) * kPart;
-            // columns 2c, 2c + 1 are dims 16c + n and 16c + 8 + n; the odd n-blocks are
-            // times 16
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float z = acc[8][2 * r + e];
-                float x[8];
-#pragma unroll
-                for (int n = 0; n < 8; ++n)
-                    x[n] = fmaf(acc[n][2 * r + e], n & 1 ? 0x1p20f : 0x1p24f, -z) * vref;
-                float4* d = reinterpret_cast<float4*>(o + 16 * c + 8 * e);
-                d[0] = make_float4(x[0], x[1], x[2], x[3]);
-                d[1] = make_float4(x[4], x[5], x[6], x[7]);
-            }
-            if (c == 0) {
-                o[kHeadDim] = ref[r];
-                o[kHeadDim + 1] = t;
+    // ---- the stretch of the tile list, or the split of the unit ----
+    int64_t cur = 0, end = 0, total = 0;
+    int64_t ctas = 0;
+    if (STREAM) {
+        find_row(p, INT64_MAX, total);
+        // at least a tile per warp
+        ctas = max((int64_t)1, min((int64_t)gridDim.x, (total + kWarpsQ - 1) / kWarpsQ));
+        const int64_t i = blockIdx.x;
+        cur = i < ctas ? total * i / ctas : total;
+        end = i < ctas ? total * (i + 1) / ctas : total;
+        // rows without a tile: flagged, or (length 0) zeros
+        for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+            const int len = row_len(p, b);
+            if (len < 0 || len > p.capacity) {
+                if (tid == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+            } else if (len == 0) {
+                const int64_t n = (int64_t)p.n_q_heads * p.qlen * (kHeadDim / 8);
+                uint4* o = static_cast<uint4*>(p.out) + b * n;
+                for (int64_t x = tid; x < n; x += kThreadsQ) o[x] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
     }
-    __syncthreads();
-    const int items = mcount * (kHeadDim / 4);  // (query vector, 4 dims)
-    float* part = red + kWarpsQ * RM * kPart;   // this CTA's partial [msub][kPart]
-    auto store = [&](int it, const float4& o, float sum) {
-        const int m = it >> 4, d = (it & 15) * 4;
-        const int i = (m0 + m) % p.qlen, hq = h * p.group + (m0 + m) / p.qlen;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint2 w;
-        w.x = Half16<T>::from_f2(o.x * inv, o.y * inv);
-        w.y = Half16<T>::from_f2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) +
-                                  (((int64_t)b * p.n_q_heads + hq) * p.qlen + i) * kHeadDim + d) = w;
-    };
-    const int unit = (b * p.n_kv_heads + h) * p.nsub + sub;
-    float* wp = p.splits > 1 && !p.cluster
-                    ? p.ws_part + ((int64_t)unit * p.splits + s) * p.msub * kPart
-                    : nullptr;
-    for (int it = tid; it < items; it += kThreadsQ) {
-        const float* r0 = red + (it >> 4) * kPart;
-        const int q4 = it & 15;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarpsQ; ++w) mx = fmaxf(mx, r0[w * RM * kPart + kHeadDim]);
-        const float rf = mx == -INFINITY ? 0.f : mx;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarpsQ; ++w) {
-            const float* pw = r0 + w * RM * kPart;
-            const float a = exp2f(pw[kHeadDim] - rf);
-            const float4 x = reinterpret_cast<const float4*>(pw)[q4];
-            sum = fmaf(pw[kHeadDim + 1], a, sum);
-            o.x = fmaf(x.x, a, o.x);
-            o.y = fmaf(x.y, a, o.y);
-            o.z = fmaf(x.z, a, o.z);
-            o.w = fmaf(x.w, a, o.w);
-        }
-        if (p.splits == 1) {
-            store(it, o, sum);
+    bool first_seg = true;
+    do {
+        int b, uh, v0, v1, len;  // uh: unit within the row
+        int64_t u0 = 0;          // STREAM: the unit's first tile of the list
+        TileMap tm;
+        if (STREAM) {
+            if (cur >= end) break;
+            int64_t before;
+            b = find_row(p, cur, before);
+            len = row_len(p, b);
+            tm = tile_map(p, len);
+            uh = (int)((cur - before) / tm.total);
+            u0 = before + (int64_t)uh * tm.total;
+            v0 = (int)(cur - u0);
+            v1 = (int)min((int64_t)tm.total, v0 + (end - cur));
+            cur += v1 - v0;
         } else {
-            float* d = (wp ? wp : part) + (it >> 4) * kPart;
-            reinterpret_cast<float4*>(d)[q4] = o;
-            if (q4 == 0) *reinterpret_cast<float4*>(d + kHeadDim) = make_float4(mx, sum, 0.f, 0.f);
+            b = blockIdx.z;
+            uh = blockIdx.y;
+            len = row_len(p, b);
+            if (len < 0 || len > p.capacity) {  // the same in every CTA of a cluster
+                if (tid == 0 && blockIdx.x == 0 && uh == 0)
+                    flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+                return;
+            }
+            tm = tile_map(p, len);
+            v0 = (int)((int64_t)tm.total * blockIdx.x / p.splits);
+            v1 = (int)((int64_t)tm.total * (blockIdx.x + 1) / p.splits);
         }
-    }
-    if (p.splits == 1) return;
+        const int h = uh / p.nsub, m0 = uh % p.nsub * p.msub;
+        const int mcount = min(p.msub, p.M - m0);
 
-    if (p.cluster) {
-        // every CTA merges a share of the outputs out of all CTAs' partials, in split order
-        cluster_sync_q4();
-        const uint32_t base = smem_u32(part);
-        for (int it = s + p.splits * tid; it < items; it += p.splits * kThreadsQ) {
-            const uint32_t off = base + (it >> 4) * (kPart * 4);
-            float mx = -INFINITY;
-            for (int i = 0; i < p.splits; ++i)
-                mx = fmaxf(mx, ld_cluster4(map_shared(off + kHeadDim * 4, i)).x);
+        // ---- the warp's ring ----
+        uint8_t* ring = smem + warp * (kStagesQ * kStageBytes);
+        const int64_t row0 = b * p.sb + h * p.sh;
+        const uint8_t* kbase = p.k + row0 * 32 + lane * 16;
+        const uint8_t* vbase = p.v + row0 * 32 + lane * 16;
+        const uint8_t* pbase = p.par + row0 * 8 + lane * 8;
+        auto fetch = [&](int v, int stage) {
+            if (v < v1) {
+                const int t0 = tm.pos(v);
+                const uint32_t dst = smem_u32(ring + stage * kStageBytes) + lane * 16;
+                const int64_t off = (int64_t)t0 * 32;
+                if (t0 + kT <= len) {
+                    cp_async16(dst, kbase + off);
+                    cp_async16(dst + 512, kbase + off + 512);
+                    cp_async16(dst + kT * 32, vbase + off);
+                    cp_async16(dst + kT * 32 + 512, vbase + off + 512);
+                    cp_async8(dst + kT * 64 - lane * 8, pbase + (int64_t)t0 * 8);
+                } else {  // zeros from the length on
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bool on = t0 + 16 * i + (lane >> 1) < len;
+                        const int64_t o = on ? off + 512 * i : 0;
+                        cp_async16_zfill(dst + 512 * i, kbase + o, on);
+                        cp_async16_zfill(dst + kT * 32 + 512 * i, vbase + o, on);
+                    }
+                    const bool on = t0 + lane < len;
+                    cp_async8_zfill(dst + kT * 64 - lane * 8, pbase + (on ? (int64_t)t0 * 8 : 0), on);
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kStagesQ - 1; ++i) fetch(v0 + warp + i * kWarpsQ, i);
+
+        // ---- the queries: lane (g, c) has dims 16c..16c+15 of query g of every block of 8,
+        // fp16, scaled by 2^e so that a row's largest value lies in [2^14, 2^15) ----
+        uint32_t qb[NT][4][2];
+        // of the queries 2c, 2c + 1 of a block: score factor (log2 units), sum of the scaled
+        // q * 2^-24, and the limit: a query sees t < lim
+        float rs[NT][2], qs[NT][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int m = 8 * nt + g;
+            float x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+            if (m < mcount) {
+                const int i = (m0 + m) % p.qlen, hq = h * p.group + (m0 + m) / p.qlen;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const T*>(p.q) +
+                    (((int64_t)b * p.n_q_heads + hq) * p.qlen + i) * kHeadDim + 16 * c);
+                unpack8<T>(src[0], x);
+                unpack8<T>(src[1], x + 8);
+            }
+            float big = 0.f;
+            bool odd = false;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                big = fmaxf(big, fabsf(x[e]));
+                odd |= !(fabsf(x[e]) < INFINITY);
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // a row with an infinity or a NaN keeps its values (its outputs are not finite)
+            const bool any_odd =
+                ((__ballot_sync(0xffffffffu, odd) >> (lane & 28)) & 15u) != 0;
+            int e2 = 0;
+            if (big > 0.f && !any_odd) {
+                frexpf(big, &e2);  // big = f * 2^e2, f in [0.5, 1)
+                e2 = min(15 - e2, 120);
+            }
+            const float up = p.scale_log2 < 0.f ? -1.f : 1.f;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                x[e] = __half2float(__float2half_rn(up * ldexpf(x[e], e2)));
+                sum += x[e];
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const float f = ldexpf(fabsf(p.scale_log2), 24 - e2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int mq = 8 * nt + 2 * c + e;
+                rs[nt][e] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + e));
+                qs[nt][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * c + e)) * 0x1p-24f;
+                const int pos1 = len - p.qlen + (m0 + mq) % p.qlen + 1;
+                lim[nt][e] = mq < mcount ? (p.causal ? max(pos1, 0) : len) : 0;
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    // nibbles n and n + 4 of word kk / 2; the odd ones come times 16
+                    const int n = 8 * (kk >> 1) + 2 * (kk & 1) + w;
+                    const float s = w ? 0.0625f : 1.f;
+                    qb[nt][kk][w] = pack_half(x[n] * s, x[n + 4] * s);
+                }
+        }
+
+        float acc[4][NT][4];  // dims 8g + 2j (and + 1, times 16) of queries 2c, 2c + 1
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
+        // references, and this lane's share of the normalisers and of the zero points' sums
+        float ref[NT][2], l[NT][2], zs[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                ref[nt][e] = -INFINITY;
+                l[nt][e] = zs[nt][e] = 0.f;
+            }
+        float vref = 0x1p-127f, vinv = 0x1p127f;  // 2^E and 2^-E of the V steps
+
+        // positions every query of the block sees wholly: t < seen_hi, and with a window
+        // t >= seen_lo or t < n_sinks
+        const int seen_hi = p.causal ? len - p.qlen + 1 : len;
+        const int seen_lo = p.window > 0 ? (int)max((int64_t)len - p.window, (int64_t)0) : 0;
+
+        auto tile = [&](const uint8_t* st, int t0, auto masked_) {
+            constexpr bool kMasked = decltype(masked_)::value;
+            const int krow = (g >> 1) + 4 * (g & 1);  // this lane's position of every 8
+            const uint8_t* sK = st + krow * 32 + c * 8;
+            const uint8_t* sV = st + kT * 32 + c * 32 + g * 4;
+            const uint8_t* sP = st + kT * 64 + krow * 8;
+            float sc[2][NT][4];  // positions 16 t + krow and + 8 of queries 2c, 2c + 1
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[t][nt][e] = 0.f;
+                const uint2 a = *reinterpret_cast<const uint2*>(sK + t * 512);
+                const uint2 d = *reinterpret_cast<const uint2*>(sK + t * 512 + 256);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint32_t wa = (kk < 2 ? a.x : a.y) >> (8 * (kk & 1));
+                    const uint32_t wd = (kk < 2 ? d.x : d.y) >> (8 * (kk & 1));
+                    const uint32_t f[4] = {wa & 0x000F000Fu, wd & 0x000F000Fu, wa & 0x00F000F0u,
+                                           wd & 0x00F000F0u};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        Mma<__half>::run(sc[t][nt], f, qb[nt][kk][0], qb[nt][kk][1]);
+                }
+            }
+            float y[2][2], vz[2][2];  // V steps / 2^E and zero points of the positions
+            float top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
+            uint32_t vraw[2][2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint2 pr = *reinterpret_cast<const uint2*>(sP + (16 * t + 8 * hh) * 8);
+                    // an infinite zero point must not reach rows that do not see it
+                    if (kMasked && ((pr.y >> 16) & 0x7C00u) == 0x7C00u) pr.y = 0x7FC0u;
+                    const float ks = __uint_as_float(pr.x << 16), kz = half_bits(pr.x >> 16);
+                    vraw[t][hh] = pr.y << 16;
+                    y[t][hh] = __uint_as_float(vraw[t][hh]) * vinv;
+                    vz[t][hh] = half_bits(pr.y >> 16);
+                    const int pos = t0 + 16 * t + 8 * hh + krow;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = fmaf(-kz, qs[nt][e], sc[t][nt][2 * hh + e]) * ks;
+                            if (kMasked) {
+                                const int lm = lim[nt][e];
+                                if (!(pos < lm && (p.window == 0 || pos >= lm - p.window ||
+                                                   pos < p.n_sinks)))
+                                    x = -INFINITY;
+                            }
+                            sc[t][nt][2 * hh + e] = x;
+                        }
+                }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    top[nt][e] = max3(max3(sc[0][nt][e], sc[0][nt][2 + e], sc[1][nt][e]),
+                                      sc[1][nt][2 + e], -INFINITY);
+            // One vote: does a query's reference or the step exponent have to move?
+            bool move = max3(max3(y[0][0], y[0][1], y[1][0]), y[1][1], 0.f) > 16.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    move |= top[nt][e] * rs[nt][e] > ref[nt][e] + kGrowLog2;
+            if (__any_sync(0xffffffffu, move)) {
+                uint32_t vb = 0;  // the largest finite step
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t v = vraw[i >> 1][i & 1];
+                    if (v < 0x7F800000u) vb = max(vb, v);
+                }
+                vb = __reduce_max_sync(0xffffffffu, vb);
+                float fv = 1.f;
+                if (__uint_as_float(vb) > 16.f * vref) {
+                    // 2^E: the largest step's power of two (at least the smallest normal)
+                    const float nv = __uint_as_float(max(vb & 0x7F800000u, 0x00800000u));
+                    fv = vref * (1.f / nv);
+                    vref = nv;
+                    vinv = 1.f / nv;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        y[i >> 1][i & 1] = __uint_as_float(vraw[i >> 1][i & 1]) * vinv;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float t = top[nt][e];
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                        t = t == -INFINITY ? t : t * rs[nt][e];
+                        const float nref = fmaxf(ref[nt][e], t);
+                        const float f = nref == -INFINITY ? 1.f : exp2f(ref[nt][e] - nref);
+                        ref[nt][e] = nref;
+                        l[nt][e] *= f;
+                        zs[nt][e] *= f * fv;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            acc[j][nt][e] *= f * fv;
+                            acc[j][nt][2 + e] *= f * fv;
+                        }
+                    }
+            }
+            // the weights times the steps, as the output product's operand
+            uint32_t pw[2][2][NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float nr[2] = {ref[nt][0] == -INFINITY ? 0.f : -ref[nt][0],
+                                     ref[nt][1] == -INFINITY ? 0.f : -ref[nt][1]};
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        float w[2], f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = sc[t][nt][2 * hh + e];
+                            w[e] = ex2_approx(fmaf(x, rs[nt][e], nr[e]));
+                            f[e] = w[e] * y[t][hh];
+                            if (kMasked && x == -INFINITY) w[e] = f[e] = 0.f;
+                            l[nt][e] += w[e];
+                        }
+                        const uint32_t pk = pack_half(f[0], f[1]);
+                        const float2 r = Half16<__half>::to_f2(pk);
+                        zs[nt][0] = fmaf(r.x, vz[t][hh], zs[nt][0]);
+                        zs[nt][1] = fmaf(r.y, vz[t][hh], zs[nt][1]);
+                        pw[t][hh][nt] = transpose8(pk);
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t w[4];  // positions c, c + 4, c + 8, c + 12
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = *reinterpret_cast<const uint32_t*>(sV + t * 512 + i * 128);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t sel = j < 2 ? 0x5410 : 0x7632;
+                    const uint32_t a = __byte_perm(w[0], w[1], sel) >> (8 * (j & 1));
+                    const uint32_t d = __byte_perm(w[2], w[3], sel) >> (8 * (j & 1));
+                    const uint32_t f[4] = {a & 0x000F000Fu, a & 0x00F000F0u, d & 0x000F000Fu,
+                                           d & 0x00F000F0u};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        Mma<__half>::run(acc[j][nt], f, pw[t][0][nt], pw[t][1][nt]);
+                }
+            }
+        };
+
+        int stage = 0;
+        for (int v = v0 + warp; v < v1; v += kWarpsQ) {
+            cp_async_wait<kStagesQ - 2>();
+            __syncwarp();
+            const int t0 = tm.pos(v);
+            const uint8_t* st = ring + stage * kStageBytes;
+            // refill the stage read in the previous iteration
+            fetch(v + (kStagesQ - 1) * kWarpsQ, stage == 0 ? kStagesQ - 1 : stage - 1);
+            if (t0 + kT <= seen_hi && (t0 >= seen_lo || t0 + kT <= p.n_sinks))
+                tile(st, t0, std::false_type{});
+            else
+                tile(st, t0, std::true_type{});
+            stage = stage + 1 == kStagesQ ? 0 : stage + 1;
+            __syncwarp();  // the tile is read before its stage is refilled
+        }
+        cp_async_wait_all();
+        __syncthreads();
+
+        // ---- merge the warps: red[warp][query][kPart] over the ring ----
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float t = l[nt][e], z = zs[nt][e];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    t += __shfl_xor_sync(0xffffffffu, t, off);
+                    z += __shfl_xor_sync(0xffffffffu, z, off);
+                }
+                const int m = 8 * nt + 2 * c + e;
+                if (m < mcount) {
+                    float* o = red + (warp * RM + m) * kPart;
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x[2 * j] = fmaf(acc[j][nt][e], 0x1p24f, -z) * vref;
+                        x[2 * j + 1] = fmaf(acc[j][nt][2 + e], 0x1p20f, -z) * vref;
+                    }
+                    float4* d = reinterpret_cast<float4*>(o + 8 * g);
+                    d[0] = make_float4(x[0], x[1], x[2], x[3]);
+                    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+                    if (g == 0) {
+                        o[kHeadDim] = ref[nt][e];
+                        o[kHeadDim + 1] = t;
+                    }
+                }
+            }
+        __syncthreads();
+        const int items = mcount * (kHeadDim / 4);  // (query vector, 4 dims)
+        auto store = [&](int it, const float4& o, float sum) {
+            const int m = it >> 4, d = (it & 15) * 4;
+            const int i = (m0 + m) % p.qlen, hq = h * p.group + (m0 + m) / p.qlen;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            uint2 w;
+            w.x = Half16<T>::from_f2(o.x * inv, o.y * inv);
+            w.y = Half16<T>::from_f2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.out) +
+                                      (((int64_t)b * p.n_q_heads + hq) * p.qlen + i) * kHeadDim +
+                                      d) = w;
+        };
+        // (max, sum, o) of n partials, load(i, quad) the i-th's float4 (quad 16: max, sum), in
+        // order
+        auto combine = [&](int n, auto&& load, int q4, float& mx, float& sum) -> float4 {
+            mx = -INFINITY;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) mx = fmaxf(mx, load(i, kHeadDim / 4).x);
             const float rf = mx == -INFINITY ? 0.f : mx;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float sum = 0.f;
+            sum = 0.f;
 #pragma unroll 4
-            for (int i = 0; i < p.splits; ++i) {
-                const float4 ml = ld_cluster4(map_shared(off + kHeadDim * 4, i));
-                const float4 x = ld_cluster4(map_shared(off + (it & 15) * 16, i));
+            for (int i = 0; i < n; ++i) {
+                const float4 ml = load(i, kHeadDim / 4), x = load(i, q4);
                 const float a = exp2f(ml.x - rf);
                 sum = fmaf(ml.y, a, sum);
                 o.x = fmaf(x.x, a, o.x);
@@ -506,46 +609,77 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                 o.z = fmaf(x.z, a, o.z);
                 o.w = fmaf(x.w, a, o.w);
             }
-            store(it, o, sum);
+            return o;
+        };
+        const bool whole = STREAM ? v0 == 0 && v1 == tm.total : p.splits == 1;
+        float* mine = part;  // where this CTA's partial goes, when the unit is not whole
+        if (STREAM) mine = p.ws_part + (2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1)) * p.msub * kPart;
+        for (int it = tid; it < items; it += kThreadsQ) {
+            const float4* r0 = reinterpret_cast<const float4*>(red + (it >> 4) * kPart);
+            float mx, sum;
+            const float4 o = combine(
+                kWarpsQ, [&](int i, int q4) { return r0[i * (RM * kPart / 4) + q4]; }, it & 15, mx,
+                sum);
+            if (whole) {
+                store(it, o, sum);
+            } else {
+                float* d = mine + (it >> 4) * kPart;
+                reinterpret_cast<float4*>(d)[it & 15] = o;
+                if ((it & 15) == 0)
+                    *reinterpret_cast<float4*>(d + kHeadDim) = make_float4(mx, sum, 0.f, 0.f);
+            }
         }
-        cluster_sync_q4();  // no CTA leaves while another may still read its partial
-        return;
-    }
-
-    // ---- the last split of the unit to arrive merges all of them, in split order ----
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(&p.ws_cnt[unit], 1) == p.splits - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    const float* up = p.ws_part + (int64_t)unit * p.splits * p.msub * kPart;
-    float* wt = red;  // the splits' maxima, [mcount][splits]
-    for (int x = tid; x < mcount * p.splits; x += kThreadsQ)
-        wt[x] = __ldcg(up + ((int64_t)(x % p.splits) * p.msub + x / p.splits) * kPart + kHeadDim);
-    __syncthreads();
-    for (int it = tid; it < items; it += kThreadsQ) {
-        const int m = it >> 4, q4 = it & 15;
-        float mx = -INFINITY;
-        for (int i = 0; i < p.splits; ++i) mx = fmaxf(mx, wt[m * p.splits + i]);
-        const float rf = mx == -INFINITY ? 0.f : mx;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < p.splits; ++i) {
-            const float* src = up + ((int64_t)i * p.msub + m) * kPart;
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(src) + q4);
-            const float li = __ldcg(src + kHeadDim + 1);
-            const float a = exp2f(wt[m * p.splits + i] - rf);
-            sum = fmaf(li, a, sum);
-            o.x = fmaf(x.x, a, o.x);
-            o.y = fmaf(x.y, a, o.y);
-            o.z = fmaf(x.z, a, o.z);
-            o.w = fmaf(x.w, a, o.w);
+        if (!STREAM) {
+            if (whole) return;
+            // every CTA merges a share of the outputs out of all CTAs' partials
+            cluster_sync_q4();
+            const uint32_t base = smem_u32(part);
+            for (int it = blockIdx.x + p.splits * tid; it < items; it += p.splits * kThreadsQ) {
+                const uint32_t off = base + (it >> 4) * (kPart * 4);
+                float mx, sum;
+                const float4 o = combine(
+                    p.splits,
+                    [&](int i, int q4) { return ld_cluster4(map_shared(off + q4 * 16, i)); },
+                    it & 15, mx, sum);
+                store(it, o, sum);
+            }
+            cluster_sync_q4();  // no CTA leaves while another may still read its partial
+            return;
         }
-        store(it, o, sum);
-    }
-    if (tid == 0) p.ws_cnt[unit] = 0;
+        if (!whole) {
+            // the CTAs whose stretches meet the unit; the last to arrive merges their partials
+            // in the order of the list
+            const int64_t i0 = ((u0 + 1) * ctas - 1) / total;
+            const int64_t i1 = ((u0 + tm.total) * ctas - 1) / total;
+            const int n = (int)(i1 - i0) + 1;
+            const int unit = b * p.n_kv_heads * p.nsub + uh;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(&p.ws_cnt[unit], 1) == n - 1;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                // the first CTA's partial is of its last unit, unless its stretch starts here
+                const int64_t slot0 = 2 * i0 + (total * i0 / ctas < u0 ? 1 : 0);
+                for (int it = tid; it < items; it += kThreadsQ) {
+                    float mx, sum;
+                    const float4 o = combine(
+                        n,
+                        [&](int i, int q4) {
+                            const int64_t slot = i == 0 ? slot0 : 2 * (i0 + i);
+                            return __ldcg(reinterpret_cast<const float4*>(
+                                              p.ws_part + (slot * p.msub + (it >> 4)) * kPart) +
+                                          q4);
+                        },
+                        it & 15, mx, sum);
+                    store(it, o, sum);
+                }
+                if (tid == 0) p.ws_cnt[unit] = 0;
+            }
+        }
+        first_seg = false;
+        __syncthreads();  // the ring is free for the next unit
+    } while (STREAM);
 }
 
 // Ring of all warps, reused for the warps' partials; the CTA's partial follows them.
@@ -554,8 +688,6 @@ constexpr uint32_t q4_smem(int rm) {
     const uint32_t red = (kWarpsQ + 1) * rm * kPart * 4;
     return ring > red ? ring : red;
 }
-// the workspace merge's maxima [rm][kMaxSplitsQ] reuse the same bytes
-static_assert(16 * kMaxSplitsQ * 4 <= q4_smem(16) && 8 * kMaxSplitsQ * 4 <= q4_smem(8), "maxima");
 
 constexpr int kMaxDevQ = 64;
 
@@ -638,56 +770,51 @@ int64_t q4_tiles(int64_t bound, int qlen, int window, int n_sinks) {
     return std::min(all, near + ((int64_t)n_sinks + kT - 1) / kT);
 }
 
-// A workspace merge is considered for at most this many units, when a cluster's CTAs would
-// each read more than this many tiles per warp.
-constexpr int kWsUnitsQ = 8;
-constexpr int kWsTilesQ = 4;
-bool q4_ws_pays(int64_t units, int64_t tiles) {
-    return units <= kWsUnitsQ && tiles > (int64_t)kMaxClusterQ * kWarpsQ * kWsTilesQ;
+// From this many tiles in all (8 per warp of one wave) the launch streams the list of tiles:
+// measured 82 -> 51 us for 16 ragged rows x 8 heads up to 32768 positions (131072 tiles at
+// most), but 12.9 -> 17.3 us for 4 rows x 20 heads, 4000 positions each (10160).
+constexpr int64_t kStreamTiles = 152 * 2 * 64;
+// (its units have a counter each; a CTA looks through the rows' lengths)
+bool q4_streams(const Q4Shape& sh, int64_t batch, int64_t tiles) {
+    return sh.units * tiles >= kStreamTiles &&
+           sh.units * (int64_t)sizeof(int32_t) <= KVD_WS_COUNTER_BYTES && batch <= 4096;
 }
 
-template <typename T, int RM>
-kvd_status run_q4(Q4AttnParams& p, const Q4Shape& sh, int batch, int64_t tiles, int nsm,
-                  void* ws, size_t ws_bytes, bool pdl, cudaStream_t st) {
-    constexpr auto kern = q4_attn_kernel<T, RM>;
-    constexpr size_t smem = q4_smem(RM);
-    const int mc = prepare_q4<kern>(smem);
-    if (mc <= 0) return KVD_ERR_CUDA;
-    const int64_t most = std::max<int64_t>(1, (tiles + kWarpsQ - 1) / kWarpsQ);
-    const int64_t slots = resident_q4<kern>(smem, 1, nsm);
-    p.splits = 1;
-    p.cluster = 0;
-    if (q4_ws_pays(sh.units, tiles)) {
-        p.splits =
-            (int)std::min<int64_t>({most, kMaxSplitsQ, std::max<int64_t>(1, slots / sh.units)});
-    } else {
-        int64_t want = std::min<int64_t>(most, mc);
-        for (; want > 1; --want)
-            if (resident_q4<kern>(smem, (int)want, nsm) >= sh.units) break;
-        p.splits = (int)std::max<int64_t>(1, want);
-        p.cluster = p.splits > 1;
-    }
-    if (p.splits > 1 && !p.cluster) {
-        const size_t need = KVD_WS_COUNTER_BYTES +
-                            (size_t)sh.units * p.splits * sh.msub * kPart * sizeof(float);
+template <typename T, int NT>
+kvd_status run_q4(Q4AttnParams& p, const Q4Shape& sh, int64_t tiles, int nsm, void* ws,
+                  size_t ws_bytes, bool pdl, cudaStream_t st) {
+    constexpr size_t smem = q4_smem(8 * NT);
+    if (q4_streams(sh, p.batch, tiles)) {
+        constexpr auto kern = q4_attn_kernel<T, NT, true>;
+        if (prepare_q4<kern>(smem) <= 0) return KVD_ERR_CUDA;
+        const int slots = std::min(kMaxStream, resident_q4<kern>(smem, 1, nsm));
+        if (slots <= 0) return KVD_ERR_CUDA;
+        const size_t need =
+            KVD_WS_COUNTER_BYTES + (size_t)2 * slots * sh.msub * kPart * sizeof(float);
         if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < need)
             return KVD_ERR_WORKSPACE;
         p.ws_cnt = static_cast<int32_t*>(ws);
         p.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + KVD_WS_COUNTER_BYTES);
+        return launch(kern, dim3((unsigned)slots), dim3(kThreadsQ), smem, st, pdl, p);
     }
-    const dim3 grid((unsigned)p.splits, (unsigned)(p.n_kv_heads * sh.nsub), (unsigned)batch);
-    return launch_ex(kern, grid, dim3(kThreadsQ), smem, st, pdl,
-                     p.cluster ? (unsigned)p.splits : 1u, p);
+    constexpr auto kern = q4_attn_kernel<T, NT, false>;
+    const int mc = prepare_q4<kern>(smem);
+    if (mc <= 0) return KVD_ERR_CUDA;
+    // the most splits (a tile per warp at least) whose clusters are all resident at once
+    int64_t want = std::min<int64_t>(std::max<int64_t>(1, (tiles + kWarpsQ - 1) / kWarpsQ), mc);
+    for (; want > 1; --want)
+        if (resident_q4<kern>(smem, (int)want, nsm) >= sh.units) break;
+    p.splits = (int)std::max<int64_t>(1, want);
+    const dim3 grid((unsigned)p.splits, (unsigned)(p.n_kv_heads * sh.nsub), (unsigned)p.batch);
+    return launch_ex(kern, grid, dim3(kThreadsQ), smem, st, pdl, (unsigned)p.splits, p);
 }
 
 }  // namespace
 
 size_t q4_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int qlen, int max_len) {
     const Q4Shape sh = q4_shape(batch, n_q_heads, n_kv_heads, qlen);
-    const int64_t tiles = q4_tiles(max_len, qlen, 0, 0);
-    if (!q4_ws_pays(sh.units, tiles)) return KVD_WS_COUNTER_BYTES;
-    const size_t part = (size_t)sh.units * kMaxSplitsQ * sh.msub * kPart * sizeof(float);
-    return KVD_WS_COUNTER_BYTES + (part + 255) / 256 * 256;
+    if (!q4_streams(sh, batch, q4_tiles(max_len, qlen, 0, 0))) return KVD_WS_COUNTER_BYTES;
+    return KVD_WS_COUNTER_BYTES + (size_t)2 * kMaxStream * sh.msub * kPart * sizeof(float);
 }
 
 }  // namespace kvd
@@ -726,6 +853,7 @@ extern "C" kvd_status kvd_q4_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_he
     p.lens = lens;
     p.fixed_len = fixed_len;
     p.capacity = cache->capacity;
+    p.batch = batch;
     p.n_q_heads = n_q_heads;
     p.n_kv_heads = cache->n_kv_heads;
     p.group = sh.group;
@@ -743,13 +871,10 @@ extern "C" kvd_status kvd_q4_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_he
         q4_tiles(lens ? cache->capacity : fixed_len, qlen, window, p.n_sinks);
     const bool pdl = (flags & (KVD_FLAG_PDL | KVD_FLAG_EARLY_KV)) != 0;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const bool one = sh.msub <= 8;
     if (dtype == KVD_BF16)
-        return sh.msub <= 8 ? run_q4<__nv_bfloat16, 8>(p, sh, batch, tiles, nsm, workspace,
-                                                       workspace_bytes, pdl, st)
-                            : run_q4<__nv_bfloat16, 16>(p, sh, batch, tiles, nsm, workspace,
-                                                        workspace_bytes, pdl, st);
-    return sh.msub <= 8 ? run_q4<__half, 8>(p, sh, batch, tiles, nsm, workspace, workspace_bytes,
-                                            pdl, st)
-                        : run_q4<__half, 16>(p, sh, batch, tiles, nsm, workspace,
-                                             workspace_bytes, pdl, st);
+        return one ? run_q4<__nv_bfloat16, 1>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st)
+                   : run_q4<__nv_bfloat16, 2>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st);
+    return one ? run_q4<__half, 1>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st)
+               : run_q4<__half, 2>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st);
 }

@@ -8,10 +8,14 @@
 //
 // Design. Both kernels are bound by HBM on a prompt (append: 128 bytes read and 36 written
 // per row; read-back the other way round) and by the launch on a step. Four lanes own a
-// row, 16 values (two 16-byte accesses) each: minimum and maximum take two shuffles, and
-// every lane packs its own 8 bytes. Division, subtraction and rounding are the IEEE
-// operations, in one fixed order, so that the stored bits follow from the definition on
-// any machine.
+// row, 16 values (two 16-byte accesses) each; minimum and maximum are taken on the 16-bit
+// values, two at a time, and over the row with two shuffles. x / step rounded correctly, for
+// every value of a row by the same step, is a product with the rounded reciprocal and one
+// remainder step (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990: exact when the reciprocal is rounded to nearest and nothing
+// leaves the normal range), a fifth of the instructions of a division; rows whose step is
+// near the ends of the range divide. Everything else is the IEEE operation in one fixed
+// order, so that the stored bits follow from the definition on any machine.
 #include "kvd_common.cuh"
 #include "kvd_internal.h"
 
@@ -39,24 +43,63 @@ __device__ __forceinline__ uint16_t f2bf(float x) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 
-// Quantise the 16 values of this lane (a quarter of a row; the row's lanes are lane ^ 1,
-// ^ 2, ^ 3): packed nibbles and the row's (step | zero point << 16). bad: the row holds an
-// infinity or a NaN.
-__device__ __forceinline__ uint2 quantise16(const float* x, uint32_t& par, bool& bad) {
-    float lo = x[0], hi = x[0], odd = 0.f;
+__device__ __forceinline__ __half2 as_pair(uint32_t v, __half) {
+    return *reinterpret_cast<__half2*>(&v);
+}
+__device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t v, __nv_bfloat16) {
+    return *reinterpret_cast<__nv_bfloat162*>(&v);
+}
+
+// n = clamp(rint(x / step + z), 0, 15) of the 16 values in the words v, packed.
+template <typename T, bool FAST>
+__device__ __forceinline__ uint2 pack16(const uint32_t* v, float step, float z) {
+    const float rcp = FAST ? __frcp_rn(step) : 0.f;
+    // the words, less what the sums below add to them besides n
+    constexpr uint32_t kMagic = 0x4B400000u;  // 1.5 * 2^23
+    constexpr uint32_t kRest = kMagic * 0x11111111u;
+    uint32_t w[2] = {0u - kRest, 0u - kRest};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        lo = fminf(lo, x[e]);
-        hi = fmaxf(hi, x[e]);
-        odd = fmaf(x[e], 0.f, odd);  // 0, or NaN from an infinity or a NaN
+    for (int e = 0; e < 8; ++e) {
+        const float2 x2 = Half16<T>::to_f2(v[e]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x = i ? x2.y : x2.x;
+            float q;
+            if (FAST) {
+                q = __fmul_rn(x, rcp);
+                q = __fmaf_rn(__fmaf_rn(-q, step, x), rcp, q);
+            } else {
+                q = __fdiv_rn(x, step);
+            }
+            // clamped, then rounded to even by adding 1.5 * 2^23: n in the low bits
+            const float t = fminf(fmaxf(__fadd_rn(q, z), 0.f), 15.f);
+            w[e >> 2] += __float_as_uint(__fadd_rn(t, 12582912.f)) << (4 * (2 * (e & 3) + i));
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Quantise the 16 values (eight words) of this lane, a quarter of a row; the row's lanes are
+// lane ^ 1, ^ 2, ^ 3: packed nibbles and the row's (step | zero point << 16). bad: the row
+// holds an infinity or a NaN.
+template <typename T>
+__device__ __forceinline__ uint2 quantise16(const uint32_t* v, uint32_t& par, bool& bad) {
+    auto l2 = as_pair(v[0], T()), h2 = l2;  // (NaN stays)
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+        l2 = __hmin2_nan(l2, as_pair(v[e], T()));
+        h2 = __hmax2_nan(h2, as_pair(v[e], T()));
     }
 #pragma unroll
     for (int off = 1; off <= 2; off <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-        odd += __shfl_xor_sync(0xffffffffu, odd, off);
+        l2 = __hmin2_nan(l2, __shfl_xor_sync(0xffffffffu, l2, off));
+        h2 = __hmax2_nan(h2, __shfl_xor_sync(0xffffffffu, h2, off));
     }
-    bad = !(odd == 0.f);
+    const float2 lf = Half16<T>::to_f2(*reinterpret_cast<const uint32_t*>(&l2));
+    const float2 hf = Half16<T>::to_f2(*reinterpret_cast<const uint32_t*>(&h2));
+    const float lo = fminf(lf.x, lf.y), hi = fmaxf(hf.x, hf.y);
+    // (0 * finite is 0)
+    bad = !(lf.x * 0.f + lf.y * 0.f + hf.x * 0.f + hf.y * 0.f == 0.f);
     // halves: no finite range overflows
     uint16_t sbits =
         f2bf(__fdiv_rn(__fsub_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo)), 7.5f));
@@ -70,21 +113,17 @@ __device__ __forceinline__ uint2 quantise16(const float* x, uint32_t& par, bool&
         }
         z = lo < 0.f ? 15.f : 0.f;
     } else {
-        z = __half2float(__float2half_rn(__fdiv_rn(-lo, step)));
+        z = __half2float(__float2half_rn(__fdiv_rn(-lo, step))) + 0.f;  // (no -0)
     }
     par = (uint32_t)sbits | ((uint32_t)__half_as_ushort(__float2half_rn(z)) << 16);
     if (bad) {
         par = 0x7FC0u;
         return make_uint2(0u, 0u);
     }
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const float t = rintf(__fadd_rn(__fdiv_rn(x[e], step), z));
-        const uint32_t n = (uint32_t)fminf(fmaxf(t, 0.f), 15.f);
-        w[e >> 3] |= n << (4 * (e & 7));
-    }
-    return make_uint2(w[0], w[1]);
+    // a quotient that leaves the normal range is far below half a step, or never occurs here
+    // (|x / step| <= 2^15 or so)
+    return step > 0x1p-90f && step < 0x1p90f ? pack16<T, true>(v, step, z)
+                                             : pack16<T, false>(v, step, z);
 }
 
 struct Q4Row {
@@ -92,10 +131,17 @@ struct Q4Row {
 };
 __device__ __forceinline__ Q4Row split_row(const Q4RowsParams& p, int64_t row) {
     Q4Row r;
-    r.j = (int)(row % p.n);
-    const int64_t bh = row / p.n;
-    r.h = (int)(bh % p.heads);
-    r.b = (int)(bh / p.heads);
+    if (p.rows <= 0xFFFFFFFFll) {  // 32-bit divisions: the usual case
+        const uint32_t bh = (uint32_t)row / (uint32_t)p.n;
+        r.j = (int)((uint32_t)row - bh * (uint32_t)p.n);
+        r.b = (int)(bh / (uint32_t)p.heads);
+        r.h = (int)(bh - (uint32_t)r.b * (uint32_t)p.heads);
+    } else {
+        const int64_t bh = row / p.n;
+        r.j = (int)(row % p.n);
+        r.h = (int)(bh % p.heads);
+        r.b = (int)(bh / p.heads);
+    }
     return r;
 }
 
@@ -108,9 +154,7 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4RowsParam
     const int t = row >= p.rows ? 1 : 0;  // K rows, then V rows
     row -= t ? p.rows : 0;
     bool live = row < p.rows;
-    float x[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.f;
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), d = a;
     Q4Row r = {0, 0, 0};
     int len = 0;
     if (live) {
@@ -123,18 +167,22 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4RowsParam
         if (first && p.lens_out) p.lens_out[r.b] = wrong ? len : len + cnt;
         live = !wrong && r.j < cnt;
     }
+    if (!__any_sync(0xffffffffu, live)) {  // (rows past their prompts)
+        pdl_trigger();
+        return;
+    }
     if (live) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.in[t] + row * kRowBytes + l * 32);
-        const uint4 a = src[0], b = src[1];
-        unpack8<T>(a, x);
-        unpack8<T>(b, x + 8);
+        const uint4* src = reinterpret_cast<const uint4*>((t ? p.in[1] : p.in[0]) + row * kRowBytes + l * 32);
+        a = src[0];
+        d = src[1];
     }
     uint32_t par;
     bool bad;
-    const uint2 w = quantise16(x, par, bad);  // every lane: the shuffles need whole rows
+    const uint32_t v[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+    const uint2 w = quantise16<T>(v, par, bad);  // every lane: the shuffles need whole rows
     if (live) {
         const int64_t at = r.b * p.sb + r.h * p.sh + len + r.j;
-        *reinterpret_cast<uint2*>(p.data[t] + at * 32 + l * 8) = w;
+        *reinterpret_cast<uint2*>((t ? p.data[1] : p.data[0]) + at * 32 + l * 8) = w;
         if (l == 0) {
             *reinterpret_cast<uint32_t*>(p.params + at * 8 + t * 4) = par;
             if (bad) flag_error(p.dev_err, KVD_ERR_NAN);
@@ -151,14 +199,14 @@ __global__ void __launch_bounds__(kQ4Threads) q4_dequant_kernel(const Q4RowsPara
     int64_t row = idx >> 2;
     const int t = row >= p.rows ? 1 : 0;
     row -= t ? p.rows : 0;
-    if (row < p.rows && p.out[t]) {
+    if (row < p.rows && (t ? p.out[1] : p.out[0])) {
         const Q4Row r = split_row(p, row);
         const int pos = p.pos0 ? p.pos0[r.b] : 0;
         if (pos < 0 || (int64_t)pos + p.n > p.capacity) {
             if (r.h == 0 && r.j == 0 && l == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
         } else {
             const int64_t at = r.b * p.sb + r.h * p.sh + pos + r.j;
-            const uint2 w = *reinterpret_cast<const uint2*>(p.data[t] + at * 32 + l * 8);
+            const uint2 w = *reinterpret_cast<const uint2*>((t ? p.data[1] : p.data[0]) + at * 32 + l * 8);
             const uint32_t par = *reinterpret_cast<const uint32_t*>(p.params + at * 8 + t * 4);
             const float step = bf16_up((uint16_t)par);
             const float z = __half2float(__ushort_as_half((uint16_t)(par >> 16)));
@@ -166,10 +214,12 @@ __global__ void __launch_bounds__(kQ4Threads) q4_dequant_kernel(const Q4RowsPara
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t v = (e < 4 ? w.x : w.y) >> (8 * (e & 3));
-                o[e] = Half16<T>::from_f2(__fmul_rn(step, (float)(v & 15u) - z),
-                                          __fmul_rn(step, (float)((v >> 4) & 15u) - z));
+                // n as 2^23 + n (no conversion), exactly
+                const float n0 = __uint_as_float(0x4B000000u | (v & 15u)) - 8388608.f;
+                const float n1 = __uint_as_float(0x4B000000u | (v >> 4 & 15u)) - 8388608.f;
+                o[e] = Half16<T>::from_f2(__fmul_rn(step, n0 - z), __fmul_rn(step, n1 - z));
             }
-            uint4* dst = reinterpret_cast<uint4*>(p.out[t] + row * kRowBytes + l * 32);
+            uint4* dst = reinterpret_cast<uint4*>((t ? p.out[1] : p.out[0]) + row * kRowBytes + l * 32);
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
             dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }

@@ -108,16 +108,20 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
             for (int u = 0; u < U; ++u) {
                 const int h0 = (int)(hg * p.iters + it + u) * 8 + (lane >> 2);
                 const bool on = it + u < p.iters && h0 < total;
-                const int t = on && h0 >= p.heads[0] ? 1 : 0;
+                // (selects: an index known only at run time would put the parameters on the
+                // stack)
+                const bool t = on && h0 >= p.heads[0];
                 const int h = t ? h0 - p.heads[0] : h0;
                 lo[u] = hi[u] = make_uint4(0u, 0u, 0u, 0u);
                 dst[u] = nullptr;
-                w[u] = p.w[t];
+                w[u] = t ? p.w[1] : p.w[0];
                 if (on) {
-                    const uint8_t* src = p.x[t] + b * p.sb[t] + h * p.sh[t] + j * p.st[t];
+                    const uint8_t* src = (t ? p.x[1] : p.x[0]) + b * (t ? p.sb[1] : p.sb[0]) +
+                                         h * (t ? p.sh[1] : p.sh[0]) + j * (t ? p.st[1] : p.st[0]);
                     lo[u] = *reinterpret_cast<const uint4*>(src + l * 16);
                     hi[u] = *reinterpret_cast<const uint4*>(src + 64 + l * 16);
-                    dst[u] = p.y[t] + (((int64_t)b * p.heads[t] + h) * p.n + j) * kRowBytes;
+                    dst[u] = (t ? p.y[1] : p.y[0]) +
+                             (((int64_t)b * (t ? p.heads[1] : p.heads[0]) + h) * p.n + j) * kRowBytes;
                 }
             }
             if (!have) {  // after the first loads are on their way

@@ -73,7 +73,7 @@ def q4_quantise(x):
     flat = step == 0
     one = bf16_round(np.abs(lo) / np.float32(15))
     one = np.where(one == 0, np.float32(1), one)
-    z = (-lo / np.where(flat, np.float32(1), step)).astype(np.float16).astype(np.float32)
+    z = (-lo / np.where(flat, np.float32(1), step)).astype(np.float16).astype(np.float32) + 0
     z = np.where(flat, np.where(lo < 0, np.float32(15), np.float32(0)), z)
     step = np.where(flat, one, step)
     n = np.clip(np.rint(x / step + z), 0, 15)
