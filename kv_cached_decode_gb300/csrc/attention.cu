@@ -754,7 +754,7 @@ __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, flo
 }
 
 // ------------------------------------------------- one query vector per KV head (SIMT) --
-template <typename T, bool ROPE, bool GROUPED = false, bool WINDOW = false>
+template <typename T, bool ROPE, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per SM
     decode_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
     const int grp = lane >> 3, c8 = lane & 7;
 
     CtaCtx c;
-    if (!prologue<ROPE, WINDOW>(p, c, smem, bars, qoff, smem + L.app_off, &tmk, &tmv)) return;
+    if (!prologue<ROPE, false>(p, c, smem, bars, qoff, smem + L.app_off, &tmk, &tmv)) return;
 
     float qf[8];
     {
@@ -805,15 +805,12 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 
-    auto visible = [&](int t) {
-        return t < c.t_end && (!WINDOW || t >= c.wlo || t < p.n_sinks);
-    };
     auto slab = [&](const uint8_t* sK, const uint8_t* sV, int tile0, int slab0) {
         float sc[4];
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const int row = slab0 + grp * 4 + jj;
-            const bool valid = visible(tile0 + row);
+            const bool valid = tile0 + row < c.t_end;
             const uint4 kr = *reinterpret_cast<const uint4*>(sK + swz(row, c8));
             float kf[8];
             unpack8<T>(kr, kf);
@@ -842,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const int row = slab0 + grp * 4 + jj;
-            const bool valid = visible(tile0 + row);
+            const bool valid = tile0 + row < c.t_end;
             const uint4 vr = *reinterpret_cast<const uint4*>(sV + swz(row, c8));
             float vf[8];
             unpack8<T>(vr, vf);
@@ -850,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(sc[jj], valid ? vf[e] : 0.f, acc[e]);
         }
     };
-    if (!run_tiles<T, ROPE, WINDOW>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
+    if (!run_tiles<T, ROPE, false>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
         return;
 
     // Merge the four 8-lane groups of each warp (they saw different positions).
@@ -879,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
         }
     }
     __syncthreads();
-    finish_cta<T, RM, GROUPED, WINDOW>(p, c, red, mrg, &bars[p.stages], misc, qoff,
+    finish_cta<T, RM, GROUPED, false>(p, c, red, mrg, &bars[p.stages], misc, qoff,
                                smem + L.bar_off - 4096);
 }
 
@@ -990,6 +987,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     auto slab = [&](uint8_t* sK, uint8_t* sV, int tile0, int slab0) {
         const int nvalid = min(16, max(0, c.t_end - tile0 - slab0));
         if (nvalid == 0) return;
+        bool partial = false;  // WINDOW: some query of the block does not see all 16 positions
         if (nvalid < 16) {
             // Rows past the end hold stale or fill data; P is 0 there but 0 * NaN would
             // still poison the product, so clear them before P.V.
@@ -1009,7 +1007,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
             const int ts = tile0 + slab0;
             if (ts >= p.n_sinks && ts + 16 <= c.wlo) return;
             const int last = (int)max((int64_t)c.len - p.window, (int64_t)0);
-            if (!(ts + 16 <= c.len - p.qlen + 1 && (ts >= last || ts + 16 <= p.n_sinks))) {
+            partial = !(ts + 16 <= c.len - p.qlen + 1 && (ts >= last || ts + 16 <= p.n_sinks));
+            if (partial) {
 #pragma unroll
                 for (int x = lane; x < 128; x += 32) {
                     const int row = x >> 3, t = ts + row;
@@ -1054,11 +1053,69 @@ __global__ void __launch_bounds__(kThreads, MINB)
             for (int e = 0; e < kAcc; ++e) {
                 const int key = tile0 + slab0 + n * 8 + qc + (e & 1);
                 const int lim = e < 2 ? limA : limB;
-                const bool in = !WINDOW || key >= (e < 2 ? wloA : wloB) || key < p.n_sinks;
-                sacc[n][e] = key < lim && in ? sacc[n][e] * p.scale_log2 : -INFINITY;
+                if (WINDOW) {
+                    sacc[n][e] *= p.scale_log2;
+                    if (partial)
+                        sacc[n][e] = key < lim && (key >= (e < 2 ? wloA : wloB) || key < p.n_sinks)
+                                         ? sacc[n][e]
+                                         : -INFINITY;
+                } else {
+                    sacc[n][e] = key < lim ? sacc[n][e] * p.scale_log2 : -INFINITY;
+                }
             }
         uint32_t pa[4];
-        if constexpr (kFull) {
+        if constexpr (WINDOW) {
+            // A row's reference moves only when a score exceeds it by 2^8 (one vote for the
+            // warp): the usual slab rescales nothing and reduces nothing across lanes. The
+            // normaliser sums the unrounded weights (rounding to nearest leaves no bias).
+            constexpr float kGrow = 8.f;
+            float tA = fmaxf(fmaxf(sacc[0][0], sacc[0][1]), fmaxf(sacc[1][0], sacc[1][1]));
+            float tB = kFull ? fmaxf(fmaxf(sacc[0][kAcc - 2], sacc[0][kAcc - 1]),
+                                     fmaxf(sacc[1][kAcc - 2], sacc[1][kAcc - 1]))
+                             : -INFINITY;
+            if (__any_sync(0xffffffffu, tA > mA + kGrow || (kFull && tB > mB + kGrow))) {
+                tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
+                tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2));
+                const float nA = fmaxf(mA, tA);
+                const float aA = nA == -INFINITY ? 1.f : exp2f(mA - nA);
+                mA = nA;
+                lA *= aA;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    oacc[n][0] *= aA;
+                    oacc[n][1] *= aA;
+                }
+                if (kFull) {
+                    tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 1));
+                    tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2));
+                    const float nB = fmaxf(mB, tB);
+                    const float aB = nB == -INFINITY ? 1.f : exp2f(mB - nB);
+                    mB = nB;
+                    lB *= aB;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        oacc[n][kAcc - 2] *= aB;
+                        oacc[n][kAcc - 1] *= aB;
+                    }
+                }
+            }
+            const float refA = mA == -INFINITY ? 0.f : mA, refB = mB == -INFINITY ? 0.f : mB;
+            const float w0 = ex2_approx(sacc[0][0] - refA), w1 = ex2_approx(sacc[0][1] - refA);
+            const float w2 = ex2_approx(sacc[1][0] - refA), w3 = ex2_approx(sacc[1][1] - refA);
+            lA += (w0 + w1) + (w2 + w3);
+            pa[0] = Half16<T>::from_f2(w0, w1);
+            pa[2] = Half16<T>::from_f2(w2, w3);
+            pa[1] = pa[3] = 0u;
+            if (kFull) {
+                const float v0 = ex2_approx(sacc[0][kAcc - 2] - refB);
+                const float v1 = ex2_approx(sacc[0][kAcc - 1] - refB);
+                const float v2 = ex2_approx(sacc[1][kAcc - 2] - refB);
+                const float v3 = ex2_approx(sacc[1][kAcc - 1] - refB);
+                lB += (v0 + v1) + (v2 + v3);
+                pa[1] = Half16<T>::from_f2(v0, v1);
+                pa[3] = Half16<T>::from_f2(v2, v3);
+            }
+        } else if constexpr (kFull) {
             // rows 0..7 (A) and 8..15 (B): two independent chains, interleaved
             float tA = fmaxf(fmaxf(sacc[0][0], sacc[0][1]), fmaxf(sacc[1][0], sacc[1][1]));
             float tB = fmaxf(fmaxf(sacc[0][2], sacc[0][3]), fmaxf(sacc[1][2], sacc[1][3]));
@@ -1245,16 +1302,15 @@ int prepare_kernel(size_t smem_bytes) {
 enum Variant {
     kSimt = 1, kMma = 2, kMma3 = 3, kSimtRope = 4, kMmaRope = 5, kMma8 = 6,
     kSimtG = 7, kMmaG = 8,  // kSimt / kMma with the merge across clusters of a unit
-    kSimtW = 9, kMmaW = 10, kSimtRopeW = 11, kMmaRopeW = 12  // with a sliding window
+    kMma8W = 9, kMmaW = 10, kMmaRopeW = 11  // with a sliding window
 };
 
 // Rows of the warp partials (the red area) of a variant: 16 for the tensor-core builds,
 // 8 for the 8-vector build, 1 for the CUDA-core kernel.
 constexpr int variant_rmax(int var) {
-    return (var == kSimt || var == kSimtRope || var == kSimtG || var == kSimtW ||
-            var == kSimtRopeW)
-               ? 1
-               : var == kMma8 ? 8 : 16;
+    return (var == kSimt || var == kSimtRope || var == kSimtG) ? 1
+           : (var == kMma8 || var == kMma8W)                   ? 8
+                                                               : 16;
 }
 
 template <typename T>
@@ -1270,8 +1326,7 @@ int prepare(int var) {
     case kSimtRope: return prepare_kernel<decode_attn_kernel<T, true>>(smem);
     case kMmaG: return prepare_kernel<block_attn_kernel<T, 2, false, 16, true>>(smem);
     case kSimtG: return prepare_kernel<decode_attn_kernel<T, false, true>>(smem);
-    case kSimtW: return prepare_kernel<decode_attn_kernel<T, false, false, true>>(smem);
-    case kSimtRopeW: return prepare_kernel<decode_attn_kernel<T, true, false, true>>(smem);
+    case kMma8W: return prepare_kernel<block_attn_kernel<T, 3, false, 8, false, true>>(smem);
     case kMmaW: return prepare_kernel<block_attn_kernel<T, 2, false, 16, false, true>>(smem);
     case kMmaRopeW: return prepare_kernel<block_attn_kernel<T, 2, true, 16, false, true>>(smem);
     default: return prepare_kernel<decode_attn_kernel<T, false>>(smem);
@@ -1288,9 +1343,8 @@ const void* kernel_of(int var) {
     case kSimtRope: return reinterpret_cast<const void*>(decode_attn_kernel<T, true>);
     case kMmaG: return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 16, true>);
     case kSimtG: return reinterpret_cast<const void*>(decode_attn_kernel<T, false, true>);
-    case kSimtW: return reinterpret_cast<const void*>(decode_attn_kernel<T, false, false, true>);
-    case kSimtRopeW:
-        return reinterpret_cast<const void*>(decode_attn_kernel<T, true, false, true>);
+    case kMma8W:
+        return reinterpret_cast<const void*>(block_attn_kernel<T, 3, false, 8, false, true>);
     case kMmaW:
         return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 16, false, true>);
     case kMmaRopeW:
@@ -1328,12 +1382,9 @@ kvd_status launch_attn(int var, dim3 grid, cudaStream_t st, bool pdl, unsigned c
     case kSimtG:
         return launch_ex(decode_attn_kernel<T, false, true>, grid, dim3(kThreads), simt_smem, st,
                          pdl, cl, mk, mv, p);
-    case kSimtW:
-        return launch_ex(decode_attn_kernel<T, false, false, true>, grid, dim3(kThreads),
-                         simt_smem, st, pdl, cl, mk, mv, p);
-    case kSimtRopeW:
-        return launch_ex(decode_attn_kernel<T, true, false, true>, grid, dim3(kThreads),
-                         simt_smem, st, pdl, cl, mk, mv, p);
+    case kMma8W:
+        return launch_ex(block_attn_kernel<T, 3, false, 8, false, true>, grid, dim3(kThreads),
+                         smem_layout(p.stages, 8, slots, app_rows).total, st, pdl, cl, mk, mv, p);
     case kMmaW:
         return launch_ex(block_attn_kernel<T, 2, false, 16, false, true>, grid, dim3(kThreads),
                          mma_smem, st, pdl, cl, mk, mv, p);
@@ -1515,9 +1566,15 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
                resident(kern, var * 2 + (bf ? 1 : 0), plan_smem(Q, var, app_rows), 1, nsm);
     };
     // the builds with the rotation compiled in stand for kSimt and kMma when it is on
-    const int simt = windowed ? (rope ? kSimtRopeW : kSimtW) : rope ? kSimtRope : kSimt;
+    // Windowed calls run on the tensor cores always: one query vector costs the CUDA cores
+    // 512 instructions per 16 positions, the 8-row build about 150 (measured, 32 rows x 20
+    // heads, a window of 2047: see the kernel's comment).
+    const int simt = rope ? kSimtRope : kSimt;
     const int mma = windowed ? (rope ? kMmaRopeW : kMmaW) : rope ? kMmaRope : kMma;
-    int var = (verify || (int64_t)rows_per_kv * group * qlen >= 2) ? mma : simt;
+    const int64_t vectors = (int64_t)rows_per_kv * group * qlen;
+    const int blocks16 = (int)((vectors + kMmaQueryBlock - 1) / kMmaQueryBlock);
+    const bool eight = (vectors + blocks16 - 1) / blocks16 <= 8;  // vectors per block
+    int var = windowed ? (eight && !rope ? kMma8W : mma) : (verify || (int64_t)rows_per_kv * group * qlen >= 2) ? mma : simt;
     AttnPlan P;
     if (!plan_for(var, P)) return KVD_ERR_CUDA;
     if (var == simt && P.tiles_per_split <= 2) {
@@ -1566,6 +1623,28 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
         if (resident(kern, var * 2 + (bf ? 1 : 0), plan_smem(D, var, app_rows), D.splits, nsm) >=
             D.units)
             P = D;
+    }
+    if (windowed && P.splits == 1 && P.rounds > 1) {
+        // More units than are resident at once, all of about the same length (a window): a
+        // last wave that is nearly empty costs as much as a full one, so cut the units where
+        // that fills it. Costs in tiles: a block streams its own, and two for its start and
+        // merge.
+        const void* kern = bf ? kernel_of<__nv_bfloat16>(var) : kernel_of<__half>(var);
+        const int kid = var * 2 + (bf ? 1 : 0);
+        auto cost = [&](const AttnPlan& Q) -> int64_t {
+            const int64_t n = resident(kern, kid, plan_smem(Q, var, app_rows), Q.splits, nsm);
+            return n > 0 ? (Q.units + n - 1) / n * (Q.tiles_per_split + 2) : INT64_MAX;
+        };
+        int64_t best = cost(P);
+        for (int sp = 2; sp <= 4; ++sp) {
+            const AttnPlan Q = plan_attention(batch, n_q_heads, kv->n_kv_heads, rows_per_kv, qlen,
+                                              len_bound, kMmaQueryBlock, sp, kMaxClusterSplits);
+            if (Q.splits != sp || !Q.cluster) continue;
+            if (const int64_t t = cost(Q); t < best) {
+                best = t;
+                P = Q;
+            }
+        }
     }
     if ((int64_t)kv->n_kv_heads * P.nsub > 65535) return KVD_ERR_UNSUPPORTED;
     const bool ws_merge = (P.splits > 1 && !P.cluster) || P.cgroups > 1;

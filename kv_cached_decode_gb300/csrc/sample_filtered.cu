@@ -36,10 +36,12 @@
 //     all CTAs instead takes longer than both). If at most kList ids are in it, every CTA
 //     gathers them and ranks them all against all; else the interval of their bit patterns is
 //     cut into 1024 again, until few are left or all are equal, when the cut falls by id.
+//     A prefix of at most kList ids (the usual top-k) is gathered whole and finished there.
 //  4. The kept mass per warp segment; one exchange; the CTA that holds u * total scans that
 //     segment and writes the row's outputs. The others have exited.
 // Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p.
 #include <algorithm>
+#include <climits>
 #include <cstddef>
 #include <mutex>
 
@@ -112,7 +114,7 @@ struct alignas(16) FilterShared {
     uint32_t ex_fin[kSfMaxCluster], ex_cnt[kSfMaxCluster], ex_tie[kSfMaxCluster];
     unsigned long long red[kSfWarps];
     uint32_t red32[kSfWarps], red_b[kSfWarps];
-    uint32_t n_list;
+    uint32_t n_list, n_all;
     float cut_x;
     int32_t cut_id;
     int32_t found;
@@ -325,13 +327,14 @@ __device__ __forceinline__ void for_ids(const Row& R, bool full, F&& f) {
     }
 }
 
-enum SelectResult { kCutHere, kBeyond, kAll };
+enum SelectResult { kCutHere, kBeyond, kAll, kFew };
 
 // The last id of the shortest prefix (within `kept`) that holds `k` ids (MASS false) or whose
 // mass reaches frac * (mass of `kept`) (MASS true; frac < 1; `light`: this CTA's light mass, 0
 // when none of it is kept). Over the listed ids, or with `full` over all. Returns kBeyond,
 // leaving `kept`, when the cut is not among the listed ids; kAll when the prefix ends among
-// ids of weight 0. Every thread of the cluster calls it; the histogram is clear before and
+// ids of weight 0; kFew (counts only) with the whole prefix, and the rest of its last bin, in
+// S.all of every CTA (S.n_all entries, in no order). Every thread of the cluster calls it; the histogram is clear before and
 // after.
 template <bool MASS>
 __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, bool full,
@@ -432,18 +435,21 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
         const int in_grp = hit ? __ffs(hit) - 1 : 0;
         before = __shfl_sync(0xffffffffu, inc - v, in_grp);
         const int bin = grp * kGroup + in_grp;
+        // a short prefix is gathered whole: what follows needs no exchange then
+        const bool few =
+            !MASS && first && __shfl_sync(0xffffffffu, inc, in_grp) <= (unsigned long long)kList;
         __syncthreads();  // n_list is 0
 
         // ---- gather its members ----
         for_ids(R, full, [&](float x, int i) {
             bool in;
             const int mine = bin_of(x, in);
-            if (in && mine == bin && kept.keeps(x, R.lo + i)) {
+            if (in && (mine == bin || (few && mine < bin)) && kept.keeps(x, R.lo + i)) {
                 const uint32_t at = atomicAdd(&S.n_list, 1u);
                 if (at < kList) {
                     S.list[at].x = x;
                     S.list[at].id = R.lo + i;
-                    S.list[at].w = MASS ? W.of(x) : 1ull;
+                    S.list[at].w = MASS || few ? W.of(x) : 1ull;
                 }
             }
         });
@@ -473,7 +479,9 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
                         R.cluster > 1 ? ld_cluster_2u64(&S.list[off], from)
                                       : *reinterpret_cast<const ulonglong2*>(&S.list[off]);
             }
+            if (tid == 0) S.n_all = n;
             __syncthreads();
+            if (few) return kFew;
             if (tid < (int)n) {
                 const Entry me = S.all[tid];
                 unsigned long long sum = before;
@@ -592,6 +600,80 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
         kept.x = xv;
         kept.id = S.cut_id;
         return kCutHere;
+    }
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float log_share(unsigned long long w, unsigned long long total) {
+    // near 1 from what is left over, which the integers know exactly
+    const float tf = (float)total;
+    return w > total / 2 ? log1pf(-((float)(total - w) / tf)) : logf((float)w / tf);
+}
+
+// A short prefix, all in S.all: top-k, top-p, min-p and the draw by ranking every entry against
+// every other.
+__device__ void draw_few(FilterShared& S, const Weights& W, const FilterParams& p, int b,
+                         int top_k, float top_p, unsigned long long w_min, float y_max, float u) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    static_assert(kList == 128, "four warps");
+    if (tid >= kList) return;
+    auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    auto sum4 = [&](unsigned long long v) {  // over the 128 threads
+        v = warp_sum(v);
+        sync();
+        if (lane == 0) S.red[warp] = v;
+        sync();
+        return S.red[0] + S.red[1] + S.red[2] + S.red[3];
+    };
+    const int n = (int)S.n_all;
+    const Entry me = tid < n ? S.all[tid] : Entry{-INFINITY, INT_MAX, 0ull};
+    int before = 0;
+    unsigned long long mass = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const Entry o = S.all[i];
+        const bool ahead = o.x > me.x || (o.x == me.x && o.id < me.id);
+        before += ahead;
+        mass += ahead ? o.w : 0ull;
+    }
+    bool in = tid < n && before < top_k;
+    if (top_p < 1.f) {  // (uniform)
+        const unsigned long long all = sum4(in ? me.w : 0ull);
+        bool rest = false;
+        unsigned long long target = top_p > 0.f ? mul_floor(top_p, all, rest) : 0ull;
+        target += rest ? 1 : 0;
+        if (target == 0) target = 1;
+        in = in && mass < target;
+    }
+    in = in && me.w >= w_min && W.lead(me.x) <= y_max;
+    const unsigned long long w = in ? me.w : 0ull;
+    const unsigned long long total = sum4(w);
+    const uint32_t cnt = (uint32_t)sum4(in ? 1ull : 0ull);
+    if (tid < n) S.all[tid].w = w;
+    if (tid == 0) S.found = -1;
+    sync();
+    // the draw, in id order
+    const bool lost = u >= 1.f;
+    bool rest;
+    const unsigned long long t = lost ? ~0ull : mul_floor(fmaxf(u, 0.f), total, rest) + 1;
+    unsigned long long run = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const Entry o = S.all[i];
+        run += o.id < me.id ? o.w : 0ull;
+    }
+    if (lost) {
+        if (w > 0) atomicMax(&S.found, me.id);
+        sync();
+    }
+    if (w > 0 && (lost ? me.id == S.found : run < t && run + w >= t)) {
+        p.token[b] = me.id;
+        if (p.logprob) p.logprob[b] = log_share(w, total);
+        if (p.n_kept) p.n_kept[b] = (int32_t)cnt;
     }
 }
 
@@ -804,6 +886,16 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     const unsigned long long light_cta = warp_sum(lane < kSfWarps ? S.red[lane] : 0ull);
     const bool plain = !cuts && !(top_p < 1.f) && !(min_p > 0.f);  // every id above -inf stays
 
+    // min-p by the weight, or (where it is too small for the weight's unit) by y
+    const bool by_w = min_p >= 0x1p-40f;
+    unsigned long long w_min = 0;
+    if (by_w) {
+        bool rest = false;
+        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;
+        w_min += rest ? 1 : 0;
+    }
+    const float y_max = min_p > 0.f && !by_w ? -log2f(min_p) : INFINITY;
+
     // ---- 3. the filters ----
     // light: what of the light ids is kept: all, none, or (all ids are to be looked at) some
     enum { kNone, kLightAll, kSome };
@@ -816,8 +908,14 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         }
         light = kNone;
         if (r == kBeyond) {
-            select<false>(S, R, W, true, kept, (unsigned long long)top_k, 0.f, 0ull);
+            r = select<false>(S, R, W, true, kept, (unsigned long long)top_k, 0.f, 0ull);
             light = kSome;
+        }
+        if (r == kFew) {
+            if (R.cluster > 1) cluster_arrive();  // this CTA has read the others' lists
+            if (R.rank == 0) draw_few(S, W, p, b, top_k, top_p, w_min, y_max, u);
+            if (R.cluster > 1) cluster_wait();  // the others have read this one's
+            return;
         }
     }
     if (top_p < 1.f) {
@@ -830,15 +928,6 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         if (r == kBeyond && select<true>(S, R, W, true, kept, 0ull, top_p, 0ull) == kCutHere)
             light = kSome;
     }
-    // min-p by the weight, or (where it is too small for the weight's unit) by y
-    const bool by_w = min_p >= 0x1p-40f;
-    unsigned long long w_min = 0;
-    if (by_w) {
-        bool rest = false;
-        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;
-        w_min += rest ? 1 : 0;
-    }
-    const float y_max = min_p > 0.f && !by_w ? -log2f(min_p) : INFINITY;
     if (light == kLightAll && min_p > 0.f) light = w_min > (1ull << 29) ? kNone : kSome;
 
     // ---- 4. the kept ids' mass, per warp segment ----
@@ -934,12 +1023,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     }
     if (token >= 0) {
         p.token[b] = R.lo + token;
-        if (p.logprob) {
-            // near 1 from what is left over, which the integers know exactly
-            const unsigned long long w = W.of(R.at(token));
-            const float tf = (float)total;
-            p.logprob[b] = w > total / 2 ? log1pf(-((float)(total - w) / tf)) : logf((float)w / tf);
-        }
+        if (p.logprob) p.logprob[b] = log_share(W.of(R.at(token)), total);
         if (p.n_kept) p.n_kept[b] = (int32_t)(top_k > 0 ? min((uint32_t)top_k, cnt) : cnt);
     }
 }
