@@ -331,15 +331,15 @@ enum SelectResult { kCutHere, kBeyond, kAll, kFew };
 
 // The last id of the shortest prefix (within `kept`) that holds `k` ids (MASS false) or whose
 // mass reaches frac * (mass of `kept`) (MASS true; frac < 1; `light`: this CTA's light mass, 0
-// when none of it is kept). Over the listed ids, or with `full` over all. Returns kBeyond,
-// leaving `kept`, when the cut is not among the listed ids; kAll when the prefix ends among
-// ids of weight 0; kFew (counts only) with the whole prefix, and the rest of its last bin, in
+// when none of it is kept; only ids of weight w_min or more can be cut at, the others just add
+// to the mass). Over the listed ids, or with `full` over all. Returns kBeyond, leaving `kept`,
+// when the cut is not among the listed ids (of that weight); kAll when it is among none; kFew (counts only) with the whole prefix, and the rest of its last bin, in
 // S.all of every CTA (S.n_all entries, in no order). Every thread of the cluster calls it; the histogram is clear before and
 // after.
 template <bool MASS>
 __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, bool full,
                                Cut& kept, unsigned long long k, float frac,
-                               unsigned long long light) {
+                               unsigned long long light, unsigned long long w_min) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto clear_hist = [&]() {
         for (int i = tid; i < kBins; i += kSfThreads) S.hist[i] = make_uint2(0u, 0u);
@@ -362,21 +362,17 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
         in = key >= klo && key <= khi;
         return (int)((khi - key) >> shift);
     };
-    if (MASS) {
-        if (R.cluster > 1) {
-            if (tid < R.cluster) st_cluster_u64(&S.ex_light[R.rank], tid, light);
-        } else if (tid == 0) {
-            S.ex_light[0] = light;
-        }
-    }
     for (;;) {
         // ---- histogram of the members over the bins ----
+        unsigned long long mass = 0;
         for_ids(R, full, [&](float x, int i) {
             bool in;
             const int bin = bin_of(x, in);
             if (in && kept.keeps(x, R.lo + i)) {
                 if (MASS) {
                     const unsigned long long w = full ? W.of(x) : W.heavy(x);
+                    mass += w;
+                    if (w < w_min) return;
                     const uint32_t lo = (uint32_t)w;
                     const uint32_t old = atomicAdd(&S.hist[bin].x, lo);
                     const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
@@ -386,7 +382,19 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
                 }
             }
         });
+        if (MASS && first) {
+            mass = warp_sum(mass);
+            if (lane == 0) S.red[warp] = mass;
+        }
         __syncthreads();
+        if (MASS && first) {  // this CTA's share of the mass that frac is of
+            mass = light + warp_sum(lane < kSfWarps ? S.red[lane] : 0ull);
+            if (R.cluster > 1) {
+                if (tid < R.cluster) st_cluster_u64(&S.ex_light[R.rank], tid, mass);
+            } else if (tid == 0) {
+                S.ex_light[0] = mass;
+            }
+        }
 #pragma unroll
         for (int h = 0; h < kGroups / kSfWarps; ++h) {
             const int g = warp * (kGroups / kSfWarps) + h;
@@ -415,7 +423,7 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
             if (MASS) {
                 bool rest = false;
                 const unsigned long long all =
-                    total + warp_sum(lane < R.cluster ? S.ex_light[lane] : 0ull);
+                    warp_sum(lane < R.cluster ? S.ex_light[lane] : 0ull);
                 target = frac > 0.f ? mul_floor(frac, all, rest) : 0ull;
                 target += rest ? 1 : 0;  // a mass reaches frac * all when it is >= this
                 if (target == 0) target = 1;
@@ -445,11 +453,13 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
             bool in;
             const int mine = bin_of(x, in);
             if (in && (mine == bin || (few && mine < bin)) && kept.keeps(x, R.lo + i)) {
+                const unsigned long long w = MASS || few ? W.of(x) : 1ull;
+                if (MASS && w < w_min) return;
                 const uint32_t at = atomicAdd(&S.n_list, 1u);
                 if (at < kList) {
                     S.list[at].x = x;
                     S.list[at].id = R.lo + i;
-                    S.list[at].w = MASS || few ? W.of(x) : 1ull;
+                    S.list[at].w = w;
                 }
             }
         });
@@ -814,9 +824,25 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         W.cl = q < 3e38f ? __fdiv_rn(fmaf(-q, T, h) + l, T) : 0.f;
     }
 
+    // min-p: by the weight, or (where it is too small for the weight's unit) by y alone. Past
+    // y_max no id is kept (with room for y's rounding where the weight decides)
+    const bool by_w = min_p >= 0x1p-40f;
+    unsigned long long w_min = 0;
+    if (by_w) {
+        bool rest = false;
+        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;
+        w_min += rest ? 1 : 0;
+    }
+    const float y_max =
+        min_p > 0.f ? fmaf(-log2f(fminf(min_p, 1.f)), by_w ? 1.00001f : 1.f, by_w ? 1e-4f : 0.f)
+                    : INFINITY;
+
     // ---- 2. the heavy ids of this warp's segment; the light ones' mass ----
     // (a top-k that cuts leaves no light id, or all ids are looked at)
     const bool cuts = top_k > 0 && (uint32_t)top_k < fin;
+    // without masses to add up, the ids that min-p drops need not be listed either
+    const bool masses = top_p < 1.f;
+    const float y_list = cuts || masses ? kHeavy : fminf(kHeavy, y_max);
     unsigned long long light_w = 0;
     R.wl = 0;
     const bool finite = W.m < INFINITY;
@@ -853,8 +879,8 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
             uint32_t mine = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e)  // (a NaN is neither: its lead is NaN, its weight 0)
-                mine |= (W.m - x[e]) * W.ch < kHeavy ? 1u << e : 0u;
-            if (!cuts) {
+                mine |= (W.m - x[e]) * W.ch < y_list ? 1u << e : 0u;
+            if (!cuts && y_list == kHeavy) {
                 // two sums of four, below 2^32
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -884,17 +910,8 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     if (lane == 0) S.red[warp] = light_w;
     __syncthreads();
     const unsigned long long light_cta = warp_sum(lane < kSfWarps ? S.red[lane] : 0ull);
+    __syncthreads();  // S.red is free
     const bool plain = !cuts && !(top_p < 1.f) && !(min_p > 0.f);  // every id above -inf stays
-
-    // min-p by the weight, or (where it is too small for the weight's unit) by y
-    const bool by_w = min_p >= 0x1p-40f;
-    unsigned long long w_min = 0;
-    if (by_w) {
-        bool rest = false;
-        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;
-        w_min += rest ? 1 : 0;
-    }
-    const float y_max = min_p > 0.f && !by_w ? -log2f(min_p) : INFINITY;
 
     // ---- 3. the filters ----
     // light: what of the light ids is kept: all, none, or (all ids are to be looked at) some
@@ -904,11 +921,11 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     if (cuts) {
         SelectResult r = kBeyond;
         if (light != kSome) {
-            r = select<false>(S, R, W, false, kept, (unsigned long long)top_k, 0.f, 0ull);
+            r = select<false>(S, R, W, false, kept, (unsigned long long)top_k, 0.f, 0ull, 0ull);
         }
         light = kNone;
         if (r == kBeyond) {
-            r = select<false>(S, R, W, true, kept, (unsigned long long)top_k, 0.f, 0ull);
+            r = select<false>(S, R, W, true, kept, (unsigned long long)top_k, 0.f, 0ull, 0ull);
             light = kSome;
         }
         if (r == kFew) {
@@ -918,26 +935,30 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
             return;
         }
     }
-    if (top_p < 1.f) {
+    if (masses) {
         SelectResult r = kBeyond;
         if (light != kSome) {
             r = select<true>(S, R, W, false, kept, 0ull, top_p,
-                             light == kLightAll ? light_cta : 0ull);
+                             light == kLightAll ? light_cta : 0ull, w_min);
             if (r == kCutHere) light = kNone;
+            // (where min-p keeps no light id, its prefix ends before top-p's)
+            if (y_max < kHeavy - 1.f) r = kCutHere;
         }
-        if (r == kBeyond && select<true>(S, R, W, true, kept, 0ull, top_p, 0ull) == kCutHere)
+        if (r == kBeyond &&
+            select<true>(S, R, W, true, kept, 0ull, top_p, 0ull, w_min) == kCutHere)
             light = kSome;
     }
-    if (light == kLightAll && min_p > 0.f) light = w_min > (1ull << 29) ? kNone : kSome;
+    if (light == kLightAll && min_p > 0.f) light = y_max < kHeavy - 1.f ? kNone : kSome;
 
     // ---- 4. the kept ids' mass, per warp segment ----
     unsigned long long sum = 0;
     uint32_t count = 0;
     auto weigh = [&](float x, int i, bool listed) -> unsigned long long {
+        if (!kept.keeps(x, R.lo + i) || !(W.lead(x) <= y_max)) return 0ull;
         const unsigned long long w = listed ? W.heavy(x) : W.of(x);
-        const bool in = kept.keeps(x, R.lo + i) && W.lead(x) <= y_max && w >= w_min;
-        count += in;
-        return in ? w : 0ull;
+        if (w < w_min) return 0ull;
+        ++count;
+        return w;
     };
     if (light == kSome) for_ids(R, true, [&](float x, int i) { sum += weigh(x, i, false); });
     else for_ids(R, false, [&](float x, int i) { sum += weigh(x, i, true); });
