@@ -401,7 +401,7 @@ kvd_status kvd_qk_norm_rope(kvd_dtype dtype, int32_t batch, int32_t n, const kvd
  * 64-position tiles some query of the block sees are read, and what lies elsewhere in the
  * cache, infinities and NaN included, does not reach a query that does not see it.
  *
- * 1 <= qlen <= KVD_MAX_QLEN; window >= 1; n_sinks >= 0.
+ * 1 <= qlen <= KVD_MAX_QLEN; window >= 1; n_sinks >= 0; out must not be q.
  */
 kvd_status kvd_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads, int32_t qlen,
                            const void *q, const kvd_cache *kv, const int32_t *lens,
@@ -503,12 +503,13 @@ kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache *cache, int32_t ba
  *   out[b,hq,i,:] = sum_t softmax_t(scale * q[b,hq,i] . K[b,h,t]) V[b,h,t] over those t,
  *   h = hq / (n_q_heads / cache->n_kv_heads); a query that sees nothing gets zeros
  *
- * q, out : device [batch, n_q_heads, qlen, 64], contiguous, 16-byte aligned; 1 <= qlen <=
- *          KVD_MAX_QLEN; batch <= cache->batch
+ * q, out : device [batch, n_q_heads, qlen, 64], contiguous, 16-byte aligned, out not q; 1 <=
+ *          qlen <= KVD_MAX_QLEN; batch <= cache->batch
  * window, n_sinks >= 0; n_sinks is ignored without a window
  * workspace : kvd_workspace_size(KVD_OP_Q4_ATTN, batch, n_q_heads, n_kv_heads, 1, qlen,
- *          max_len) bytes with max_len = the capacity (or fixed_len); used only by few long
- *          rows, under the rules of the other attention calls
+ *          max_len) bytes with max_len = the capacity (or fixed_len); used where that size is
+ *          more than the counters' (many rows or long ones), under the rules of the other
+ *          attention calls
  * Products run on the tensor cores with fp32 accumulation; the softmax is fp32.
  * Flags: KVD_FLAG_PDL; KVD_FLAG_EARLY_KV gives what KVD_FLAG_PDL gives (nothing is read
  * before the wait).

@@ -1748,7 +1748,7 @@ extern "C" kvd_status kvd_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_
                                       int32_t n_sinks, float scale, void* out, void* workspace,
                                       size_t workspace_bytes, uint32_t flags, int32_t* dev_err,
                                       kvd_stream_t stream) {
-    if (window < 1 || n_sinks < 0) return KVD_ERR_INVALID_ARG;
+    if (window < 1 || n_sinks < 0 || (q && q == out)) return KVD_ERR_INVALID_ARG;
     // (qlen outside 1..KVD_MAX_QLEN is refused with the other arguments)
     return kvd::attention(qlen > 1, dtype, batch, n_q_heads, qlen, q, kv, lens, fixed_len,
                           append, 1, 1, scale, out, workspace, workspace_bytes, flags, dev_err,

@@ -835,7 +835,7 @@ extern "C" kvd_status kvd_q4_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_he
     if (window < 0 || n_sinks < 0 || (window > 0 && !causal)) return KVD_ERR_INVALID_ARG;
     if (!(scale < INFINITY) || !(scale > -INFINITY)) return KVD_ERR_INVALID_ARG;
     if (batch == 0) return KVD_OK;
-    if (!q || !out || !aligned16(q) || !aligned16(out)) return KVD_ERR_INVALID_ARG;
+    if (!q || !out || q == out || !aligned16(q) || !aligned16(out)) return KVD_ERR_INVALID_ARG;
     if (!lens && (fixed_len < 0 || fixed_len > cache->capacity)) return KVD_ERR_INVALID_ARG;
     const Q4Shape sh = q4_shape(batch, n_q_heads, cache->n_kv_heads, qlen);
     if (batch > 65535 || (int64_t)cache->n_kv_heads * sh.nsub > 65535 || sh.units > 0x7fffffff)
