@@ -35,7 +35,7 @@
 //    thread-block cluster and merge through distributed shared memory, every CTA a share of
 //    the outputs. Much work (STREAM): the tiles of all units form one list, every CTA of one
 //    wave takes an equal stretch of it, and units cut by a stretch's end merge through the
-//    workspace (last arrival): ragged lengths then cost nothing.
+//    workspace (last arrival): the longest row does not set the time.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -53,6 +53,14 @@ constexpr int kStagesQ = 4;                  // cp.async stages per warp
 constexpr int kStageBytes = kT * (32 + 32 + 8);
 constexpr int kMaxClusterQ = 16;
 constexpr int kMaxStream = 512;              // CTAs of a STREAM launch
+// STREAM: a unit counts as its tiles and kUnitCost more, for the time that a CTA needs for any
+// unit at all (loads that nothing hides, the merge). 37 rows x 16 heads, lengths in equal steps up
+// to 32768: 179 us without it, 160, 142, 134 us with 8, 16, 24; up to 8192: 102, 70, 57, 50 us.
+constexpr uint32_t kUnitCost = 24;
+// No cut this close to a unit's ends (20.8 -> 15.3 us: 37 x 16, up to 2048, before kUnitCost).
+constexpr uint32_t kSnap = 8;
+// Lists this short per CTA (in weight) are cut evenly among units; see shares().
+constexpr uint32_t kAlignFew = 64, kAlignMost = 128;
 constexpr float kGrowLog2 = 8.f;
 constexpr int kPart = kHeadDim + 4;          // floats per partial: o[64], max, sum, 2 pad
 
@@ -152,23 +160,28 @@ __device__ __forceinline__ int row_len(const Q4AttnParams& p, int b) {
     return p.lens ? p.lens[b] : p.fixed_len;
 }
 
-// STREAM: the tiles of rows 0 .. batch-1, each row's times its units (KV heads x blocks).
-// The row that holds tile `at` of the list, and the list's tiles before that row; with at past
+// STREAM: what a unit counts in the list.
+__device__ __forceinline__ uint32_t weight(const TileMap& m) {
+    return m.total ? m.total + kUnitCost : 0;
+}
+
+// STREAM: the list has the units of rows 0 .. batch-1 (a row's: KV heads x blocks), by weight.
+// The row that holds place `at` of the list, and the list's length before that row; with at past
 // the end, `before` is the length of the list. One warp, the same in all of them.
-__device__ __forceinline__ int find_row(const Q4AttnParams& p, int64_t at, int64_t& before) {
+__device__ __forceinline__ int find_row(const Q4AttnParams& p, uint32_t at, uint32_t& before) {
     const int lane = threadIdx.x & 31;
-    const int64_t units = (int64_t)p.n_kv_heads * p.nsub;
+    const uint32_t units = (uint32_t)(p.n_kv_heads * p.nsub);
     before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        int64_t n = 0;
+        uint32_t n = 0;
         if (b0 + lane < p.batch) {
             const int len = row_len(p, b0 + lane);
-            if (len >= 0 && len <= p.capacity) n = tile_map(p, len).total * units;
+            if (len >= 0 && len <= p.capacity) n = weight(tile_map(p, len)) * units;
         }
-        int64_t inc = n;
+        uint32_t inc = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, inc, off);
+            const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += o;
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, before + inc > at);
@@ -180,6 +193,62 @@ __device__ __forceinline__ int find_row(const Q4AttnParams& p, int64_t at, int64
         before += __shfl_sync(0xffffffffu, inc, 31);
     }
     return p.batch;
+}
+
+// STREAM: stretches of the list, CTA i's from floor(total i / ctas) on.
+struct Shares {
+    uint32_t total, ctas, per, rest;  // total = per ctas + rest
+    __device__ __forceinline__ uint32_t start(uint32_t i) const {
+        return i * per + i * rest / ctas;  // (rest < ctas <= 512)
+    }
+    __device__ __forceinline__ uint32_t holder(uint32_t at) const {  // whose share has place `at`
+        uint32_t i = (uint32_t)((float)at * ((float)ctas / (float)total));
+        i = min(i, ctas - 1);
+        while (start(i) > at) --i;
+        while (start(i + 1) <= at) ++i;
+        return i;
+    }
+};
+// How many CTAs share a list of weight `total`: a tile per warp at least, but not fewer CTAs than
+// units. Short lists: a number of CTAs per unit, or of units per CTA, so that equal lengths are
+// cut at the ends of units and a CTA meets no more of them than it must (37 rows x 16 heads of
+// 1024: 22.8 -> 16.1 us; 16 x 8 of 2048: 15.9 -> 11.9 us). With long ones the idle CTAs cost more
+// (16 x 8 of 16384: 38.5 -> 40.6 us).
+__device__ __forceinline__ Shares shares(const Q4AttnParams& p, uint32_t total) {
+    const uint32_t units = (uint32_t)(p.batch * p.n_kv_heads * p.nsub);
+    uint32_t n = min((uint32_t)gridDim.x, max((total + kWarpsQ - 1) / kWarpsQ, units));
+    uint32_t even = n / units * units;
+    if (even == 0) {
+        const uint32_t least = (units + n - 1) / n;
+        for (uint32_t k = least; k < 2 * least && even == 0; ++k)
+            if (units % k == 0) even = units / k;
+    }
+    if (even > 0 && total < gridDim.x * (4 * even >= 3 * n ? kAlignMost : kAlignFew)) n = even;
+    n = max(1u, min(n, total));
+    Shares s;
+    s.total = total;
+    s.ctas = n;
+    s.per = total / n;
+    s.rest = total - s.per * n;
+    return s;
+}
+
+// Where the stretch really starts whose share starts at `at`: inside a unit of weight w from
+// keep_lo to keep_hi - 1, else at the nearer end of the unit, as a cut costs more than some tiles.
+// (Units too small for that are not cut.)
+__device__ __forceinline__ bool cuttable(uint32_t w) { return w >= kUnitCost + 2 * kSnap; }
+__device__ __forceinline__ uint32_t keep_lo(uint32_t w) {
+    return cuttable(w) ? kUnitCost + kSnap : (w + 1) / 2;
+}
+__device__ __forceinline__ uint32_t keep_hi(uint32_t w) {
+    return cuttable(w) ? w - kSnap : keep_lo(w);
+}
+__device__ __forceinline__ uint32_t cut(const Q4AttnParams& p, uint32_t total, uint32_t at) {
+    if (at >= total) return total;
+    uint32_t before;
+    const int b = find_row(p, at, before);
+    const uint32_t w = weight(tile_map(p, row_len(p, b))), in = (at - before) % w;
+    return in < keep_lo(w) ? at - in : in >= keep_hi(w) ? at - in + w : at;
 }
 
 // NT: blocks of 8 query vectors.
@@ -197,15 +266,15 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
     pdl_trigger();
 
     // ---- the stretch of the tile list, or the split of the unit ----
-    int64_t cur = 0, end = 0, total = 0;
-    int64_t ctas = 0;
+    uint32_t cur = 0, end = 0;
+    Shares sh = {};
     if (STREAM) {
-        find_row(p, INT64_MAX, total);
-        // at least a tile per warp
-        ctas = max((int64_t)1, min((int64_t)gridDim.x, (total + kWarpsQ - 1) / kWarpsQ));
-        const int64_t i = blockIdx.x;
-        cur = i < ctas ? total * i / ctas : total;
-        end = i < ctas ? total * (i + 1) / ctas : total;
+        uint32_t total;
+        find_row(p, 0xffffffffu, total);
+        sh = shares(p, total);
+        const uint32_t i = blockIdx.x;
+        cur = cut(p, total, i < sh.ctas ? sh.start(i) : total);
+        end = cut(p, total, i < sh.ctas ? sh.start(i + 1) : total);
         // rows without a tile: flagged, or (length 0) zeros
         for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
             const int len = row_len(p, b);
@@ -218,22 +287,22 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
             }
         }
     }
-    bool first_seg = true;
     do {
         int b, uh, v0, v1, len;  // uh: unit within the row
-        int64_t u0 = 0;          // STREAM: the unit's first tile of the list
+        uint32_t u0 = 0;         // STREAM: where the unit starts in the list
         TileMap tm;
         if (STREAM) {
             if (cur >= end) break;
-            int64_t before;
+            uint32_t before;
             b = find_row(p, cur, before);
             len = row_len(p, b);
             tm = tile_map(p, len);
-            uh = (int)((cur - before) / tm.total);
-            u0 = before + (int64_t)uh * tm.total;
-            v0 = (int)(cur - u0);
-            v1 = (int)min((int64_t)tm.total, v0 + (end - cur));
-            cur += v1 - v0;
+            const uint32_t w = weight(tm);
+            uh = (int)((cur - before) / w);
+            u0 = before + uh * w;
+            v0 = max((int)(cur - u0) - (int)kUnitCost, 0);
+            cur = min(u0 + w, end);
+            v1 = (int)(cur - u0 - kUnitCost);
         } else {
             b = blockIdx.z;
             uh = blockIdx.y;
@@ -613,7 +682,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
         };
         const bool whole = STREAM ? v0 == 0 && v1 == tm.total : p.splits == 1;
         float* mine = part;  // where this CTA's partial goes, when the unit is not whole
-        if (STREAM) mine = p.ws_part + (2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1)) * p.msub * kPart;
+        if (STREAM) mine = p.ws_part + (2 * (int64_t)blockIdx.x + (v0 == 0)) * p.msub * kPart;
         for (int it = tid; it < items; it += kThreadsQ) {
             const float4* r0 = reinterpret_cast<const float4*>(red + (it >> 4) * kPart);
             float mx, sum;
@@ -649,8 +718,10 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
         if (!whole) {
             // the CTAs whose stretches meet the unit; the last to arrive merges their partials
             // in the order of the list
-            const int64_t i0 = ((u0 + 1) * ctas - 1) / total;
-            const int64_t i1 = ((u0 + tm.total) * ctas - 1) / total;
+            // (the last whose share starts before the unit's first, and before its last cut)
+            const uint32_t w = weight(tm);
+            const uint32_t i0 = sh.holder(u0 + keep_lo(w) - 1);
+            const uint32_t i1 = sh.holder(u0 + keep_hi(w) - 1);
             const int n = (int)(i1 - i0) + 1;
             const int unit = b * p.n_kv_heads * p.nsub + uh;
             __threadfence();
@@ -659,14 +730,12 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                // the first CTA's partial is of its last unit, unless its stretch starts here
-                const int64_t slot0 = 2 * i0 + (total * i0 / ctas < u0 ? 1 : 0);
                 for (int it = tid; it < items; it += kThreadsQ) {
                     float mx, sum;
                     const float4 o = combine(
                         n,
                         [&](int i, int q4) {
-                            const int64_t slot = i == 0 ? slot0 : 2 * (i0 + i);
+                            const int64_t slot = 2 * (int64_t)(i0 + i) + (i == 0);
                             return __ldcg(reinterpret_cast<const float4*>(
                                               p.ws_part + (slot * p.msub + (it >> 4)) * kPart) +
                                           q4);
@@ -677,7 +746,6 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                 if (tid == 0) p.ws_cnt[unit] = 0;
             }
         }
-        first_seg = false;
         __syncthreads();  // the ring is free for the next unit
     } while (STREAM);
 }
@@ -770,33 +838,31 @@ int64_t q4_tiles(int64_t bound, int qlen, int window, int n_sinks) {
     return std::min(all, near + ((int64_t)n_sinks + kT - 1) / kT);
 }
 
-// From this many tiles in all (8 per warp of one wave) the launch streams the list of tiles:
-// measured 82 -> 51 us for 16 ragged rows x 8 heads up to 32768 positions (131072 tiles at
-// most), but 12.9 -> 17.3 us for 4 rows x 20 heads, 4000 positions each (10160).
-constexpr int64_t kStreamTiles = 152 * 2 * 64;
-// (its units have a counter each; a CTA looks through the rows' lengths)
-bool q4_streams(const Q4Shape& sh, int64_t batch, int64_t tiles) {
-    return sh.units * tiles >= kStreamTiles &&
-           sh.units * (int64_t)sizeof(int32_t) <= KVD_WS_COUNTER_BYTES && batch <= 4096;
+// A launch streams the list of tiles when a split could have this many of them. The host knows
+// the bound of the lengths only, and streaming pays where they differ or the units fill a wave
+// badly (splits | stream, us, lengths equal / in equal steps):
+//   16 rows x 8 heads, to 32768 (512 tiles a split):  64.7 / 50.9 | 63.1 / 41.3
+//   24 x 8 (1 split each), to 8192 (256):             34.2 / 29.9 | 33.0 / 23.0
+//   24 x 8, to 2048 (64):                             11.9 / 11.1 | 13.9 / 16.8
+//   40 x 8, to 32768 (1024):                         179.6 /  102 |  137 / 78.9
+// one row of 32768 among 40 of 2048: 78.7 | 34.4; all of 600 in a cache of 32768: 10.2 | 15.0.
+constexpr int64_t kStreamTiles = 256;
+constexpr int64_t kStreamLeast = 152 * 2 * 64;  // and in all: 8 per warp of a wave
+// With more units than this (two waves) the block scheduler spreads whole units better: 128 rows x
+// 8 heads, to 8192: 112 / 68.8 | 125 / 76.0; 64 x 8: 66.1 / 42.0 | 68.4 / 43.5, one long row 26.7
+// | 20.4.
+constexpr int64_t kStreamUnits = 640;
+static_assert(kStreamUnits * sizeof(int32_t) <= KVD_WS_COUNTER_BYTES, "a counter per unit");
+bool q4_streams(const Q4Shape& sh, int64_t tiles) {
+    return tiles >= kStreamTiles && sh.units * tiles >= kStreamLeast &&
+           sh.units <= kStreamUnits &&
+           sh.units * (tiles + kUnitCost) < (INT64_C(1) << 31);
 }
 
 template <typename T, int NT>
 kvd_status run_q4(Q4AttnParams& p, const Q4Shape& sh, int64_t tiles, int nsm, void* ws,
                   size_t ws_bytes, bool pdl, cudaStream_t st) {
     constexpr size_t smem = q4_smem(8 * NT);
-    if (q4_streams(sh, p.batch, tiles)) {
-        constexpr auto kern = q4_attn_kernel<T, NT, true>;
-        if (prepare_q4<kern>(smem) <= 0) return KVD_ERR_CUDA;
-        const int slots = std::min(kMaxStream, resident_q4<kern>(smem, 1, nsm));
-        if (slots <= 0) return KVD_ERR_CUDA;
-        const size_t need =
-            KVD_WS_COUNTER_BYTES + (size_t)2 * slots * sh.msub * kPart * sizeof(float);
-        if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < need)
-            return KVD_ERR_WORKSPACE;
-        p.ws_cnt = static_cast<int32_t*>(ws);
-        p.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + KVD_WS_COUNTER_BYTES);
-        return launch(kern, dim3((unsigned)slots), dim3(kThreadsQ), smem, st, pdl, p);
-    }
     constexpr auto kern = q4_attn_kernel<T, NT, false>;
     const int mc = prepare_q4<kern>(smem);
     if (mc <= 0) return KVD_ERR_CUDA;
@@ -804,7 +870,20 @@ kvd_status run_q4(Q4AttnParams& p, const Q4Shape& sh, int64_t tiles, int nsm, vo
     int64_t want = std::min<int64_t>(std::max<int64_t>(1, (tiles + kWarpsQ - 1) / kWarpsQ), mc);
     for (; want > 1; --want)
         if (resident_q4<kern>(smem, (int)want, nsm) >= sh.units) break;
-    p.splits = (int)std::max<int64_t>(1, want);
+    if (tiles >= want * kStreamTiles && q4_streams(sh, tiles)) {
+        constexpr auto stream = q4_attn_kernel<T, NT, true>;
+        if (prepare_q4<stream>(smem) <= 0) return KVD_ERR_CUDA;
+        const int slots = std::min(kMaxStream, resident_q4<stream>(smem, 1, nsm));
+        if (slots <= 0) return KVD_ERR_CUDA;
+        const size_t need =
+            KVD_WS_COUNTER_BYTES + (size_t)2 * slots * sh.msub * kPart * sizeof(float);
+        if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < need)
+            return KVD_ERR_WORKSPACE;
+        p.ws_cnt = static_cast<int32_t*>(ws);
+        p.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + KVD_WS_COUNTER_BYTES);
+        return launch(stream, dim3((unsigned)slots), dim3(kThreadsQ), smem, st, pdl, p);
+    }
+    p.splits = (int)want;
     const dim3 grid((unsigned)p.splits, (unsigned)(p.n_kv_heads * sh.nsub), (unsigned)p.batch);
     return launch_ex(kern, grid, dim3(kThreadsQ), smem, st, pdl, (unsigned)p.splits, p);
 }
@@ -813,7 +892,7 @@ kvd_status run_q4(Q4AttnParams& p, const Q4Shape& sh, int64_t tiles, int nsm, vo
 
 size_t q4_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int qlen, int max_len) {
     const Q4Shape sh = q4_shape(batch, n_q_heads, n_kv_heads, qlen);
-    if (!q4_streams(sh, batch, q4_tiles(max_len, qlen, 0, 0))) return KVD_WS_COUNTER_BYTES;
+    if (!q4_streams(sh, q4_tiles(max_len, qlen, 0, 0))) return KVD_WS_COUNTER_BYTES;
     return KVD_WS_COUNTER_BYTES + (size_t)2 * kMaxStream * sh.msub * kPart * sizeof(float);
 }
 

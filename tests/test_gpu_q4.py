@@ -255,31 +255,36 @@ def test_one_long_row():
 
 @pytest.mark.parametrize("Hq,n,dtype,window", [(8, 1, torch.float16, 0), (8, 1, torch.bfloat16, 0),
                                                (24, 2, torch.float16, 0), (8, 5, torch.float16, 0),
-                                               (8, 2, torch.float16, 6450)])
+                                               (8, 2, torch.float16, 8160)])
 def test_many_tiles_stream_through_the_workspace(Hq, n, dtype, window):
     """Work enough for the launches whose CTAs take stretches of one list of tiles: ragged rows,
-    rows that are empty or hold a tile, units cut by many CTAs."""
+    rows that are empty or hold a tile, units cut by many CTAs, lists cut at the ends of units."""
     import kv_cached_decode_gb300 as kvd
 
     g = torch.Generator(device="cuda").manual_seed(Hq + n)
-    B, H, cap = 12, 8, 6501
+    B, H, cap = 20, 8, 8201
     c = kvd.new_q4_cache(B, H, cap)
     kvd.kvd_q4_append(c, *(torch.randn(B, H, cap, 64, generator=g, device="cuda").half()
                            for _ in "kv"))
     q = torch.randn(B, Hq, n, 64, generator=g, device="cuda").to(dtype)
     kw = dict(window=window, n_sinks=40) if window else {}
     full = _attend(c, q, [cap] * B, **kw)
-    _attend(c, q, [cap, 0, 1, 17, 3000, 0, 33, 2, 500, 64, 0, 900], **kw)
+    few = [0, 1, 17, 3000, 0, 33, 2, 500, 64, 0, 900]
+    _attend(c, q, [cap] + few + [31, 32, 0, 1500, 700, 8200, 8000, 300], **kw)
+    _attend(c, q, few + [1] * 8 + [cap], **kw)
+    for L in (40, 250, 700):
+        _attend(c, q, [L] * B, **kw)
+    _attend(c, q, [cap * (b + 1) // B for b in range(B)], **kw)
     _attend(c, q, [0] * B, **kw)
-    _attend(c, q, [0, 0, 0, 5] + [0] * 8, **kw)
+    _attend(c, q, [0, 0, 0, 5] + [0] * 16, **kw)
     # a length out of range leaves its row
     ws = kvd.new_workspace(kvd.kvd_workspace_size(kvd.KVD_OP_Q4_ATTN, B, Hq, H, 1, n, cap))
     out, err = torch.full_like(q, 9.0), new_err()
-    kvd.kvd_q4_attn(q, c, out, ws, lens=_i32(cap, -1, cap, cap, cap + 1, *[cap] * 7), dev_err=err,
+    kvd.kvd_q4_attn(q, c, out, ws, lens=_i32(cap, -1, cap, cap, cap + 1, *[cap] * 15), dev_err=err,
                     **kw)
     torch.cuda.synchronize()
     assert int(err) == 16 and (out[[1, 4]] == 9).all()
-    keep = [0, 2, 3, 5, 6, 7, 8, 9, 10, 11]
+    keep = [0, 2, 3] + list(range(5, B))
     assert torch.allclose(out[keep].float(), full[keep].float(), rtol=2 ** -7, atol=2 ** -10)
     for w in (None, ws[:4096 * 16]):
         with pytest.raises(kvd.KvdError) as e:
