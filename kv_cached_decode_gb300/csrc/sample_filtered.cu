@@ -61,8 +61,10 @@ constexpr int kList = 128;
 constexpr int kKeep = 8192;                          // logits of a slice kept in shared memory
 constexpr int kMaxSlice = KVD_MAX_VOCAB / kSfMaxCluster;
 constexpr float kYMax = 45.5f;                       // 2^-y below this is 0
-constexpr float kHeavy = 16.f;                       // y of the listed ids is below this
+constexpr float kHeavy = 16.f;                       // y of the heavy ids is below this,
+constexpr float kHeavyFew = 8.f;                     // where min-p drops the light ones this
 constexpr unsigned long long kOne = 1ull << 44;      // w = 1
+constexpr uint32_t kMeanError = 149;                 // of ex2.approx, in 2^-32: 3.47e-8
 
 // 2^(-j/256) in units of 2^-30, j < 256, from repeated products of 2^(-1/256).
 struct PowTable {
@@ -186,13 +188,14 @@ __device__ __forceinline__ void sync_row(int cluster) {
 // The row's weights, in units of 2^-44.
 struct Weights {
     float m, ch, cl;  // largest logit; log2(e) / T in two floats
+    float split;      // heavy ids: y below this
     const uint32_t* pow;
 
     // y's leading part, monotone in x; 0 at the largest (which may be infinite)
     __device__ __forceinline__ float lead(float x) const {
         return (x == m ? 0.f : m - x) * ch;
     }
-    // y < kHeavy
+    // y < split
     __device__ __forceinline__ unsigned long long heavy(float x) const {
         const float d = x == m ? 0.f : m - x;
         const float p = d * ch;
@@ -211,16 +214,21 @@ struct Weights {
         return (unsigned long long)(uint32_t)(t + __mulhi(t, __float2int_rn(q))) *
                    (65536u >> n) >> 2;
     }
-    // y >= kHeavy; 0 for -inf
-    __device__ __forceinline__ uint32_t light(float x) const {
+    // w * 2^13 * unit, with the mean error of the hardware's 2^x; 0 for -inf and NaN (a sum that
+    // overflows is -inf or NaN, too)
+    __device__ __forceinline__ uint32_t raw(float x, float unit) const {
         const float d = m - x;
-        // 2^a, at most 2^28 (far below 2^-1 the sums may overflow, or be NaN for -inf)
-        const float a = d * ch < 64.f ? 44.f - fmaf(d, ch, d * cl) : -10.f;
-        const uint32_t w = __float2uint_rn(ex2_approx(a));
-        return w - __umulhi(w, 149u);  // 149 / 2^32 = 3.47e-8
+        // 13 - y: a small number where the weight is not, so hardly rounded there
+        const float a = fmaf(-d, cl, fmaf(-d, ch, 13.f));
+        return __float2uint_rn(ex2_approx(a) * unit);
+    }
+    // y >= split = kHeavy
+    __device__ __forceinline__ uint32_t light(float x) const {
+        const uint32_t w = raw(x, 0x1p31f);
+        return w - __umulhi(w, kMeanError);
     }
     __device__ __forceinline__ unsigned long long of(float x) const {
-        return lead(x) < kHeavy ? heavy(x) : (unsigned long long)light(x);
+        return lead(x) < split ? heavy(x) : (unsigned long long)light(x);
     }
 };
 
@@ -351,11 +359,11 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
     int shift = 0;
     unsigned long long before = 0;   // count or mass before the interval
     unsigned long long target = k;   // the prefix is complete once its count or mass is this
-    const float scale = full ? kBins / kYMax : kBins / kHeavy;
+    const float scale = kBins / (full ? kYMax : W.split);
     auto bin_of = [&](float x, bool& in) -> int {
         if (first) {
             const float y = W.lead(x);
-            in = y < kYMax;  // (the listed ones are below kHeavy)
+            in = y < kYMax;  // (the listed ones are below W.split)
             return min((int)(y * scale), kBins - 1);
         }
         const uint32_t key = ordered(x);
@@ -842,8 +850,10 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     const bool cuts = top_k > 0 && (uint32_t)top_k < fin;
     // without masses to add up, the ids that min-p drops need not be listed either
     const bool masses = top_p < 1.f;
-    const float y_list = cuts || masses ? kHeavy : fminf(kHeavy, y_max);
-    unsigned long long light_w = 0;
+    // Where min-p drops an id, its weight is only added up: fp32's 2^-22 of it is enough.
+    W.split = cuts ? kHeavy : fminf(kHeavy, fmaxf(kHeavyFew, y_max + 1.5f));
+    const float y_list = cuts ? kHeavy : fminf(W.split, y_max);
+    unsigned long long light_w = 0, light_40 = 0;  // (the second in units of 2^-40)
     R.wl = 0;
     const bool finite = W.m < INFINITY;
     if (finite) {
@@ -880,17 +890,22 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
 #pragma unroll
             for (int e = 0; e < 8; ++e)  // (a NaN is neither: its lead is NaN, its weight 0)
                 mine |= (W.m - x[e]) * W.ch < y_list ? 1u << e : 0u;
-            if (!cuts && y_list == kHeavy) {
-                // two sums of four, below 2^32
+            if (masses && y_list < W.split) {
+                uint32_t some = 0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t l4 = 0;
-#pragma unroll
-                    for (int e = 4 * h; e < 4 * h + 4; ++e)
-                        l4 += mine >> e & 1 ? 0u : W.light(x[e]);
-                    light_w += l4;
+                for (int e = 0; e < 8; ++e) {
+                    const bool heavy = (W.m - x[e]) * W.ch < W.split;
+                    some |= heavy ? 1u << e : 0u;
+                    light_40 += heavy ? 0u : W.raw(x[e], 0x1p27f);
                 }
+                // few: read again rather than a branch for each of the eight
+                for (some &= ~mine; some; some &= some - 1)
+                    light_w += W.heavy(R.x[R.w0 + place(jb, __ffs(some) - 1, q)]);
+            } else if (!cuts && y_list == W.split) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) light_w += mine >> e & 1 ? 0u : W.light(x[e]);
             }
+            if (!__any_sync(0xffffffffu, mine != 0)) continue;
             uint32_t inc = __popc(mine);
             const uint32_t own = inc;
 #pragma unroll
@@ -905,7 +920,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
                 if (mine >> e & 1) lj[at++] = (uint16_t)place(jb, e, q);
         }
     }
-    light_w = warp_sum(light_w);
+    light_w = warp_sum(light_w + ((light_40 - (light_40 * kMeanError >> 32)) << 4));
     __syncthreads();  // S.red is free
     if (lane == 0) S.red[warp] = light_w;
     __syncthreads();
@@ -942,13 +957,13 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
                              light == kLightAll ? light_cta : 0ull, w_min);
             if (r == kCutHere) light = kNone;
             // (where min-p keeps no light id, its prefix ends before top-p's)
-            if (y_max < kHeavy - 1.f) r = kCutHere;
+            if (y_max < W.split - 1.f) r = kCutHere;
         }
         if (r == kBeyond &&
             select<true>(S, R, W, true, kept, 0ull, top_p, 0ull, w_min) == kCutHere)
             light = kSome;
     }
-    if (light == kLightAll && min_p > 0.f) light = y_max < kHeavy - 1.f ? kNone : kSome;
+    if (light == kLightAll && min_p > 0.f) light = y_max < W.split - 1.f ? kNone : kSome;
 
     // ---- 4. the kept ids' mass, per warp segment ----
     unsigned long long sum = 0;
