@@ -605,7 +605,9 @@ kvd_status kvd_sample_accept(const float *target, const float *draft, const int3
  *             (the last kept id with w > 0 if rounding leaves none)
  *   logprob = log(w_token / sum(w))
  * T = 0 takes the largest logit (kept: that id). Masses are integers in units of 2^-44 (the
- * largest w is 1; w is formed to a relative 2^-32): the same bits on every run and batch.
+ * largest w is 1; a w that can be kept is formed to 2^-29 of itself or to 2^-36, one that min-p
+ * drops, of which step 2 needs the sum, to 2^-21 of itself): the same bits on every run and
+ * batch.
  *
  * logits      : device fp32, row r at logits + r * row_stride; vocab <= KVD_MAX_VOCAB;
  *               row_stride >= vocab. A NaN counts as -inf. With +inf logits those ids alone

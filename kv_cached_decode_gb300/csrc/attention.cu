@@ -61,6 +61,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSlot = kHeadDim + 4;   // floats per merge slot: o[64], max, sum, 2 pad
 constexpr int kSlotQuads = kSlot / 4;  // 17 float4 per slot
+constexpr int kMaxQueryBlock = 32;     // query vectors of a block of the largest build
 // Row stride (floats) of the warp partials o[warp][row][.]: with 16 rows per warp the
 // fragment layout writes 8 rows at once, and a stride of 72 (8 banks apart) keeps
 // those float2 stores free of bank conflicts.
@@ -123,13 +124,13 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int rmax, int merg
                                                   int app_rows) {
     SmemLayout L;
     const uint32_t tiles = stages * 2 * kTileBytes;
-    const uint32_t red = kWarps * rmax * (red_stride(rmax) + 2) * 4;
+    const uint32_t red = kWarps * (rmax < 16 ? rmax : 16) * (red_stride(rmax) + 2) * 4;
     L.red_off = 0;
     L.bar_off = ((tiles > red ? tiles : red) + 1023) & ~1023u;
     L.mrg_off = (L.bar_off + (stages + 1) * 8 + 15) & ~15u;
     L.misc_off = L.mrg_off + merge_slots * kSlot * 4;
     L.qoff_off = L.misc_off + 16;  // element offsets of the block's query rows in q / out
-    L.app_off = L.qoff_off + kMmaQueryBlock * 8;  // appended rows: K [qlen][128 B], V, table
+    L.app_off = L.qoff_off + (rmax > kMmaQueryBlock ? rmax : kMmaQueryBlock) * 8;  // appended rows: K [qlen][128 B], V, table
     L.total = L.app_off + app_rows * 2 * kRowBytes + 1024;  // + slack to align the base
     return L;
 }
@@ -302,7 +303,7 @@ __device__ __forceinline__ bool prologue(const AttnParams& p, CtaCtx& c, uint8_t
             issue_tile(tmk, tmv, smem, bars, j, tile_pos<WINDOW>(c, j), c.h, c.bk, tx);
     }
     // the last warp, clear of thread 0's copies
-    const int qi = tid - (kThreads - kMmaQueryBlock);
+    const int qi = tid - (kThreads - kMaxQueryBlock);
     if (qi >= 0 && qi < c.mcount) {
         const int64_t off = qrow(p, c.bk, c.h, c.m0 + qi);
         qoff[qi] = off;
@@ -445,8 +446,10 @@ __device__ void abort_after_timeout(const AttnParams& p, const CtaCtx& c, uint64
 
 // The tile loop shared by both kernels. Tiles are taken two at a time (a round); warp w
 // works on tile 2r + w/4, positions (w%4)*16 .. +15, through slab(sK, sV, tile0, slab0).
+// WIDE: warp w works on positions (w%4)*16 .. +15 of both tiles, for query vectors 16 (w/4) on;
+// the two warps of a slab make the same writes to it, never others.
 // Returns false after a timeout (already handled: the caller just returns).
-template <typename T, bool ROPE, bool WINDOW, typename Slab>
+template <typename T, bool ROPE, bool WINDOW, bool WIDE, typename Slab>
 __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, uint8_t* smem,
                                           uint64_t* bars, float* mrg, uint8_t* app,
                                           const CUtensorMap* tmk, const CUtensorMap* tmv,
@@ -459,13 +462,16 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
     const int rounds = (c.n_tiles + 1) / 2;
     if (p.append && c.new0 < c.t_end) {
         for (int r = 0; r < rounds; ++r)
-            if (2 * r + half < c.n_tiles)
-                stage_appended(p, c, app, tile_pos<WINDOW>(c, 2 * r + half), slab0);
+            for (int j = 2 * r + (WIDE ? 0 : half); j < 2 * r + (WIDE ? 2 : half + 1); ++j)
+                if (j < c.n_tiles)
+                    stage_appended(p, c, app, tile_pos<WINDOW>(c, j), slab0);
         cp_async_commit();
     }
     for (int r = 0; r < rounds; ++r) {
-        const int j = 2 * r + half;
-        if (j < c.n_tiles) {
+#pragma unroll
+        for (int k = 0; k < (WIDE ? 2 : 1); ++k) {
+            const int j = 2 * r + (WIDE ? k : half);
+            if (j >= c.n_tiles) break;
             const int st = j % p.stages;
             // after a failed wait this thread does not wait again; the block aborts at the
             // next block barrier
@@ -630,15 +636,22 @@ __device__ __forceinline__ void merge_cluster_quad(const float* sl0, int stride,
 // merge across clusters is compiled only into the GROUPED builds, which run the launches
 // whose plan has several clusters per unit: kept out of the other builds, the code after
 // the cluster merge stays as short as the chain of every single-cluster launch needs.
-// red: o [8][RMAX][red_stride], m [8][RMAX], l [8][RMAX]; mrg: [splits][msub][kSlot].
+// red: o [8][RMAX][red_stride], m [8][RMAX], l [8][RMAX], with RMAX 32 warps 0-3 the first 16
+// query vectors and warps 4-7 the others ([8][16]); mrg: [splits][msub][kSlot].
 template <typename T, int RMAX, bool GROUPED, bool WINDOW>
 __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, float* mrg,
                            uint64_t* merge_bar, int* misc, const int64_t* qoff,
                            uint8_t* scratch4k) {
     constexpr int RS = red_stride(RMAX);
+    // of query vector m: kW warps' partials, the w-th in row part(w, m)
+    constexpr int kW = RMAX == 32 ? kWarps / 2 : kWarps;
+    constexpr int kRows = kWarps * (RMAX < 16 ? RMAX : 16);
+    auto part = [](int w, int m) {
+        return RMAX == 32 ? ((m >> 4) * kW + w) * 16 + (m & 15) : w * RMAX + m;
+    };
     const float* red_o = red;
-    const float* red_m = red + kWarps * RMAX * RS;
-    const float* red_l = red_m + kWarps * RMAX;
+    const float* red_m = red + kRows * RS;
+    const float* red_l = red_m + kRows;
     const int tid = threadIdx.x;
     const int S = p.splits;
     const size_t base = (size_t)c.unit * S * p.msub;
@@ -657,20 +670,20 @@ __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, flo
             const int kk = min(k, kHeadDim / 4 - 1);
             float mx = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w * RMAX + m]);
+            for (int w = 0; w < kW; ++w) mx = fmaxf(mx, red_m[part(w, m)]);
             const float ref = mx == -INFINITY ? 0.f : mx;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             float l = 0.f;
 #pragma unroll
-            for (int w0 = 0; w0 < kWarps; w0 += 4) {
+            for (int w0 = 0; w0 < kW; w0 += 4) {
                 float4 o[4];
                 float mw[4], lw[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int w = w0 + j;
-                    o[j] = *reinterpret_cast<const float4*>(red_o + (w * RMAX + m) * RS + 4 * kk);
-                    mw[j] = red_m[w * RMAX + m];
-                    lw[j] = red_l[w * RMAX + m];
+                    o[j] = *reinterpret_cast<const float4*>(red_o + part(w, m) * RS + 4 * kk);
+                    mw[j] = red_m[part(w, m)];
+                    lw[j] = red_l[part(w, m)];
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -733,14 +746,14 @@ __device__ void finish_cta(const AttnParams& p, const CtaCtx& c, float* red, flo
         const int m = idx >> 6, d = idx & 63;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, red_m[w * RMAX + m]);
+        for (int w = 0; w < kW; ++w) mx = fmaxf(mx, red_m[part(w, m)]);
         const float ref = mx == -INFINITY ? 0.f : mx;
         float l = 0.f, o = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float a = exp2f(red_m[w * RMAX + m] - ref);
-            l = fmaf(red_l[w * RMAX + m], a, l);
-            o = fmaf(red_o[(w * RMAX + m) * RS + d], a, o);
+        for (int w = 0; w < kW; ++w) {
+            const float a = exp2f(red_m[part(w, m)] - ref);
+            l = fmaf(red_l[part(w, m)], a, l);
+            o = fmaf(red_o[part(w, m) * RS + d], a, o);
         }
         if (S == 1) {
             store_out<T>(p, qoff, m, d, l > 0.f ? o / l : 0.f);
@@ -847,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(sc[jj], valid ? vf[e] : 0.f, acc[e]);
         }
     };
-    if (!run_tiles<T, ROPE, false>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
+    if (!run_tiles<T, ROPE, false, false>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
         return;
 
     // Merge the four 8-lane groups of each warp (they saw different positions).
@@ -890,13 +903,16 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
 // constant 0, their S and O accumulators are not kept, and the block needs about 30
 // fewer registers -- three blocks per SM without spilling, so that more of the next
 // launch's blocks (and its thread-block clusters) fit beside a running launch.
+// RM 32 (windowed calls): warps 0-3 take the first 16 query vectors, warps 4-7 the others,
+// so that a tile is read once for up to 32.
 template <typename T, int MINB, bool ROPE, int RM = 16, bool GROUPED = false,
           bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads, MINB)
     block_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const AttnParams p) {
-    static_assert(RM == 16 || (RM == 8 && !ROPE), "the 8-row build has no rotation");
-    constexpr bool kFull = RM == 16;
+    static_assert(RM == 16 || (RM == 8 && !ROPE) || (RM == 32 && !ROPE && WINDOW),
+                  "the 8-row and 32-row builds have no rotation");
+    constexpr bool kFull = RM >= 16;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
     const SmemLayout L = smem_layout(p.stages, RM,
@@ -910,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int qr = lane >> 2, qc = (lane & 3) * 2;  // fragment row / column pair
     const int jm = lane >> 3, rr = lane & 7;         // ldmatrix matrix / row
+    const int g0 = RM == 32 ? warp >> 2 << 4 : 0;    // the warp's first query vector
 
     CtaCtx c;
     if (!prologue<ROPE, WINDOW>(p, c, smem, bars, qoff, smem + L.app_off, &tmk, &tmv)) return;
@@ -917,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     // Q as m16n8k16 A fragments for the four 16-dim k-steps (rows >= mcount are 0).
     uint32_t qa[4][4];
     const T* qbase = static_cast<const T*>(p.q);
-    const bool rowA = qr < c.mcount, rowB = kFull && qr + 8 < c.mcount;
+    const bool rowA = g0 + qr < c.mcount, rowB = kFull && g0 + qr + 8 < c.mcount;
     if (ROPE) {
         // The block's query rows are rotated once, into shared memory (16 threads per
         // row, 2 rotation pairs each; query m is token m % qlen of the new tokens), and
@@ -946,8 +963,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
         for (int kk = 0; kk < 4; ++kk)
             ldsm_x4(qb + kk * 32, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3]);
     } else {
-        const int64_t offA = rowA ? qoff[qr] : 0;
-        const int64_t offB = rowB ? qoff[qr + 8] : 0;
+        const int64_t offA = rowA ? qoff[g0 + qr] : 0;
+        const int64_t offB = rowB ? qoff[g0 + qr + 8] : 0;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
             const int d0 = kk * 16 + qc;
@@ -968,13 +985,13 @@ __global__ void __launch_bounds__(kThreads, MINB)
         const int lim = p.causal ? c.len - p.qlen + 1 + (c.m0 + r) % p.qlen : c.len;
         return min(lim, c.t_end);
     };
-    const int limA = limit_of(qr, rowA), limB = limit_of(qr + 8, rowB);
+    const int limA = limit_of(g0 + qr, rowA), limB = limit_of(g0 + qr + 8, rowB);
     // WINDOW: the row's first position; query i's is i further than query 0's
     auto first_of = [&](int r) -> int {
         const int64_t lo = (int64_t)c.len - p.qlen - p.window + 1 + (c.m0 + r) % p.qlen;
         return lo > 0 ? (int)lo : 0;
     };
-    const int wloA = WINDOW ? first_of(qr) : 0, wloB = WINDOW ? first_of(qr + 8) : 0;
+    const int wloA = WINDOW ? first_of(g0 + qr) : 0, wloB = WINDOW ? first_of(g0 + qr + 8) : 0;
 
     constexpr int kAcc = kFull ? 4 : 2;  // accumulator elements kept per n8 block
     float oacc[8][kAcc];
@@ -1001,7 +1018,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
         // WINDOW: V rows that some queries see and others do not, or none does. 0 * inf and
         // 0 * NaN would poison the queries that do not see them: rows of the second kind
         // are cleared, rows of the first kind that hold such values are kept out of the
-        // product and added to the queries that see them one by one (odd).
+        // product (in its operand's registers: with RM 32 another warp reads the slab, too)
+        // and added to the queries that see them one by one (odd).
         uint32_t odd = 0;
         if (WINDOW) {
             const int ts = tile0 + slab0;
@@ -1163,6 +1181,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 oacc[n][1] *= aA;
             }
         }
+        // of rows r and r + 1, as halves: all ones unless the row is odd
+        auto even = [&](int r) -> uint32_t {
+            return (odd >> r & 1 ? 0u : 0xFFFFu) | (odd >> (r + 1) & 1 ? 0u : 0xFFFF0000u);
+        };
         if (WINDOW && odd) {  // warp-uniform
             for (uint32_t left = odd; left; left &= left - 1) {
                 const int row = __ffs(left) - 1, t = tile0 + slab0 + row;
@@ -1187,24 +1209,23 @@ __global__ void __launch_bounds__(kThreads, MINB)
                     }
                 }
             }
-            __syncwarp();
-            for (int x = lane; x < 128; x += 32)
-                if (odd >> (x >> 3) & 1)
-                    *reinterpret_cast<uint4*>(sV + swz(slab0 + (x >> 3), x & 7)) =
-                        make_uint4(0, 0, 0, 0);
-            fence_proxy_async();
-            __syncwarp();
         }
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             const int vrow = slab0 + (jm & 1) * 8 + rr;
             uint32_t v0, v1, v2, v3;
             ldsm_x4_t(vb + swz(vrow, 2 * np + (jm >> 1)), v0, v1, v2, v3);
+            if (WINDOW && odd) {  // without the rows added above
+                v0 &= even(qc);
+                v1 &= even(qc + 8);
+                v2 &= even(qc);
+                v3 &= even(qc + 8);
+            }
             mma(oacc[2 * np], pa, v0, v1);
             mma(oacc[2 * np + 1], pa, v2, v3);
         }
     };
-    if (!run_tiles<T, ROPE, WINDOW>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
+    if (!run_tiles<T, ROPE, WINDOW, RM == 32>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
         return;
 
     lA += __shfl_xor_sync(0xffffffffu, lA, 1);
@@ -1214,26 +1235,26 @@ __global__ void __launch_bounds__(kThreads, MINB)
         lB += __shfl_xor_sync(0xffffffffu, lB, 2);
     }
     {
-        constexpr int RS = red_stride(RM);
+        constexpr int RS = red_stride(RM), R = RM == 8 ? 8 : 16;
         float* red_o = red;
-        float* red_m = red + kWarps * RM * RS;
-        float* red_l = red_m + kWarps * RM;
+        float* red_m = red + kWarps * R * RS;
+        float* red_l = red_m + kWarps * R;
         // only the rows that hold query vectors are read back
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
             if (rowA)
-                *reinterpret_cast<float2*>(red_o + (warp * RM + qr) * RS + n * 8 + qc) =
+                *reinterpret_cast<float2*>(red_o + (warp * R + qr) * RS + n * 8 + qc) =
                     make_float2(oacc[n][0], oacc[n][1]);
             if (rowB)
-                *reinterpret_cast<float2*>(red_o + (warp * RM + qr + 8) * RS + n * 8 + qc) =
+                *reinterpret_cast<float2*>(red_o + (warp * R + qr + 8) * RS + n * 8 + qc) =
                     make_float2(oacc[n][kAcc - 2], oacc[n][kAcc - 1]);
         }
         if ((lane & 3) == 0) {
-            red_m[warp * RM + qr] = mA;
-            red_l[warp * RM + qr] = lA;
+            red_m[warp * R + qr] = mA;
+            red_l[warp * R + qr] = lA;
             if (kFull) {
-                red_m[warp * RM + qr + 8] = mB;
-                red_l[warp * RM + qr + 8] = lB;
+                red_m[warp * R + qr + 8] = mB;
+                red_l[warp * R + qr + 8] = lB;
             }
         }
     }
@@ -1302,15 +1323,21 @@ int prepare_kernel(size_t smem_bytes) {
 enum Variant {
     kSimt = 1, kMma = 2, kMma3 = 3, kSimtRope = 4, kMmaRope = 5, kMma8 = 6,
     kSimtG = 7, kMmaG = 8,  // kSimt / kMma with the merge across clusters of a unit
-    kMma8W = 9, kMmaW = 10, kMmaRopeW = 11  // with a sliding window
+    kMma8W = 9, kMmaW = 10, kMmaRopeW = 11, kMma32W = 12  // with a sliding window
 };
 
 // Rows of the warp partials (the red area) of a variant: 16 for the tensor-core builds,
-// 8 for the 8-vector build, 1 for the CUDA-core kernel.
+// 8 for the 8-vector build, 1 for the CUDA-core kernel. And the query vectors of a block.
 constexpr int variant_rmax(int var) {
     return (var == kSimt || var == kSimtRope || var == kSimtG) ? 1
            : (var == kMma8 || var == kMma8W)                   ? 8
+           : var == kMma32W                                    ? 32
                                                                : 16;
+}
+
+// Most query vectors of a block in a plan (8-row builds: plans of 16 whose blocks hold 8).
+constexpr int query_block(int var) {
+    return variant_rmax(var) == 1 ? 1 : std::max(variant_rmax(var), kMmaQueryBlock);
 }
 
 template <typename T>
@@ -1328,6 +1355,7 @@ int prepare(int var) {
     case kSimtG: return prepare_kernel<decode_attn_kernel<T, false, true>>(smem);
     case kMma8W: return prepare_kernel<block_attn_kernel<T, 3, false, 8, false, true>>(smem);
     case kMmaW: return prepare_kernel<block_attn_kernel<T, 2, false, 16, false, true>>(smem);
+    case kMma32W: return prepare_kernel<block_attn_kernel<T, 2, false, 32, false, true>>(smem);
     case kMmaRopeW: return prepare_kernel<block_attn_kernel<T, 2, true, 16, false, true>>(smem);
     default: return prepare_kernel<decode_attn_kernel<T, false>>(smem);
     }
@@ -1347,6 +1375,8 @@ const void* kernel_of(int var) {
         return reinterpret_cast<const void*>(block_attn_kernel<T, 3, false, 8, false, true>);
     case kMmaW:
         return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 16, false, true>);
+    case kMma32W:
+        return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 32, false, true>);
     case kMmaRopeW:
         return reinterpret_cast<const void*>(block_attn_kernel<T, 2, true, 16, false, true>);
     default: return reinterpret_cast<const void*>(decode_attn_kernel<T, false>);
@@ -1388,6 +1418,9 @@ kvd_status launch_attn(int var, dim3 grid, cudaStream_t st, bool pdl, unsigned c
     case kMmaW:
         return launch_ex(block_attn_kernel<T, 2, false, 16, false, true>, grid, dim3(kThreads),
                          mma_smem, st, pdl, cl, mk, mv, p);
+    case kMma32W:
+        return launch_ex(block_attn_kernel<T, 2, false, 32, false, true>, grid, dim3(kThreads),
+                         smem_layout(p.stages, 32, slots, app_rows).total, st, pdl, cl, mk, mv, p);
     case kMmaRopeW:
         return launch_ex(block_attn_kernel<T, 2, true, 16, false, true>, grid, dim3(kThreads),
                          mma_smem, st, pdl, cl, mk, mv, p);
@@ -1456,7 +1489,7 @@ int resident(const void* kern, int kid, size_t smem, int cluster, int nsm) {
 AttnPlan choose_plan(const void* kern, int kid, int var, int nsm, int batch, int n_q_heads,
                      int n_kv_heads, int rows_per_kv, int qlen, int len_bound, int max_cluster,
                      int app_rows, const void* kern_g, int kid_g) {
-    const int mmax = variant_rmax(var) > 1 ? kMmaQueryBlock : 1;
+    const int mmax = query_block(var);
     const AttnPlan P1 = plan_attention(batch, n_q_heads, n_kv_heads, rows_per_kv, qlen, len_bound,
                                        mmax, 1, max_cluster);
     if (P1.rounds <= 1) return P1;
@@ -1574,7 +1607,9 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
     const int64_t vectors = (int64_t)rows_per_kv * group * qlen;
     const int blocks16 = (int)((vectors + kMmaQueryBlock - 1) / kMmaQueryBlock);
     const bool eight = (vectors + blocks16 - 1) / blocks16 <= 8;  // vectors per block
-    int var = windowed ? (eight && !rope ? kMma8W : mma) : (verify || (int64_t)rows_per_kv * group * qlen >= 2) ? mma : simt;
+    int var = windowed                   ? (eight && !rope ? kMma8W : mma)
+              : (verify || vectors >= 2) ? mma
+                                         : simt;
     AttnPlan P;
     if (!plan_for(var, P)) return KVD_ERR_CUDA;
     if (var == simt && P.tiles_per_split <= 2) {
@@ -1624,6 +1659,14 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
             D.units)
             P = D;
     }
+    if (var == kMmaW && vectors > kMmaQueryBlock && P.cgroups == 1 &&
+        (P.cluster || P.splits == 1)) {
+        AttnPlan P2;
+        if (plan_for(kMma32W, P2) && (P2.cluster || P2.splits == 1) && P2.cgroups == 1) {
+            var = kMma32W;
+            P = P2;
+        }
+    }
     if (windowed && P.splits == 1 && P.rounds > 1) {
         // More units than are resident at once, all of about the same length (a window): a
         // last wave that is nearly empty costs as much as a full one, so cut the units where
@@ -1638,7 +1681,7 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
         int64_t best = cost(P);
         for (int sp = 2; sp <= 4; ++sp) {
             const AttnPlan Q = plan_attention(batch, n_q_heads, kv->n_kv_heads, rows_per_kv, qlen,
-                                              len_bound, kMmaQueryBlock, sp, kMaxClusterSplits);
+                                              len_bound, query_block(var), sp, kMaxClusterSplits);
             if (Q.splits != sp || !Q.cluster) continue;
             if (const int64_t t = cost(Q); t < best) {
                 best = t;
@@ -1680,7 +1723,8 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
     p.cgroups = P.cgroups;
     p.csize = P.splits / P.cgroups;
     p.test_stall = (flags & KVD_FLAG_TEST_STALL) ? 1 : 0;
-    p.merge_wait_ns = merge_wait_budget(P.tiles_per_split, p.stages);
+    // (a thread of the 32-row build waits twice in a round)
+    p.merge_wait_ns = merge_wait_budget(P.tiles_per_split * (var == kMma32W ? 2 : 1), p.stages);
     p.append = app ? 1 : 0;
     p.rope = rope ? 1 : 0;
     p.rope_log2_base = rope ? log2f(app->rope_base) : 0.f;

@@ -14,9 +14,13 @@
 // counts is the sum of all errors against the spacing of the running sums, so w has no bias:
 // w = 2^-y, y = (max - x) * log2(e) / T carried in two floats. For y < 16 (heavy ids) y is
 // taken apart as n + j/256 + r: a table, a cubic in r, a relative 2^-29, about 30 instructions.
-// Below (light ids), fp32 rounding of y (unbiased, its constant in two floats) and the
-// hardware's 2^x, whose measured mean error of 3.47e-8 is taken off, are 2^-33 absolute at a
-// third of the price. Below 2^-45.5 w is 0. (Double precision would be 30 times slower here.)
+// Below (light ids), fp32 rounding of y (unbiased, its constant in two floats: 2^-24 y) and the
+// hardware's 2^x, whose measured mean error of 3.47e-8 is taken off, come to 2^-36 absolute at
+// a third of the price. Below 2^-45.5 w is 0. (Double precision would be 30 times slower here.)
+// Where min-p drops all ids from some y below 14.5 on, the light form starts at 8 or 1.5 above
+// that y: the weights of dropped ids only add up to the mass that top-p is a share of, and 2^-21
+// of one, unbiased, is enough there (64 rows x 128000 ids, top-p 0.95, min-p 0.02: 63.6 ->
+// 37.5 us, as none of them is listed either).
 //
 // Design. Bound by the chain of passes and exchanges for few rows, by instruction issue (the
 // weights) for many. One thread-block cluster per row; CTA c has the ids [c * slice, (c + 1) *
@@ -1127,10 +1131,13 @@ extern "C" kvd_status kvd_sample_filtered(const float* logits, int64_t row_strid
     const int mc = prepare_filtered();
     if (nsm <= 0 || mc <= 0) return KVD_ERR_CUDA;
     // CTAs per row, a power of two: enough for the longest slice; then more while slices stay
-    // long and all rows' CTAs are resident at once (two per SM)
+    // long and all rows' CTAs are resident at once: two per SM, but one where 16 form a cluster,
+    // which fewer places fit (16 rows x 128000, top-p and min-p: 24.3 us with 16, 20.0 with 8,
+    // 21.9 with 4; 64 rows: 69, 43.7, 34.0; 8 rows: 16.6, 15.9, 21.3; 1 row: 11.5, 13.9, 18.8)
     int c = 1;
     while (c < mc && ((int64_t)c * kMaxSlice < vocab ||
-                      (2ll * c * batch <= 2ll * nsm && (int64_t)c * 2048 < vocab)))
+                      (2ll * c * batch <= (c < 8 ? 2ll * nsm : nsm) &&
+                       (int64_t)c * 2048 < vocab)))
         c *= 2;
     FilterParams p;
     p.slice = ((vocab + c - 1) / c + kSfThreads - 1) / kSfThreads * kSfThreads;

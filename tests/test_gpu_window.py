@@ -101,6 +101,20 @@ def test_blocks(dtype, window, sinks, n):
         _compare(out, q, k, v, lens, window, sinks)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("Hq,H,n", [(17, 1, 1), (8, 2, 5), (2, 1, 16), (12, 2, 11), (36, 1, 3)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (17, 5), (100, 130), (2000, 4)])
+def test_more_query_vectors_than_sixteen(dtype, Hq, H, n, window, sinks):
+    """Query blocks of up to 32 (17, 20, 32, 2 x 33, 4 x 27), rows empty or shorter than n."""
+    for B, lens, cap in ((5, [2900, 0, n, 64, 129], 2900), (1, [n - 1], 40)):
+        q, k, v = _inputs(dtype, B, Hq, H, n, cap, window + cap + n)
+        out = _run(q, k, v, lens, window, sinks)
+        _compare(out, q, k, v, lens, window, sinks)
+        lens = [max(L, n) for L in lens]
+        out = _run(q, k, v, lens, window, sinks, append=True)
+        _compare(out, q, k, v, lens, window, sinks)
+
+
 @pytest.mark.parametrize("n", [1, 5])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (30, 3), (64, 64), (1000, 1)])
 def test_fused_append(window, sinks, n):
