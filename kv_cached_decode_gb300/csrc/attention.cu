@@ -108,6 +108,7 @@ struct AttnParams {
     int32_t* dev_err;
     int32_t window;    // WINDOW builds: query at p sees t <= p, t < n_sinks or t > p - window
     int32_t n_sinks;
+    float scale_abs;   // |scale_log2|, at least 2^-126: hidden scores (-inf) stay -inf
 };
 
 // Shared memory: [stages x (K tile, V tile); after the tile loop the same bytes hold the
@@ -458,7 +459,6 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
     const int half = warp >> 2, slab0 = (warp & 3) * 16;
     const uint32_t tx = 2u * p.box_rows * kRowBytes;
     bool all_ok = true;
-    int issued = min(p.stages, c.n_tiles);
     const int rounds = (c.n_tiles + 1) / 2;
     if (p.append && c.new0 < c.t_end) {
         for (int r = 0; r < rounds; ++r)
@@ -467,15 +467,20 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
                     stage_appended(p, c, app, tile_pos<WINDOW>(c, j), slab0);
         cp_async_commit();
     }
+    int at = 0;  // tile 2r's place in two turns of the ring: stage at % stages, phase at / stages
     for (int r = 0; r < rounds; ++r) {
 #pragma unroll
         for (int k = 0; k < (WIDE ? 2 : 1); ++k) {
             const int j = 2 * r + (WIDE ? k : half);
             if (j >= c.n_tiles) break;
-            const int st = j % p.stages;
+            int st = at + (j & 1);
+            if (st >= 2 * p.stages) st -= 2 * p.stages;
+            const bool odd = st >= p.stages;
+            if (odd) st -= p.stages;
             // after a failed wait this thread does not wait again; the block aborts at the
             // next block barrier
-            const bool ok = all_ok && mbar_wait_bounded(smem_u32(&bars[st]), (j / p.stages) & 1);
+            const bool ok =
+                all_ok && mbar_wait_bounded(smem_u32(&bars[st]), odd);
             all_ok = ok;
             if (ok) {
                 uint8_t* sK = smem + st * 2 * kTileBytes;
@@ -487,22 +492,24 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
         }
         if (2 * r + p.stages < c.n_tiles) {  // this round's stages are refilled
             if (__syncthreads_or(!all_ok)) {
-                abort_after_timeout(p, c, bars, mrg, issued);
+                abort_after_timeout(p, c, bars, mrg, 2 * r + p.stages);
                 return false;
             }
             if (tid == 0) {
                 fence_proxy_async();
                 for (int k = 0; k < 2 && 2 * r + p.stages + k < c.n_tiles; ++k) {
                     const int jn = 2 * r + p.stages + k;
-                    issue_tile(tmk, tmv, smem, bars, jn % p.stages, tile_pos<WINDOW>(c, jn), c.h,
-                               c.bk, tx);
+                    int sn = at + k;
+                    while (sn >= p.stages) sn -= p.stages;
+                    issue_tile(tmk, tmv, smem, bars, sn, tile_pos<WINDOW>(c, jn), c.h, c.bk, tx);
                 }
             }
-            issued = min(c.n_tiles, issued + 2);
         }
+        at += 2;
+        if (at >= 2 * p.stages) at -= 2 * p.stages;
     }
     if (__syncthreads_or(!all_ok)) {
-        abort_after_timeout(p, c, bars, mrg, issued);
+        abort_after_timeout(p, c, bars, mrg, c.n_tiles);
         return false;
     }
     return true;
@@ -993,6 +1000,14 @@ __global__ void __launch_bounds__(kThreads, MINB)
     };
     const int wloA = WINDOW ? first_of(g0 + qr) : 0, wloB = WINDOW ? first_of(g0 + qr + 8) : 0;
 
+    // WINDOW: the score factor's sign goes into the queries
+    if (WINDOW && p.scale_log2 < 0.f) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qa[kk][e] ^= 0x80008000u;
+    }
+
     constexpr int kAcc = kFull ? 4 : 2;  // accumulator elements kept per n8 block
     float oacc[8][kAcc];
 #pragma unroll
@@ -1024,8 +1039,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
         if (WINDOW) {
             const int ts = tile0 + slab0;
             if (ts >= p.n_sinks && ts + 16 <= c.wlo) return;
-            const int last = (int)max((int64_t)c.len - p.window, (int64_t)0);
-            partial = !(ts + 16 <= c.len - p.qlen + 1 && (ts >= last || ts + 16 <= p.n_sinks));
+            partial = !(ts + 15 <= c.len - p.qlen &&
+                        (ts >= c.len - p.window || ts + 16 <= p.n_sinks));
             if (partial) {
 #pragma unroll
                 for (int x = lane; x < 128; x += 32) {
@@ -1072,7 +1087,6 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 const int key = tile0 + slab0 + n * 8 + qc + (e & 1);
                 const int lim = e < 2 ? limA : limB;
                 if (WINDOW) {
-                    sacc[n][e] *= p.scale_log2;
                     if (partial)
                         sacc[n][e] = key < lim && (key >= (e < 2 ? wloA : wloB) || key < p.n_sinks)
                                          ? sacc[n][e]
@@ -1087,13 +1101,15 @@ __global__ void __launch_bounds__(kThreads, MINB)
             // warp): the usual slab rescales nothing and reduces nothing across lanes. The
             // normaliser sums the unrounded weights (rounding to nearest leaves no bias).
             constexpr float kGrow = 8.f;
-            float tA = fmaxf(fmaxf(sacc[0][0], sacc[0][1]), fmaxf(sacc[1][0], sacc[1][1]));
-            float tB = kFull ? fmaxf(fmaxf(sacc[0][kAcc - 2], sacc[0][kAcc - 1]),
-                                     fmaxf(sacc[1][kAcc - 2], sacc[1][kAcc - 1]))
+            const float scale = p.scale_abs;
+            float tA = max3(max3(sacc[0][0], sacc[0][1], sacc[1][0]), sacc[1][1], -INFINITY);
+            float tB = kFull ? max3(max3(sacc[0][kAcc - 2], sacc[0][kAcc - 1], sacc[1][kAcc - 2]),
+                                    sacc[1][kAcc - 1], -INFINITY)
                              : -INFINITY;
-            if (__any_sync(0xffffffffu, tA > mA + kGrow || (kFull && tB > mB + kGrow))) {
+            if (__any_sync(0xffffffffu, tA * scale > mA + kGrow ||
+                                            (kFull && tB * scale > mB + kGrow))) {
                 tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
-                tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2));
+                tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2)) * scale;
                 const float nA = fmaxf(mA, tA);
                 const float aA = nA == -INFINITY ? 1.f : exp2f(mA - nA);
                 mA = nA;
@@ -1105,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 }
                 if (kFull) {
                     tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 1));
-                    tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2));
+                    tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2)) * scale;
                     const float nB = fmaxf(mB, tB);
                     const float aB = nB == -INFINITY ? 1.f : exp2f(mB - nB);
                     mB = nB;
@@ -1117,18 +1133,18 @@ __global__ void __launch_bounds__(kThreads, MINB)
                     }
                 }
             }
-            const float refA = mA == -INFINITY ? 0.f : mA, refB = mB == -INFINITY ? 0.f : mB;
-            const float w0 = ex2_approx(sacc[0][0] - refA), w1 = ex2_approx(sacc[0][1] - refA);
-            const float w2 = ex2_approx(sacc[1][0] - refA), w3 = ex2_approx(sacc[1][1] - refA);
+            const float refA = mA == -INFINITY ? 0.f : -mA, refB = mB == -INFINITY ? 0.f : -mB;
+            const float w0 = ex2_approx(fmaf(sacc[0][0], scale, refA)), w1 = ex2_approx(fmaf(sacc[0][1], scale, refA));
+            const float w2 = ex2_approx(fmaf(sacc[1][0], scale, refA)), w3 = ex2_approx(fmaf(sacc[1][1], scale, refA));
             lA += (w0 + w1) + (w2 + w3);
             pa[0] = Half16<T>::from_f2(w0, w1);
             pa[2] = Half16<T>::from_f2(w2, w3);
             pa[1] = pa[3] = 0u;
             if (kFull) {
-                const float v0 = ex2_approx(sacc[0][kAcc - 2] - refB);
-                const float v1 = ex2_approx(sacc[0][kAcc - 1] - refB);
-                const float v2 = ex2_approx(sacc[1][kAcc - 2] - refB);
-                const float v3 = ex2_approx(sacc[1][kAcc - 1] - refB);
+                const float v0 = ex2_approx(fmaf(sacc[0][kAcc - 2], scale, refB));
+                const float v1 = ex2_approx(fmaf(sacc[0][kAcc - 1], scale, refB));
+                const float v2 = ex2_approx(fmaf(sacc[1][kAcc - 2], scale, refB));
+                const float v3 = ex2_approx(fmaf(sacc[1][kAcc - 1], scale, refB));
                 lB += (v0 + v1) + (v2 + v3);
                 pa[1] = Half16<T>::from_f2(v0, v1);
                 pa[3] = Half16<T>::from_f2(v2, v3);
@@ -1716,7 +1732,7 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
     p.nsub = P.nsub;
     p.splits = P.splits;
     p.tiles_per_split = P.tiles_per_split;
-    p.stages = std::max(1, P.stages);
+    p.stages = std::max(2, P.stages);  // (a round takes two)
     p.box_rows = std::min(64, kv->capacity);
     p.early = (flags & KVD_FLAG_EARLY_KV) ? 1 : 0;
     p.cluster = P.cluster ? 1 : 0;
@@ -1738,6 +1754,7 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
     p.st = kv->stride_t * 2;
     p.n_kv_heads = kv->n_kv_heads;
     p.scale_log2 = scale * kLog2e;
+    p.scale_abs = std::max(std::fabs(p.scale_log2), 0x1p-126f);
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     p.ws_cnt = reinterpret_cast<int32_t*>(wsb);
     p.ws_part = wsb ? reinterpret_cast<float*>(wsb + P.part_offset) : nullptr;
