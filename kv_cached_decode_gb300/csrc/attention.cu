@@ -1016,6 +1016,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
         for (int e = 0; e < kAcc; ++e) oacc[n][e] = 0.f;
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
 
+    // (slabs start at multiples of 16 rows)
+    const uint32_t kofs = swz((jm >> 1) * 8 + rr, jm & 1), vofs = swz((jm & 1) * 8 + rr, jm >> 1);
     auto slab = [&](uint8_t* sK, uint8_t* sV, int tile0, int slab0) {
         const int nvalid = min(16, max(0, c.t_end - tile0 - slab0));
         if (nvalid == 0) return;
@@ -1066,7 +1068,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 __syncwarp();
             }
         }
-        const uint32_t kb = smem_u32(sK), vb = smem_u32(sV);
+        // ldmatrix addresses of the lane's row: chunks kk * 2 + (jm & 1) of K, 2 np + (jm >> 1) of
+        // V (tiles are 1024-byte aligned, so the chunk is the address's bits 4 to 6)
+        const uint32_t kb = smem_u32(sK) + slab0 * kRowBytes + kofs;
+        const uint32_t vb = smem_u32(sV) + slab0 * kRowBytes + vofs;
         float sacc[2][kAcc];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -1074,9 +1079,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
             for (int e = 0; e < kAcc; ++e) sacc[n][e] = 0.f;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            const int krow = slab0 + (jm >> 1) * 8 + rr;
             uint32_t b0, b1, b2, b3;
-            ldsm_x4(kb + swz(krow, kk * 2 + (jm & 1)), b0, b1, b2, b3);
+            ldsm_x4(kb ^ (kk * 32), b0, b1, b2, b3);
             mma(sacc[0], qa[kk], b0, b1);
             mma(sacc[1], qa[kk], b2, b3);
         }
@@ -1228,9 +1232,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
         }
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
-            const int vrow = slab0 + (jm & 1) * 8 + rr;
             uint32_t v0, v1, v2, v3;
-            ldsm_x4_t(vb + swz(vrow, 2 * np + (jm >> 1)), v0, v1, v2, v3);
+            ldsm_x4_t(vb ^ (np * 32), v0, v1, v2, v3);
             if (WINDOW && odd) {  // without the rows added above
                 v0 &= even(qc);
                 v1 &= even(qc + 8);
@@ -1339,15 +1342,16 @@ int prepare_kernel(size_t smem_bytes) {
 enum Variant {
     kSimt = 1, kMma = 2, kMma3 = 3, kSimtRope = 4, kMmaRope = 5, kMma8 = 6,
     kSimtG = 7, kMmaG = 8,  // kSimt / kMma with the merge across clusters of a unit
-    kMma8W = 9, kMmaW = 10, kMmaRopeW = 11, kMma32W = 12  // with a sliding window
+    kMma8W = 9, kMmaW = 10, kMmaRopeW = 11, kMma32W = 12,  // with a sliding window
+    kMma8W3 = 13  // kMma8W cut for three blocks per SM
 };
 
 // Rows of the warp partials (the red area) of a variant: 16 for the tensor-core builds,
 // 8 for the 8-vector build, 1 for the CUDA-core kernel. And the query vectors of a block.
 constexpr int variant_rmax(int var) {
     return (var == kSimt || var == kSimtRope || var == kSimtG) ? 1
-           : (var == kMma8 || var == kMma8W)                   ? 8
-           : var == kMma32W                                    ? 32
+           : (var == kMma8 || var == kMma8W || var == kMma8W3) ? 8
+           : var == kMma32W                                     ? 32
                                                                : 16;
 }
 
@@ -1369,7 +1373,8 @@ int prepare(int var) {
     case kSimtRope: return prepare_kernel<decode_attn_kernel<T, true>>(smem);
     case kMmaG: return prepare_kernel<block_attn_kernel<T, 2, false, 16, true>>(smem);
     case kSimtG: return prepare_kernel<decode_attn_kernel<T, false, true>>(smem);
-    case kMma8W: return prepare_kernel<block_attn_kernel<T, 3, false, 8, false, true>>(smem);
+    case kMma8W: return prepare_kernel<block_attn_kernel<T, 2, false, 8, false, true>>(smem);
+    case kMma8W3: return prepare_kernel<block_attn_kernel<T, 3, false, 8, false, true>>(smem);
     case kMmaW: return prepare_kernel<block_attn_kernel<T, 2, false, 16, false, true>>(smem);
     case kMma32W: return prepare_kernel<block_attn_kernel<T, 2, false, 32, false, true>>(smem);
     case kMmaRopeW: return prepare_kernel<block_attn_kernel<T, 2, true, 16, false, true>>(smem);
@@ -1388,6 +1393,8 @@ const void* kernel_of(int var) {
     case kMmaG: return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 16, true>);
     case kSimtG: return reinterpret_cast<const void*>(decode_attn_kernel<T, false, true>);
     case kMma8W:
+        return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 8, false, true>);
+    case kMma8W3:
         return reinterpret_cast<const void*>(block_attn_kernel<T, 3, false, 8, false, true>);
     case kMmaW:
         return reinterpret_cast<const void*>(block_attn_kernel<T, 2, false, 16, false, true>);
@@ -1429,6 +1436,9 @@ kvd_status launch_attn(int var, dim3 grid, cudaStream_t st, bool pdl, unsigned c
         return launch_ex(decode_attn_kernel<T, false, true>, grid, dim3(kThreads), simt_smem, st,
                          pdl, cl, mk, mv, p);
     case kMma8W:
+        return launch_ex(block_attn_kernel<T, 2, false, 8, false, true>, grid, dim3(kThreads),
+                         smem_layout(p.stages, 8, slots, app_rows).total, st, pdl, cl, mk, mv, p);
+    case kMma8W3:
         return launch_ex(block_attn_kernel<T, 3, false, 8, false, true>, grid, dim3(kThreads),
                          smem_layout(p.stages, 8, slots, app_rows).total, st, pdl, cl, mk, mv, p);
     case kMmaW:
@@ -1616,8 +1626,11 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
     };
     // the builds with the rotation compiled in stand for kSimt and kMma when it is on
     // Windowed calls run on the tensor cores always: one query vector costs the CUDA cores
-    // 512 instructions per 16 positions, the 8-row build about 150 (measured, 32 rows x 20
-    // heads, a window of 2047: see the kernel's comment).
+    // 512 instructions per 16 positions, the 8-row build about 150 (32 rows x 20 heads, a
+    // window of 2047: 64.0 -> 58.5 us). The 8-row build leaves two blocks per SM their
+    // registers (8 rows x 8 heads x 2 vectors, a window of 16384: 42.8 us, cut for three
+    // 48.7, the 16-row build 43.4), but three where more units wait than two take (32 rows x
+    // 20 heads, windows of 64 and 2047: 9.7 and 60.5 us, with two 11.8 and 61.6).
     const int simt = rope ? kSimtRope : kSimt;
     const int mma = windowed ? (rope ? kMmaRopeW : kMmaW) : rope ? kMmaRope : kMma;
     const int64_t vectors = (int64_t)rows_per_kv * group * qlen;
@@ -1675,6 +1688,16 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
             D.units)
             P = D;
     }
+    if (var == kMma8W && P.splits == 1 && !one_wave(var, P)) {
+        AttnPlan P2;
+        if (plan_for(kMma8W3, P2) && P2.splits == 1) {
+            var = kMma8W3;
+            P = P2;
+        }
+    }
+    // Blocks of up to 32 vectors read a tile once for all of them (8 rows x 8 heads x 20
+    // vectors, a window of 4096: 26.1 -> 23.5 us). Not where few units over a long window are
+    // merged through the workspace, whose plans are those of 16.
     if (var == kMmaW && vectors > kMmaQueryBlock && P.cgroups == 1 &&
         (P.cluster || P.splits == 1)) {
         AttnPlan P2;
