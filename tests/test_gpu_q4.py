@@ -70,6 +70,32 @@ def test_append_bits_follow_the_definition(dtype):
 
 
 @pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("n", [64, 1100])
+def test_append_bits_of_random_rows(dtype, n):
+    """Rows of every magnitude and offset: the quotients round as the definition's divisions."""
+    import kv_cached_decode_gb300 as kvd
+
+    g = torch.Generator().manual_seed(n)
+    H = 8
+    low, high = (-120, 120) if dtype == torch.bfloat16 else (-20, 13)
+    x = []
+    for _ in "kv":
+        e = torch.randint(low, high, (1, H, n, 1), generator=g).double()
+        off = torch.randn(1, H, n, 1, generator=g) * (torch.rand(1, H, n, 1, generator=g) < 0.5)
+        x.append(((torch.randn(1, H, n, 64, generator=g).double() + 4 * off) * 2 ** e).to(dtype))
+    c = kvd.new_q4_cache(1, H, n)
+    err = new_err()
+    kvd.kvd_q4_append(c, x[0].cuda(), x[1].cuda(), dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    k, v, par = _host(c)
+    for t, data, at in ((x[0], k, 0), (x[1], v, 2)):
+        want, step, z = ref64.q4_quantise(t.float().numpy())
+        assert np.array_equal(par[..., at:at + 2], ref64.q4_params(step, z))
+        assert np.array_equal(data, ref64.q4_pack(want))
+
+
+@pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("B,H,n,cap", [(1, 1, 1, 1), (3, 5, 33, 97), (2, 8, 700, 1001)])
 def test_append_counts_and_read_back(dtype, B, H, n, cap):
     import kv_cached_decode_gb300 as kvd
