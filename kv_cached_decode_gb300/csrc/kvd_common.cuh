@@ -127,6 +127,31 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// Two fp32 operations in one instruction, each rounded as by itself.
+struct Pair {
+    uint64_t v;
+    __device__ __forceinline__ Pair(float x, float y) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    }
+    __device__ __forceinline__ float2 get() const {
+        float2 r;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+        return r;
+    }
+};
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
+    return c;
+}
+
 // ---------------------------------------------------------------- shared memory ----
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -482,18 +482,23 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                     vz[t][hh] = half_bits(pr.y >> 16);
                     const int pos = t0 + 16 * t + 8 * hh + krow;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float* s2 = &sc[t][nt][2 * hh];
+                        const float2 x2 = mul2(fma2(Pair(-kz, -kz), Pair(qs[nt][0], qs[nt][1]),
+                                                    Pair(s2[0], s2[1])),
+                                               Pair(ks, ks)).get();
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float x = fmaf(-kz, qs[nt][e], sc[t][nt][2 * hh + e]) * ks;
+                            float x = e ? x2.y : x2.x;
                             if (kMasked) {
                                 const int lm = lim[nt][e];
                                 if (!(pos < lm && (p.window == 0 || pos >= lm - p.window ||
                                                    pos < p.n_sinks)))
                                     x = -INFINITY;
                             }
-                            sc[t][nt][2 * hh + e] = x;
+                            s2[e] = x;
                         }
+                    }
                 }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -558,19 +563,29 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        float w[2], f[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = sc[t][nt][2 * hh + e];
-                            w[e] = ex2_approx(fmaf(x, rs[nt][e], nr[e]));
-                            f[e] = w[e] * y[t][hh];
-                            if (kMasked && x == -INFINITY) w[e] = f[e] = 0.f;
-                            l[nt][e] += w[e];
+                        const float* x = &sc[t][nt][2 * hh];
+                        const float2 a = fma2(Pair(x[0], x[1]), Pair(rs[nt][0], rs[nt][1]),
+                                              Pair(nr[0], nr[1])).get();
+                        float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+                        if (kMasked) {
+                            if (x[0] == -INFINITY) w.x = 0.f;
+                            if (x[1] == -INFINITY) w.y = 0.f;
                         }
-                        const uint32_t pk = pack_half(f[0], f[1]);
+                        const Pair w2(w.x, w.y);
+                        float2 f = mul2(w2, Pair(y[t][hh], y[t][hh])).get();
+                        if (kMasked) {  // (an infinite step)
+                            if (x[0] == -INFINITY) f.x = 0.f;
+                            if (x[1] == -INFINITY) f.y = 0.f;
+                        }
+                        const float2 l2 = add2(Pair(l[nt][0], l[nt][1]), w2).get();
+                        l[nt][0] = l2.x;
+                        l[nt][1] = l2.y;
+                        const uint32_t pk = pack_half(f.x, f.y);
                         const float2 r = Half16<__half>::to_f2(pk);
-                        zs[nt][0] = fmaf(r.x, vz[t][hh], zs[nt][0]);
-                        zs[nt][1] = fmaf(r.y, vz[t][hh], zs[nt][1]);
+                        const float2 z2 = fma2(Pair(r.x, r.y), Pair(vz[t][hh], vz[t][hh]),
+                                               Pair(zs[nt][0], zs[nt][1])).get();
+                        zs[nt][0] = z2.x;
+                        zs[nt][1] = z2.y;
                         pw[t][hh][nt] = transpose8(pk);
                     }
             }

@@ -6,15 +6,17 @@
 // inputs of 11 bits). Both are rounded BEFORE n is formed, so their rounding moves the
 // grid and is not an error of every value.
 //
-// Design. Both kernels are bound by HBM on a prompt (append: 128 bytes read and 36 written
-// per row; read-back the other way round) and by the launch on a step. Four lanes own a
+// Design. On a prompt HBM bounds the read-back (36 bytes read, 128 written per row: 16 rows x 8
+// heads x 4096 of K and V in 33.0 us, 5.2 TB/s), HBM and the issue of instructions the append
+// (37.4 us, 4.6 TB/s); on a step the launch (2.2 us). Four lanes own a
 // row, 16 values (two 16-byte accesses) each; minimum and maximum are taken on the 16-bit
 // values, two at a time, and over the row with two shuffles. x / step rounded correctly, for
 // every value of a row by the same step, is a product with the rounded reciprocal and one
 // remainder step (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990: exact when the reciprocal is rounded to nearest and nothing
 // leaves the normal range), a fifth of the instructions of a division; rows whose step is
-// near the ends of the range divide. Everything else is the IEEE operation in one fixed
+// near the ends of the range divide. Two values share an instruction (fp32 pairs, rounded each
+// by itself). Everything else is the IEEE operation in one fixed
 // order, so that the stored bits follow from the definition on any machine.
 #include "kvd_common.cuh"
 #include "kvd_internal.h"
@@ -48,31 +50,6 @@ __device__ __forceinline__ __half2 as_pair(uint32_t v, __half) {
 }
 __device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t v, __nv_bfloat16) {
     return *reinterpret_cast<__nv_bfloat162*>(&v);
-}
-
-// Two fp32 operations in one instruction, each rounded as by itself.
-struct Pair {
-    uint64_t v;
-    __device__ __forceinline__ Pair(float x, float y) {
-        asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-    }
-    __device__ __forceinline__ float2 get() const {
-        float2 r;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-        return r;
-    }
-};
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c.v) : "l"(a.v), "l"(b.v));
-    return c;
 }
 
 // n = clamp(rint(x / step + z), 0, 15) of the 16 values in the words v, packed.
@@ -115,6 +92,11 @@ __device__ __forceinline__ float quotient(float a, float b, float rcp) {
     const float q = __fmul_rn(a, rcp);
     return __fmaf_rn(__fmaf_rn(-q, b, a), rcp, q);
 }
+// a / b for a >= 0 and a constant b. (A division of 0 would take its slow path: a warp with one
+// row of zeros, or one past its prompt, took 8 us.)
+__device__ __forceinline__ float by_const(float a, float b, float rcp) {
+    return a == 0.f ? 0.f : a > kQuickMin && a < kQuickMax ? quotient(a, b, rcp) : __fdiv_rn(a, b);
+}
 
 // Quantise the 16 values (eight words) of this lane, a quarter of a row; the row's lanes are
 // lane ^ 1, ^ 2, ^ 3: packed nibbles and the row's (step | zero point << 16). bad: the row
@@ -139,20 +121,18 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t* v, uint32_t& par, bo
     bad = !(lf.x * 0.f + lf.y * 0.f + hf.x * 0.f + hf.y * 0.f == 0.f);
     // halves: no finite range overflows
     const float d = __fsub_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo));
-    uint16_t sbits =
-        f2bf(d > kQuickMin && d < kQuickMax ? quotient(d, 7.5f, 1.f / 7.5f) : __fdiv_rn(d, 7.5f));
-    float step = bf16_up(sbits), z;
+    uint16_t sbits = f2bf(by_const(d, 7.5f, 1.f / 7.5f));
+    float step = bf16_up(sbits);
+    const bool flat = step == 0.f;
+    if (flat) {
+        sbits = f2bf(by_const(fabsf(lo), 15.f, 1.f / 15.f));
+        if (sbits == 0) sbits = f2bf(1.f);
+        step = bf16_up(sbits);
+    }
     const bool quick = step > kQuickMin && step < kQuickMax;
     const float rcp = quick ? __frcp_rn(step) : 0.f;
-    if (step == 0.f) {
-        sbits = f2bf(__fdiv_rn(fabsf(lo), 15.f));
-        step = bf16_up(sbits);
-        if (step == 0.f) {
-            sbits = f2bf(1.f);
-            step = 1.f;
-        }
-        z = lo < 0.f ? 15.f : 0.f;
-    } else {
+    float z = lo < 0.f ? 15.f : 0.f;
+    if (!flat) {
         const float q = quick ? quotient(-lo, step, rcp) : __fdiv_rn(-lo, step);
         z = __half2float(__float2half_rn(q)) + 0.f;  // (no -0)
     }
