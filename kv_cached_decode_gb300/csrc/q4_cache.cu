@@ -7,9 +7,8 @@
 // grid and is not an error of every value.
 //
 // Design. On a prompt HBM bounds the read-back (36 bytes read, 128 written per row: 16 rows x 8
-// heads x 4096 of K and V in 33.0 us, 5.2 TB/s), HBM and the issue of instructions the append
-// (37.4 us, 4.6 TB/s); on a step the launch (2.2 us). Four lanes own a
-// row, 16 values (two 16-byte accesses) each; minimum and maximum are taken on the 16-bit
+// heads x 4096 of K and V in 32.6 us, 5.3 TB/s), HBM and the issue of instructions the append
+// (36.6 us, 4.7 TB/s); on a step the launch (1.9 and 2.2 us). Four lanes own a row, 16 values (two 16-byte accesses) each; minimum and maximum are taken on the 16-bit
 // values, two at a time, and over the row with two shuffles. x / step rounded correctly, for
 // every value of a row by the same step, is a product with the rounded reciprocal and one
 // remainder step (P. Markstein, "Computation of elementary functions on the IBM RISC
@@ -18,6 +17,8 @@
 // near the ends of the range divide. Two values share an instruction (fp32 pairs, rounded each
 // by itself). Everything else is the IEEE operation in one fixed
 // order, so that the stored bits follow from the definition on any machine.
+#include <algorithm>
+
 #include "kvd_common.cuh"
 #include "kvd_internal.h"
 
@@ -37,7 +38,6 @@ struct Q4RowsParams {
     int32_t* lens_out;
     int32_t* dev_err;
     int32_t capacity, heads, n;
-    int64_t rows;          // batch * heads * n, per tensor
 };
 
 __device__ __forceinline__ float bf16_up(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
@@ -144,36 +144,18 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t* v, uint32_t& par, bo
     return quick ? pack16<T, true>(v, step, rcp, z) : pack16<T, false>(v, step, rcp, z);
 }
 
-struct Q4Row {
-    int b, h, j;
-};
-__device__ __forceinline__ Q4Row split_row(const Q4RowsParams& p, int64_t row) {
-    Q4Row r;
-    if (p.rows <= 0xFFFFFFFFll) {  // 32-bit divisions: the usual case
-        const uint32_t bh = (uint32_t)row / (uint32_t)p.n;
-        r.j = (int)((uint32_t)row - bh * (uint32_t)p.n);
-        r.b = (int)(bh / (uint32_t)p.heads);
-        r.h = (int)(bh - (uint32_t)r.b * (uint32_t)p.heads);
-    } else {
-        const int64_t bh = row / p.n;
-        r.j = (int)(row % p.n);
-        r.h = (int)(bh % p.heads);
-        r.b = (int)(bh / p.heads);
-    }
-    return r;
-}
-
-// BOTH: four lanes do K's row and V's of a head and position (one set of indexes, twice the
-// loads in flight, parameters stored together): prompts. Else K's only or V's only (blockIdx.y):
-// the chain of a step is shorter.
+// Block (x, y, z): rows 64 x on of a head of batch row z; no index needs a division.
+// BOTH: four lanes do K's row and V's of a head (y) and position (twice the loads in flight,
+// parameters stored together): prompts. Else K's only or V's only (y: 2 head + tensor): the chain
+// of a step is shorter.
 template <typename T, bool BOTH>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4RowsParams p) {
     constexpr int N = BOTH ? 2 : 1;
     pdl_wait();
-    const int64_t idx = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x;
-    const int l = (int)(idx & 3), t0 = BOTH ? 0 : (int)blockIdx.y;
-    const int64_t row = idx >> 2;
-    const bool have = row < p.rows;
+    const int b = blockIdx.z, h = BOTH ? blockIdx.y : blockIdx.y >> 1;
+    const int t0 = BOTH ? 0 : (int)(blockIdx.y & 1);
+    const int l = (int)(threadIdx.x & 3), j = (int)(blockIdx.x * (kQ4Threads / 4) + threadIdx.x / 4);
+    const int64_t row = ((int64_t)b * p.heads + h) * p.n + j;
     uint4 in[N][2] = {};
     auto load = [&]() {
 #pragma unroll
@@ -184,26 +166,20 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4RowsParam
             in[k][1] = src[1];
         }
     };
-    if (have && !p.counts) load();  // before the row's length is known
-    bool live = have;
-    Q4Row r = {0, 0, 0};
-    int len = 0;
-    if (live) {
-        r = split_row(p, row);
-        len = p.pos0 ? p.pos0[r.b] : 0;
-        const int cnt = p.counts ? p.counts[r.b] : p.n;
-        const bool first = t0 == 0 && r.h == 0 && r.j == 0 && l == 0;
-        const bool wrong = len < 0 || cnt < 0 || cnt > p.n || (int64_t)len + cnt > p.capacity;
-        if (first && wrong) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
-        if (first && p.lens_out) p.lens_out[r.b] = wrong ? len : len + cnt;
-        live = !wrong && r.j < cnt;
-    }
+    if (!p.counts && j < p.n) load();  // before the row's length is known
+    const int len = p.pos0 ? p.pos0[b] : 0;
+    const int cnt = p.counts ? p.counts[b] : p.n;
+    const bool first = t0 == 0 && h == 0 && j == 0 && l == 0;
+    const bool wrong = len < 0 || cnt < 0 || cnt > p.n || (int64_t)len + cnt > p.capacity;
+    if (first && wrong) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+    if (first && p.lens_out) p.lens_out[b] = wrong ? len : len + cnt;
+    const bool live = !wrong && j < cnt;
     if (!__any_sync(0xffffffffu, live)) {  // (rows past their prompts)
         pdl_trigger();
         return;
     }
     if (live && p.counts) load();
-    const int64_t at = r.b * p.sb + r.h * p.sh + len + r.j;
+    const int64_t at = b * p.sb + h * p.sh + len + j;
     uint32_t par[N];
     bool any_bad = false;
 #pragma unroll
@@ -227,40 +203,40 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4RowsParam
     pdl_trigger();
 }
 
-// blockIdx.y: K or V (both by one group of lanes: 33.2 -> 36.2 us for 16 rows x 8 heads x 4096).
+// Blocks as the append's, K or V (both by one group of lanes: 33.2 -> 36.2 us for 16 rows x 8
+// heads x 4096).
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) q4_dequant_kernel(const Q4RowsParams p) {
     pdl_wait();
-    const int64_t idx = (int64_t)blockIdx.x * kQ4Threads + threadIdx.x;
-    const int l = (int)(idx & 3);
-    const int t = gridDim.y == 2 ? (int)blockIdx.y : p.out[0] ? 0 : 1;
-    const int64_t row = idx >> 2;
-    if (row < p.rows) {
-        const Q4Row r = split_row(p, row);
-        const int pos = p.pos0 ? p.pos0[r.b] : 0;
-        if (pos < 0 || (int64_t)pos + p.n > p.capacity) {
-            if (r.h == 0 && r.j == 0 && l == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
-        } else {
-            const int64_t at = r.b * p.sb + r.h * p.sh + pos + r.j;
-            const uint2 w = *reinterpret_cast<const uint2*>((t ? p.data[1] : p.data[0]) + at * 32 + l * 8);
-            const uint32_t par = *reinterpret_cast<const uint32_t*>(p.params + at * 8 + t * 4);
-            const float step = bf16_up((uint16_t)par);
-            const float z = __half2float(__ushort_as_half((uint16_t)(par >> 16)));
-            const Pair step2(step, step), z2(-z, -z), base(-8388608.f, -8388608.f);
-            uint32_t o[8];
+    const bool two = p.out[0] && p.out[1];
+    const int b = blockIdx.z, h = two ? blockIdx.y >> 1 : blockIdx.y;
+    const int t = two ? (int)(blockIdx.y & 1) : p.out[0] ? 0 : 1;
+    const int l = (int)(threadIdx.x & 3), j = (int)(blockIdx.x * (kQ4Threads / 4) + threadIdx.x / 4);
+    const int pos = p.pos0 ? p.pos0[b] : 0;
+    if (pos < 0 || (int64_t)pos + p.n > p.capacity) {
+        if (h == 0 && j == 0 && l == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+    } else if (j < p.n) {
+        const int64_t at = b * p.sb + h * p.sh + pos + j;
+        const uint2 w = *reinterpret_cast<const uint2*>((t ? p.data[1] : p.data[0]) + at * 32 + l * 8);
+        const uint32_t par = *reinterpret_cast<const uint32_t*>(p.params + at * 8 + t * 4);
+        const float step = bf16_up((uint16_t)par);
+        const float z = __half2float(__ushort_as_half((uint16_t)(par >> 16)));
+        const Pair step2(step, step), z2(-z, -z), base(-8388608.f, -8388608.f);
+        uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t v = (e < 4 ? w.x : w.y) >> (8 * (e & 3));
-                // n as 2^23 + n (no conversion), exactly
-                const Pair n(__uint_as_float(0x4B000000u | (v & 15u)),
-                             __uint_as_float(0x4B000000u | (v >> 4 & 15u)));
-                const float2 x = mul2(step2, add2(add2(n, base), z2)).get();
-                o[e] = Half16<T>::from_f2(x.x, x.y);
-            }
-            uint4* dst = reinterpret_cast<uint4*>((t ? p.out[1] : p.out[0]) + row * kRowBytes + l * 32);
-            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t v = (e < 4 ? w.x : w.y) >> (8 * (e & 3));
+            // n as 2^23 + n (no conversion), exactly
+            const Pair n(__uint_as_float(0x4B000000u | (v & 15u)),
+                         __uint_as_float(0x4B000000u | (v >> 4 & 15u)));
+            const float2 x = mul2(step2, add2(add2(n, base), z2)).get();
+            o[e] = Half16<T>::from_f2(x.x, x.y);
         }
+        const int64_t row = ((int64_t)b * p.heads + h) * p.n + j;
+        uint4* dst =
+            reinterpret_cast<uint4*>((t ? p.out[1] : p.out[0]) + row * kRowBytes + l * 32);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
     pdl_trigger();
 }
@@ -269,21 +245,30 @@ __global__ void __launch_bounds__(kQ4Threads) q4_dequant_kernel(const Q4RowsPara
 // 8 x 2048 3.32 -> 3.21 us, but 16 x 8 x 1 2.20 -> 2.67 us.
 constexpr int64_t kBothRows = 8192;
 
-template <typename T>
-kvd_status run_append(const Q4RowsParams& p, dim3 grid, cudaStream_t st, bool pdl) {
-    if (p.rows >= kBothRows)
-        return launch(q4_append_kernel<T, true>, grid, dim3(kQ4Threads), 0, st, pdl, p);
-    grid.y = 2;
-    return launch(q4_append_kernel<T, false>, grid, dim3(kQ4Threads), 0, st, pdl, p);
+// per_head: blocks' y per head
+dim3 rows_grid(const Q4RowsParams& p, int32_t batch, int per_head) {
+    return dim3((unsigned)((p.n + kQ4Threads / 4 - 1) / (kQ4Threads / 4)),
+                (unsigned)(p.heads * per_head), (unsigned)batch);
 }
-template <typename T>
-kvd_status run_dequant(const Q4RowsParams& p, dim3 grid, cudaStream_t st, bool pdl) {
-    grid.y = p.out[0] && p.out[1] ? 2 : 1;
-    return launch(q4_dequant_kernel<T>, grid, dim3(kQ4Threads), 0, st, pdl, p);
+// Whole warps for the rows there are.
+dim3 rows_block(const Q4RowsParams& p) {
+    return dim3((unsigned)std::min<int64_t>(kQ4Threads, ((int64_t)p.n * 4 + 31) / 32 * 32));
 }
 
-kvd_status rows_params(Q4RowsParams& p, const kvd_q4_cache* c, int32_t batch, int32_t n,
-                       dim3& grid) {
+template <typename T>
+kvd_status run_append(const Q4RowsParams& p, int32_t batch, cudaStream_t st, bool pdl) {
+    if ((int64_t)batch * p.heads * p.n >= kBothRows)
+        return launch(q4_append_kernel<T, true>, rows_grid(p, batch, 1), rows_block(p), 0, st, pdl,
+                      p);
+    return launch(q4_append_kernel<T, false>, rows_grid(p, batch, 2), rows_block(p), 0, st, pdl, p);
+}
+template <typename T>
+kvd_status run_dequant(const Q4RowsParams& p, int32_t batch, cudaStream_t st, bool pdl) {
+    return launch(q4_dequant_kernel<T>, rows_grid(p, batch, p.out[0] && p.out[1] ? 2 : 1),
+                  rows_block(p), 0, st, pdl, p);
+}
+
+kvd_status rows_params(Q4RowsParams& p, const kvd_q4_cache* c, int32_t batch, int32_t n) {
     p.data[0] = static_cast<uint8_t*>(c->k);
     p.data[1] = static_cast<uint8_t*>(c->v);
     p.params = static_cast<uint8_t*>(c->params);
@@ -292,11 +277,7 @@ kvd_status rows_params(Q4RowsParams& p, const kvd_q4_cache* c, int32_t batch, in
     p.capacity = c->capacity;
     p.heads = c->n_kv_heads;
     p.n = n;
-    p.rows = (int64_t)batch * c->n_kv_heads * n;
-    const int64_t blocks = (p.rows * 4 + kQ4Threads - 1) / kQ4Threads;
-    if (blocks > 0x7fffffff) return KVD_ERR_UNSUPPORTED;
-    grid = dim3((unsigned)blocks);
-    return KVD_OK;
+    return batch > 65535 || c->n_kv_heads > 32767 ? KVD_ERR_UNSUPPORTED : KVD_OK;  // the grid's
 }
 
 }  // namespace
@@ -330,8 +311,7 @@ extern "C" kvd_status kvd_q4_append(kvd_dtype dtype, const kvd_q4_cache* cache, 
     if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return KVD_ERR_INVALID_ARG;
     if (lens_out && (lens_out == lens_in || lens_out == counts)) return KVD_ERR_INVALID_ARG;
     Q4RowsParams p = {};
-    dim3 grid;
-    if (kvd_status s = rows_params(p, cache, batch, q, grid)) return s;
+    if (kvd_status s = rows_params(p, cache, batch, q)) return s;
     p.in[0] = static_cast<const uint8_t*>(k_new);
     p.in[1] = static_cast<const uint8_t*>(v_new);
     p.pos0 = lens_in;
@@ -340,8 +320,8 @@ extern "C" kvd_status kvd_q4_append(kvd_dtype dtype, const kvd_q4_cache* cache, 
     p.dev_err = dev_err;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool pdl = (flags & KVD_FLAG_PDL) != 0;
-    return dtype == KVD_BF16 ? run_append<__nv_bfloat16>(p, grid, st, pdl)
-                             : run_append<__half>(p, grid, st, pdl);
+    return dtype == KVD_BF16 ? run_append<__nv_bfloat16>(p, batch, st, pdl)
+                             : run_append<__half>(p, batch, st, pdl);
 }
 
 extern "C" kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache* cache, int32_t batch,
@@ -353,14 +333,13 @@ extern "C" kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache* cache,
     if (batch == 0 || n == 0 || (!k_out && !v_out)) return KVD_OK;
     if (!aligned16(k_out) || !aligned16(v_out)) return KVD_ERR_INVALID_ARG;
     Q4RowsParams p = {};
-    dim3 grid;
-    if (kvd_status s = rows_params(p, cache, batch, n, grid)) return s;
+    if (kvd_status s = rows_params(p, cache, batch, n)) return s;
     p.out[0] = static_cast<uint8_t*>(k_out);
     p.out[1] = static_cast<uint8_t*>(v_out);
     p.pos0 = pos0;
     p.dev_err = dev_err;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool pdl = (flags & KVD_FLAG_PDL) != 0;
-    return dtype == KVD_BF16 ? run_dequant<__nv_bfloat16>(p, grid, st, pdl)
-                             : run_dequant<__half>(p, grid, st, pdl);
+    return dtype == KVD_BF16 ? run_dequant<__nv_bfloat16>(p, batch, st, pdl)
+                             : run_dequant<__half>(p, batch, st, pdl);
 }
