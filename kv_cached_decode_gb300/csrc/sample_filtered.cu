@@ -44,6 +44,11 @@
 //  4. The kept mass per warp segment; one exchange; the CTA that holds u * total scans that
 //     segment and writes the row's outputs. The others have exited.
 // Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p.
+//
+// Measured (logits normal, sigma 2.5 or 3): 1 row x 51865 ids, top-k 50 and top-p 11.6 us; 64
+// rows x 128000: min-p 20 us, top-p and min-p 37.5 us (of 70000 cycles 9500 read, 14500 weigh, 13000
+// cut, the rest draws and waits), top-k 50 and top-p 39 us, no filter 42 us, top-p alone 100 us
+// (half of the ids are listed and weighed as heavy ones). Reading them once takes 4.9 us.
 #include <algorithm>
 #include <climits>
 #include <cstddef>

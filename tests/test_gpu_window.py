@@ -296,3 +296,26 @@ def test_prefill_rotation_and_agreement_with_the_token_by_token_call():
                             append=(new[1], new[2], None, 10000.0))
         assert torch.allclose(o.cpu().float(), out[:, :, j:j + 1].float(), rtol=2 ** -8,
                               atol=2 ** -9), j
+
+
+@pytest.mark.parametrize("Hq,H,n", [(8, 2, 5), (4, 4, 1), (16, 16, 12)])
+def test_a_wait_that_runs_out_is_reported(Hq, H, n):
+    """The first stage of every unit's last split never completes (KVD_FLAG_TEST_STALL): the
+    blocks of 32, 8 and 16 query vectors give up, write nothing, and the next call is right."""
+    import kv_cached_decode_gb300 as kvd
+
+    L = 1500
+    q, k, v = _inputs(torch.float16, 1, Hq, H, n, L, n)
+    cache = kvd.make_cache(k.cuda(), v.cuda())
+    ws = kvd.new_workspace(kvd.kvd_workspace_size(kvd.KVD_OP_WINDOW_ATTN, 1, Hq, H, 1, n, L))
+    qd = q.cuda()
+    out, err = torch.full_like(qd, 3.0), new_err()
+    kvd.kvd_window_attn(qd, cache, out, ws, L, fixed_len=L, flags=kvd.KVD_FLAG_TEST_STALL,
+                        dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 20 and (out == 3.0).all()
+    err.zero_()
+    kvd.kvd_window_attn(qd, cache, out, ws, L, fixed_len=L, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    _compare(out.cpu(), q, k, v, [L], L, 0)
