@@ -438,8 +438,9 @@ def _at(t, dtype, shape, what, dev):
 def _scratch(workspace, dev):
     if workspace is None:
         return 0, 0
-    return (_at(workspace, workspace.dtype, None, "workspace", dev),
-            workspace.numel() * workspace.element_size())
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(workspace, workspace.dtype, None, "workspace", dev)
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _device_of(t, what):
@@ -573,7 +574,9 @@ def _query_shape(q, out, dev):
     shape = q.shape
     if len(shape) != 4 or shape[3] != HEAD_DIM:
         raise ValueError("q must be [batch, n_q_heads, qlen, 64]")
-    return shape, _at(q, q.dtype, None, "q", dev), _at(out, q.dtype, shape, "out", dev)
+    if not q.is_contiguous():  # (its device is dev)
+        raise ValueError("q must be contiguous")
+    return shape, q.data_ptr(), _at(out, q.dtype, shape, "out", dev)
 
 
 def kvd_window_attn(q, cache: Cache, out, workspace, window: int, n_sinks: int = 0, lens=None,
