@@ -25,13 +25,15 @@
 // coefficients of each pair, used for every further group of eight heads the warp takes:
 //   out[i] = inv (x[i] w[i] cos - x[i+32] w[i+32] sin), out[i+32] likewise
 // at three operations a value. A warp takes more than one group only while the launch still
-// has many warps; the loads of three groups are in flight at a time.
+// has many warps; the loads of four groups are in flight at a time, and as soon as one is stored
+// the next is loaded.
 //
-// Measured: 4 x 4096 tokens x 40 heads of fp16, 168 MB, 34 us, 4.9 TB/s (a plain copy of as many
-// bytes takes 26 us, a transposing one 104 us); 16 tokens 2.3 us. Eight sincospi per lane and
+// Measured: 4 x 4096 tokens x 40 heads of fp16, 168 MB, 30.5 us, 5.5 TB/s (a plain copy of as many
+// bytes takes 26 us, a transposing one 104 us); 16 tokens 2.6 us. Eight sincospi per lane and
 // weights applied per row were 359 instructions per eight heads, bound by their issue; now the
-// loads in flight bound it: 1, 2 or 5 groups ahead, and four tokens per warp (44.5 us), are
-// slower.
+// loads in flight bound it: cos and sin kept in registers, pointers kept with the data and batches
+// of loads instead of the rolling ones 34.4; two, three or five groups ahead 30.4 to 32.3 with the
+// registers cut to fit, 31.2 and more without; four tokens per warp 44.5.
 #include <cmath>
 #include <cstring>
 
@@ -45,7 +47,7 @@ constexpr int kNrThreads = 128;
 // Warps a launch should have before a warp takes more than one group of heads: 152
 // SMs x 16 warps keep enough 16-byte loads in flight.
 constexpr int64_t kNrManyWarps = 152 * 16;
-constexpr int kAhead = 3;  // groups of heads whose loads a warp has in flight
+constexpr int kAhead = 4;  // groups of heads whose loads a warp has in flight
 
 struct NormRopeParams {
     const uint8_t* x[2];   // q, k
@@ -61,12 +63,13 @@ struct NormRopeParams {
     uint64_t freq[32];     // base^(-i/32) / (2 pi) modulo 1, in units of 2^-64 turns
 };
 
-// The coefficients of this lane's eight pairs: w[i] cos, w[i+32] sin, w[i+32] cos, w[i] sin.
+// The coefficients of this lane's eight pairs: w[i] cos, w[i+32] sin, w[i+32] cos, w[i] sin; lane i
+// of the warp has the cos and sin of pair i in `mine`.
 struct Coef {
     float a[8], b[8], c[8], d[8];
 };
 template <typename T>
-__device__ __forceinline__ void make_coef(Coef& k, const float2 (&cs)[8], const uint8_t* w, int l) {
+__device__ __forceinline__ void make_coef(Coef& k, float2 mine, const uint8_t* w, int l) {
     float wa[8], wb[8];
     if (w) {
         unpack8<T>(__ldg(reinterpret_cast<const uint4*>(w) + l), wa);
@@ -77,10 +80,12 @@ __device__ __forceinline__ void make_coef(Coef& k, const float2 (&cs)[8], const 
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        k.a[e] = wa[e] * cs[e].x;
-        k.b[e] = wb[e] * cs[e].y;
-        k.c[e] = wb[e] * cs[e].x;
-        k.d[e] = wa[e] * cs[e].y;
+        const float cos = __shfl_sync(0xffffffffu, mine.x, 8 * l + e);
+        const float sin = __shfl_sync(0xffffffffu, mine.y, 8 * l + e);
+        k.a[e] = wa[e] * cos;
+        k.b[e] = wb[e] * sin;
+        k.c[e] = wb[e] * cos;
+        k.d[e] = wa[e] * sin;
     }
 }
 
@@ -113,7 +118,7 @@ __device__ __forceinline__ void norm_rotate(uint4& lo, uint4& hi, const Coef& k,
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, 5) qk_norm_rope_kernel(const NormRopeParams p) {
     __shared__ uint64_t s_freq[32];
     if (threadIdx.x < 32) s_freq[threadIdx.x] = p.freq[threadIdx.x];
     pdl_wait();
@@ -126,36 +131,29 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
     // this lane's row of group `it` of the token
     struct Item {
         uint4 lo, hi;
-        uint8_t* dst;
-        bool k;
     };
+    auto head = [&](uint32_t it) { return (int)(hg * p.iters + it) * 8 + (lane >> 2); };
     auto load = [&](uint32_t it) {
         Item r;
         r.lo = r.hi = make_uint4(0u, 0u, 0u, 0u);
-        r.dst = nullptr;
-        const int h0 = (int)(hg * p.iters + it) * 8 + (lane >> 2);
-        r.k = h0 >= p.heads[0];
+        const int h0 = head(it);
         if (it < p.iters && h0 < total) {
-            const int h = r.k ? h0 - p.heads[0] : h0;
             // (selects: an index known only at run time would put the parameters on the stack)
-            const uint8_t* src = (r.k ? p.x[1] : p.x[0]) + b * (r.k ? p.sb[1] : p.sb[0]) +
-                                 h * (r.k ? p.sh[1] : p.sh[0]) + j * (r.k ? p.st[1] : p.st[0]);
+            const bool k = h0 >= p.heads[0];
+            const int h = k ? h0 - p.heads[0] : h0;
+            const uint8_t* src = (k ? p.x[1] : p.x[0]) + b * (k ? p.sb[1] : p.sb[0]) +
+                                 h * (k ? p.sh[1] : p.sh[0]) + j * (k ? p.st[1] : p.st[0]);
             r.lo = *reinterpret_cast<const uint4*>(src + l * 16);
             r.hi = *reinterpret_cast<const uint4*>(src + 64 + l * 16);
-            r.dst = (r.k ? p.y[1] : p.y[0]) +
-                    (((int64_t)b * (r.k ? p.heads[1] : p.heads[0]) + h) * p.n + j) * kRowBytes;
         }
         return r;
     };
     if (token < p.tokens) {  // warp-uniform
-        // kAhead groups' loads at a time, the first ones before the token's cos/sin
+        // kAhead groups' loads in flight, the first ones before the token's cos/sin
         Item item[kAhead];
-        auto load_all = [&](uint32_t it) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) item[u] = load(it + u);
-        };
-        load_all(0);
-        // cos/sin: pair `lane`, then this lane's eight
+        for (int u = 0; u < kAhead; ++u) item[u] = load(u);
+        // cos/sin of pair `lane`
         float2 mine = make_float2(1.f, 0.f);
         if (p.rotate) {
             const int64_t pos = (int64_t)(p.pos0 ? p.pos0[b] : 0) + j;
@@ -163,30 +161,29 @@ __global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRope
             // half turns in [-1, 1]
             sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &mine.y, &mine.x);
         }
-        float2 cs[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cs[e].x = __shfl_sync(0xffffffffu, mine.x, 8 * l + e);
-            cs[e].y = __shfl_sync(0xffffffffu, mine.y, 8 * l + e);
-        }
         Coef coef;
         int have = -1;  // which weights the coefficients hold
         for (uint32_t it = 0; it < p.iters; it += kAhead) {
-            if (it > 0) load_all(it);
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (it + u >= p.iters) break;
                 Item& cur = item[u];
-                if (have != (int)cur.k) {
-                    have = cur.k;
-                    make_coef<T>(coef, cs, cur.k ? p.w[1] : p.w[0], l);
+                const int h0 = head(it + u);
+                const bool k = h0 >= p.heads[0];
+                if (__any_sync(0xffffffffu, have != (int)k)) {
+                    have = k;
+                    make_coef<T>(coef, mine, k ? p.w[1] : p.w[0], l);
                 }
-                __syncwarp();
                 norm_rotate<T>(cur.lo, cur.hi, coef, p.eps);
-                if (cur.dst) {
-                    *reinterpret_cast<uint4*>(cur.dst + l * 16) = cur.lo;
-                    *reinterpret_cast<uint4*>(cur.dst + 64 + l * 16) = cur.hi;
+                if (h0 < total) {
+                    const int h = k ? h0 - p.heads[0] : h0;
+                    uint8_t* dst = (k ? p.y[1] : p.y[0]) +
+                                   (((int64_t)b * (k ? p.heads[1] : p.heads[0]) + h) * p.n + j) *
+                                       kRowBytes;
+                    *reinterpret_cast<uint4*>(dst + l * 16) = cur.lo;
+                    *reinterpret_cast<uint4*>(dst + 64 + l * 16) = cur.hi;
                 }
+                if (it + u + kAhead < p.iters) cur = load(it + u + kAhead);
             }
         }
     }
