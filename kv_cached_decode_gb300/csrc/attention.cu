@@ -52,6 +52,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 #include <unordered_map>

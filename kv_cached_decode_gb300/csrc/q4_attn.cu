@@ -44,6 +44,7 @@
 // registers 57.3, 4-warp CTAs 58 to 64, 3 or 5 stages 51.1 and 52.0 (then 51.2); the next unit's
 // first tiles fetched before the last one's merge 52.5.
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -798,16 +799,13 @@ int prepare_q4(size_t smem) {
     return result[dev];
 }
 
-// Blocks (cluster == 1) or clusters of `cluster` blocks resident at once on the device.
+// Blocks (cluster == 1) or clusters of `cluster` blocks resident at once on the device, which
+// prepare_q4 has found in range.
 template <auto Kern>
-int resident_q4(size_t smem, int cluster, int nsm) {
-    static std::mutex mu;
-    static int cache[kMaxDevQ][kMaxClusterQ + 1];  // value + 1
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevQ) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    int& v = cache[dev][cluster];
-    if (v) return v - 1;
+int resident_q4(int dev, size_t smem, int cluster, int nsm) {
+    static std::atomic<int> cache[kMaxDevQ][kMaxClusterQ + 1];  // value + 1
+    std::atomic<int>& v = cache[dev][cluster];
+    if (const int have = v.load(std::memory_order_relaxed)) return have - 1;
     int n = 0;
     if (cluster <= 1) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Kern, kThreadsQ, smem) !=
@@ -829,7 +827,7 @@ int resident_q4(size_t smem, int cluster, int nsm) {
         if (cudaOccupancyMaxActiveClusters(&n, Kern, &cfg) != cudaSuccess) n = 0;
     }
     cudaGetLastError();
-    v = n + 1;
+    v.store(n + 1, std::memory_order_relaxed);
     return n;
 }
 
@@ -882,15 +880,16 @@ kvd_status run_q4(Q4AttnParams& p, const Q4Shape& sh, int64_t tiles, int nsm, vo
     constexpr size_t smem = q4_smem(8 * NT);
     constexpr auto kern = q4_attn_kernel<T, NT, false>;
     const int mc = prepare_q4<kern>(smem);
-    if (mc <= 0) return KVD_ERR_CUDA;
+    int dev = 0;
+    if (mc <= 0 || cudaGetDevice(&dev) != cudaSuccess) return KVD_ERR_CUDA;
     // the most splits (a tile per warp at least) whose clusters are all resident at once
     int64_t want = std::min<int64_t>(std::max<int64_t>(1, (tiles + kWarpsQ - 1) / kWarpsQ), mc);
     for (; want > 1; --want)
-        if (resident_q4<kern>(smem, (int)want, nsm) >= sh.units) break;
+        if (resident_q4<kern>(dev, smem, (int)want, nsm) >= sh.units) break;
     if (tiles >= want * kStreamTiles && q4_streams(sh, tiles)) {
         constexpr auto stream = q4_attn_kernel<T, NT, true>;
         if (prepare_q4<stream>(smem) <= 0) return KVD_ERR_CUDA;
-        const int slots = std::min(kMaxStream, resident_q4<stream>(smem, 1, nsm));
+        const int slots = std::min(kMaxStream, resident_q4<stream>(dev, smem, 1, nsm));
         if (slots <= 0) return KVD_ERR_CUDA;
         const size_t need =
             KVD_WS_COUNTER_BYTES + (size_t)2 * slots * sh.msub * kPart * sizeof(float);
