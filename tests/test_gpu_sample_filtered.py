@@ -174,3 +174,16 @@ def test_frequencies():
     freq = np.bincount(tok, minlength=V)[:n[0]] / N
     # evenly spaced uniforms: every frequency within 2 draws of its probability
     assert np.abs(freq - w / w.sum()).max() <= 2.0 / N and tok.max() < n[0]
+
+
+@pytest.mark.parametrize("V", [700, 40000])
+@pytest.mark.parametrize("logm", [0.01, 6.4, 6.6, 7.9, 8.1, 12.0, 14.4, 14.6, 15.1, 15.9, 16.1, 24.0,
+                                  39.9, 40.1])
+def test_min_p_where_its_forms_change(V, logm):
+    """min_p = 2^-logm: what it drops is only added up below 2^-14.5, listed or weighed above."""
+    g = torch.Generator(device="cuda").manual_seed(int(10 * logm))
+    x = torch.randn(6, V, generator=g, device="cuda") * 3.0
+    u = torch.rand(6, generator=g, device="cuda").cpu().numpy()
+    for p in (0.3, 0.9, 0.999, 1.0):
+        _check(x, u, m=2.0 ** -logm, p=p)
+        _check(x, u, m=2.0 ** -logm, p=p, k=300, T=0.9)
