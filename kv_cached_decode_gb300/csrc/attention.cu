@@ -43,9 +43,9 @@
 //    on; the splits share that list, and nothing between is read. Compiled into builds of
 //    their own (WINDOW), so the others keep their code. Measured, lengths past the window:
 //    32 rows x 20 heads, window 2047 (335 MB) 57.3 us, 5.9 TB/s; 8 rows x 8 heads, window 4096
-//    (67 MB), 1, 4, 16 and 20 query vectors per head 12.7, 13.3, 14.9 and 21.4 us (the last in
-//    blocks of 32, bound by the products and the softmax of two 16-row halves); 1 row x 4 heads,
-//    window 1024: 4.6 us, the chain of launch, tiles and merge.
+//    (67 MB, in L2), 1, 4, 16 and 20 query vectors per head 12.7, 13.3, 14.9 and 16.5 us (the
+//    last in blocks of 32); 1 row x 4 heads, window 1024: 4.6 us, the chain of launch, tiles and
+//    merge.
 //  * Programmatic dependent launch: every block lets the next kernel on the stream
 //    start as soon as its own copies are issued; with KVD_FLAG_EARLY_KV it also issues
 //    those copies before waiting for the previous kernel.
@@ -66,6 +66,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSlot = kHeadDim + 4;   // floats per merge slot: o[64], max, sum, 2 pad
 constexpr int kSlotQuads = kSlot / 4;  // 17 float4 per slot
+constexpr float kGrowLog2 = 8.f;       // WINDOW: a reference moves for scores above it by this
 constexpr int kMaxQueryBlock = 32;     // query vectors of a block of the largest build
 // Row stride (floats) of the warp partials o[warp][row][.]: with 16 rows per warp the
 // fragment layout writes 8 rows at once, and a stride of 72 (8 banks apart) keeps
@@ -456,11 +457,13 @@ __device__ void abort_after_timeout(const AttnParams& p, const CtaCtx& c, uint64
 // WIDE: warp w works on positions (w%4)*16 .. +15 of both tiles, for query vectors 16 (w/4) on;
 // the two warps of a slab make the same writes to it, never others.
 // Returns false after a timeout (already handled: the caller just returns).
-template <typename T, bool ROPE, bool WINDOW, bool WIDE, typename Slab>
+// two(sK0, sV0, sK1, sV1, tile0, tile1, slab0), WIDE only: both slabs at once, false if it leaves
+// them to slab.
+template <typename T, bool ROPE, bool WINDOW, bool WIDE, typename Slab, typename Two>
 __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, uint8_t* smem,
                                           uint64_t* bars, float* mrg, uint8_t* app,
                                           const CUtensorMap* tmk, const CUtensorMap* tmv,
-                                          Slab&& slab) {
+                                          Slab&& slab, Two&& two) {
     const int tid = threadIdx.x, warp = tid >> 5;
     const int half = warp >> 2, slab0 = (warp & 3) * 16;
     const uint32_t tx = 2u * p.box_rows * kRowBytes;
@@ -475,8 +478,24 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
     }
     int at = 0;  // tile 2r's place in two turns of the ring: stage at % stages, phase at / stages
     for (int r = 0; r < rounds; ++r) {
+        bool done = false;
+        if (WIDE && all_ok && 2 * r + 1 < c.n_tiles) {
+            int st[2];
+            uint8_t* sK[2];
 #pragma unroll
-        for (int k = 0; k < (WIDE ? 2 : 1); ++k) {
+            for (int k = 0; k < 2; ++k) {
+                st[k] = at + k;
+                if (st[k] >= 2 * p.stages) st[k] -= 2 * p.stages;
+                const bool odd = st[k] >= p.stages;
+                if (odd) st[k] -= p.stages;
+                all_ok = all_ok && mbar_wait_bounded(smem_u32(&bars[st[k]]), odd);
+                sK[k] = smem + st[k] * 2 * kTileBytes;
+            }
+            done = all_ok && two(sK[0], sK[0] + kTileBytes, sK[1], sK[1] + kTileBytes,
+                                 tile_pos<WINDOW>(c, 2 * r), tile_pos<WINDOW>(c, 2 * r + 1), slab0);
+        }
+#pragma unroll
+        for (int k = 0; k < (WIDE ? 2 : 1) && !done; ++k) {
             const int j = 2 * r + (WIDE ? k : half);
             if (j >= c.n_tiles) break;
             int st = at + (j & 1);
@@ -873,7 +892,8 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(sc[jj], valid ? vf[e] : 0.f, acc[e]);
         }
     };
-    if (!run_tiles<T, ROPE, false, false>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
+    if (!run_tiles<T, ROPE, false, false>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab,
+                                          [](auto&&...) { return false; }))
         return;
 
     // Merge the four 8-lane groups of each warp (they saw different positions).
@@ -917,7 +937,8 @@ __global__ void __launch_bounds__(kThreads, 4)  // <= 64 registers: 4 blocks per
 // fewer registers -- three blocks per SM without spilling, so that more of the next
 // launch's blocks (and its thread-block clusters) fit beside a running launch.
 // RM 32 (windowed calls): warps 0-3 take the first 16 query vectors, warps 4-7 the others,
-// so that a tile is read once for up to 32.
+// so that a tile is read once for up to 32, and takes the slabs of a round's two tiles
+// together (22.6 -> 18.4 us for 20 vectors, 8 rows x 8 heads, window 4096).
 template <typename T, int MINB, bool ROPE, int RM = 16, bool GROUPED = false,
           bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads, MINB)
@@ -1024,6 +1045,84 @@ __global__ void __launch_bounds__(kThreads, MINB)
 
     // (slabs start at multiples of 16 rows)
     const uint32_t kofs = swz((jm >> 1) * 8 + rr, jm & 1), vofs = swz((jm & 1) * 8 + rr, jm >> 1);
+    // RM 32: slabs of two tiles at once where every query sees all of their positions and none is
+    // of a new token: one vote for both, and twice the independent products.
+    auto two = [&](uint8_t* sK0, uint8_t* sV0, uint8_t* sK1, uint8_t* sV1, int tile0, int tile1,
+                   int slab0) -> bool {
+        if constexpr (RM == 32) {
+            auto whole = [&](int ts) {
+                return ts + 15 <= c.len - p.qlen && ts + 16 <= c.new0 &&
+                       (ts >= c.len - p.window || ts + 16 <= p.n_sinks);
+            };
+            if (!whole(tile0 + slab0) || !whole(tile1 + slab0)) return false;
+            const uint32_t off = slab0 * kRowBytes;
+            const uint32_t kb[2] = {smem_u32(sK0) + off + kofs, smem_u32(sK1) + off + kofs};
+            const uint32_t vb[2] = {smem_u32(sV0) + off + vofs, smem_u32(sV1) + off + vofs};
+            float s[4][4];  // keys 8 n2 .. of slab n / 2
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4(kb[t] ^ (kk * 32), b0, b1, b2, b3);
+                    mma(s[2 * t], qa[kk], b0, b1);
+                    mma(s[2 * t + 1], qa[kk], b2, b3);
+                }
+            const float scale = p.scale_abs;
+            float top[2];  // rows qr, qr + 8
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float a = max3(s[0][2 * h], s[0][2 * h + 1], s[1][2 * h]);
+                const float b = max3(s[1][2 * h + 1], s[2][2 * h], s[2][2 * h + 1]);
+                top[h] = max3(max3(s[3][2 * h], s[3][2 * h + 1], a), b, -INFINITY);
+            }
+            if (__any_sync(0xffffffffu,
+                           top[0] * scale > mA + kGrowLog2 || top[1] * scale > mB + kGrowLog2)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float& m = h ? mB : mA;
+                    float t = top[h];
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2)) * scale;
+                    const float next = fmaxf(m, t);
+                    const float a = next == -INFINITY ? 1.f : exp2f(m - next);
+                    m = next;
+                    (h ? lB : lA) *= a;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        oacc[n][2 * h] *= a;
+                        oacc[n][2 * h + 1] *= a;
+                    }
+                }
+            }
+            const float ref[2] = {mA == -INFINITY ? 0.f : -mA, mB == -INFINITY ? 0.f : -mB};
+            uint32_t pa[2][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float w0 = ex2_approx(fmaf(s[n][2 * h], scale, ref[h]));
+                    const float w1 = ex2_approx(fmaf(s[n][2 * h + 1], scale, ref[h]));
+                    (h ? lB : lA) += w0 + w1;
+                    pa[n >> 1][(n & 1) * 2 + h] = Half16<T>::from_f2(w0, w1);
+                }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int np = 0; np < 4; ++np) {
+                    uint32_t v0, v1, v2, v3;
+                    ldsm_x4_t(vb[t] ^ (np * 32), v0, v1, v2, v3);
+                    mma(oacc[2 * np], pa[t], v0, v1);
+                    mma(oacc[2 * np + 1], pa[t], v2, v3);
+                }
+            return true;
+        }
+        return false;
+    };
     auto slab = [&](uint8_t* sK, uint8_t* sV, int tile0, int slab0) {
         const int nvalid = min(16, max(0, c.t_end - tile0 - slab0));
         if (nvalid == 0) return;
@@ -1110,14 +1209,13 @@ __global__ void __launch_bounds__(kThreads, MINB)
             // A row's reference moves only when a score exceeds it by 2^8 (one vote for the
             // warp): the usual slab rescales nothing and reduces nothing across lanes. The
             // normaliser sums the unrounded weights (rounding to nearest leaves no bias).
-            constexpr float kGrow = 8.f;
             const float scale = p.scale_abs;
             float tA = max3(max3(sacc[0][0], sacc[0][1], sacc[1][0]), sacc[1][1], -INFINITY);
             float tB = kFull ? max3(max3(sacc[0][kAcc - 2], sacc[0][kAcc - 1], sacc[1][kAcc - 2]),
                                     sacc[1][kAcc - 1], -INFINITY)
                              : -INFINITY;
-            if (__any_sync(0xffffffffu, tA * scale > mA + kGrow ||
-                                            (kFull && tB * scale > mB + kGrow))) {
+            if (__any_sync(0xffffffffu, tA * scale > mA + kGrowLog2 ||
+                                            (kFull && tB * scale > mB + kGrowLog2))) {
                 tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
                 tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2)) * scale;
                 const float nA = fmaxf(mA, tA);
@@ -1250,7 +1348,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
             mma(oacc[2 * np + 1], pa, v2, v3);
         }
     };
-    if (!run_tiles<T, ROPE, WINDOW, RM == 32>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv, slab))
+    if (!run_tiles<T, ROPE, WINDOW, RM == 32>(p, c, smem, bars, mrg, smem + L.app_off, &tmk, &tmv,
+                                              slab, two))
         return;
 
     lA += __shfl_xor_sync(0xffffffffu, lA, 1);
@@ -1702,7 +1801,7 @@ kvd_status attention(bool verify, kvd_dtype dtype, int32_t batch, int32_t n_q_he
         }
     }
     // Blocks of up to 32 vectors read a tile once for all of them (8 rows x 8 heads x 20
-    // vectors, a window of 4096: 26.1 -> 23.5 us). Not where few units over a long window are
+    // vectors, a window of 4096: 26.7 -> 18.4 us). Not where few units over a long window are
     // merged through the workspace, whose plans are those of 16.
     if (var == kMmaW && vectors > kMmaQueryBlock && P.cgroups == 1 &&
         (P.cluster || P.splits == 1)) {
