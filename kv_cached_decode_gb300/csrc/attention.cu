@@ -491,6 +491,7 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
                 all_ok = all_ok && mbar_wait_bounded(smem_u32(&bars[st[k]]), odd);
                 sK[k] = smem + st[k] * 2 * kTileBytes;
             }
+            all_ok = __all_sync(0xffffffffu, all_ok);
             done = all_ok && two(sK[0], sK[0] + kTileBytes, sK[1], sK[1] + kTileBytes,
                                  tile_pos<WINDOW>(c, 2 * r), tile_pos<WINDOW>(c, 2 * r + 1), slab0);
         }
@@ -504,8 +505,8 @@ __device__ __forceinline__ bool run_tiles(const AttnParams& p, const CtaCtx& c, 
             if (odd) st -= p.stages;
             // after a failed wait this thread does not wait again; the block aborts at the
             // next block barrier
-            const bool ok =
-                all_ok && mbar_wait_bounded(smem_u32(&bars[st]), odd);
+            bool ok = all_ok && mbar_wait_bounded(smem_u32(&bars[st]), odd);
+            if (WINDOW) ok = __all_sync(0xffffffffu, ok);  // a warp gives up as a whole
             all_ok = ok;
             if (ok) {
                 uint8_t* sK = smem + st * 2 * kTileBytes;

@@ -40,15 +40,17 @@
 //     all CTAs instead takes longer than both). If at most kList ids are in it, every CTA
 //     gathers them and ranks them all against all; else the interval of their bit patterns is
 //     cut into 1024 again, until few are left or all are equal, when the cut falls by id.
-//     A prefix of at most kList ids (the usual top-k) is gathered whole and finished there.
+//     A prefix of at most kFewList ids (the usual top-k) is gathered whole and finished there.
 //  4. The kept mass per warp segment; one exchange; the CTA that holds u * total scans that
 //     segment and writes the row's outputs. The others have exited.
 // Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p.
 //
 // Measured (logits normal, sigma 2.5 or 3): 1 row x 51865 ids, top-k 50 and top-p 11.6 us; 64
 // rows x 128000: min-p 20 us, top-p and min-p 37.5 us (of 70000 cycles 9500 read, 14500 weigh, 13000
-// cut, the rest draws and waits), top-k 50 and top-p 39 us, no filter 42 us, top-p alone 100 us
-// (half of the ids are listed and weighed as heavy ones). Reading them once takes 4.9 us.
+// cut, the rest draws and waits), top-k 50 and top-p 39 us, no filter 42 us, top-p alone 76 us
+// (half of the ids are listed and weighed as heavy ones). Reading them once takes 4.9 us. Ranking
+// by one 64-bit key, a warp's neighbours sharing an entry, and up to 256 ids: top-p alone 97.7 ->
+// 76.5 us, one row of 128000 27.8 -> 19.5.
 #include <algorithm>
 #include <climits>
 #include <cstddef>
@@ -66,7 +68,9 @@ constexpr int kSfMaxCluster = 16;
 constexpr int kGroup = 32;                           // bins per group: a lane each
 constexpr int kGroups = 32;
 constexpr int kBins = kGroup * kGroups;
-constexpr int kList = 128;
+constexpr int kList = 256;                           // ids ranked all against all
+constexpr int kFewList = 128;                        // the longest prefix finished that way
+static_assert(kList <= kSfThreads && kFewList <= kList, "a thread per entry at least");
 constexpr int kKeep = 8192;                          // logits of a slice kept in shared memory
 constexpr int kMaxSlice = KVD_MAX_VOCAB / kSfMaxCluster;
 constexpr float kYMax = 45.5f;                       // 2^-y below this is 0
@@ -105,10 +109,9 @@ struct FilterParams {
     int32_t vocab, cluster, slice;  // slice: ids per CTA, a multiple of kSfThreads
 };
 
+// An id and its weight; keys fall with the order of the ids.
 struct Entry {
-    float x;
-    int32_t id;
-    unsigned long long w;
+    unsigned long long key, w;
 };
 
 struct alignas(16) FilterShared {
@@ -145,6 +148,13 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+
+// Logit descending, then id ascending.
+__device__ __forceinline__ unsigned long long key_of(float x, int id) {
+    return ((unsigned long long)ordered(x) << 32) | ~(uint32_t)id;
+}
+__device__ __forceinline__ float key_x(unsigned long long k) { return unordered((uint32_t)(k >> 32)); }
+__device__ __forceinline__ int key_id(unsigned long long k) { return (int)~(uint32_t)k; }
 
 __device__ __forceinline__ void st_cluster_u64(void* local, int rank, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(
@@ -344,6 +354,21 @@ __device__ __forceinline__ void for_ids(const Row& R, bool full, F&& f) {
     }
 }
 
+// The block's threads over n <= kSfThreads entries: `parts` neighbours (a power of two, at most a
+// warp) share an entry, part p taking every parts-th of the others.
+struct Share {
+    int entry, part, parts;
+};
+__device__ __forceinline__ Share share_of(int n) {
+    int lg = 0;
+    while (lg < 5 && (n << (lg + 1)) <= kSfThreads) ++lg;
+    return Share{(int)threadIdx.x >> lg, (int)threadIdx.x & ((1 << lg) - 1), 1 << lg};
+}
+__device__ __forceinline__ unsigned long long join(unsigned long long v, int parts) {
+    for (int off = 1; off < parts; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
 enum SelectResult { kCutHere, kBeyond, kAll, kFew };
 
 // The last id of the shortest prefix (within `kept`) that holds `k` ids (MASS false) or whose
@@ -462,7 +487,8 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
         const int bin = grp * kGroup + in_grp;
         // a short prefix is gathered whole: what follows needs no exchange then
         const bool few =
-            !MASS && first && __shfl_sync(0xffffffffu, inc, in_grp) <= (unsigned long long)kList;
+            !MASS && first && __shfl_sync(0xffffffffu, inc, in_grp) <=
+                                  (unsigned long long)kFewList;
         __syncthreads();  // n_list is 0
 
         // ---- gather its members ----
@@ -473,11 +499,7 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
                 const unsigned long long w = MASS || few ? W.of(x) : 1ull;
                 if (MASS && w < w_min) return;
                 const uint32_t at = atomicAdd(&S.n_list, 1u);
-                if (at < kList) {
-                    S.list[at].x = x;
-                    S.list[at].id = R.lo + i;
-                    S.list[at].w = w;
-                }
+                if (at < kList) S.list[at] = Entry{key_of(x, R.lo + i), w};
             }
         });
         sync_row(R.cluster);
@@ -509,18 +531,18 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
             if (tid == 0) S.n_all = n;
             __syncthreads();
             if (few) return kFew;
-            if (tid < (int)n) {
-                const Entry me = S.all[tid];
-                unsigned long long sum = before;
+            const Share sh = share_of((int)n);
+            const Entry me = S.all[min(sh.entry, max((int)n - 1, 0))];
+            unsigned long long sum = 0;
 #pragma unroll 4
-                for (uint32_t i = 0; i < n; ++i) {
-                    const Entry o = S.all[i];
-                    sum += o.x > me.x || (o.x == me.x && o.id < me.id) ? o.w : 0ull;
-                }
-                if (sum < target && sum + me.w >= target) {
-                    S.cut_x = me.x;
-                    S.cut_id = me.id;
-                }
+            for (int k = sh.part; k < (int)n; k += sh.parts) {
+                const Entry o = S.all[k];
+                sum += o.key > me.key ? o.w : 0ull;
+            }
+            sum = before + join(sum, sh.parts);
+            if (sh.entry < (int)n && sh.part == 0 && sum < target && sum + me.w >= target) {
+                S.cut_x = key_x(me.key);
+                S.cut_id = key_id(me.key);
             }
             __syncthreads();
             kept.x = S.cut_x;
@@ -646,59 +668,62 @@ __device__ __forceinline__ float log_share(unsigned long long w, unsigned long l
 __device__ void draw_few(FilterShared& S, const Weights& W, const FilterParams& p, int b,
                          int top_k, float top_p, unsigned long long w_min, float y_max, float u) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    static_assert(kList == 128, "four warps");
-    if (tid >= kList) return;
-    auto sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
-    auto sum4 = [&](unsigned long long v) {  // over the 128 threads
-        v = warp_sum(v);
-        sync();
-        if (lane == 0) S.red[warp] = v;
-        sync();
-        return S.red[0] + S.red[1] + S.red[2] + S.red[3];
-    };
     const int n = (int)S.n_all;
-    const Entry me = tid < n ? S.all[tid] : Entry{-INFINITY, INT_MAX, 0ull};
-    int before = 0;
-    unsigned long long mass = 0;
+    const Share sh = share_of(n);
+    const bool mine = sh.entry < n;  // (its other threads know the same of the entry)
+    const Entry me = S.all[min(sh.entry, max(n - 1, 0))];
+    auto sum_all = [&](unsigned long long v) {  // over the entries
+        v = warp_sum(mine && sh.part == 0 ? v : 0ull);
+        __syncthreads();
+        if (lane == 0) S.red[warp] = v;
+        __syncthreads();
+        return warp_sum(lane < kSfWarps ? S.red[lane] : 0ull);
+    };
+    unsigned long long before = 0, mass = 0;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+    for (int i = sh.part; i < n; i += sh.parts) {
         const Entry o = S.all[i];
-        const bool ahead = o.x > me.x || (o.x == me.x && o.id < me.id);
+        const bool ahead = o.key > me.key;
         before += ahead;
         mass += ahead ? o.w : 0ull;
     }
-    bool in = tid < n && before < top_k;
+    before = join(before, sh.parts);
+    mass = join(mass, sh.parts);
+    bool in = mine && before < (unsigned long long)top_k;
     if (top_p < 1.f) {  // (uniform)
-        const unsigned long long all = sum4(in ? me.w : 0ull);
+        const unsigned long long all = sum_all(in ? me.w : 0ull);
         bool rest = false;
         unsigned long long target = top_p > 0.f ? mul_floor(top_p, all, rest) : 0ull;
         target += rest ? 1 : 0;
         if (target == 0) target = 1;
         in = in && mass < target;
     }
-    in = in && me.w >= w_min && W.lead(me.x) <= y_max;
+    in = in && me.w >= w_min && W.lead(key_x(me.key)) <= y_max;
     const unsigned long long w = in ? me.w : 0ull;
-    const unsigned long long total = sum4(w);
-    const uint32_t cnt = (uint32_t)sum4(in ? 1ull : 0ull);
-    if (tid < n) S.all[tid].w = w;
+    const unsigned long long total = sum_all(w);
+    const uint32_t cnt = (uint32_t)sum_all(in ? 1ull : 0ull);
+    // (all have read the entries before the sums)
+    if (mine && sh.part == 0) S.all[sh.entry].w = w;
     if (tid == 0) S.found = -1;
-    sync();
+    __syncthreads();
     // the draw, in id order
     const bool lost = u >= 1.f;
     bool rest;
     const unsigned long long t = lost ? ~0ull : mul_floor(fmaxf(u, 0.f), total, rest) + 1;
     unsigned long long run = 0;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+    for (int i = sh.part; i < n; i += sh.parts) {
         const Entry o = S.all[i];
-        run += o.id < me.id ? o.w : 0ull;
+        run += (uint32_t)o.key > (uint32_t)me.key ? o.w : 0ull;  // (a smaller id)
     }
+    run = join(run, sh.parts);
+    const int id = key_id(me.key);
     if (lost) {
-        if (w > 0) atomicMax(&S.found, me.id);
-        sync();
+        if (w > 0) atomicMax(&S.found, id);
+        __syncthreads();
     }
-    if (w > 0 && (lost ? me.id == S.found : run < t && run + w >= t)) {
-        p.token[b] = me.id;
+    if (w > 0 && sh.part == 0 && (lost ? id == S.found : run < t && run + w >= t)) {
+        p.token[b] = id;
         if (p.logprob) p.logprob[b] = log_share(w, total);
         if (p.n_kept) p.n_kept[b] = (int32_t)cnt;
     }
