@@ -24,9 +24,9 @@
  *    too small). KVD_ERR_CUDA reports a launch failure (cudaGetLastError).
  *  - Device errors: conditions only visible on the device (a length past the
  *    capacity, a parent outside its window, a draft id outside the vocabulary, a
- *    NaN logit, a sampling parameter out of range) are written to `*dev_err` with an atomic compare-and-swap from 0, so
- *    the first code wins; the offending unit of work is skipped, nothing traps and
- *    nothing spins. `dev_err` (device int32) may be NULL to ignore them. The caller
+ *    NaN logit, a sampling parameter out of range) are written to `*dev_err` with an
+ *    atomic compare-and-swap from 0, so the first code wins; the offending unit of work
+ *    is skipped, nothing traps and nothing spins. `dev_err` (device int32) may be NULL to ignore them. The caller
  *    reads and clears it when it chooses.
  *  - Layout: a per-layer cache is K, V : [batch, n_kv_heads, capacity, head_dim],
  *    head_dim contiguous ([N] "KV キャッシュが推論を最適化する方法": the per-layer key

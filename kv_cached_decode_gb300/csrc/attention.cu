@@ -137,7 +137,8 @@ __host__ __device__ inline SmemLayout smem_layout(int stages, int rmax, int merg
     L.mrg_off = (L.bar_off + (stages + 1) * 8 + 15) & ~15u;
     L.misc_off = L.mrg_off + merge_slots * kSlot * 4;
     L.qoff_off = L.misc_off + 16;  // element offsets of the block's query rows in q / out
-    L.app_off = L.qoff_off + (rmax > kMmaQueryBlock ? rmax : kMmaQueryBlock) * 8;  // appended rows: K [qlen][128 B], V, table
+    // appended rows: K [qlen][128 B], V, table
+    L.app_off = L.qoff_off + (rmax > kMmaQueryBlock ? rmax : kMmaQueryBlock) * 8;
     L.total = L.app_off + app_rows * 2 * kRowBytes + 1024;  // + slack to align the base
     return L;
 }
@@ -174,8 +175,8 @@ struct CtaCtx {
 // slow), and they are ordered so that a first CTA that receives its cluster peers'
 // partials never exits while a peer can still send:
 //  * a thread's tile waits: at most one per round, each within 1 s, and none after the
-//    first that runs out -- at most `rounds` seconds in all (two per
-//    round in the 32-row build, whose budget counts twice the rounds);
+//    first that runs out -- at most `rounds` seconds in all (two per round in the 32-row
+//    build, whose budget counts twice the rounds);
 //  * a block that gave up drains its copies in flight (at most one wait per stage, each
 //    within 1 s) and sends nothing;
 //  * so every peer that sends has sent within `rounds` seconds of passing the
@@ -619,9 +620,10 @@ __device__ void ws_merge_last(const AttnParams& p, const CtaCtx& c, float* red, 
 
 // A cluster's merge of float4 q4 of one query vector's output: the vector's slots in
 // the cluster's CS splits (at sl0 + r * stride: o[64], max, sum) combined in split order
-// into (max, sum, o), o unnormalised. Loads are unconditional (a split past CS re-reads the last slot and gets
-// weight 0) and go in batches of four, so they overlap. WINDOW builds, which promise what an
-// infinite value does, drop the re-read slot's values too (0 * inf would be NaN).
+// into (max, sum, o), o unnormalised. Loads are unconditional (a split past CS re-reads the
+// last slot and gets weight 0) and go in batches of four, so they overlap. WINDOW builds,
+// which promise what an infinite value does, drop the re-read slot's values too (0 * inf
+// would be NaN).
 template <bool WINDOW>
 __device__ __forceinline__ void merge_cluster_quad(const float* sl0, int stride, int CS, int q4,
                                                    float& mx, float& l, float4& o) {
@@ -1243,8 +1245,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 }
             }
             const float refA = mA == -INFINITY ? 0.f : -mA, refB = mB == -INFINITY ? 0.f : -mB;
-            const float w0 = ex2_approx(fmaf(sacc[0][0], scale, refA)), w1 = ex2_approx(fmaf(sacc[0][1], scale, refA));
-            const float w2 = ex2_approx(fmaf(sacc[1][0], scale, refA)), w3 = ex2_approx(fmaf(sacc[1][1], scale, refA));
+            const float w0 = ex2_approx(fmaf(sacc[0][0], scale, refA));
+            const float w1 = ex2_approx(fmaf(sacc[0][1], scale, refA));
+            const float w2 = ex2_approx(fmaf(sacc[1][0], scale, refA));
+            const float w3 = ex2_approx(fmaf(sacc[1][1], scale, refA));
             lA += (w0 + w1) + (w2 + w3);
             pa[0] = Half16<T>::from_f2(w0, w1);
             pa[2] = Half16<T>::from_f2(w2, w3);

@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                         cp_async16_zfill(dst + kT * 32 + 512 * i, vbase + o, on);
                     }
                     const bool on = t0 + lane < len;
-                    cp_async8_zfill(dst + kT * 64 - lane * 8, pbase + (on ? (int64_t)t0 * 8 : 0), on);
+                    cp_async8_zfill(dst + kT * 64 - lane * 8, pbase + (on ? (int64_t)t0 * 8 : 0),
+                                    on);
                 }
             }
             cp_async_commit();
@@ -968,8 +969,10 @@ extern "C" kvd_status kvd_q4_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_he
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const bool one = sh.msub <= 8;
     if (dtype == KVD_BF16)
-        return one ? run_q4<__nv_bfloat16, 1>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st)
-                   : run_q4<__nv_bfloat16, 2>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st);
+        return one ? run_q4<__nv_bfloat16, 1>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl,
+                                              st)
+                   : run_q4<__nv_bfloat16, 2>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl,
+                                              st);
     return one ? run_q4<__half, 1>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st)
                : run_q4<__half, 2>(p, sh, tiles, nsm, workspace, workspace_bytes, pdl, st);
 }

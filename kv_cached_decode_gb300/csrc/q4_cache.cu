@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(const Q4RowsParam
     pdl_wait();
     const int b = blockIdx.z, h = BOTH ? blockIdx.y : blockIdx.y >> 1;
     const int t0 = BOTH ? 0 : (int)(blockIdx.y & 1);
-    const int l = (int)(threadIdx.x & 3), j = (int)(blockIdx.x * (kQ4Threads / 4) + threadIdx.x / 4);
+    const int l = (int)(threadIdx.x & 3);
+    const int j = (int)(blockIdx.x * (kQ4Threads / 4) + threadIdx.x / 4);
     const int64_t row = ((int64_t)b * p.heads + h) * p.n + j;
     uint4 in[N][2] = {};
     auto load = [&]() {
@@ -212,13 +213,15 @@ __global__ void __launch_bounds__(kQ4Threads) q4_dequant_kernel(const Q4RowsPara
     const bool two = p.out[0] && p.out[1];
     const int b = blockIdx.z, h = two ? blockIdx.y >> 1 : blockIdx.y;
     const int t = two ? (int)(blockIdx.y & 1) : p.out[0] ? 0 : 1;
-    const int l = (int)(threadIdx.x & 3), j = (int)(blockIdx.x * (kQ4Threads / 4) + threadIdx.x / 4);
+    const int l = (int)(threadIdx.x & 3);
+    const int j = (int)(blockIdx.x * (kQ4Threads / 4) + threadIdx.x / 4);
     const int pos = p.pos0 ? p.pos0[b] : 0;
     if (pos < 0 || (int64_t)pos + p.n > p.capacity) {
         if (h == 0 && j == 0 && l == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
     } else if (j < p.n) {
         const int64_t at = b * p.sb + h * p.sh + pos + j;
-        const uint2 w = *reinterpret_cast<const uint2*>((t ? p.data[1] : p.data[0]) + at * 32 + l * 8);
+        const uint8_t* from = (t ? p.data[1] : p.data[0]) + at * 32 + l * 8;
+        const uint2 w = *reinterpret_cast<const uint2*>(from);
         const uint32_t par = *reinterpret_cast<const uint32_t*>(p.params + at * 8 + t * 4);
         const float step = bf16_up((uint16_t)par);
         const float z = __half2float(__ushort_as_half((uint16_t)(par >> 16)));

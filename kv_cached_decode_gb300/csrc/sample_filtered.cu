@@ -46,8 +46,8 @@
 // Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p.
 //
 // Measured (logits normal, sigma 2.5 or 3): 1 row x 51865 ids, top-k 50 and top-p 11.6 us; 64
-// rows x 128000: min-p 20 us, top-p and min-p 37.5 us (of 70000 cycles 9500 read, 14500 weigh, 13000
-// cut, the rest draws and waits), top-k 50 and top-p 39 us, no filter 42 us, top-p alone 76 us
+// rows x 128000: min-p 20 us, top-p and min-p 37.5 us (of 70000 cycles 9500 read, 14500 weigh,
+// 13000 cut, the rest draws and waits), top-k 50 and top-p 39 us, no filter 42 us, top-p alone 76 us
 // (half of the ids are listed and weighed as heavy ones). Reading them once takes 4.9 us. Ranking
 // by one 64-bit key, a warp's neighbours sharing an entry, and up to 256 ids: top-p alone 97.7 ->
 // 76.5 us, one row of 128000 27.8 -> 19.5.
@@ -153,7 +153,9 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 __device__ __forceinline__ unsigned long long key_of(float x, int id) {
     return ((unsigned long long)ordered(x) << 32) | ~(uint32_t)id;
 }
-__device__ __forceinline__ float key_x(unsigned long long k) { return unordered((uint32_t)(k >> 32)); }
+__device__ __forceinline__ float key_x(unsigned long long k) {
+    return unordered((uint32_t)(k >> 32));
+}
 __device__ __forceinline__ int key_id(unsigned long long k) { return (int)~(uint32_t)k; }
 
 __device__ __forceinline__ void st_cluster_u64(void* local, int rank, unsigned long long v) {
@@ -375,9 +377,10 @@ enum SelectResult { kCutHere, kBeyond, kAll, kFew };
 // mass reaches frac * (mass of `kept`) (MASS true; frac < 1; `light`: this CTA's light mass, 0
 // when none of it is kept; only ids of weight w_min or more can be cut at, the others just add
 // to the mass). Over the listed ids, or with `full` over all. Returns kBeyond, leaving `kept`,
-// when the cut is not among the listed ids (of that weight); kAll when it is among none; kFew (counts only) with the whole prefix, and the rest of its last bin, in
-// S.all of every CTA (S.n_all entries, in no order). Every thread of the cluster calls it; the histogram is clear before and
-// after.
+// when the cut is not among the listed ids (of that weight); kAll when it is among none; kFew
+// (counts only) with the whole prefix, and the rest of its last bin, in S.all of every CTA
+// (S.n_all entries, in no order). Every thread of the cluster calls it; the histogram is clear
+// before and after.
 template <bool MASS>
 __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, bool full,
                                Cut& kept, unsigned long long k, float frac,
