@@ -118,14 +118,15 @@ struct alignas(16) FilterShared {
     uint32_t pow[256];
     // one bin: its mass (or its count), low and high half. Cleared after every use.
     uint2 hist[kBins];
-    unsigned long long group[kGroups];                  // sums of kGroup bins
+    unsigned long long group[kSfMaxCluster][kGroups];   // sums of kGroup bins, of every CTA
     unsigned long long part[kSfMaxCluster][kGroup];     // one row per CTA of the cluster
     Entry list[kList];                   // this CTA's members
     Entry all[kList];                    // the cluster's
     // exchanged: written by CTA c into slot c of every CTA, each once per use below
     unsigned long long ex_best[kSfMaxCluster], ex_sum[kSfMaxCluster], ex_light[kSfMaxCluster],
         ex_key[kSfMaxCluster];
-    uint32_t ex_fin[kSfMaxCluster], ex_cnt[kSfMaxCluster], ex_tie[kSfMaxCluster];
+    uint32_t ex_fin[kSfMaxCluster], ex_cnt[kSfMaxCluster], ex_tie[kSfMaxCluster],
+        ex_n[kSfMaxCluster];
     unsigned long long red[kSfWarps];
     uint32_t red32[kSfWarps], red_b[kSfWarps];
     uint32_t n_list, n_all;
@@ -445,23 +446,30 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
             const int g = warp * (kGroups / kSfWarps) + h;
             const uint2 v = S.hist[g * kGroup + lane];
             const unsigned long long sum = warp_sum(((unsigned long long)v.y << 32) | v.x);
-            if (lane == 0) S.group[g] = sum;
+            if (lane < R.cluster) {  // into every CTA
+                if (R.cluster > 1) st_cluster_u64(&S.group[R.rank][g], lane, sum);
+                else S.group[0][g] = sum;
+            }
         }
         sync_row(R.cluster);
         // ---- the group, then the bin in which the prefix becomes complete ----
-        // `from`: 32 sums in every CTA; lane l gets the cluster's l-th
-        auto sums_of = [&](const unsigned long long* from) -> unsigned long long {
-            if (R.cluster == 1) return from[lane];
-            if (warp < R.cluster) S.part[warp][lane] = ld_cluster_u64(from + lane, warp);
-            __syncthreads();
+        // lane l gets the cluster's l-th of 32 sums in every CTA
+        auto over_ctas = [&](const unsigned long long (*from)[kGroup]) -> unsigned long long {
             unsigned long long v = 0;
 #pragma unroll 4
-            for (int r = 0; r < R.cluster; ++r) v += S.part[r][lane];
-            __syncthreads();
+            for (int r = 0; r < R.cluster; ++r) v += from[r][lane];
             return v;
         };
+        auto bins_of = [&](int g) -> unsigned long long {
+            const unsigned long long* mine =
+                reinterpret_cast<const unsigned long long*>(S.hist) + g * kGroup + lane;
+            if (R.cluster == 1) return *mine;
+            if (warp < R.cluster) S.part[warp][lane] = ld_cluster_u64(mine, warp);
+            __syncthreads();
+            return over_ctas(S.part);
+        };
         if (tid == 0) S.n_list = 0;  // (every CTA has read the last list: it has arrived above)
-        unsigned long long v = sums_of(S.group);
+        unsigned long long v = over_ctas(S.group);
         unsigned long long inc = before + warp_incl(v);
         if (first) {
             const unsigned long long total = __shfl_sync(0xffffffffu, inc, 31);
@@ -482,7 +490,7 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
         uint32_t hit = __ballot_sync(0xffffffffu, inc >= target);
         const int grp = hit ? __ffs(hit) - 1 : 0;
         before = __shfl_sync(0xffffffffu, inc - v, grp);
-        v = sums_of(reinterpret_cast<const unsigned long long*>(S.hist) + grp * kGroup);
+        v = bins_of(grp);
         inc = before + warp_incl(v);
         hit = __ballot_sync(0xffffffffu, inc >= target);
         const int in_grp = hit ? __ffs(hit) - 1 : 0;
@@ -505,11 +513,14 @@ __device__ SelectResult select(FilterShared& S, const Row& R, const Weights& W, 
                 if (at < kList) S.list[at] = Entry{key_of(x, R.lo + i), w};
             }
         });
+        __syncthreads();
+        if (tid < R.cluster) {
+            if (R.cluster > 1) st_cluster_u32(&S.ex_n[R.rank], tid, S.n_list);
+            else S.ex_n[0] = S.n_list;
+        }
         sync_row(R.cluster);
-        clear_hist();  // all have read them
-        const uint32_t nr = lane < R.cluster
-                                ? (R.cluster > 1 ? ld_cluster_u32(&S.n_list, lane) : S.n_list)
-                                : 0u;
+        if (!few) clear_hist();  // all have read them (and after `few` no one does)
+        const uint32_t nr = lane < R.cluster ? S.ex_n[lane] : 0u;
         const uint32_t n = __reduce_add_sync(0xffffffffu, nr);
 
         // ---- few: rank them all against all ----
@@ -703,8 +714,11 @@ __device__ void draw_few(FilterShared& S, const Weights& W, const FilterParams& 
     }
     in = in && me.w >= w_min && W.lead(key_x(me.key)) <= y_max;
     const unsigned long long w = in ? me.w : 0ull;
+    if (tid == 0) S.n_list = 0;  // (the entries are in S.all: it counts the kept ones)
+    __syncthreads();
+    if (in && sh.part == 0) atomicAdd(&S.n_list, 1u);
     const unsigned long long total = sum_all(w);
-    const uint32_t cnt = (uint32_t)sum_all(in ? 1ull : 0ull);
+    const uint32_t cnt = S.n_list;
     // (all have read the entries before the sums)
     if (mine && sh.part == 0) S.all[sh.entry].w = w;
     if (tid == 0) S.found = -1;
@@ -1164,12 +1178,13 @@ extern "C" kvd_status kvd_sample_filtered(const float* logits, int64_t row_strid
     const int mc = prepare_filtered();
     if (nsm <= 0 || mc <= 0) return KVD_ERR_CUDA;
     // CTAs per row, a power of two: enough for the longest slice; then more while slices stay
-    // long and all rows' CTAs are resident at once: two per SM, but one where 16 form a cluster,
-    // which fewer places fit (16 rows x 128000, top-p and min-p: 24.3 us with 16, 20.0 with 8,
-    // 21.9 with 4; 64 rows: 69, 43.7, 34.0; 8 rows: 16.6, 15.9, 21.3; 1 row: 11.5, 13.9, 18.8)
+    // long and all rows' CTAs are resident at once: two per SM, but one on every other SM where
+    // 16 form a cluster, which fewer places fit (128000 ids, top-p and min-p, with 16, 8, 4: 1 row
+    // 11.9, 15.1, 20.0 us, 4 rows 12.2, 15.4, 21.3, 8 rows 15.5, 16.3, 22.5, 16 rows 24.3, 20.0,
+    // 21.9, 64 rows 69, 43.7, 34.0; 51865 ids, 8 rows: 13.6, 12.4, 16.6)
     int c = 1;
     while (c < mc && ((int64_t)c * kMaxSlice < vocab ||
-                      (2ll * c * batch <= (c < 8 ? 2ll * nsm : nsm) &&
+                      (2ll * c * batch <= (c < 8 ? 2 * nsm : nsm / 2) &&
                        (int64_t)c * 2048 < vocab)))
         c *= 2;
     FilterParams p;
