@@ -511,7 +511,11 @@ kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache *cache, int32_t ba
  *          max_len) bytes with max_len = the capacity (or fixed_len); used where that size is
  *          more than the counters' (many rows or long ones), under the rules of the other
  *          attention calls
- * Products run on the tensor cores with fp32 accumulation; the softmax is fp32.
+ * Products run on the tensor cores with fp32 accumulation; the softmax is fp32. A weight enters
+ * the second product times its row's step, rounded to binary16: off by 2^-11 of itself or by
+ * 2^-32 of the largest such product among the rows that the query sees (steps from 2^-104 on).
+ * What a query does not see, whatever it holds, changes no bit of its output. |scale * q| is
+ * to stay below 2^100.
  * Flags: KVD_FLAG_PDL; KVD_FLAG_EARLY_KV gives what KVD_FLAG_PDL gives (nothing is read
  * before the wait).
  * Device error: len < 0 or len > capacity -> KVD_ERR_LEN_OVERFLOW, the row's output is

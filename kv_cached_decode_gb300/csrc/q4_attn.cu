@@ -22,11 +22,18 @@
 //    same order; the row order of the output product is free, so lane g takes word g of a V
 //    row, dims 8g..8g+7. Row g of 8 positions is position g / 2 + 4 (g % 2), which keeps both
 //    reads free of bank conflicts. Pairs of positions are two words merged with PRMT.
-//  * The weights that multiply V are fp16(w * sV / 2^E), E a per-warp exponent that follows
-//    the largest step; the zero points multiply the same rounded weights, so their rounding
-//    is not amplified by n - z cancelling. The normaliser sums w unrounded in fp32.
-//  * References move only when a score exceeds them by 2^8, decided by one vote per tile: the
-//    usual tile has no reduction across lanes at all.
+//  * One reference C per query and warp (log2 units, a whole number) serves softmax and V alike:
+//    w = 2^(score - C), summed unrounded in fp32, and w * sV, rounded to binary16, multiplies
+//    nV. C is set so that the largest w * sV of the rows the query sees is 2^7.5 or more and
+//    moves only when one nears 2^15 (or a w 2^96). So what a product loses below binary16's
+//    normal range is 2^-32 of the largest product, and neither rows the query does not see nor
+//    rows of little weight, whatever their steps, cost the others bits. Rows of zeros (n = z =
+//    0) add nothing and do not set C: their step is 1 however small V is. (V steps below
+//    2^-104 do lose bits: the largest w is 2^90 at most when C is set.) The zero points
+//    multiply the same rounded products, so their rounding is not amplified by n - z
+//    cancelling. Whether any may have to move is one vote per tile: the usual tile has no
+//    reduction across lanes at all. Each query then moves by what it sees itself, so its bits
+//    do not depend on others.
 //  * Each warp streams its own tiles of 32 positions (2304 bytes with the parameters)
 //    through a ring of cp.async stages: no block barrier in the loop, and rows at or past
 //    the length are filled with zeros and never read.
@@ -37,9 +44,9 @@
 //    wave takes an equal stretch of it, and units cut by a stretch's end merge through the
 //    workspace (last arrival): the longest row does not set the time.
 //
-// Measured: 16 rows x 8 heads (4 queries each), ragged to 32768 positions, 227 MB: 49.7 us, 4.6
+// Measured: 16 rows x 8 heads (4 queries each), ragged to 32768 positions, 227 MB: 49.0 us, 4.6
 // TB/s, bound by the issue of about 300 instructions per tile; 16 rows of 65536 positions 112 us,
-// 5.4 TB/s. 1 row x 8 heads x 8192: 8.1 us, the chain of launch, first tile and merge.
+// 5.4 TB/s. 1 row x 8 heads x 8192: 8.2 us, the chain of launch, first tile and merge.
 // Tried: 10 or 12 warps 59 and 57 us, 16 warps and one CTA per SM 52.7, three CTAs at 80
 // registers 57.3, 4-warp CTAs 58 to 64, 3 or 5 stages 51.1 and 52.0 (then 51.2); the next unit's
 // first tiles fetched before the last one's merge 52.5.
@@ -69,7 +76,10 @@ constexpr uint32_t kUnitCost = 24;
 constexpr uint32_t kSnap = 8;
 // Lists this short per CTA (in weight) are cut evenly among units; see shares().
 constexpr uint32_t kAlignFew = 64, kAlignMost = 128;
-constexpr float kGrowLog2 = 8.f;
+// Powers of two of a query's largest product w * sV and of its largest w, when C is set; C moves
+// when one is kSlackLog2 more. (A product's exponent is that of w plus that of sV, or one more:
+// below 2^16. A lane's 2^24 rows with w of 2^96 add up to 2^120.)
+constexpr float kSetLog2 = 8.f, kSetWeightLog2 = 90.f, kSlackLog2 = 6.f;
 constexpr int kPart = kHeadDim + 4;          // floats per partial: o[64], max, sum, 2 pad
 
 struct Q4AttnParams {
@@ -133,6 +143,10 @@ __device__ __forceinline__ float half_bits(uint32_t b) {
 }
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return Half16<__half>::from_f2(a, b);
+}
+// The exponent of x >= 0 (-127 for 0 and subnormals).
+__device__ __forceinline__ float power_of(float x) {
+    return __uint_as_float(0x4B400000u + (__float_as_uint(x) >> 23)) - (0x1.8p23f + 127.f);
 }
 
 // The tiles a unit reads, numbered 0 .. total-1: with a window, the tiles of the sinks, then
@@ -431,16 +445,15 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
-        // references, and this lane's share of the normalisers and of the zero points' sums
+        // -C, and this lane's share of the normalisers and of the zero points' sums
         float ref[NT][2], l[NT][2], zs[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                ref[nt][e] = -INFINITY;
+                ref[nt][e] = INFINITY;  // (the first row seen moves it)
                 l[nt][e] = zs[nt][e] = 0.f;
             }
-        float vref = 0x1p-127f, vinv = 0x1p127f;  // 2^E and 2^-E of the V steps
 
         // positions every query of the block sees wholly: t < seen_hi, and with a window
         // t >= seen_lo or t < n_sinks
@@ -473,11 +486,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                         Mma<__half>::run(sc[t][nt], f, qb[nt][kk][0], qb[nt][kk][1]);
                 }
             }
-            float y[2][2], vz[2][2];  // V steps / 2^E and zero points of the positions
-            float top[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
-            uint32_t vraw[2][2];
+            float vs[2][2], vz[2][2];  // V steps and zero points of the positions
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -486,8 +495,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                     // an infinite zero point must not reach rows that do not see it
                     if (kMasked && ((pr.y >> 16) & 0x7C00u) == 0x7C00u) pr.y = 0x7FC0u;
                     const float ks = __uint_as_float(pr.x << 16), kz = half_bits(pr.x >> 16);
-                    vraw[t][hh] = pr.y << 16;
-                    y[t][hh] = __uint_as_float(vraw[t][hh]) * vinv;
+                    vs[t][hh] = __uint_as_float(pr.y << 16);
                     vz[t][hh] = half_bits(pr.y >> 16);
                     const int pos = t0 + 16 * t + 8 * hh + krow;
 #pragma unroll
@@ -509,79 +517,86 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                         }
                     }
                 }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    top[nt][e] = max3(max3(sc[0][nt][e], sc[0][nt][2 + e], sc[1][nt][e]),
-                                      sc[1][nt][2 + e], -INFINITY);
-            // One vote: does a query's reference or the step exponent have to move?
-            bool move = max3(max3(y[0][0], y[0][1], y[1][0]), y[1][1], 0.f) > 16.f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    move |= top[nt][e] * rs[nt][e] > ref[nt][e] + kGrowLog2;
-            if (__any_sync(0xffffffffu, move)) {
-                uint32_t vb = 0;  // the largest finite step
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t v = vraw[i >> 1][i & 1];
-                    if (v < 0x7F800000u) vb = max(vb, v);
-                }
-                vb = __reduce_max_sync(0xffffffffu, vb);
-                float fv = 1.f;
-                if (__uint_as_float(vb) > 16.f * vref) {
-                    // 2^E: the largest step's power of two (at least the smallest normal)
-                    const float nv = __uint_as_float(max(vb & 0x7F800000u, 0x00800000u));
-                    fv = vref * (1.f / nv);
-                    vref = nv;
-                    vinv = 1.f / nv;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        y[i >> 1][i & 1] = __uint_as_float(vraw[i >> 1][i & 1]) * vinv;
-                }
+            // One vote: may a query's reference have to move? By the largest score and the largest
+            // step of a lane's rows, seen or not; what moves is decided by the rows themselves.
+            {
+                const float big = max3(max3(vs[0][0], vs[0][1], vs[1][0]), vs[1][1], 0.f);
+                const float over = fmaxf(power_of(big) - kSetLog2, -kSetWeightLog2) - kSlackLog2;
+                bool move = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float t = top[nt][e];
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                        t = t == -INFINITY ? t : t * rs[nt][e];
-                        const float nref = fmaxf(ref[nt][e], t);
-                        const float f = nref == -INFINITY ? 1.f : exp2f(ref[nt][e] - nref);
-                        ref[nt][e] = nref;
-                        l[nt][e] *= f;
-                        zs[nt][e] *= f * fv;
+                        const float top = max3(max3(sc[0][nt][e], sc[0][nt][2 + e], sc[1][nt][e]),
+                                               sc[1][nt][2 + e], -INFINITY);
+                        move |= fmaf(top, rs[nt][e], over) > -ref[nt][e];
+                    }
+                if (__any_sync(0xffffffffu, move)) {
+                    if (vz[0][0] * vz[0][1] * vz[1][0] * vz[1][1] == 0.f) {  // rows of zeros?
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            acc[j][nt][e] *= f * fv;
-                            acc[j][nt][2 + e] *= f * fv;
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4* v = reinterpret_cast<const uint4*>(
+                                st + kT * 32 + (8 * i + krow) * 32);
+                            const uint4 u = v[0], w = v[1];
+                            if (vz[i >> 1][i & 1] == 0.f &&
+                                (u.x | u.y | u.z | u.w | w.x | w.y | w.z | w.w) == 0u)
+                                vs[i >> 1][i & 1] = 0.f;
                         }
                     }
+                    float lv[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // (a step of 0 or an infinity: by w alone)
+                        const float s = vs[i >> 1][i & 1];
+                        lv[i] = fmaxf(s > 0.f && s < INFINITY ? power_of(s) - kSetLog2 : -INFINITY,
+                                      -kSetWeightLog2);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float to = -INFINITY;  // where C has to be
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float x = sc[i >> 1][nt][2 * (i & 1) + e];
+                                if (kMasked && x == -INFINITY) continue;
+                                to = fmaxf(to, fmaf(x, rs[nt][e], lv[i]));
+                            }
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1)
+                                to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, off));
+                            if (to - kSlackLog2 > -ref[nt][e]) {
+                                to = rintf(to);
+                                const float f = exp2f(-to - ref[nt][e]);  // (from INFINITY: 0)
+                                ref[nt][e] = -to;
+                                l[nt][e] *= f;
+                                zs[nt][e] *= f;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    acc[j][nt][e] *= f;
+                                    acc[j][nt][2 + e] *= f;
+                                }
+                            }
+                        }
+                }
             }
             // the weights times the steps, as the output product's operand
             uint32_t pw[2][2][NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float nr[2] = {ref[nt][0] == -INFINITY ? 0.f : -ref[nt][0],
-                                     ref[nt][1] == -INFINITY ? 0.f : -ref[nt][1]};
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         const float* x = &sc[t][nt][2 * hh];
                         const float2 a = fma2(Pair(x[0], x[1]), Pair(rs[nt][0], rs[nt][1]),
-                                              Pair(nr[0], nr[1])).get();
+                                              Pair(ref[nt][0], ref[nt][1])).get();
                         float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         if (kMasked) {
                             if (x[0] == -INFINITY) w.x = 0.f;
                             if (x[1] == -INFINITY) w.y = 0.f;
                         }
                         const Pair w2(w.x, w.y);
-                        float2 f = mul2(w2, Pair(y[t][hh], y[t][hh])).get();
+                        float2 f = mul2(w2, Pair(vs[t][hh], vs[t][hh])).get();
                         if (kMasked) {  // (an infinite step)
                             if (x[0] == -INFINITY) f.x = 0.f;
                             if (x[1] == -INFINITY) f.y = 0.f;
@@ -597,7 +612,6 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                         zs[nt][1] = z2.y;
                         pw[t][hh][nt] = transpose8(pk);
                     }
-            }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 uint32_t w[4];  // positions c, c + 4, c + 8, c + 12
@@ -649,19 +663,22 @@ __global__ void __launch_bounds__(kThreadsQ, 2) q4_attn_kernel(const Q4AttnParam
                 }
                 const int m = 8 * nt + 2 * c + e;
                 if (m < mcount) {
+                    // partials of different C meet: the sum's power of two goes into it
+                    const int up = min(max((int)(__float_as_uint(t) >> 23), 1), 253) - 127;
+                    const float down = __uint_as_float((uint32_t)(127 - up) << 23);
                     float* o = red + (warp * RM + m) * kPart;
                     float x[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        x[2 * j] = fmaf(acc[j][nt][e], 0x1p24f, -z) * vref;
-                        x[2 * j + 1] = fmaf(acc[j][nt][2 + e], 0x1p20f, -z) * vref;
+                        x[2 * j] = fmaf(acc[j][nt][e], 0x1p24f, -z) * down;
+                        x[2 * j + 1] = fmaf(acc[j][nt][2 + e], 0x1p20f, -z) * down;
                     }
                     float4* d = reinterpret_cast<float4*>(o + 8 * g);
                     d[0] = make_float4(x[0], x[1], x[2], x[3]);
                     d[1] = make_float4(x[4], x[5], x[6], x[7]);
                     if (g == 0) {
-                        o[kHeadDim] = ref[nt][e];
-                        o[kHeadDim + 1] = t;
+                        o[kHeadDim] = (float)up - ref[nt][e];
+                        o[kHeadDim + 1] = t * down;
                     }
                 }
             }
