@@ -43,7 +43,8 @@
 //     A prefix of at most kFewList ids (the usual top-k) is gathered whole and finished there.
 //  4. The kept mass per warp segment; one exchange; the CTA that holds u * total scans that
 //     segment and writes the row's outputs. The others have exited.
-// Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p.
+// Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p. One more,
+// arrived at before the read and waited for after it, tells that all CTAs have started.
 //
 // Measured (logits normal, sigma 2.5 or 3): 1 row x 51865 ids, top-k 50 and top-p 11.6 us; 64
 // rows x 128000: min-p 20 us, top-p and min-p 37.5 us (of 70000 cycles 9500 read, 14500 weigh,
@@ -774,6 +775,10 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         return;
     }
 
+    // (every CTA of the row comes here or none: the first exchange waits until all have, as
+    // nothing may be written into a CTA that has not started)
+    if (R.cluster > 1) cluster_arrive_relaxed();
+
     // ---- 1. read; the largest logit, lowest id first; how many are above -inf ----
     const float* src = p.logits + (int64_t)b * p.row_stride + R.lo;
     const bool keep = p.slice <= kKeep;
@@ -847,6 +852,8 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     unsigned long long best = best_of(lane < kSfWarps ? S.red[lane] : 0ull);
     uint32_t fin = __reduce_add_sync(0xffffffffu, lane < kSfWarps ? S.red32[lane] : 0u);
     if (R.cluster > 1) {
+        __syncwarp();
+        cluster_wait();  // every CTA has started: its shared memory can be written
         if (tid < R.cluster) {
             st_cluster_u64(&S.ex_best[R.rank], tid, best);
             st_cluster_u32(&S.ex_fin[R.rank], tid, fin);
