@@ -265,6 +265,8 @@ __global__ void __launch_bounds__(kSaThreads, 1) sample_accept_kernel(const Samp
         }
         __syncthreads();
     } else {
+        // (n is the same in every CTA of the row: all of them come here or none)
+        if (p.cluster > 1) cluster_arrive_relaxed();
         chunk_pass();
         float rw = sw, rp = sp;
 #pragma unroll
@@ -277,6 +279,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) sample_accept_kernel(const Samp
             S.warp_s[warp][1] = rp;
         }
         __syncthreads();
+        if (p.cluster > 1) cluster_wait();  // every CTA has started: it can be written into
         if (tid < p.cluster) {
             // this CTA's pair into every CTA (so that no shared memory is read remotely after
             // the barrier, and a CTA may exit as soon as it is done)

@@ -13,7 +13,7 @@ REMOTE = r"\b(st_cluster_\w+|ld_cluster\w*|st_async_v4|map_shared)\s*\("
 BARRIER = r"\b(cluster_wait|cluster_sync_q4|cluster_sync_all|sync_row)\s*\("
 # a kernel's helpers, as far as they touch other CTAs, are called behind its own first access
 KERNELS = [("sample_filtered.cu", "sample_filtered_kernel"), ("q4_attn.cu", "q4_attn_kernel"),
-           ("beam_select.cu", "beam_select_kernel")]
+           ("beam_select.cu", "beam_select_kernel"), ("sample_accept.cu", "sample_accept_kernel")]
 
 
 def body(source, kernel):
