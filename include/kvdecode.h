@@ -605,7 +605,7 @@ kvd_status kvd_sample_accept(const float *target, const float *draft, const int3
  *   2. ends at the latest with the id at which the prefix's mass reaches top_p times the
  *      mass of what step 1 left                                    (top_p >= 1: all)
  *   3. has w_t >= min_p for every id                               (min_p <= 0: all)
- * and at least one id. Ids with logit -inf are never kept. Then, over the kept ids,
+ * and at least one id (with min_p > 1 that one: no w is above 1). Ids with logit -inf are never kept. Then, over the kept ids,
  *   token   = the smallest id whose running sum of w, in id order, exceeds u * sum(w)
  *             (the last kept id with w > 0 if rounding leaves none)
  *   logprob = log(w_token / sum(w))

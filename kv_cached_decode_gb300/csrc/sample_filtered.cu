@@ -871,7 +871,8 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         // (no CTA reads another's memory after the exchange)
         return;
     }
-    if (T == 0.f || top_k == 1) {
+    // (no weight is above 1)
+    if (T == 0.f || top_k == 1 || min_p > 1.f) {
         if (tid == 0 && R.rank == 0) {
             p.token[b] = (int32_t)~(uint32_t)best;
             if (p.logprob) p.logprob[b] = 0.f;
@@ -896,11 +897,11 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     unsigned long long w_min = 0;
     if (by_w) {
         bool rest = false;
-        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;
+        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;  // (1 at most here)
         w_min += rest ? 1 : 0;
     }
     const float y_max =
-        min_p > 0.f ? fmaf(-log2f(fminf(min_p, 1.f)), by_w ? 1.00001f : 1.f, by_w ? 1e-4f : 0.f)
+        min_p > 0.f ? fmaf(-log2f(min_p), by_w ? 1.00001f : 1.f, by_w ? 1e-4f : 0.f)
                     : INFINITY;
 
     // ---- 2. the heavy ids of this warp's segment; the light ones' mass ----

@@ -187,3 +187,24 @@ def test_min_p_where_its_forms_change(V, logm):
     for p in (0.3, 0.9, 0.999, 1.0):
         _check(x, u, m=2.0 ** -logm, p=p)
         _check(x, u, m=2.0 ** -logm, p=p, k=300, T=0.9)
+
+
+@pytest.mark.parametrize("V", [5, 700, 40000])
+def test_min_p_above_one_keeps_one_id(V):
+    """No weight is above 1, so nothing passes and the one id that is always kept is the first of
+    the order: the lowest of those tied for the largest logit. At 1 all of these stay."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn(5, V, generator=g, device="cuda").clamp(max=1.0)
+    first = torch.tensor([0, 1, V // 3, V - 3, 2], device="cuda")
+    for b in range(5):
+        x[b, first[b]:first[b] + 3] = 1.5
+    x[4, 2:5] = float("inf")
+    u = [0.0, 0.3, 0.6, 0.999, 0.5]
+    for m in (np.nextafter(np.float32(1), np.float32(2)), 1.5, 1e30, np.inf):
+        for kw in (dict(), dict(p=0.9), dict(k=3), dict(k=2, p=0.5), dict(T=0.3)):
+            tok, lp, n, err = _draw(x, u, m=m, **kw)
+            assert err == 0 and (n == 1).all() and (lp == 0).all()
+            assert (tok == first.cpu().numpy()).all(), (m, kw)
+    _, lp, n, _ = _draw(x, u, m=1.0)
+    ties = (x == x.max(1, keepdim=True).values).sum(1).cpu().numpy()
+    assert (ties >= 3).all() and (n == ties).all() and np.allclose(lp, -np.log(ties))
