@@ -17,6 +17,18 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Counters, then `slots` partial outputs, then as many (max, sum) pairs.
+struct WorkspaceLayout {
+    size_t part, ml, bytes;
+};
+WorkspaceLayout workspace_layout(size_t slots) {
+    WorkspaceLayout w;
+    w.part = KVD_WS_COUNTER_BYTES;
+    w.ml = align_up(w.part + slots * 64 * sizeof(float), 256);
+    w.bytes = w.ml + slots * 2 * sizeof(float);
+    return w;
+}
 }  // namespace
 
 int sm_count() {
@@ -113,10 +125,10 @@ AttnPlan plan_attention(int batch, int n_q_heads, int n_kv_heads, int rows_per_k
     P.cluster = P.splits > 1 && P.splits <= max_cluster;
     P.cgroups = 1;
     P.stages = P.tiles_per_split >= 4 ? 4 : 2;
-    P.part_offset = KVD_WS_COUNTER_BYTES;
-    const size_t slots = (size_t)P.units * P.splits * P.msub;
-    P.ml_offset = align_up(P.part_offset + slots * 64 * sizeof(float), 256);
-    P.ws_bytes = (P.splits > 1 && !P.cluster) ? P.ml_offset + slots * 2 * sizeof(float) : 0;
+    const WorkspaceLayout w = workspace_layout((size_t)P.units * P.splits * P.msub);
+    P.part_offset = w.part;
+    P.ml_offset = w.ml;
+    P.ws_bytes = (P.splits > 1 && !P.cluster) ? w.bytes : 0;
     return P;
 }
 
@@ -128,9 +140,9 @@ AttnPlan plan_grouped(int batch, int n_q_heads, int n_kv_heads, int rows_per_kv,
     P.cgroups = groups;
     P.splits = cs * groups;
     P.cluster = true;
-    const size_t slots = (size_t)P.units * groups * P.msub;
-    P.ml_offset = align_up(P.part_offset + slots * 64 * sizeof(float), 256);
-    P.ws_bytes = P.ml_offset + slots * 2 * sizeof(float);
+    const WorkspaceLayout w = workspace_layout((size_t)P.units * groups * P.msub);
+    P.ml_offset = w.ml;
+    P.ws_bytes = w.bytes;
     return P;
 }
 
@@ -140,6 +152,13 @@ bool workspace_merge_pays(int units, int rounds) {
     const int s = std::min(rounds, kMaxSplits);
     const int tps_ws = 2 * ((rounds + s - 1) / s);
     return tps_cluster - tps_ws > kWsMergeTiles;
+}
+
+int most_workspace_splits(int units, int rounds) {
+    // no range of `r` rounds is cut into more than min(r, kMaxSplits)
+    for (int r = std::min(rounds, kMaxSplits); r > 0; --r)
+        if (workspace_merge_pays(units, r)) return std::min(rounds, kMaxSplits);
+    return 0;
 }
 
 }  // namespace kvd
@@ -161,14 +180,14 @@ extern "C" size_t kvd_workspace_size(kvd_op op, int32_t batch, int32_t n_q_heads
         // one query vector per KV head runs alone; two or more go in blocks of 16
         const int64_t M = (int64_t)rows_per_kv * (n_q_heads / n_kv_heads) * q;
         const int mmax = M >= 2 ? kMmaQueryBlock : 1;
-        const AttnPlan P1 = plan_attention(batch, n_q_heads, n_kv_heads, rows_per_kv, q, max_len,
-                                           mmax, 1, 1);
-        if (!workspace_merge_pays(P1.units, P1.rounds)) return KVD_WS_COUNTER_BYTES;
-        // The most splits a launch can use bounds every workspace plan (a grouped plan
-        // keeps kMaxGroups <= kMaxSplits partials per unit).
         const AttnPlan P = plan_attention(batch, n_q_heads, n_kv_heads, rows_per_kv, q, max_len,
-                                          mmax, kMaxSplits, 1);
-        return std::max<size_t>(P.ws_bytes, KVD_WS_COUNTER_BYTES);
+                                          mmax, 1, 1);
+        // A call attends over max_len or less (fixed_len, a window), and fewer rounds can take
+        // more splits: the most of all of them. (A grouped plan keeps kMaxGroups <= kMaxSplits
+        // partials per unit.)
+        const int splits = most_workspace_splits(P.units, P.rounds);
+        return splits ? workspace_layout((size_t)P.units * splits * P.msub).bytes
+                      : KVD_WS_COUNTER_BYTES;
     }
     case KVD_OP_Q4_ATTN:
         if (batch <= 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||

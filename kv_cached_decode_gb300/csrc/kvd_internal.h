@@ -112,6 +112,11 @@ AttnPlan plan_attention(int batch, int n_q_heads, int n_kv_heads, int rows_per_k
 // on the shape, so workspace sizing and the launcher agree.
 bool workspace_merge_pays(int units, int rounds);
 
+// The most splits per unit that a merge through the workspace has over any range of up to
+// `rounds` rounds; 0 where none pays. (Not monotone in the range: 118 rounds take 118 splits, 129
+// rounds, in twos, 65.)
+int most_workspace_splits(int units, int rounds);
+
 // The plan with `groups` clusters of at most `csize` splits per unit (the splits of the
 // plan for groups * csize blocks, padded to a multiple of `groups`: padding blocks have no
 // tiles). Their first CTAs merge through the workspace. It is considered only where

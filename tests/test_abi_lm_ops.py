@@ -255,3 +255,35 @@ def test_sample_form_on_small_rows():
     assert ref64.sample([-np.inf, np.nan], 0.5) == (-1, -np.inf, 0)
     tok, lp, n = ref64.sample(x, 0.99, top_k=3, top_p=0.9)
     assert tok == 3 and n == 3 and abs(lp - np.log(0.3 / 0.9)) < 1e-12
+
+
+@pytest.mark.parametrize("Hq,H,n", [(1, 1, 1), (2, 2, 1), (8, 1, 5), (20, 4, 1), (17, 1, 4)])
+def test_workspace_of_a_capacity_covers_every_window(lib, Hq, H, n):
+    """A call plans over what its window leaves of the capacity, and a shorter range can be cut
+    into more splits than a longer one: blocks take tiles in rounds of two, one round each up to
+    128 rounds and two each from 129 on. The reported size grows with the capacity and holds
+    the partials (64 values, a maximum and a sum) of every shorter range that is worth cutting."""
+    from kv_cached_decode_gb300 import (KVD_OP_DECODE_ATTN, KVD_OP_VERIFY_ATTN, KVD_OP_WINDOW_ATTN,
+                                        KVD_WS_COUNTER_BYTES, kvd_workspace_size)
+
+    M = Hq // H * n
+    nsub = -(-M // 16)
+    msub, units = -(-M // nsub), H * nsub
+
+    def need(L):
+        tiles = -(-L // 64)
+        rounds = -(-tiles // 2)
+        per = 2 * -(-rounds // min(rounds, 128))
+        if units > 8 or 2 * -(-rounds // 16) - per <= 12:
+            return KVD_WS_COUNTER_BYTES
+        slots = units * -(-tiles // per) * msub
+        return KVD_WS_COUNTER_BYTES + -(-slots * 64 * 4 // 256) * 256 + slots * 2 * 4
+
+    ops = [KVD_OP_WINDOW_ATTN, KVD_OP_VERIFY_ATTN] + [KVD_OP_DECODE_ATTN] * (n == 1)
+    most = 0
+    for L in range(64, 100000, 64):
+        most = max(most, need(L))
+        for op in ops:
+            assert kvd_workspace_size(op, 1, Hq, H, 1, n, L) >= most, L
+    # 16512 positions: 65 splits of four tiles; a window of 15000: 118 of two
+    assert need(15104) > need(16512) or units > 8

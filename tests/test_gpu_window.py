@@ -319,3 +319,14 @@ def test_a_wait_that_runs_out_is_reported(Hq, H, n):
     torch.cuda.synchronize()
     assert int(err) == 0
     _compare(out.cpu(), q, k, v, [L], L, 0)
+
+
+@pytest.mark.parametrize("Hq,H,n,cap,window", [(1, 1, 1, 16512, 15000), (2, 2, 1, 16512, 15000),
+                                               (8, 1, 5, 33000, 16200), (1, 1, 4, 70000, 15500)])
+def test_a_long_window_with_the_workspace_of_its_capacity(Hq, H, n, cap, window):
+    """Windows that are cut into more splits than the whole capacity would be, with a workspace of
+    exactly the reported size."""
+    lens = [cap]
+    q, k, v = _inputs(torch.float16, 1, Hq, H, n, cap, cap + n)
+    out = _run(q, k, v, lens, window, 3)
+    _compare(out, q, k, v, lens, window, 3)
