@@ -926,7 +926,9 @@ kvd_status run_q4(Q4AttnParams& p, const Q4Shape& sh, int64_t tiles, int nsm, vo
 
 size_t q4_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int qlen, int max_len) {
     const Q4Shape sh = q4_shape(batch, n_q_heads, n_kv_heads, qlen);
-    if (!q4_streams(sh, q4_tiles(max_len, qlen, 0, 0))) return KVD_WS_COUNTER_BYTES;
+    // (max_len may be any bound: beyond the longest range that streams, shorter ones still do)
+    const int64_t most = INT64_C(0x7fffffff) / std::max<int64_t>(sh.units, 1) - kUnitCost;
+    if (!q4_streams(sh, std::min(q4_tiles(max_len, qlen, 0, 0), most))) return KVD_WS_COUNTER_BYTES;
     return KVD_WS_COUNTER_BYTES + (size_t)2 * kMaxStream * sh.msub * kPart * sizeof(float);
 }
 

@@ -287,3 +287,16 @@ def test_workspace_of_a_capacity_covers_every_window(lib, Hq, H, n):
             assert kvd_workspace_size(op, 1, Hq, H, 1, n, L) >= most, L
     # 16512 positions: 65 splits of four tiles; a window of 15000: 118 of two
     assert need(15104) > need(16512) or units > 8
+
+
+def test_q4_workspace_of_a_loose_bound(lib):
+    """max_len may be any upper bound of the length: a looser one never gives less."""
+    from kv_cached_decode_gb300 import KVD_OP_Q4_ATTN, kvd_workspace_size
+
+    for B, Hq, H, n in ((1, 8, 8, 1), (16, 32, 8, 1), (64, 32, 8, 1), (80, 8, 8, 5), (81, 8, 8, 1)):
+        last = 0
+        for e in range(5, 31):
+            for L in (1 << e, (1 << e) + (1 << e - 1)):
+                size = kvd_workspace_size(KVD_OP_Q4_ATTN, B, Hq, H, 1, n, L)
+                assert size >= last, (B, L)
+                last = size
