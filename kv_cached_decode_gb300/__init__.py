@@ -221,6 +221,8 @@ def make_cache(k: torch.Tensor, v: torch.Tensor) -> Cache:
         raise ValueError("cache must be [batch, heads, capacity, 64] with the last axis contiguous")
     if not (k.is_cuda and v.is_cuda):
         raise ValueError("cache tensors must be CUDA tensors")
+    if k.get_device() != v.get_device():
+        raise ValueError("K and V must be on one device")
     B, H, cap, D = shape
     c = Cache(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], B, H, D, cap)
     c._tensors = (k, v)  # the struct holds raw pointers: keep the tensors alive with it

@@ -300,3 +300,19 @@ def test_q4_workspace_of_a_loose_bound(lib):
                 size = kvd_workspace_size(KVD_OP_Q4_ATTN, B, Hq, H, 1, n, L)
                 assert size >= last, (B, L)
                 last = size
+
+
+def test_a_cache_split_over_two_devices_is_refused():
+    """One address of the two would be another device's."""
+    from types import SimpleNamespace
+
+    import kv_cached_decode_gb300 as kvd
+
+    def fake(dev):
+        return SimpleNamespace(shape=torch.Size((1, 2, 5, 64)), stride=lambda: (640, 320, 64, 1),
+                               dtype=torch.float16, is_cuda=True, get_device=lambda: dev,
+                               data_ptr=lambda: P)
+
+    assert kvd.make_cache(fake(0), fake(0)).capacity == 5
+    with pytest.raises(ValueError, match="one device"):
+        kvd.make_cache(fake(0), fake(1))
