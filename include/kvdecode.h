@@ -514,6 +514,8 @@ kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache *cache, int32_t ba
  * Products run on the tensor cores with fp32 accumulation; the softmax is fp32. A weight enters
  * the second product times its row's step, rounded to binary16: off by 2^-11 of itself or by
  * 2^-32 of the largest such product among the rows that the query sees (steps from 2^-104 on).
+ * Both products' sums are cut, in units of n, at 2^-15 of the largest q, or the largest weight
+ * times step, of 16 neighbours: far below the format's half steps, but more than fp32 rounding.
  * What a query does not see, whatever it holds, changes no bit of its output. |scale * q| is
  * to stay below 2^100.
  * Flags: KVD_FLAG_PDL; KVD_FLAG_EARLY_KV gives what KVD_FLAG_PDL gives (nothing is read

@@ -52,14 +52,20 @@ def _compare(c, q, L, **kw):
       p s to binary16: half a step of 2^-11 of each row's share, below the normal range 2^-25
         where the largest p s of a row that is not zero stands at 2^7 or more: 2^-32 of it times
         |n - z|, for every row;
-      fp32: the scores (64 products, twice), and 16 roundings of 2^-22 in the sums over n and
-        over z, which are formed apart; the output's own rounding."""
+      the tensor cores add 16 products at a time, aligned by their factors' exponents, where n,
+        held as n 2^-24 (half of K's as n 2^-20), counts as 2^-14: every product is cut at 2^-15
+        of the largest other factor. For the output that is 16 times 2^-15 of the largest p s of
+        16 positions; for a score 32 times 2^-15 (and 32 times 2^-19) of the largest |q| times
+        the step of K;
+      fp32: the scores (64 products), and 16 roundings of 2^-22 in the sums over n and over z,
+        which are formed apart; the output's own rounding.
+    A score's error counts twice: in its weight and in their sum."""
     out = _run(c, q, L, **kw)
     kd, vd, par = [t[0, :, :L].cpu().numpy() for t in c._tensors]
     k, v = (ref64.q4_values(d, par[..., a:a + 2]) for d, a in ((kd, 0), (vd, 2)))
     ks, vs = (ref64.q4_values(d, par[..., a:a + 2], size=True) for d, a in ((kd, 0), (vd, 2)))
-    step = (np.ascontiguousarray(par[..., 2:3]).view(np.uint16).astype(np.uint32) << 16).view(
-        np.float32).astype(np.float64)
+    kstep, step = ((np.ascontiguousarray(par[..., a:a + 1]).view(np.uint16).astype(np.uint32) <<
+                    16).view(np.float32).astype(np.float64) for a in (0, 2))
     grid = np.abs(v) / step                       # |n - z|
     live = np.where((vs == 0).all(-1, keepdims=True), 0.0, step)
     _, n = q.shape[1:3]
@@ -78,8 +84,13 @@ def _compare(c, q, L, **kw):
             want = (p * v[h][at]).sum(0)
             mag, size = (p * np.abs(v[h][at])).sum(0), (p * vs[h][at]).sum(0)
             smax = (ks[h][at] @ np.abs(x)).max() * 0.125
-            floor = 2.0 ** -32 * (p * live[h][at]).max() * grid[h][at].sum(0)
-            tol = mag * (2.0 ** -11 + 2 * 72 * 2.0 ** -24 * smax) + size * 16 * 2.0 ** -22 + floor
+            ps = p * live[h][at]
+            floor = 2.0 ** -32 * ps.max() * grid[h][at].sum(0)
+            tops = [ps[at // 16 == j].max() for j in np.unique(at // 16)]
+            score = 72 * 2.0 ** -24 * smax + 34 * 2.0 ** -15 * (
+                np.abs(x).max() * 0.125 * kstep[h][at].max())
+            tol = (mag * (2.0 ** -11 + 2 * score) + size * 16 * 2.0 ** -22 + floor +
+                   16 * 2.0 ** -15 * sum(tops))
             tol = tol + half * (np.abs(want) + tol) + tiny
             off = np.abs(out[0, hq, i].double().cpu().numpy() - want)
             assert (off <= tol).all(), (hq, i, float((off / tol).max()), int((off > tol).sum()))
