@@ -26,8 +26,8 @@
  *    capacity, a parent outside its window, a draft id outside the vocabulary, a
  *    NaN logit, a sampling parameter out of range) are written to `*dev_err` with an
  *    atomic compare-and-swap from 0, so the first code wins; the offending unit of work
- *    is skipped, nothing traps and nothing spins. `dev_err` (device int32) may be NULL to ignore them. The caller
- *    reads and clears it when it chooses.
+ *    is skipped, nothing traps and nothing spins. `dev_err` (device int32) may be NULL to
+ *    ignore them. The caller reads and clears it when it chooses.
  *  - Layout: a per-layer cache is K, V : [batch, n_kv_heads, capacity, head_dim],
  *    head_dim contiguous ([N] "KV キャッシュが推論を最適化する方法": the per-layer key
  *    and value tensors are kept as (batch, heads, seq_len_cached, head_dim)). Other
@@ -400,6 +400,8 @@ kvd_status kvd_qk_norm_rope(kvd_dtype dtype, int32_t batch, int32_t n, const kvd
  * fused append, workspace (KVD_OP_WINDOW_ATTN), flags, errors; rows_per_kv is 1. Only the
  * 64-position tiles some query of the block sees are read, and what lies elsewhere in the
  * cache, infinities and NaN included, does not reach a query that does not see it.
+ * Weights are rounded to the storage type before they meet V (bf16: by 2^-8 of each; fp16: by
+ * 2^-11 of each or 2^-25 of the largest); their sum is taken before that.
  *
  * 1 <= qlen <= KVD_MAX_QLEN; window >= 1; n_sinks >= 0; out must not be q.
  */
@@ -416,7 +418,8 @@ kvd_status kvd_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads, in
  * Prompt token j, at position p = lens_in[b] + j, sees t <= p with t < n_sinks or
  * t > p - window; everything else is kvd_prefill_attn. window >= 1; n_sinks >= 0.
  * Cached positions that no token of the prompt sees do not reach the outputs, whatever
- * they hold.
+ * they hold. (An infinity or a NaN in V that some tokens see can make others' outputs NaN:
+ * their weight for it is 0, and 0 * inf is NaN.) Weights are rounded as kvd_window_attn's.
  */
 kvd_status kvd_prefill_window_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads,
                                    int32_t max_len, const void *q, const kvd_cache *kv,

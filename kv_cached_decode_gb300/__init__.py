@@ -655,7 +655,8 @@ def kvd_q4_attn(q, cache: Q4Cache, out, workspace=None, lens=None, fixed_len: in
                 flags: int = 0, dev_err=None, stream=None):
     """Attention of 1..16 query tokens per row over a 4-bit cache (the block's K/V already
     appended). ``window`` > 0: a sliding window with ``n_sinks`` sinks. workspace:
-    kvd_workspace_size(KVD_OP_Q4_ATTN, ...) bytes, used by a few long rows only."""
+    kvd_workspace_size(KVD_OP_Q4_ATTN, ...) bytes; calls with much work (many rows over a large
+    capacity) need it, for the others it may be None."""
     dev = _device_of(q, "q")
     (B, Hq, ql, _), qp, op = _query_shape(q, out, dev)
     ws, ws_bytes = _scratch(workspace, dev)

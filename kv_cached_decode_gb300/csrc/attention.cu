@@ -42,7 +42,7 @@
 //    queries can see: the tiles of the sinks, then those from the window's first position
 //    on; the splits share that list, and nothing between is read. Compiled into builds of
 //    their own (WINDOW), so the others keep their code. Measured, lengths past the window:
-//    32 rows x 20 heads, window 2047 (335 MB) 57.3 us, 5.9 TB/s; 8 rows x 8 heads, window 4096
+//    32 rows x 20 heads, window 2047 (335 MB) 57 to 59 us, 5.8 TB/s; 8 rows x 8 heads, window 4096
 //    (67 MB, in L2), 1, 4, 16 and 20 query vectors per head 12.7, 13.3, 14.9 and 16.5 us (the
 //    last in blocks of 32); 1 row x 4 heads, window 1024: 4.6 us, the chain of launch, tiles and
 //    merge.

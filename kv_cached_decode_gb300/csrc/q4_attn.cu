@@ -48,9 +48,10 @@
 //    wave takes an equal stretch of it, and units cut by a stretch's end merge through the
 //    workspace (last arrival): the longest row does not set the time.
 //
-// Measured: 16 rows x 8 heads (4 queries each), ragged to 32768 positions, 227 MB: 49.0 us, 4.6
-// TB/s, bound by the issue of about 300 instructions per tile; 16 rows of 65536 positions 112 us,
-// 5.4 TB/s. 1 row x 8 heads x 8192: 8.2 us, the chain of launch, first tile and merge.
+// Measured: 16 rows x 8 heads (4 queries each), ragged to 32768 positions, 227 MB: 49.0 to 49.6 us,
+// 4.6 TB/s, bound by the chain of a tile (about 300 instructions, four warps per scheduler: issue on
+// half of the cycles, DRAM 57 %, tensor cores 24 %); 16 rows of 65536 positions 112 us, 5.4 TB/s.
+// 1 row x 8 heads x 8192: 8.2 to 8.4 us, the chain of launch, first tile and merge.
 // Tried: 10 or 12 warps 59 and 57 us, 16 warps and one CTA per SM 52.7, three CTAs at 80
 // registers 57.3, 4-warp CTAs 58 to 64, 3 or 5 stages 51.1 and 52.0 (then 51.2); the next unit's
 // first tiles fetched before the last one's merge 52.5.

@@ -46,12 +46,13 @@
 // Exchanges are one cluster barrier each: 2, and 2 more for each of top-k and top-p. One more,
 // arrived at before the read and waited for after it, tells that all CTAs have started.
 //
-// Measured (logits normal, sigma 2.5 or 3): 1 row x 51865 ids, top-k 50 and top-p 11.6 us; 64
-// rows x 128000: min-p 20 us, top-p and min-p 37.5 us (of 70000 cycles 9500 read, 14500 weigh,
-// 13000 cut, the rest draws and waits), top-k 50 and top-p 39 us, no filter 42 us, top-p alone 76 us
-// (half of the ids are listed and weighed as heavy ones). Reading them once takes 4.9 us. Ranking
-// by one 64-bit key, a warp's neighbours sharing an entry, and up to 256 ids: top-p alone 97.7 ->
-// 76.5 us, one row of 128000 27.8 -> 19.5.
+// Measured (logits normal, sigma 2.5 or 3): 1 row x 51865 ids, top-k 50 and top-p 12 us; 64
+// rows x 128000: min-p 21 us, top-p and min-p 38 us (of 70000 cycles 9500 read, 14500 weigh,
+// 13000 cut, the rest draws and waits), top-k 50 and top-p 39.5 us, no filter 42 us, top-p 0.95
+// alone 56 to 79 us (half of the ids are listed and weighed as heavy ones, up to four times),
+// where more than 256 ids share a row's last bin another round of bins: up to 115, at top-p 0.99
+// 129 to 142. Reading them once takes 4.8 us. Ranking by one 64-bit key, a warp's neighbours
+// sharing an entry, and up to 256 ids: top-p 0.95 alone 97.7 -> 76.5 us on one set of logits.
 #include <algorithm>
 #include <climits>
 #include <cstddef>
@@ -1126,7 +1127,6 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
 constexpr int kMaxDevF = 64;
 constexpr size_t kSfSmem = sizeof(FilterShared);
 static_assert(2 * (kSfSmem + 1024) <= 227 * 1024, "two CTAs per SM");
-static_assert(kMaxSlice / kSfWarps <= 65536, "places in a segment are 16 bits");
 
 // Once per device: shared memory and clusters of 16; the largest usable cluster.
 int prepare_filtered() {
