@@ -515,8 +515,9 @@ kvd_status kvd_q4_dequant(kvd_dtype dtype, const kvd_q4_cache *cache, int32_t ba
  *          more than the counters' (many rows or long ones), under the rules of the other
  *          attention calls
  * Products run on the tensor cores with fp32 accumulation; the softmax is fp32. A weight enters
- * the second product times its row's step, rounded to binary16: off by 2^-11 of itself or by
- * 2^-32 of the largest such product among the rows that the query sees (steps from 2^-104 on).
+ * the second product times its row's step, rounded to binary16: off by 2^-11 of itself, by
+ * 2^-32 of the largest such product among the rows that the query sees, or by 2^-114 of the
+ * largest weight.
  * Both products' sums are cut, in units of n, at 2^-15 of the largest q, or the largest weight
  * times step, of 16 neighbours: far below the format's half steps, but more than fp32 rounding.
  * What a query does not see, whatever it holds, changes no bit of its output. |scale * q| is
@@ -610,7 +611,8 @@ kvd_status kvd_sample_accept(const float *target, const float *draft, const int3
  *   2. ends at the latest with the id at which the prefix's mass reaches top_p times the
  *      mass of what step 1 left                                    (top_p >= 1: all)
  *   3. has w_t >= min_p for every id                               (min_p <= 0: all)
- * and at least one id (with min_p > 1 that one: no w is above 1). Ids with logit -inf are never kept. Then, over the kept ids,
+ * and at least one id (with min_p > 1 that one: no w is above 1). Ids with logit -inf are never
+ * kept. Then, over the kept ids,
  *   token   = the smallest id whose running sum of w, in id order, exceeds u * sum(w)
  *             (the last kept id with w > 0 if rounding leaves none)
  *   logprob = log(w_token / sum(w))

@@ -32,12 +32,11 @@
 //    moves only when one nears 2^15 (or a w 2^96). So what a product loses below binary16's
 //    normal range is 2^-32 of the largest product, and neither rows the query does not see nor
 //    rows of little weight, whatever their steps, cost the others bits. Rows of zeros (n = z =
-//    0) add nothing and do not set C: their step is 1 however small V is. (V steps below
-//    2^-104 do lose bits: the largest w is 2^90 at most when C is set.) The zero points
-//    multiply the same rounded products, so their rounding is not amplified by n - z
-//    cancelling. Whether any may have to move is one vote per tile: the usual tile has no
-//    reduction across lanes at all. Each query then moves by what it sees itself, so its bits
-//    do not depend on others.
+//    0) add nothing and do not set C: their step is 1 however small V is. (Products below 2^-82
+//    of the largest w lose more: w is 2^90 at most when C is set.) The zero points multiply the
+//    same rounded products, so their rounding is not amplified by n - z cancelling. Whether any
+//    may have to move is one vote per tile: the usual tile has no reduction across lanes at all.
+//    Each query then moves by what it sees itself, so its bits do not depend on others.
 //  * Each warp streams its own tiles of 32 positions (2304 bytes with the parameters)
 //    through a ring of cp.async stages: no block barrier in the loop, and rows at or past
 //    the length are filled with zeros and never read.

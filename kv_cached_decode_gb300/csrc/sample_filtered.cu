@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     unsigned long long w_min = 0;
     if (by_w) {
         bool rest = false;
-        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;  // (1 at most here)
+        w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;
         w_min += rest ? 1 : 0;
     }
     const float y_max =
