@@ -615,7 +615,7 @@ kvd_status kvd_sample_accept(const float *target, const float *draft, const int3
  * kept. Then, over the kept ids,
  *   token   = the smallest id whose running sum of w, in id order, exceeds u * sum(w)
  *             (the last kept id with w > 0 if rounding leaves none)
- *   logprob = log(w_token / sum(w))
+ *   logprob = log(w_token / sum(w)), to fp32 rounding for an id of any weight
  * T = 0 takes the largest logit (kept: that id). Masses are integers in units of 2^-44 (the
  * largest w is 1; a w that can be kept is formed to 2^-29 of itself or to 2^-36, one that min-p
  * drops, of which step 2 needs the sum, to 2^-21 of itself): the same bits on every run and

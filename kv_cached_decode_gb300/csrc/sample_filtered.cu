@@ -219,14 +219,25 @@ struct Weights {
     __device__ __forceinline__ float lead(float x) const {
         return (x == m ? 0.f : m - x) * ch;
     }
-    // y < split
-    __device__ __forceinline__ unsigned long long heavy(float x) const {
+    // y = p + e
+    __device__ __forceinline__ void exact(float x, float& p, float& e) const {
         const float d = x == m ? 0.f : m - x;
-        const float p = d * ch;
+        p = d * ch;
         // m - x = d + dl exactly
         const float bb = d - m;
         const float dl = x == m ? 0.f : (m - (d - bb)) - (x + bb);
-        const float e = fmaf(d, ch, -p) + fmaf(d, cl, dl * ch);
+        e = fmaf(d, ch, -p) + fmaf(d, cl, dl * ch);
+    }
+    // (m - x) / T
+    __device__ __forceinline__ float nats(float x) const {
+        float p, e;
+        exact(x, p, e);
+        return fmaf(e, 0.693147181f, p * 0.693147181f);
+    }
+    // y < split
+    __device__ __forceinline__ unsigned long long heavy(float x) const {
+        float p, e;
+        exact(x, p, e);
         // k = p * 256 rounded, in the low bits of kf + 1.5 * 2^23
         const float ks = fmaf(p, 256.f, 12582912.f), kf = ks - 12582912.f;
         const float r = fmaf(kf, -0.00390625f, p) + e;  // the first part is exact; |r| <= 2^-9
@@ -673,10 +684,15 @@ __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float log_share(unsigned long long w, unsigned long long total) {
-    // near 1 from what is left over, which the integers know exactly
+// log of the share that the id with logit x and weight w has of `total`.
+__device__ __forceinline__ float log_share(const Weights& W, float x, unsigned long long w,
+                                           unsigned long long total) {
+    // near 1 from what is left over, which the integers know exactly; for a light id from its
+    // logit, as its weight is a number of few bits
     const float tf = (float)total;
-    return w > total / 2 ? log1pf(-((float)(total - w) / tf)) : logf((float)w / tf);
+    if (w > total / 2) return log1pf(-((float)(total - w) / tf));
+    if (W.lead(x) < kHeavy) return logf((float)w / tf);
+    return -W.nats(x) - logf(tf * 0x1p-44f);
 }
 
 // A short prefix, all in S.all: top-k, top-p, min-p and the draw by ranking every entry against
@@ -743,7 +759,7 @@ __device__ void draw_few(FilterShared& S, const Weights& W, const FilterParams& 
     }
     if (w > 0 && sh.part == 0 && (lost ? id == S.found : run < t && run + w >= t)) {
         p.token[b] = id;
-        if (p.logprob) p.logprob[b] = log_share(w, total);
+        if (p.logprob) p.logprob[b] = log_share(W, key_x(me.key), w, total);
         if (p.n_kept) p.n_kept[b] = (int32_t)cnt;
     }
 }
@@ -1119,7 +1135,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
     }
     if (token >= 0) {
         p.token[b] = R.lo + token;
-        if (p.logprob) p.logprob[b] = log_share(W.of(R.at(token)), total);
+        if (p.logprob) p.logprob[b] = log_share(W, R.at(token), W.of(R.at(token)), total);
         if (p.n_kept) p.n_kept[b] = (int32_t)(top_k > 0 ? min((uint32_t)top_k, cnt) : cnt);
     }
 }

@@ -208,3 +208,20 @@ def test_min_p_above_one_keeps_one_id(V):
     _, lp, n, _ = _draw(x, u, m=1.0)
     ties = (x == x.max(1, keepdim=True).values).sum(1).cpu().numpy()
     assert (ties >= 3).all() and (n == ties).all() and np.allclose(lp, -np.log(ties))
+
+
+@pytest.mark.parametrize("V", [600, 30000])
+@pytest.mark.parametrize("T", [0.3, 1.0, 7.0])
+def test_the_logprob_of_a_drawn_id_of_little_weight(V, T):
+    """u = 0 draws the first kept id, whatever its weight (2^-16 down to 2^-44 of the largest)."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn(24, V, generator=g, device="cuda") * T
+    x[:, V // 2] = x.max() + 3 * T
+    x[:, 0] = x[:, V // 2] - T * torch.linspace(11.2, 30.4, 24, device="cuda")
+    for kw in (dict(), dict(k=min(V - 1, 20000)), dict(k=100) if V == 600 else dict(p=1.0)):
+        _check(x, np.zeros(24), T=T, **kw)
+    few = torch.full((24, V), float("-inf"), device="cuda")
+    few[:, 0], few[:, 5:9] = x[:, 0], x[:, V // 2:V // 2 + 1]
+    _check(few, np.zeros(24), T=T, k=4)
+    _check(few, np.zeros(24), T=T, k=5)
+    _check(few, np.zeros(24), T=T)
