@@ -619,7 +619,8 @@ kvd_status kvd_sample_accept(const float *target, const float *draft, const int3
  * T = 0 takes the largest logit (kept: that id). Masses are integers in units of 2^-44 (the
  * largest w is 1; a w that can be kept is formed to 2^-29 of itself or to 2^-36, one that min-p
  * drops, of which step 2 needs the sum, to 2^-21 of itself): the same bits on every run and
- * batch.
+ * batch. An id whose w is below half a unit can be kept, but is not drawn. Step 3 compares to
+ * 2^-29 of w for min_p from 2^-14 on and logits with a 64-bit bound for less.
  *
  * logits      : device fp32, row r at logits + r * row_stride; vocab <= KVD_MAX_VOCAB;
  *               row_stride >= vocab. A NaN counts as -inf. With +inf logits those ids alone

@@ -132,7 +132,7 @@ struct alignas(16) FilterShared {
     unsigned long long red[kSfWarps];
     uint32_t red32[kSfWarps], red_b[kSfWarps];
     uint32_t n_list, n_all;
-    float cut_x;
+    float cut_x, min_x;
     int32_t cut_id;
     int32_t found;
     // places of the listed ids in their warp's segment, a segment's length apart
@@ -698,7 +698,8 @@ __device__ __forceinline__ float log_share(const Weights& W, float x, unsigned l
 // A short prefix, all in S.all: top-k, top-p, min-p and the draw by ranking every entry against
 // every other.
 __device__ void draw_few(FilterShared& S, const Weights& W, const FilterParams& p, int b,
-                         int top_k, float top_p, unsigned long long w_min, float y_max, float u) {
+                         int top_k, float top_p, unsigned long long w_min, float min_x, float y_max,
+                         float u) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = (int)S.n_all;
     const Share sh = share_of(n);
@@ -730,7 +731,7 @@ __device__ void draw_few(FilterShared& S, const Weights& W, const FilterParams& 
         if (target == 0) target = 1;
         in = in && mass < target;
     }
-    in = in && me.w >= w_min && W.lead(key_x(me.key)) <= y_max;
+    in = in && me.w >= w_min && W.lead(key_x(me.key)) <= y_max && key_x(me.key) >= min_x;
     const unsigned long long w = in ? me.w : 0ull;
     if (tid == 0) S.n_list = 0;  // (the entries are in S.all: it counts the kept ones)
     __syncthreads();
@@ -908,18 +909,19 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         W.cl = q < 3e38f ? __fdiv_rn(fmaf(-q, T, h) + l, T) : 0.f;
     }
 
-    // min-p: by the weight, or (where it is too small for the weight's unit) by y alone. Past
-    // y_max no id is kept (with room for y's rounding where the weight decides)
-    const bool by_w = min_p >= 0x1p-40f;
+    // min-p: by the weight of heavy ids, else (weights of fewer bits) by the least logit that
+    // passes, which one thread works out in 64 bits. Past y_max no id is kept (with room for y's
+    // rounding)
+    const bool by_w = !(min_p > 0.f && min_p < 0x1p-14f);
+    if (!by_w && tid == 0)
+        S.min_x = __double2float_ru((double)W.m + (double)T * log((double)min_p));
     unsigned long long w_min = 0;
-    if (by_w) {
+    if (by_w && min_p > 0.f) {
         bool rest = false;
         w_min = min_p < 1.f ? mul_floor(min_p, kOne, rest) : kOne;
         w_min += rest ? 1 : 0;
     }
-    const float y_max =
-        min_p > 0.f ? fmaf(-log2f(min_p), by_w ? 1.00001f : 1.f, by_w ? 1e-4f : 0.f)
-                    : INFINITY;
+    const float y_max = min_p > 0.f ? fmaf(-log2f(min_p), 1.00001f, 1e-4f) : INFINITY;
 
     // ---- 2. the heavy ids of this warp's segment; the light ones' mass ----
     // (a top-k that cuts leaves no light id, or all ids are looked at)
@@ -1021,7 +1023,8 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
         }
         if (r == kFew) {
             if (R.cluster > 1) cluster_arrive();  // this CTA has read the others' lists
-            if (R.rank == 0) draw_few(S, W, p, b, top_k, top_p, w_min, y_max, u);
+            if (R.rank == 0)
+                draw_few(S, W, p, b, top_k, top_p, w_min, by_w ? -INFINITY : S.min_x, y_max, u);
             if (R.cluster > 1) cluster_wait();  // the others have read this one's
             return;
         }
@@ -1039,6 +1042,7 @@ __global__ void __launch_bounds__(kSfThreads, 2) sample_filtered_kernel(const Fi
             select<true>(S, R, W, true, kept, 0ull, top_p, 0ull, w_min) == kCutHere)
             light = kSome;
     }
+    if (!by_w && S.min_x > kept.x) kept = Cut{S.min_x, INT_MAX};
     if (light == kLightAll && min_p > 0.f) light = y_max < W.split - 1.f ? kNone : kSome;
 
     // ---- 4. the kept ids' mass, per warp segment ----

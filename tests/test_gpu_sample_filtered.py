@@ -225,3 +225,27 @@ def test_the_logprob_of_a_drawn_id_of_little_weight(V, T):
     _check(few, np.zeros(24), T=T, k=4)
     _check(few, np.zeros(24), T=T, k=5)
     _check(few, np.zeros(24), T=T)
+
+
+@pytest.mark.parametrize("min_p", [1e-30, 1e-13, 2.0 ** -40, 1e-9, 1e-6, 2.0 ** -14 * 0.99, 2.0 ** -14,
+                                   0.02])
+@pytest.mark.parametrize("T", [0.3, 1.0, 40.0])
+def test_how_many_ids_pass_min_p(min_p, T):
+    """Thousands of logits within 1e-4 of the border, a few units of fp32 apart: the count is that
+    of 64 bits."""
+    V = 20000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    m = torch.tensor([0.0, 3.75, -700.0], dtype=torch.float64, device="cuda")[:, None]
+    edge = T * float(np.log(np.float64(np.float32(min_p))))
+    at = edge * (1 + 1e-4 * (2 * torch.rand(3, V, generator=g, device="cuda",
+                                            dtype=torch.float64) - 1))
+    x = (m + at).float()
+    x[:, 77] = m[:, 0].float()
+    u = np.array([0.01, 0.5, 0.9])
+    T = float(np.float32(T))
+    for kw in (dict(), dict(k=V - 5), dict(p=0.9999999), dict(k=100)):
+        _check(x, u, T=T, m=min_p, **kw)
+    few = torch.full((3, V), float("-inf"), device="cuda")
+    few[:, 50:150] = x[:, 50:150]
+    _check(few, u, T=T, m=min_p, k=99)
+    _check(few, u, T=T, m=min_p)
