@@ -381,8 +381,9 @@ typedef struct kvd_head_rows {
  *         The angle is exact modulo a turn (64-bit fixed point) at every position, where
  *         kvd_rope forms it in fp32: at far positions the two differ by kvd_rope's
  *         rounding of the angle, so encode all keys of a cache with the same one.
- * eps >= 0 and finite; eps 0 makes a row of zeros NaN. No device errors; dev_err is
- * accepted for symmetry.
+ * eps >= 0 and finite; eps 0 makes a row of zeros NaN. The squares are summed in fp32: values
+ * stay below 2^60 in size (and with eps 0 a row's largest above 2^-60). No device errors;
+ * dev_err is accepted for symmetry.
  */
 kvd_status kvd_qk_norm_rope(kvd_dtype dtype, int32_t batch, int32_t n, const kvd_head_rows *q,
                             const kvd_head_rows *k, const int32_t *pos0, float eps, float base,
