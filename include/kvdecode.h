@@ -76,15 +76,17 @@ typedef enum kvd_status {
     KVD_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed */
     /* device-side codes, written to *dev_err */
     KVD_ERR_LEN_OVERFLOW = 16, /* a length < 0 or > capacity (or lens + q > capacity) */
-    KVD_ERR_BAD_INDEX = 17,    /* a beam parent outside its window's block */
-    KVD_ERR_BAD_TOKEN = 18,    /* a draft id outside [0, vocab) */
+    KVD_ERR_BAD_INDEX = 17,    /* a beam parent outside its window's block, or a page
+                                  outside the pool */
+    KVD_ERR_BAD_TOKEN = 18,    /* a draft id or a given token outside [0, vocab) */
     KVD_ERR_NAN = 19,          /* a NaN among the logits */
     KVD_ERR_TIMEOUT = 20,      /* a bounded wait for a shared-memory copy gave up; the
                                   workspace counters may be left non-zero: re-zero them */
     KVD_ERR_BAD_PARAM = 21     /* a per-row sampling parameter out of range */
 } kvd_status;
 
-typedef enum kvd_dtype { KVD_F16 = 0, KVD_BF16 = 1 } kvd_dtype;
+/* KVD_F32: kvd_token_logprobs only */
+typedef enum kvd_dtype { KVD_F16 = 0, KVD_BF16 = 1, KVD_F32 = 2 } kvd_dtype;
 
 typedef enum kvd_op {
     KVD_OP_DECODE_ATTN = 0,
@@ -92,7 +94,8 @@ typedef enum kvd_op {
     KVD_OP_GREEDY_ACCEPT = 2,
     KVD_OP_SAMPLE_ACCEPT = 3,
     KVD_OP_WINDOW_ATTN = 4,
-    KVD_OP_Q4_ATTN = 5
+    KVD_OP_Q4_ATTN = 5,
+    KVD_OP_PAGED_ATTN = 6
 } kvd_op;
 
 enum {
@@ -121,6 +124,11 @@ enum {
 #define KVD_MAX_BEAM 8
 #define KVD_MAX_VOCAB 524288
 #define KVD_MAX_LAYERS_PER_CALL 64
+#define KVD_MIN_PAGE 8      /* positions per page of a paged cache: powers of two */
+#define KVD_MAX_PAGE 65536
+#define KVD_MAX_GROUP 128   /* query heads per KV head of kvd_paged_attn */
+#define KVD_MAX_GIVEN 16    /* given tokens per row of kvd_token_logprobs */
+#define KVD_MAX_TOP 32      /* alternatives per row of kvd_token_logprobs */
 
 /* The new tokens' K/V for a fused append inside an attention call. */
 typedef struct kvd_new_tokens {
@@ -534,6 +542,153 @@ kvd_status kvd_q4_attn(kvd_dtype dtype, int32_t batch, int32_t n_q_heads, int32_
                        float scale, void *out, void *workspace, size_t workspace_bytes,
                        uint32_t flags, int32_t *dev_err, kvd_stream_t stream);
 
+/* How the frequencies of a rotation are scaled for contexts longer than the trained one. */
+typedef enum kvd_rope_scaling {
+    KVD_ROPE_NONE = 0,
+    KVD_ROPE_LINEAR = 1,    /* t_i / factor                                              */
+    KVD_ROPE_BANDS = 2,     /* by turns over the trained length: fewer than `low` are    */
+                            /* divided by factor, more than `high` kept, blended between */
+    KVD_ROPE_RAMP = 3       /* the same, blended by a ramp over the pairs                */
+} kvd_rope_scaling;
+
+/* A rotation: which pairs of a head turn, and how fast. With t_i = base^(-2i/rot_dim), i <
+ * rot_dim/2, N = original_len, and s_i the part of a pair that keeps its frequency,
+ *   theta_i = t_i * (s_i + (1 - s_i) / factor)
+ *   BANDS: s_i = clamp((N t_i / 2 pi - low) / (high - low), 0, 1)
+ *   RAMP : s_i = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1), where pair(r) = rot_dim *
+ *          ln(N / (2 pi r)) / (2 ln base) turns r times over N positions, a = max(0,
+ *          floor(pair(high))), b = min(rot_dim - 1, ceil(pair(low)))
+ * Frequencies are formed in 64 bits, angles are exact modulo a turn to position * 2^-53. */
+typedef struct kvd_rope_spec {
+    float base;             /* > 0 (RAMP: > 1)                                            */
+    int32_t rot_dim;        /* dims 0 .. rot_dim-1 turn, the others are copied: 16, 32,   */
+                            /* 48 or 64                                                   */
+    int32_t interleaved;    /* 0: pairs (i, i + rot_dim/2); 1: pairs (2i, 2i + 1)         */
+    int32_t scaling;        /* kvd_rope_scaling                                           */
+    float factor;           /* > 0; not read for NONE                                     */
+    float low, high;        /* BANDS, RAMP: 0 < low < high                                */
+    int32_t original_len;   /* BANDS, RAMP: >= 1                                          */
+    float magnitude;        /* cos and sin are multiplied by it (1 for the plain form)    */
+} kvd_rope_spec;
+
+/*
+ * kvd_rope_scaled -- rotary encoding in the layouts and scalings of a kvd_rope_spec.
+ *
+ * Beside kvd_rope (halves, the whole head, no scaling, in place). With (a, b) the pair i at
+ * position p,
+ *   y[a] = magnitude * (x[a] cos(p theta_i) - x[b] sin(p theta_i))
+ *   y[b] = magnitude * (x[b] cos(p theta_i) + x[a] sin(p theta_i))
+ * fp32 arithmetic, one rounding to the storage type; dims from rot_dim on keep their bits.
+ *
+ * q, k  : as in kvd_qk_norm_rope (rows of any strides into contiguous [batch, n_heads, n, 64];
+ *         in place, too), weight NULL. Either may be NULL.
+ * pos0  : device int32 [batch] or NULL (0): token j of row b is at pos0[b] + j. Any value:
+ *         negative positions turn back.
+ * positions : device int32 [batch, n] or NULL; instead of pos0, a position of its own for
+ *         every token. Not both.
+ * Encode queries and keys of a cache with the same call: kvd_rope's angles are formed in fp32.
+ * No device errors; dev_err is accepted for symmetry.
+ */
+kvd_status kvd_rope_scaled(kvd_dtype dtype, int32_t batch, int32_t n, const kvd_head_rows *q,
+                           const kvd_head_rows *k, const int32_t *pos0, const int32_t *positions,
+                           const kvd_rope_spec *spec, uint32_t flags, int32_t *dev_err,
+                           kvd_stream_t stream);
+
+/*
+ * A layer's cache in pages of one pool, and the table that gives every sequence its pages.
+ *
+ * No counterpart on the pages. Position t of row b is slot t % page_size of page
+ * table[b, t / page_size]. Rows may share pages; entries past a row's last page are not read.
+ */
+typedef struct kvd_paged_cache {
+    void *k;                /* device, 16-byte aligned: n_pages pages of n_kv_heads x     */
+    void *v;                /* page_size rows of 64 values; the same layout               */
+    int64_t stride_p;       /* elements between consecutive pages,                        */
+    int64_t stride_h;       /* heads of a page                                            */
+    int64_t stride_t;       /* and positions of a page; multiples of 8, >= 64             */
+    int32_t n_pages;
+    int32_t n_kv_heads;
+    int32_t head_dim;       /* must be 64                                                 */
+    int32_t page_size;      /* a power of two, KVD_MIN_PAGE .. KVD_MAX_PAGE               */
+    const int32_t *table;   /* device int32 [batch, table_width]                          */
+    int64_t table_stride;   /* entries between consecutive rows of the table              */
+    int32_t table_width;    /* page_size * table_width <= 2^30: a row's capacity          */
+    int32_t batch;
+} kvd_paged_cache;
+
+/* Head rows of packed tokens: token t's row of head h starts at x + t*stride_t + h*stride_h. */
+typedef struct kvd_token_rows {
+    const void *x;          /* device, 16-byte aligned                                    */
+    int64_t stride_t;       /* strides in elements, >= 0 and multiples of 8: a view of a  */
+    int64_t stride_h;       /* fused projection is read where it is                       */
+    void *out;              /* device [n_tokens, n_heads, 64], contiguous; NULL where the */
+    int32_t n_heads;        /* call writes no rows of this tensor                         */
+} kvd_token_rows;
+
+/*
+ * A packed ragged batch. The new tokens of all rows stand one after the other: row b has tokens
+ * starts[b] .. starts[b+1]-1 (starts: device int32 [batch + 1], ascending), and n_b = starts[b+1]
+ * - starts[b] may be 0. Tokens before starts[0] and from starts[batch] on belong to no row: they
+ * are not read, and their output rows are left as they were. A row whose tokens are not within
+ * [0, n_tokens] is flagged KVD_ERR_LEN_OVERFLOW and skipped.
+ *
+ * kvd_paged_append -- write a packed batch's new K/V into a paged cache.
+ *
+ * As kvd_kv_append (kvd_kv_append_rope), for a kvd_paged_cache: with s = lens_in[b] + j,
+ *   slot (b, s) of K = k_new[starts[b] + j], rotated at s by `spec` (NULL: as it is)
+ *   slot (b, s) of V = v_new[starts[b] + j]                                 j < n_b
+ *   q->out[starts[b] + j] = q[starts[b] + j], rotated at s      (q != NULL)
+ *   lens_out[b] = lens_in[b] + n_b                              (lens_out != NULL)
+ *
+ * k_new, v_new : n_kv_heads heads, out NULL. q: NULL, or the queries of the same tokens; out may
+ *            equal x when x is contiguous; no other overlap.
+ * lens_in  : device int32 [batch]; lens_out: device int32 [batch] or NULL, not lens_in
+ * Slots written by one call are to be distinct: rows that append share no page they write to.
+ * Device errors: lens_in[b] < 0 or lens_in[b] + n_b > the capacity -> KVD_ERR_LEN_OVERFLOW, row b
+ * is not written, q->out neither, and lens_out[b] = lens_in[b]; a page outside [0, n_pages) ->
+ * KVD_ERR_BAD_INDEX, the token's K/V are not written.
+ */
+kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32_t n_tokens,
+                            const kvd_token_rows *k_new, const kvd_token_rows *v_new,
+                            const kvd_token_rows *q, const int32_t *starts,
+                            const int32_t *lens_in, int32_t *lens_out, const kvd_rope_spec *spec,
+                            uint32_t flags, int32_t *dev_err, kvd_stream_t stream);
+
+/*
+ * kvd_paged_attn -- the new tokens of a packed ragged batch attend over a paged cache.
+ *
+ * One call for sequences that decode one token, verify a block of drafts and run a chunk of
+ * their prompt. The new tokens' K/V are already appended (kvd_paged_append), so token j of row b
+ * sits at position p_j = lens[b] - n_b + j and
+ *   out[starts[b] + j, hq] = sum_{t <= p_j} softmax_t(scale * q[starts[b] + j, hq] . K_t) V_t
+ * over the slots (b, t) of KV head hq / (n_heads / n_kv_heads).
+ *
+ * q        : n_heads query heads (a multiple of n_kv_heads, at most KVD_MAX_GROUP times it); out
+ *            is the output, not x
+ * lens     : device int32 [batch], positions of the row with its new tokens (>= n_b); row b's
+ *            is not read when n_b is 0
+ * max_new  : an upper bound of n_b, >= 1 (a row above it is flagged); a tight one needs less
+ *            workspace
+ * workspace: kvd_workspace_size(KVD_OP_PAGED_ATTN, batch, n_heads, n_kv_heads, 1, max_new, ..)
+ *            bytes, under the rules of the other attention calls
+ * Q.K^T and P.V run on the tensor cores with fp32 accumulation. Weights are rounded to the storage
+ * type before they meet V, as kvd_window_attn's; their sum is taken before that. Positions from
+ * lens[b] on do not reach the outputs, whatever the pages hold there. (An infinity or a NaN in V
+ * of a new token can make the outputs of other new tokens of its row NaN: their weight for it is
+ * 0, and 0 * inf is NaN.)
+ * The same call gives the same bits on every run; how a row is split depends on the whole batch.
+ * Flags: KVD_FLAG_PDL; KVD_FLAG_EARLY_KV gives what KVD_FLAG_PDL gives. KVD_FLAG_TEST_STALL: the
+ * first tile of every thread block never completes (the call reports KVD_ERR_TIMEOUT).
+ * Device errors: lens[b] outside [n_b, capacity] or n_b > max_new -> KVD_ERR_LEN_OVERFLOW, the
+ * row's outputs are left as they are; a page outside [0, n_pages) -> KVD_ERR_BAD_INDEX, its
+ * positions count as rows of zeros.
+ */
+kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache *cache, int32_t n_tokens,
+                          int32_t max_new, const kvd_token_rows *q, const int32_t *starts,
+                          const int32_t *lens, float scale, void *workspace,
+                          size_t workspace_bytes, uint32_t flags, int32_t *dev_err,
+                          kvd_stream_t stream);
+
 /*
  * kvd_greedy_accept -- greedy verification of k draft tokens.
  *
@@ -643,6 +798,42 @@ kvd_status kvd_sample_filtered(const float *logits, int64_t row_stride, int32_t 
                                int32_t *dev_err, kvd_stream_t stream);
 
 /*
+ * kvd_token_logprobs -- log probabilities of given tokens, with their ranks, the row's entropy and
+ * its best alternatives.
+ *
+ * [W] "Inference 抽象と KV キャッシュ" (the decoder keeps the sum of the chosen tokens' log
+ * probabilities); ranks, entropy and alternatives have no counterpart on the pages. For a row x of
+ * logits (a sampled step, a scored prompt position) with y = x / T, Z = log sum exp(y):
+ *   logprob[r, i]     = y_t - Z for t = tokens[r, i]
+ *   rank[r, i]        = how many ids come before t in the order by logit, ties lower id first
+ *   entropy[r]        = - sum_v p_v log p_v, p = exp(y - Z)
+ *   lse[r]            = Z
+ *   top_id[r, j]      = the id in place j of that order; top_logprob[r, j] its log probability
+ *
+ * logits      : device, `dtype` KVD_F32, KVD_F16 or KVD_BF16, row r at logits + r * row_stride
+ *               elements, aligned to an element; row_stride >= vocab; vocab <= KVD_MAX_VOCAB
+ * temperature : device fp32 [rows] (> 0, finite) or NULL (1)
+ * tokens      : device int32 [rows, n_given], 0 <= n_given <= KVD_MAX_GIVEN (0: NULL); -1 marks a
+ *               slot without a token (logprob 0, rank -1)
+ * logprob, rank : device fp32 / int32 [rows, n_given] or NULL
+ * entropy, lse : device fp32 [rows] or NULL
+ * top_id, top_logprob : device int32 / fp32 [rows, n_top], 0 <= n_top <= KVD_MAX_TOP, or NULL
+ * Sums are fp32 relative to the largest logit, whose weight is counted apart, so a log probability
+ * near 0 keeps its relative precision. A NaN counts as -inf. With +inf logits those ids alone have
+ * mass. Ids with logit -inf are never listed (slots left over: -1, -inf). A row without any logit
+ * above -inf has Z = -inf, entropy 0, logprob -inf. The same bits on every run.
+ * Device errors: a NaN logit -> KVD_ERR_NAN; a token outside [-1, vocab) -> KVD_ERR_BAD_TOKEN
+ * (treated as -1); a temperature out of range -> KVD_ERR_BAD_PARAM, the row's outputs are left as
+ * they are. No workspace. rows <= 2^31 / 16.
+ */
+kvd_status kvd_token_logprobs(kvd_dtype dtype, const void *logits, int64_t row_stride,
+                              int32_t rows, int32_t vocab, const float *temperature,
+                              const int32_t *tokens, int32_t n_given, float *logprob,
+                              int32_t *rank, float *entropy, float *lse, int32_t n_top,
+                              int32_t *top_id, float *top_logprob, uint32_t flags,
+                              int32_t *dev_err, kvd_stream_t stream);
+
+/*
  * kvd_beam_reorder_kv -- reorder the self-attention caches of all layers.
  *
  * [W] "Inference 抽象と KV キャッシュ" (BeamSearchDecoder.update, rearrange_kv_cache):
@@ -721,6 +912,7 @@ kvd_status kvd_beam_select(const float *logits, int32_t windows, int32_t beam, i
  *   KVD_OP_SAMPLE_ACCEPT: batch, qlen = k, vocab
  *   KVD_OP_WINDOW_ATTN : batch, n_q_heads, n_kv_heads, qlen, max_len (rows_per_kv 1)
  *   KVD_OP_Q4_ATTN     : the same
+ *   KVD_OP_PAGED_ATTN  : n_q_heads, n_kv_heads, qlen = max_new
  * max_len is an upper bound of the attended length (the capacity, or fixed_len).
  * Returns 0 for invalid arguments.
  */

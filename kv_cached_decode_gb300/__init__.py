@@ -11,8 +11,10 @@ the last axis contiguous; queries/outputs are contiguous ``[batch, n_q_heads, ql
 lengths, drafts, parents and outputs of ``kvd_greedy_accept`` are int32 CUDA tensors;
 logits are contiguous fp32 ``[batch, k+1, vocab]`` (``kvd_greedy_accept``) or
 ``[windows*beam, vocab]`` (``kvd_beam_select``). ``kvd_qk_norm_rope`` reads strided head
-rows and ``kvd_sample_filtered`` strided logit rows. A 4-bit cache is a ``Q4Cache`` over
-``[batch, n_kv_heads, capacity, 32]`` uint8 data and ``[..., 4]`` int16 parameters.
+rows, ``kvd_sample_filtered`` and ``kvd_token_logprobs`` strided logit rows. A 4-bit cache is a
+``Q4Cache`` over ``[batch, n_kv_heads, capacity, 32]`` uint8 data and ``[..., 4]`` int16
+parameters. A paged cache is a ``PagedCache`` over ``[n_pages, n_kv_heads, page_size, 64]`` pools
+(of any strides) and an int32 table; its calls take packed tokens ``[n_tokens, heads, 64]``.
 """
 
 from __future__ import annotations
@@ -31,9 +33,10 @@ STATUS_NAMES = {0: "KVD_OK", 1: "KVD_ERR_INVALID_ARG", 2: "KVD_ERR_UNSUPPORTED",
                 3: "KVD_ERR_WORKSPACE", 4: "KVD_ERR_CUDA", 16: "KVD_ERR_LEN_OVERFLOW",
                 17: "KVD_ERR_BAD_INDEX", 18: "KVD_ERR_BAD_TOKEN", 19: "KVD_ERR_NAN",
                 20: "KVD_ERR_TIMEOUT", 21: "KVD_ERR_BAD_PARAM"}
-KVD_F16, KVD_BF16 = 0, 1
+KVD_F16, KVD_BF16, KVD_F32 = 0, 1, 2
 KVD_OP_DECODE_ATTN, KVD_OP_VERIFY_ATTN, KVD_OP_GREEDY_ACCEPT, KVD_OP_SAMPLE_ACCEPT = 0, 1, 2, 3
-KVD_OP_WINDOW_ATTN, KVD_OP_Q4_ATTN = 4, 5
+KVD_OP_WINDOW_ATTN, KVD_OP_Q4_ATTN, KVD_OP_PAGED_ATTN = 4, 5, 6
+KVD_ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "ramp": 3}
 KVD_FLAG_PDL, KVD_FLAG_EARLY_KV = 1, 2
 KVD_FLAG_TEST_STALL = 1 << 8  # test only: see include/kvdecode.h
 KVD_WS_COUNTER_BYTES = 65536
@@ -44,7 +47,8 @@ EXPORTED = ("kvd_kv_append", "kvd_decode_attn", "kvd_verify_attn", "kvd_greedy_a
             "kvd_decode_attn_noalloc", "kvd_prefill_attn", "kvd_rope", "kvd_beam_select",
             "kvd_kv_append_rope", "kvd_sample_accept", "kvd_noalloc_test_fill_counters",
             "kvd_qk_norm_rope", "kvd_window_attn", "kvd_prefill_window_attn", "kvd_q4_append",
-            "kvd_q4_dequant", "kvd_q4_attn", "kvd_sample_filtered")
+            "kvd_q4_dequant", "kvd_q4_attn", "kvd_sample_filtered", "kvd_rope_scaled",
+            "kvd_paged_append", "kvd_paged_attn", "kvd_token_logprobs")
 
 
 class KvdError(RuntimeError):
@@ -88,6 +92,34 @@ class Q4Cache(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32)]
 
 
+class RopeSpec(ctypes.Structure):
+    """Mirror of ``kvd_rope_spec``: which pairs of a head turn, and how fast."""
+
+    _fields_ = [("base", ctypes.c_float), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("low", ctypes.c_float), ("high", ctypes.c_float),
+                ("original_len", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class PagedCache(ctypes.Structure):
+    """Mirror of ``kvd_paged_cache``: one layer's pools of pages and the page table."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stride_p", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_width", ctypes.c_int32), ("batch", ctypes.c_int32)]
+
+
+class TokenRows(ctypes.Structure):
+    """Mirror of ``kvd_token_rows``: head rows of packed tokens."""
+
+    _fields_ = [("x", ctypes.c_void_p), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("n_heads", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -110,6 +142,9 @@ def load_library(path: str = LIB_PATH):
         CP = ctypes.POINTER(Cache)
         NP = ctypes.POINTER(NewTokens)
         QP = ctypes.POINTER(Q4Cache)
+        HP, RP = ctypes.POINTER(HeadRows), ctypes.POINTER(RopeSpec)
+        GP, TP = ctypes.POINTER(PagedCache), ctypes.POINTER(TokenRows)
+        I64 = ctypes.c_int64
         sig = {
             "kvd_kv_append": [I32, CP, I32, I32, P, P, P, P, U32, P, P],
             "kvd_decode_attn": [I32, I32, I32, P, CP, P, I32, NP, I32, F, P, P, SZ, U32, P, P],
@@ -137,6 +172,11 @@ def load_library(path: str = LIB_PATH):
                             P, P],
             "kvd_sample_filtered": [P, ctypes.c_int64, I32, I32, P, P, P, P, P, P, P, P, U32,
                                     P, P],
+            "kvd_rope_scaled": [I32, I32, I32, HP, HP, P, P, RP, U32, P, P],
+            "kvd_paged_append": [I32, GP, I32, TP, TP, TP, P, P, P, RP, U32, P, P],
+            "kvd_paged_attn": [I32, GP, I32, I32, TP, P, P, F, P, SZ, U32, P, P],
+            "kvd_token_logprobs": [I32, P, I64, I32, I32, P, P, I32, P, P, P, P, I32, P, P, U32,
+                                   P, P],
             "kvd_workspace_size": [I32, I32, I32, I32, I32, I32, I32, I32],
             "kvd_status_string": [I32],
             "kvd_version": [],
@@ -686,3 +726,178 @@ def kvd_sample_filtered(logits, u, token, temperature=None, top_k=None, top_p=No
         _at(token, _I32, b, "token", dev), _at(logprob, _F32, b, "logprob", dev),
         _at(n_kept, _I32, b, "n_kept", dev), flags, _at(dev_err, _I32, None, "dev_err", dev),
         _on(stream, dev)), "kvd_sample_filtered")
+
+
+def make_rope(base: float = 10000.0, rot_dim: int = HEAD_DIM, interleaved: bool = False,
+              scaling: str = "none", factor: float = 1.0, original_len: int = 0,
+              low: float = 1.0, high: float = 1.0, magnitude: float = 1.0) -> RopeSpec:
+    """A rotation: pairs ``(i, i + rot_dim/2)`` or, interleaved, ``(2i, 2i + 1)`` of a head's
+    first ``rot_dim`` dims (16, 32, 48 or 64). ``scaling``: ``"none"``; ``"linear"`` divides the
+    frequencies by ``factor``; ``"bands"`` and ``"ramp"`` divide those that turn fewer than
+    ``low`` times over ``original_len`` positions, keep those that turn more than ``high`` times
+    and blend between, by turns or by pairs. ``magnitude`` multiplies cos and sin."""
+    if scaling not in KVD_ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(KVD_ROPE_SCALINGS)}")
+    return RopeSpec(base, rot_dim, int(bool(interleaved)), KVD_ROPE_SCALINGS[scaling], factor, low,
+                    high, original_len, magnitude)
+
+
+def _spec(rope):
+    if not isinstance(rope, RopeSpec):
+        raise TypeError("rope must be a RopeSpec (make_rope)")
+    return ctypes.byref(rope)
+
+
+def kvd_rope_scaled(q=None, k=None, q_out=None, k_out=None, rope: RopeSpec = None, pos0=None,
+                    positions=None, flags: int = 0, dev_err=None, stream=None):
+    """Rotary encoding by ``rope`` (make_rope) of ``q [batch, n_q_heads, n, 64]`` and/or ``k
+    [batch, n_k_heads, n, 64]`` of any strides into contiguous ``q_out`` / ``k_out`` (``q`` and
+    ``k`` themselves when contiguous). Token j of row b is at ``pos0[b] + j``, or at
+    ``positions[b, j]``."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k is needed")
+    if ref.dim() != 4:
+        raise ValueError("q and k must be [batch, heads, n, 64]")
+    dev = _device_of(ref, "q" if q is not None else "k")
+    B, _, n, _ = ref.shape
+    if q is not None and k is not None and (k.shape[0] != B or k.shape[2] != n):
+        raise ValueError("q and k must share batch and n")
+    if (q is not None and q_out is None) or (k is not None and k_out is None):
+        raise ValueError("q_out (k_out) is needed with q (k)")
+    rq = _head_rows(q, q_out, None, ref.dtype, n, "q", dev)
+    rk = _head_rows(k, k_out, None, ref.dtype, n, "k", dev)
+    _check(load_library().kvd_rope_scaled(
+        _dtype_code(ref), B, n, None if rq is None else ctypes.byref(rq),
+        None if rk is None else ctypes.byref(rk), _at(pos0, _I32, (B,), "pos0", dev),
+        _at(positions, _I32, (B, n), "positions", dev), _spec(rope), flags,
+        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_rope_scaled")
+
+
+def make_paged_cache(k: torch.Tensor, v: torch.Tensor, table: torch.Tensor) -> PagedCache:
+    """Describe one layer's pools ``[n_pages, n_kv_heads, page_size, 64]`` (a pool laid out
+    ``[n_pages, page_size, n_kv_heads, 64]`` as its ``transpose(1, 2)``) and the int32 page table
+    ``[batch, width]`` for the C ABI."""
+    shape, st = k.shape, k.stride()
+    if shape != v.shape or st != v.stride() or k.dtype != v.dtype:
+        raise ValueError("K and V must share shape, strides and dtype")
+    if len(shape) != 4 or shape[3] != HEAD_DIM or st[3] != 1:
+        raise ValueError("pools must be [n_pages, n_kv_heads, page_size, 64] with the last axis "
+                         "contiguous")
+    if table.dtype != _I32:
+        raise TypeError(f"table must be {_I32}, got {table.dtype}")
+    if table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be [batch, width] with contiguous rows")
+    dev = k.get_device()
+    if dev < 0 or v.get_device() != dev or table.get_device() != dev:
+        raise ValueError("pools and table must be CUDA tensors on one device")
+    pages, H, ps, D = shape
+    B, width = table.shape
+    # (the stride of an axis of size 1 is arbitrary and never used)
+    c = PagedCache(k.data_ptr(), v.data_ptr(), st[0] if pages > 1 else H * ps * D,
+                   st[1] if H > 1 else ps * D, st[2], pages, H, D, ps, table.data_ptr(),
+                   table.stride(0) if B > 1 else width, width, B)
+    c._tensors = (k, v, table)  # the struct holds raw pointers: keep the tensors alive with it
+    return c
+
+
+def _token_rows(x, out, dtype, what, dev, heads=None):
+    """Packed tokens' head rows ``[n_tokens, heads, 64]`` of any strides."""
+    if x.get_device() != dev:
+        raise ValueError(f"{what} must be on the current device (cuda:{dev})")
+    if x.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {x.dtype}")
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or st[2] != 1 or (
+            heads is not None and shape[1] != heads):
+        raise ValueError(f"{what} must be [n_tokens, {heads or 'heads'}, 64] with the last axis "
+                         "contiguous")
+    T, H = shape[0], shape[1]
+    return TokenRows(x.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0,
+                     _at(out, dtype, tuple(shape), what + "_out", dev), H)
+
+
+def kvd_paged_append(cache: PagedCache, k_new, v_new, starts, lens_in, lens_out=None, q=None,
+                     q_out=None, rope: RopeSpec = None, flags: int = 0, dev_err=None,
+                     stream=None):
+    """Write packed new tokens ``k_new``, ``v_new`` ``[n_tokens, n_kv_heads, 64]`` (of any
+    strides) to the pages of their rows: row b has tokens ``starts[b] .. starts[b + 1] - 1`` and
+    ``lens_in[b]`` positions before them. With ``rope`` the keys, and ``q [n_tokens, n_q_heads,
+    64]`` into ``q_out``, are rotated at their positions."""
+    dev = _device_of(k_new, "k_new")
+    dt, B, H = k_new.dtype, cache.batch, cache.n_kv_heads
+    rk = _token_rows(k_new, None, dt, "k_new", dev, H)
+    rv = _token_rows(v_new, None, dt, "v_new", dev, H)
+    T = k_new.shape[0]
+    if v_new.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("k_new, v_new and q must share n_tokens")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    rq = None if q is None else _token_rows(q, q_out, dt, "q", dev)
+    if starts is None or lens_in is None:
+        raise ValueError("starts and lens_in are needed")
+    _check(load_library().kvd_paged_append(
+        _dtype_code(k_new), _cache_on(cache, dev, dt), T, ctypes.byref(rk), ctypes.byref(rv),
+        None if rq is None else ctypes.byref(rq), _at(starts, _I32, (B + 1,), "starts", dev),
+        _at(lens_in, _I32, (B,), "lens_in", dev), _at(lens_out, _I32, (B,), "lens_out", dev),
+        None if rope is None else _spec(rope), flags, _at(dev_err, _I32, None, "dev_err", dev),
+        _on(stream, dev)), "kvd_paged_append")
+
+
+def kvd_paged_attn(q, cache: PagedCache, out, workspace, starts, lens, max_new: int = None,
+                   scale: float = 0.125, flags: int = 0, dev_err=None, stream=None):
+    """Causal attention of packed new tokens ``q [n_tokens, n_q_heads, 64]`` (of any strides)
+    over a paged cache that holds their K/V already: row b's tokens are ``starts[b] .. starts[b +
+    1] - 1``, the last of its ``lens[b]`` positions. ``max_new``: an upper bound of a row's new
+    tokens (default: n_tokens). workspace: kvd_workspace_size(KVD_OP_PAGED_ATTN, batch,
+    n_q_heads, n_kv_heads, qlen=max_new) bytes."""
+    dev = _device_of(q, "q")
+    B = cache.batch
+    if out is None or starts is None or lens is None:
+        raise ValueError("out, starts and lens are needed")
+    rq = _token_rows(q, out, q.dtype, "q", dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    T = q.shape[0]
+    _check(load_library().kvd_paged_attn(
+        _dtype_code(q), _cache_on(cache, dev, q.dtype), T, max(T, 1) if max_new is None else max_new,
+        ctypes.byref(rq), _at(starts, _I32, (B + 1,), "starts", dev),
+        _at(lens, _I32, (B,), "lens", dev), scale, ws, ws_bytes, flags,
+        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_paged_attn")
+
+
+_LOGIT_TYPES = {torch.float16: KVD_F16, torch.bfloat16: KVD_BF16, torch.float32: KVD_F32}
+
+
+def kvd_token_logprobs(logits, tokens=None, logprob=None, rank=None, entropy=None, lse=None,
+                       top_id=None, top_logprob=None, temperature=None, flags: int = 0,
+                       dev_err=None, stream=None):
+    """Log probabilities (``logprob``) and ranks of ``tokens [rows, n]`` (-1: none), the entropy
+    and log-sum-exp of every row of ``logits [rows, vocab]`` (fp32, fp16 or bf16; rows may be
+    strided), and its best ``top_id`` / ``top_logprob [rows, n_top]``, after ``temperature
+    [rows]``. Outputs that are None are not written."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, vocab] with contiguous rows")
+    if logits.dtype not in _LOGIT_TYPES:
+        raise TypeError(f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
+    dev = _device_of(logits, "logits")
+    R, V = logits.shape
+    if tokens is None:
+        if logprob is not None or rank is not None:
+            raise ValueError("logprob and rank need tokens")
+        n = 0
+    else:
+        if tokens.dim() != 2:
+            raise ValueError("tokens must be [rows, n]")
+        n = tokens.shape[1]
+    top = top_id if top_id is not None else top_logprob
+    if top is not None and top.dim() != 2:
+        raise ValueError("top_id and top_logprob must be [rows, n_top]")
+    k = 0 if top is None else top.shape[1]
+    _check(load_library().kvd_token_logprobs(
+        _LOGIT_TYPES[logits.dtype], logits.data_ptr(), logits.stride(0) if R > 1 else V, R, V,
+        _at(temperature, _F32, (R,), "temperature", dev), _at(tokens, _I32, (R, n), "tokens", dev),
+        n, _at(logprob, _F32, (R, n), "logprob", dev), _at(rank, _I32, (R, n), "rank", dev),
+        _at(entropy, _F32, (R,), "entropy", dev), _at(lse, _F32, (R,), "lse", dev), k,
+        _at(top_id, _I32, (R, k), "top_id", dev),
+        _at(top_logprob, _F32, (R, k), "top_logprob", dev), flags,
+        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_token_logprobs")

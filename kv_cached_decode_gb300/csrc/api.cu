@@ -95,6 +95,19 @@ kvd_status encode_rows_map(CUtensorMap* map, kvd_dtype dtype, void* base, int ro
     return r == CUDA_SUCCESS ? KVD_OK : KVD_ERR_INVALID_ARG;
 }
 
+kvd_status encode_pool_map(CUtensorMap* map, kvd_dtype dtype, void* base,
+                           const kvd_paged_cache* pool) {
+    kvd_cache c = {};
+    c.head_dim = KVD_HEAD_DIM;
+    c.capacity = pool->page_size;
+    c.n_kv_heads = pool->n_kv_heads;
+    c.batch = pool->n_pages;
+    c.stride_t = pool->stride_t;
+    c.stride_h = pool->stride_h;
+    c.stride_b = pool->stride_p;
+    return encode_cache_map(map, dtype, base, &c);
+}
+
 kvd_status validate_cache(const kvd_cache* c) {
     if (!c || !c->k || !c->v) return KVD_ERR_INVALID_ARG;
     if (c->head_dim != KVD_HEAD_DIM) return KVD_ERR_UNSUPPORTED;
@@ -194,6 +207,11 @@ extern "C" size_t kvd_workspace_size(kvd_op op, int32_t batch, int32_t n_q_heads
             qlen < 1 || qlen > KVD_MAX_QLEN || max_len < 0)
             return 0;
         return q4_workspace_bytes(batch, n_q_heads, n_kv_heads, qlen, max_len);
+    case KVD_OP_PAGED_ATTN:
+        if (n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
+            n_q_heads / n_kv_heads > KVD_MAX_GROUP || qlen < 1)
+            return 0;
+        return paged_workspace_bytes(n_q_heads, n_kv_heads, qlen);
     case KVD_OP_GREEDY_ACCEPT: {
         if (batch <= 0 || qlen < 1 || qlen > KVD_MAX_QLEN || vocab <= 0) return 0;
         return accept_workspace_bytes(batch, qlen, vocab, kWsTargetBound);
@@ -214,8 +232,8 @@ extern "C" const char* kvd_status_string(kvd_status s) {
     case KVD_ERR_WORKSPACE: return "KVD_ERR_WORKSPACE: workspace missing or too small";
     case KVD_ERR_CUDA: return "KVD_ERR_CUDA: CUDA call failed";
     case KVD_ERR_LEN_OVERFLOW: return "KVD_ERR_LEN_OVERFLOW: length outside [0, capacity]";
-    case KVD_ERR_BAD_INDEX: return "KVD_ERR_BAD_INDEX: beam parent outside its window";
-    case KVD_ERR_BAD_TOKEN: return "KVD_ERR_BAD_TOKEN: draft id outside the vocabulary";
+    case KVD_ERR_BAD_INDEX: return "KVD_ERR_BAD_INDEX: beam parent outside its window, or page outside the pool";
+    case KVD_ERR_BAD_TOKEN: return "KVD_ERR_BAD_TOKEN: token id outside the vocabulary";
     case KVD_ERR_NAN: return "KVD_ERR_NAN: NaN in the logits";
     case KVD_ERR_TIMEOUT: return "KVD_ERR_TIMEOUT: a bounded device wait gave up";
     case KVD_ERR_BAD_PARAM: return "KVD_ERR_BAD_PARAM: sampling parameter out of range";

@@ -27,6 +27,15 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 kvd_status validate_cache(const kvd_cache* c);
 kvd_status validate_q4_cache(const kvd_q4_cache* c);
+kvd_status validate_paged_cache(const kvd_paged_cache* c);   // paged_append.cu
+kvd_status validate_token_rows(const kvd_token_rows* r);
+
+// 4-D TMA descriptor over one pool of a paged cache: dims (64, page_size, heads, pages), box (64
+// dims, min(64, page_size) positions, 1, 1), 128-byte swizzle, zero fill out of range.
+kvd_status encode_pool_map(CUtensorMap* map, kvd_dtype dtype, void* base, const kvd_paged_cache* c);
+
+// Workspace bytes of kvd_paged_attn (paged_attn.cu).
+size_t paged_workspace_bytes(int n_q_heads, int n_kv_heads, int max_new);
 
 // Workspace bytes of kvd_q4_attn for an attended length of at most max_len (q4_attn.cu).
 size_t q4_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int qlen, int max_len);

@@ -1,0 +1,958 @@
+// paged_attn.cu -- the new tokens of a packed ragged batch attend over a paged cache.
+//
+// No counterpart on the pages: a server's batch holds sequences that decode one token, verify a
+// block of drafts and run a chunk of their prompt. Row b has n new tokens, the last n of len
+// positions; query head hq of token j sees position t <= len - n + j of KV head hq / g:
+//   out[j, hq] = sum_t softmax_t(scale * q[j, hq] . K_t) V_t
+//
+// Design.
+//  * A unit is one row, KV head and block of up to 128 query vectors: 128 / g tokens times the g
+//    query heads that share the KV head, so K and V are read once for all of them. Its products
+//    run on the fifth-generation tensor cores as in prefill.cu: S = Q.K^T (M 128, N 64, K 64) and
+//    O += P.V, accumulators and P in tensor memory, Q, K, V in 128-byte-swizzled shared memory.
+//  * Six warps: four hold the rows (thread t: tensor-memory lane t), one issues the MMAs, one
+//    copies K/V tiles of 64 positions through a ring of slots. Pages of fewer than 64 positions
+//    are one TMA box each, a lane of the copying warp per page; its page numbers are read a tile
+//    ahead. Boxes from the unit's last visible position on are not read.
+//  * Units of at most 32 (64) vectors hold them four (two) times, in lanes 32 (64) apart, and each
+//    copy takes the softmax of a quarter (half) of a tile's positions, with P zero elsewhere: a
+//    decoding sequence, with 4 query vectors, uses all four warps. The copies are merged at the
+//    unit's end. The products cost the same: 256 of the about 700 cycles that a tile takes to
+//    arrive at HBM's rate.
+//  * Work. The tiles of all units form one list, by weight, and every CTA of one wave takes an
+//    equal stretch of it; units cut by a stretch's end merge through the workspace, the last CTA
+//    to arrive in the order of the list. So neither one long row nor few rows leave SMs idle, and
+//    the tiles of decoding rows (HBM) and of prompt chunks (softmax) run at the same time. The
+//    copying warp runs ahead into the CTA's next unit.
+//  * A softmax row's reference moves only when its maximum grows by more than 2^8.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include "kvd_paged.cuh"
+#include "kvd_tc.cuh"
+
+namespace kvd {
+namespace {
+
+constexpr int kRowThreads = 128;               // the softmax warps
+constexpr int kPgThreads = kRowThreads + 64;   // + the MMA warp and the copying warp
+constexpr int kPgRows = 128;                   // query vectors per unit
+constexpr int kPgSlots = 5;                    // K/V tile pairs in flight
+constexpr int kPgMinBlocks = 2;                // blocks per SM the sizes below are chosen for
+// tensor memory: two S buffers (64 fp32 columns each), O (64), two P buffers (32 columns each)
+constexpr uint32_t kPgColsO = 2 * kTile;
+constexpr uint32_t kPgColsP = kPgColsO + kHeadDim;
+constexpr uint32_t kPgCols = 256;
+static_assert(kPgCols >= kPgColsP + 2 * (kTile / 2) && kPgMinBlocks * kPgCols <= 512,
+              "the resident blocks' tensor memory");
+constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
+constexpr uint32_t kPgSmem = 2 * kPgSlots * kTileBytes + kPgQBytes + 256 + kPgRows * 8 + 1024;
+constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
+
+// The list's weights: a tile of a unit with more than 64 vectors (bound by the softmax) and with
+// at most 64 (bound by the copies), and what a unit costs besides.
+constexpr uint32_t kHeavy = 3, kLight = 2, kUnit = 24;
+constexpr uint32_t kSnap = 8;       // no cut this close to a unit's ends
+constexpr uint32_t kLeast = 12;     // a CTA's least share
+constexpr int kMaxCtas = 512;
+
+struct PagedParams {
+    const uint8_t* q;
+    int64_t q_st, q_sh;       // bytes
+    void* out;                // [n_tokens, n_q_heads, 64]
+    const int32_t* starts;
+    const int32_t* lens;
+    const int32_t* table;
+    int64_t table_stride;
+    int32_t batch, n_tokens, max_new, capacity;
+    int32_t n_q_heads, n_kv_heads, group, tq;  // tq: tokens per unit
+    int32_t n_pages, page_log2, box_rows, boxes;  // boxes per tile
+    float scale_log2;
+    float* ws_part;           // [2 CTAs][slot_rows][64]
+    float2* ws_ml;            // [2 CTAs][slot_rows]: reference, sum
+    int32_t* ws_cnt;          // a ticket per CTA that holds the first piece of a cut unit
+    int32_t slot_rows;
+    int32_t* dev_err;
+    int32_t test_stall;
+};
+
+// ---------------------------------------------------------------- the list of tiles --
+struct Row {
+    int s, n, len;  // first packed token, new tokens (0: nothing to do), positions
+};
+__device__ __forceinline__ Row row_of(const PagedParams& p, int b, bool& bad) {
+    Row r;
+    bad = !row_tokens(p.starts, b, p.n_tokens, r.s, r.n);
+    r.len = 0;
+    if (r.n > 0) {
+        r.len = p.lens[b];
+        if (r.n > p.max_new || r.len < r.n || r.len > p.capacity) {
+            bad = true;
+            r.n = 0;
+        }
+    }
+    return r;
+}
+
+// sum_{i < n} floor((a i + b) / 64), by the Euclidean recursion on (a, 64).
+__device__ __forceinline__ uint64_t floor_sum64(uint64_t n, uint64_t a, uint64_t b) {
+    uint64_t sum = 0, m = 64;
+    while (n > 0) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const uint64_t top = a * n + b;
+        n = top / m;
+        b = top % m;
+        const uint64_t x = m;
+        m = a;
+        a = x;
+        if (n == 0) break;
+    }
+    return sum;
+}
+
+struct Shape {  // of a row's units
+    Row r;
+    int nmb;     // blocks of tq tokens
+    __device__ __forceinline__ int s0() const { return r.len - r.n; }
+};
+__device__ __forceinline__ Shape shape_of(const PagedParams& p, const Row& r) {
+    Shape s;
+    s.r = r;
+    s.nmb = (r.n + p.tq - 1) / p.tq;
+    return s;
+}
+// Vectors, tiles and weight of block mb.
+__device__ __forceinline__ int live_rows(const PagedParams& p, const Shape& s, int mb) {
+    return min(p.tq, s.r.n - mb * p.tq) * p.group;
+}
+__device__ __forceinline__ int kv_end(const PagedParams& p, const Shape& s, int mb) {
+    return s.s0() + min(s.r.n, (mb + 1) * p.tq);
+}
+__device__ __forceinline__ int tiles_of(const PagedParams& p, const Shape& s, int mb) {
+    return (kv_end(p, s, mb) + kTile - 1) / kTile;
+}
+__device__ __forceinline__ uint32_t tile_weight(int live) { return live > 64 ? kHeavy : kLight; }
+__device__ __forceinline__ uint32_t unit_weight(const PagedParams& p, const Shape& s, int mb) {
+    return tiles_of(p, s, mb) * tile_weight(live_rows(p, s, mb)) + kUnit;
+}
+// Weight of the first k blocks of one head, k < nmb: they are full, so heavy (tq * g > 64).
+__device__ __forceinline__ uint64_t full_blocks(const PagedParams& p, const Shape& s, int k) {
+    return kHeavy * floor_sum64((uint64_t)k, (uint64_t)p.tq,
+                                (uint64_t)(s.s0() + p.tq + kTile - 1)) +
+           (uint64_t)k * kUnit;
+}
+__device__ __forceinline__ uint64_t row_weight(const PagedParams& p, const Row& r) {
+    if (r.n == 0) return 0;
+    const Shape s = shape_of(p, r);
+    return p.n_kv_heads *
+           ((s.nmb > 1 ? full_blocks(p, s, s.nmb - 1) : 0) + unit_weight(p, s, s.nmb - 1));
+}
+
+__device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int lane) {
+    return __shfl_sync(0xffffffffu, (unsigned long long)v, lane);
+}
+
+// The row that holds place `at`, and the list's length before it; with at past the end, `before`
+// is the length of the list. One warp.
+__device__ __forceinline__ int find_row(const PagedParams& p, uint64_t at, uint64_t& before) {
+    const int lane = threadIdx.x & 31;
+    before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        uint64_t w = 0;
+        bool bad = false;
+        if (b0 + lane < p.batch) w = row_weight(p, row_of(p, b0 + lane, bad));
+        uint64_t inc = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint64_t o = __shfl_up_sync(0xffffffffu, (unsigned long long)inc, off);
+            if (lane >= off) inc += o;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > at);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            before += shfl_u64(inc - w, l);
+            return b0 + l;
+        }
+        before += shfl_u64(inc, 31);
+    }
+    return p.batch;
+}
+
+struct Place {  // of a unit
+    int b, mb, h;
+    uint32_t w;
+    uint64_t u0;  // where it starts in the list
+};
+// The unit at place `at`, which is below the list's length. One warp.
+__device__ __forceinline__ Place find_unit(const PagedParams& p, uint64_t at) {
+    Place u;
+    uint64_t before;
+    u.b = find_row(p, at, before);
+    bool bad;
+    const Shape s = shape_of(p, row_of(p, u.b, bad));
+    const uint64_t in = at - before;
+    // the last block that starts at or before `at`: 32 probes a step
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = s.nmb;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int k = lo + (lane + 1) * step;
+        const unsigned le =
+            __ballot_sync(0xffffffffu, k < hi && p.n_kv_heads * full_blocks(p, s, k) <= in);
+        lo += __popc(le) * step;
+        hi = min(lo + step, hi);
+    }
+    u.mb = lo;
+    const uint64_t pre = lo > 0 ? p.n_kv_heads * full_blocks(p, s, lo) : 0;
+    u.w = unit_weight(p, s, lo);
+    u.h = (int)((in - pre) / u.w);
+    u.u0 = before + pre + (uint64_t)u.h * u.w;
+    return u;
+}
+
+// Stretches of the list: CTA i's share starts at floor(i total / ctas).
+struct Shares {
+    uint64_t total;
+    uint32_t ctas;
+    __device__ __forceinline__ uint64_t start(uint32_t i) const { return i * total / ctas; }
+    __device__ __forceinline__ uint32_t holder(uint64_t at) const {  // whose share has place `at`
+        return (uint32_t)(((at + 1) * ctas - 1) / total);
+    }
+};
+__device__ __forceinline__ Shares shares(uint64_t total) {
+    Shares s;
+    s.total = total;
+    s.ctas = (uint32_t)max((uint64_t)1, min((uint64_t)gridDim.x, total / kLeast));
+    return s;
+}
+// Where the stretch really starts whose share starts at `at`: inside a unit of weight w from
+// keep_lo to keep_hi - 1, else at the nearer end of the unit, as a cut costs more than some tiles.
+// (Units too small for that are not cut.)
+__device__ __forceinline__ bool cuttable(uint32_t w) { return w >= kUnit + 2 * kSnap; }
+__device__ __forceinline__ uint32_t keep_lo(uint32_t w) {
+    return cuttable(w) ? kUnit + kSnap : (w + 1) / 2;
+}
+__device__ __forceinline__ uint32_t keep_hi(uint32_t w) {
+    return cuttable(w) ? w - kSnap : keep_lo(w);
+}
+__device__ __forceinline__ uint64_t cut(const PagedParams& p, uint64_t total, uint64_t at) {
+    if (at >= total) return total;
+    const Place u = find_unit(p, at);
+    const uint32_t in = (uint32_t)(at - u.u0);
+    return in < keep_lo(u.w) ? u.u0 : in >= keep_hi(u.w) ? u.u0 + u.w : at;
+}
+
+// A walk through the units of the CTA's stretch [cur, end); every role warp has its own.
+struct Walk {
+    uint64_t cur, end, u0;
+    int b, mb, h;
+    Shape s;
+    // of the unit
+    int live, kvend, tiles, v0, v1;
+    uint32_t w;
+    __device__ __forceinline__ void unit(const PagedParams& p) {
+        live = live_rows(p, s, mb);
+        kvend = kv_end(p, s, mb);
+        tiles = tiles_of(p, s, mb);
+        const uint32_t tw = tile_weight(live);
+        w = tiles * tw + kUnit;
+        const uint32_t in = (uint32_t)(cur - u0);
+        v0 = in > kUnit ? (in - kUnit) / tw : 0;
+        const uint32_t out = (uint32_t)min((uint64_t)w, end - u0);
+        v1 = out == w ? tiles : (out - kUnit) / tw;
+    }
+    __device__ __forceinline__ void start(const PagedParams& p, const Place& u, uint64_t from,
+                                          uint64_t to) {
+        cur = from;
+        end = to;
+        u0 = u.u0;
+        b = u.b;
+        mb = u.mb;
+        h = u.h;
+        bool bad;
+        s = shape_of(p, row_of(p, b, bad));
+        unit(p);
+    }
+    // The next unit; false at the stretch's end.
+    __device__ __forceinline__ bool next(const PagedParams& p) {
+        u0 += w;
+        cur = u0;
+        if (cur >= end) return false;
+        if (++h == p.n_kv_heads) {
+            h = 0;
+            if (++mb == s.nmb) {
+                mb = 0;
+                Row r;
+                bool bad;
+                do r = row_of(p, ++b, bad);
+                while (r.n == 0 && b + 1 < p.batch);
+                s = shape_of(p, r);
+            }
+        }
+        unit(p);
+        return true;
+    }
+};
+
+enum PgBar {
+    kBarFull = 0,                       // K and V of slot s landed (TMA bytes)
+    kBarFree = kBarFull + kPgSlots,     // the products that read slot s are done (MMA commit)
+    kBarS = kBarFree + kPgSlots,        // S buffer written (MMA commit)
+    kBarP = kBarS + 2,                  // P buffer written by every row (128 arrivals)
+    kBarO = kBarP + 2,                  // P.V from the P buffer done (MMA commit)
+    kBarQ = kBarO + 2,                  // the unit's rows staged (128 arrivals)
+    kBarDrain = kBarQ + 1,              // every MMA issued so far done (after a failure)
+    kBarCount = kBarDrain + 1
+};
+
+__device__ __forceinline__ void rows_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kRowThreads) : "memory");
+}
+// Whether `x` holds in any of the row threads.
+__device__ __forceinline__ bool rows_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(kRowThreads)
+        : "memory");
+    return r != 0;
+}
+
+struct Smem {
+    uint8_t *k, *v, *q;
+    uint64_t* bars;
+    float2* ml;  // [128]
+    __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&bars[i]); }
+};
+
+// ---------------------------------------------------------------- the rows ----------
+// Tiles v0 .. v1-1 of a unit, whose first has number it0 in the CTA: S into P, one row per thread.
+// REP copies of the rows, each with W = 64 / REP positions of a tile. Returns whether every wait
+// ended; m, l: this thread's reference (log2 units) and sum.
+template <typename T, int REP>
+__device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, uint32_t tmem,
+                                         const Walk& u, uint32_t it0, int lim, float& m,
+                                         float& l) {
+    constexpr int W = kTile / REP;
+    const int tid = threadIdx.x;
+    const int base = tid / (kPgRows / REP) * W;  // of this copy's positions in a tile
+    const uint32_t lane_off = (uint32_t)(tid & ~31) << 16;
+    const uint32_t t_o = tmem + lane_off + kPgColsO;
+    const bool pos_scale = p.scale_log2 > 0.f;
+    const float cs = pos_scale ? p.scale_log2 : 1.f;
+    const int lim_least = __reduce_min_sync(0xffffffffu, lim);
+    const int lim_most = __reduce_max_sync(0xffffffffu, lim);
+    m = -INFINITY;
+    l = 0.f;
+    if (REP > 1) {
+        // what the other copies hold stays zero in this lane
+        uint32_t z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0u;
+        tc_st32_u(tmem + lane_off + kPgColsP, z);
+        tc_st32_u(tmem + lane_off + kPgColsP + kTile / 2, z);
+    }
+    for (int j = 0; j < u.v1 - u.v0; ++j) {
+        const uint32_t it = it0 + j, buf = it & 1;
+        const int t0 = (u.v0 + j) * kTile;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarS + buf), (it >> 1) & 1)))
+            return false;
+        tc_fence_after();
+        uint32_t w[W / 2];
+        const uint32_t t_p = tmem + lane_off + kPgColsP + buf * (kTile / 2) + base / 2;
+        if (t0 + base >= lim_most) {
+            // the warp sees nothing of it
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) w[i] = 0u;
+        } else {
+            float s[W];
+            const uint32_t t_s = tmem + lane_off + buf * kTile + base;
+            if constexpr (W == 64) {
+                tc_ld32(t_s, s);
+                tc_ld32(t_s + 32, s + 32);
+            } else if constexpr (W == 32) {
+                tc_ld32(t_s, s);
+            } else {
+                tc_ld16(t_s, s);
+            }
+            if (!pos_scale) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) s[i] *= p.scale_log2;
+            }
+            if (t0 + base + W > lim_least) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) s[i] = t0 + base + i < lim ? s[i] : -INFINITY;
+            }
+            float pm[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                pm[e] = s[e];
+#pragma unroll
+                for (int i = e + 8; i + 8 < W; i += 16) pm[e] = max3(pm[e], s[i], s[i + 8]);
+                if ((W / 8) % 2 == 0) pm[e] = fmaxf(pm[e], s[W - 8 + e]);
+            }
+            const float tmax = max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]),
+                                    fmaxf(pm[6], pm[7])) * cs;
+            const float mc = fmaxf(m, tmax);
+            const bool grow = mc > m + kPgGrow;
+            float factor = 1.f;
+            if (grow) {
+                factor = exp2f(m - mc);  // 0 on the first tile
+                m = mc;
+            }
+            l *= factor;
+            if (j >= 1 && __any_sync(0xffffffffu, grow)) {
+                // O is rescaled once P.V of the tile before is done
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarO + (buf ^ 1)),
+                                                               ((it - 1) >> 1) & 1)))
+                    return false;
+                tc_fence_after();
+                float ov[32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    tc_ld32(t_o + h * 32, ov);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) ov[i] *= factor;
+                    tc_st32(t_o + h * 32, ov);
+                }
+            }
+            // the weights, rounded to the storage type; their sum is taken before that (rounding
+            // to nearest leaves no bias)
+            const float nref = m == -INFINITY ? 0.f : -m;
+            const Pair cs2(cs, cs), ref2(nref, nref);
+            Pair sum[4] = {Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f)};
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                const float2 x = fma2(Pair(s[2 * i], s[2 * i + 1]), cs2, ref2).get();
+                const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                sum[i & 3] = add2(sum[i & 3], Pair(e.x, e.y));
+                w[i] = Half16<T>::from_f2(e.x, e.y);
+            }
+            const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])).get();
+            l += all.x + all.y;
+        }
+        // (the buffer's last reader, P.V of two tiles before, was done before this S was)
+        if constexpr (W == 64) tc_st32_u(t_p, w);
+        else if constexpr (W == 32) tc_st16_u(t_p, w);
+        else tc_st8_u(t_p, w);
+        if (t0 + kTile > u.kvend) {
+            // Positions past the last visible one hold other data (or nothing): P is 0 there, but
+            // 0 * NaN would still poison P.V, so those V rows are cleared once the copy landed.
+            const uint32_t slot = it % kPgSlots;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarFull + slot),
+                                                           (it / kPgSlots) & 1)))
+                return false;
+            uint8_t* vt = sm.v + slot * kTileBytes;
+            const int first = u.kvend - t0;
+            for (int x = tid; x < (kTile - first) * 8; x += kRowThreads)
+                *reinterpret_cast<uint4*>(vt + swz(first + (x >> 3), x & 7)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async();
+        }
+        tc_fence_before();
+        mbar_arrive(sm.bar(kBarP + buf));
+    }
+    return true;
+}
+
+// Where 4 dims of vector r of a unit go.
+template <typename T>
+__device__ __forceinline__ T* out_row(const PagedParams& p, const Walk& u, int r) {
+    const int tok = r / p.group, hg = r - tok * p.group;
+    const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
+    return static_cast<T*>(p.out) + (t * p.n_q_heads + u.h * p.group + hg) * kHeadDim;
+}
+template <typename T>
+__device__ __forceinline__ uint2 pack4(const float4& o, float inv) {
+    return make_uint2(Half16<T>::from_f2(o.x * inv, o.y * inv),
+                      Half16<T>::from_f2(o.z * inv, o.w * inv));
+}
+
+// The unit's outputs from tensor memory: written, or (a piece of the unit) left in the workspace.
+// Every product of the unit is done.
+template <typename T, int REP>
+__device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm, uint32_t tmem,
+                                            const Walk& u, bool whole, int64_t slot, float m,
+                                            float l) {
+    const int tid = threadIdx.x;
+    constexpr int R = kPgRows / REP;
+    const int r = tid & (R - 1), part = tid / R;
+    const uint32_t t_o = tmem + ((uint32_t)(tid & ~31) << 16) + kPgColsO;
+    T* dst = r < u.live ? out_row<T>(p, u, r) : nullptr;
+    float* wsp = p.ws_part + (slot * p.slot_rows + r) * kHeadDim;
+    if constexpr (REP == 1) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float o[32];
+            tc_ld32(t_o + half * 32, o);
+            if (r < u.live) {
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint2 a = pack4<T>(make_float4(o[8 * c], o[8 * c + 1], o[8 * c + 2],
+                                                             o[8 * c + 3]), inv);
+                        const uint2 b = pack4<T>(make_float4(o[8 * c + 4], o[8 * c + 5],
+                                                             o[8 * c + 6], o[8 * c + 7]), inv);
+                        reinterpret_cast<uint4*>(dst + half * 32)[c] =
+                            make_uint4(a.x, a.y, b.x, b.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        reinterpret_cast<float4*>(wsp + half * 32)[c] =
+                            make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                }
+            }
+        }
+        if (!whole && r < u.live) p.ws_ml[slot * p.slot_rows + r] = make_float2(m, l);
+    } else {
+        // the copies' partials meet in the rows' shared memory (every S is done), 32 dims at a
+        // time; copy `part` writes its share of the dims
+        sm.ml[tid] = make_float2(m, l);
+        rows_sync();
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < REP; ++k) top = fmaxf(top, sm.ml[r + k * R].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float all = 0.f;
+#pragma unroll
+        for (int k = 0; k < REP; ++k) {
+            const float2 o = sm.ml[r + k * R];
+            all = fmaf(o.y, exp2f(o.x - ref), all);
+        }
+        const float f = exp2f(m - ref), inv = all > 0.f ? 1.f / all : 0.f;
+        constexpr int C = 8 / REP;  // float4s per thread and half
+        float4* buf = reinterpret_cast<float4*>(sm.q);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float o[32];
+            tc_ld32(t_o + half * 32, o);
+            if (half) rows_sync();  // the first half is read
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                buf[tid * 8 + (c ^ (tid & 7))] = make_float4(o[4 * c] * f, o[4 * c + 1] * f,
+                                                             o[4 * c + 2] * f, o[4 * c + 3] * f);
+            rows_sync();
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int c = part * C + i;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < REP; ++k) {
+                    const float4 y = buf[(r + k * R) * 8 + (c ^ (r & 7))];
+                    x.x += y.x;
+                    x.y += y.y;
+                    x.z += y.z;
+                    x.w += y.w;
+                }
+                if (r < u.live) {
+                    if (whole)
+                        *reinterpret_cast<uint2*>(dst + half * 32 + c * 4) = pack4<T>(x, inv);
+                    else
+                        *reinterpret_cast<float4*>(wsp + half * 32 + c * 4) = x;
+                }
+            }
+        }
+        if (!whole && part == 0 && r < u.live)
+            p.ws_ml[slot * p.slot_rows + r] = make_float2(top, all);
+        rows_sync();  // the buffer is read before the next unit's rows are staged
+    }
+}
+
+// A cut unit's pieces, which lie in the workspace: CTAs i0 .. i0 + n - 1, the last to arrive merges
+// them in that order.
+template <typename T>
+__device__ __forceinline__ void merge_pieces(const PagedParams& p, const Walk& u, uint32_t i0,
+                                             int n, int* s_last) {
+    const int tid = threadIdx.x;
+    __threadfence();
+    rows_sync();
+    if (tid == 0) *s_last = atomicAdd(&p.ws_cnt[i0], 1) == n - 1;
+    rows_sync();
+    if (!*s_last) return;
+    __threadfence();
+    for (int x = tid; x < u.live * (kHeadDim / 4); x += kRowThreads) {
+        const int r = x >> 4, d4 = x & 15;
+        auto at = [&](int i) { return (2 * (int64_t)(i0 + i) + (i == 0)) * p.slot_rows + r; };
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(&p.ws_ml[at(i)]).x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float2 ml = __ldcg(&p.ws_ml[at(i)]);
+            const float4 y =
+                __ldcg(reinterpret_cast<const float4*>(p.ws_part + at(i) * kHeadDim) + d4);
+            const float f = exp2f(ml.x - ref);
+            l = fmaf(ml.y, f, l);
+            o.x = fmaf(y.x, f, o.x);
+            o.y = fmaf(y.y, f, o.y);
+            o.z = fmaf(y.z, f, o.z);
+            o.w = fmaf(y.w, f, o.w);
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        *reinterpret_cast<uint2*>(out_row<T>(p, u, r) + d4 * 4) = pack4<T>(o, inv);
+    }
+    if (tid == 0) p.ws_cnt[i0] = 0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const PagedParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem sm;
+    sm.k = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~uintptr_t(1023));
+    sm.v = sm.k + kPgSlots * kTileBytes;
+    sm.q = sm.v + kPgSlots * kTileBytes;
+    sm.bars = reinterpret_cast<uint64_t*>(sm.q + kPgQBytes);
+    sm.ml = reinterpret_cast<float2*>(sm.q + kPgQBytes + 256);
+    static_assert(kBarCount * 8 <= 256, "the barriers' place");
+    __shared__ Place s_place;
+    __shared__ uint64_t s_from, s_to, s_total;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_last;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool mma_warp = warp == kRowThreads / 32, copy_warp = warp == kRowThreads / 32 + 1;
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        uint64_t total;
+        find_row(p, ~0ull, total);
+        uint64_t from = 0, to = 0;
+        if (total > 0) {
+            const Shares sh = shares(total);
+            if (blockIdx.x < sh.ctas) {
+                from = cut(p, total, sh.start(blockIdx.x));
+                to = cut(p, total, sh.start(blockIdx.x + 1));
+            }
+        }
+        if (from < to) {
+            const Place u = find_unit(p, from);
+            if (lane == 0) s_place = u;
+        }
+        if (lane == 0) {
+            s_from = from;
+            s_to = to;
+            s_total = total;
+        }
+    } else if (copy_warp && lane == 0) {
+        for (int i = 0; i < kBarCount; ++i)
+            mbar_init(sm.bar(i), i == kBarP || i == kBarP + 1 || i == kBarQ ? kRowThreads : 1);
+        fence_barrier_init();
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    } else if (warp == 1) {
+        // rows that do not fit
+        for (int b = blockIdx.x + lane * gridDim.x; b < p.batch; b += 32 * gridDim.x) {
+            bool bad;
+            row_of(p, b, bad);
+            if (bad) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+        }
+    }
+    __syncthreads();
+    if (s_from >= s_to) return;
+    if (mma_warp) {
+        tc_alloc(smem_u32(&s_tmem), kPgCols);
+        tc_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    Walk u;
+    u.start(p, s_place, s_from, s_to);
+    bool ok = true;
+
+    if (copy_warp) {
+        // ---- K/V tiles, a slot each ----
+        uint32_t it = 0;
+        const int in_page = (1 << p.page_log2) - 1;
+        do {
+            // lane i: box i of K, lane 16 + i: box i of V
+            const int box = lane & 15;
+            const bool mine = box < p.boxes;
+            const int32_t* row = p.table + u.b * p.table_stride;
+            auto page_of = [&](int v) {
+                const int pos = v * kTile + box * p.box_rows;
+                return mine && v < u.v1 && pos < u.kvend ? __ldg(row + (pos >> p.page_log2)) : 0;
+            };
+            int page = page_of(u.v0);
+            for (int v = u.v0; v < u.v1; ++v, ++it) {
+                const int pos = v * kTile + box * p.box_rows;
+                const bool on = mine && pos < u.kvend;
+                const uint32_t slot = it % kPgSlots;
+                int pg = page;
+                page = page_of(v + 1);
+                if (on && (pg < 0 || pg >= p.n_pages)) {
+                    flag_error(p.dev_err, KVD_ERR_BAD_INDEX);
+                    pg = p.n_pages;  // outside the tensor: zeros
+                }
+                if (it >= kPgSlots &&
+                    !__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarFree + slot),
+                                                               (it / kPgSlots - 1) & 1))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = sm.bar(kBarFull + slot);
+                const int n_on = __popc(__ballot_sync(0xffffffffu, on));
+                if (lane == 0) {
+                    // test only: 16 bytes more than the copies bring
+                    if (p.test_stall && it == 0) mbar_expect_tx_only(bar, 16);
+                    mbar_expect_tx(bar, n_on * p.box_rows * kRowBytes);
+                }
+                __syncwarp();
+                if (on) {
+                    const bool is_v = lane >= 16;
+                    const uint32_t dst = smem_u32((is_v ? sm.v : sm.k) + slot * kTileBytes) +
+                                         box * p.box_rows * kRowBytes;
+                    tma_load_4d(dst, is_v ? &tmv : &tmk, bar, 0, pos & in_page, u.h, pg);
+                }
+                __syncwarp();
+            }
+        } while (ok && u.next(p));
+        if (!ok) {
+            if (lane == 0) flag_error(p.dev_err, KVD_ERR_TIMEOUT);
+            // the copies in flight land before the block leaves
+            for (uint32_t i = it > kPgSlots ? it - kPgSlots : 0; i < it; ++i)
+                mbar_wait_bounded(sm.bar(kBarFull + i % kPgSlots), (i / kPgSlots) & 1);
+        }
+    } else if (mma_warp) {
+        // ---- the products: the whole warp runs the loop, one elected lane issues ----
+        constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+        constexpr uint32_t kIdS = tc_idesc_f16(kBf16, kPgRows, kTile, false);
+        constexpr uint32_t kIdO = tc_idesc_f16(kBf16, kPgRows, kHeadDim, true);
+        const uint32_t qaddr = smem_u32(sm.q);
+        auto wait_all = [&](int i, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(i), parity));
+        };
+        auto issue_s = [&](uint32_t it) -> bool {
+            const uint32_t slot = it % kPgSlots, buf = it & 1;
+            if (!wait_all(kBarFull + slot, (it / kPgSlots) & 1)) return false;
+            tc_fence_after();
+            const uint32_t kaddr = smem_u32(sm.k + slot * kTileBytes);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_f16(tmem + buf * kTile, tc_desc_sw128(qaddr + kk * 32),
+                               tc_desc_sw128(kaddr + kk * 32), kIdS, kk);
+                tc_commit(sm.bar(kBarS + buf));
+            }
+            __syncwarp();
+            return true;
+        };
+        uint32_t it0 = 0, units = 0;
+        do {
+            const int nt = u.v1 - u.v0;
+            if (!(ok = wait_all(kBarQ, units & 1))) break;
+            tc_fence_after();
+            for (int j = 0; ok && j < min(2, nt); ++j) ok = issue_s(it0 + j);
+            for (int j = 0; ok && j < nt; ++j) {
+                const uint32_t it = it0 + j, buf = it & 1, slot = it % kPgSlots;
+                if (!(ok = wait_all(kBarP + buf, (it >> 1) & 1))) break;
+                tc_fence_after();
+                const uint32_t t_p = tmem + kPgColsP + buf * (kTile / 2);
+                const uint32_t vaddr = smem_u32(sm.v + slot * kTileBytes);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_f16_tmem_a(tmem + kPgColsO, t_p + kk * 8,
+                                          tc_desc_sw128(vaddr + kk * 16 * kRowBytes), kIdO,
+                                          j > 0 || kk > 0);
+                    tc_commit(sm.bar(kBarO + buf));
+                    tc_commit(sm.bar(kBarFree + slot));
+                }
+                __syncwarp();
+                if (j + 2 < nt) ok = issue_s(it + 2);
+            }
+            it0 += nt;
+            ++units;
+        } while (ok && u.next(p));
+        if (!ok) {
+            if (elect_one()) {
+                flag_error(p.dev_err, KVD_ERR_TIMEOUT);
+                tc_commit(sm.bar(kBarDrain));
+                mbar_wait_bounded(sm.bar(kBarDrain), 0);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---- the rows ----
+        uint32_t it0 = 0;
+        Shares sh;
+        sh.total = s_total;
+        sh.ctas = shares(s_total).ctas;
+        do {
+            const int rep = u.live > 64 ? 1 : u.live > 32 ? 2 : 4;
+            const int r = tid & (kPgRows / rep - 1);
+            const int tok = r / p.group;
+            const bool live = r < u.live;
+            {
+                // this thread's query row (zeros past the unit's) into the swizzled A operand
+                const int hg = r - tok * p.group;
+                const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    p.q + t * p.q_st + (int64_t)(u.h * p.group + hg) * p.q_sh);
+                uint4 qv[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) qv[c] = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sm.q + swz(tid, c)) = qv[c];
+                fence_proxy_async();
+            }
+            mbar_arrive(sm.bar(kBarQ));
+            // keys t < lim are visible; rows past the unit's see all of it (and are not written)
+            const int lim = live ? u.s.s0() + u.mb * p.tq + tok + 1 : u.kvend;
+            float m, l;
+            if (rep == 1) ok = run_rows<T, 1>(p, sm, tmem, u, it0, lim, m, l);
+            else if (rep == 2) ok = run_rows<T, 2>(p, sm, tmem, u, it0, lim, m, l);
+            else ok = run_rows<T, 4>(p, sm, tmem, u, it0, lim, m, l);
+            it0 += u.v1 - u.v0;
+            const uint32_t last = it0 - 1;
+            ok = ok && mbar_wait_bounded(sm.bar(kBarO + (last & 1)), (last >> 1) & 1);
+            if (rows_any(!ok)) {
+                if (tid == 0) flag_error(p.dev_err, KVD_ERR_TIMEOUT);
+                break;
+            }
+            tc_fence_after();
+            const bool whole = u.v0 == 0 && u.v1 == u.tiles;
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (u.v0 == 0);
+            if (rep == 1) finish_rows<T, 1>(p, sm, tmem, u, whole, slot, m, l);
+            else if (rep == 2) finish_rows<T, 2>(p, sm, tmem, u, whole, slot, m, l);
+            else finish_rows<T, 4>(p, sm, tmem, u, whole, slot, m, l);
+            if (!whole) {
+                // (the last share that starts before the unit's first cut, and before its last)
+                const uint32_t i0 = sh.holder(u.u0 + keep_lo(u.w) - 1);
+                const uint32_t i1 = sh.holder(u.u0 + keep_hi(u.w) - 1);
+                merge_pieces<T>(p, u, i0, (int)(i1 - i0) + 1, &s_last);
+            }
+            tc_fence_before();  // O is read before the next unit's products
+        } while (u.next(p));
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (mma_warp) {
+        tc_fence_after();
+        tc_dealloc(tmem, kPgCols);
+    }
+}
+
+constexpr int kMaxDevP = 64;
+
+// Once per kernel and device: its shared memory; the blocks resident at once (0: an error).
+template <typename T>
+int prepare_paged(int nsm) {
+    static std::once_flag once[kMaxDevP];
+    static int blocks[kMaxDevP];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevP) return 0;
+    std::call_once(once[dev], [dev, nsm] {
+        int n = 0;
+        if (cudaFuncSetAttribute(paged_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kPgSmem) == cudaSuccess &&
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attn_kernel<T>, kPgThreads,
+                                                          kPgSmem) == cudaSuccess)
+            blocks[dev] = std::min(kMaxCtas, nsm * std::min(n, kPgMinBlocks));
+        cudaGetLastError();
+    });
+    return blocks[dev];
+}
+
+template <typename T>
+kvd_status run_paged(PagedParams& p, int nsm, const CUtensorMap& mk, const CUtensorMap& mv,
+                     uint8_t* ws, bool pdl, cudaStream_t st) {
+    const int blocks = prepare_paged<T>(nsm);
+    if (blocks <= 0) return KVD_ERR_CUDA;
+    p.ws_cnt = reinterpret_cast<int32_t*>(ws);
+    p.ws_part = reinterpret_cast<float*>(ws + KVD_WS_COUNTER_BYTES);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_part + (size_t)2 * blocks * p.slot_rows * kHeadDim);
+    return launch(paged_attn_kernel<T>, dim3((unsigned)blocks), dim3(kPgThreads), kPgSmem, st, pdl,
+                  mk, mv, p);
+}
+
+// Query vectors of the largest unit.
+int unit_rows(int group, int max_new) {
+    return (int)std::min<int64_t>(kPgRows / group, max_new) * group;
+}
+
+}  // namespace
+
+size_t paged_workspace_bytes(int n_q_heads, int n_kv_heads, int max_new) {
+    return KVD_WS_COUNTER_BYTES + (size_t)2 * kMaxCtas * unit_rows(n_q_heads / n_kv_heads, max_new) *
+                                      (kHeadDim + 2) * sizeof(float);
+}
+
+}  // namespace kvd
+
+using namespace kvd;
+
+extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cache,
+                                     int32_t n_tokens, int32_t max_new, const kvd_token_rows* q,
+                                     const int32_t* starts, const int32_t* lens, float scale,
+                                     void* workspace, size_t workspace_bytes, uint32_t flags,
+                                     int32_t* dev_err, kvd_stream_t stream) {
+    if (dtype != KVD_F16 && dtype != KVD_BF16) return KVD_ERR_INVALID_ARG;
+    if (kvd_status s = validate_paged_cache(cache)) return s;
+    if (n_tokens < 0 || max_new < 1 || !starts || !lens) return KVD_ERR_INVALID_ARG;
+    if (!(scale < INFINITY) || !(scale > -INFINITY)) return KVD_ERR_INVALID_ARG;
+    if (n_tokens == 0) return KVD_OK;
+    if (kvd_status s = validate_token_rows(q)) return s;
+    if (!q->out || q->out == q->x || q->n_heads % cache->n_kv_heads) return KVD_ERR_INVALID_ARG;
+    const int group = q->n_heads / cache->n_kv_heads;
+    if (group > KVD_MAX_GROUP) return KVD_ERR_UNSUPPORTED;
+    max_new = std::min(max_new, n_tokens);
+    const size_t need = paged_workspace_bytes(q->n_heads, cache->n_kv_heads, max_new);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
+        return KVD_ERR_WORKSPACE;
+    const int nsm = sm_count();
+    if (nsm <= 0) return KVD_ERR_CUDA;
+    CUtensorMap mk, mv;
+    if (kvd_status s = encode_pool_map(&mk, dtype, cache->k, cache)) return s;
+    if (kvd_status s = encode_pool_map(&mv, dtype, cache->v, cache)) return s;
+    PagedParams p = {};
+    p.q = static_cast<const uint8_t*>(q->x);
+    p.q_st = q->stride_t * 2;
+    p.q_sh = q->stride_h * 2;
+    p.out = q->out;
+    p.starts = starts;
+    p.lens = lens;
+    p.table = cache->table;
+    p.table_stride = cache->table_stride;
+    p.batch = cache->batch;
+    p.n_tokens = n_tokens;
+    p.max_new = max_new;
+    p.capacity = cache->table_width * cache->page_size;
+    p.n_q_heads = q->n_heads;
+    p.n_kv_heads = cache->n_kv_heads;
+    p.group = group;
+    p.tq = kPgRows / group;
+    p.n_pages = cache->n_pages;
+    while ((1 << p.page_log2) < cache->page_size) ++p.page_log2;
+    p.box_rows = std::min(kTile, cache->page_size);
+    p.boxes = kTile / p.box_rows;
+    p.scale_log2 = scale * kLog2e;
+    p.slot_rows = unit_rows(group, max_new);
+    p.dev_err = dev_err;
+    p.test_stall = (flags & KVD_FLAG_TEST_STALL) ? 1 : 0;
+    const bool pdl = (flags & (KVD_FLAG_PDL | KVD_FLAG_EARLY_KV)) != 0;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    return dtype == KVD_BF16 ? run_paged<__nv_bfloat16>(p, nsm, mk, mv, ws, pdl, st)
+                             : run_paged<__half>(p, nsm, mk, mv, ws, pdl, st);
+}
