@@ -49,10 +49,12 @@ constexpr uint32_t kPgCols = 256;
 static_assert(kPgCols >= kPgColsP + 2 * (kTile / 2) && kPgMinBlocks * kPgCols <= 512,
               "the resident blocks' tensor memory");
 constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
+// shared memory: K slots | V slots | Q | barriers | rows' references and sums
 constexpr uint32_t kPgSmem = 2 * kPgSlots * kTileBytes + kPgQBytes + 256 + kPgRows * 8 + 1024;
+constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
 
-// The list's weights: a tile of a unit with more than 64 vectors (bound by the softmax) and with
+// The list's weights (its length is below 2^32, see the host's check): a tile of a unit with more than 64 vectors (bound by the softmax) and with
 // at most 64 (bound by the copies), and what a unit costs besides.
 constexpr uint32_t kHeavy = 3, kLight = 2, kUnit = 24;
 constexpr uint32_t kSnap = 8;       // no cut this close to a unit's ends
@@ -97,27 +99,26 @@ __device__ __forceinline__ Row row_of(const PagedParams& p, int b, bool& bad) {
     return r;
 }
 
-// sum_{i < n} floor((a i + b) / 64), by the Euclidean recursion on (a, 64).
-__device__ __forceinline__ uint64_t floor_sum64(uint64_t n, uint64_t a, uint64_t b) {
-    uint64_t sum = 0, m = 64;
-    while (n > 0) {
+// sum_{i < n} floor((a i + b) / 64), by the Euclidean recursion on (a, 64). The sum is below 2^32.
+__device__ __forceinline__ uint32_t floor_sum64(uint32_t n, uint32_t a, uint32_t b) {
+    uint32_t sum = 0, m = 64;
+    for (;;) {
         if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
+            sum += (uint32_t)((uint64_t)n * (n - 1) / 2) * (a / m);
             a %= m;
         }
         if (b >= m) {
             sum += n * (b / m);
             b %= m;
         }
-        const uint64_t top = a * n + b;
+        const uint32_t top = a * n + b;
+        if (top < m) return sum;
         n = top / m;
         b = top % m;
-        const uint64_t x = m;
+        const uint32_t x = m;
         m = a;
         a = x;
-        if (n == 0) break;
     }
-    return sum;
 }
 
 struct Shape {  // of a row's units
@@ -128,7 +129,7 @@ struct Shape {  // of a row's units
 __device__ __forceinline__ Shape shape_of(const PagedParams& p, const Row& r) {
     Shape s;
     s.r = r;
-    s.nmb = (r.n + p.tq - 1) / p.tq;
+    s.nmb = r.n <= p.tq ? (r.n > 0) : (r.n + p.tq - 1) / p.tq;
     return s;
 }
 // Vectors, tiles and weight of block mb.
@@ -145,62 +146,96 @@ __device__ __forceinline__ uint32_t tile_weight(int live) { return live > 64 ? k
 __device__ __forceinline__ uint32_t unit_weight(const PagedParams& p, const Shape& s, int mb) {
     return tiles_of(p, s, mb) * tile_weight(live_rows(p, s, mb)) + kUnit;
 }
-// Weight of the first k blocks of one head, k < nmb: they are full, so heavy (tq * g > 64).
-__device__ __forceinline__ uint64_t full_blocks(const PagedParams& p, const Shape& s, int k) {
-    return kHeavy * floor_sum64((uint64_t)k, (uint64_t)p.tq,
-                                (uint64_t)(s.s0() + p.tq + kTile - 1)) +
-           (uint64_t)k * kUnit;
+// Weight of the first k blocks of one head, 0 <= k < nmb: they are full, so heavy (tq * g > 64).
+__device__ __forceinline__ uint32_t full_blocks(const PagedParams& p, const Shape& s, int k) {
+    if (k == 0) return 0;
+    return kHeavy * floor_sum64((uint32_t)k, (uint32_t)p.tq,
+                                (uint32_t)(s.s0() + p.tq + kTile - 1)) + (uint32_t)k * kUnit;
 }
-__device__ __forceinline__ uint64_t row_weight(const PagedParams& p, const Row& r) {
+__device__ __forceinline__ uint32_t row_weight(const PagedParams& p, const Row& r) {
     if (r.n == 0) return 0;
     const Shape s = shape_of(p, r);
-    return p.n_kv_heads *
-           ((s.nmb > 1 ? full_blocks(p, s, s.nmb - 1) : 0) + unit_weight(p, s, s.nmb - 1));
+    return p.n_kv_heads * (full_blocks(p, s, s.nmb - 1) + unit_weight(p, s, s.nmb - 1));
 }
 
-__device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int lane) {
-    return __shfl_sync(0xffffffffu, (unsigned long long)v, lane);
+// Prefix sums over the rows' weights: tab[e] is the list's length up to and with the rows of entry
+// e, `each` rows an entry.
+struct Table {
+    uint32_t* tab;
+    int each, n;
+};
+// All threads; the sums are whole behind a barrier and finish_table (one warp).
+__device__ __forceinline__ Table fill_table(const PagedParams& p, uint32_t* tab) {
+    Table t;
+    t.tab = tab;
+    t.each = (p.batch + kTable - 1) / kTable;
+    t.n = t.each == 1 ? p.batch : (p.batch + t.each - 1) / t.each;
+    for (int e = threadIdx.x; e < t.n; e += kPgThreads) {
+        uint32_t w = 0;
+        for (int b = e * t.each; b < min((e + 1) * t.each, p.batch); ++b) {
+            bool bad;
+            w += row_weight(p, row_of(p, b, bad));
+            if (bad && blockIdx.x == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+        }
+        tab[e] = w;
+    }
+    return t;
 }
-
-// The row that holds place `at`, and the list's length before it; with at past the end, `before`
-// is the length of the list. One warp.
-__device__ __forceinline__ int find_row(const PagedParams& p, uint64_t at, uint64_t& before) {
+__device__ __forceinline__ uint32_t finish_table(const Table& t) {
     const int lane = threadIdx.x & 31;
-    before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        uint64_t w = 0;
-        bool bad = false;
-        if (b0 + lane < p.batch) w = row_weight(p, row_of(p, b0 + lane, bad));
-        uint64_t inc = w;
+    uint32_t before = 0;
+    for (int e0 = 0; e0 < t.n; e0 += 32) {
+        uint32_t inc = e0 + lane < t.n ? t.tab[e0 + lane] : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const uint64_t o = __shfl_up_sync(0xffffffffu, (unsigned long long)inc, off);
+            const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += o;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > at);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            before += shfl_u64(inc - w, l);
-            return b0 + l;
-        }
-        before += shfl_u64(inc, 31);
+        inc += before;
+        if (e0 + lane < t.n) t.tab[e0 + lane] = inc;
+        before = __shfl_sync(0xffffffffu, inc, 31);
     }
-    return p.batch;
+    __syncwarp();
+    return before;
+}
+// The row that holds place `at`, which is below the list's length, and the list's length before
+// it. One warp.
+__device__ __forceinline__ int find_row(const PagedParams& p, const Table& t, uint32_t at,
+                                        uint32_t& before) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = t.n;  // the first entry above `at`: 32 probes a step
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int e = lo + (lane + 1) * step;
+        lo += __popc(__ballot_sync(0xffffffffu, e < hi && t.tab[e - 1] <= at)) * step;
+        hi = min(lo + step, hi);
+    }
+    before = lo > 0 ? t.tab[lo - 1] : 0;
+    int b = lo * t.each;
+    for (const int last = min(b + t.each, p.batch) - 1; b < last; ++b) {
+        bool bad;
+        const uint32_t w = row_weight(p, row_of(p, b, bad));
+        if (before + w > at) break;
+        before += w;
+    }
+    return b;
 }
 
 struct Place {  // of a unit
+    Row r;
     int b, mb, h;
     uint32_t w;
-    uint64_t u0;  // where it starts in the list
+    uint32_t u0;  // where it starts in the list
 };
 // The unit at place `at`, which is below the list's length. One warp.
-__device__ __forceinline__ Place find_unit(const PagedParams& p, uint64_t at) {
+__device__ __forceinline__ Place find_unit(const PagedParams& p, const Table& t, uint32_t at) {
     Place u;
-    uint64_t before;
-    u.b = find_row(p, at, before);
+    uint32_t before;
+    u.b = find_row(p, t, at, before);
     bool bad;
-    const Shape s = shape_of(p, row_of(p, u.b, bad));
-    const uint64_t in = at - before;
+    u.r = row_of(p, u.b, bad);
+    const Shape s = shape_of(p, u.r);
+    const uint32_t in = at - before;
     // the last block that starts at or before `at`: 32 probes a step
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = s.nmb;
@@ -213,31 +248,37 @@ __device__ __forceinline__ Place find_unit(const PagedParams& p, uint64_t at) {
         hi = min(lo + step, hi);
     }
     u.mb = lo;
-    const uint64_t pre = lo > 0 ? p.n_kv_heads * full_blocks(p, s, lo) : 0;
+    const uint32_t pre = p.n_kv_heads * full_blocks(p, s, lo);
     u.w = unit_weight(p, s, lo);
     u.h = (int)((in - pre) / u.w);
-    u.u0 = before + pre + (uint64_t)u.h * u.w;
+    u.u0 = before + pre + (uint32_t)u.h * u.w;
     return u;
 }
 
 // Stretches of the list: CTA i's share starts at floor(i total / ctas).
 struct Shares {
-    uint64_t total;
-    uint32_t ctas;
-    __device__ __forceinline__ uint64_t start(uint32_t i) const { return i * total / ctas; }
-    __device__ __forceinline__ uint32_t holder(uint64_t at) const {  // whose share has place `at`
-        return (uint32_t)(((at + 1) * ctas - 1) / total);
+    uint32_t total, ctas, per, rest;  // total = per ctas + rest
+    __device__ __forceinline__ uint32_t start(uint32_t i) const {
+        return i * per + i * rest / ctas;  // (rest < ctas <= kMaxCtas)
+    }
+    __device__ __forceinline__ uint32_t holder(uint32_t at) const {  // whose share has place `at`
+        uint32_t i = min((uint32_t)((float)at * ((float)ctas / (float)total)), ctas - 1);
+        while (start(i) > at) --i;
+        while (i + 1 < ctas && start(i + 1) <= at) ++i;
+        return i;
     }
 };
-__device__ __forceinline__ Shares shares(uint64_t total) {
+__device__ __forceinline__ Shares shares(uint32_t total) {
     Shares s;
     s.total = total;
-    s.ctas = (uint32_t)max((uint64_t)1, min((uint64_t)gridDim.x, total / kLeast));
+    s.ctas = max(1u, min(gridDim.x, total / kLeast));
+    s.per = total / s.ctas;
+    s.rest = total - s.per * s.ctas;
     return s;
 }
-// Where the stretch really starts whose share starts at `at`: inside a unit of weight w from
-// keep_lo to keep_hi - 1, else at the nearer end of the unit, as a cut costs more than some tiles.
-// (Units too small for that are not cut.)
+// Where the stretch really starts whose share starts inside a unit of weight w: there from keep_lo
+// to keep_hi - 1, else at the nearer end of the unit, as a cut costs more than some tiles. (Units
+// too small for that are not cut.)
 __device__ __forceinline__ bool cuttable(uint32_t w) { return w >= kUnit + 2 * kSnap; }
 __device__ __forceinline__ uint32_t keep_lo(uint32_t w) {
     return cuttable(w) ? kUnit + kSnap : (w + 1) / 2;
@@ -245,16 +286,14 @@ __device__ __forceinline__ uint32_t keep_lo(uint32_t w) {
 __device__ __forceinline__ uint32_t keep_hi(uint32_t w) {
     return cuttable(w) ? w - kSnap : keep_lo(w);
 }
-__device__ __forceinline__ uint64_t cut(const PagedParams& p, uint64_t total, uint64_t at) {
-    if (at >= total) return total;
-    const Place u = find_unit(p, at);
-    const uint32_t in = (uint32_t)(at - u.u0);
+__device__ __forceinline__ uint32_t cut(const Place& u, uint32_t at) {
+    const uint32_t in = at - u.u0;
     return in < keep_lo(u.w) ? u.u0 : in >= keep_hi(u.w) ? u.u0 + u.w : at;
 }
 
 // A walk through the units of the CTA's stretch [cur, end); every role warp has its own.
 struct Walk {
-    uint64_t cur, end, u0;
+    uint32_t cur, end, u0;
     int b, mb, h;
     Shape s;
     // of the unit
@@ -266,22 +305,25 @@ struct Walk {
         tiles = tiles_of(p, s, mb);
         const uint32_t tw = tile_weight(live);
         w = tiles * tw + kUnit;
-        const uint32_t in = (uint32_t)(cur - u0);
+        const uint32_t in = cur - u0, out = min(w, end - u0);
         v0 = in > kUnit ? (in - kUnit) / tw : 0;
-        const uint32_t out = (uint32_t)min((uint64_t)w, end - u0);
         v1 = out == w ? tiles : (out - kUnit) / tw;
     }
-    __device__ __forceinline__ void start(const PagedParams& p, const Place& u, uint64_t from,
-                                          uint64_t to) {
+    // From the unit that holds `from` or ends there; false if there is nothing before `to`.
+    __device__ __forceinline__ bool start(const PagedParams& p, const Place& u, uint32_t from,
+                                          uint32_t to) {
         cur = from;
         end = to;
         u0 = u.u0;
         b = u.b;
         mb = u.mb;
         h = u.h;
-        bool bad;
-        s = shape_of(p, row_of(p, b, bad));
+        s = shape_of(p, u.r);
+        w = u.w;
+        if (from >= to) return false;
+        if (from >= u0 + w) return next(p);
         unit(p);
+        return true;
     }
     // The next unit; false at the stretch's end.
     __device__ __forceinline__ bool next(const PagedParams& p) {
@@ -308,9 +350,10 @@ enum PgBar {
     kBarFull = 0,                       // K and V of slot s landed (TMA bytes)
     kBarFree = kBarFull + kPgSlots,     // the products that read slot s are done (MMA commit)
     kBarS = kBarFree + kPgSlots,        // S buffer written (MMA commit)
-    kBarP = kBarS + 2,                  // P buffer written by every row (128 arrivals)
+    kBarRead = kBarS + 2,               // S buffer read by every row (an arrival per warp)
+    kBarP = kBarRead + 2,               // P buffer written by every row (an arrival per warp)
     kBarO = kBarP + 2,                  // P.V from the P buffer done (MMA commit)
-    kBarQ = kBarO + 2,                  // the unit's rows staged (128 arrivals)
+    kBarQ = kBarO + 2,                  // the unit's rows staged (an arrival per warp)
     kBarDrain = kBarQ + 1,              // every MMA issued so far done (after a failure)
     kBarCount = kBarDrain + 1
 };
@@ -329,11 +372,16 @@ __device__ __forceinline__ bool rows_any(bool x) {
         : "memory");
     return r != 0;
 }
+// One arrival for the warp, behind what its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 struct Smem {
     uint8_t *k, *v, *q;
     uint64_t* bars;
-    float2* ml;  // [128]
+    float2* ml;   // [128]
     __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&bars[i]); }
 };
 
@@ -364,29 +412,28 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
         tc_st32_u(tmem + lane_off + kPgColsP, z);
         tc_st32_u(tmem + lane_off + kPgColsP + kTile / 2, z);
     }
-    for (int j = 0; j < u.v1 - u.v0; ++j) {
+    const int n = u.v1 - u.v0, kvend = u.kvend;
+    int t0 = u.v0 * kTile;
+    for (int j = 0; j < n; ++j, t0 += kTile) {
         const uint32_t it = it0 + j, buf = it & 1;
-        const int t0 = (u.v0 + j) * kTile;
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarS + buf), (it >> 1) & 1)))
             return false;
         tc_fence_after();
         uint32_t w[W / 2];
-        const uint32_t t_p = tmem + lane_off + kPgColsP + buf * (kTile / 2) + base / 2;
         if (t0 + base >= lim_most) {
             // the warp sees nothing of it
+            tc_fence_before();
+            warp_arrive(sm.bar(kBarRead + buf));
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) w[i] = 0u;
         } else {
             float s[W];
             const uint32_t t_s = tmem + lane_off + buf * kTile + base;
-            if constexpr (W == 64) {
-                tc_ld32(t_s, s);
-                tc_ld32(t_s + 32, s + 32);
-            } else if constexpr (W == 32) {
-                tc_ld32(t_s, s);
-            } else {
-                tc_ld16(t_s, s);
-            }
+            if constexpr (W == 64) tc_ld64(t_s, s);
+            else if constexpr (W == 32) tc_ld32(t_s, s);
+            else tc_ld16(t_s, s);
+            tc_fence_before();
+            warp_arrive(sm.bar(kBarRead + buf));
             if (!pos_scale) {
 #pragma unroll
                 for (int i = 0; i < W; ++i) s[i] *= p.scale_log2;
@@ -401,31 +448,32 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
                 pm[e] = s[e];
 #pragma unroll
                 for (int i = e + 8; i + 8 < W; i += 16) pm[e] = max3(pm[e], s[i], s[i + 8]);
-                if ((W / 8) % 2 == 0) pm[e] = fmaxf(pm[e], s[W - 8 + e]);
+                pm[e] = fmaxf(pm[e], s[W - 8 + e]);
             }
             const float tmax = max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]),
                                     fmaxf(pm[6], pm[7])) * cs;
-            const float mc = fmaxf(m, tmax);
-            const bool grow = mc > m + kPgGrow;
-            float factor = 1.f;
-            if (grow) {
-                factor = exp2f(m - mc);  // 0 on the first tile
-                m = mc;
-            }
-            l *= factor;
-            if (j >= 1 && __any_sync(0xffffffffu, grow)) {
-                // O is rescaled once P.V of the tile before is done
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarO + (buf ^ 1)),
-                                                               ((it - 1) >> 1) & 1)))
-                    return false;
-                tc_fence_after();
-                float ov[32];
+            const bool grow = tmax > m + kPgGrow;
+            if (__any_sync(0xffffffffu, grow)) {
+                float factor = 1.f;
+                if (grow) {
+                    factor = exp2f(m - tmax);  // 0 on the first tile
+                    m = tmax;
+                }
+                l *= factor;
+                if (j >= 1) {
+                    // O is rescaled once P.V of the tile before is done
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarO + (buf ^ 1)),
+                                                                   ((it - 1) >> 1) & 1)))
+                        return false;
+                    tc_fence_after();
+                    float ov[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    tc_ld32(t_o + h * 32, ov);
+                    for (int h = 0; h < 2; ++h) {
+                        tc_ld32(t_o + h * 32, ov);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) ov[i] *= factor;
-                    tc_st32(t_o + h * 32, ov);
+                        for (int i = 0; i < 32; ++i) ov[i] *= factor;
+                        tc_st32(t_o + h * 32, ov);
+                    }
                 }
             }
             // the weights, rounded to the storage type; their sum is taken before that (rounding
@@ -443,11 +491,16 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
             const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])).get();
             l += all.x + all.y;
         }
-        // (the buffer's last reader, P.V of two tiles before, was done before this S was)
+        // the buffer's last reader is P.V of two tiles before
+        if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarO + buf),
+                                                                 ((it - 2) >> 1) & 1)))
+            return false;
+        tc_fence_after();
+        const uint32_t t_p = tmem + lane_off + kPgColsP + buf * (kTile / 2) + base / 2;
         if constexpr (W == 64) tc_st32_u(t_p, w);
         else if constexpr (W == 32) tc_st16_u(t_p, w);
         else tc_st8_u(t_p, w);
-        if (t0 + kTile > u.kvend) {
+        if (t0 + kTile > kvend) {
             // Positions past the last visible one hold other data (or nothing): P is 0 there, but
             // 0 * NaN would still poison P.V, so those V rows are cleared once the copy landed.
             const uint32_t slot = it % kPgSlots;
@@ -455,14 +508,14 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
                                                            (it / kPgSlots) & 1)))
                 return false;
             uint8_t* vt = sm.v + slot * kTileBytes;
-            const int first = u.kvend - t0;
+            const int first = kvend - t0;
             for (int x = tid; x < (kTile - first) * 8; x += kRowThreads)
                 *reinterpret_cast<uint4*>(vt + swz(first + (x >> 3), x & 7)) =
                     make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async();
         }
         tc_fence_before();
-        mbar_arrive(sm.bar(kBarP + buf));
+        warp_arrive(sm.bar(kBarP + buf));
     }
     return true;
 }
@@ -484,14 +537,14 @@ __device__ __forceinline__ uint2 pack4(const float4& o, float inv) {
 // Every product of the unit is done.
 template <typename T, int REP>
 __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm, uint32_t tmem,
-                                            const Walk& u, bool whole, int64_t slot, float m,
+                                            const Walk& u, bool whole, int slot, float m,
                                             float l) {
     const int tid = threadIdx.x;
     constexpr int R = kPgRows / REP;
     const int r = tid & (R - 1), part = tid / R;
     const uint32_t t_o = tmem + ((uint32_t)(tid & ~31) << 16) + kPgColsO;
     T* dst = r < u.live ? out_row<T>(p, u, r) : nullptr;
-    float* wsp = p.ws_part + (slot * p.slot_rows + r) * kHeadDim;
+    float* wsp = p.ws_part + ((int64_t)slot * p.slot_rows + r) * kHeadDim;
     if constexpr (REP == 1) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
@@ -517,7 +570,7 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
                 }
             }
         }
-        if (!whole && r < u.live) p.ws_ml[slot * p.slot_rows + r] = make_float2(m, l);
+        if (!whole && r < u.live) p.ws_ml[(int64_t)slot * p.slot_rows + r] = make_float2(m, l);
     } else {
         // the copies' partials meet in the rows' shared memory (every S is done), 32 dims at a
         // time; copy `part` writes its share of the dims
@@ -567,46 +620,100 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
             }
         }
         if (!whole && part == 0 && r < u.live)
-            p.ws_ml[slot * p.slot_rows + r] = make_float2(top, all);
+            p.ws_ml[(int64_t)slot * p.slot_rows + r] = make_float2(top, all);
         rows_sync();  // the buffer is read before the next unit's rows are staged
     }
 }
 
 // A cut unit's pieces, which lie in the workspace: CTAs i0 .. i0 + n - 1, the last to arrive merges
-// them in that order.
+// them: a thread a quad of dims of a row and a share of the pieces, the shares in order.
 template <typename T>
-__device__ __forceinline__ void merge_pieces(const PagedParams& p, const Walk& u, uint32_t i0,
-                                             int n, int* s_last) {
+__device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& sm, const Walk& u,
+                                             uint32_t i0, int n, int* s_last) {
     const int tid = threadIdx.x;
-    __threadfence();
     rows_sync();
-    if (tid == 0) *s_last = atomicAdd(&p.ws_cnt[i0], 1) == n - 1;
+    if (tid == 0) {
+        // (released and acquired for the other threads of the block by the barriers around it)
+        int old;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(old)
+                     : "l"(p.ws_cnt + i0)
+                     : "memory");
+        *s_last = old == n - 1;
+    }
     rows_sync();
     if (!*s_last) return;
-    __threadfence();
-    for (int x = tid; x < u.live * (kHeadDim / 4); x += kRowThreads) {
-        const int r = x >> 4, d4 = x & 15;
-        auto at = [&](int i) { return (2 * (int64_t)(i0 + i) + (i == 0)) * p.slot_rows + r; };
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(&p.ws_ml[at(i)]).x);
-        const float ref = top == -INFINITY ? 0.f : top;
+    constexpr int kBatch = 6;  // pieces whose loads are in flight
+    const int items = u.live * (kHeadDim / 4);
+    const int shares = items >= kRowThreads ? 1 : min(kRowThreads / items, n);
+    float4* so = reinterpret_cast<float4*>(sm.q);          // [shares][items] (every S is done)
+    float2* sl = reinterpret_cast<float2*>(sm.q) + 2 * kRowThreads;
+    for (int x = tid; x < items * shares; x += kRowThreads) {
+        const int share = x / items, y = x - share * items;
+        const int r = y >> 4, d4 = y & 15;
+        const int first = n * share / shares, last = n * (share + 1) / shares;
+        float top = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float2 ml = __ldcg(&p.ws_ml[at(i)]);
-            const float4 y =
-                __ldcg(reinterpret_cast<const float4*>(p.ws_part + at(i) * kHeadDim) + d4);
-            const float f = exp2f(ml.x - ref);
-            l = fmaf(ml.y, f, l);
-            o.x = fmaf(y.x, f, o.x);
-            o.y = fmaf(y.y, f, o.y);
-            o.z = fmaf(y.z, f, o.z);
-            o.w = fmaf(y.w, f, o.w);
+        for (int i = first; i < last; i += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int c = min(i + k, last - 1);
+                const int64_t at = (2 * (int64_t)(i0 + c) + (c == 0)) * p.slot_rows + r;
+                ml[k] = __ldcg(&p.ws_ml[at]);
+                v[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_part + at * kHeadDim) + d4);
+            }
+            float t = top;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) t = fmaxf(t, ml[k].x);
+            const float ref = t == -INFINITY ? 0.f : t, f0 = exp2f(top - ref);
+            top = t;
+            l *= f0;
+            o.x *= f0;
+            o.y *= f0;
+            o.z *= f0;
+            o.w *= f0;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (i + k >= last) break;
+                const float f = exp2f(ml[k].x - ref);
+                l = fmaf(ml[k].y, f, l);
+                o.x = fmaf(v[k].x, f, o.x);
+                o.y = fmaf(v[k].y, f, o.y);
+                o.z = fmaf(v[k].z, f, o.z);
+                o.w = fmaf(v[k].w, f, o.w);
+            }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        *reinterpret_cast<uint2*>(out_row<T>(p, u, r) + d4 * 4) = pack4<T>(o, inv);
+        if (shares == 1) {
+            *reinterpret_cast<uint2*>(out_row<T>(p, u, r) + d4 * 4) =
+                pack4<T>(o, l > 0.f ? 1.f / l : 0.f);
+        } else {
+            so[x] = o;
+            sl[x] = make_float2(top, l);
+        }
+    }
+    if (shares > 1) {
+        rows_sync();
+        if (tid < items) {
+            float top = -INFINITY, l = 0.f;
+            for (int k = 0; k < shares; ++k) top = fmaxf(top, sl[k * items + tid].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < shares; ++k) {
+                const float2 ml = sl[k * items + tid];
+                const float4 v = so[k * items + tid];
+                const float f = exp2f(ml.x - ref);
+                l = fmaf(ml.y, f, l);
+                o.x = fmaf(v.x, f, o.x);
+                o.y = fmaf(v.y, f, o.y);
+                o.z = fmaf(v.z, f, o.z);
+                o.w = fmaf(v.w, f, o.w);
+            }
+            *reinterpret_cast<uint2*>(out_row<T>(p, u, tid >> 4) + (tid & 15) * 4) =
+                pack4<T>(o, l > 0.f ? 1.f / l : 0.f);
+        }
+        rows_sync();
     }
     if (tid == 0) p.ws_cnt[i0] = 0;
 }
@@ -625,50 +732,26 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     sm.ml = reinterpret_cast<float2*>(sm.q + kPgQBytes + 256);
     static_assert(kBarCount * 8 <= 256, "the barriers' place");
     __shared__ Place s_place;
-    __shared__ uint64_t s_from, s_to, s_total;
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_total, s_from, s_to, s_tmem;
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool mma_warp = warp == kRowThreads / 32, copy_warp = warp == kRowThreads / 32 + 1;
-    pdl_wait();
-    pdl_trigger();
-    if (warp == 0) {
-        uint64_t total;
-        find_row(p, ~0ull, total);
-        uint64_t from = 0, to = 0;
-        if (total > 0) {
-            const Shares sh = shares(total);
-            if (blockIdx.x < sh.ctas) {
-                from = cut(p, total, sh.start(blockIdx.x));
-                to = cut(p, total, sh.start(blockIdx.x + 1));
-            }
-        }
-        if (from < to) {
-            const Place u = find_unit(p, from);
-            if (lane == 0) s_place = u;
-        }
-        if (lane == 0) {
-            s_from = from;
-            s_to = to;
-            s_total = total;
-        }
-    } else if (copy_warp && lane == 0) {
+    if (copy_warp && lane == 0) {
         for (int i = 0; i < kBarCount; ++i)
-            mbar_init(sm.bar(i), i == kBarP || i == kBarP + 1 || i == kBarQ ? kRowThreads : 1);
+            mbar_init(sm.bar(i), i >= kBarRead && i < kBarP + 2 || i == kBarQ ? kRowThreads / 32
+                                                                               : 1);
         fence_barrier_init();
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
-    } else if (warp == 1) {
-        // rows that do not fit
-        for (int b = blockIdx.x + lane * gridDim.x; b < p.batch; b += 32 * gridDim.x) {
-            bool bad;
-            row_of(p, b, bad);
-            if (bad) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
-        }
     }
+    pdl_wait();
+    pdl_trigger();
+    const Table tab = fill_table(p, reinterpret_cast<uint32_t*>(sm.q));
     __syncthreads();
-    if (s_from >= s_to) return;
-    if (mma_warp) {
+    if (warp == 0) {
+        const uint32_t total = finish_table(tab);
+        if (lane == 0) s_total = total;
+    } else if (mma_warp) {
         tc_alloc(smem_u32(&s_tmem), kPgCols);
         tc_relinquish();
     }
@@ -676,9 +759,27 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    const Shares sh = shares(s_total);
+    // warp 0 finds where the stretch starts, warp 1 where it ends
+    if (warp < 2) {
+        const uint32_t at = sh.start(blockIdx.x + warp);
+        if (blockIdx.x >= sh.ctas || at >= s_total) {
+            if (lane == 0) *(warp ? &s_to : &s_from) = warp ? s_total : 0xffffffffu;
+        } else {
+            const Place u = find_unit(p, tab, at);
+            if (lane == 0) {
+                if (warp == 0) s_place = u;
+                *(warp ? &s_to : &s_from) = cut(u, at);
+            }
+        }
+    }
+    __syncthreads();
     Walk u;
-    u.start(p, s_place, s_from, s_to);
-    bool ok = true;
+    bool ok = u.start(p, s_place, s_from, s_to);
+    if (!ok) {
+        if (mma_warp) tc_dealloc(tmem, kPgCols);
+        return;
+    }
 
     if (copy_warp) {
         // ---- K/V tiles, a slot each ----
@@ -765,6 +866,10 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             for (int j = 0; ok && j < min(2, nt); ++j) ok = issue_s(it0 + j);
             for (int j = 0; ok && j < nt; ++j) {
                 const uint32_t it = it0 + j, buf = it & 1, slot = it % kPgSlots;
+                // the next S of the buffer as soon as the rows have read this one, while they
+                // form the weights
+                if (!(ok = wait_all(kBarRead + buf, (it >> 1) & 1))) break;
+                if (j + 2 < nt && !(ok = issue_s(it + 2))) break;
                 if (!(ok = wait_all(kBarP + buf, (it >> 1) & 1))) break;
                 tc_fence_after();
                 const uint32_t t_p = tmem + kPgColsP + buf * (kTile / 2);
@@ -779,7 +884,6 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                     tc_commit(sm.bar(kBarFree + slot));
                 }
                 __syncwarp();
-                if (j + 2 < nt) ok = issue_s(it + 2);
             }
             it0 += nt;
             ++units;
@@ -795,9 +899,6 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     } else {
         // ---- the rows ----
         uint32_t it0 = 0;
-        Shares sh;
-        sh.total = s_total;
-        sh.ctas = shares(s_total).ctas;
         do {
             const int rep = u.live > 64 ? 1 : u.live > 32 ? 2 : 4;
             const int r = tid & (kPgRows / rep - 1);
@@ -816,7 +917,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                 for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sm.q + swz(tid, c)) = qv[c];
                 fence_proxy_async();
             }
-            mbar_arrive(sm.bar(kBarQ));
+            warp_arrive(sm.bar(kBarQ));
             // keys t < lim are visible; rows past the unit's see all of it (and are not written)
             const int lim = live ? u.s.s0() + u.mb * p.tq + tok + 1 : u.kvend;
             float m, l;
@@ -832,7 +933,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             }
             tc_fence_after();
             const bool whole = u.v0 == 0 && u.v1 == u.tiles;
-            const int64_t slot = 2 * (int64_t)blockIdx.x + (u.v0 == 0);
+            const int slot = 2 * (int)blockIdx.x + (u.v0 == 0);
             if (rep == 1) finish_rows<T, 1>(p, sm, tmem, u, whole, slot, m, l);
             else if (rep == 2) finish_rows<T, 2>(p, sm, tmem, u, whole, slot, m, l);
             else finish_rows<T, 4>(p, sm, tmem, u, whole, slot, m, l);
@@ -840,7 +941,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                 // (the last share that starts before the unit's first cut, and before its last)
                 const uint32_t i0 = sh.holder(u.u0 + keep_lo(u.w) - 1);
                 const uint32_t i1 = sh.holder(u.u0 + keep_hi(u.w) - 1);
-                merge_pieces<T>(p, u, i0, (int)(i1 - i0) + 1, &s_last);
+                merge_pieces<T>(p, sm, u, i0, (int)(i1 - i0) + 1, &s_last);
             }
             tc_fence_before();  // O is read before the next unit's products
         } while (u.next(p));
@@ -855,30 +956,27 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
 
 constexpr int kMaxDevP = 64;
 
-// Once per kernel and device: its shared memory; the blocks resident at once (0: an error).
+// Once per kernel and device: its shared memory.
 template <typename T>
-int prepare_paged(int nsm) {
+bool prepare_paged() {
     static std::once_flag once[kMaxDevP];
-    static int blocks[kMaxDevP];
+    static bool ok[kMaxDevP];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevP) return 0;
-    std::call_once(once[dev], [dev, nsm] {
-        int n = 0;
-        if (cudaFuncSetAttribute(paged_attn_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kPgSmem) == cudaSuccess &&
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_attn_kernel<T>, kPgThreads,
-                                                          kPgSmem) == cudaSuccess)
-            blocks[dev] = std::min(kMaxCtas, nsm * std::min(n, kPgMinBlocks));
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevP) return false;
+    std::call_once(once[dev], [dev] {
+        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kPgSmem) == cudaSuccess;
         cudaGetLastError();
     });
-    return blocks[dev];
+    return ok[dev];
 }
 
 template <typename T>
 kvd_status run_paged(PagedParams& p, int nsm, const CUtensorMap& mk, const CUtensorMap& mv,
                      uint8_t* ws, bool pdl, cudaStream_t st) {
-    const int blocks = prepare_paged<T>(nsm);
-    if (blocks <= 0) return KVD_ERR_CUDA;
+    if (!prepare_paged<T>()) return KVD_ERR_CUDA;
+    const int blocks = std::min(kMaxCtas, nsm * kPgMinBlocks);
     p.ws_cnt = reinterpret_cast<int32_t*>(ws);
     p.ws_part = reinterpret_cast<float*>(ws + KVD_WS_COUNTER_BYTES);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_part + (size_t)2 * blocks * p.slot_rows * kHeadDim);
@@ -922,6 +1020,11 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
         return KVD_ERR_WORKSPACE;
     const int nsm = sm_count();
     if (nsm <= 0) return KVD_ERR_CUDA;
+    // the list of tiles, at its longest, is counted in 32 bits
+    const int tq = kPgRows / group;
+    const double blocks = (double)cache->n_kv_heads * ((double)n_tokens / tq + cache->batch);
+    const double longest = kHeavy * ((double)cache->table_width * cache->page_size / kTile + 1.);
+    if (blocks * (longest + kUnit) > 4e9) return KVD_ERR_UNSUPPORTED;
     CUtensorMap mk, mv;
     if (kvd_status s = encode_pool_map(&mk, dtype, cache->k, cache)) return s;
     if (kvd_status s = encode_pool_map(&mv, dtype, cache->v, cache)) return s;
@@ -941,7 +1044,7 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     p.n_q_heads = q->n_heads;
     p.n_kv_heads = cache->n_kv_heads;
     p.group = group;
-    p.tq = kPgRows / group;
+    p.tq = tq;
     p.n_pages = cache->n_pages;
     while ((1 << p.page_log2) < cache->page_size) ++p.page_log2;
     p.box_rows = std::min(kTile, cache->page_size);
