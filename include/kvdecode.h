@@ -665,8 +665,8 @@ kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32
  *
  * q        : n_heads query heads (a multiple of n_kv_heads, at most KVD_MAX_GROUP times it); out
  *            is the output, not x
- * lens     : device int32 [batch], positions of the row with its new tokens (>= n_b); row b's
- *            is not read when n_b is 0
+ * lens     : device int32 [batch], positions of the row with its new tokens (>= n_b; any
+ *            value where n_b is 0)
  * max_new  : an upper bound of n_b, >= 1 (a row above it is flagged); a tight one needs less
  *            workspace
  * workspace: kvd_workspace_size(KVD_OP_PAGED_ATTN, batch, n_heads, n_kv_heads, 1, max_new, ..)

@@ -49,8 +49,10 @@ constexpr uint32_t kPgCols = 256;
 static_assert(kPgCols >= kPgColsP + 2 * (kTile / 2) && kPgMinBlocks * kPgCols <= 512,
               "the resident blocks' tensor memory");
 constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
-// shared memory: K slots | V slots | Q | barriers | rows' references and sums
-constexpr uint32_t kPgSmem = 2 * kPgSlots * kTileBytes + kPgQBytes + 256 + kPgRows * 8 + 1024;
+constexpr int kMergeTable = 1024;              // (row, piece) pairs of a merge's step
+// shared memory: K slots | V slots | Q | barriers | rows' references and sums | merge
+constexpr uint32_t kPgSmem = 2 * kPgSlots * kTileBytes + kPgQBytes + 256 + kPgRows * 8 +
+                             kMergeTable * 8 + kRowThreads * 16 + 1024;
 constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
 
@@ -87,14 +89,11 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const PagedParams& p, int b, bool& bad) {
     Row r;
+    r.len = p.lens[b];
     bad = !row_tokens(p.starts, b, p.n_tokens, r.s, r.n);
-    r.len = 0;
-    if (r.n > 0) {
-        r.len = p.lens[b];
-        if (r.n > p.max_new || r.len < r.n || r.len > p.capacity) {
-            bad = true;
-            r.n = 0;
-        }
+    if (r.n > 0 && (r.n > p.max_new || r.len < r.n || r.len > p.capacity)) {
+        bad = true;
+        r.n = 0;
     }
     return r;
 }
@@ -372,6 +371,24 @@ __device__ __forceinline__ bool rows_any(bool x) {
         : "memory");
     return r != 0;
 }
+// Whether phase `parity` of the barrier is complete, without waiting. Asked for ahead of the use: an
+// answer takes about a hundred cycles.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// The warp's wait for a phase, of which `done` may tell that it is complete.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool done = false) {
+    if (__all_sync(0xffffffffu, done)) return true;
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
 // One arrival for the warp, behind what its lanes did.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     __syncwarp();
@@ -381,7 +398,9 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 struct Smem {
     uint8_t *k, *v, *q;
     uint64_t* bars;
-    float2* ml;   // [128]
+    float2* ml;      // [128]
+    float2* pieces;  // [kMergeTable]
+    float4* part;    // [128]
     __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&bars[i]); }
 };
 
@@ -414,11 +433,12 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
     }
     const int n = u.v1 - u.v0, kvend = u.kvend;
     int t0 = u.v0 * kTile;
+    bool s_done = false, p_free = false;
     for (int j = 0; j < n; ++j, t0 += kTile) {
         const uint32_t it = it0 + j, buf = it & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarS + buf), (it >> 1) & 1)))
-            return false;
+        if (!warp_wait(sm.bar(kBarS + buf), (it >> 1) & 1, s_done)) return false;
         tc_fence_after();
+        p_free = j < 2 || mbar_done(sm.bar(kBarO + buf), ((it - 2) >> 1) & 1);
         uint32_t w[W / 2];
         if (t0 + base >= lim_most) {
             // the warp sees nothing of it
@@ -462,9 +482,7 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
                 l *= factor;
                 if (j >= 1) {
                     // O is rescaled once P.V of the tile before is done
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarO + (buf ^ 1)),
-                                                                   ((it - 1) >> 1) & 1)))
-                        return false;
+                    if (!warp_wait(sm.bar(kBarO + (buf ^ 1)), ((it - 1) >> 1) & 1)) return false;
                     tc_fence_after();
                     float ov[32];
 #pragma unroll
@@ -491,10 +509,9 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
             const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])).get();
             l += all.x + all.y;
         }
+        s_done = j + 1 < n && mbar_done(sm.bar(kBarS + (buf ^ 1)), ((it + 1) >> 1) & 1);
         // the buffer's last reader is P.V of two tiles before
-        if (j >= 2 && !__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarO + buf),
-                                                                 ((it - 2) >> 1) & 1)))
-            return false;
+        if (!warp_wait(sm.bar(kBarO + buf), ((it - 2) >> 1) & 1, p_free)) return false;
         tc_fence_after();
         const uint32_t t_p = tmem + lane_off + kPgColsP + buf * (kTile / 2) + base / 2;
         if constexpr (W == 64) tc_st32_u(t_p, w);
@@ -504,9 +521,7 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
             // Positions past the last visible one hold other data (or nothing): P is 0 there, but
             // 0 * NaN would still poison P.V, so those V rows are cleared once the copy landed.
             const uint32_t slot = it % kPgSlots;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarFull + slot),
-                                                           (it / kPgSlots) & 1)))
-                return false;
+            if (!warp_wait(sm.bar(kBarFull + slot), (it / kPgSlots) & 1)) return false;
             uint8_t* vt = sm.v + slot * kTileBytes;
             const int first = kvend - t0;
             for (int x = tid; x < (kTile - first) * 8; x += kRowThreads)
@@ -626,11 +641,12 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
 }
 
 // A cut unit's pieces, which lie in the workspace: CTAs i0 .. i0 + n - 1, the last to arrive merges
-// them: a thread a quad of dims of a row and a share of the pieces, the shares in order.
+// them in that order. The pieces' weights are formed first, so that all loads of values are
+// independent.
 template <typename T>
 __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& sm, const Walk& u,
-                                             uint32_t i0, int n, int* s_last) {
-    const int tid = threadIdx.x;
+                                             int i0, int n, int* s_last) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     rows_sync();
     if (tid == 0) {
         // (released and acquired for the other threads of the block by the barriers around it)
@@ -643,77 +659,110 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
     }
     rows_sync();
     if (!*s_last) return;
-    constexpr int kBatch = 6;  // pieces whose loads are in flight
-    const int items = u.live * (kHeadDim / 4);
-    const int shares = items >= kRowThreads ? 1 : min(kRowThreads / items, n);
-    float4* so = reinterpret_cast<float4*>(sm.q);          // [shares][items] (every S is done)
-    float2* sl = reinterpret_cast<float2*>(sm.q) + 2 * kRowThreads;
-    for (int x = tid; x < items * shares; x += kRowThreads) {
-        const int share = x / items, y = x - share * items;
-        const int r = y >> 4, d4 = y & 15;
-        const int first = n * share / shares, last = n * (share + 1) / shares;
-        float top = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = first; i < last; i += kBatch) {
-            float2 ml[kBatch];
-            float4 v[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int c = min(i + k, last - 1);
-                const int64_t at = (2 * (int64_t)(i0 + c) + (c == 0)) * p.slot_rows + r;
-                ml[k] = __ldcg(&p.ws_ml[at]);
-                v[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_part + at * kHeadDim) + d4);
-            }
-            float t = top;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) t = fmaxf(t, ml[k].x);
-            const float ref = t == -INFINITY ? 0.f : t, f0 = exp2f(top - ref);
-            top = t;
-            l *= f0;
-            o.x *= f0;
-            o.y *= f0;
-            o.z *= f0;
-            o.w *= f0;
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (i + k >= last) break;
-                const float f = exp2f(ml[k].x - ref);
-                l = fmaf(ml[k].y, f, l);
-                o.x = fmaf(v[k].x, f, o.x);
-                o.y = fmaf(v[k].y, f, o.y);
-                o.z = fmaf(v[k].z, f, o.z);
-                o.w = fmaf(v[k].w, f, o.w);
-            }
-        }
-        if (shares == 1) {
-            *reinterpret_cast<uint2*>(out_row<T>(p, u, r) + d4 * 4) =
-                pack4<T>(o, l > 0.f ? 1.f / l : 0.f);
-        } else {
-            so[x] = o;
-            sl[x] = make_float2(top, l);
-        }
-    }
-    if (shares > 1) {
-        rows_sync();
-        if (tid < items) {
-            float top = -INFINITY, l = 0.f;
-            for (int k = 0; k < shares; ++k) top = fmaxf(top, sl[k * items + tid].x);
-            const float ref = top == -INFINITY ? 0.f : top;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < shares; ++k) {
-                const float2 ml = sl[k * items + tid];
-                const float4 v = so[k * items + tid];
-                const float f = exp2f(ml.x - ref);
-                l = fmaf(ml.y, f, l);
-                o.x = fmaf(v.x, f, o.x);
-                o.y = fmaf(v.y, f, o.y);
-                o.z = fmaf(v.z, f, o.z);
-                o.w = fmaf(v.w, f, o.w);
-            }
-            *reinterpret_cast<uint2*>(out_row<T>(p, u, tid >> 4) + (tid & 15) * 4) =
-                pack4<T>(o, l > 0.f ? 1.f / l : 0.f);
+    const int step = min(u.live, kMergeTable / n);  // rows at a time (n <= kMaxCtas)
+    auto slot = [&](int i) { return 2 * (i0 + i) + (i == 0); };
+    for (int r0 = 0; r0 < u.live; r0 += step) {
+        const int rows = min(step, u.live - r0);
+        float2* tab = sm.pieces;  // [n][rows]: reference and sum, then the weight
+        for (int x = tid; x < rows * n; x += kRowThreads) {
+            const int i = x / rows;
+            tab[x] = __ldcg(&p.ws_ml[(int64_t)slot(i) * p.slot_rows + r0 + (x - i * rows)]);
         }
         rows_sync();
+        if (n <= rows) {  // a thread per row
+            for (int r = tid; r < rows; r += kRowThreads) {
+                float top = -INFINITY, l = 0.f;
+                for (int i = 0; i < n; ++i) top = fmaxf(top, tab[i * rows + r].x);
+                const float ref = top == -INFINITY ? 0.f : top;
+                for (int i = 0; i < n; ++i) {
+                    const float2 ml = tab[i * rows + r];
+                    const float f = exp2f(ml.x - ref);
+                    l = fmaf(ml.y, f, l);
+                    tab[i * rows + r].x = f;
+                }
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                for (int i = 0; i < n; ++i) tab[i * rows + r].x *= inv;
+            }
+        } else {  // a warp per row
+            for (int r = warp; r < rows; r += kRowThreads / 32) {
+                float top = -INFINITY, l = 0.f;
+                for (int i = lane; i < n; i += 32) top = fmaxf(top, tab[i * rows + r].x);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float ref = top == -INFINITY ? 0.f : top;
+                for (int i = lane; i < n; i += 32) {
+                    const float2 ml = tab[i * rows + r];
+                    const float f = exp2f(ml.x - ref);
+                    l = fmaf(ml.y, f, l);
+                    tab[i * rows + r].x = f;
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                for (int i = lane; i < n; i += 32) tab[i * rows + r].x *= inv;
+            }
+        }
+        rows_sync();
+        const int items = rows * (kHeadDim / 4);  // (row, 4 dims)
+        auto part_of = [&](int i, int y) {
+            return __ldcg(reinterpret_cast<const float4*>(
+                              p.ws_part +
+                              ((int64_t)slot(i) * p.slot_rows + r0 + (y >> 4)) * kHeadDim) +
+                          (y & 15));
+        };
+        auto add = [](float4& o, const float4& v, float f) {
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+        };
+        auto store = [&](int y, const float4& o) {
+            *reinterpret_cast<uint2*>(out_row<T>(p, u, r0 + (y >> 4)) + (y & 15) * 4) =
+                pack4<T>(o, 1.f);
+        };
+        if (items >= 4 * kRowThreads) {  // many rows, few pieces: four items at a time
+            for (int x = tid; x < items; x += 4 * kRowThreads) {
+                float4 o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int i = 0; i < n; ++i) {
+                    float4 v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = part_of(i, min(x + k * kRowThreads, items - 1));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        add(o[k], v[k],
+                            tab[i * rows + (min(x + k * kRowThreads, items - 1) >> 4)].x);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (x + k * kRowThreads < items) store(x + k * kRowThreads, o[k]);
+            }
+        } else {  // few rows: their pieces shared out among threads, the shares added in order
+            const int shares = max(1, kRowThreads / items);
+            for (int x = tid; x < items * shares; x += kRowThreads) {
+                const int share = x / items, y = x - share * items;
+                const int last = n * (share + 1) / shares;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (int i = n * share / shares; i < last; ++i)
+                    add(o, part_of(i, y), tab[i * rows + (y >> 4)].x);
+                if (shares == 1) store(y, o);
+                else sm.part[x] = o;
+            }
+            if (shares > 1) {
+                rows_sync();
+                if (tid < items) {
+                    float4 o = sm.part[tid];
+                    for (int k = 1; k < shares; ++k) add(o, sm.part[k * items + tid], 1.f);
+                    store(tid, o);
+                }
+            }
+        }
+        rows_sync();  // the table is read
     }
     if (tid == 0) p.ws_cnt[i0] = 0;
 }
@@ -730,6 +779,8 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     sm.q = sm.v + kPgSlots * kTileBytes;
     sm.bars = reinterpret_cast<uint64_t*>(sm.q + kPgQBytes);
     sm.ml = reinterpret_cast<float2*>(sm.q + kPgQBytes + 256);
+    sm.pieces = sm.ml + kPgRows;
+    sm.part = reinterpret_cast<float4*>(sm.pieces + kMergeTable);
     static_assert(kBarCount * 8 <= 256, "the barriers' place");
     __shared__ Place s_place;
     __shared__ uint32_t s_total, s_from, s_to, s_tmem;
@@ -806,8 +857,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                     pg = p.n_pages;  // outside the tensor: zeros
                 }
                 if (it >= kPgSlots &&
-                    !__all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(kBarFree + slot),
-                                                               (it / kPgSlots - 1) & 1))) {
+                    !warp_wait(sm.bar(kBarFree + slot), (it / kPgSlots - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -839,57 +889,50 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
         constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
         constexpr uint32_t kIdS = tc_idesc_f16(kBf16, kPgRows, kTile, false);
         constexpr uint32_t kIdO = tc_idesc_f16(kBf16, kPgRows, kHeadDim, true);
-        const uint32_t qaddr = smem_u32(sm.q);
-        auto wait_all = [&](int i, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait_bounded(sm.bar(i), parity));
-        };
+        const uint64_t qdesc = tc_desc_sw128(smem_u32(sm.q));
+        const uint64_t kdesc = tc_desc_sw128(smem_u32(sm.k)), vdesc = tc_desc_sw128(smem_u32(sm.v));
+        constexpr uint64_t kTileDesc = kTileBytes / 16;  // a descriptor's addresses are in 16 bytes
+        const uint32_t lead = elect_one();
         auto issue_s = [&](uint32_t it) -> bool {
             const uint32_t slot = it % kPgSlots, buf = it & 1;
-            if (!wait_all(kBarFull + slot, (it / kPgSlots) & 1)) return false;
+            if (!warp_wait(sm.bar(kBarFull + slot), (it / kPgSlots) & 1)) return false;
             tc_fence_after();
-            const uint32_t kaddr = smem_u32(sm.k + slot * kTileBytes);
-            if (elect_one()) {
+            const uint64_t kd = kdesc + slot * kTileDesc;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_f16(tmem + buf * kTile, tc_desc_sw128(qaddr + kk * 32),
-                               tc_desc_sw128(kaddr + kk * 32), kIdS, kk);
-                tc_commit(sm.bar(kBarS + buf));
-            }
-            __syncwarp();
+            for (int kk = 0; kk < 4; ++kk)
+                tc_mma_f16_if(lead, tmem + buf * kTile, qdesc + kk * 2, kd + kk * 2, kIdS, kk > 0);
+            tc_commit_if(lead, sm.bar(kBarS + buf));
             return true;
         };
         uint32_t it0 = 0, units = 0;
         do {
             const int nt = u.v1 - u.v0;
-            if (!(ok = wait_all(kBarQ, units & 1))) break;
+            if (!(ok = warp_wait(sm.bar(kBarQ), units & 1))) break;
             tc_fence_after();
             for (int j = 0; ok && j < min(2, nt); ++j) ok = issue_s(it0 + j);
             for (int j = 0; ok && j < nt; ++j) {
                 const uint32_t it = it0 + j, buf = it & 1, slot = it % kPgSlots;
                 // the next S of the buffer as soon as the rows have read this one, while they
                 // form the weights
-                if (!(ok = wait_all(kBarRead + buf, (it >> 1) & 1))) break;
+                if (!(ok = warp_wait(sm.bar(kBarRead + buf), (it >> 1) & 1))) break;
                 if (j + 2 < nt && !(ok = issue_s(it + 2))) break;
-                if (!(ok = wait_all(kBarP + buf, (it >> 1) & 1))) break;
+                if (!(ok = warp_wait(sm.bar(kBarP + buf), (it >> 1) & 1))) break;
                 tc_fence_after();
                 const uint32_t t_p = tmem + kPgColsP + buf * (kTile / 2);
-                const uint32_t vaddr = smem_u32(sm.v + slot * kTileBytes);
-                if (elect_one()) {
+                const uint64_t vd = vdesc + slot * kTileDesc;
+                tc_mma_f16_tmem_a_if(lead, tmem + kPgColsO, t_p, vd, kIdO, j > 0);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_f16_tmem_a(tmem + kPgColsO, t_p + kk * 8,
-                                          tc_desc_sw128(vaddr + kk * 16 * kRowBytes), kIdO,
-                                          j > 0 || kk > 0);
-                    tc_commit(sm.bar(kBarO + buf));
-                    tc_commit(sm.bar(kBarFree + slot));
-                }
-                __syncwarp();
+                for (int kk = 1; kk < 4; ++kk)
+                    tc_mma_f16_tmem_a_if(lead, tmem + kPgColsO, t_p + kk * 8,
+                                         vd + kk * (16 * kRowBytes / 16), kIdO, 1);
+                tc_commit_if(lead, sm.bar(kBarO + buf));
+                tc_commit_if(lead, sm.bar(kBarFree + slot));
             }
             it0 += nt;
             ++units;
         } while (ok && u.next(p));
         if (!ok) {
-            if (elect_one()) {
+            if (lead) {
                 flag_error(p.dev_err, KVD_ERR_TIMEOUT);
                 tc_commit(sm.bar(kBarDrain));
                 mbar_wait_bounded(sm.bar(kBarDrain), 0);
@@ -899,32 +942,41 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     } else {
         // ---- the rows ----
         uint32_t it0 = 0;
-        do {
-            const int rep = u.live > 64 ? 1 : u.live > 32 ? 2 : 4;
-            const int r = tid & (kPgRows / rep - 1);
-            const int tok = r / p.group;
-            const bool live = r < u.live;
-            {
-                // this thread's query row (zeros past the unit's) into the swizzled A operand
-                const int hg = r - tok * p.group;
-                const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    p.q + t * p.q_st + (int64_t)(u.h * p.group + hg) * p.q_sh);
-                uint4 qv[8];
+        uint4 qv[8];
+        auto rep_of = [](int live) { return live > 64 ? 1 : live > 32 ? 2 : 4; };
+        // this thread's query row (zeros past the unit's)
+        auto load_q = [&](const Walk& u) {
+            const int r = tid & (kPgRows / rep_of(u.live) - 1);
+            const int tok = r / p.group, hg = r - tok * p.group;
+            const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.q + t * p.q_st + (int64_t)(u.h * p.group + hg) * p.q_sh);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) qv[c] = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < 8; ++c)
+                qv[c] = r < u.live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        // into the swizzled A operand
+        auto stage_q = [&]() {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sm.q + swz(tid, c)) = qv[c];
-                fence_proxy_async();
-            }
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sm.q + swz(tid, c)) = qv[c];
+            fence_proxy_async();
             warp_arrive(sm.bar(kBarQ));
+        };
+        load_q(u);
+        stage_q();
+        for (bool more = true; more;) {
+            const int rep = rep_of(u.live), r = tid & (kPgRows / rep - 1);
             // keys t < lim are visible; rows past the unit's see all of it (and are not written)
-            const int lim = live ? u.s.s0() + u.mb * p.tq + tok + 1 : u.kvend;
+            const int lim =
+                r < u.live ? u.s.s0() + u.mb * p.tq + r / p.group + 1 : u.kvend;
             float m, l;
             if (rep == 1) ok = run_rows<T, 1>(p, sm, tmem, u, it0, lim, m, l);
             else if (rep == 2) ok = run_rows<T, 2>(p, sm, tmem, u, it0, lim, m, l);
             else ok = run_rows<T, 4>(p, sm, tmem, u, it0, lim, m, l);
-            it0 += u.v1 - u.v0;
+            const Walk done = u;
+            more = u.next(p);
+            if (more) load_q(u);  // on their way while this unit ends
+            it0 += done.v1 - done.v0;
             const uint32_t last = it0 - 1;
             ok = ok && mbar_wait_bounded(sm.bar(kBarO + (last & 1)), (last >> 1) & 1);
             if (rows_any(!ok)) {
@@ -932,19 +984,20 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                 break;
             }
             tc_fence_after();
-            const bool whole = u.v0 == 0 && u.v1 == u.tiles;
-            const int slot = 2 * (int)blockIdx.x + (u.v0 == 0);
-            if (rep == 1) finish_rows<T, 1>(p, sm, tmem, u, whole, slot, m, l);
-            else if (rep == 2) finish_rows<T, 2>(p, sm, tmem, u, whole, slot, m, l);
-            else finish_rows<T, 4>(p, sm, tmem, u, whole, slot, m, l);
+            const bool whole = done.v0 == 0 && done.v1 == done.tiles;
+            const int slot = 2 * (int)blockIdx.x + (done.v0 == 0);
+            if (rep == 1) finish_rows<T, 1>(p, sm, tmem, done, whole, slot, m, l);
+            else if (rep == 2) finish_rows<T, 2>(p, sm, tmem, done, whole, slot, m, l);
+            else finish_rows<T, 4>(p, sm, tmem, done, whole, slot, m, l);
+            tc_fence_before();  // O is read before the next unit's products
+            if (more) stage_q();
             if (!whole) {
                 // (the last share that starts before the unit's first cut, and before its last)
-                const uint32_t i0 = sh.holder(u.u0 + keep_lo(u.w) - 1);
-                const uint32_t i1 = sh.holder(u.u0 + keep_hi(u.w) - 1);
-                merge_pieces<T>(p, sm, u, i0, (int)(i1 - i0) + 1, &s_last);
+                const uint32_t i0 = sh.holder(done.u0 + keep_lo(done.w) - 1);
+                const uint32_t i1 = sh.holder(done.u0 + keep_hi(done.w) - 1);
+                merge_pieces<T>(p, sm, done, (int)i0, (int)(i1 - i0) + 1, &s_last);
             }
-            tc_fence_before();  // O is read before the next unit's products
-        } while (u.next(p));
+        }
     }
     tc_fence_before();
     __syncthreads();
