@@ -11,18 +11,24 @@
 //
 // Design. One read of the row bounds many rows (HBM), the chain of a pass few.
 //  * A row is one block, or for few rows one cluster of blocks with a slice each, merged in the
-//    first block's shared memory. A block takes rounds of 4096 logits, 16 per thread, the next
-//    round's loads in flight. The chunk's maximum decides once per 16 logits whether the running
-//    maximum moves; sums are two-lane fp32.
-//  * Ranks: a compare and an add per logit and token; ids below the token count equal logits, ids
-//    above do not, so the threshold is set per vector of consecutive ids.
+//    first block's shared memory. A block takes rounds of 4096 logits, 16 per thread, which bulk
+//    copies bring into a ring in shared memory.
+//  * Per logit: y = x c - M c in one FMA (c = log2 e / T), its power of two, two sums, in two-lane
+//    fp32: 2.5 instructions. M is the block's largest of the first round, and a warp's own from
+//    where that is exceeded; only a warp whose chunk holds M itself tells it apart from the rest.
+//    What rounding M c shifts every y by is known and undone in the sums.
+//  * Ranks: a compare and half an add per logit and token, only for chunks that reach the token's
+//    logit; ids below the token count equal logits, ids above do not, so the threshold is set per
+//    vector of consecutive ids.
 //  * Alternatives: an id is one 64-bit key (order of the logit, then lower id). After the first
 //    round the n-th largest of 64 groups' maxima is a bound that at least n ids reach; from then
-//    on only ids that reach it go to a list, one compare per 16 logits. When the list grows the
-//    same step over its entries raises the bound, at least halving it whatever the order of the
-//    row, and at the end it leaves at most 128, ranked by counting.
+//    on a thread whose chunk exceeds it notes the chunk, one compare per 16 logits. Noted chunks
+//    are read again, their keys that reach the bound listed, and the same step over the list
+//    raises the bound: it leaves at most half of it, whatever the order of the row, and in the end
+//    at most 128 keys, ranked by counting.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "kvd_common.cuh"
 #include "kvd_internal.h"
@@ -34,15 +40,21 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kPer = 16;                          // logits per thread and round
 constexpr int kRound = kLpThreads * kPer;
-constexpr int kListSoft = 1000;                   // entries from which the list is cut down
-constexpr int kListCap = kListSoft + kRound + 32; // (a round adds kRound at most, the first 2 x 7)
+constexpr int kRingBytes = 3 * kRound * 4;         // 3 rounds of fp32, 6 of 16-bit logits
+constexpr int kLpStages = 6;
 constexpr int kGroups = 64;
-constexpr int kRanked = 128;                      // entries ranked by counting
+constexpr int kRanked = 128;                      // keys ranked by counting
+constexpr int kNotedSoft = 128;                   // noted chunks that are looked into at once
+constexpr int kNotedCap = kNotedSoft + kLpThreads;  // (a round notes one per thread at most)
+constexpr int kPass = 64;                         // noted chunks per pass
+constexpr int kListSoft = 256;                    // keys from which the list is cut
+constexpr int kListCap = kListSoft + kPass * kPer + 32;  // (and 2 x 7 from the row's ends)
 constexpr int kLpMaxCluster = 16;
-constexpr float kFar = -3.402823466e38f;          // for the distance to a logit of -inf in weight *
-                                                  // distance (0 * -inf is NaN)
+constexpr float kFar = -3.402823466e38f;          // for -inf in weight * exponent (0 * -inf is NaN)
 // Blocks a launch should have before rows are no longer split.
 constexpr int64_t kLpManyBlocks = 152 * 3;
+
+constexpr float kLn2 = 0.69314718056f;
 
 typedef unsigned long long Key;
 
@@ -64,14 +76,17 @@ struct LogprobParams {
 };
 
 // Sums of a part of a row: largest logit (-inf: none), how many have it, the others' weights
-// relative to it and their sum of weight * distance.
+// relative to it and their sum of weight * exponent (log2 units).
 struct Part {
     float m, n, rest, ent;
 };
-struct __align__(16) LpShared {
+struct __align__(128) LpShared {
+    uint8_t ring[kRingBytes];
     Key list[kListCap];
     Key group[kLpThreads];
+    int32_t noted[kNotedCap];                       // round * kLpThreads + thread
     Part part[kLpWarps];
+    float first[kLpWarps];                          // largest logits of the first round
     int32_t count[KVD_MAX_GIVEN];
     // of every CTA of the cluster, in the first one's: nothing else lies there, as the others
     // write it while the first may still be at its own slice
@@ -81,8 +96,9 @@ struct __align__(16) LpShared {
     int32_t token[KVD_MAX_GIVEN];
     float value[KVD_MAX_GIVEN];                     // the tokens' logits
     int32_t place[kGroups];
+    uint64_t bars[kLpStages];
     Key bound;
-    int32_t n_list;
+    int32_t n_list, n_noted;
 };
 
 // Order-preserving image of a logit (not NaN, -0 as +0) above the complement of the id.
@@ -106,6 +122,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
+// -1 if v >= at, else 0 (one compare, and half a three-input add).
+__device__ __forceinline__ int at_least(float v, float at) {
+    int d;
+    asm("set.ge.s32.f32 %0, %1, %2;" : "=r"(d) : "f"(v), "f"(at));
+    return d;
+}
 // The next fp32 above v; NaN, which nothing reaches, above +inf.
 __device__ __forceinline__ float next_up(float v) {
     if (!(v < INFINITY)) return __uint_as_float(0x7fffffffu);
@@ -127,10 +149,10 @@ __device__ __forceinline__ Part join(const Part& a, const Part& b, float c) {
             r.rest += x.rest;
             r.ent += x.ent;
         } else if (x.m > -INFINITY) {
-            const float d = x.m - r.m, f = exp2f(d * c), s = x.n + x.rest;
+            const float y = (x.m - r.m) * c, f = exp2f(y), s = x.n + x.rest;
             if (f > 0.f) {
                 r.rest = fmaf(s, f, r.rest);
-                r.ent = fmaf(f, fmaf(d, s, x.ent), r.ent);
+                r.ent = fmaf(f, fmaf(y, s, x.ent), r.ent);
             }
         }
     }
@@ -145,46 +167,74 @@ __device__ __forceinline__ Part shfl_part(const Part& a, int off) {
     return r;
 }
 
-// One thread's chunk of a round joins its sums; cm: the chunk's largest, above -inf.
-template <int N>
-__device__ __forceinline__ void add_chunk(Part& a, const float (&x)[N], float cm, float c) {
-    if (cm > a.m) {
+// The largest of the warp's values (none is NaN).
+__device__ __forceinline__ float warp_max(float v) {
+    float d;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    return d;
+}
+// A thread's running sums: exponents are x c + mc, mc = -m c rounded, and lo what that lacks.
+struct Sums {
+    Part a;
+    float c, mc, lo;
+    __device__ __forceinline__ void set_reference(float m) {
+        a.m = m;
+        mc = -(m * c);
+        lo = -fmaf(m, c, mc);
+        if (!(fabsf(lo) < INFINITY)) lo = 0.f;  // (then no exponent by mc is finite)
+    }
+    // lo goes into the sums.
+    __device__ __forceinline__ void settle() {
+        const float f = exp2f(lo);
+        a.ent = f * fmaf(lo, a.rest, a.ent);
+        a.rest *= f;
+    }
+    __device__ __forceinline__ void raise_to(float m) {
+        if (!(m > a.m)) return;
         if (a.m > -INFINITY) {
-            const float d = a.m - cm, f = exp2f(d * c), s = a.n + a.rest;
+            settle();
+            const float y = (a.m - m) * c, f = exp2f(y), s = a.n + a.rest;
             a.rest = s * f;
-            a.ent = f > 0.f ? f * fmaf(d, s, a.ent) : 0.f;
+            a.ent = f > 0.f ? f * fmaf(y, s, a.ent) : 0.f;
         }
         a.n = 0.f;
-        a.m = cm;
+        set_reference(m);
     }
-    if (cm == a.m) {  // (rarely: the row's maximum moves a few times per thread)
+    __device__ __forceinline__ void add_one(float x) {
+        if (x == a.m) {
+            a.n += 1.f;
+        } else {
+            const float y = (x - a.m) * c - lo, e = ex2_approx(y);
+            a.rest += e;
+            a.ent = fmaf(e, fmaxf(y, kFar), a.ent);
+        }
+    }
+    // None of the logits is above a.m, which is above -inf. top: whether any of the warp's is a.m.
+    template <int N>
+    __device__ __forceinline__ void add_chunk(const float (&x)[N], bool top) {
+        if (!top) {
+            Pair r[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)}, t[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
+            const Pair cc(c, c), mm(mc, mc);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (x[i] == a.m) {
-                a.n += 1.f;
-            } else {
-                const float d = x[i] - a.m, e = ex2_approx(d * c);
-                a.rest += e;
-                a.ent = fmaf(e, fmaxf(d, kFar), a.ent);
+            for (int i = 0; i < N; i += 2) {
+                const Pair y = fma2(Pair(x[i], x[i + 1]), cc, mm);
+                const float2 z = y.get();
+                const Pair e(ex2_approx(z.x), ex2_approx(z.y));
+                r[(i >> 1) & 1] = add2(r[(i >> 1) & 1], e);
+                t[(i >> 1) & 1] = fma2(e, y, t[(i >> 1) & 1]);
+            }
+            const float2 rs = add2(r[0], r[1]).get(), ts = add2(t[0], t[1]).get();
+            const float ent = ts.x + ts.y;
+            if (ent == ent) {  // (a logit of -inf: 0 * -inf is NaN)
+                a.rest += rs.x + rs.y;
+                a.ent += ent;
+                return;
             }
         }
-        return;
-    }
-    Pair r[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)}, t[2] = {Pair(0.f, 0.f), Pair(0.f, 0.f)};
-    const Pair neg(-a.m, -a.m), cc(c, c);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const Pair dd = add2(Pair(x[i], x[i + 1]), neg);
-        const float2 d = dd.get(), y = mul2(dd, cc).get();
-        const Pair e(ex2_approx(y.x), ex2_approx(y.y));
-        r[(i >> 1) & 1] = add2(r[(i >> 1) & 1], e);
-        t[(i >> 1) & 1] =
-            fma2(e, Pair(fmaxf(d.x, kFar), fmaxf(d.y, kFar)), t[(i >> 1) & 1]);
+        for (int i = 0; i < N; ++i) add_one(x[i]);
     }
-    const float2 rs = add2(r[0], r[1]).get(), ts = add2(t[0], t[1]).get();
-    a.rest += rs.x + rs.y;
-    a.ent += ts.x + ts.y;
-}
+};
 
 template <typename T> struct Vec;  // 16 bytes of logits
 template <> struct Vec<float> {
@@ -209,14 +259,6 @@ template <> struct Vec<__nv_bfloat16> {
     }
     static __device__ __forceinline__ float one(__nv_bfloat16 v) { return __bfloat162float(v); }
 };
-__device__ __forceinline__ uint4 load_stream(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 // S.bound: the n-th largest of 64 groups' largest keys, out of S.group[t], a key per thread
 // (thread t's group is t % 64). All threads; the caller has not synchronised since its write.
 __device__ __forceinline__ void set_bound(LpShared& S, int n) {
@@ -293,6 +335,40 @@ __device__ __forceinline__ void rank_list(LpShared& S, int n, Key* out) {
 
 __device__ __forceinline__ void push(LpShared& S, Key k) { S.list[atomicAdd(&S.n_list, 1)] = k; }
 
+// The noted chunks' keys that reach the bound go to the list, which is cut as it grows. x: the
+// row's first whole vector, of id `id0`; `vecs` of them. All threads, after a barrier; ends with
+// one.
+template <typename T>
+__device__ __noinline__ void look_into(LpShared& S, const T* x, int id0, int vecs, int n) {
+    constexpr int VN = Vec<T>::n, NV = kPer / VN;
+    const int tid = threadIdx.x, have = S.n_noted;
+    for (int c0 = 0; c0 < have; c0 += kPass) {
+        const int i = c0 + tid / NV;
+        if (tid < kPass * NV && i < have) {
+            const int chunk = S.noted[i], r = chunk / kLpThreads;
+            const int v = (r * NV + tid % NV) * kLpThreads + chunk % kLpThreads;
+            if (v < vecs) {
+                float f[VN];
+                Vec<T>::get(__ldg(reinterpret_cast<const uint4*>(x) + v), f);
+                const Key bound = S.bound;
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    if (f[e] > -INFINITY) {  // (not NaN)
+                        const Key k = make_key(f[e], id0 + v * VN + e);
+                        if (k >= bound) push(S, k);
+                    }
+            }
+        }
+        __syncthreads();
+        if (S.n_list > kListSoft) {
+            while (S.n_list > kRanked) cut_list(S, n);
+        }
+        __syncthreads();  // nobody adds before all have seen the count
+    }
+    if (tid == 0) S.n_noted = 0;
+    __syncthreads();
+}
+
 __device__ __forceinline__ void st_cluster_key(void* local, int rank, Key v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(
                      map_shared(smem_u32(local), (uint32_t)rank)),
@@ -308,16 +384,24 @@ __device__ __forceinline__ void st_cluster_word(void* local, int rank, uint32_t 
 
 // GIVEN: 0 no ranks; 1 one token per row; 2 up to KVD_MAX_GIVEN.
 template <typename T, int GIVEN>
-__global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
+__global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 3)
     token_logprobs_kernel(const LogprobParams p) {
-    extern __shared__ __align__(16) uint8_t lp_smem[];
-    LpShared& S = *reinterpret_cast<LpShared*>(lp_smem);
+    extern __shared__ uint8_t lp_smem[];
+    LpShared& S = *reinterpret_cast<LpShared*>(
+        (reinterpret_cast<uintptr_t>(lp_smem) + 127) & ~uintptr_t(127));
     constexpr int VN = Vec<T>::n, NV = kPer / VN;
+    constexpr int kStageBytes = kRound * (int)sizeof(T), kStages = kRingBytes / kStageBytes;
+    static_assert(kStages <= kLpStages, "a barrier per stage");
     constexpr int kTok = GIVEN == 2 ? KVD_MAX_GIVEN : 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)(blockIdx.x % (unsigned)p.cluster);
     const int row = (int)(blockIdx.x / (unsigned)p.cluster);
     if (p.cluster > 1) cluster_arrive_relaxed();
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&S.bars[i]), 1);
+        fence_barrier_init();
+        S.n_list = S.n_noted = 0;
+    }
     pdl_wait();
     pdl_trigger();
     const T* x = static_cast<const T*>(p.x) + row * p.stride;
@@ -326,18 +410,18 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     const int off = (int)((reinterpret_cast<uintptr_t>(x + lo) / sizeof(T)) % VN);
     const int body = min(hi, lo + (off ? VN - off : 0));
     const int vecs = (hi - body) / VN, tail = body + vecs * VN;
-    uint4 buf[NV];
-    auto fetch = [&](int r) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int v = (r * NV + k) * kLpThreads + tid;
-            if (v < vecs) buf[k] = load_stream(x + body + v * VN);
-        }
+    const int rounds = (vecs + NV * kLpThreads - 1) / (NV * kLpThreads);
+    auto copy = [&](int r) {  // one thread
+        const int at = r * kStageBytes, bytes = min(kStageBytes, vecs * 16 - at);
+        const uint32_t bar = smem_u32(&S.bars[r % kStages]);
+        mbar_expect_tx(bar, bytes);
+        bulk_load(smem_u32(S.ring + r % kStages * kStageBytes),
+                  reinterpret_cast<const uint8_t*>(x + body) + at, bytes, bar);
     };
-    fetch(0);
+    if (tid == 0)
+        for (int r = 0; r < min(kStages, rounds); ++r) copy(r);
     const float T_ = p.temperature ? p.temperature[row] : 1.f;
     const bool bad_t = !(T_ > 0.f) || !(T_ < INFINITY);
-    const float c = kLog2e / T_;
     if (tid < p.given) {
         const int t = p.tokens[(int64_t)row * p.given + tid];
         const bool in = t >= 0 && t < p.vocab;
@@ -346,7 +430,17 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
         S.count[tid] = 0;
         if (!in && t != -1 && rank == 0) flag_error(p.dev_err, KVD_ERR_BAD_TOKEN);
     }
-    if (tid == 0) S.n_list = 0;
+    // the ends that are not whole vectors: one logit of a thread
+    float end_v = -INFINITY;
+    int end_id = -1;
+    bool nan = false;
+    if (tid < body - lo) end_id = lo + tid;
+    else if (tid >= 32 && tid - 32 < hi - tail) end_id = tail + tid - 32;
+    if (end_id >= 0) {
+        const float one = Vec<T>::one(x[end_id]);
+        nan = one != one;
+        end_v = fmaxf(one, -INFINITY);
+    }
     __syncthreads();
     int tok[kTok], cnt[kTok];
     float val[kTok], val_up[kTok];
@@ -357,51 +451,56 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
             tok[i] = S.token[i];
             val[i] = S.value[i];
             val_up[i] = next_up(val[i]);
+            if (end_id >= 0)
+                cnt[i] -= end_v > val[i] || (end_v == val[i] && end_id < tok[i]);
         }
     }
-    // before[i] += 1 for a logit v of id `id` ahead of token i
-    auto count_one = [&](float v, int id) {
-#pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (GIVEN && (GIVEN == 1 || i < p.given))
-                cnt[i] += v > val[i] || (v == val[i] && id < tok[i]);
-    };
 
-    Part a = {-INFINITY, 0.f, 0.f, 0.f};
-    bool nan = false;
-    // the ends that are not whole vectors: one logit of a thread
-    float end_v = -INFINITY;
-    int end_id = 0;
-    if (tid < body - lo) end_id = lo + tid;
-    else if (tid >= 32 && tid - 32 < hi - tail) end_id = tail + tid - 32;
-    else end_id = -1;
-    if (end_id >= 0) {
-        const float one[1] = {Vec<T>::one(x[end_id])};
-        nan = one[0] != one[0];
-        end_v = fmaxf(one[0], -INFINITY);
-        if (end_v > -INFINITY) {
-            a.m = end_v;
-            a.n = 1.f;
-        }
-        if (GIVEN) count_one(end_v, end_id);
-    }
-
-    const int rounds = max(1, (vecs + NV * kLpThreads - 1) / (NV * kLpThreads));
+    Sums sum;
+    sum.a = {-INFINITY, 0.f, 0.f, 0.f};
+    sum.c = kLog2e / T_;
+    sum.mc = sum.lo = 0.f;
     float bound_v = -INFINITY;  // of S.bound
-    for (int r = 0; r < rounds; ++r) {
+    // The first round's largest logits and bound. cm: the thread's largest, of id `id`.
+    auto begin = [&](float cm, int id) {
+        const float w = warp_max(fmaxf(cm, end_v));
+        if (lane == 0) S.first[warp] = w;
+        if (p.top > 0) {
+            const bool head = end_v > -INFINITY && end_id < body;
+            const Key mine = head ? make_key(end_v, end_id) : 0;
+            S.group[tid] = max(mine, cm > -INFINITY ? make_key(cm, id) : 0);
+            set_bound(S, p.top);
+            const Key bound = S.bound;
+            bound_v = bound == 1 ? -INFINITY : key_value(bound);
+            if (head && mine >= bound) push(S, mine);
+        } else {
+            __syncthreads();
+        }
+        float m = S.first[0];
+#pragma unroll
+        for (int k = 1; k < kLpWarps; ++k) m = fmaxf(m, S.first[k]);
+        if (m > -INFINITY) {
+            sum.set_reference(m);
+            if (end_v > -INFINITY) sum.add_one(end_v);
+        }
+    };
+    bool dead = false, full = false;
+    // One round; MASKED: the first, or one with vectors that lie behind the slice.
+    auto round = [&](int r, auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        dead = dead || !mbar_wait_bounded(smem_u32(&S.bars[r % kStages]), (r / kStages) & 1);
+        const uint4* st = reinterpret_cast<const uint4*>(S.ring + r % kStages * kStageBytes) + tid;
+        const int v0 = r * NV * kLpThreads + tid;  // the thread's first vector; kLpThreads apart
         float v[kPer];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            Vec<T>::get(buf[k], v + k * VN);
-            if ((r * NV + k) * kLpThreads + tid >= vecs) {
+            if (!MASKED || v0 + k * kLpThreads < vecs) {
+                Vec<T>::get(st[k * kLpThreads], v + k * VN);
+            } else {
 #pragma unroll
                 for (int i = 0; i < VN; ++i) v[k * VN + i] = -INFINITY;
             }
         }
-        if (r + 1 < rounds) fetch(r + 1);
-        auto id_of = [&](int i) {
-            return body + ((r * NV + i / VN) * kLpThreads + tid) * VN + i % VN;
-        };
         auto largest = [&]() {
             float q[4];
 #pragma unroll
@@ -416,70 +515,78 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
             for (int i = 0; i < kPer; ++i) v[i] = fmaxf(v[i], -INFINITY);
             cm = largest();
         }
-        if (cm > -INFINITY) add_chunk(a, v, cm, c);
+        if (MASKED && r == 0) {
+            int id = 0;
+            if (p.top > 0) {
+#pragma unroll
+                for (int i = kPer - 1; i >= 0; --i)
+                    if (v[i] == cm) id = body + (v0 + i / VN * kLpThreads) * VN + i % VN;
+            }
+            begin(cm, id);
+        }
+        const float top_of = warp_max(cm);
+        if (top_of > -INFINITY) {  // (the same in the whole warp, like the reference)
+            sum.raise_to(top_of);
+            if (!MASKED || cm > -INFINITY) sum.add_chunk(v, top_of == sum.a.m);
+        }
         if (GIVEN) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int id0 = id_of(k * VN);
-                if (id0 >= tail) break;
+            for (int i = 0; i < kTok; ++i) {
+                if (GIVEN == 2 && i >= p.given) break;
+                if (cm < val[i]) continue;
 #pragma unroll
-                for (int i = 0; i < kTok; ++i) {
-                    if (GIVEN == 2 && i >= p.given) break;
+                for (int k = 0; k < NV; ++k) {
+                    if (MASKED && v0 + k * kLpThreads >= vecs) break;
                     // ids below the token's count equal logits
+                    const int id0 = body + (v0 + k * kLpThreads) * VN;
                     const float at = id0 < tok[i] ? val[i] : val_up[i];
-                    if (tok[i] - id0 < VN && tok[i] > id0) {
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) cnt[i] += at_least(v[k * VN + e], at);
+                    // (of the vector that holds the token, those from it on do not)
+                    if ((unsigned)(tok[i] - id0 - 1) < (unsigned)(VN - 1)) {
 #pragma unroll
                         for (int e = 0; e < VN; ++e)
-                            cnt[i] += v[k * VN + e] > val[i] ||
-                                      (v[k * VN + e] == val[i] && id0 + e < tok[i]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VN; ++e) cnt[i] += v[k * VN + e] >= at;
+                            cnt[i] += id0 + e >= tok[i] && v[k * VN + e] == val[i];
                     }
                 }
             }
         }
-        if (p.top > 0) {
-            if (r == 0) {
-                // a bound that at least `top` ids of the round reach
-                Key best = end_v > -INFINITY ? make_key(end_v, end_id) : 0;
-                if (cm > -INFINITY) {
-                    int id = 0;
-#pragma unroll
-                    for (int i = kPer - 1; i >= 0; --i)
-                        if (v[i] == cm) id = id_of(i);
-                    best = max(best, make_key(cm, id));
-                }
-                S.group[tid] = best;
-                set_bound(S, p.top);
-                const Key bound = S.bound;
-                bound_v = bound == 1 ? -INFINITY : key_value(bound);
-                if (end_v > -INFINITY && make_key(end_v, end_id) >= bound)
-                    push(S, make_key(end_v, end_id));
+        // (later ids need more than the bound's logit)
+        if (p.top > 0 && (MASKED && r == 0 ? cm >= bound_v : cm > bound_v) && cm > -INFINITY) {
+            const int at = atomicAdd(&S.n_noted, 1);
+            S.noted[at] = r * kLpThreads + tid;
+            full = at >= kNotedSoft;
+        }
+    };
+    int issued = min(kStages, rounds);
+    bool lost = false;
+    if (rounds == 0) begin(-INFINITY, 0);
+    for (int r = 0; r < rounds; ++r) {
+        full = false;
+        if (r > 0 && (r + 1) * NV * kLpThreads <= vecs) round(r, std::false_type{});
+        else round(r, std::true_type{});
+        if (r + 1 == rounds) break;
+        // the stage is read; (nobody notes a chunk while they are looked into)
+        if (__syncthreads_or(dead || full)) {
+            if ((lost = __syncthreads_or(dead))) break;
+            look_into<T>(S, x + body, body, vecs, p.top);
+            const Key bound = S.bound;
+            bound_v = bound == 1 ? -INFINITY : key_value(bound);
+        }
+        if (issued < rounds) {
+            if (tid == 0) {
+                fence_proxy_async();
+                copy(issued);
             }
-            if (cm >= bound_v && cm > -INFINITY) {
-                const Key bound = S.bound;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (v[i] >= bound_v && v[i] > -INFINITY) {
-                        const Key k = make_key(v[i], id_of(i));
-                        if (k >= bound) push(S, k);
-                    }
-            }
-            if (r + 1 < rounds) {
-                __syncthreads();
-                if (S.n_list > kListSoft) {  // uniform: nobody adds before the next barrier
-                    while (S.n_list > kListSoft / 4) cut_list(S, p.top);
-                    const Key bound = S.bound;
-                    bound_v = bound == 1 ? -INFINITY : key_value(bound);
-                }
-                __syncthreads();
-            }
+            ++issued;
         }
     }
 
     // ---- the block's sums and counts ----
     if (nan) flag_error(p.dev_err, KVD_ERR_NAN);
+    if (sum.a.m > -INFINITY) sum.settle();
+    Part a = sum.a;
+    const float c = sum.c;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = join(a, shfl_part(a, o), c);
     if (lane == 0) S.part[warp] = a;
@@ -488,17 +595,32 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
         for (int i = 0; i < kTok; ++i) {
             if (GIVEN == 2 && i >= p.given) break;
             const int n = __reduce_add_sync(0xffffffffu, cnt[i]);
-            if (lane == 0) atomicAdd(&S.count[i], n);
+            if (lane == 0) atomicSub(&S.count[i], n);
         }
     }
-    __syncthreads();
+    // (a wait that ran out: the copies in flight land before the block leaves, and it writes
+    // nothing; a cluster's blocks all pass its barriers)
+    if (__syncthreads_or(dead)) lost = true;
+    if (lost && tid == 0) {
+        flag_error(p.dev_err, KVD_ERR_TIMEOUT);
+        for (int r = max(0, issued - kStages); r < issued; ++r)
+            mbar_wait_bounded(smem_u32(&S.bars[r % kStages]), (r / kStages) & 1);
+    }
     if (tid == 0) {
 #pragma unroll 1
         for (int w = 1; w < kLpWarps; ++w) a = join(a, S.part[w], c);
     }
-    // ---- the cluster's, in its first block ----
     Key* best = S.group;  // [top]
-    if (p.top > 0) rank_list(S, p.top, best);
+    if (p.top > 0) {
+        if (S.n_noted > 0 && !lost) look_into<T>(S, x + body, body, vecs, p.top);
+        if (end_id >= body && end_v > -INFINITY) {
+            const Key k = make_key(end_v, end_id);
+            if (k >= S.bound) push(S, k);
+        }
+        __syncthreads();
+        rank_list(S, p.top, best);
+    }
+    // ---- the cluster's, in its first block ----
     if (p.cluster > 1) {
         cluster_wait();  // every block has started: its shared memory can be written
         if (tid < p.top) st_cluster_key(&S.ex_key[rank * p.top + tid], 0, best[tid]);
@@ -529,8 +651,8 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
         __syncthreads();
         if (p.top > 0) rank_list(S, p.top, best);
     }
-    if (bad_t) {
-        if (tid == 0) flag_error(p.dev_err, KVD_ERR_BAD_PARAM);
+    if (bad_t || lost) {
+        if (bad_t && tid == 0) flag_error(p.dev_err, KVD_ERR_BAD_PARAM);
         return;
     }
     // ---- the outputs ----
@@ -559,10 +681,11 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     if (tid == 0) {
         if (p.lse) p.lse[row] = none ? -INFINITY : a.m / T_ + log_s;
         if (p.entropy)
-            p.entropy[row] = none ? 0.f : log_s - a.ent / T_ / (a.n + a.rest);
+            p.entropy[row] = none ? 0.f : log_s - a.ent * kLn2 / (a.n + a.rest);
     }
 }
 
+constexpr size_t kLpSmem = sizeof(LpShared) + 128;
 constexpr int kMaxDevL = 64;
 
 // Once per kernel and device: shared memory, clusters of 16.
@@ -574,7 +697,7 @@ bool prepare_logprobs() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevL) return false;
     std::call_once(once[dev], [&] {
         ok[dev] = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(LpShared)) == cudaSuccess &&
+                                       (int)kLpSmem) == cudaSuccess &&
                   cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
                       cudaSuccess;
         cudaGetLastError();
@@ -587,7 +710,7 @@ kvd_status run(const LogprobParams& p, bool pdl, cudaStream_t st) {
     constexpr auto kern = token_logprobs_kernel<T, GIVEN>;
     if (!prepare_logprobs<kern>()) return KVD_ERR_CUDA;
     return launch_ex(kern, dim3((unsigned)p.rows * (unsigned)p.cluster), dim3(kLpThreads),
-                     sizeof(LpShared), st, pdl, (unsigned)p.cluster, p);
+                     kLpSmem, st, pdl, (unsigned)p.cluster, p);
 }
 template <typename T>
 kvd_status run_type(const LogprobParams& p, bool pdl, cudaStream_t st) {
