@@ -40,11 +40,11 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kPer = 16;                          // logits per thread and round
 constexpr int kRound = kLpThreads * kPer;
-constexpr int kRingBytes = 3 * kRound * 4;         // 3 rounds of fp32, 6 of 16-bit logits
-constexpr int kLpStages = 6;
+constexpr int kRingBytes = 2 * kRound * 4;         // 2 rounds of fp32, 4 of 16-bit logits
+constexpr int kLpStages = 4;
 constexpr int kGroups = 64;
 constexpr int kRanked = 128;                      // keys ranked by counting
-constexpr int kNotedSoft = 128;                   // noted chunks that are looked into at once
+constexpr int kNotedSoft = 64;                    // noted chunks from which they are looked into
 constexpr int kNotedCap = kNotedSoft + kLpThreads;  // (a round notes one per thread at most)
 constexpr int kPass = 64;                         // noted chunks per pass
 constexpr int kListSoft = 256;                    // keys from which the list is cut
@@ -365,6 +365,7 @@ __device__ __noinline__ void look_into(LpShared& S, const T* x, int id0, int vec
         }
         __syncthreads();  // nobody adds before all have seen the count
     }
+    if (S.n_list > kGroups) cut_list(S, n);  // a higher bound for what comes
     if (tid == 0) S.n_noted = 0;
     __syncthreads();
 }
@@ -384,7 +385,7 @@ __device__ __forceinline__ void st_cluster_word(void* local, int rank, uint32_t 
 
 // GIVEN: 0 no ranks; 1 one token per row; 2 up to KVD_MAX_GIVEN.
 template <typename T, int GIVEN>
-__global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 3)
+__global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     token_logprobs_kernel(const LogprobParams p) {
     extern __shared__ uint8_t lp_smem[];
     LpShared& S = *reinterpret_cast<LpShared*>(
@@ -490,7 +491,8 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 3)
         constexpr bool MASKED = decltype(masked)::value;
         dead = dead || !mbar_wait_bounded(smem_u32(&S.bars[r % kStages]), (r / kStages) & 1);
         const uint4* st = reinterpret_cast<const uint4*>(S.ring + r % kStages * kStageBytes) + tid;
-        const int v0 = r * NV * kLpThreads + tid;  // the thread's first vector; kLpThreads apart
+        // the thread's first vector; kLpThreads apart
+        const int v0 = r * NV * kLpThreads + tid;
         float v[kPer];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -552,10 +554,30 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 3)
             }
         }
         // (later ids need more than the bound's logit)
-        if (p.top > 0 && (MASKED && r == 0 ? cm >= bound_v : cm > bound_v) && cm > -INFINITY) {
+        const bool note = p.top > 0 && cm > -INFINITY &&
+                          (MASKED && r == 0 ? cm >= bound_v : cm > bound_v);
+        if (note) {
             const int at = atomicAdd(&S.n_noted, 1);
             S.noted[at] = r * kLpThreads + tid;
             full = at >= kNotedSoft;
+        }
+        if (MASKED && rounds == 1 && p.top > 0) {
+            // a short slice: straight to the list, while the logits are at hand
+            __syncthreads();
+            const int noted = S.n_noted;
+            __syncthreads();
+            if (noted <= kPass) {
+                if (tid == 0) S.n_noted = 0;
+                if (note) {
+                    const Key bound = S.bound;
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) {
+                        const Key k =
+                            make_key(v[i], body + (v0 + i / VN * kLpThreads) * VN + i % VN);
+                        if (k >= bound && v[i] > -INFINITY) push(S, k);
+                    }
+                }
+            }
         }
     };
     int issued = min(kStages, rounds);
