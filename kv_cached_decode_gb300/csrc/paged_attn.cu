@@ -40,26 +40,28 @@ namespace {
 constexpr int kRowThreads = 128;               // the softmax warps
 constexpr int kPgThreads = kRowThreads + 64;   // + the MMA warp and the copying warp
 constexpr int kPgRows = 128;                   // query vectors per unit
-constexpr int kPgSlots = 5;                    // K/V tile pairs in flight
+constexpr int kStep = 128;                     // positions per tile: two TMA boxes or more
+constexpr int kStepBytes = kStep * kRowBytes;  // of K (or V)
+constexpr int kSlotsK = 2, kSlotsV = 3;        // K and V tiles in flight: K is read first
 constexpr int kPgMinBlocks = 2;                // blocks per SM the sizes below are chosen for
-// tensor memory: two S buffers (64 fp32 columns each), O (64), two P buffers (32 columns each)
-constexpr uint32_t kPgColsO = 2 * kTile;
+// tensor memory: scores (128 fp32 columns), output (64), weights (64 columns of two)
+constexpr uint32_t kPgColsO = kStep;
 constexpr uint32_t kPgColsP = kPgColsO + kHeadDim;
 constexpr uint32_t kPgCols = 256;
-static_assert(kPgCols >= kPgColsP + 2 * (kTile / 2) && kPgMinBlocks * kPgCols <= 512,
+static_assert(kPgCols >= kPgColsP + kStep / 2 && kPgMinBlocks * kPgCols <= 512,
               "the resident blocks' tensor memory");
 constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
 constexpr int kMergeTable = 1024;              // (row, piece) pairs of a merge's step
 // shared memory: K slots | V slots | Q | barriers | rows' references and sums | merge
-constexpr uint32_t kPgSmem = 2 * kPgSlots * kTileBytes + kPgQBytes + 256 + kPgRows * 8 +
+constexpr uint32_t kPgSmem = (kSlotsK + kSlotsV) * kStepBytes + kPgQBytes + 256 + kPgRows * 8 +
                              kMergeTable * 8 + kRowThreads * 16 + 1024;
 constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
 
 // The list's weights (its length is below 2^32, see the host's check): a tile of a unit with more than 64 vectors (bound by the softmax) and with
 // at most 64 (bound by the copies), and what a unit costs besides.
-constexpr uint32_t kHeavy = 3, kLight = 2, kUnit = 24;
-constexpr uint32_t kSnap = 8;       // no cut this close to a unit's ends
+constexpr uint32_t kHeavy = 6, kLight = 4, kUnit = 24;
+constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
 constexpr uint32_t kLeast = 12;     // a CTA's least share
 constexpr int kMaxCtas = 512;
 
@@ -75,7 +77,7 @@ struct PagedParams {
     int32_t n_q_heads, n_kv_heads, group, tq;  // tq: tokens per unit
     int32_t n_pages, page_log2, box_rows, boxes;  // boxes per tile
     float scale_log2;
-    float* ws_part;           // [2 CTAs][slot_rows][64]
+    float4* ws_part;          // [2 CTAs][16][slot_rows]: 4 dims of a row
     float2* ws_ml;            // [2 CTAs][slot_rows]: reference, sum
     int32_t* ws_cnt;          // a ticket per CTA that holds the first piece of a cut unit
     int32_t slot_rows;
@@ -98,9 +100,9 @@ __device__ __forceinline__ Row row_of(const PagedParams& p, int b, bool& bad) {
     return r;
 }
 
-// sum_{i < n} floor((a i + b) / 64), by the Euclidean recursion on (a, 64). The sum is below 2^32.
-__device__ __forceinline__ uint32_t floor_sum64(uint32_t n, uint32_t a, uint32_t b) {
-    uint32_t sum = 0, m = 64;
+// sum_{i < n} floor((a i + b) / 128), by the Euclidean recursion on (a, 128). The sum is below 2^32.
+__device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+    uint32_t sum = 0, m = kStep;
     for (;;) {
         if (a >= m) {
             sum += (uint32_t)((uint64_t)n * (n - 1) / 2) * (a / m);
@@ -139,7 +141,7 @@ __device__ __forceinline__ int kv_end(const PagedParams& p, const Shape& s, int 
     return s.s0() + min(s.r.n, (mb + 1) * p.tq);
 }
 __device__ __forceinline__ int tiles_of(const PagedParams& p, const Shape& s, int mb) {
-    return (kv_end(p, s, mb) + kTile - 1) / kTile;
+    return (kv_end(p, s, mb) + kStep - 1) / kStep;
 }
 __device__ __forceinline__ uint32_t tile_weight(int live) { return live > 64 ? kHeavy : kLight; }
 __device__ __forceinline__ uint32_t unit_weight(const PagedParams& p, const Shape& s, int mb) {
@@ -148,8 +150,8 @@ __device__ __forceinline__ uint32_t unit_weight(const PagedParams& p, const Shap
 // Weight of the first k blocks of one head, 0 <= k < nmb: they are full, so heavy (tq * g > 64).
 __device__ __forceinline__ uint32_t full_blocks(const PagedParams& p, const Shape& s, int k) {
     if (k == 0) return 0;
-    return kHeavy * floor_sum64((uint32_t)k, (uint32_t)p.tq,
-                                (uint32_t)(s.s0() + p.tq + kTile - 1)) + (uint32_t)k * kUnit;
+    return kHeavy * floor_sum((uint32_t)k, (uint32_t)p.tq,
+                                (uint32_t)(s.s0() + p.tq + kStep - 1)) + (uint32_t)k * kUnit;
 }
 __device__ __forceinline__ uint32_t row_weight(const PagedParams& p, const Row& r) {
     if (r.n == 0) return 0;
@@ -346,13 +348,15 @@ struct Walk {
 };
 
 enum PgBar {
-    kBarFull = 0,                       // K and V of slot s landed (TMA bytes)
-    kBarFree = kBarFull + kPgSlots,     // the products that read slot s are done (MMA commit)
-    kBarS = kBarFree + kPgSlots,        // S buffer written (MMA commit)
-    kBarRead = kBarS + 2,               // S buffer read by every row (an arrival per warp)
-    kBarP = kBarRead + 2,               // P buffer written by every row (an arrival per warp)
-    kBarO = kBarP + 2,                  // P.V from the P buffer done (MMA commit)
-    kBarQ = kBarO + 2,                  // the unit's rows staged (an arrival per warp)
+    kBarFullK = 0,                      // K of slot s landed (TMA bytes)
+    kBarFreeK = kBarFullK + kSlotsK,    // the products that read it are done (MMA commit)
+    kBarFullV = kBarFreeK + kSlotsK,    // the same for V
+    kBarFreeV = kBarFullV + kSlotsV,
+    kBarS = kBarFreeV + kSlotsV,        // scores written (MMA commit)
+    kBarRead = kBarS + 1,               // scores read by every row (an arrival per warp)
+    kBarP = kBarRead + 1,               // weights written by every row (an arrival per warp)
+    kBarO = kBarP + 1,                  // the products with V done (MMA commit)
+    kBarQ = kBarO + 1,                  // the unit's rows staged (an arrival per warp)
     kBarDrain = kBarQ + 1,              // every MMA issued so far done (after a failure)
     kBarCount = kBarDrain + 1
 };
@@ -371,22 +375,8 @@ __device__ __forceinline__ bool rows_any(bool x) {
         : "memory");
     return r != 0;
 }
-// Whether phase `parity` of the barrier is complete, without waiting. Asked for ahead of the use: an
-// answer takes about a hundred cycles.
-__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// The warp's wait for a phase, of which `done` may tell that it is complete.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool done = false) {
-    if (__all_sync(0xffffffffu, done)) return true;
+// The warp's wait for a phase.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
 // One arrival for the warp, behind what its lanes did.
@@ -405,62 +395,62 @@ struct Smem {
 };
 
 // ---------------------------------------------------------------- the rows ----------
-// Tiles v0 .. v1-1 of a unit, whose first has number it0 in the CTA: S into P, one row per thread.
-// REP copies of the rows, each with W = 64 / REP positions of a tile. Returns whether every wait
-// ended; m, l: this thread's reference (log2 units) and sum.
+// `n` tiles of a unit from v0 on, the first with number it0 in the CTA: scores into weights, one
+// row per thread. REP copies of the rows, each with W = 128 / REP positions of a tile. Keys t < lim
+// are visible, and t < kvend to any row. (A function of its own, so that what the caller keeps
+// takes no registers from the loop.)
+struct RowsEnd {
+    float m, l;  // this thread's reference (log2 units) and sum
+    bool ok;     // every wait ended
+};
 template <typename T, int REP>
-__device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, uint32_t tmem,
-                                         const Walk& u, uint32_t it0, int lim, float& m,
-                                         float& l) {
-    constexpr int W = kTile / REP;
+__device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32_t sv,
+                                         uint32_t tmem, int v0, int n, int kvend, uint32_t it0,
+                                         int lim) {
+    constexpr int W = kStep / REP;
     const int tid = threadIdx.x;
     const int base = tid / (kPgRows / REP) * W;  // of this copy's positions in a tile
-    const uint32_t lane_off = (uint32_t)(tid & ~31) << 16;
-    const uint32_t t_o = tmem + lane_off + kPgColsO;
-    const bool pos_scale = p.scale_log2 > 0.f;
-    const float cs = pos_scale ? p.scale_log2 : 1.f;
+    const uint32_t lanes = tmem + ((uint32_t)(tid & ~31) << 16);
+    const uint32_t t_s = lanes + base, t_o = lanes + kPgColsO, t_p = lanes + kPgColsP;
+    const bool pos_scale = scale_log2 > 0.f;
+    const float cs = pos_scale ? scale_log2 : 1.f;
     const int lim_least = __reduce_min_sync(0xffffffffu, lim);
     const int lim_most = __reduce_max_sync(0xffffffffu, lim);
-    m = -INFINITY;
-    l = 0.f;
+    float m = -INFINITY, l = 0.f;
     if (REP > 1) {
         // what the other copies hold stays zero in this lane
         uint32_t z[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = 0u;
-        tc_st32_u(tmem + lane_off + kPgColsP, z);
-        tc_st32_u(tmem + lane_off + kPgColsP + kTile / 2, z);
+        tc_st32_u(t_p, z);
+        tc_st32_u(t_p + 32, z);
     }
-    const int n = u.v1 - u.v0, kvend = u.kvend;
-    int t0 = u.v0 * kTile;
-    bool s_done = false, p_free = false;
-    for (int j = 0; j < n; ++j, t0 += kTile) {
-        const uint32_t it = it0 + j, buf = it & 1;
-        if (!warp_wait(sm.bar(kBarS + buf), (it >> 1) & 1, s_done)) return false;
+    int t0 = v0 * kStep + base;  // of this thread's positions
+    for (int j = 0; j < n; ++j, t0 += kStep) {
+        const uint32_t it = it0 + j;
+        if (!warp_wait(bars + 8 * kBarS, it & 1)) return {m, l, false};
         tc_fence_after();
-        p_free = j < 2 || mbar_done(sm.bar(kBarO + buf), ((it - 2) >> 1) & 1);
         uint32_t w[W / 2];
-        if (t0 + base >= lim_most) {
+        if (t0 >= lim_most) {
             // the warp sees nothing of it
             tc_fence_before();
-            warp_arrive(sm.bar(kBarRead + buf));
+            warp_arrive(bars + 8 * kBarRead);
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) w[i] = 0u;
         } else {
             float s[W];
-            const uint32_t t_s = tmem + lane_off + buf * kTile + base;
-            if constexpr (W == 64) tc_ld64(t_s, s);
-            else if constexpr (W == 32) tc_ld32(t_s, s);
-            else tc_ld16(t_s, s);
+            if constexpr (W == 128) tc_ld128(t_s, s);
+            else if constexpr (W == 64) tc_ld64(t_s, s);
+            else tc_ld32(t_s, s);
             tc_fence_before();
-            warp_arrive(sm.bar(kBarRead + buf));
+            warp_arrive(bars + 8 * kBarRead);
             if (!pos_scale) {
 #pragma unroll
-                for (int i = 0; i < W; ++i) s[i] *= p.scale_log2;
+                for (int i = 0; i < W; ++i) s[i] *= scale_log2;
             }
-            if (t0 + base + W > lim_least) {
+            if (t0 + W > lim_least) {
 #pragma unroll
-                for (int i = 0; i < W; ++i) s[i] = t0 + base + i < lim ? s[i] : -INFINITY;
+                for (int i = 0; i < W; ++i) s[i] = t0 + i < lim ? s[i] : -INFINITY;
             }
             float pm[8];
 #pragma unroll
@@ -482,15 +472,16 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
                 l *= factor;
                 if (j >= 1) {
                     // O is rescaled once P.V of the tile before is done
-                    if (!warp_wait(sm.bar(kBarO + (buf ^ 1)), ((it - 1) >> 1) & 1)) return false;
+                    if (!warp_wait(bars + 8 * kBarO, (it - 1) & 1)) return {m, l, false};
                     tc_fence_after();
-                    float ov[32];
+                    float ov[16];
+                    uint32_t ow[16];
+#pragma unroll 1
+                    for (int h = 0; h < kHeadDim; h += 16) {
+                        tc_ld16(t_o + h, ov);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tc_ld32(t_o + h * 32, ov);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) ov[i] *= factor;
-                        tc_st32(t_o + h * 32, ov);
+                        for (int i = 0; i < 16; ++i) ow[i] = __float_as_uint(ov[i] * factor);
+                        tc_st16_u(t_o + h, ow);
                     }
                 }
             }
@@ -509,30 +500,36 @@ __device__ __forceinline__ bool run_rows(const PagedParams& p, const Smem& sm, u
             const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])).get();
             l += all.x + all.y;
         }
-        s_done = j + 1 < n && mbar_done(sm.bar(kBarS + (buf ^ 1)), ((it + 1) >> 1) & 1);
-        // the buffer's last reader is P.V of two tiles before
-        if (!warp_wait(sm.bar(kBarO + buf), ((it - 2) >> 1) & 1, p_free)) return false;
+        // the weights' last reader is P.V of the tile before
+        if (j >= 1 && !warp_wait(bars + 8 * kBarO, (it - 1) & 1)) return {m, l, false};
         tc_fence_after();
-        const uint32_t t_p = tmem + lane_off + kPgColsP + buf * (kTile / 2) + base / 2;
-        if constexpr (W == 64) tc_st32_u(t_p, w);
-        else if constexpr (W == 32) tc_st16_u(t_p, w);
-        else tc_st8_u(t_p, w);
-        if (t0 + kTile > kvend) {
+        if constexpr (W == 128) {
+            tc_st32_u(t_p, w);
+            tc_st32_u(t_p + 32, w + 32);
+        } else if constexpr (W == 64) {
+            tc_st32_u(t_p + base / 2, w);
+        } else {
+            tc_st16_u(t_p + base / 2, w);
+        }
+        const int first = kvend - (v0 + j) * kStep;
+        if (first < kStep) {
             // Positions past the last visible one hold other data (or nothing): P is 0 there, but
             // 0 * NaN would still poison P.V, so those V rows are cleared once the copy landed.
-            const uint32_t slot = it % kPgSlots;
-            if (!warp_wait(sm.bar(kBarFull + slot), (it / kPgSlots) & 1)) return false;
-            uint8_t* vt = sm.v + slot * kTileBytes;
-            const int first = kvend - t0;
-            for (int x = tid; x < (kTile - first) * 8; x += kRowThreads)
-                *reinterpret_cast<uint4*>(vt + swz(first + (x >> 3), x & 7)) =
-                    make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t slot = it % kSlotsV;
+            if (!warp_wait(bars + 8 * (kBarFullV + slot), (it / kSlotsV) & 1))
+                return {m, l, false};
+            const uint32_t vt = sv + slot * kStepBytes;
+            for (int x = tid; x < (kStep - first) * 8; x += kRowThreads)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 vt + swz(first + (x >> 3), x & 7)),
+                             "r"(0u)
+                             : "memory");
             fence_proxy_async();
         }
         tc_fence_before();
-        warp_arrive(sm.bar(kBarP + buf));
+        warp_arrive(bars + 8 * kBarP);
     }
-    return true;
+    return {m, l, true};
 }
 
 // Where 4 dims of vector r of a unit go.
@@ -559,7 +556,7 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
     const int r = tid & (R - 1), part = tid / R;
     const uint32_t t_o = tmem + ((uint32_t)(tid & ~31) << 16) + kPgColsO;
     T* dst = r < u.live ? out_row<T>(p, u, r) : nullptr;
-    float* wsp = p.ws_part + ((int64_t)slot * p.slot_rows + r) * kHeadDim;
+    float4* wsp = p.ws_part + (int64_t)slot * 16 * p.slot_rows + r;  // + 4 dims * slot_rows
     if constexpr (REP == 1) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
@@ -580,7 +577,7 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
                 } else {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        reinterpret_cast<float4*>(wsp + half * 32)[c] =
+                        wsp[(half * 8 + c) * p.slot_rows] =
                             make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 }
             }
@@ -630,7 +627,7 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
                     if (whole)
                         *reinterpret_cast<uint2*>(dst + half * 32 + c * 4) = pack4<T>(x, inv);
                     else
-                        *reinterpret_cast<float4*>(wsp + half * 32 + c * 4) = x;
+                        wsp[(half * 8 + c) * p.slot_rows] = x;
                 }
             }
         }
@@ -704,12 +701,9 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
             }
         }
         rows_sync();
-        const int items = rows * (kHeadDim / 4);  // (row, 4 dims)
-        auto part_of = [&](int i, int y) {
-            return __ldcg(reinterpret_cast<const float4*>(
-                              p.ws_part +
-                              ((int64_t)slot(i) * p.slot_rows + r0 + (y >> 4)) * kHeadDim) +
-                          (y & 15));
+        const int items = rows * (kHeadDim / 4);  // (4 dims, row)
+        auto part_of = [&](int i, int c, int r) {
+            return __ldcg(p.ws_part + ((int64_t)slot(i) * 16 + c) * p.slot_rows + r0 + r);
         };
         auto add = [](float4& o, const float4& v, float f) {
             o.x = fmaf(v.x, f, o.x);
@@ -717,39 +711,38 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
             o.z = fmaf(v.z, f, o.z);
             o.w = fmaf(v.w, f, o.w);
         };
-        auto store = [&](int y, const float4& o) {
-            *reinterpret_cast<uint2*>(out_row<T>(p, u, r0 + (y >> 4)) + (y & 15) * 4) =
-                pack4<T>(o, 1.f);
-        };
-        if (items >= 4 * kRowThreads) {  // many rows, few pieces: four items at a time
-            for (int x = tid; x < items; x += 4 * kRowThreads) {
-                float4 o[4];
+        if (rows > 32) {  // a thread per row and half of its dims
+            for (int x = tid; x < 2 * rows; x += kRowThreads) {
+                const int half = x >= rows, r = x - half * rows;
+                float4 o[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int c = 0; c < 8; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                 for (int i = 0; i < n; ++i) {
-                    float4 v[4];
+                    const float f = tab[i * rows + r].x;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = part_of(i, min(x + k * kRowThreads, items - 1));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        add(o[k], v[k],
-                            tab[i * rows + (min(x + k * kRowThreads, items - 1) >> 4)].x);
+                    for (int c = 0; c < 8; ++c) add(o[c], part_of(i, half * 8 + c, r), f);
                 }
+                uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, u, r0 + r) + half * 32);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (x + k * kRowThreads < items) store(x + k * kRowThreads, o[k]);
+                for (int c = 0; c < 4; ++c) {
+                    const uint2 a = pack4<T>(o[2 * c], 1.f), b = pack4<T>(o[2 * c + 1], 1.f);
+                    dst[c] = make_uint4(a.x, a.y, b.x, b.y);
+                }
             }
         } else {  // few rows: their pieces shared out among threads, the shares added in order
+            auto store = [&](int y, const float4& o) {
+                *reinterpret_cast<uint2*>(out_row<T>(p, u, r0 + y % rows) + y / rows * 4) =
+                    pack4<T>(o, 1.f);
+            };
             const int shares = max(1, kRowThreads / items);
             for (int x = tid; x < items * shares; x += kRowThreads) {
-                const int share = x / items, y = x - share * items;
+                const int share = x / items, y = x - share * items, c = y / rows, r = y - c * rows;
                 const int last = n * (share + 1) / shares;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
                 for (int i = n * share / shares; i < last; ++i)
-                    add(o, part_of(i, y), tab[i * rows + (y >> 4)].x);
+                    add(o, part_of(i, c, r), tab[i * rows + r].x);
                 if (shares == 1) store(y, o);
                 else sm.part[x] = o;
             }
@@ -775,8 +768,8 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     Smem sm;
     sm.k = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~uintptr_t(1023));
-    sm.v = sm.k + kPgSlots * kTileBytes;
-    sm.q = sm.v + kPgSlots * kTileBytes;
+    sm.v = sm.k + kSlotsK * kStepBytes;
+    sm.q = sm.v + kSlotsV * kStepBytes;
     sm.bars = reinterpret_cast<uint64_t*>(sm.q + kPgQBytes);
     sm.ml = reinterpret_cast<float2*>(sm.q + kPgQBytes + 256);
     sm.pieces = sm.ml + kPgRows;
@@ -789,8 +782,8 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     const bool mma_warp = warp == kRowThreads / 32, copy_warp = warp == kRowThreads / 32 + 1;
     if (copy_warp && lane == 0) {
         for (int i = 0; i < kBarCount; ++i)
-            mbar_init(sm.bar(i), i >= kBarRead && i < kBarP + 2 || i == kBarQ ? kRowThreads / 32
-                                                                               : 1);
+            mbar_init(sm.bar(i),
+                      i == kBarRead || i == kBarP || i == kBarQ ? kRowThreads / 32 : 1);
         fence_barrier_init();
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
@@ -834,101 +827,103 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
 
     if (copy_warp) {
         // ---- K/V tiles, a slot each ----
-        uint32_t it = 0;
+        uint32_t it = 0, it_k = 0;  // tiles of V and K copied
         const int in_page = (1 << p.page_log2) - 1;
         do {
             // lane i: box i of K, lane 16 + i: box i of V
             const int box = lane & 15;
-            const bool mine = box < p.boxes;
+            const bool mine = box < p.boxes, is_v = lane >= 16;
             const int32_t* row = p.table + u.b * p.table_stride;
             auto page_of = [&](int v) {
-                const int pos = v * kTile + box * p.box_rows;
+                const int pos = v * kStep + box * p.box_rows;
                 return mine && v < u.v1 && pos < u.kvend ? __ldg(row + (pos >> p.page_log2)) : 0;
             };
             int page = page_of(u.v0);
-            for (int v = u.v0; v < u.v1; ++v, ++it) {
-                const int pos = v * kTile + box * p.box_rows;
+            for (int v = u.v0; ok && v < u.v1; ++v, ++it) {
+                const int pos = v * kStep + box * p.box_rows;
                 const bool on = mine && pos < u.kvend;
-                const uint32_t slot = it % kPgSlots;
                 int pg = page;
                 page = page_of(v + 1);
                 if (on && (pg < 0 || pg >= p.n_pages)) {
                     flag_error(p.dev_err, KVD_ERR_BAD_INDEX);
                     pg = p.n_pages;  // outside the tensor: zeros
                 }
-                if (it >= kPgSlots &&
-                    !warp_wait(sm.bar(kBarFree + slot), (it / kPgSlots - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t bar = sm.bar(kBarFull + slot);
-                const int n_on = __popc(__ballot_sync(0xffffffffu, on));
-                if (lane == 0) {
-                    // test only: 16 bytes more than the copies bring
-                    if (p.test_stall && it == 0) mbar_expect_tx_only(bar, 16);
-                    mbar_expect_tx(bar, n_on * p.box_rows * kRowBytes);
-                }
-                __syncwarp();
-                if (on) {
-                    const bool is_v = lane >= 16;
-                    const uint32_t dst = smem_u32((is_v ? sm.v : sm.k) + slot * kTileBytes) +
-                                         box * p.box_rows * kRowBytes;
-                    tma_load_4d(dst, is_v ? &tmv : &tmk, bar, 0, pos & in_page, u.h, pg);
-                }
-                __syncwarp();
+                const uint32_t bytes =
+                    __popc(__ballot_sync(0xffffffffu, on)) / 2 * p.box_rows * kRowBytes;
+                auto copy = [&](int slots, int full, int free, const uint8_t* to,
+                                const CUtensorMap* map, bool half) {
+                    const uint32_t slot = it % slots, turn = it / slots;
+                    if (turn > 0 && !warp_wait(sm.bar(free + slot), (turn - 1) & 1)) return false;
+                    const uint32_t bar = sm.bar(full + slot);
+                    if (lane == 0) {
+                        // test only: 16 bytes more than the copies bring
+                        if (p.test_stall && it == 0) mbar_expect_tx_only(bar, 16);
+                        mbar_expect_tx(bar, bytes);
+                    }
+                    __syncwarp();
+                    if (on && half)
+                        tma_load_4d(smem_u32(to + slot * kStepBytes) + box * p.box_rows * kRowBytes,
+                                    map, bar, 0, pos & in_page, u.h, pg);
+                    __syncwarp();
+                    return true;
+                };
+                if (!(ok = copy(kSlotsK, kBarFullK, kBarFreeK, sm.k, &tmk, !is_v))) break;
+                ++it_k;
+                if (!(ok = copy(kSlotsV, kBarFullV, kBarFreeV, sm.v, &tmv, is_v))) break;
             }
         } while (ok && u.next(p));
         if (!ok) {
             if (lane == 0) flag_error(p.dev_err, KVD_ERR_TIMEOUT);
             // the copies in flight land before the block leaves
-            for (uint32_t i = it > kPgSlots ? it - kPgSlots : 0; i < it; ++i)
-                mbar_wait_bounded(sm.bar(kBarFull + i % kPgSlots), (i / kPgSlots) & 1);
+            for (uint32_t i = it_k > kSlotsK ? it_k - kSlotsK : 0; i < it_k; ++i)
+                mbar_wait_bounded(sm.bar(kBarFullK + i % kSlotsK), (i / kSlotsK) & 1);
+            for (uint32_t i = it > kSlotsV ? it - kSlotsV : 0; i < it; ++i)
+                mbar_wait_bounded(sm.bar(kBarFullV + i % kSlotsV), (i / kSlotsV) & 1);
         }
     } else if (mma_warp) {
         // ---- the products: the whole warp runs the loop, one elected lane issues ----
         constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-        constexpr uint32_t kIdS = tc_idesc_f16(kBf16, kPgRows, kTile, false);
+        constexpr uint32_t kIdS = tc_idesc_f16(kBf16, kPgRows, kStep, false);
         constexpr uint32_t kIdO = tc_idesc_f16(kBf16, kPgRows, kHeadDim, true);
         const uint64_t qdesc = tc_desc_sw128(smem_u32(sm.q));
         const uint64_t kdesc = tc_desc_sw128(smem_u32(sm.k)), vdesc = tc_desc_sw128(smem_u32(sm.v));
-        constexpr uint64_t kTileDesc = kTileBytes / 16;  // a descriptor's addresses are in 16 bytes
+        constexpr uint64_t kStepDesc = kStepBytes / 16;  // a descriptor's addresses: 16 bytes
         const uint32_t lead = elect_one();
         auto issue_s = [&](uint32_t it) -> bool {
-            const uint32_t slot = it % kPgSlots, buf = it & 1;
-            if (!warp_wait(sm.bar(kBarFull + slot), (it / kPgSlots) & 1)) return false;
+            const uint32_t slot = it % kSlotsK;
+            if (!warp_wait(sm.bar(kBarFullK + slot), (it / kSlotsK) & 1)) return false;
             tc_fence_after();
-            const uint64_t kd = kdesc + slot * kTileDesc;
+            const uint64_t kd = kdesc + slot * kStepDesc;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                tc_mma_f16_if(lead, tmem + buf * kTile, qdesc + kk * 2, kd + kk * 2, kIdS, kk > 0);
-            tc_commit_if(lead, sm.bar(kBarS + buf));
+                tc_mma_f16_if(lead, tmem, qdesc + kk * 2, kd + kk * 2, kIdS, kk > 0);
+            tc_commit_if(lead, sm.bar(kBarS));
+            tc_commit_if(lead, sm.bar(kBarFreeK + slot));
             return true;
         };
-        uint32_t it0 = 0, units = 0;
+        uint32_t it = 0, units = 0;
         do {
-            const int nt = u.v1 - u.v0;
             if (!(ok = warp_wait(sm.bar(kBarQ), units & 1))) break;
             tc_fence_after();
-            for (int j = 0; ok && j < min(2, nt); ++j) ok = issue_s(it0 + j);
-            for (int j = 0; ok && j < nt; ++j) {
-                const uint32_t it = it0 + j, buf = it & 1, slot = it % kPgSlots;
-                // the next S of the buffer as soon as the rows have read this one, while they
-                // form the weights
-                if (!(ok = warp_wait(sm.bar(kBarRead + buf), (it >> 1) & 1))) break;
-                if (j + 2 < nt && !(ok = issue_s(it + 2))) break;
-                if (!(ok = warp_wait(sm.bar(kBarP + buf), (it >> 1) & 1))) break;
+            const int nt = u.v1 - u.v0;
+            ok = issue_s(it);
+            for (int j = 0; ok && j < nt; ++j, ++it) {
+                // the next scores as soon as the rows have read these, while they form the weights
+                if (!(ok = warp_wait(sm.bar(kBarRead), it & 1))) break;
+                if (j + 1 < nt && !(ok = issue_s(it + 1))) break;
+                const uint32_t slot = it % kSlotsV;
+                if (!(ok = warp_wait(sm.bar(kBarFullV + slot), (it / kSlotsV) & 1))) break;
+                if (!(ok = warp_wait(sm.bar(kBarP), it & 1))) break;
                 tc_fence_after();
-                const uint32_t t_p = tmem + kPgColsP + buf * (kTile / 2);
-                const uint64_t vd = vdesc + slot * kTileDesc;
-                tc_mma_f16_tmem_a_if(lead, tmem + kPgColsO, t_p, vd, kIdO, j > 0);
+                const uint64_t vd = vdesc + slot * kStepDesc;
+                tc_mma_f16_tmem_a_if(lead, tmem + kPgColsO, tmem + kPgColsP, vd, kIdO, j > 0);
 #pragma unroll
-                for (int kk = 1; kk < 4; ++kk)
-                    tc_mma_f16_tmem_a_if(lead, tmem + kPgColsO, t_p + kk * 8,
+                for (int kk = 1; kk < kStep / 16; ++kk)
+                    tc_mma_f16_tmem_a_if(lead, tmem + kPgColsO, tmem + kPgColsP + kk * 8,
                                          vd + kk * (16 * kRowBytes / 16), kIdO, 1);
-                tc_commit_if(lead, sm.bar(kBarO + buf));
-                tc_commit_if(lead, sm.bar(kBarFree + slot));
+                tc_commit_if(lead, sm.bar(kBarO));
+                tc_commit_if(lead, sm.bar(kBarFreeV + slot));
             }
-            it0 += nt;
             ++units;
         } while (ok && u.next(p));
         if (!ok) {
@@ -969,16 +964,20 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             // keys t < lim are visible; rows past the unit's see all of it (and are not written)
             const int lim =
                 r < u.live ? u.s.s0() + u.mb * p.tq + r / p.group + 1 : u.kvend;
-            float m, l;
-            if (rep == 1) ok = run_rows<T, 1>(p, sm, tmem, u, it0, lim, m, l);
-            else if (rep == 2) ok = run_rows<T, 2>(p, sm, tmem, u, it0, lim, m, l);
-            else ok = run_rows<T, 4>(p, sm, tmem, u, it0, lim, m, l);
+            const int nt = u.v1 - u.v0;
+            auto run = [&](auto copies) {
+                return run_rows<T, decltype(copies)::value>(p.scale_log2, sm.bar(0),
+                                                            smem_u32(sm.v), tmem, u.v0, nt,
+                                                            u.kvend, it0, lim);
+            };
+            const RowsEnd e = rep == 1   ? run(std::integral_constant<int, 1>{})
+                              : rep == 2 ? run(std::integral_constant<int, 2>{})
+                                         : run(std::integral_constant<int, 4>{});
             const Walk done = u;
             more = u.next(p);
             if (more) load_q(u);  // on their way while this unit ends
-            it0 += done.v1 - done.v0;
-            const uint32_t last = it0 - 1;
-            ok = ok && mbar_wait_bounded(sm.bar(kBarO + (last & 1)), (last >> 1) & 1);
+            it0 += nt;
+            ok = e.ok && mbar_wait_bounded(sm.bar(kBarO), (it0 - 1) & 1);
             if (rows_any(!ok)) {
                 if (tid == 0) flag_error(p.dev_err, KVD_ERR_TIMEOUT);
                 break;
@@ -986,9 +985,9 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             tc_fence_after();
             const bool whole = done.v0 == 0 && done.v1 == done.tiles;
             const int slot = 2 * (int)blockIdx.x + (done.v0 == 0);
-            if (rep == 1) finish_rows<T, 1>(p, sm, tmem, done, whole, slot, m, l);
-            else if (rep == 2) finish_rows<T, 2>(p, sm, tmem, done, whole, slot, m, l);
-            else finish_rows<T, 4>(p, sm, tmem, done, whole, slot, m, l);
+            if (rep == 1) finish_rows<T, 1>(p, sm, tmem, done, whole, slot, e.m, e.l);
+            else if (rep == 2) finish_rows<T, 2>(p, sm, tmem, done, whole, slot, e.m, e.l);
+            else finish_rows<T, 4>(p, sm, tmem, done, whole, slot, e.m, e.l);
             tc_fence_before();  // O is read before the next unit's products
             if (more) stage_q();
             if (!whole) {
@@ -1031,8 +1030,8 @@ kvd_status run_paged(PagedParams& p, int nsm, const CUtensorMap& mk, const CUten
     if (!prepare_paged<T>()) return KVD_ERR_CUDA;
     const int blocks = std::min(kMaxCtas, nsm * kPgMinBlocks);
     p.ws_cnt = reinterpret_cast<int32_t*>(ws);
-    p.ws_part = reinterpret_cast<float*>(ws + KVD_WS_COUNTER_BYTES);
-    p.ws_ml = reinterpret_cast<float2*>(p.ws_part + (size_t)2 * blocks * p.slot_rows * kHeadDim);
+    p.ws_part = reinterpret_cast<float4*>(ws + KVD_WS_COUNTER_BYTES);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_part + (size_t)2 * blocks * 16 * p.slot_rows);
     return launch(paged_attn_kernel<T>, dim3((unsigned)blocks), dim3(kPgThreads), kPgSmem, st, pdl,
                   mk, mv, p);
 }
@@ -1076,7 +1075,7 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     // the list of tiles, at its longest, is counted in 32 bits
     const int tq = kPgRows / group;
     const double blocks = (double)cache->n_kv_heads * ((double)n_tokens / tq + cache->batch);
-    const double longest = kHeavy * ((double)cache->table_width * cache->page_size / kTile + 1.);
+    const double longest = kHeavy * ((double)cache->table_width * cache->page_size / kStep + 1.);
     if (blocks * (longest + kUnit) > 4e9) return KVD_ERR_UNSUPPORTED;
     CUtensorMap mk, mv;
     if (kvd_status s = encode_pool_map(&mk, dtype, cache->k, cache)) return s;
@@ -1101,7 +1100,7 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     p.n_pages = cache->n_pages;
     while ((1 << p.page_log2) < cache->page_size) ++p.page_log2;
     p.box_rows = std::min(kTile, cache->page_size);
-    p.boxes = kTile / p.box_rows;
+    p.boxes = kStep / p.box_rows;
     p.scale_log2 = scale * kLog2e;
     p.slot_rows = unit_rows(group, max_new);
     p.dev_err = dev_err;
