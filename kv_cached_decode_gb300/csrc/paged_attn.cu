@@ -51,10 +51,10 @@ constexpr uint32_t kPgCols = 256;
 static_assert(kPgCols >= kPgColsP + kStep / 2 && kPgMinBlocks * kPgCols <= 512,
               "the resident blocks' tensor memory");
 constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
-constexpr int kMergeTable = 1024;              // (row, piece) pairs of a merge's step
+constexpr int kFewPieces = 6;                  // of a merge with a thread per row
 // shared memory: K slots | V slots | Q | barriers | rows' references and sums | merge
 constexpr uint32_t kPgSmem = (kSlotsK + kSlotsV) * kStepBytes + kPgQBytes + 256 + kPgRows * 8 +
-                             kMergeTable * 8 + kRowThreads * 16 + 1024;
+                             kRowThreads * 16 + 1024;
 constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
 
@@ -102,24 +102,31 @@ __device__ __forceinline__ Row row_of(const PagedParams& p, int b, bool& bad) {
 
 // sum_{i < n} floor((a i + b) / 128), by the Euclidean recursion on (a, 128). The sum is below 2^32.
 __device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
-    uint32_t sum = 0, m = kStep;
-    for (;;) {
-        if (a >= m) {
-            sum += (uint32_t)((uint64_t)n * (n - 1) / 2) * (a / m);
-            a %= m;
-        }
+    auto pairs = [](uint32_t n) { return (uint32_t)((uint64_t)n * (n - 1) / 2); };
+    // (the first step by hand: divisions by a constant)
+    uint32_t sum = pairs(n) * (a / kStep) + n * (b / kStep);
+    a %= kStep;
+    b %= kStep;
+    uint32_t top = a * n + b, m = a;
+    n = top / kStep;
+    b = top % kStep;
+    a = kStep;
+    while (n > 0) {
+        sum += pairs(n) * (a / m);
+        a %= m;
         if (b >= m) {
             sum += n * (b / m);
             b %= m;
         }
-        const uint32_t top = a * n + b;
-        if (top < m) return sum;
+        top = a * n + b;
+        if (top < m) break;
         n = top / m;
         b = top % m;
         const uint32_t x = m;
         m = a;
         a = x;
     }
+    return sum;
 }
 
 struct Shape {  // of a row's units
@@ -143,11 +150,13 @@ __device__ __forceinline__ int kv_end(const PagedParams& p, const Shape& s, int 
 __device__ __forceinline__ int tiles_of(const PagedParams& p, const Shape& s, int mb) {
     return (kv_end(p, s, mb) + kStep - 1) / kStep;
 }
-__device__ __forceinline__ uint32_t tile_weight(int live) { return live > 64 ? kHeavy : kLight; }
+// Units of at most 32 vectors hold them four times.
+__device__ __forceinline__ int copies_of(int live) { return live > 32 ? 1 : 4; }
+__device__ __forceinline__ uint32_t tile_weight(int live) { return live > 32 ? kHeavy : kLight; }
 __device__ __forceinline__ uint32_t unit_weight(const PagedParams& p, const Shape& s, int mb) {
     return tiles_of(p, s, mb) * tile_weight(live_rows(p, s, mb)) + kUnit;
 }
-// Weight of the first k blocks of one head, 0 <= k < nmb: they are full, so heavy (tq * g > 64).
+// Weight of the first k blocks of one head, 0 <= k < nmb: they are full, so heavy (tq * g > 32).
 __device__ __forceinline__ uint32_t full_blocks(const PagedParams& p, const Shape& s, int k) {
     if (k == 0) return 0;
     return kHeavy * floor_sum((uint32_t)k, (uint32_t)p.tq,
@@ -256,14 +265,15 @@ __device__ __forceinline__ Place find_unit(const PagedParams& p, const Table& t,
     return u;
 }
 
-// Stretches of the list: CTA i's share starts at floor(i total / ctas).
+// Stretches of the list: CTA i's share starts at floor(i total / ctas), the quotient in 16.16 bits.
 struct Shares {
-    uint32_t total, ctas, per, rest;  // total = per ctas + rest
+    uint32_t total, ctas;
+    uint64_t each;  // floor(2^16 total / ctas)
     __device__ __forceinline__ uint32_t start(uint32_t i) const {
-        return i * per + i * rest / ctas;  // (rest < ctas <= kMaxCtas)
+        return i < ctas ? (uint32_t)(i * each >> 16) : total;
     }
     __device__ __forceinline__ uint32_t holder(uint32_t at) const {  // whose share has place `at`
-        uint32_t i = min((uint32_t)((float)at * ((float)ctas / (float)total)), ctas - 1);
+        uint32_t i = min((uint32_t)__fdividef((float)at * (float)ctas, (float)total), ctas - 1);
         while (start(i) > at) --i;
         while (i + 1 < ctas && start(i + 1) <= at) ++i;
         return i;
@@ -273,8 +283,8 @@ __device__ __forceinline__ Shares shares(uint32_t total) {
     Shares s;
     s.total = total;
     s.ctas = max(1u, min(gridDim.x, total / kLeast));
-    s.per = total / s.ctas;
-    s.rest = total - s.per * s.ctas;
+    const uint32_t per = total / s.ctas;
+    s.each = ((uint64_t)per << 16) + ((total - per * s.ctas) << 16) / s.ctas;
     return s;
 }
 // Where the stretch really starts whose share starts inside a unit of weight w: there from keep_lo
@@ -389,7 +399,6 @@ struct Smem {
     uint8_t *k, *v, *q;
     uint64_t* bars;
     float2* ml;      // [128]
-    float2* pieces;  // [kMergeTable]
     float4* part;    // [128]
     __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&bars[i]); }
 };
@@ -407,6 +416,7 @@ template <typename T, int REP>
 __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32_t sv,
                                          uint32_t tmem, int v0, int n, int kvend, uint32_t it0,
                                          int lim) {
+    static_assert(REP == 1 || REP == 4, "W is 128 or 32");
     constexpr int W = kStep / REP;
     const int tid = threadIdx.x;
     const int base = tid / (kPgRows / REP) * W;  // of this copy's positions in a tile
@@ -440,7 +450,6 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
         } else {
             float s[W];
             if constexpr (W == 128) tc_ld128(t_s, s);
-            else if constexpr (W == 64) tc_ld64(t_s, s);
             else tc_ld32(t_s, s);
             tc_fence_before();
             warp_arrive(bars + 8 * kBarRead);
@@ -506,8 +515,6 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
         if constexpr (W == 128) {
             tc_st32_u(t_p, w);
             tc_st32_u(t_p + 32, w + 32);
-        } else if constexpr (W == 64) {
-            tc_st32_u(t_p + base / 2, w);
         } else {
             tc_st16_u(t_p + base / 2, w);
         }
@@ -553,10 +560,10 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
                                             float l) {
     const int tid = threadIdx.x;
     constexpr int R = kPgRows / REP;
-    const int r = tid & (R - 1), part = tid / R;
+    const int r = tid & (R - 1);
     const uint32_t t_o = tmem + ((uint32_t)(tid & ~31) << 16) + kPgColsO;
-    T* dst = r < u.live ? out_row<T>(p, u, r) : nullptr;
-    float4* wsp = p.ws_part + (int64_t)slot * 16 * p.slot_rows + r;  // + 4 dims * slot_rows
+    float4* wsp = p.ws_part + (int64_t)slot * 16 * p.slot_rows;  // + 4 dims * slot_rows + row
+    float2* wsm = p.ws_ml + (int64_t)slot * p.slot_rows;
     if constexpr (REP == 1) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
@@ -565,85 +572,124 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
             tc_ld32(t_o + half * 32, o);
             if (r < u.live) {
                 if (whole) {
+                    uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, u, r) + half * 32);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const uint2 a = pack4<T>(make_float4(o[8 * c], o[8 * c + 1], o[8 * c + 2],
                                                              o[8 * c + 3]), inv);
                         const uint2 b = pack4<T>(make_float4(o[8 * c + 4], o[8 * c + 5],
                                                              o[8 * c + 6], o[8 * c + 7]), inv);
-                        reinterpret_cast<uint4*>(dst + half * 32)[c] =
-                            make_uint4(a.x, a.y, b.x, b.y);
+                        dst[c] = make_uint4(a.x, a.y, b.x, b.y);
                     }
                 } else {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        wsp[(half * 8 + c) * p.slot_rows] =
+                        wsp[(half * 8 + c) * p.slot_rows + r] =
                             make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 }
             }
         }
-        if (!whole && r < u.live) p.ws_ml[(int64_t)slot * p.slot_rows + r] = make_float2(m, l);
+        if (!whole && r < u.live) wsm[r] = make_float2(m, l);
     } else {
         // the copies' partials meet in the rows' shared memory (every S is done), 32 dims at a
-        // time; copy `part` writes its share of the dims
+        // time where all 64 do not fit
         sm.ml[tid] = make_float2(m, l);
-        rows_sync();
-        float top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < REP; ++k) top = fmaxf(top, sm.ml[r + k * R].x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        float all = 0.f;
-#pragma unroll
-        for (int k = 0; k < REP; ++k) {
-            const float2 o = sm.ml[r + k * R];
-            all = fmaf(o.y, exp2f(o.x - ref), all);
-        }
-        const float f = exp2f(m - ref), inv = all > 0.f ? 1.f / all : 0.f;
-        constexpr int C = 8 / REP;  // float4s per thread and half
+        float o[64];
+        tc_ld64(t_o, o);
         float4* buf = reinterpret_cast<float4*>(sm.q);
+        const int phases = u.live > 16 ? 2 : 1, quads = 16 / phases, rows = 16 * phases;
+#pragma unroll 1
+        for (int h = 0; h < phases; ++h) {
+            if (r < u.live) {  // [quad][copy][row]
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float o[32];
-            tc_ld32(t_o + half * 32, o);
-            if (half) rows_sync();  // the first half is read
+                for (int c = 0; c < 8; ++c)
+                    buf[(c * REP + tid / R) * rows + r] =
+                        make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                if (phases == 1) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                buf[tid * 8 + (c ^ (tid & 7))] = make_float4(o[4 * c] * f, o[4 * c + 1] * f,
-                                                             o[4 * c + 2] * f, o[4 * c + 3] * f);
-            rows_sync();
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                const int c = part * C + i;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < REP; ++k) {
-                    const float4 y = buf[(r + k * R) * 8 + (c ^ (r & 7))];
-                    x.x += y.x;
-                    x.y += y.y;
-                    x.z += y.z;
-                    x.w += y.w;
-                }
-                if (r < u.live) {
-                    if (whole)
-                        *reinterpret_cast<uint2*>(dst + half * 32 + c * 4) = pack4<T>(x, inv);
-                    else
-                        wsp[(half * 8 + c) * p.slot_rows] = x;
+                    for (int c = 8; c < 16; ++c)
+                        buf[(c * REP + tid / R) * rows + r] =
+                            make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 }
             }
+            rows_sync();
+            for (int x = tid; x < quads * rows; x += kRowThreads) {
+                const int y = x & (rows - 1), c = x / rows;  // (rows: 16 or 32)
+                if (y >= u.live) continue;
+                float top = -INFINITY, all = 0.f;
+#pragma unroll
+                for (int k = 0; k < REP; ++k) top = fmaxf(top, sm.ml[y + k * R].x);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < REP; ++k) {
+                    const float2 ml = sm.ml[y + k * R];
+                    const float4 b = buf[(c * REP + k) * rows + y];
+                    const float f = exp2f(ml.x - ref);
+                    all = fmaf(ml.y, f, all);
+                    a.x = fmaf(b.x, f, a.x);
+                    a.y = fmaf(b.y, f, a.y);
+                    a.z = fmaf(b.z, f, a.z);
+                    a.w = fmaf(b.w, f, a.w);
+                }
+                const int d4 = h * 8 + c;
+                if (whole) {
+                    *reinterpret_cast<uint2*>(out_row<T>(p, u, y) + d4 * 4) =
+                        pack4<T>(a, all > 0.f ? 1.f / all : 0.f);
+                } else {
+                    wsp[d4 * p.slot_rows + y] = a;
+                    if (d4 == 0) wsm[y] = make_float2(top, all);
+                }
+            }
+            if (phases == 2) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = o[32 + i];
+            }
+            rows_sync();  // read before the second half, or the next unit's rows, are written
         }
-        if (!whole && part == 0 && r < u.live)
-            p.ws_ml[(int64_t)slot * p.slot_rows + r] = make_float2(top, all);
-        rows_sync();  // the buffer is read before the next unit's rows are staged
     }
 }
 
+// Partials (reference, sum, o) joined one after the other.
+struct Joined {
+    float top, l;
+    float4 o;
+    __device__ __forceinline__ void clear() {
+        top = -INFINITY;
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    template <int N>
+    __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N], int n) {
+        float t = top;
+#pragma unroll
+        for (int k = 0; k < N; ++k) t = fmaxf(t, k < n ? ml[k].x : t);
+        const float ref = t == -INFINITY ? 0.f : t, f0 = exp2f(top - ref);
+        top = t;
+        l *= f0;
+        o.x *= f0;
+        o.y *= f0;
+        o.z *= f0;
+        o.w *= f0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (k >= n) break;
+            const float f = exp2f(ml[k].x - ref);
+            l = fmaf(ml[k].y, f, l);
+            o.x = fmaf(v[k].x, f, o.x);
+            o.y = fmaf(v[k].y, f, o.y);
+            o.z = fmaf(v[k].z, f, o.z);
+            o.w = fmaf(v[k].w, f, o.w);
+        }
+    }
+};
+
 // A cut unit's pieces, which lie in the workspace: CTAs i0 .. i0 + n - 1, the last to arrive merges
-// them in that order. The pieces' weights are formed first, so that all loads of values are
-// independent.
-template <typename T>
+// them in that order. MANY: units of more than 32 rows are among the call's.
+template <typename T, bool MANY>
 __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& sm, const Walk& u,
                                              int i0, int n, int* s_last) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
     rows_sync();
     if (tid == 0) {
         // (released and acquired for the other threads of the block by the barriers around it)
@@ -656,114 +702,101 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
     }
     rows_sync();
     if (!*s_last) return;
-    const int step = min(u.live, kMergeTable / n);  // rows at a time (n <= kMaxCtas)
-    auto slot = [&](int i) { return 2 * (i0 + i) + (i == 0); };
-    for (int r0 = 0; r0 < u.live; r0 += step) {
-        const int rows = min(step, u.live - r0);
-        float2* tab = sm.pieces;  // [n][rows]: reference and sum, then the weight
-        for (int x = tid; x < rows * n; x += kRowThreads) {
-            const int i = x / rows;
-            tab[x] = __ldcg(&p.ws_ml[(int64_t)slot(i) * p.slot_rows + r0 + (x - i * rows)]);
-        }
-        rows_sync();
-        if (n <= rows) {  // a thread per row
-            for (int r = tid; r < rows; r += kRowThreads) {
-                float top = -INFINITY, l = 0.f;
-                for (int i = 0; i < n; ++i) top = fmaxf(top, tab[i * rows + r].x);
-                const float ref = top == -INFINITY ? 0.f : top;
-                for (int i = 0; i < n; ++i) {
-                    const float2 ml = tab[i * rows + r];
-                    const float f = exp2f(ml.x - ref);
-                    l = fmaf(ml.y, f, l);
-                    tab[i * rows + r].x = f;
-                }
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                for (int i = 0; i < n; ++i) tab[i * rows + r].x *= inv;
-            }
-        } else {  // a warp per row
-            for (int r = warp; r < rows; r += kRowThreads / 32) {
-                float top = -INFINITY, l = 0.f;
-                for (int i = lane; i < n; i += 32) top = fmaxf(top, tab[i * rows + r].x);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float ref = top == -INFINITY ? 0.f : top;
-                for (int i = lane; i < n; i += 32) {
-                    const float2 ml = tab[i * rows + r];
-                    const float f = exp2f(ml.x - ref);
-                    l = fmaf(ml.y, f, l);
-                    tab[i * rows + r].x = f;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                for (int i = lane; i < n; i += 32) tab[i * rows + r].x *= inv;
-            }
-        }
-        rows_sync();
-        const int items = rows * (kHeadDim / 4);  // (4 dims, row)
-        auto part_of = [&](int i, int c, int r) {
-            return __ldcg(p.ws_part + ((int64_t)slot(i) * 16 + c) * p.slot_rows + r0 + r);
-        };
-        auto add = [](float4& o, const float4& v, float f) {
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
-        };
-        if (rows > 32) {  // a thread per row and half of its dims
-            for (int x = tid; x < 2 * rows; x += kRowThreads) {
-                const int half = x >= rows, r = x - half * rows;
-                float4 o[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-                for (int i = 0; i < n; ++i) {
-                    const float f = tab[i * rows + r].x;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) add(o[c], part_of(i, half * 8 + c, r), f);
-                }
-                uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, u, r0 + r) + half * 32);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint2 a = pack4<T>(o[2 * c], 1.f), b = pack4<T>(o[2 * c + 1], 1.f);
-                    dst[c] = make_uint4(a.x, a.y, b.x, b.y);
-                }
-            }
-        } else {  // few rows: their pieces shared out among threads, the shares added in order
-            auto store = [&](int y, const float4& o) {
-                *reinterpret_cast<uint2*>(out_row<T>(p, u, r0 + y % rows) + y / rows * 4) =
-                    pack4<T>(o, 1.f);
-            };
-            const int shares = max(1, kRowThreads / items);
-            for (int x = tid; x < items * shares; x += kRowThreads) {
-                const int share = x / items, y = x - share * items, c = y / rows, r = y - c * rows;
-                const int last = n * (share + 1) / shares;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                for (int i = n * share / shares; i < last; ++i)
-                    add(o, part_of(i, c, r), tab[i * rows + r].x);
-                if (shares == 1) store(y, o);
-                else sm.part[x] = o;
-            }
-            if (shares > 1) {
-                rows_sync();
-                if (tid < items) {
-                    float4 o = sm.part[tid];
-                    for (int k = 1; k < shares; ++k) add(o, sm.part[k * items + tid], 1.f);
-                    store(tid, o);
-                }
-            }
-        }
-        rows_sync();  // the table is read
-    }
     if (tid == 0) p.ws_cnt[i0] = 0;
+    auto slot = [&](int i) { return (int64_t)(2 * (i0 + i) + (i == 0)); };
+    auto ml_of = [&](int i, int r) { return __ldcg(p.ws_ml + slot(i) * p.slot_rows + r); };
+    auto part_of = [&](int i, int c, int r) {
+        return __ldcg(p.ws_part + (slot(i) * 16 + c) * p.slot_rows + r);
+    };
+    if (MANY && u.live > 32 && n <= kFewPieces) {
+        // many rows, few pieces: a thread per row
+        if (tid < u.live) {
+            float2 ml[kFewPieces];
+#pragma unroll
+            for (int i = 0; i < kFewPieces; ++i)
+                ml[i] = i < n ? ml_of(i, tid) : make_float2(-INFINITY, 0.f);
+            float top = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kFewPieces; ++i) top = fmaxf(top, ml[i].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float4 o[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kFewPieces; ++i) {
+                if (i >= n) break;
+                const float f = exp2f(ml[i].x - ref);
+                l = fmaf(ml[i].y, f, l);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float4 v = part_of(i, c, tid);
+                    o[c].x = fmaf(v.x, f, o[c].x);
+                    o[c].y = fmaf(v.y, f, o[c].y);
+                    o[c].z = fmaf(v.z, f, o[c].z);
+                    o[c].w = fmaf(v.w, f, o[c].w);
+                }
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, u, tid));
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint2 a = pack4<T>(o[2 * c], inv), b = pack4<T>(o[2 * c + 1], inv);
+                dst[c] = make_uint4(a.x, a.y, b.x, b.y);
+            }
+        }
+        return;
+    }
+    // a thread per row, 4 dims and, of few rows, share of the pieces; the shares joined in order
+    constexpr int kBatch = 8;  // pieces whose loads are in flight
+    const int items = u.live * 16, shares = max(1, kRowThreads / items);
+    auto store = [&](int y, const Joined& a) {
+        *reinterpret_cast<uint2*>(out_row<T>(p, u, y % u.live) + y / u.live * 4) =
+            pack4<T>(a.o, a.l > 0.f ? 1.f / a.l : 0.f);
+    };
+    for (int x = tid; x < items * shares; x += kRowThreads) {
+        const int share = x / items, y = x - share * items, c = y / u.live, r = y - c * u.live;
+        const int last = n * (share + 1) / shares;
+        Joined a;
+        a.clear();
+        for (int i = n * share / shares; i < last; i += kBatch) {
+            float2 ml[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                ml[k] = ml_of(min(i + k, last - 1), r);
+                v[k] = part_of(min(i + k, last - 1), c, r);
+            }
+            a.add(ml, v, last - i);
+        }
+        if (shares == 1) {
+            store(y, a);
+        } else {
+            sm.part[x] = a.o;
+            sm.ml[x] = make_float2(a.top, a.l);
+        }
+    }
+    if (shares > 1) {
+        rows_sync();
+        if (tid < items) {
+            Joined a;
+            a.clear();
+            for (int k = 0; k < shares; ++k) {
+                const float2 ml[1] = {sm.ml[k * items + tid]};
+                const float4 v[1] = {sm.part[k * items + tid]};
+                a.add(ml, v, 1);
+            }
+            store(tid, a);
+        }
+        rows_sync();  // read before the next unit's sums are written
+    }
 }
 
-template <typename T>
+// MANY: units of more than 32 query vectors are among the call's.
+template <typename T, bool MANY>
 __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv, const PagedParams p) {
+                      const __grid_constant__ CUtensorMap tmv,
+                      const PagedParams p) {
     extern __shared__ uint8_t smem_raw[];
     Smem sm;
     sm.k = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -772,8 +805,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     sm.q = sm.v + kSlotsV * kStepBytes;
     sm.bars = reinterpret_cast<uint64_t*>(sm.q + kPgQBytes);
     sm.ml = reinterpret_cast<float2*>(sm.q + kPgQBytes + 256);
-    sm.pieces = sm.ml + kPgRows;
-    sm.part = reinterpret_cast<float4*>(sm.pieces + kMergeTable);
+    sm.part = reinterpret_cast<float4*>(sm.ml + kPgRows);
     static_assert(kBarCount * 8 <= 256, "the barriers' place");
     __shared__ Place s_place;
     __shared__ uint32_t s_total, s_from, s_to, s_tmem;
@@ -938,7 +970,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
         // ---- the rows ----
         uint32_t it0 = 0;
         uint4 qv[8];
-        auto rep_of = [](int live) { return live > 64 ? 1 : live > 32 ? 2 : 4; };
+        auto rep_of = [](int live) { return MANY ? copies_of(live) : 4; };
         // this thread's query row (zeros past the unit's)
         auto load_q = [&](const Walk& u) {
             const int r = tid & (kPgRows / rep_of(u.live) - 1);
@@ -970,9 +1002,9 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                                                             smem_u32(sm.v), tmem, u.v0, nt,
                                                             u.kvend, it0, lim);
             };
-            const RowsEnd e = rep == 1   ? run(std::integral_constant<int, 1>{})
-                              : rep == 2 ? run(std::integral_constant<int, 2>{})
-                                         : run(std::integral_constant<int, 4>{});
+            RowsEnd e;
+            if (MANY && rep == 1) e = run(std::integral_constant<int, 1>{});
+            else e = run(std::integral_constant<int, 4>{});
             const Walk done = u;
             more = u.next(p);
             if (more) load_q(u);  // on their way while this unit ends
@@ -985,8 +1017,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             tc_fence_after();
             const bool whole = done.v0 == 0 && done.v1 == done.tiles;
             const int slot = 2 * (int)blockIdx.x + (done.v0 == 0);
-            if (rep == 1) finish_rows<T, 1>(p, sm, tmem, done, whole, slot, e.m, e.l);
-            else if (rep == 2) finish_rows<T, 2>(p, sm, tmem, done, whole, slot, e.m, e.l);
+            if (MANY && rep == 1) finish_rows<T, 1>(p, sm, tmem, done, whole, slot, e.m, e.l);
             else finish_rows<T, 4>(p, sm, tmem, done, whole, slot, e.m, e.l);
             tc_fence_before();  // O is read before the next unit's products
             if (more) stage_q();
@@ -994,7 +1025,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                 // (the last share that starts before the unit's first cut, and before its last)
                 const uint32_t i0 = sh.holder(done.u0 + keep_lo(done.w) - 1);
                 const uint32_t i1 = sh.holder(done.u0 + keep_hi(done.w) - 1);
-                merge_pieces<T>(p, sm, done, (int)i0, (int)(i1 - i0) + 1, &s_last);
+                merge_pieces<T, MANY>(p, sm, done, (int)i0, (int)(i1 - i0) + 1, &s_last);
             }
         }
     }
@@ -1009,14 +1040,14 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
 constexpr int kMaxDevP = 64;
 
 // Once per kernel and device: its shared memory.
-template <typename T>
+template <typename T, bool MANY>
 bool prepare_paged() {
     static std::once_flag once[kMaxDevP];
     static bool ok[kMaxDevP];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevP) return false;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T>,
+        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T, MANY>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kPgSmem) == cudaSuccess;
         cudaGetLastError();
@@ -1024,16 +1055,16 @@ bool prepare_paged() {
     return ok[dev];
 }
 
-template <typename T>
+template <typename T, bool MANY>
 kvd_status run_paged(PagedParams& p, int nsm, const CUtensorMap& mk, const CUtensorMap& mv,
                      uint8_t* ws, bool pdl, cudaStream_t st) {
-    if (!prepare_paged<T>()) return KVD_ERR_CUDA;
+    if (!prepare_paged<T, MANY>()) return KVD_ERR_CUDA;
     const int blocks = std::min(kMaxCtas, nsm * kPgMinBlocks);
     p.ws_cnt = reinterpret_cast<int32_t*>(ws);
     p.ws_part = reinterpret_cast<float4*>(ws + KVD_WS_COUNTER_BYTES);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_part + (size_t)2 * blocks * 16 * p.slot_rows);
-    return launch(paged_attn_kernel<T>, dim3((unsigned)blocks), dim3(kPgThreads), kPgSmem, st, pdl,
-                  mk, mv, p);
+    return launch(paged_attn_kernel<T, MANY>, dim3((unsigned)blocks), dim3(kPgThreads), kPgSmem, st,
+                  pdl, mk, mv, p);
 }
 
 // Query vectors of the largest unit.
@@ -1108,6 +1139,9 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     const bool pdl = (flags & (KVD_FLAG_PDL | KVD_FLAG_EARLY_KV)) != 0;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    return dtype == KVD_BF16 ? run_paged<__nv_bfloat16>(p, nsm, mk, mv, ws, pdl, st)
-                             : run_paged<__half>(p, nsm, mk, mv, ws, pdl, st);
+    if (p.slot_rows > 32)
+        return dtype == KVD_BF16 ? run_paged<__nv_bfloat16, true>(p, nsm, mk, mv, ws, pdl, st)
+                                 : run_paged<__half, true>(p, nsm, mk, mv, ws, pdl, st);
+    return dtype == KVD_BF16 ? run_paged<__nv_bfloat16, false>(p, nsm, mk, mv, ws, pdl, st)
+                             : run_paged<__half, false>(p, nsm, mk, mv, ws, pdl, st);
 }
