@@ -60,9 +60,9 @@ constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it b
 
 // The list's weights (its length is below 2^32, see the host's check): a tile of a unit with more than 64 vectors (bound by the softmax) and with
 // at most 64 (bound by the copies), and what a unit costs besides.
-constexpr uint32_t kHeavy = 6, kLight = 4, kUnit = 24;
+constexpr uint32_t kHeavy = 6, kLight = 5, kUnit = 20;
 constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
-constexpr uint32_t kLeast = 12;     // a CTA's least share
+constexpr uint32_t kLeast = 20;     // a CTA's least share
 constexpr int kMaxCtas = 512;
 
 struct PagedParams {
@@ -385,8 +385,22 @@ __device__ __forceinline__ bool rows_any(bool x) {
         : "memory");
     return r != 0;
 }
-// The warp's wait for a phase.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+// Whether phase `parity` of the barrier is complete, without waiting. Asked for ahead of the use: an
+// answer takes about a hundred cycles.
+__device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// The warp's wait for a phase, of which `done` may tell that it is complete.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool done = false) {
+    if (__all_sync(0xffffffffu, done)) return true;
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
 }
 // One arrival for the warp, behind what its lanes did.
@@ -436,10 +450,12 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
         tc_st32_u(t_p + 32, z);
     }
     int t0 = v0 * kStep + base;  // of this thread's positions
+    bool s_done = false;
     for (int j = 0; j < n; ++j, t0 += kStep) {
         const uint32_t it = it0 + j;
-        if (!warp_wait(bars + 8 * kBarS, it & 1)) return {m, l, false};
+        if (!warp_wait(bars + 8 * kBarS, it & 1, s_done)) return {m, l, false};
         tc_fence_after();
+        bool p_free = false;
         uint32_t w[W / 2];
         if (t0 >= lim_most) {
             // the warp sees nothing of it
@@ -496,6 +512,7 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
             }
             // the weights, rounded to the storage type; their sum is taken before that (rounding
             // to nearest leaves no bias)
+            if (j >= 1) p_free = mbar_done(bars + 8 * kBarO, (it - 1) & 1);
             const float nref = m == -INFINITY ? 0.f : -m;
             const Pair cs2(cs, cs), ref2(nref, nref);
             Pair sum[4] = {Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f)};
@@ -510,8 +527,9 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
             l += all.x + all.y;
         }
         // the weights' last reader is P.V of the tile before
-        if (j >= 1 && !warp_wait(bars + 8 * kBarO, (it - 1) & 1)) return {m, l, false};
+        if (j >= 1 && !warp_wait(bars + 8 * kBarO, (it - 1) & 1, p_free)) return {m, l, false};
         tc_fence_after();
+        s_done = j + 1 < n && mbar_done(bars + 8 * kBarS, (it + 1) & 1);
         if constexpr (W == 128) {
             tc_st32_u(t_p, w);
             tc_st32_u(t_p + 32, w + 32);
@@ -747,14 +765,14 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
         return;
     }
     // a thread per row, 4 dims and, of few rows, share of the pieces; the shares joined in order
-    constexpr int kBatch = 8;  // pieces whose loads are in flight
+    constexpr int kBatch = MANY ? 8 : 12;  // pieces whose loads are in flight
     const int items = u.live * 16, shares = max(1, kRowThreads / items);
     auto store = [&](int y, const Joined& a) {
-        *reinterpret_cast<uint2*>(out_row<T>(p, u, y % u.live) + y / u.live * 4) =
+        *reinterpret_cast<uint2*>(out_row<T>(p, u, y >> 4) + (y & 15) * 4) =
             pack4<T>(a.o, a.l > 0.f ? 1.f / a.l : 0.f);
     };
     for (int x = tid; x < items * shares; x += kRowThreads) {
-        const int share = x / items, y = x - share * items, c = y / u.live, r = y - c * u.live;
+        const int share = x / items, y = x - share * items, c = y & 15, r = y >> 4;
         const int last = n * (share + 1) / shares;
         Joined a;
         a.clear();
