@@ -40,19 +40,19 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kPer = 16;                          // logits per thread and round
 constexpr int kRound = kLpThreads * kPer;
-constexpr int kRingBytes = 2 * kRound * 4;         // 2 rounds of fp32, 4 of 16-bit logits
-constexpr int kLpStages = 4;
+constexpr int kStageBytes = kRound * 4;           // a round of fp32, two of 16-bit logits
+constexpr int kStages = 2;                        // of the ring
 constexpr int kGroups = 64;
 constexpr int kRanked = 128;                      // keys ranked by counting
 constexpr int kNotedSoft = 64;                    // noted chunks from which they are looked into
-constexpr int kNotedCap = kNotedSoft + kLpThreads;  // (a round notes one per thread at most)
+constexpr int kNotedCap = kNotedSoft + 2 * kLpThreads;  // (a round notes one per thread at most)
 constexpr int kPass = 64;                         // noted chunks per pass
 constexpr int kListSoft = 256;                    // keys from which the list is cut
 constexpr int kListCap = kListSoft + kPass * kPer + 32;  // (and 2 x 7 from the row's ends)
 constexpr int kLpMaxCluster = 16;
 constexpr float kFar = -3.402823466e38f;          // for -inf in weight * exponent (0 * -inf is NaN)
 // Blocks a launch should have before rows are no longer split.
-constexpr int64_t kLpManyBlocks = 152 * 3;
+constexpr int64_t kLpManyBlocks = 152 * 4;
 
 constexpr float kLn2 = 0.69314718056f;
 
@@ -81,7 +81,7 @@ struct Part {
     float m, n, rest, ent;
 };
 struct __align__(128) LpShared {
-    uint8_t ring[kRingBytes];
+    uint8_t ring[kStages * kStageBytes];
     Key list[kListCap];
     Key group[kLpThreads];
     int32_t noted[kNotedCap];                       // round * kLpThreads + thread
@@ -96,7 +96,7 @@ struct __align__(128) LpShared {
     int32_t token[KVD_MAX_GIVEN];
     float value[KVD_MAX_GIVEN];                     // the tokens' logits
     int32_t place[kGroups];
-    uint64_t bars[kLpStages];
+    uint64_t bars[kStages];
     Key bound;
     int32_t n_list, n_noted;
 };
@@ -111,6 +111,13 @@ __device__ __forceinline__ float key_value(Key k) {
     return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 __device__ __forceinline__ int key_id(Key k) { return (int)~(uint32_t)k; }
+
+// The largest key of a warp: the high words first, then the low ones of the lanes that have it.
+__device__ __forceinline__ Key warp_max_key(Key k) {
+    const uint32_t hi = (uint32_t)(k >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, hi == top ? (uint32_t)k : 0u);
+    return ((Key)top << 32) | lo;
+}
 
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float d;
@@ -165,6 +172,17 @@ __device__ __forceinline__ Part shfl_part(const Part& a, int off) {
     r.rest = __shfl_xor_sync(0xffffffffu, a.rest, off);
     r.ent = __shfl_xor_sync(0xffffffffu, a.ent, off);
     return r;
+}
+
+// n parts, at most N of them (a power of two), joined by a warp; every lane gets the result.
+template <int N>
+__device__ __forceinline__ Part join_few(const Part* parts, int n, float c) {
+    const int lane = threadIdx.x & 31;
+    Part a = {-INFINITY, 0.f, 0.f, 0.f};
+    if (lane < n) a = parts[lane];
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) a = join(a, shfl_part(a, o), c);
+    return a;
 }
 
 // The largest of the warp's values (none is NaN).
@@ -321,13 +339,18 @@ __device__ __noinline__ void cut_list(LpShared& S, int n) {
 __device__ __forceinline__ void rank_list(LpShared& S, int n, Key* out) {
     const int tid = threadIdx.x;
     while (S.n_list > kRanked) cut_list(S, n);  // (uniform)
-    const int have = S.n_list;
+    const int have = S.n_list, whole = (have + 3) & ~3;
     if (tid < n) out[tid] = 0;
+    if (tid >= have && tid < whole) S.list[tid] = 0;
     __syncthreads();
     if (tid < have) {
         const Key mine = S.list[tid];
+        const ulonglong2* list = reinterpret_cast<const ulonglong2*>(S.list);
         int above = 0;
-        for (int i = 0; i < have; ++i) above += S.list[i] > mine;
+        for (int i = 0; i < whole / 2; i += 2) {
+            const ulonglong2 a = list[i], b = list[i + 1];
+            above += (a.x > mine) + (a.y > mine) + (b.x > mine) + (b.y > mine);
+        }
         if (above < n) out[above] = mine;
     }
     __syncthreads();
@@ -343,20 +366,30 @@ __device__ __noinline__ void look_into(LpShared& S, const T* x, int id0, int vec
     constexpr int VN = Vec<T>::n, NV = kPer / VN;
     const int tid = threadIdx.x, have = S.n_noted;
     for (int c0 = 0; c0 < have; c0 += kPass) {
-        const int i = c0 + tid / NV;
-        if (tid < kPass * NV && i < have) {
-            const int chunk = S.noted[i], r = chunk / kLpThreads;
-            const int v = (r * NV + tid % NV) * kLpThreads + chunk % kLpThreads;
-            if (v < vecs) {
-                float f[VN];
-                Vec<T>::get(__ldg(reinterpret_cast<const uint4*>(x) + v), f);
-                const Key bound = S.bound;
+        const int n_vec = min(kPass, have - c0) * NV;
+        constexpr int kEach = (kPass * NV + kLpThreads - 1) / kLpThreads;  // vectors per thread
+        uint4 raw[kEach];
+        int at[kEach];
 #pragma unroll
-                for (int e = 0; e < VN; ++e)
-                    if (f[e] > -INFINITY) {  // (not NaN)
-                        const Key k = make_key(f[e], id0 + v * VN + e);
-                        if (k >= bound) push(S, k);
-                    }
+        for (int k = 0; k < kEach; ++k) {
+            const int i = tid + k * kLpThreads;
+            at[k] = vecs;
+            if (i < n_vec) {
+                const int chunk = S.noted[c0 + i / NV];
+                at[k] = (chunk / kLpThreads * NV + i % NV) * kLpThreads + chunk % kLpThreads;
+                if (at[k] < vecs) raw[k] = __ldg(reinterpret_cast<const uint4*>(x) + at[k]);
+            }
+        }
+        const Key bound = S.bound;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            if (at[k] >= vecs) continue;
+            float f[VN];
+            Vec<T>::get(raw[k], f);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                const Key key = make_key(f[e], id0 + at[k] * VN + e);
+                if (key >= bound && f[e] > -INFINITY) push(S, key);  // (not NaN)
             }
         }
         __syncthreads();
@@ -391,8 +424,8 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     LpShared& S = *reinterpret_cast<LpShared*>(
         (reinterpret_cast<uintptr_t>(lp_smem) + 127) & ~uintptr_t(127));
     constexpr int VN = Vec<T>::n, NV = kPer / VN;
-    constexpr int kStageBytes = kRound * (int)sizeof(T), kStages = kRingBytes / kStageBytes;
-    static_assert(kStages <= kLpStages, "a barrier per stage");
+    constexpr int kSub = 4 / (int)sizeof(T);  // rounds per stage
+    static_assert(kSub <= 2, "the noted chunks' place");
     constexpr int kTok = GIVEN == 2 ? KVD_MAX_GIVEN : 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)(blockIdx.x % (unsigned)p.cluster);
@@ -412,15 +445,16 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     const int body = min(hi, lo + (off ? VN - off : 0));
     const int vecs = (hi - body) / VN, tail = body + vecs * VN;
     const int rounds = (vecs + NV * kLpThreads - 1) / (NV * kLpThreads);
-    auto copy = [&](int r) {  // one thread
-        const int at = r * kStageBytes, bytes = min(kStageBytes, vecs * 16 - at);
-        const uint32_t bar = smem_u32(&S.bars[r % kStages]);
+    const int stages = (rounds + kSub - 1) / kSub;
+    auto copy = [&](int g) {  // one thread
+        const int at = g * kStageBytes, bytes = min(kStageBytes, vecs * 16 - at);
+        const uint32_t bar = smem_u32(&S.bars[g % kStages]);
         mbar_expect_tx(bar, bytes);
-        bulk_load(smem_u32(S.ring + r % kStages * kStageBytes),
+        bulk_load(smem_u32(S.ring + g % kStages * kStageBytes),
                   reinterpret_cast<const uint8_t*>(x + body) + at, bytes, bar);
     };
     if (tid == 0)
-        for (int r = 0; r < min(kStages, rounds); ++r) copy(r);
+        for (int g = 0; g < min(kStages, stages); ++g) copy(g);
     const float T_ = p.temperature ? p.temperature[row] : 1.f;
     const bool bad_t = !(T_ > 0.f) || !(T_ < INFINITY);
     if (tid < p.given) {
@@ -461,12 +495,15 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     sum.a = {-INFINITY, 0.f, 0.f, 0.f};
     sum.c = kLog2e / T_;
     sum.mc = sum.lo = 0.f;
-    float bound_v = -INFINITY;  // of S.bound
+    // alternatives: one is the largest key seen, several take a bound and a list
+    const bool single = p.top == 1, several = p.top > 1;
+    float bound_v = -INFINITY;  // of S.bound; of a single one, the thread's largest so far
+    int best_id = -1;
     // The first round's largest logits and bound. cm: the thread's largest, of id `id`.
     auto begin = [&](float cm, int id) {
         const float w = warp_max(fmaxf(cm, end_v));
         if (lane == 0) S.first[warp] = w;
-        if (p.top > 0) {
+        if (several) {
             const bool head = end_v > -INFINITY && end_id < body;
             const Key mine = head ? make_key(end_v, end_id) : 0;
             S.group[tid] = max(mine, cm > -INFINITY ? make_key(cm, id) : 0);
@@ -489,8 +526,11 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     // One round; MASKED: the first, or one with vectors that lie behind the slice.
     auto round = [&](int r, auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
-        dead = dead || !mbar_wait_bounded(smem_u32(&S.bars[r % kStages]), (r / kStages) & 1);
-        const uint4* st = reinterpret_cast<const uint4*>(S.ring + r % kStages * kStageBytes) + tid;
+        const int g = r / kSub, sub = r % kSub;
+        if (sub == 0)
+            dead = dead || !mbar_wait_bounded(smem_u32(&S.bars[g % kStages]), (g / kStages) & 1);
+        const uint4* st = reinterpret_cast<const uint4*>(S.ring + g % kStages * kStageBytes) +
+                          sub * NV * kLpThreads + tid;
         // the thread's first vector; kLpThreads apart
         const int v0 = r * NV * kLpThreads + tid;
         float v[kPer];
@@ -517,14 +557,17 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
             for (int i = 0; i < kPer; ++i) v[i] = fmaxf(v[i], -INFINITY);
             cm = largest();
         }
-        if (MASKED && r == 0) {
+        auto id_of_largest = [&]() {
             int id = 0;
-            if (p.top > 0) {
 #pragma unroll
-                for (int i = kPer - 1; i >= 0; --i)
-                    if (v[i] == cm) id = body + (v0 + i / VN * kLpThreads) * VN + i % VN;
-            }
-            begin(cm, id);
+            for (int i = kPer - 1; i >= 0; --i)
+                if (v[i] == cm) id = body + (v0 + i / VN * kLpThreads) * VN + i % VN;
+            return id;
+        };
+        if (MASKED && r == 0) begin(cm, several ? id_of_largest() : 0);
+        if (single && cm > bound_v) {
+            bound_v = cm;
+            best_id = id_of_largest();
         }
         const float top_of = warp_max(cm);
         if (top_of > -INFINITY) {  // (the same in the whole warp, like the reference)
@@ -554,14 +597,14 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
             }
         }
         // (later ids need more than the bound's logit)
-        const bool note = p.top > 0 && cm > -INFINITY &&
+        const bool note = several && cm > -INFINITY &&
                           (MASKED && r == 0 ? cm >= bound_v : cm > bound_v);
         if (note) {
             const int at = atomicAdd(&S.n_noted, 1);
             S.noted[at] = r * kLpThreads + tid;
-            full = at >= kNotedSoft;
+            full |= at >= kNotedSoft;
         }
-        if (MASKED && rounds == 1 && p.top > 0) {
+        if (MASKED && rounds == 1 && several) {
             // a short slice: straight to the list, while the logits are at hand
             __syncthreads();
             const int noted = S.n_noted;
@@ -580,14 +623,19 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
             }
         }
     };
-    int issued = min(kStages, rounds);
+    int issued = min(kStages, stages);
     bool lost = false;
     if (rounds == 0) begin(-INFINITY, 0);
-    for (int r = 0; r < rounds; ++r) {
+    for (int g = 0; g < stages; ++g) {
         full = false;
-        if (r > 0 && (r + 1) * NV * kLpThreads <= vecs) round(r, std::false_type{});
-        else round(r, std::true_type{});
-        if (r + 1 == rounds) break;
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+            const int r = g * kSub + sub;
+            if (r >= rounds) break;
+            if (r > 0 && (r + 1) * NV * kLpThreads <= vecs) round(r, std::false_type{});
+            else round(r, std::true_type{});
+        }
+        if (g + 1 == stages) break;
         // the stage is read; (nobody notes a chunk while they are looked into)
         if (__syncthreads_or(dead || full)) {
             if ((lost = __syncthreads_or(dead))) break;
@@ -595,7 +643,7 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
             const Key bound = S.bound;
             bound_v = bound == 1 ? -INFINITY : key_value(bound);
         }
-        if (issued < rounds) {
+        if (issued < stages) {
             if (tid == 0) {
                 fence_proxy_async();
                 copy(issued);
@@ -610,8 +658,18 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     Part a = sum.a;
     const float c = sum.c;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = join(a, shfl_part(a, o), c);
+    for (int o = 16; o > 0; o >>= 1) {  // (the warp shares its reference)
+        a.n += __shfl_xor_sync(0xffffffffu, a.n, o);
+        a.rest += __shfl_xor_sync(0xffffffffu, a.rest, o);
+        a.ent += __shfl_xor_sync(0xffffffffu, a.ent, o);
+    }
     if (lane == 0) S.part[warp] = a;
+    if (single) {
+        Key k = best_id >= 0 ? make_key(bound_v, best_id) : 0;
+        if (end_v > -INFINITY) k = max(k, make_key(end_v, end_id));
+        k = warp_max_key(k);
+        if (lane == 0) S.group[warp] = k;
+    }
     if (GIVEN) {
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
@@ -625,15 +683,17 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     if (__syncthreads_or(dead)) lost = true;
     if (lost && tid == 0) {
         flag_error(p.dev_err, KVD_ERR_TIMEOUT);
-        for (int r = max(0, issued - kStages); r < issued; ++r)
-            mbar_wait_bounded(smem_u32(&S.bars[r % kStages]), (r / kStages) & 1);
+        for (int g = max(0, issued - kStages); g < issued; ++g)
+            mbar_wait_bounded(smem_u32(&S.bars[g % kStages]), (g / kStages) & 1);
     }
-    if (tid == 0) {
-#pragma unroll 1
-        for (int w = 1; w < kLpWarps; ++w) a = join(a, S.part[w], c);
-    }
+    if (warp == 0) a = join_few<kLpWarps>(S.part, kLpWarps, c);
     Key* best = S.group;  // [top]
-    if (p.top > 0) {
+    if (single) {
+        if (warp == 0) {
+            const Key k = warp_max_key(lane < kLpWarps ? S.group[lane] : 0);
+            if (lane == 0) best[0] = k;
+        }
+    } else if (several) {
         if (S.n_noted > 0 && !lost) look_into<T>(S, x + body, body, vecs, p.top);
         if (end_id >= body && end_v > -INFINITY) {
             const Key k = make_key(end_v, end_id);
@@ -658,20 +718,23 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
         asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (rank != 0) return;
-        if (tid == 0) {
-            a = S.ex_part[0];
-#pragma unroll 1
-            for (int k = 1; k < p.cluster; ++k) a = join(a, S.ex_part[k], c);
-            S.n_list = p.cluster * p.top;
-        }
+        if (warp == 0) a = join_few<kLpMaxCluster>(S.ex_part, p.cluster, c);
+        if (tid == 0) S.n_list = p.cluster * p.top;
         if (GIVEN && tid < p.given) {
             int n = 0;
             for (int k = 0; k < p.cluster; ++k) n += S.ex_count[k][tid];
             S.count[tid] = n;
         }
-        for (int i = tid; i < p.cluster * p.top; i += kLpThreads) S.list[i] = S.ex_key[i];
-        __syncthreads();
-        if (p.top > 0) rank_list(S, p.top, best);
+        if (single) {
+            if (warp == 0) {
+                const Key k = warp_max_key(lane < p.cluster ? S.ex_key[lane] : 0);
+                if (lane == 0) best[0] = k;
+            }
+        } else if (several) {
+            for (int i = tid; i < p.cluster * p.top; i += kLpThreads) S.list[i] = S.ex_key[i];
+            __syncthreads();
+            rank_list(S, p.top, best);
+        }
     }
     if (bad_t || lost) {
         if (bad_t && tid == 0) flag_error(p.dev_err, KVD_ERR_BAD_PARAM);
