@@ -672,16 +672,19 @@ kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32
  * workspace: kvd_workspace_size(KVD_OP_PAGED_ATTN, batch, n_heads, n_kv_heads, 1, max_new, ..)
  *            bytes, under the rules of the other attention calls
  * Q.K^T and P.V run on the tensor cores with fp32 accumulation. Weights are rounded to the storage
- * type before they meet V, as kvd_window_attn's; their sum is taken before that. Positions from
- * lens[b] on do not reach the outputs, whatever the pages hold there. (An infinity or a NaN in V
- * of a new token can make the outputs of other new tokens of its row NaN: their weight for it is
- * 0, and 0 * inf is NaN.)
+ * type before they meet V, as kvd_window_attn's; their sum is taken before that. What a token does
+ * not see does not reach its outputs, whatever the pages hold there, infinities and NaN included.
+ * (An infinity in V that it sees makes that output the infinity, or NaN where its weight rounds to
+ * 0.)
  * The same call gives the same bits on every run; how a row is split depends on the whole batch.
  * Flags: KVD_FLAG_PDL; KVD_FLAG_EARLY_KV gives what KVD_FLAG_PDL gives. KVD_FLAG_TEST_STALL: the
  * first tile of every thread block never completes (the call reports KVD_ERR_TIMEOUT).
  * Device errors: lens[b] outside [n_b, capacity] or n_b > max_new -> KVD_ERR_LEN_OVERFLOW, the
- * row's outputs are left as they are; a page outside [0, n_pages) -> KVD_ERR_BAD_INDEX, its
- * positions count as rows of zeros.
+ * row's outputs are left as they are (all rows' where overlapping stretches of `starts` make more
+ * tiles than 32 bits count); KVD_ERR_TIMEOUT as in kvd_decode_attn; a page outside [0, n_pages) -> KVD_ERR_BAD_INDEX, its
+ * positions count as rows of zeros. KVD_ERR_UNSUPPORTED: more tiles than 32 bits count, with rows
+ * as long as the table allows (n_kv_heads * (n_tokens * n_heads / n_kv_heads / 128 + batch) units
+ * of up to page_size * table_width / 128 tiles: above about 8e8).
  */
 kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache *cache, int32_t n_tokens,
                           int32_t max_new, const kvd_token_rows *q, const int32_t *starts,
@@ -824,7 +827,8 @@ kvd_status kvd_sample_filtered(const float *logits, int64_t row_stride, int32_t 
  * above -inf has Z = -inf, entropy 0, logprob -inf. The same bits on every run.
  * Device errors: a NaN logit -> KVD_ERR_NAN; a token outside [-1, vocab) -> KVD_ERR_BAD_TOKEN
  * (treated as -1); a temperature out of range -> KVD_ERR_BAD_PARAM, the row's outputs are left as
- * they are. No workspace. rows <= 2^31 / 16.
+ * they are; KVD_ERR_TIMEOUT: a bounded wait gave up, the row's outputs are left. No workspace. rows
+ * <= 2^31 / 16.
  */
 kvd_status kvd_token_logprobs(kvd_dtype dtype, const void *logits, int64_t row_stride,
                               int32_t rows, int32_t vocab, const float *temperature,

@@ -26,8 +26,9 @@
 //    copying warp runs ahead into the CTA's next unit.
 //  * A softmax row's reference moves only when its maximum grows by more than 2^8.
 #include <algorithm>
-#include <atomic>
+#include <climits>
 #include <cmath>
+#include <cstring>
 #include <mutex>
 #include <type_traits>
 
@@ -52,15 +53,16 @@ static_assert(kPgCols >= kPgColsP + kStep / 2 && kPgMinBlocks * kPgCols <= 512,
               "the resident blocks' tensor memory");
 constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
 constexpr int kFewPieces = 6;                  // of a merge with a thread per row
-// shared memory: K slots | V slots | Q | barriers | rows' references and sums | merge
+constexpr uint32_t kOddOffset = 256 + kPgRows * 8 + kRowThreads * 16;  // behind the barriers
+constexpr int kOddWords = 3 * kHeadDim;        // see scan_hidden
+// shared memory: K slots | V slots | Q | barriers | rows' references and sums | merge | odd
 constexpr uint32_t kPgSmem = (kSlotsK + kSlotsV) * kStepBytes + kPgQBytes + 256 + kPgRows * 8 +
-                             kRowThreads * 16 + 1024;
+                             kRowThreads * 16 + kOddWords * 4 + 16 + 1024;
 constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
 
-// The list's weights (its length is below 2^32, see the host's check): a tile of a unit with more than 64 vectors (bound by the softmax) and with
-// at most 64 (bound by the copies), and what a unit costs besides.
-constexpr uint32_t kHeavy = 6, kLight = 5, kUnit = 20;
+// The list's weights: of a tile, and what a unit costs besides.
+constexpr uint32_t kWeight = 5, kUnit = 20;
 constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
 constexpr uint32_t kLeast = 20;     // a CTA's least share
 constexpr int kMaxCtas = 512;
@@ -76,7 +78,8 @@ struct PagedParams {
     int32_t batch, n_tokens, max_new, capacity;
     int32_t n_q_heads, n_kv_heads, group, tq;  // tq: tokens per unit
     int32_t n_pages, page_log2, box_rows, boxes;  // boxes per tile
-    float scale_log2;
+    float scale_log2;         // above 0; the scale's sign goes into the queries
+    int32_t scale_sign;
     float4* ws_part;          // [2 CTAs][16][slot_rows]: 4 dims of a row
     float2* ws_ml;            // [2 CTAs][slot_rows]: reference, sum
     int32_t* ws_cnt;          // a ticket per CTA that holds the first piece of a cut unit
@@ -152,14 +155,13 @@ __device__ __forceinline__ int tiles_of(const PagedParams& p, const Shape& s, in
 }
 // Units of at most 32 vectors hold them four times.
 __device__ __forceinline__ int copies_of(int live) { return live > 32 ? 1 : 4; }
-__device__ __forceinline__ uint32_t tile_weight(int live) { return live > 32 ? kHeavy : kLight; }
 __device__ __forceinline__ uint32_t unit_weight(const PagedParams& p, const Shape& s, int mb) {
-    return tiles_of(p, s, mb) * tile_weight(live_rows(p, s, mb)) + kUnit;
+    return tiles_of(p, s, mb) * kWeight + kUnit;
 }
-// Weight of the first k blocks of one head, 0 <= k < nmb: they are full, so heavy (tq * g > 32).
+// Weight of the first k blocks of one head, 0 <= k < nmb (they are full).
 __device__ __forceinline__ uint32_t full_blocks(const PagedParams& p, const Shape& s, int k) {
     if (k == 0) return 0;
-    return kHeavy * floor_sum((uint32_t)k, (uint32_t)p.tq,
+    return kWeight * floor_sum((uint32_t)k, (uint32_t)p.tq,
                                 (uint32_t)(s.s0() + p.tq + kStep - 1)) + (uint32_t)k * kUnit;
 }
 __device__ __forceinline__ uint32_t row_weight(const PagedParams& p, const Row& r) {
@@ -169,7 +171,13 @@ __device__ __forceinline__ uint32_t row_weight(const PagedParams& p, const Row& 
 }
 
 // Prefix sums over the rows' weights: tab[e] is the list's length up to and with the rows of entry
-// e, `each` rows an entry.
+// e, `each` rows an entry. The host has bounded the length that distinct rows can give; sums that
+// leave 32 bits all the same (stretches of tokens that overlap) stay at kTooLong.
+constexpr uint32_t kTooLong = 0xffffffffu;
+__device__ __forceinline__ uint32_t add_length(uint32_t a, uint32_t b) {
+    const uint32_t s = a + b;
+    return s < a ? kTooLong : s;
+}
 struct Table {
     uint32_t* tab;
     int each, n;
@@ -184,7 +192,7 @@ __device__ __forceinline__ Table fill_table(const PagedParams& p, uint32_t* tab)
         uint32_t w = 0;
         for (int b = e * t.each; b < min((e + 1) * t.each, p.batch); ++b) {
             bool bad;
-            w += row_weight(p, row_of(p, b, bad));
+            w = add_length(w, row_weight(p, row_of(p, b, bad)));
             if (bad && blockIdx.x == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
         }
         tab[e] = w;
@@ -199,9 +207,9 @@ __device__ __forceinline__ uint32_t finish_table(const Table& t) {
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += o;
+            if (lane >= off) inc = add_length(inc, o);
         }
-        inc += before;
+        inc = add_length(inc, before);
         if (e0 + lane < t.n) t.tab[e0 + lane] = inc;
         before = __shfl_sync(0xffffffffu, inc, 31);
     }
@@ -310,15 +318,22 @@ struct Walk {
     // of the unit
     int live, kvend, tiles, v0, v1;
     uint32_t w;
+    // The first position that some token of the unit does not see, and whether the stretch has it.
+    __device__ __forceinline__ int hidden(const PagedParams& p) const {
+        return s.s0() + mb * p.tq + 1;
+    }
+    __device__ __forceinline__ bool hides(const PagedParams& p) const {
+        const int at = hidden(p);
+        return at < kvend && at < v1 * kStep;
+    }
     __device__ __forceinline__ void unit(const PagedParams& p) {
         live = live_rows(p, s, mb);
         kvend = kv_end(p, s, mb);
         tiles = tiles_of(p, s, mb);
-        const uint32_t tw = tile_weight(live);
-        w = tiles * tw + kUnit;
+        w = tiles * kWeight + kUnit;
         const uint32_t in = cur - u0, out = min(w, end - u0);
-        v0 = in > kUnit ? (in - kUnit) / tw : 0;
-        v1 = out == w ? tiles : (out - kUnit) / tw;
+        v0 = in > kUnit ? (in - kUnit) / kWeight : 0;
+        v1 = out == w ? tiles : (out - kUnit) / kWeight;
     }
     // From the unit that holds `from` or ends there; false if there is nothing before `to`.
     __device__ __forceinline__ bool start(const PagedParams& p, const Place& u, uint32_t from,
@@ -367,7 +382,8 @@ enum PgBar {
     kBarP = kBarRead + 1,               // weights written by every row (an arrival per warp)
     kBarO = kBarP + 1,                  // the products with V done (MMA commit)
     kBarQ = kBarO + 1,                  // the unit's rows staged (an arrival per warp)
-    kBarDrain = kBarQ + 1,              // every MMA issued so far done (after a failure)
+    kBarScan = kBarQ + 1,               // the unit's hidden rows of V looked through (an arrival)
+    kBarDrain = kBarScan + 1,           // every MMA issued so far done (after a failure)
     kBarCount = kBarDrain + 1
 };
 
@@ -414,32 +430,141 @@ struct Smem {
     uint64_t* bars;
     float2* ml;      // [128]
     float4* part;    // [128]
+    int32_t* odd;    // [3][64], see scan_hidden
     __device__ __forceinline__ uint32_t bar(int i) const { return smem_u32(&bars[i]); }
 };
 
+__device__ __forceinline__ Smem smem_at(uint8_t* base) {
+    Smem sm;
+    sm.k = base;
+    sm.v = sm.k + kSlotsK * kStepBytes;
+    sm.q = sm.v + kSlotsV * kStepBytes;
+    sm.bars = reinterpret_cast<uint64_t*>(sm.q + kPgQBytes);
+    sm.ml = reinterpret_cast<float2*>(sm.q + kPgQBytes + 256);
+    sm.part = reinterpret_cast<float4*>(sm.ml + kPgRows);
+    sm.odd = reinterpret_cast<int32_t*>(sm.part + kRowThreads);
+    return sm;
+}
+
+// The loop over a unit's tiles takes all registers that a thread has. So what the row warps need
+// before and behind it is not kept meanwhile: the walk lies in shared memory, a copy per warp,
+// written by every lane alike; addresses and the thread's number are formed anew (these forms keep
+// the compiler from saving them). With 25 registers spilled around the loop a chunk of 512 tokens
+// over 16384 positions took 94 us, without 75.
+template <typename S> __device__ __forceinline__ void put_away(uint32_t* to, const S& s) {
+    uint32_t w[sizeof(S) / 4];
+    memcpy(w, &s, sizeof(S));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(S) / 4; ++i) reinterpret_cast<volatile uint32_t*>(to)[i] = w[i];
+    __syncwarp();
+}
+template <typename S> __device__ __forceinline__ S take_back(const uint32_t* from) {
+    uint32_t w[sizeof(S) / 4];
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(S) / 4; ++i)
+        w[i] = reinterpret_cast<const volatile uint32_t*>(from)[i];
+    S s;
+    memcpy(&s, w, sizeof(S));
+    return s;
+}
+__device__ __forceinline__ uint8_t* smem_base(uint8_t* raw) {
+    asm volatile("" : "+l"(raw));
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+}
+__device__ __forceinline__ int row_thread() {
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    return t;
+}
+
+// ------------------------------------------------- infinities and NaN behind the mask --
+// Positions that only some tokens of a unit see have weight 0 for the others, and 0 * inf is NaN.
+// So what is not finite in those rows of V is taken out before the product, and noted: the first
+// position of each dim with +inf, -inf and NaN. It is added to the outputs of the tokens that see it
+// (repair). One warp, behind the copy of the tile at `base` and before the product that reads it;
+// positions lo .. hi - 1. Returns whether there was any.
+template <typename T>
+__device__ __forceinline__ bool scan_hidden(uint32_t tile, int base, int lo, int hi, int32_t* odd) {
+    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    bool any = false;
+    for (int x = threadIdx.x & 31; x < (hi - lo) * 8; x += 32) {
+        const int pos = lo + (x >> 3);
+        const uint32_t at = tile + swz(pos - base, x & 7);
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at)
+                     : "memory");
+        bool here = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) here |= ((w[i >> 1] >> (16 * (i & 1))) & kExp) == kExp;
+        if (!here) continue;
+        any = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t v = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+            if ((v & kExp) != kExp) continue;
+            const int kind = (v & 0x7fffu) != kExp ? 2 : (int)(v >> 15);
+            atomicMin(odd + kind * kHeadDim + (x & 7) * 8 + i, pos);
+            w[i >> 1] &= i & 1 ? 0xffffu : 0xffff0000u;
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3])
+                     : "memory");
+    }
+    any = __any_sync(0xffffffffu, any);
+    if (any) fence_proxy_async();
+    __syncwarp();
+    return any;
+}
+__device__ __forceinline__ int lds_s32(uint32_t at) {
+    int v;
+    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+// A lane's outputs, with what scan_hidden took out at positions before `lim`; of a copy of the row,
+// with those of its W positions of a tile from `base` on.
+__device__ __forceinline__ void repair(uint32_t t_o, uint32_t odd, int lim, int base, int W) {
+#pragma unroll 1
+    for (int h = 0; h < kHeadDim; h += 16) {
+        float o[16];
+        uint32_t w[16];
+        tc_ld16(t_o + h, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+#pragma unroll
+            for (int kind = 0; kind < 3; ++kind) {
+                const int pos = lds_s32(odd + 4 * (kind * kHeadDim + h + i));
+                if (pos < lim && (uint32_t)(pos % kStep - base) < (uint32_t)W)
+                    o[i] += __uint_as_float(kind == 0 ? 0x7f800000u
+                                                      : kind == 1 ? 0xff800000u : 0x7fffffffu);
+            }
+            w[i] = __float_as_uint(o[i]);
+        }
+        tc_st16_u(t_o + h, w);
+    }
+}
+
 // ---------------------------------------------------------------- the rows ----------
-// `n` tiles of a unit from v0 on, the first with number it0 in the CTA: scores into weights, one
-// row per thread. REP copies of the rows, each with W = 128 / REP positions of a tile. Keys t < lim
-// are visible, and t < kvend to any row. (A function of its own, so that what the caller keeps
-// takes no registers from the loop.)
+// Tiles of a unit from v0 on, with numbers it .. end - 1 in the CTA: scores into weights, one row
+// per thread. REP copies of the rows, each with W = 128 / REP positions of a tile. Keys t < lim are
+// visible, and t < kvend to any row. scan: -1, or the phase of kBarScan. (A function of its own, so
+// that what the caller keeps takes no registers from the loop.)
 struct RowsEnd {
     float m, l;  // this thread's reference (log2 units) and sum
     bool ok;     // every wait ended
 };
 template <typename T, int REP>
-__device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32_t sv,
-                                         uint32_t tmem, int v0, int n, int kvend, uint32_t it0,
-                                         int lim) {
+__device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32_t tmem, int v0,
+                                         uint32_t it, uint32_t end, int kvend, int lim, int scan) {
     static_assert(REP == 1 || REP == 4, "W is 128 or 32");
     constexpr int W = kStep / REP;
     const int tid = threadIdx.x;
-    const int base = tid / (kPgRows / REP) * W;  // of this copy's positions in a tile
+    const int base = REP == 1 ? 0 : tid / (kPgRows / REP) * W;  // of this copy's positions in a tile
     const uint32_t lanes = tmem + ((uint32_t)(tid & ~31) << 16);
     const uint32_t t_s = lanes + base, t_o = lanes + kPgColsO, t_p = lanes + kPgColsP;
-    const bool pos_scale = scale_log2 > 0.f;
-    const float cs = pos_scale ? scale_log2 : 1.f;
-    const int lim_least = __reduce_min_sync(0xffffffffu, lim);
-    const int lim_most = __reduce_max_sync(0xffffffffu, lim);
+    bool first_tile = true;
     float m = -INFINITY, l = 0.f;
     if (REP > 1) {
         // what the other copies hold stays zero in this lane
@@ -451,13 +576,12 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
     }
     int t0 = v0 * kStep + base;  // of this thread's positions
     bool s_done = false;
-    for (int j = 0; j < n; ++j, t0 += kStep) {
-        const uint32_t it = it0 + j;
+    for (; it != end; ++it, t0 += kStep, first_tile = false) {
         if (!warp_wait(bars + 8 * kBarS, it & 1, s_done)) return {m, l, false};
         tc_fence_after();
         bool p_free = false;
         uint32_t w[W / 2];
-        if (t0 >= lim_most) {
+        if (__builtin_expect(__all_sync(0xffffffffu, t0 >= lim), 0)) {
             // the warp sees nothing of it
             tc_fence_before();
             warp_arrive(bars + 8 * kBarRead);
@@ -469,11 +593,7 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
             else tc_ld32(t_s, s);
             tc_fence_before();
             warp_arrive(bars + 8 * kBarRead);
-            if (!pos_scale) {
-#pragma unroll
-                for (int i = 0; i < W; ++i) s[i] *= scale_log2;
-            }
-            if (t0 + W > lim_least) {
+            if (__builtin_expect(__any_sync(0xffffffffu, t0 + W > lim), 0)) {
 #pragma unroll
                 for (int i = 0; i < W; ++i) s[i] = t0 + i < lim ? s[i] : -INFINITY;
             }
@@ -486,16 +606,16 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
                 pm[e] = fmaxf(pm[e], s[W - 8 + e]);
             }
             const float tmax = max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]),
-                                    fmaxf(pm[6], pm[7])) * cs;
+                                    fmaxf(pm[6], pm[7])) * scale_log2;
             const bool grow = tmax > m + kPgGrow;
-            if (__any_sync(0xffffffffu, grow)) {
+            if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
                 float factor = 1.f;
                 if (grow) {
                     factor = exp2f(m - tmax);  // 0 on the first tile
                     m = tmax;
                 }
                 l *= factor;
-                if (j >= 1) {
+                if (!first_tile) {
                     // O is rescaled once P.V of the tile before is done
                     if (!warp_wait(bars + 8 * kBarO, (it - 1) & 1)) return {m, l, false};
                     tc_fence_after();
@@ -512,9 +632,9 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
             }
             // the weights, rounded to the storage type; their sum is taken before that (rounding
             // to nearest leaves no bias)
-            if (j >= 1) p_free = mbar_done(bars + 8 * kBarO, (it - 1) & 1);
+            if (!first_tile) p_free = mbar_done(bars + 8 * kBarO, (it - 1) & 1);
             const float nref = m == -INFINITY ? 0.f : -m;
-            const Pair cs2(cs, cs), ref2(nref, nref);
+            const Pair cs2(scale_log2, scale_log2), ref2(nref, nref);
             Pair sum[4] = {Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f)};
 #pragma unroll
             for (int i = 0; i < W / 2; ++i) {
@@ -527,23 +647,23 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
             l += all.x + all.y;
         }
         // the weights' last reader is P.V of the tile before
-        if (j >= 1 && !warp_wait(bars + 8 * kBarO, (it - 1) & 1, p_free)) return {m, l, false};
+        if (!first_tile && !warp_wait(bars + 8 * kBarO, (it - 1) & 1, p_free)) return {m, l, false};
         tc_fence_after();
-        s_done = j + 1 < n && mbar_done(bars + 8 * kBarS, (it + 1) & 1);
+        s_done = it + 1 != end && mbar_done(bars + 8 * kBarS, (it + 1) & 1);
         if constexpr (W == 128) {
             tc_st32_u(t_p, w);
             tc_st32_u(t_p + 32, w + 32);
         } else {
             tc_st16_u(t_p + base / 2, w);
         }
-        const int first = kvend - (v0 + j) * kStep;
-        if (first < kStep) {
+        const int first = kvend - (t0 - base);
+        if (__builtin_expect(first < kStep, 0)) {
             // Positions past the last visible one hold other data (or nothing): P is 0 there, but
             // 0 * NaN would still poison P.V, so those V rows are cleared once the copy landed.
             const uint32_t slot = it % kSlotsV;
             if (!warp_wait(bars + 8 * (kBarFullV + slot), (it / kSlotsV) & 1))
                 return {m, l, false};
-            const uint32_t vt = sv + slot * kStepBytes;
+            const uint32_t vt = bars - kPgQBytes - (kSlotsV - slot) * kStepBytes;
             for (int x = tid; x < (kStep - first) * 8; x += kRowThreads)
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
                                  vt + swz(first + (x >> 3), x & 7)),
@@ -554,6 +674,13 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
         tc_fence_before();
         warp_arrive(bars + 8 * kBarP);
     }
+    if (scan >= 0) {
+        if (!warp_wait(bars + 8 * kBarO, (end - 1) & 1) || !warp_wait(bars + 8 * kBarScan, scan))
+            return {m, l, false};
+        tc_fence_after();
+        const uint32_t odd = bars + kOddOffset;
+        if (lds_s32(odd + 4 * kOddWords)) repair(t_o, odd, lim, base, W);
+    }
     return {m, l, true};
 }
 
@@ -563,6 +690,16 @@ __device__ __forceinline__ T* out_row(const PagedParams& p, const Walk& u, int r
     const int tok = r / p.group, hg = r - tok * p.group;
     const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
     return static_cast<T*>(p.out) + (t * p.n_q_heads + u.h * p.group + hg) * kHeadDim;
+}
+// 0 * x of eight values.
+template <typename T>
+__device__ __forceinline__ uint4 times_zero(const uint4& x) {
+    float f[8];
+    unpack8<T>(x, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= 0.f;
+    return make_uint4(Half16<T>::from_f2(f[0], f[1]), Half16<T>::from_f2(f[2], f[3]),
+                      Half16<T>::from_f2(f[4], f[5]), Half16<T>::from_f2(f[6], f[7]));
 }
 template <typename T>
 __device__ __forceinline__ uint2 pack4(const float4& o, float inv) {
@@ -816,17 +953,11 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                       const __grid_constant__ CUtensorMap tmv,
                       const PagedParams p) {
     extern __shared__ uint8_t smem_raw[];
-    Smem sm;
-    sm.k = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                      ~uintptr_t(1023));
-    sm.v = sm.k + kSlotsK * kStepBytes;
-    sm.q = sm.v + kSlotsV * kStepBytes;
-    sm.bars = reinterpret_cast<uint64_t*>(sm.q + kPgQBytes);
-    sm.ml = reinterpret_cast<float2*>(sm.q + kPgQBytes + 256);
-    sm.part = reinterpret_cast<float4*>(sm.ml + kPgRows);
+    const Smem sm = smem_at(smem_base(smem_raw));
     static_assert(kBarCount * 8 <= 256, "the barriers' place");
     __shared__ Place s_place;
     __shared__ uint32_t s_total, s_from, s_to, s_tmem;
+    __shared__ uint32_t s_walk[kRowThreads / 32][sizeof(Walk) / 4];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool mma_warp = warp == kRowThreads / 32, copy_warp = warp == kRowThreads / 32 + 1;
@@ -844,7 +975,10 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     __syncthreads();
     if (warp == 0) {
         const uint32_t total = finish_table(tab);
-        if (lane == 0) s_total = total;
+        if (lane == 0) {
+            s_total = total == kTooLong ? 0 : total;
+            if (total == kTooLong && blockIdx.x == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+        }
     } else if (mma_warp) {
         tc_alloc(smem_u32(&s_tmem), kPgCols);
         tc_relinquish();
@@ -952,18 +1086,32 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             return true;
         };
         uint32_t it = 0, units = 0;
+        bool odd = true;  // (at first: what the table holds is not known)
         do {
             if (!(ok = warp_wait(sm.bar(kBarQ), units & 1))) break;
             tc_fence_after();
+            // (the rows are done with the last unit's)
+            const bool hides = u.hides(p);
+            const int hidden = u.hidden(p);
+            if (hides && odd) {
+                for (int i = lane; i < kOddWords; i += 32) sm.odd[i] = INT_MAX;
+                __syncwarp();
+                odd = false;
+            }
             const int nt = u.v1 - u.v0;
             ok = issue_s(it);
-            for (int j = 0; ok && j < nt; ++j, ++it) {
+            auto tile = [&](int j, bool scan) {
                 // the next scores as soon as the rows have read these, while they form the weights
-                if (!(ok = warp_wait(sm.bar(kBarRead), it & 1))) break;
-                if (j + 1 < nt && !(ok = issue_s(it + 1))) break;
+                if (!warp_wait(sm.bar(kBarRead), it & 1)) return false;
+                if (j + 1 < nt && !issue_s(it + 1)) return false;
                 const uint32_t slot = it % kSlotsV;
-                if (!(ok = warp_wait(sm.bar(kBarFullV + slot), (it / kSlotsV) & 1))) break;
-                if (!(ok = warp_wait(sm.bar(kBarP), it & 1))) break;
+                if (!warp_wait(sm.bar(kBarFullV + slot), (it / kSlotsV) & 1)) return false;
+                if (scan) {
+                    const int base = (u.v0 + j) * kStep;
+                    odd |= scan_hidden<T>(smem_u32(sm.v) + slot * kStepBytes, base,
+                                          max(hidden, base), min(u.kvend, base + kStep), sm.odd);
+                }
+                if (!warp_wait(sm.bar(kBarP), it & 1)) return false;
                 tc_fence_after();
                 const uint64_t vd = vdesc + slot * kStepDesc;
                 tc_mma_f16_tmem_a_if(lead, tmem + kPgColsO, tmem + kPgColsP, vd, kIdO, j > 0);
@@ -973,8 +1121,19 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                                          vd + kk * (16 * kRowBytes / 16), kIdO, 1);
                 tc_commit_if(lead, sm.bar(kBarO));
                 tc_commit_if(lead, sm.bar(kBarFreeV + slot));
-            }
+                ++it;
+                return true;
+            };
+            const int seen = hides ? max(hidden / kStep - u.v0, 0) : nt;  // tiles that all see
+            int j = 0;
+            for (; ok && j < seen; ++j) ok = tile(j, false);
+#pragma unroll 1
+            for (; ok && j < nt; ++j) ok = tile(j, true);
             ++units;
+            if (ok && hides) {
+                if (lane == 0) sm.odd[kOddWords] = odd;
+                warp_arrive(sm.bar(kBarScan));
+            }
         } while (ok && u.next(p));
         if (!ok) {
             if (lead) {
@@ -986,60 +1145,72 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
         }
     } else {
         // ---- the rows ----
-        uint32_t it0 = 0;
-        uint4 qv[8];
+        uint32_t it0 = 0, scans = 0;
         auto rep_of = [](int live) { return MANY ? copies_of(live) : 4; };
-        // this thread's query row (zeros past the unit's)
-        auto load_q = [&](const Walk& u) {
-            const int r = tid & (kPgRows / rep_of(u.live) - 1);
+        auto walk = [&]() { return s_walk[row_thread() / 32]; };
+        // this thread's query row (zeros past the unit's) into the swizzled A operand
+        auto stage_q = [&](const Walk& u) {
+            const Smem sm = smem_at(smem_base(smem_raw));
+            const int r = row_thread() & (kPgRows / rep_of(u.live) - 1);
             const int tok = r / p.group, hg = r - tok * p.group;
             const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
             const uint4* src = reinterpret_cast<const uint4*>(
                 p.q + t * p.q_st + (int64_t)(u.h * p.group + hg) * p.q_sh);
+            uint4 qv[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 qv[c] = r < u.live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-        };
-        // into the swizzled A operand
-        auto stage_q = [&]() {
+            // (the loop over the tiles knows positive scales only)
+            const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(sm.q + swz(tid, c)) = qv[c];
+            for (int c = 0; c < 8; ++c) {
+                uint4 v = make_uint4(qv[c].x ^ flip, qv[c].y ^ flip, qv[c].z ^ flip, qv[c].w ^ flip);
+                if (p.scale_sign == 0) v = times_zero<T>(v);
+                *reinterpret_cast<uint4*>(sm.q + swz(row_thread(), c)) = v;
+            }
             fence_proxy_async();
             warp_arrive(sm.bar(kBarQ));
         };
-        load_q(u);
-        stage_q();
-        for (bool more = true; more;) {
-            const int rep = rep_of(u.live), r = tid & (kPgRows / rep - 1);
+        // the tiles of the unit that is put away
+        auto weigh = [&]() {
+            const Walk u = take_back<Walk>(walk());
+            const uint32_t bars = smem_at(smem_base(smem_raw)).bar(0), end = it0 + u.v1 - u.v0;
+            const int rep = rep_of(u.live), r = row_thread() & (kPgRows / rep - 1);
             // keys t < lim are visible; rows past the unit's see all of it (and are not written)
-            const int lim =
-                r < u.live ? u.s.s0() + u.mb * p.tq + r / p.group + 1 : u.kvend;
-            const int nt = u.v1 - u.v0;
-            auto run = [&](auto copies) {
-                return run_rows<T, decltype(copies)::value>(p.scale_log2, sm.bar(0),
-                                                            smem_u32(sm.v), tmem, u.v0, nt,
-                                                            u.kvend, it0, lim);
-            };
-            RowsEnd e;
-            if (MANY && rep == 1) e = run(std::integral_constant<int, 1>{});
-            else e = run(std::integral_constant<int, 4>{});
-            const Walk done = u;
+            const int lim = r < u.live ? u.s.s0() + u.mb * p.tq + r / p.group + 1 : u.kvend;
+            const int scan = u.hides(p) ? (int)(scans & 1) : -1;
+            if (MANY && rep == 1)
+                return run_rows<T, 1>(p.scale_log2, bars, tmem, u.v0, it0, end, u.kvend, lim, scan);
+            return run_rows<T, 4>(p.scale_log2, bars, tmem, u.v0, it0, end, u.kvend, lim, scan);
+        };
+        put_away(walk(), u);
+        stage_q(u);
+        for (bool more = true; more;) {
+            const RowsEnd e = weigh();
+            const Walk done = take_back<Walk>(walk());
+            u = done;
             more = u.next(p);
-            if (more) load_q(u);  // on their way while this unit ends
-            it0 += nt;
+            put_away(walk(), u);
+            const Smem sm = smem_at(smem_base(smem_raw));
+            it0 += done.v1 - done.v0;
+            scans += done.hides(p);
             ok = e.ok && mbar_wait_bounded(sm.bar(kBarO), (it0 - 1) & 1);
             if (rows_any(!ok)) {
-                if (tid == 0) flag_error(p.dev_err, KVD_ERR_TIMEOUT);
+                if (row_thread() == 0) flag_error(p.dev_err, KVD_ERR_TIMEOUT);
                 break;
             }
             tc_fence_after();
             const bool whole = done.v0 == 0 && done.v1 == done.tiles;
             const int slot = 2 * (int)blockIdx.x + (done.v0 == 0);
-            if (MANY && rep == 1) finish_rows<T, 1>(p, sm, tmem, done, whole, slot, e.m, e.l);
-            else finish_rows<T, 4>(p, sm, tmem, done, whole, slot, e.m, e.l);
+            if (MANY && rep_of(done.live) == 1)
+                finish_rows<T, 1>(p, sm, tmem, done, whole, slot, e.m, e.l);
+            else
+                finish_rows<T, 4>(p, sm, tmem, done, whole, slot, e.m, e.l);
             tc_fence_before();  // O is read before the next unit's products
-            if (more) stage_q();
+            // (loaded here and not before the unit's end: rows in flight over it would be spilled)
+            if (more) stage_q(take_back<Walk>(walk()));
             if (!whole) {
+                const Shares sh = shares(s_total);
                 // (the last share that starts before the unit's first cut, and before its last)
                 const uint32_t i0 = sh.holder(done.u0 + keep_lo(done.w) - 1);
                 const uint32_t i1 = sh.holder(done.u0 + keep_hi(done.w) - 1);
@@ -1124,7 +1295,7 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     // the list of tiles, at its longest, is counted in 32 bits
     const int tq = kPgRows / group;
     const double blocks = (double)cache->n_kv_heads * ((double)n_tokens / tq + cache->batch);
-    const double longest = kHeavy * ((double)cache->table_width * cache->page_size / kStep + 1.);
+    const double longest = kWeight * ((double)cache->table_width * cache->page_size / kStep + 1.);
     if (blocks * (longest + kUnit) > 4e9) return KVD_ERR_UNSUPPORTED;
     CUtensorMap mk, mv;
     if (kvd_status s = encode_pool_map(&mk, dtype, cache->k, cache)) return s;
@@ -1150,7 +1321,9 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     while ((1 << p.page_log2) < cache->page_size) ++p.page_log2;
     p.box_rows = std::min(kTile, cache->page_size);
     p.boxes = kStep / p.box_rows;
-    p.scale_log2 = scale * kLog2e;
+    const float scale_log2 = scale * kLog2e;
+    p.scale_sign = (scale_log2 > 0.f) - (scale_log2 < 0.f);
+    p.scale_log2 = p.scale_sign ? std::fabs(scale_log2) : 1.f;
     p.slot_rows = unit_rows(group, max_new);
     p.dev_err = dev_err;
     p.test_stall = (flags & KVD_FLAG_TEST_STALL) ? 1 : 0;
