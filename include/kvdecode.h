@@ -681,8 +681,8 @@ kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32
  * first tile of every thread block never completes (the call reports KVD_ERR_TIMEOUT).
  * Device errors: lens[b] outside [n_b, capacity] or n_b > max_new -> KVD_ERR_LEN_OVERFLOW, the
  * row's outputs are left as they are (all rows' where overlapping stretches of `starts` make more
- * tiles than 32 bits count); KVD_ERR_TIMEOUT as in kvd_decode_attn; a page outside [0, n_pages) -> KVD_ERR_BAD_INDEX, its
- * positions count as rows of zeros. KVD_ERR_UNSUPPORTED: more tiles than 32 bits count, with rows
+ * tiles than 32 bits count); KVD_ERR_TIMEOUT: a bounded wait gave up; a page outside [0, n_pages)
+ * -> KVD_ERR_BAD_INDEX, its positions count as rows of zeros. KVD_ERR_UNSUPPORTED: more tiles than 32 bits count, with rows
  * as long as the table allows (n_kv_heads * (n_tokens * n_heads / n_kv_heads / 128 + batch) units
  * of up to page_size * table_width / 128 tiles: above about 8e8).
  */

@@ -232,7 +232,8 @@ extern "C" const char* kvd_status_string(kvd_status s) {
     case KVD_ERR_WORKSPACE: return "KVD_ERR_WORKSPACE: workspace missing or too small";
     case KVD_ERR_CUDA: return "KVD_ERR_CUDA: CUDA call failed";
     case KVD_ERR_LEN_OVERFLOW: return "KVD_ERR_LEN_OVERFLOW: length outside [0, capacity]";
-    case KVD_ERR_BAD_INDEX: return "KVD_ERR_BAD_INDEX: beam parent outside its window, or page outside the pool";
+    case KVD_ERR_BAD_INDEX:
+        return "KVD_ERR_BAD_INDEX: beam parent outside its window, or page outside the pool";
     case KVD_ERR_BAD_TOKEN: return "KVD_ERR_BAD_TOKEN: token id outside the vocabulary";
     case KVD_ERR_NAN: return "KVD_ERR_NAN: NaN in the logits";
     case KVD_ERR_TIMEOUT: return "KVD_ERR_TIMEOUT: a bounded device wait gave up";

@@ -11,6 +11,10 @@
 // at a time, eight lanes a row, so a token's row, page and angles are found once. The row comes
 // from a search over `starts`, 32 probes a step; rows, lengths and pages that do not fit are
 // flagged and skipped.
+//
+// Measured (in a graph): 64 tokens x 40 heads 3.5 us, a launch and four loads that need one
+// another (row, length, page, rows); 6 rows of up to 2000 tokens x 28 heads 16.7 us, 3.9 TB/s of
+// what is read and written: one wave of warps, so the loads and the stores hardly overlap.
 #include <algorithm>
 
 #include "kvd_paged.cuh"
@@ -51,7 +55,10 @@ kvd_status validate_token_rows(const kvd_token_rows* r) {
 namespace {
 
 constexpr int kPaThreads = 128;
-constexpr int64_t kPaManyWarps = 152 * 16;  // warps a launch should have before a warp takes more
+// Warps that a launch should have before a warp takes more heads (64 tokens x 40 heads: 4.4 us at 1
+// per SM, 3.5 from 4 on; 6 x 2000 tokens x 28 heads: 16.6 us at 1 to 64 per SM, a warp per four
+// heads and token 36.4).
+constexpr int64_t kPaManyWarps = 152 * 16;
 constexpr int kPaAhead = 4;                 // groups of four heads whose loads are in flight
 
 struct PagedAppendParams {

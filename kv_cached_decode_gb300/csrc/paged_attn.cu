@@ -4,27 +4,41 @@
 // block of drafts and run a chunk of their prompt. Row b has n new tokens, the last n of len
 // positions; query head hq of token j sees position t <= len - n + j of KV head hq / g:
 //   out[j, hq] = sum_t softmax_t(scale * q[j, hq] . K_t) V_t
+// One pass over the tiles with a running reference m and sum l per query: p_t = 2^(s_t - m),
+// O += p V, l += p; m moves only when a row's maximum exceeds it by more than 2^8 (O and l are then
+// scaled).
 //
 // Design.
 //  * A unit is one row, KV head and block of up to 128 query vectors: 128 / g tokens times the g
 //    query heads that share the KV head, so K and V are read once for all of them. Its products
-//    run on the fifth-generation tensor cores as in prefill.cu: S = Q.K^T (M 128, N 64, K 64) and
-//    O += P.V, accumulators and P in tensor memory, Q, K, V in 128-byte-swizzled shared memory.
-//  * Six warps: four hold the rows (thread t: tensor-memory lane t), one issues the MMAs, one
-//    copies K/V tiles of 64 positions through a ring of slots. Pages of fewer than 64 positions
-//    are one TMA box each, a lane of the copying warp per page; its page numbers are read a tile
-//    ahead. Boxes from the unit's last visible position on are not read.
-//  * Units of at most 32 (64) vectors hold them four (two) times, in lanes 32 (64) apart, and each
-//    copy takes the softmax of a quarter (half) of a tile's positions, with P zero elsewhere: a
-//    decoding sequence, with 4 query vectors, uses all four warps. The copies are merged at the
-//    unit's end. The products cost the same: 256 of the about 700 cycles that a tile takes to
-//    arrive at HBM's rate.
+//    run on the fifth-generation tensor cores: S = Q.K^T (M 128, N 128, K 64) and O += P.V
+//    (M 128, N 64, K 128); scores, outputs and P (as the A operand) in tensor memory, Q, K and V in
+//    128-byte-swizzled shared memory. Tiles are 128 positions: with 64, and so twice the hand-offs
+//    between the roles, a chunk of 512 tokens over 16384 took 104 us instead of 98.
+//  * Six warps: four hold the rows (thread t: tensor-memory lane t), one issues the products, one
+//    copies K and V through two and three slots. A page that holds less than a tile is a TMA box of
+//    its own, a lane of the copying warp per page; page numbers are read a tile ahead. Boxes from
+//    the unit's last visible position on are not read. The scores of the next tile are issued as
+//    soon as these are in registers. Two blocks per SM: while one waits, the other computes.
+//  * Units of at most 32 vectors hold them four times, in lanes 32 apart, and each copy takes the
+//    softmax of a quarter of a tile's positions, with P zero elsewhere: a decoding sequence, with 4
+//    query vectors, uses all four warps. The copies are joined at the unit's end. (One row of 8192:
+//    14.1 us against 14.4 with the vectors held once; 8 rows of 5 tokens: 33.4 against 35.2.)
 //  * Work. The tiles of all units form one list, by weight, and every CTA of one wave takes an
 //    equal stretch of it; units cut by a stretch's end merge through the workspace, the last CTA
 //    to arrive in the order of the list. So neither one long row nor few rows leave SMs idle, and
 //    the tiles of decoding rows (HBM) and of prompt chunks (softmax) run at the same time. The
-//    copying warp runs ahead into the CTA's next unit.
-//  * A softmax row's reference moves only when its maximum grows by more than 2^8.
+//    copying warp runs ahead into the CTA's next unit. The list is not made by the host, as lengths
+//    lie on the device: every CTA sums the rows' weights (64 rows: about 2 us).
+//
+// Measured (in a graph, caches warm where they fit; a copy runs at 6.8 TB/s, a large product at
+// 1928 TFLOP/s):
+//   1 row x 8192 positions, 32/8 heads         13.7 us   the launch, the list and the merge
+//   32 rows to 16384, 32/8 heads                125 us   6.4 TB/s
+//   8 rows x 5 tokens over up to 8192            33 us   3.8 TB/s
+//   a chunk of 512 over 16384, 32/8 heads        73 us   934 TFLOP/s: the four row warps' chain of
+//                                                        loads, maxima and exponentials, twice per SM
+//   30 rows, two with chunks of 1000 at 8000    101 us   the same
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -52,7 +66,9 @@ constexpr uint32_t kPgCols = 256;
 static_assert(kPgCols >= kPgColsP + kStep / 2 && kPgMinBlocks * kPgCols <= 512,
               "the resident blocks' tensor memory");
 constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
-constexpr int kFewPieces = 6;                  // of a merge with a thread per row
+// Pieces of a merge with a thread per row (a chunk of 512 over 16384, three pieces per unit of 128
+// rows: 73 us; with a thread per 4 dims of a row, as for more pieces or fewer rows, 100).
+constexpr int kFewPieces = 6;
 constexpr uint32_t kOddOffset = 256 + kPgRows * 8 + kRowThreads * 16;  // behind the barriers
 constexpr int kOddWords = 3 * kHeadDim;        // see scan_hidden
 // shared memory: K slots | V slots | Q | barriers | rows' references and sums | merge | odd
@@ -61,10 +77,13 @@ constexpr uint32_t kPgSmem = (kSlotsK + kSlotsV) * kStepBytes + kPgQBytes + 256 
 constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
 
-// The list's weights: of a tile, and what a unit costs besides.
+// The list's weights: of a tile, and what a unit costs besides (its start, end and merge). Measured
+// on one row of 8192 positions (64 tiles x 8 heads) and on a mixed batch: a unit as 3, 4, 5 and 6
+// tiles 15.4, 13.6, 15.3, 15.3 us and 101.9, 101.5, 102.3, 103.3; tiles of few vectors lighter by
+// 1/6 than the others 14.2 and 104.2, heavier by 1/5 15.3 and 105.3.
 constexpr uint32_t kWeight = 5, kUnit = 20;
-constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
-constexpr uint32_t kLeast = 20;     // a CTA's least share
+constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends (20: 17.3 us; 5: no change)
+constexpr uint32_t kLeast = 20;     // a CTA's least share (15: 15.7 us, 25: 15.1, 30: 16.7)
 constexpr int kMaxCtas = 512;
 
 struct PagedParams {
@@ -103,7 +122,8 @@ __device__ __forceinline__ Row row_of(const PagedParams& p, int b, bool& bad) {
     return r;
 }
 
-// sum_{i < n} floor((a i + b) / 128), by the Euclidean recursion on (a, 128). The sum is below 2^32.
+// sum_{i < n} floor((a i + b) / 128), by the Euclidean recursion on (a, 128). The sum is below
+// 2^32.
 __device__ __forceinline__ uint32_t floor_sum(uint32_t n, uint32_t a, uint32_t b) {
     auto pairs = [](uint32_t n) { return (uint32_t)((uint64_t)n * (n - 1) / 2); };
     // (the first step by hand: divisions by a constant)
@@ -401,8 +421,8 @@ __device__ __forceinline__ bool rows_any(bool x) {
         : "memory");
     return r != 0;
 }
-// Whether phase `parity` of the barrier is complete, without waiting. Asked for ahead of the use: an
-// answer takes about a hundred cycles.
+// Whether phase `parity` of the barrier is complete, without waiting. Asked for ahead of the use:
+// an answer takes about a hundred cycles.
 __device__ __forceinline__ bool mbar_done(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -481,8 +501,8 @@ __device__ __forceinline__ int row_thread() {
 // ------------------------------------------------- infinities and NaN behind the mask --
 // Positions that only some tokens of a unit see have weight 0 for the others, and 0 * inf is NaN.
 // So what is not finite in those rows of V is taken out before the product, and noted: the first
-// position of each dim with +inf, -inf and NaN. It is added to the outputs of the tokens that see it
-// (repair). One warp, behind the copy of the tile at `base` and before the product that reads it;
+// position of each dim with +inf, -inf and NaN. It is added to the outputs of the tokens that see
+// it (repair). One warp, behind the copy of the tile at `base` and before the product that reads it;
 // positions lo .. hi - 1. Returns whether there was any.
 template <typename T>
 __device__ __forceinline__ bool scan_hidden(uint32_t tile, int base, int lo, int hi, int32_t* odd) {
@@ -561,7 +581,7 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
     static_assert(REP == 1 || REP == 4, "W is 128 or 32");
     constexpr int W = kStep / REP;
     const int tid = threadIdx.x;
-    const int base = REP == 1 ? 0 : tid / (kPgRows / REP) * W;  // of this copy's positions in a tile
+    const int base = REP == 1 ? 0 : tid / (kPgRows / REP) * W;  // of the copy's positions in a tile
     const uint32_t lanes = tmem + ((uint32_t)(tid & ~31) << 16);
     const uint32_t t_s = lanes + base, t_o = lanes + kPgColsO, t_p = lanes + kPgColsP;
     bool first_tile = true;
@@ -840,8 +860,8 @@ struct Joined {
 };
 
 // A cut unit's pieces, which lie in the workspace: CTAs i0 .. i0 + n - 1, the last to arrive merges
-// them in that order. MANY: units of more than 32 rows are among the call's.
-template <typename T, bool MANY>
+// them in that order.
+template <typename T>
 __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& sm, const Walk& u,
                                              int i0, int n, int* s_last) {
     const int tid = threadIdx.x;
@@ -863,7 +883,7 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
     auto part_of = [&](int i, int c, int r) {
         return __ldcg(p.ws_part + (slot(i) * 16 + c) * p.slot_rows + r);
     };
-    if (MANY && u.live > 32 && n <= kFewPieces) {
+    if (u.live > 32 && n <= kFewPieces) {
         // many rows, few pieces: a thread per row
         if (tid < u.live) {
             float2 ml[kFewPieces];
@@ -902,7 +922,7 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
         return;
     }
     // a thread per row, 4 dims and, of few rows, share of the pieces; the shares joined in order
-    constexpr int kBatch = MANY ? 8 : 12;  // pieces whose loads are in flight
+    constexpr int kBatch = 8;  // pieces whose loads are in flight
     const int items = u.live * 16, shares = max(1, kRowThreads / items);
     auto store = [&](int y, const Joined& a) {
         *reinterpret_cast<uint2*>(out_row<T>(p, u, y >> 4) + (y & 15) * 4) =
@@ -946,8 +966,7 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
     }
 }
 
-// MANY: units of more than 32 query vectors are among the call's.
-template <typename T, bool MANY>
+template <typename T>
 __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv,
@@ -1146,12 +1165,11 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     } else {
         // ---- the rows ----
         uint32_t it0 = 0, scans = 0;
-        auto rep_of = [](int live) { return MANY ? copies_of(live) : 4; };
         auto walk = [&]() { return s_walk[row_thread() / 32]; };
         // this thread's query row (zeros past the unit's) into the swizzled A operand
         auto stage_q = [&](const Walk& u) {
             const Smem sm = smem_at(smem_base(smem_raw));
-            const int r = row_thread() & (kPgRows / rep_of(u.live) - 1);
+            const int r = row_thread() & (kPgRows / copies_of(u.live) - 1);
             const int tok = r / p.group, hg = r - tok * p.group;
             const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
             const uint4* src = reinterpret_cast<const uint4*>(
@@ -1164,7 +1182,8 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                uint4 v = make_uint4(qv[c].x ^ flip, qv[c].y ^ flip, qv[c].z ^ flip, qv[c].w ^ flip);
+                uint4 v = qv[c];
+                v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
                 if (p.scale_sign == 0) v = times_zero<T>(v);
                 *reinterpret_cast<uint4*>(sm.q + swz(row_thread(), c)) = v;
             }
@@ -1175,11 +1194,11 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
         auto weigh = [&]() {
             const Walk u = take_back<Walk>(walk());
             const uint32_t bars = smem_at(smem_base(smem_raw)).bar(0), end = it0 + u.v1 - u.v0;
-            const int rep = rep_of(u.live), r = row_thread() & (kPgRows / rep - 1);
+            const int rep = copies_of(u.live), r = row_thread() & (kPgRows / rep - 1);
             // keys t < lim are visible; rows past the unit's see all of it (and are not written)
             const int lim = r < u.live ? u.s.s0() + u.mb * p.tq + r / p.group + 1 : u.kvend;
             const int scan = u.hides(p) ? (int)(scans & 1) : -1;
-            if (MANY && rep == 1)
+            if (rep == 1)
                 return run_rows<T, 1>(p.scale_log2, bars, tmem, u.v0, it0, end, u.kvend, lim, scan);
             return run_rows<T, 4>(p.scale_log2, bars, tmem, u.v0, it0, end, u.kvend, lim, scan);
         };
@@ -1202,7 +1221,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             tc_fence_after();
             const bool whole = done.v0 == 0 && done.v1 == done.tiles;
             const int slot = 2 * (int)blockIdx.x + (done.v0 == 0);
-            if (MANY && rep_of(done.live) == 1)
+            if (copies_of(done.live) == 1)
                 finish_rows<T, 1>(p, sm, tmem, done, whole, slot, e.m, e.l);
             else
                 finish_rows<T, 4>(p, sm, tmem, done, whole, slot, e.m, e.l);
@@ -1214,7 +1233,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                 // (the last share that starts before the unit's first cut, and before its last)
                 const uint32_t i0 = sh.holder(done.u0 + keep_lo(done.w) - 1);
                 const uint32_t i1 = sh.holder(done.u0 + keep_hi(done.w) - 1);
-                merge_pieces<T, MANY>(p, sm, done, (int)i0, (int)(i1 - i0) + 1, &s_last);
+                merge_pieces<T>(p, sm, done, (int)i0, (int)(i1 - i0) + 1, &s_last);
             }
         }
     }
@@ -1229,14 +1248,14 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
 constexpr int kMaxDevP = 64;
 
 // Once per kernel and device: its shared memory.
-template <typename T, bool MANY>
+template <typename T>
 bool prepare_paged() {
     static std::once_flag once[kMaxDevP];
     static bool ok[kMaxDevP];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevP) return false;
     std::call_once(once[dev], [dev] {
-        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T, MANY>,
+        ok[dev] = cudaFuncSetAttribute(paged_attn_kernel<T>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kPgSmem) == cudaSuccess;
         cudaGetLastError();
@@ -1244,15 +1263,15 @@ bool prepare_paged() {
     return ok[dev];
 }
 
-template <typename T, bool MANY>
+template <typename T>
 kvd_status run_paged(PagedParams& p, int nsm, const CUtensorMap& mk, const CUtensorMap& mv,
                      uint8_t* ws, bool pdl, cudaStream_t st) {
-    if (!prepare_paged<T, MANY>()) return KVD_ERR_CUDA;
+    if (!prepare_paged<T>()) return KVD_ERR_CUDA;
     const int blocks = std::min(kMaxCtas, nsm * kPgMinBlocks);
     p.ws_cnt = reinterpret_cast<int32_t*>(ws);
     p.ws_part = reinterpret_cast<float4*>(ws + KVD_WS_COUNTER_BYTES);
     p.ws_ml = reinterpret_cast<float2*>(p.ws_part + (size_t)2 * blocks * 16 * p.slot_rows);
-    return launch(paged_attn_kernel<T, MANY>, dim3((unsigned)blocks), dim3(kPgThreads), kPgSmem, st,
+    return launch(paged_attn_kernel<T>, dim3((unsigned)blocks), dim3(kPgThreads), kPgSmem, st,
                   pdl, mk, mv, p);
 }
 
@@ -1264,8 +1283,8 @@ int unit_rows(int group, int max_new) {
 }  // namespace
 
 size_t paged_workspace_bytes(int n_q_heads, int n_kv_heads, int max_new) {
-    return KVD_WS_COUNTER_BYTES + (size_t)2 * kMaxCtas * unit_rows(n_q_heads / n_kv_heads, max_new) *
-                                      (kHeadDim + 2) * sizeof(float);
+    return KVD_WS_COUNTER_BYTES + (size_t)2 * kMaxCtas * (kHeadDim + 2) * sizeof(float) *
+                                      unit_rows(n_q_heads / n_kv_heads, max_new);
 }
 
 }  // namespace kvd
@@ -1330,9 +1349,6 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     const bool pdl = (flags & (KVD_FLAG_PDL | KVD_FLAG_EARLY_KV)) != 0;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    if (p.slot_rows > 32)
-        return dtype == KVD_BF16 ? run_paged<__nv_bfloat16, true>(p, nsm, mk, mv, ws, pdl, st)
-                                 : run_paged<__half, true>(p, nsm, mk, mv, ws, pdl, st);
-    return dtype == KVD_BF16 ? run_paged<__nv_bfloat16, false>(p, nsm, mk, mv, ws, pdl, st)
-                             : run_paged<__half, false>(p, nsm, mk, mv, ws, pdl, st);
+    return dtype == KVD_BF16 ? run_paged<__nv_bfloat16>(p, nsm, mk, mv, ws, pdl, st)
+                             : run_paged<__half>(p, nsm, mk, mv, ws, pdl, st);
 }

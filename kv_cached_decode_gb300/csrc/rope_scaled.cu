@@ -12,6 +12,9 @@
 // A warp takes the heads of one token, four at a time, so that cos and sin are formed once per
 // token and lane; several groups of heads are in flight, and the next is loaded as soon as one is
 // stored. A launch with few tokens spreads a token's heads over several warps.
+//
+// Measured (in a graph): 16 tokens x 24 heads 2.5 us, a launch's time; 4 x 4096 tokens x 24 heads
+// 18.7 us, 5.4 TB/s of what is read and written (a copy: 6.8).
 #include <cmath>
 #include <cstring>
 
@@ -21,7 +24,9 @@ namespace kvd {
 namespace {
 
 constexpr int kRsThreads = 128;
-constexpr int64_t kRsManyWarps = 152 * 16;  // warps a launch should have before a warp takes more
+// Warps that a launch should have before a warp takes more heads (4 x 4096 tokens x 24 heads: 18.7
+// us at 1 to 64 per SM; a warp per four heads and token 35.6).
+constexpr int64_t kRsManyWarps = 152 * 16;
 constexpr int kRsAhead = 4;                 // groups of four heads whose loads are in flight
 
 struct RopeScaledParams {
@@ -141,7 +146,9 @@ kvd_status rope_turns(const kvd_rope_spec* s, RopeTurns* t) {
     double lo = 0., hi = 0.;
     if (s->scaling == KVD_ROPE_RAMP) {
         // the pair that turns r times over the trained length
-        auto pair = [&](double r) { return rot * std::log(len / (two_pi * r)) / (2. * std::log(base)); };
+        auto pair = [&](double r) {
+            return rot * std::log(len / (two_pi * r)) / (2. * std::log(base));
+        };
         lo = std::fmax(std::floor(pair(s->high)), 0.);
         hi = std::fmin(std::ceil(pair(s->low)), rot - 1.);
     }
