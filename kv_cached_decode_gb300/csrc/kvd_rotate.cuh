@@ -17,11 +17,13 @@ namespace kvd {
 // Of the calling lane, for one token.
 struct Turn {
     float c[8], s[8];
+    bool turns;  // whether the lane's dims do
 };
 
 template <bool INTER>
 __device__ __forceinline__ void make_turn(Turn& t, uint64_t freq, int64_t pos, int rot, float mag) {
     const int lane = threadIdx.x & 31, ch = lane & 7;
+    t.turns = 8 * ch < rot;
     float sn, cs;
     // half turns in [-1, 1)
     sincospif((float)(int32_t)((uint64_t)pos * freq >> 32) * 0x1p-31f, &sn, &cs);
@@ -52,16 +54,18 @@ __device__ __forceinline__ uint4 rotate_chunk(const uint4& x, const Turn& t, int
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const float2 a = Half16<T>::to_f2(in[w]);
-        float2 b;
+        float2 y;
         if (INTER) {
-            b = make_float2(a.y, a.x);
+            y = make_float2(fmaf(a.x, t.c[2 * w], a.y * t.s[2 * w]),
+                            fmaf(a.y, t.c[2 * w + 1], a.x * t.s[2 * w + 1]));
         } else {
-            b = Half16<T>::to_f2(__shfl_sync(0xffffffffu, in[w], from));
+            const float2 b = Half16<T>::to_f2(__shfl_sync(0xffffffffu, in[w], from));
+            const Pair p = mul2(Pair(b.x, b.y), Pair(t.s[2 * w], t.s[2 * w + 1]));
+            y = fma2(Pair(a.x, a.y), Pair(t.c[2 * w], t.c[2 * w + 1]), p).get();
         }
-        out[w] = Half16<T>::from_f2(fmaf(a.x, t.c[2 * w], b.x * t.s[2 * w]),
-                                    fmaf(a.y, t.c[2 * w + 1], b.y * t.s[2 * w + 1]));
+        out[w] = Half16<T>::from_f2(y.x, y.y);
     }
-    return 8 * ch >= rot ? x : make_uint4(out[0], out[1], out[2], out[3]);
+    return t.turns ? make_uint4(out[0], out[1], out[2], out[3]) : x;
 }
 
 // Host: the scaled frequencies of a spec as fractions of a turn, in units of 2^-64 turns

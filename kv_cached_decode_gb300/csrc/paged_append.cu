@@ -13,7 +13,7 @@
 // flagged and skipped.
 //
 // Measured (in a graph): 64 tokens x 40 heads 3.5 us, a launch and four loads that need one
-// another (row, length, page, rows); 6 rows of up to 2000 tokens x 28 heads 16.7 us, 3.9 TB/s of
+// another (row, length, page, rows); 6 rows of up to 2000 tokens x 28 heads 14.2 us, 4.5 TB/s of
 // what is read and written: one wave of warps, so the loads and the stores hardly overlap.
 #include <algorithm>
 
@@ -56,8 +56,8 @@ namespace {
 
 constexpr int kPaThreads = 128;
 // Warps that a launch should have before a warp takes more heads (64 tokens x 40 heads: 4.4 us at 1
-// per SM, 3.5 from 4 on; 6 x 2000 tokens x 28 heads: 16.6 us at 1 to 64 per SM, a warp per four
-// heads and token 36.4).
+// per SM, 3.5 from 4 on; 6 x 2000 tokens x 28 heads: the same time at 1 to 64 per SM, a warp per
+// four heads and token takes twice as long).
 constexpr int64_t kPaManyWarps = 152 * 16;
 constexpr int kPaAhead = 4;                 // groups of four heads whose loads are in flight
 
@@ -102,22 +102,23 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const PagedApp
     const uint32_t hg = (uint32_t)(wid % p.hgroups);
     const int lane = threadIdx.x & 31, ch = lane & 7;
     if (t < p.n_tokens) {  // warp-uniform
-        const int hk = p.hk, total = 2 * p.hk + p.hq;
-        auto head = [&](uint32_t it) { return (int)(hg * p.iters + it) * 4 + (lane >> 3); };
-        auto load = [&](uint32_t it) {
-            const int h0 = head(it);
-            if (it >= p.iters || h0 >= total) return make_uint4(0u, 0u, 0u, 0u);
-            const bool k = h0 < hk, q = h0 >= 2 * hk;
-            const int h = k ? h0 : q ? h0 - 2 * hk : h0 - hk;
-            const uint8_t* base = k ? p.x[0] : q ? p.x[2] : p.x[1];
-            const int64_t st = k ? p.st[0] : q ? p.st[2] : p.st[1];
-            const int64_t sh = k ? p.sh[0] : q ? p.sh[2] : p.sh[1];
-            return *reinterpret_cast<const uint4*>(base + t * st + h * sh + ch * 16);
+        // this lane's heads are h0, h0 + 4, ..: those of K, of V and of q
+        const int hk = p.hk, h0 = (int)(hg * p.iters) * 4 + (lane >> 3);
+        const int last = min(2 * p.hk + p.hq, (int)((hg + 1) * p.iters) * 4);
+        // the token's rows, as if each tensor's heads were numbered so
+        const uint8_t* xk = p.x[0] + t * p.st[0] + ch * 16;
+        const uint8_t* xv = p.x[1] + t * p.st[1] - hk * p.sh[1] + ch * 16;
+        const uint8_t* xq = p.x[2] + t * p.st[2] - 2 * hk * p.sh[2] + ch * 16;
+        auto load = [&](int h) {
+            if (h >= last) return make_uint4(0u, 0u, 0u, 0u);
+            return *reinterpret_cast<const uint4*>(h < hk       ? xk + h * p.sh[0]
+                                                   : h < 2 * hk ? xv + h * p.sh[1]
+                                                                : xq + h * p.sh[2]);
         };
         // (the rows do not depend on where they go)
         uint4 item[kPaAhead];
 #pragma unroll
-        for (int u = 0; u < kPaAhead; ++u) item[u] = load(u);
+        for (int u = 0; u < kPaAhead; ++u) item[u] = load(h0 + 4 * u);
         const int b = find_token_row(p.starts, p.batch, t);
         int s, n;
         const bool in_row = row_tokens(p.starts, b, p.n_tokens, s, n) && t >= s && t < s + n;
@@ -129,28 +130,28 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const PagedApp
             if (!page_ok && hg == 0 && lane == 0) flag_error(p.dev_err, KVD_ERR_BAD_INDEX);
             const int64_t slot =
                 page * p.sp + (int64_t)(pos & ((1 << p.page_log2) - 1)) * p.ct + ch * 16;
+            uint8_t* yk = p.kc + slot;
+            uint8_t* yv = p.vc + slot - hk * p.ch;
+            uint8_t* yq = p.q_out + ((int64_t)t * p.hq - 2 * hk) * kRowBytes + ch * 16;
             Turn turn;
             if (p.rotate)
                 make_turn<INTER>(turn, s_freq[lane], pos, p.turns.rot, p.turns.mag);
-            for (uint32_t it = 0; it < p.iters; it += kPaAhead) {
+            for (int g = h0; g - (lane >> 3) < last; g += 4 * kPaAhead) {  // (the warp's bound)
 #pragma unroll
                 for (int u = 0; u < kPaAhead; ++u) {
-                    if (it + u >= p.iters) break;
-                    const int h0 = head(it + u);
-                    const bool k = h0 < hk, q = h0 >= 2 * hk;
+                    const int h = g + 4 * u;
+                    if (h - (lane >> 3) >= last) break;
+                    const bool k = h < hk, q = h >= 2 * hk;
                     uint4 v = item[u];
                     if (p.rotate) {
                         const uint4 r = rotate_chunk<T, INTER>(v, turn, p.turns.rot);
                         if (k || q) v = r;
                     }
-                    if (h0 < total && (page_ok || q)) {
-                        uint8_t* dst =
-                            q ? p.q_out +
-                                    ((int64_t)t * p.hq + (h0 - 2 * hk)) * kRowBytes + ch * 16
-                              : (k ? p.kc + h0 * p.ch : p.vc + (h0 - hk) * p.ch) + slot;
-                        *reinterpret_cast<uint4*>(dst) = v;
-                    }
-                    if (it + u + kPaAhead < p.iters) item[u] = load(it + u + kPaAhead);
+                    if (h < last && (page_ok || q))
+                        *reinterpret_cast<uint4*>(q   ? yq + (int64_t)h * kRowBytes
+                                                  : k ? yk + h * p.ch
+                                                      : yv + h * p.ch) = v;
+                    item[u] = load(h + 4 * kPaAhead);
                 }
             }
         }

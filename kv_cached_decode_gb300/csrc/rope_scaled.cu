@@ -14,7 +14,8 @@
 // stored. A launch with few tokens spreads a token's heads over several warps.
 //
 // Measured (in a graph): 16 tokens x 24 heads 2.5 us, a launch's time; 4 x 4096 tokens x 24 heads
-// 18.7 us, 5.4 TB/s of what is read and written (a copy: 6.8).
+// 15.7 us, 6.4 TB/s of what is read and written (a copy: 6.8). Addresses are formed once per token:
+// with all of a row's strides multiplied for each row it was 18.7 us, bound by instructions.
 #include <cmath>
 #include <cstring>
 
@@ -24,8 +25,8 @@ namespace kvd {
 namespace {
 
 constexpr int kRsThreads = 128;
-// Warps that a launch should have before a warp takes more heads (4 x 4096 tokens x 24 heads: 18.7
-// us at 1 to 64 per SM; a warp per four heads and token 35.6).
+// Warps that a launch should have before a warp takes more heads (4 x 4096 tokens x 24 heads: the
+// same time at 1 to 64 per SM; a warp per four heads and token takes twice as long).
 constexpr int64_t kRsManyWarps = 152 * 16;
 constexpr int kRsAhead = 4;                 // groups of four heads whose loads are in flight
 
@@ -51,40 +52,37 @@ __global__ void __launch_bounds__(kRsThreads) rope_scaled_kernel(const RopeScale
     const uint32_t token = wid / p.hgroups, hg = wid % p.hgroups;
     const int b = (int)(token / (uint32_t)p.n), j = (int)(token % (uint32_t)p.n);
     const int lane = threadIdx.x & 31, ch = lane & 7;
-    const int total = p.heads[0] + p.heads[1];
-    auto head = [&](uint32_t it) { return (int64_t)(hg * p.iters + it) * 4 + (lane >> 3); };
-    auto load = [&](uint32_t it) {
-        const int64_t h0 = head(it);
-        if (it >= p.iters || h0 >= total) return make_uint4(0u, 0u, 0u, 0u);
-        const bool k = h0 >= p.heads[0];
-        const int64_t h = k ? h0 - p.heads[0] : h0;
-        return *reinterpret_cast<const uint4*>((k ? p.x[1] : p.x[0]) + b * (k ? p.sb[1] : p.sb[0]) +
-                                               h * (k ? p.sh[1] : p.sh[0]) +
-                                               j * (k ? p.st[1] : p.st[0]) + ch * 16);
+    // this lane's heads are h0, h0 + 4, ..: those of q, then those of k
+    const int h0 = (int)(hg * p.iters) * 4 + (lane >> 3), total = p.heads[0] + p.heads[1];
+    const int last = min(total, (int)((hg + 1) * p.iters) * 4);
+    // the token's rows of q's (k's) first head
+    const uint8_t* xq = p.x[0] + b * p.sb[0] + j * p.st[0] + ch * 16;
+    const uint8_t* xk = p.x[1] + b * p.sb[1] + j * p.st[1] + ch * 16;
+    uint8_t* yq = p.y[0] + ((int64_t)b * p.heads[0] * p.n + j) * kRowBytes + ch * 16;
+    uint8_t* yk = p.y[1] + ((int64_t)b * p.heads[1] * p.n + j) * kRowBytes + ch * 16;
+    const int64_t to_head = (int64_t)p.n * kRowBytes;
+    auto load = [&](int h) {
+        if (h >= last) return make_uint4(0u, 0u, 0u, 0u);
+        const int hk = h - p.heads[0];
+        return *reinterpret_cast<const uint4*>(hk >= 0 ? xk + hk * p.sh[1] : xq + h * p.sh[0]);
     };
     if (token < p.tokens) {  // warp-uniform
         uint4 item[kRsAhead];
 #pragma unroll
-        for (int u = 0; u < kRsAhead; ++u) item[u] = load(u);
+        for (int u = 0; u < kRsAhead; ++u) item[u] = load(h0 + 4 * u);
         const int64_t pos =
             p.positions ? p.positions[token] : (int64_t)(p.pos0 ? p.pos0[b] : 0) + j;
         Turn t;
         make_turn<INTER>(t, s_freq[lane], pos, p.turns.rot, p.turns.mag);
-        for (uint32_t it = 0; it < p.iters; it += kRsAhead) {
+        for (int g = h0; g - (lane >> 3) < last; g += 4 * kRsAhead) {  // (the warp's bound)
 #pragma unroll
             for (int u = 0; u < kRsAhead; ++u) {
-                if (it + u >= p.iters) break;
-                const int64_t h0 = head(it + u);
+                const int h = g + 4 * u, hk = h - p.heads[0];
+                if (h - (lane >> 3) >= last) break;
                 const uint4 v = rotate_chunk<T, INTER>(item[u], t, p.turns.rot);
-                if (h0 < total) {
-                    const bool k = h0 >= p.heads[0];
-                    const int64_t h = k ? h0 - p.heads[0] : h0;
-                    uint8_t* dst = (k ? p.y[1] : p.y[0]) +
-                                   (((int64_t)b * (k ? p.heads[1] : p.heads[0]) + h) * p.n + j) *
-                                       kRowBytes;
-                    *reinterpret_cast<uint4*>(dst + ch * 16) = v;
-                }
-                if (it + u + kRsAhead < p.iters) item[u] = load(it + u + kRsAhead);
+                if (h < last)
+                    *reinterpret_cast<uint4*>(hk >= 0 ? yk + hk * to_head : yq + h * to_head) = v;
+                item[u] = load(h + 4 * kRsAhead);
             }
         }
     }
