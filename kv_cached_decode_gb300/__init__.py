@@ -745,7 +745,27 @@ def make_rope(base: float = 10000.0, rot_dim: int = HEAD_DIM, interleaved: bool 
 def _spec(rope):
     if not isinstance(rope, RopeSpec):
         raise TypeError("rope must be a RopeSpec (make_rope)")
-    return ctypes.byref(rope)
+    return rope
+
+
+def _out_at(out, shape, dtype, what, dev):
+    """As _at, for the output of rows of this shape."""
+    if (out.get_device() != dev or out.dtype != dtype or out.shape != shape
+            or not out.is_contiguous()):
+        _refuse(out, dtype, tuple(shape), what + "_out", dev)
+    return out.data_ptr()
+
+
+def _turned_rows(x, out, dtype, n, what, dev):
+    """Head rows [batch, heads, n, 64] of any strides and where they go."""
+    shape, st = x.shape, x.stride()
+    if (x.dtype != dtype or x.get_device() != dev or len(shape) != 4 or shape[3] != HEAD_DIM
+            or st[3] != 1):
+        return _head_rows(x, out, None, dtype, n, what, dev)  # (which refuses it)
+    B, H = shape[0], shape[1]
+    # (the stride of an axis of size 1 is arbitrary and never used)
+    return HeadRows(x.data_ptr(), st[0] if B > 1 else 0, st[1] if H > 1 else 0,
+                    st[2] if n > 1 else 0, 0, _out_at(out, shape, dtype, what, dev), H)
 
 
 def kvd_rope_scaled(q=None, k=None, q_out=None, k_out=None, rope: RopeSpec = None, pos0=None,
@@ -761,17 +781,20 @@ def kvd_rope_scaled(q=None, k=None, q_out=None, k_out=None, rope: RopeSpec = Non
         raise ValueError("q and k must be [batch, heads, n, 64]")
     dev = _device_of(ref, "q" if q is not None else "k")
     B, _, n, _ = ref.shape
+    dt, rq, rk = ref.dtype, None, None
     if q is not None and k is not None and (k.shape[0] != B or k.shape[2] != n):
         raise ValueError("q and k must share batch and n")
-    if (q is not None and q_out is None) or (k is not None and k_out is None):
-        raise ValueError("q_out (k_out) is needed with q (k)")
-    rq = _head_rows(q, q_out, None, ref.dtype, n, "q", dev)
-    rk = _head_rows(k, k_out, None, ref.dtype, n, "k", dev)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out (k and k_out) go together")
+    if q is not None:
+        rq = _turned_rows(q, q_out, dt, n, "q", dev)
+    if k is not None:
+        rk = _turned_rows(k, k_out, dt, n, "k", dev)
     _check(load_library().kvd_rope_scaled(
-        _dtype_code(ref), B, n, None if rq is None else ctypes.byref(rq),
-        None if rk is None else ctypes.byref(rk), _at(pos0, _I32, (B,), "pos0", dev),
-        _at(positions, _I32, (B, n), "positions", dev), _spec(rope), flags,
-        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_rope_scaled")
+        _dtype_code(ref), B, n, rq, rk, _at(pos0, _I32, (B,), "pos0", dev),
+        0 if positions is None else _at(positions, _I32, (B, n), "positions", dev), _spec(rope),
+        flags, 0 if dev_err is None else _at(dev_err, _I32, None, "dev_err", dev),
+        _on(stream, dev)), "kvd_rope_scaled")
 
 
 def make_paged_cache(k: torch.Tensor, v: torch.Tensor, table: torch.Tensor) -> PagedCache:
@@ -814,7 +837,7 @@ def _token_rows(x, out, dtype, what, dev, heads=None):
                          "contiguous")
     T, H = shape[0], shape[1]
     return TokenRows(x.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0,
-                     _at(out, dtype, tuple(shape), what + "_out", dev), H)
+                     0 if out is None else _out_at(out, shape, dtype, what, dev), H)
 
 
 def kvd_paged_append(cache: PagedCache, k_new, v_new, starts, lens_in, lens_out=None, q=None,
@@ -837,10 +860,10 @@ def kvd_paged_append(cache: PagedCache, k_new, v_new, starts, lens_in, lens_out=
     if starts is None or lens_in is None:
         raise ValueError("starts and lens_in are needed")
     _check(load_library().kvd_paged_append(
-        _dtype_code(k_new), _cache_on(cache, dev, dt), T, ctypes.byref(rk), ctypes.byref(rv),
-        None if rq is None else ctypes.byref(rq), _at(starts, _I32, (B + 1,), "starts", dev),
-        _at(lens_in, _I32, (B,), "lens_in", dev), _at(lens_out, _I32, (B,), "lens_out", dev),
-        None if rope is None else _spec(rope), flags, _at(dev_err, _I32, None, "dev_err", dev),
+        _dtype_code(k_new), _cache_on(cache, dev, dt), T, rk, rv, rq,
+        _at(starts, _I32, (B + 1,), "starts", dev), _at(lens_in, _I32, (B,), "lens_in", dev),
+        _at(lens_out, _I32, (B,), "lens_out", dev), None if rope is None else _spec(rope), flags,
+        0 if dev_err is None else _at(dev_err, _I32, None, "dev_err", dev),
         _on(stream, dev)), "kvd_paged_append")
 
 
