@@ -22,8 +22,8 @@
 //    soon as these are in registers. Two blocks per SM: while one waits, the other computes.
 //  * Units of at most 32 vectors hold them four times, in lanes 32 apart, and each copy takes the
 //    softmax of a quarter of a tile's positions, with P zero elsewhere: a decoding sequence, with 4
-//    query vectors, uses all four warps. The copies are joined at the unit's end. (One row of 8192:
-//    14.1 us against 14.4 with the vectors held once; 8 rows of 5 tokens: 33.4 against 35.2.)
+//    query vectors, uses all four warps. The copies are joined at the unit's end. (Held once,
+//    one row of 8192 takes 2 % longer, 32 rows to 16384 2 %, 8 rows of 5 tokens 5 %.)
 //  * Work. The tiles of all units form one list, by weight, and every CTA of one wave takes an
 //    equal stretch of it; units cut by a stretch's end merge through the workspace, the last CTA
 //    to arrive in the order of the list. So neither one long row nor few rows leave SMs idle, and
@@ -33,12 +33,12 @@
 //
 // Measured (in a graph, caches warm where they fit; a copy runs at 6.8 TB/s, a large product at
 // 1928 TFLOP/s):
-//   1 row x 8192 positions, 32/8 heads         13.7 us   the launch, the list and the merge
+//   1 row x 8192 positions, 32/8 heads         12.6 us   the launch, the list and the merge
 //   32 rows to 16384, 32/8 heads                125 us   6.4 TB/s
 //   8 rows x 5 tokens over up to 8192            33 us   3.8 TB/s
-//   a chunk of 512 over 16384, 32/8 heads        73 us   934 TFLOP/s: the four row warps' chain of
-//                                                        loads, maxima and exponentials, twice per SM
-//   30 rows, two with chunks of 1000 at 8000    101 us   the same
+//   a chunk of 512 over 16384, 32/8 heads        72 us   936 TFLOP/s: the row warps' chain of
+//                                                        loads, maxima, exponentials, twice per SM
+//   30 rows, two with chunks of 1000 at 8000     99 us   the same
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -77,13 +77,15 @@ constexpr uint32_t kPgSmem = (kSlotsK + kSlotsV) * kStepBytes + kPgQBytes + 256 
 constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
 
-// The list's weights: of a tile, and what a unit costs besides (its start, end and merge). Measured
-// on one row of 8192 positions (64 tiles x 8 heads) and on a mixed batch: a unit as 3, 4, 5 and 6
-// tiles 15.4, 13.6, 15.3, 15.3 us and 101.9, 101.5, 102.3, 103.3; tiles of few vectors lighter by
-// 1/6 than the others 14.2 and 104.2, heavier by 1/5 15.3 and 105.3.
+// The list's weights: of a tile, and what a unit costs besides (its start, end and merge).
+// Measured, before the merge took its present form, on one row of 8192 positions (64 tiles x 8
+// heads) and on a mixed batch: a unit as 3, 4, 5 and 6 tiles 15.4, 13.6, 15.3, 15.3 us and 101.9,
+// 101.5, 102.3, 103.3; tiles of few vectors lighter by 1/6 than the others 14.2 and 104.2, heavier
+// by 1/5 15.3 and 105.3. A cut at least 20 from a unit's ends: 17.3 us for the row (5: no change); a
+// least share of 15, 25, 30: 15.7, 15.1, 16.7.
 constexpr uint32_t kWeight = 5, kUnit = 20;
-constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends (20: 17.3 us; 5: no change)
-constexpr uint32_t kLeast = 20;     // a CTA's least share (15: 15.7 us, 25: 15.1, 30: 16.7)
+constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
+constexpr uint32_t kLeast = 20;     // a CTA's least share
 constexpr int kMaxCtas = 512;
 
 struct PagedParams {
@@ -502,8 +504,8 @@ __device__ __forceinline__ int row_thread() {
 // Positions that only some tokens of a unit see have weight 0 for the others, and 0 * inf is NaN.
 // So what is not finite in those rows of V is taken out before the product, and noted: the first
 // position of each dim with +inf, -inf and NaN. It is added to the outputs of the tokens that see
-// it (repair). One warp, behind the copy of the tile at `base` and before the product that reads it;
-// positions lo .. hi - 1. Returns whether there was any.
+// it (repair). One warp, behind the copy of the tile at `base` and before the product that reads
+// it; positions lo .. hi - 1. Returns whether there was any.
 template <typename T>
 __device__ __forceinline__ bool scan_hidden(uint32_t tile, int base, int lo, int hi, int32_t* odd) {
     constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
@@ -772,7 +774,9 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
         float o[64];
         tc_ld64(t_o, o);
         float4* buf = reinterpret_cast<float4*>(sm.q);
-        const int phases = u.live > 16 ? 2 : 1, quads = 16 / phases, rows = 16 * phases;
+        // (places for 4, 16 or 32 rows: with 16 for the 4 of a decoding row most threads idle)
+        const int phases = u.live > 16 ? 2 : 1, quads = 16 / phases;
+        const int log_rows = u.live > 16 ? 5 : u.live > 4 ? 4 : 2, rows = 1 << log_rows;
 #pragma unroll 1
         for (int h = 0; h < phases; ++h) {
             if (r < u.live) {  // [quad][copy][row]
@@ -789,7 +793,7 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
             }
             rows_sync();
             for (int x = tid; x < quads * rows; x += kRowThreads) {
-                const int y = x & (rows - 1), c = x / rows;  // (rows: 16 or 32)
+                const int y = x & (rows - 1), c = x >> log_rows;
                 if (y >= u.live) continue;
                 float top = -INFINITY, all = 0.f;
 #pragma unroll
@@ -800,7 +804,7 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
                 for (int k = 0; k < REP; ++k) {
                     const float2 ml = sm.ml[y + k * R];
                     const float4 b = buf[(c * REP + k) * rows + y];
-                    const float f = exp2f(ml.x - ref);
+                    const float f = ex2_approx(ml.x - ref);
                     all = fmaf(ml.y, f, all);
                     a.x = fmaf(b.x, f, a.x);
                     a.y = fmaf(b.y, f, a.y);
@@ -839,7 +843,7 @@ struct Joined {
         float t = top;
 #pragma unroll
         for (int k = 0; k < N; ++k) t = fmaxf(t, k < n ? ml[k].x : t);
-        const float ref = t == -INFINITY ? 0.f : t, f0 = exp2f(top - ref);
+        const float ref = t == -INFINITY ? 0.f : t, f0 = ex2_approx(top - ref);
         top = t;
         l *= f0;
         o.x *= f0;
@@ -849,7 +853,7 @@ struct Joined {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             if (k >= n) break;
-            const float f = exp2f(ml[k].x - ref);
+            const float f = ex2_approx(ml[k].x - ref);
             l = fmaf(ml[k].y, f, l);
             o.x = fmaf(v[k].x, f, o.x);
             o.y = fmaf(v[k].y, f, o.y);
@@ -858,6 +862,22 @@ struct Joined {
         }
     }
 };
+
+// Loads that are issued where they stand. (The compiler would put them behind the tests for which
+// piece is there, one round trip after the other.)
+__device__ __forceinline__ float4 load_now(const float4* at) {
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 load_now(const float2* at) {
+    float2 v;
+    asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(at) : "memory");
+    return v;
+}
 
 // A cut unit's pieces, which lie in the workspace: CTAs i0 .. i0 + n - 1, the last to arrive merges
 // them in that order.
@@ -878,10 +898,11 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
     rows_sync();
     if (!*s_last) return;
     if (tid == 0) p.ws_cnt[i0] = 0;
-    auto slot = [&](int i) { return (int64_t)(2 * (i0 + i) + (i == 0)); };
-    auto ml_of = [&](int i, int r) { return __ldcg(p.ws_ml + slot(i) * p.slot_rows + r); };
+    // (2 x 512 slots of 16 x 128 places: indexes of 32 bits)
+    auto slot = [&](int i) { return (2 * (i0 + i) + (i == 0)) * p.slot_rows; };
+    auto ml_of = [&](int i, int r) { return load_now(p.ws_ml + (slot(i) + r)); };
     auto part_of = [&](int i, int c, int r) {
-        return __ldcg(p.ws_part + (slot(i) * 16 + c) * p.slot_rows + r);
+        return load_now(p.ws_part + (slot(i) * 16 + c * p.slot_rows + r));
     };
     if (u.live > 32 && n <= kFewPieces) {
         // many rows, few pieces: a thread per row
@@ -900,7 +921,7 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
 #pragma unroll
             for (int i = 0; i < kFewPieces; ++i) {
                 if (i >= n) break;
-                const float f = exp2f(ml[i].x - ref);
+                const float f = ex2_approx(ml[i].x - ref);
                 l = fmaf(ml[i].y, f, l);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
@@ -929,17 +950,32 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
             pack4<T>(a.o, a.l > 0.f ? 1.f / a.l : 0.f);
     };
     for (int x = tid; x < items * shares; x += kRowThreads) {
-        const int share = x / items, y = x - share * items, c = y & 15, r = y >> 4;
+        const int share = shares == 1 ? 0 : (unsigned)x / (unsigned)items;
+        const int y = x - share * items, c = y & 15, r = y >> 4;
         const int last = n * (share + 1) / shares;
         Joined a;
         a.clear();
         for (int i = n * share / shares; i < last; i += kBatch) {
+            // the pieces from CTA i0 + i on (the first piece's slot is one further). One warp runs
+            // on each scheduler here, so every instruction counts: an address worked out per piece
+            // instead of a step cost the row of 8192 1.2 us.
+            const float2* at_ml = p.ws_ml + (slot(i) + r);
+            const float4* at_v = p.ws_part + (slot(i) * 16 + c * p.slot_rows + r);
+            const int back = i == 0 ? p.slot_rows : 0, step = 2 * p.slot_rows;
             float2 ml[kBatch];
             float4 v[kBatch];
+            ml[0] = load_now(at_ml);
+            v[0] = load_now(at_v);
+            at_ml -= back;
+            at_v -= back * 16;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                ml[k] = ml_of(min(i + k, last - 1), r);
-                v[k] = part_of(min(i + k, last - 1), c, r);
+            for (int k = 1; k < kBatch; ++k) {
+                if (i + k < last) {
+                    at_ml += step;
+                    at_v += step * 16;
+                }
+                ml[k] = load_now(at_ml);
+                v[k] = load_now(at_v);
             }
             a.add(ml, v, last - i);
         }
