@@ -66,9 +66,6 @@ constexpr uint32_t kPgCols = 256;
 static_assert(kPgCols >= kPgColsP + kStep / 2 && kPgMinBlocks * kPgCols <= 512,
               "the resident blocks' tensor memory");
 constexpr uint32_t kPgQBytes = kPgRows * kRowBytes;
-// Pieces of a merge with a thread per row (a chunk of 512 over 16384, three pieces per unit of 128
-// rows: 73 us; with a thread per 4 dims of a row, as for more pieces or fewer rows, 100).
-constexpr int kFewPieces = 6;
 constexpr uint32_t kOddOffset = 256 + kPgRows * 8 + kRowThreads * 16;  // behind the barriers
 constexpr int kOddWords = 3 * kHeadDim;        // see scan_hidden
 // shared memory: K slots | V slots | Q | barriers | rows' references and sums | merge | odd
@@ -81,8 +78,8 @@ constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it b
 // Measured, before the merge took its present form, on one row of 8192 positions (64 tiles x 8
 // heads) and on a mixed batch: a unit as 3, 4, 5 and 6 tiles 15.4, 13.6, 15.3, 15.3 us and 101.9,
 // 101.5, 102.3, 103.3; tiles of few vectors lighter by 1/6 than the others 14.2 and 104.2, heavier
-// by 1/5 15.3 and 105.3. A cut at least 20 from a unit's ends: 17.3 us for the row (5: no change); a
-// least share of 15, 25, 30: 15.7, 15.1, 16.7.
+// by 1/5 15.3 and 105.3. A cut at least 20 from a unit's ends: 17.3 us for the row (5: no change);
+// a least share of 15, 25, 30: 15.7, 15.1, 16.7.
 constexpr uint32_t kWeight = 5, kUnit = 20;
 constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
 constexpr uint32_t kLeast = 20;     // a CTA's least share
@@ -829,38 +826,48 @@ __device__ __forceinline__ void finish_rows(const PagedParams& p, const Smem& sm
     }
 }
 
-// Partials (reference, sum, o) joined one after the other.
+// Partials (reference, sum, Q quads of dims) joined, N at a time.
+template <int Q>
 struct Joined {
     float top, l;
-    float4 o;
+    float4 o[Q];
     __device__ __forceinline__ void clear() {
         top = -INFINITY;
         l = 0.f;
-        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < Q; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    // The first n of them.
     template <int N>
-    __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N], int n) {
+    __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N][Q], int n) {
         float t = top;
 #pragma unroll
         for (int k = 0; k < N; ++k) t = fmaxf(t, k < n ? ml[k].x : t);
         const float ref = t == -INFINITY ? 0.f : t, f0 = ex2_approx(top - ref);
         top = t;
         l *= f0;
-        o.x *= f0;
-        o.y *= f0;
-        o.z *= f0;
-        o.w *= f0;
+#pragma unroll
+        for (int c = 0; c < Q; ++c) {
+            o[c].x *= f0;
+            o[c].y *= f0;
+            o[c].z *= f0;
+            o[c].w *= f0;
+        }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             if (k >= n) break;
             const float f = ex2_approx(ml[k].x - ref);
             l = fmaf(ml[k].y, f, l);
-            o.x = fmaf(v[k].x, f, o.x);
-            o.y = fmaf(v[k].y, f, o.y);
-            o.z = fmaf(v[k].z, f, o.z);
-            o.w = fmaf(v[k].w, f, o.w);
+#pragma unroll
+            for (int c = 0; c < Q; ++c) {
+                o[c].x = fmaf(v[k][c].x, f, o[c].x);
+                o[c].y = fmaf(v[k][c].y, f, o[c].y);
+                o[c].z = fmaf(v[k][c].z, f, o[c].z);
+                o[c].w = fmaf(v[k][c].w, f, o[c].w);
+            }
         }
     }
+    __device__ __forceinline__ float inv() const { return l > 0.f ? 1.f / l : 0.f; }
 };
 
 // Loads that are issued where they stand. (The compiler would put them behind the tests for which
@@ -877,6 +884,38 @@ __device__ __forceinline__ float2 load_now(const float2* at) {
     float2 v;
     asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(at) : "memory");
     return v;
+}
+
+// Pieces i .. last - 1 of row r, quads c .. c + Q - 1, N pieces in flight. The first CTA's piece lies
+// one slot further. One warp runs on each scheduler here, so every instruction counts: an address
+// worked out per piece instead of a step cost one row of 8192 positions 1.2 us.
+template <int Q, int N>
+__device__ __forceinline__ Joined<Q> join_pieces(const PagedParams& p, int i0, int i, int last,
+                                                 int r, int c) {
+    Joined<Q> a;
+    a.clear();
+    const int S = p.slot_rows;
+#pragma unroll 1
+    for (; i < last; i += N) {
+        // (2 x 512 slots of 16 x 128 places: indexes of 32 bits)
+        const int slot = (2 * (i0 + i) + (i == 0)) * S, back = i == 0 ? S : 0;
+        const float2* at_ml = p.ws_ml + (slot + r);
+        const float4* at_v = p.ws_part + (slot * 16 + c * S + r);
+        float2 ml[N];
+        float4 v[N][Q];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (k > 0 && i + k < last) {
+                at_ml += 2 * S - (k == 1 ? back : 0);
+                at_v += (2 * S - (k == 1 ? back : 0)) * 16;
+            }
+            ml[k] = load_now(at_ml);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) v[k][q] = load_now(at_v + q * S);
+        }
+        a.add(ml, v, last - i);
+    }
+    return a;
 }
 
 // A cut unit's pieces, which lie in the workspace: CTAs i0 .. i0 + n - 1, the last to arrive merges
@@ -898,107 +937,62 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
     rows_sync();
     if (!*s_last) return;
     if (tid == 0) p.ws_cnt[i0] = 0;
-    // (2 x 512 slots of 16 x 128 places: indexes of 32 bits)
-    auto slot = [&](int i) { return (2 * (i0 + i) + (i == 0)) * p.slot_rows; };
-    auto ml_of = [&](int i, int r) { return load_now(p.ws_ml + (slot(i) + r)); };
-    auto part_of = [&](int i, int c, int r) {
-        return load_now(p.ws_part + (slot(i) * 16 + c * p.slot_rows + r));
-    };
-    if (u.live > 32 && n <= kFewPieces) {
-        // many rows, few pieces: a thread per row
-        if (tid < u.live) {
-            float2 ml[kFewPieces];
+    // (two rows of 211 tokens at 11523, 24 pieces of 128 rows a unit: 34 us; a thread per 4 dims of a
+    // row, 16 turns of it, 60)
+    if (u.live > 32) {
+        // a thread per row
+        if (tid >= u.live) return;
+        const Joined<16> a = join_pieces<16, 1>(p, i0, 0, n, tid, 0);
+        const float inv = a.inv();
+        uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, u, tid));
 #pragma unroll
-            for (int i = 0; i < kFewPieces; ++i)
-                ml[i] = i < n ? ml_of(i, tid) : make_float2(-INFINITY, 0.f);
-            float top = -INFINITY, l = 0.f;
+        for (int c = 0; c < 8; ++c) {
+            const uint2 x = pack4<T>(a.o[2 * c], inv), y = pack4<T>(a.o[2 * c + 1], inv);
+            dst[c] = make_uint4(x.x, x.y, y.x, y.y);
+        }
+    } else if (u.live > 8) {
+        // a lane per row, a quarter of the dims per warp
+        const int r = tid & 31, c = tid / 32 * 4;
+        if (r >= u.live) return;
+        const Joined<4> a = join_pieces<4, 4>(p, i0, 0, n, r, c);
+        const float inv = a.inv();
+        uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, u, r) + c * 4);
 #pragma unroll
-            for (int i = 0; i < kFewPieces; ++i) top = fmaxf(top, ml[i].x);
-            const float ref = top == -INFINITY ? 0.f : top;
-            float4 o[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < kFewPieces; ++i) {
-                if (i >= n) break;
-                const float f = ex2_approx(ml[i].x - ref);
-                l = fmaf(ml[i].y, f, l);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const float4 v = part_of(i, c, tid);
-                    o[c].x = fmaf(v.x, f, o[c].x);
-                    o[c].y = fmaf(v.y, f, o[c].y);
-                    o[c].z = fmaf(v.z, f, o[c].z);
-                    o[c].w = fmaf(v.w, f, o[c].w);
+        for (int k = 0; k < 2; ++k) {
+            const uint2 x = pack4<T>(a.o[2 * k], inv), y = pack4<T>(a.o[2 * k + 1], inv);
+            dst[k] = make_uint4(x.x, x.y, y.x, y.y);
+        }
+    } else {
+        // a thread per row, 4 dims and, of at most 4 rows, share of the pieces, joined in order
+        const int items = u.live * 16, shares = kRowThreads / items;
+        const int share = (int)((unsigned)tid / (unsigned)items);  // (of the last threads: none)
+        const int y = tid - share * items, c = y & 15, r = y >> 4;
+        auto store = [&](const Joined<1>& a) {
+            *reinterpret_cast<uint2*>(out_row<T>(p, u, r) + c * 4) = pack4<T>(a.o[0], a.inv());
+        };
+        Joined<1> a;
+        if (share < shares) {
+            a = join_pieces<1, 8>(p, i0, n * share / shares, n * (share + 1) / shares, r, c);
+            if (shares == 1) {
+                store(a);
+            } else {
+                sm.part[tid] = a.o[0];
+                sm.ml[tid] = make_float2(a.top, a.l);
+            }
+        }
+        if (shares > 1) {
+            rows_sync();
+            if (tid < items) {
+                a.clear();
+                for (int k = 0; k < shares; ++k) {
+                    const float2 ml[1] = {sm.ml[k * items + tid]};
+                    const float4 v[1][1] = {{sm.part[k * items + tid]}};
+                    a.add(ml, v, 1);
                 }
+                store(a);
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            uint4* dst = reinterpret_cast<uint4*>(out_row<T>(p, u, tid));
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint2 a = pack4<T>(o[2 * c], inv), b = pack4<T>(o[2 * c + 1], inv);
-                dst[c] = make_uint4(a.x, a.y, b.x, b.y);
-            }
+            rows_sync();  // read before the next unit's sums are written
         }
-        return;
-    }
-    // a thread per row, 4 dims and, of few rows, share of the pieces; the shares joined in order
-    constexpr int kBatch = 8;  // pieces whose loads are in flight
-    const int items = u.live * 16, shares = max(1, kRowThreads / items);
-    auto store = [&](int y, const Joined& a) {
-        *reinterpret_cast<uint2*>(out_row<T>(p, u, y >> 4) + (y & 15) * 4) =
-            pack4<T>(a.o, a.l > 0.f ? 1.f / a.l : 0.f);
-    };
-    for (int x = tid; x < items * shares; x += kRowThreads) {
-        const int share = shares == 1 ? 0 : (unsigned)x / (unsigned)items;
-        const int y = x - share * items, c = y & 15, r = y >> 4;
-        const int last = n * (share + 1) / shares;
-        Joined a;
-        a.clear();
-        for (int i = n * share / shares; i < last; i += kBatch) {
-            // the pieces from CTA i0 + i on (the first piece's slot is one further). One warp runs
-            // on each scheduler here, so every instruction counts: an address worked out per piece
-            // instead of a step cost the row of 8192 1.2 us.
-            const float2* at_ml = p.ws_ml + (slot(i) + r);
-            const float4* at_v = p.ws_part + (slot(i) * 16 + c * p.slot_rows + r);
-            const int back = i == 0 ? p.slot_rows : 0, step = 2 * p.slot_rows;
-            float2 ml[kBatch];
-            float4 v[kBatch];
-            ml[0] = load_now(at_ml);
-            v[0] = load_now(at_v);
-            at_ml -= back;
-            at_v -= back * 16;
-#pragma unroll
-            for (int k = 1; k < kBatch; ++k) {
-                if (i + k < last) {
-                    at_ml += step;
-                    at_v += step * 16;
-                }
-                ml[k] = load_now(at_ml);
-                v[k] = load_now(at_v);
-            }
-            a.add(ml, v, last - i);
-        }
-        if (shares == 1) {
-            store(y, a);
-        } else {
-            sm.part[x] = a.o;
-            sm.ml[x] = make_float2(a.top, a.l);
-        }
-    }
-    if (shares > 1) {
-        rows_sync();
-        if (tid < items) {
-            Joined a;
-            a.clear();
-            for (int k = 0; k < shares; ++k) {
-                const float2 ml[1] = {sm.ml[k * items + tid]};
-                const float4 v[1] = {sm.part[k * items + tid]};
-                a.add(ml, v, 1);
-            }
-            store(tid, a);
-        }
-        rows_sync();  // read before the next unit's sums are written
     }
 }
 

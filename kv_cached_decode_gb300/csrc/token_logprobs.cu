@@ -55,6 +55,10 @@ constexpr float kFar = -3.402823466e38f;          // for -inf in weight * expone
 // SM: 27.8, 21.4, 21.4, 21.5 us; 256 x 32000: 20.0, 19.9, 20.0, 21.5).
 constexpr int64_t kLpManyBlocks = 152 * 2;
 
+// Tokens per row that a build of three blocks per SM holds (771 rows of 102542 fp32 logits with 2
+// given tokens: 78 us, 95 with the build for 16; 1514 of 18529 f16 with 4: 53 and 62).
+constexpr int kFewGiven = 4;
+
 constexpr float kLn2 = 0.69314718056f;
 
 typedef unsigned long long Key;
@@ -417,9 +421,9 @@ __device__ __forceinline__ void st_cluster_word(void* local, int rank, uint32_t 
                  : "memory");
 }
 
-// GIVEN: 0 no ranks; 1 one token per row; 2 up to KVD_MAX_GIVEN.
+// GIVEN: the most tokens per row whose ranks are counted.
 template <typename T, int GIVEN>
-__global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
+__global__ void __launch_bounds__(kLpThreads, GIVEN > 4 ? 2 : GIVEN > 1 ? 3 : 4)
     token_logprobs_kernel(const LogprobParams p) {
     extern __shared__ uint8_t lp_smem[];
     LpShared& S = *reinterpret_cast<LpShared*>(
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     constexpr int VN = Vec<T>::n, NV = kPer / VN;
     constexpr int kSub = 4 / (int)sizeof(T);  // rounds per stage
     static_assert(kSub <= 2, "the noted chunks' place");
-    constexpr int kTok = GIVEN == 2 ? KVD_MAX_GIVEN : 1;
+    constexpr int kTok = GIVEN > 1 ? GIVEN : 1;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)(blockIdx.x % (unsigned)p.cluster);
     const int row = (int)(blockIdx.x / (unsigned)p.cluster);
@@ -578,7 +582,7 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
         if (GIVEN) {
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
-                if (GIVEN == 2 && i >= p.given) break;
+                if (GIVEN > 1 && i >= p.given) break;
                 if (cm < val[i]) continue;
                 // all of a round before the token, or behind it
                 const int from = body + r * NV * kLpThreads * VN;  // the round's first id
@@ -683,7 +687,7 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN == 2 ? 2 : 4)
     if (GIVEN) {
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
-            if (GIVEN == 2 && i >= p.given) break;
+            if (GIVEN > 1 && i >= p.given) break;
             const int n = __reduce_add_sync(0xffffffffu, cnt[i]);
             if (lane == 0) atomicSub(&S.count[i], n);
         }
@@ -810,7 +814,9 @@ kvd_status run(const LogprobParams& p, bool pdl, cudaStream_t st) {
 template <typename T>
 kvd_status run_type(const LogprobParams& p, bool pdl, cudaStream_t st) {
     if (!p.rank || p.given == 0) return run<T, 0>(p, pdl, st);
-    return p.given == 1 ? run<T, 1>(p, pdl, st) : run<T, 2>(p, pdl, st);
+    if (p.given == 1) return run<T, 1>(p, pdl, st);
+    return p.given <= kFewGiven ? run<T, kFewGiven>(p, pdl, st)
+                                : run<T, KVD_MAX_GIVEN>(p, pdl, st);
 }
 
 }  // namespace
