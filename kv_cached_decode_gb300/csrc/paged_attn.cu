@@ -886,8 +886,8 @@ __device__ __forceinline__ float2 load_now(const float2* at) {
     return v;
 }
 
-// Pieces i .. last - 1 of row r, quads c .. c + Q - 1, N pieces in flight. The first CTA's piece lies
-// one slot further. One warp runs on each scheduler here, so every instruction counts: an address
+// Pieces i .. last - 1 of row r, quads c .. c + Q - 1, N pieces in flight. (The first CTA's lies
+// one slot further.) One warp runs on each scheduler here, so every instruction counts: an address
 // worked out per piece instead of a step cost one row of 8192 positions 1.2 us.
 template <int Q, int N>
 __device__ __forceinline__ Joined<Q> join_pieces(const PagedParams& p, int i0, int i, int last,
