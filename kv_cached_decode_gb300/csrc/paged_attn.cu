@@ -1339,13 +1339,13 @@ extern "C" kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache* cac
     const size_t need = paged_workspace_bytes(q->n_heads, cache->n_kv_heads, max_new);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need)
         return KVD_ERR_WORKSPACE;
-    const int nsm = sm_count();
-    if (nsm <= 0) return KVD_ERR_CUDA;
     // the list of tiles, at its longest, is counted in 32 bits
     const int tq = kPgRows / group;
     const double blocks = (double)cache->n_kv_heads * ((double)n_tokens / tq + cache->batch);
     const double longest = kWeight * ((double)cache->table_width * cache->page_size / kStep + 1.);
     if (blocks * (longest + kUnit) > 4e9) return KVD_ERR_UNSUPPORTED;
+    const int nsm = sm_count();
+    if (nsm <= 0) return KVD_ERR_CUDA;
     CUtensorMap mk, mv;
     if (kvd_status s = encode_pool_map(&mk, dtype, cache->k, cache)) return s;
     if (kvd_status s = encode_pool_map(&mv, dtype, cache->v, cache)) return s;
