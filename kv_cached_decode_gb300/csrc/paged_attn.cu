@@ -29,13 +29,13 @@
 //    to arrive in the order of the list. So neither one long row nor few rows leave SMs idle, and
 //    the tiles of decoding rows (HBM) and of prompt chunks (softmax) run at the same time. The
 //    copying warp runs ahead into the CTA's next unit. The list is not made by the host, as lengths
-//    lie on the device: every CTA sums the rows' weights (64 rows: about 2 us).
+//    lie on the device: every CTA sums the rows' weights (about 2 us).
 //
 // Measured (in a graph, caches warm where they fit; a copy runs at 6.8 TB/s, a large product at
 // 1928 TFLOP/s):
-//   1 row x 8192 positions, 32/8 heads         12.6 us   the launch, the list and the merge
+//   1 row x 8192 positions, 32/8 heads         12.2 us   the launch, the list and the merge
 //   32 rows to 16384, 32/8 heads                125 us   6.4 TB/s
-//   8 rows x 5 tokens over up to 8192            33 us   3.8 TB/s
+//   8 rows x 5 tokens over up to 4095            32 us   4.0 TB/s
 //   a chunk of 512 over 16384, 32/8 heads        72 us   936 TFLOP/s: the row warps' chain of
 //                                                        loads, maxima, exponentials, twice per SM
 //   30 rows, two with chunks of 1000 at 8000     99 us   the same
@@ -218,17 +218,22 @@ __device__ __forceinline__ Table fill_table(const PagedParams& p, uint32_t* tab)
     }
     return t;
 }
+// Sums of the warp's values up to and with each lane's.
+__device__ __forceinline__ uint32_t scan_rows(uint32_t inc) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc = add_length(inc, o);
+    }
+    return inc;
+}
 __device__ __forceinline__ uint32_t finish_table(const Table& t) {
     const int lane = threadIdx.x & 31;
     uint32_t before = 0;
     for (int e0 = 0; e0 < t.n; e0 += 32) {
-        uint32_t inc = e0 + lane < t.n ? t.tab[e0 + lane] : 0;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc = add_length(inc, o);
-        }
-        inc = add_length(inc, before);
+        const uint32_t inc =
+            add_length(scan_rows(e0 + lane < t.n ? t.tab[e0 + lane] : 0), before);
         if (e0 + lane < t.n) t.tab[e0 + lane] = inc;
         before = __shfl_sync(0xffffffffu, inc, 31);
     }
@@ -264,13 +269,10 @@ struct Place {  // of a unit
     uint32_t w;
     uint32_t u0;  // where it starts in the list
 };
-// The unit at place `at`, which is below the list's length. One warp.
-__device__ __forceinline__ Place find_unit(const PagedParams& p, const Table& t, uint32_t at) {
-    Place u;
-    uint32_t before;
-    u.b = find_row(p, t, at, before);
-    bool bad;
-    u.r = row_of(p, u.b, bad);
+// The unit of u's row at place `at`, which the row holds; the list's length before the row. One
+// warp.
+__device__ __forceinline__ void find_unit(const PagedParams& p, Place& u, uint32_t at,
+                                          uint32_t before) {
     const Shape s = shape_of(p, u.r);
     const uint32_t in = at - before;
     // the last block that starts at or before `at`: 32 probes a step
@@ -289,7 +291,6 @@ __device__ __forceinline__ Place find_unit(const PagedParams& p, const Table& t,
     u.w = unit_weight(p, s, lo);
     u.h = (int)((in - pre) / u.w);
     u.u0 = before + pre + (uint32_t)u.h * u.w;
-    return u;
 }
 
 // Stretches of the list: CTA i's share starts at floor(i total / ctas), the quotient in 16.16 bits.
@@ -937,8 +938,8 @@ __device__ __forceinline__ void merge_pieces(const PagedParams& p, const Smem& s
     rows_sync();
     if (!*s_last) return;
     if (tid == 0) p.ws_cnt[i0] = 0;
-    // (two rows of 211 tokens at 11523, 24 pieces of 128 rows a unit: 34 us; a thread per 4 dims of a
-    // row, 16 turns of it, 60)
+    // (two rows of 211 tokens at 11523, 24 pieces of 128 rows a unit: 34 us; a thread per 4 dims of
+    // a row, 16 turns of it, 60)
     if (u.live > 32) {
         // a thread per row
         if (tid >= u.live) return;
@@ -1020,37 +1021,70 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     }
     pdl_wait();
     pdl_trigger();
-    const Table tab = fill_table(p, reinterpret_cast<uint32_t*>(sm.q));
-    __syncthreads();
-    if (warp == 0) {
-        const uint32_t total = finish_table(tab);
-        if (lane == 0) {
-            s_total = total == kTooLong ? 0 : total;
-            if (total == kTooLong && blockIdx.x == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
-        }
-    } else if (mma_warp) {
+    if (mma_warp) {
         tc_alloc(smem_u32(&s_tmem), kPgCols);
         tc_relinquish();
+        tc_fence_before();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    const Shares sh = shares(s_total);
-    // warp 0 finds where the stretch starts, warp 1 where it ends
+    // Warp 0 finds where the stretch starts, warp 1 where it ends: each from a list of its own of
+    // at most 32 rows, or from the block's table (1 row x 8192 that way: 12.6 us instead of 12.2).
+    const bool few = p.batch <= 32;
+    Table tab;
+    uint32_t total = 0, sum = 0;
+    if (!few) {
+        tab = fill_table(p, reinterpret_cast<uint32_t*>(sm.q));
+        __syncthreads();
+        if (warp == 0) {
+            total = finish_table(tab);
+            if (lane == 0) s_total = total;
+        }
+        __syncthreads();
+        total = s_total;
+    }
     if (warp < 2) {
+        Row mine = {0, 0, 0};
+        if (few) {
+            bool bad = false;
+            if (lane < p.batch) mine = row_of(p, lane, bad);
+            if (bad && blockIdx.x == 0 && warp == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+            sum = scan_rows(row_weight(p, mine));
+            total = __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (total == kTooLong) {
+            if (lane == 0 && warp == 0 && blockIdx.x == 0)
+                flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
+            total = 0;
+        }
+        const Shares sh = shares(total);
         const uint32_t at = sh.start(blockIdx.x + warp);
-        if (blockIdx.x >= sh.ctas || at >= s_total) {
-            if (lane == 0) *(warp ? &s_to : &s_from) = warp ? s_total : 0xffffffffu;
+        if (blockIdx.x >= sh.ctas || at >= total) {
+            if (lane == 0) *(warp ? &s_to : &s_from) = warp ? total : 0xffffffffu;
         } else {
-            const Place u = find_unit(p, tab, at);
+            Place u;
+            uint32_t before;
+            bool bad;
+            if (few) {
+                u.b = __popc(__ballot_sync(0xffffffffu, sum <= at));
+                before = __shfl_sync(0xffffffffu, sum, max(u.b - 1, 0));
+                if (u.b == 0) before = 0;
+                u.r.s = __shfl_sync(0xffffffffu, mine.s, u.b);
+                u.r.n = __shfl_sync(0xffffffffu, mine.n, u.b);
+                u.r.len = __shfl_sync(0xffffffffu, mine.len, u.b);
+            } else {
+                u.b = find_row(p, tab, at, before);
+                u.r = row_of(p, u.b, bad);
+            }
+            find_unit(p, u, at, before);
             if (lane == 0) {
                 if (warp == 0) s_place = u;
                 *(warp ? &s_to : &s_from) = cut(u, at);
             }
         }
+        if (tid == 0) s_total = total;
     }
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
     Walk u;
     bool ok = u.start(p, s_place, s_from, s_to);
     if (!ok) {

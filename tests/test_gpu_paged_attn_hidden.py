@@ -91,9 +91,11 @@ def test_a_whole_row_of_odd_values_in_every_new_token():
     assert not out.isfinite().any() and not (out == -INF).any()
 
 
-def test_overlapping_stretches_too_long_for_the_list():
-    """Tokens claimed by 64 rows of 2^19 positions each: more tiles than the list can count."""
-    T, rows, page = 8192, 128, 65536
+@pytest.mark.parametrize("T,rows", [(8192, 128), (14000, 32)])
+def test_overlapping_stretches_too_long_for_the_list(T, rows):
+    """Tokens claimed by half the rows of 2^19 positions each: more tiles than the list can
+    count."""
+    page = 65536
     b = Batch([(1, 8)], 128, 1, page, F16)
     b.starts = torch.tensor([0, T] * (rows // 2) + [0], dtype=torch.int32, device="cuda")
     b.lens = torch.full((rows,), 8 * page, dtype=torch.int32, device="cuda")
