@@ -492,6 +492,11 @@ __device__ __forceinline__ uint8_t* smem_base(uint8_t* raw) {
     asm volatile("" : "+l"(raw));
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
 }
+// 16 bytes into shared memory, the first n of them from `from`, the others zeros.
+__device__ __forceinline__ void cp_async16_part(uint32_t to, const void* from, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n)
+                 : "memory");
+}
 __device__ __forceinline__ int row_thread() {
     int t;
     asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
@@ -1230,26 +1235,32 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
         // ---- the rows ----
         uint32_t it0 = 0, scans = 0;
         auto walk = [&]() { return s_walk[row_thread() / 32]; };
-        // this thread's query row (zeros past the unit's) into the swizzled A operand
-        auto stage_q = [&](const Walk& u) {
-            const Smem sm = smem_at(smem_base(smem_raw));
+        // this thread's query row (zeros past the unit's) on its way into the swizzled A operand,
+        // and handed over
+        auto fetch_q = [&](const Walk& u) {
+            const uint32_t to = smem_u32(smem_at(smem_base(smem_raw)).q);
             const int r = row_thread() & (kPgRows / copies_of(u.live) - 1);
-            const int tok = r / p.group, hg = r - tok * p.group;
+            const int from = r < u.live ? r : 0, tok = from / p.group, hg = from - tok * p.group;
             const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.q + t * p.q_st + (int64_t)(u.h * p.group + hg) * p.q_sh);
-            uint4 qv[8];
+            const uint8_t* src = p.q + t * p.q_st + (int64_t)(u.h * p.group + hg) * p.q_sh;
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                qv[c] = r < u.live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-            // (the loop over the tiles knows positive scales only)
-            const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint4 v = qv[c];
-                v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-                if (p.scale_sign == 0) v = times_zero<T>(v);
-                *reinterpret_cast<uint4*>(sm.q + swz(row_thread(), c)) = v;
+                cp_async16_part(to + swz(row_thread(), c), src + c * 16, r < u.live ? 16 : 0);
+            cp_async_commit();
+        };
+        auto stage_q = [&]() {
+            const Smem sm = smem_at(smem_base(smem_raw));
+            cp_async_wait_all();
+            if (p.scale_sign <= 0) {
+                // (the loop over the tiles knows positive scales only)
+                const uint32_t flip = p.scale_sign < 0 ? 0x80008000u : 0u;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint4* at = reinterpret_cast<uint4*>(sm.q + swz(row_thread(), c));
+                    const uint4 v = *at;
+                    *at = flip ? make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip)
+                               : times_zero<T>(v);
+                }
             }
             fence_proxy_async();
             warp_arrive(sm.bar(kBarQ));
@@ -1267,19 +1278,24 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             return run_rows<T, 4>(p.scale_log2, bars, tmem, u.v0, it0, end, u.kvend, lim, scan);
         };
         put_away(walk(), u);
-        stage_q(u);
+        fetch_q(u);
+        stage_q();
         for (bool more = true; more;) {
             const RowsEnd e = weigh();
             const Walk done = take_back<Walk>(walk());
             u = done;
             more = u.next(p);
             put_away(walk(), u);
+            // (every score of the unit is done, so Q's place is free, but for the join of copies)
+            const bool early = copies_of(done.live) == 1;
+            if (more && early) fetch_q(u);
             const Smem sm = smem_at(smem_base(smem_raw));
             it0 += done.v1 - done.v0;
             scans += done.hides(p);
             ok = e.ok && mbar_wait_bounded(sm.bar(kBarO), (it0 - 1) & 1);
             if (rows_any(!ok)) {
                 if (row_thread() == 0) flag_error(p.dev_err, KVD_ERR_TIMEOUT);
+                cp_async_wait_all();
                 break;
             }
             tc_fence_after();
@@ -1290,8 +1306,10 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             else
                 finish_rows<T, 4>(p, sm, tmem, done, whole, slot, e.m, e.l);
             tc_fence_before();  // O is read before the next unit's products
-            // (loaded here and not before the unit's end: rows in flight over it would be spilled)
-            if (more) stage_q(take_back<Walk>(walk()));
+            if (more) {
+                if (!early) fetch_q(take_back<Walk>(walk()));
+                stage_q();
+            }
             if (!whole) {
                 const Shares sh = shares(s_total);
                 // (the last share that starts before the unit's first cut, and before its last)
