@@ -33,12 +33,13 @@
 //
 // Measured (in a graph, caches warm where they fit; a copy runs at 6.8 TB/s, a large product at
 // 1928 TFLOP/s):
-//   1 row x 8192 positions, 32/8 heads         12.2 us   the launch, the list and the merge
+//   1 row x 8192 positions, 32/8 heads         12.1 us   the launch, the list and the merge
 //   32 rows to 16384, 32/8 heads                125 us   6.4 TB/s
 //   8 rows x 5 tokens over up to 4095            32 us   4.0 TB/s
-//   a chunk of 512 over 16384, 32/8 heads        72 us   936 TFLOP/s: the row warps' chain of
-//                                                        loads, maxima, exponentials, twice per SM
-//   30 rows, two with chunks of 1000 at 8000     99 us   the same
+//   a chunk of 512 over 16384, 32/8 heads        73 us   930 TFLOP/s: the row warps' chain of
+//                                                        loads, maxima, exponentials and
+//                                                        hand-offs, 2200 cycles a tile
+//   30 rows, two with chunks of 1000 at 8000     98 us   the same
 #include <algorithm>
 #include <climits>
 #include <cmath>
