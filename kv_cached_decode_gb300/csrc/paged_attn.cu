@@ -84,6 +84,11 @@ constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it b
 constexpr uint32_t kWeight = 5, kUnit = 20;
 constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
 constexpr uint32_t kLeast = 20;     // a CTA's least share
+// A unit of more than 32 vectors and T tiles, cut into n pieces, takes T / n tiles and n joins of
+// 128 rows, one after the other, which cost half a tile each: about 1.4 sqrt(T) pieces are best, so
+// a least share of kShare sqrt(T) for calls with few units. (16 tokens x 8 heads at 20000: 29 us
+// with it, 34.5 without; at 100000 46 and 143; two rows of 211 tokens at 11523 29 and 33.)
+constexpr float kShare = 4.f;
 constexpr int kMaxCtas = 512;
 
 struct PagedParams {
@@ -190,6 +195,11 @@ __device__ __forceinline__ uint32_t row_weight(const PagedParams& p, const Row& 
     return p.n_kv_heads * (full_blocks(p, s, s.nmb - 1) + unit_weight(p, s, s.nmb - 1));
 }
 
+// Tiles of a row's longest unit, where that has more than 32 vectors.
+__device__ __forceinline__ int heavy_tiles(const PagedParams& p, const Row& r) {
+    return min(r.n, p.tq) * p.group > 32 ? r.len / kStep : 0;
+}
+
 // Prefix sums over the rows' weights: tab[e] is the list's length up to and with the rows of entry
 // e, `each` rows an entry. The host has bounded the length that distinct rows can give; sums that
 // leave 32 bits all the same (stretches of tokens that overlap) stay at kTooLong.
@@ -203,8 +213,9 @@ struct Table {
     int each, n;
 };
 // All threads; the sums are whole behind a barrier and finish_table (one warp).
-__device__ __forceinline__ Table fill_table(const PagedParams& p, uint32_t* tab) {
+__device__ __forceinline__ Table fill_table(const PagedParams& p, uint32_t* tab, int& longest) {
     Table t;
+    longest = 0;
     t.tab = tab;
     t.each = (p.batch + kTable - 1) / kTable;
     t.n = t.each == 1 ? p.batch : (p.batch + t.each - 1) / t.each;
@@ -212,7 +223,9 @@ __device__ __forceinline__ Table fill_table(const PagedParams& p, uint32_t* tab)
         uint32_t w = 0;
         for (int b = e * t.each; b < min((e + 1) * t.each, p.batch); ++b) {
             bool bad;
-            w = add_length(w, row_weight(p, row_of(p, b, bad)));
+            const Row r = row_of(p, b, bad);
+            w = add_length(w, row_weight(p, r));
+            longest = max(longest, heavy_tiles(p, r));
             if (bad && blockIdx.x == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
         }
         tab[e] = w;
@@ -308,10 +321,10 @@ struct Shares {
         return i;
     }
 };
-__device__ __forceinline__ Shares shares(uint32_t total) {
+__device__ __forceinline__ Shares shares(uint32_t total, uint32_t least) {
     Shares s;
     s.total = total;
-    s.ctas = max(1u, min(gridDim.x, total / kLeast));
+    s.ctas = max(1u, min(gridDim.x, total / least));
     const uint32_t per = total / s.ctas;
     s.each = ((uint64_t)per << 16) + ((total - per * s.ctas) << 16) / s.ctas;
     return s;
@@ -1012,9 +1025,9 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     const Smem sm = smem_at(smem_base(smem_raw));
     static_assert(kBarCount * 8 <= 256, "the barriers' place");
     __shared__ Place s_place;
-    __shared__ uint32_t s_total, s_from, s_to, s_tmem;
+    __shared__ uint32_t s_total, s_least, s_from, s_to, s_tmem;
     __shared__ uint32_t s_walk[kRowThreads / 32][sizeof(Walk) / 4];
-    __shared__ int s_last;
+    __shared__ int s_last, s_longest[kPgThreads / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool mma_warp = warp == kRowThreads / 32, copy_warp = warp == kRowThreads / 32 + 1;
     if (copy_warp && lane == 0) {
@@ -1037,8 +1050,11 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     const bool few = p.batch <= 32;
     Table tab;
     uint32_t total = 0, sum = 0;
+    int longest = 0;
     if (!few) {
-        tab = fill_table(p, reinterpret_cast<uint32_t*>(sm.q));
+        tab = fill_table(p, reinterpret_cast<uint32_t*>(sm.q), longest);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) s_longest[warp] = longest;
         __syncthreads();
         if (warp == 0) {
             total = finish_table(tab);
@@ -1049,19 +1065,24 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
     }
     if (warp < 2) {
         Row mine = {0, 0, 0};
+        uint32_t least = kLeast;
         if (few) {
             bool bad = false;
             if (lane < p.batch) mine = row_of(p, lane, bad);
             if (bad && blockIdx.x == 0 && warp == 0) flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
             sum = scan_rows(row_weight(p, mine));
             total = __shfl_sync(0xffffffffu, sum, 31);
+            longest = __reduce_max_sync(0xffffffffu, heavy_tiles(p, mine));
+        } else {
+            longest = __reduce_max_sync(0xffffffffu, lane < kPgThreads / 32 ? s_longest[lane] : 0);
         }
+        least = max(least, (uint32_t)(kShare * sqrtf((float)longest)));
         if (total == kTooLong) {
             if (lane == 0 && warp == 0 && blockIdx.x == 0)
                 flag_error(p.dev_err, KVD_ERR_LEN_OVERFLOW);
             total = 0;
         }
-        const Shares sh = shares(total);
+        const Shares sh = shares(total, least);
         const uint32_t at = sh.start(blockIdx.x + warp);
         if (blockIdx.x >= sh.ctas || at >= total) {
             if (lane == 0) *(warp ? &s_to : &s_from) = warp ? total : 0xffffffffu;
@@ -1086,7 +1107,10 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                 *(warp ? &s_to : &s_from) = cut(u, at);
             }
         }
-        if (tid == 0) s_total = total;
+        if (tid == 0) {
+            s_total = total;
+            s_least = least;
+        }
     }
     __syncthreads();
     tc_fence_after();
@@ -1312,7 +1336,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
                 stage_q();
             }
             if (!whole) {
-                const Shares sh = shares(s_total);
+                const Shares sh = shares(s_total, s_least);
                 // (the last share that starts before the unit's first cut, and before its last)
                 const uint32_t i0 = sh.holder(done.u0 + keep_lo(done.w) - 1);
                 const uint32_t i1 = sh.holder(done.u0 + keep_hi(done.w) - 1);

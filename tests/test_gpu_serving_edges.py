@@ -223,3 +223,12 @@ def test_tensors_of_another_device_or_stream_are_refused():
         with pytest.raises(ValueError):
             call()
     assert (lse == 9.0).all()
+
+
+@pytest.mark.parametrize("pad", [0, 60])
+def test_one_long_chunk_of_many_vectors(pad):
+    """A unit of 128 vectors cut into many pieces, alone or in a batch padded with empty rows."""
+    b = Batch([(0, 5)] * (pad // 2) + [(16, 30000)] + [(0, 9)] * (pad // 2), 8, 1, 64, F16, seed=2)
+    first = b.attend()
+    b.check(first)
+    assert torch.equal(b.attend(), first)
