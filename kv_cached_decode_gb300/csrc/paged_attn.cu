@@ -20,8 +20,8 @@
 //    its own, a lane of the copying warp per page; page numbers are read a tile ahead. Boxes from
 //    the unit's last visible position on are not read. The scores of the next tile are issued as
 //    soon as these are in registers. Two blocks per SM: while one waits, the other computes.
-//  * Units of at most 32 vectors hold them four times, in lanes 32 apart, and each copy takes the
-//    softmax of a quarter of a tile's positions, with P zero elsewhere: a decoding sequence, with 4
+//  * Units of at most 32 vectors (16 in short ones) hold them four times, in lanes 32 apart, and
+//    each copy takes the softmax of a quarter of a tile's positions, with P zero elsewhere: a decoding sequence, with 4
 //    query vectors, uses all four warps. The copies are joined at the unit's end. (Held once,
 //    one row of 8192 takes 2 % longer, 32 rows to 16384 2 %, 8 rows of 5 tokens 5 %.)
 //  * Work. The tiles of all units form one list, by weight, and every CTA of one wave takes an
@@ -82,6 +82,7 @@ constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it b
 // by 1/5 15.3 and 105.3. A cut at least 20 from a unit's ends: 17.3 us for the row (5: no change);
 // a least share of 15, 25, 30: 15.7, 15.1, 16.7.
 constexpr uint32_t kWeight = 5, kUnit = 20;
+constexpr int kShort = 2;           // see copies_of
 constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends
 constexpr uint32_t kLeast = 20;     // a CTA's least share
 // A unit of more than 32 vectors and T tiles, cut into n pieces, takes T / n tiles and n joins of
@@ -178,8 +179,13 @@ __device__ __forceinline__ int kv_end(const PagedParams& p, const Shape& s, int 
 __device__ __forceinline__ int tiles_of(const PagedParams& p, const Shape& s, int mb) {
     return (kv_end(p, s, mb) + kStep - 1) / kStep;
 }
-// Units of at most 32 vectors hold them four times.
-__device__ __forceinline__ int copies_of(int live) { return live > 32 ? 1 : 4; }
+// Units of at most 32 vectors hold them four times; those of more than 16 only if they have more
+// than kShort tiles, as the join of their copies takes as long as two tiles (106 rows of 5 tokens x
+// 80/20 heads and one tile: 50 us with it, 42 without; 64 of 5 x 32/8 at 700, five tiles: 24.8 and
+// 28.6).
+__device__ __forceinline__ int copies_of(int live, int tiles) {
+    return live > 32 || (live > 16 && tiles <= kShort) ? 1 : 4;
+}
 __device__ __forceinline__ uint32_t unit_weight(const PagedParams& p, const Shape& s, int mb) {
     return tiles_of(p, s, mb) * kWeight + kUnit;
 }
@@ -1264,7 +1270,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
         // and handed over
         auto fetch_q = [&](const Walk& u) {
             const uint32_t to = smem_u32(smem_at(smem_base(smem_raw)).q);
-            const int r = row_thread() & (kPgRows / copies_of(u.live) - 1);
+            const int r = row_thread() & (kPgRows / copies_of(u.live, u.tiles) - 1);
             const int from = r < u.live ? r : 0, tok = from / p.group, hg = from - tok * p.group;
             const int64_t t = u.s.r.s + (int64_t)u.mb * p.tq + tok;
             const uint8_t* src = p.q + t * p.q_st + (int64_t)(u.h * p.group + hg) * p.q_sh;
@@ -1294,7 +1300,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
         auto weigh = [&]() {
             const Walk u = take_back<Walk>(walk());
             const uint32_t bars = smem_at(smem_base(smem_raw)).bar(0), end = it0 + u.v1 - u.v0;
-            const int rep = copies_of(u.live), r = row_thread() & (kPgRows / rep - 1);
+            const int rep = copies_of(u.live, u.tiles), r = row_thread() & (kPgRows / rep - 1);
             // keys t < lim are visible; rows past the unit's see all of it (and are not written)
             const int lim = r < u.live ? u.s.s0() + u.mb * p.tq + r / p.group + 1 : u.kvend;
             const int scan = u.hides(p) ? (int)(scans & 1) : -1;
@@ -1312,7 +1318,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             more = u.next(p);
             put_away(walk(), u);
             // (every score of the unit is done, so Q's place is free, but for the join of copies)
-            const bool early = copies_of(done.live) == 1;
+            const bool early = copies_of(done.live, done.tiles) == 1;
             if (more && early) fetch_q(u);
             const Smem sm = smem_at(smem_base(smem_raw));
             it0 += done.v1 - done.v0;
@@ -1326,7 +1332,7 @@ __global__ void __launch_bounds__(kPgThreads, kPgMinBlocks)
             tc_fence_after();
             const bool whole = done.v0 == 0 && done.v1 == done.tiles;
             const int slot = 2 * (int)blockIdx.x + (done.v0 == 0);
-            if (copies_of(done.live) == 1)
+            if (copies_of(done.live, done.tiles) == 1)
                 finish_rows<T, 1>(p, sm, tmem, done, whole, slot, e.m, e.l);
             else
                 finish_rows<T, 4>(p, sm, tmem, done, whole, slot, e.m, e.l);
