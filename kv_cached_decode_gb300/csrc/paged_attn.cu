@@ -21,9 +21,10 @@
 //    the unit's last visible position on are not read. The scores of the next tile are issued as
 //    soon as these are in registers. Two blocks per SM: while one waits, the other computes.
 //  * Units of at most 32 vectors (16 in short ones) hold them four times, in lanes 32 apart, and
-//    each copy takes the softmax of a quarter of a tile's positions, with P zero elsewhere: a decoding sequence, with 4
-//    query vectors, uses all four warps. The copies are joined at the unit's end. (Held once,
-//    one row of 8192 takes 2 % longer, 32 rows to 16384 2 %, 8 rows of 5 tokens 5 %.)
+//    each copy takes the softmax of a quarter of a tile's positions, with P zero elsewhere: a
+//    decoding sequence, with 4 query vectors, uses all four warps. The copies are joined at the
+//    unit's end. (Held once, one row of 8192 takes 2 % longer, 32 rows to 16384 2 %, 8 rows of 5
+//    tokens 5 %.)
 //  * Work. The tiles of all units form one list, by weight, and every CTA of one wave takes an
 //    equal stretch of it; units cut by a stretch's end merge through the workspace, the last CTA
 //    to arrive in the order of the list. So neither one long row nor few rows leave SMs idle, and
