@@ -196,7 +196,9 @@ __device__ __forceinline__ float warp_max(float v) {
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
     return d;
 }
-// A thread's running sums: exponents are x c + mc, mc = -m c rounded, and lo what that lacks.
+// A thread's running sums: exponents are x c + mc, mc = -m c rounded, and lo what that lacks. Where
+// |m c| is so large (2^25 on, past fp32, or NaN) that lo may be more than 1, 2^lo may leave fp32. mc
+// is NaN then, which sends every chunk to add_one and its exponents (x - m) c.
 struct Sums {
     Part a;
     float c, mc, lo;
@@ -204,7 +206,10 @@ struct Sums {
         a.m = m;
         mc = -(m * c);
         lo = -fmaf(m, c, mc);
-        if (!(fabsf(lo) < INFINITY)) lo = 0.f;  // (then no exponent by mc is finite)
+        if (!(fabsf(lo) <= 1.f)) {
+            lo = 0.f;
+            mc = __uint_as_float(0x7fffffffu);
+        }
     }
     // lo goes into the sums.
     __device__ __forceinline__ void settle() {
@@ -248,7 +253,7 @@ struct Sums {
             }
             const float2 rs = add2(r[0], r[1]).get(), ts = add2(t[0], t[1]).get();
             const float ent = ts.x + ts.y;
-            if (ent == ent) {  // (a logit of -inf: 0 * -inf is NaN)
+            if (ent == ent) {  // (a logit of -inf: 0 * -inf is NaN; and see mc)
                 a.rest += rs.x + rs.y;
                 a.ent += ent;
                 return;
