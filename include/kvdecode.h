@@ -828,7 +828,8 @@ kvd_status kvd_sample_filtered(const float *logits, int64_t row_stride, int32_t 
  * Device errors: a NaN logit -> KVD_ERR_NAN; a token outside [-1, vocab) -> KVD_ERR_BAD_TOKEN
  * (treated as -1); a temperature out of range -> KVD_ERR_BAD_PARAM, the row's outputs are left as
  * they are; KVD_ERR_TIMEOUT: a bounded wait gave up, the row's outputs are left. No workspace. rows
- * <= 2^31 / 16.
+ * <= 2^31 / 16. Flags: KVD_FLAG_PDL; KVD_FLAG_TEST_STALL: in one of the thread blocks that share a
+ * row (block r modulo their number for row r) the first logits never arrive.
  */
 kvd_status kvd_token_logprobs(kvd_dtype dtype, const void *logits, int64_t row_stride,
                               int32_t rows, int32_t vocab, const float *temperature,

@@ -78,6 +78,7 @@ struct LogprobParams {
     int32_t* top_id;
     float* top_logprob;
     int32_t* dev_err;
+    int32_t test_stall;
 };
 
 // Sums of a part of a row: largest logit (-inf: none), how many have it, the others' weights
@@ -98,12 +99,13 @@ struct __align__(128) LpShared {
     Key ex_key[kLpMaxCluster * KVD_MAX_TOP];
     Part ex_part[kLpMaxCluster];
     int32_t ex_count[kLpMaxCluster][KVD_MAX_GIVEN];
+    int32_t ex_lost[kLpMaxCluster];                 // whether one's wait ran out
     int32_t token[KVD_MAX_GIVEN];
     float value[KVD_MAX_GIVEN];                     // the tokens' logits
     int32_t place[kGroups];
     uint64_t bars[kStages];
     Key bound;
-    int32_t n_list, n_noted;
+    int32_t n_list, n_noted, lost;
 };
 
 // Order-preserving image of a logit (not NaN, -0 as +0) above the complement of the id.
@@ -463,8 +465,12 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN > 4 ? 2 : GIVEN > 1 ? 3 : 4)
         bulk_load(smem_u32(S.ring + g % kStages * kStageBytes),
                   reinterpret_cast<const uint8_t*>(x + body) + at, bytes, bar);
     };
-    if (tid == 0)
+    if (tid == 0) {
+        // test only: 16 bytes more than the first copy brings
+        if (p.test_stall && stages > 0 && rank == row % p.cluster)
+            mbar_expect_tx_only(smem_u32(&S.bars[0]), 16);
         for (int g = 0; g < min(kStages, stages); ++g) copy(g);
+    }
     const float T_ = p.temperature ? p.temperature[row] : 1.f;
     const bool bad_t = !(T_ > 0.f) || !(T_ < INFINITY);
     if (tid < p.given) {
@@ -672,7 +678,7 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN > 4 ? 2 : GIVEN > 1 ? 3 : 4)
     }
 
     // ---- the block's sums and counts ----
-    if (nan) flag_error(p.dev_err, KVD_ERR_NAN);
+    if (nan && !dead) flag_error(p.dev_err, KVD_ERR_NAN);
     if (sum.a.m > -INFINITY) sum.settle();
     Part a = sum.a;
     const float c = sum.c;
@@ -697,8 +703,8 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN > 4 ? 2 : GIVEN > 1 ? 3 : 4)
             if (lane == 0) atomicSub(&S.count[i], n);
         }
     }
-    // (a wait that ran out: the copies in flight land before the block leaves, and it writes
-    // nothing; a cluster's blocks all pass its barriers)
+    // (a wait that ran out: the copies in flight land before the block leaves, and the row is not
+    // written; a cluster's blocks all pass its barriers)
     if (__syncthreads_or(dead)) lost = true;
     if (lost && tid == 0) {
         flag_error(p.dev_err, KVD_ERR_TIMEOUT);
@@ -730,6 +736,7 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN > 4 ? 2 : GIVEN > 1 ? 3 : 4)
             st_cluster_word(&S.ex_part[rank].n, 0, __float_as_uint(a.n));
             st_cluster_word(&S.ex_part[rank].rest, 0, __float_as_uint(a.rest));
             st_cluster_word(&S.ex_part[rank].ent, 0, __float_as_uint(a.ent));
+            st_cluster_word(&S.ex_lost[rank], 0, lost);
         }
         if (GIVEN && tid < p.given)
             st_cluster_word(&S.ex_count[rank][tid], 0, (uint32_t)S.count[tid]);
@@ -737,7 +744,10 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN > 4 ? 2 : GIVEN > 1 ? 3 : 4)
         asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                      "barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (rank != 0) return;
-        if (warp == 0) a = join_few<kLpMaxCluster>(S.ex_part, p.cluster, c);
+        if (warp == 0) {
+            a = join_few<kLpMaxCluster>(S.ex_part, p.cluster, c);
+            lost = __any_sync(0xffffffffu, lane < p.cluster && S.ex_lost[lane]);
+        }
         if (tid == 0) S.n_list = p.cluster * p.top;
         if (GIVEN && tid < p.given) {
             int n = 0;
@@ -755,14 +765,17 @@ __global__ void __launch_bounds__(kLpThreads, GIVEN > 4 ? 2 : GIVEN > 1 ? 3 : 4)
             rank_list(S, p.top, best);
         }
     }
-    if (bad_t || lost) {
+    // ---- the outputs ----
+    __syncthreads();
+    if (tid == 0) {
+        S.part[0] = a;
+        S.lost = lost;
+    }
+    __syncthreads();
+    if (bad_t || S.lost) {
         if (bad_t && tid == 0) flag_error(p.dev_err, KVD_ERR_BAD_PARAM);
         return;
     }
-    // ---- the outputs ----
-    __syncthreads();
-    if (tid == 0) S.part[0] = a;
-    __syncthreads();
     a = S.part[0];
     const bool none = a.m == -INFINITY;
     const float log_s = none ? -INFINITY : a.n == 1.f ? log1pf(a.rest) : logf(a.n + a.rest);
@@ -861,6 +874,7 @@ extern "C" kvd_status kvd_token_logprobs(kvd_dtype dtype, const void* logits, in
     p.top_id = top_id;
     p.top_logprob = top_logprob;
     p.dev_err = dev_err;
+    p.test_stall = (flags & KVD_FLAG_TEST_STALL) ? 1 : 0;
     // split a row while the launch has few blocks and a block keeps a round of logits at least
     int cluster = 1;
     while (2 * cluster <= kLpMaxCluster && (int64_t)rows * cluster * 2 <= kLpManyBlocks &&
