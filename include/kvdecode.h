@@ -674,8 +674,8 @@ kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32
  * Q.K^T and P.V run on the tensor cores with fp32 accumulation. Weights are rounded to the storage
  * type before they meet V, as kvd_window_attn's; their sum is taken before that. What a token does
  * not see does not reach its outputs, whatever the pages hold there, infinities and NaN included.
- * (An infinity in V that it sees makes that output the infinity, or NaN where its weight rounds to
- * 0.)
+ * An infinity in V that it sees makes that output the infinity; where its weight rounds to 0, the
+ * infinity or NaN.
  * The same call gives the same bits on every run; how a row is split depends on the whole batch.
  * Flags: KVD_FLAG_PDL; KVD_FLAG_EARLY_KV gives what KVD_FLAG_PDL gives. KVD_FLAG_TEST_STALL: the
  * first tile of every thread block never completes (the call reports KVD_ERR_TIMEOUT).
