@@ -672,7 +672,8 @@ kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32
  * workspace: kvd_workspace_size(KVD_OP_PAGED_ATTN, batch, n_heads, n_kv_heads, 1, max_new, ..)
  *            bytes, under the rules of the other attention calls
  * Q.K^T and P.V run on the tensor cores with fp32 accumulation. Weights are rounded to the storage
- * type before they meet V, as kvd_window_attn's; their sum is taken before that. What a token does
+ * type before they meet V, as kvd_window_attn's, and their sum is taken before that; KVD_F16 drops
+ * weights below 2^-32 of the largest so far. What a token does
  * not see does not reach its outputs, whatever the pages hold there, infinities and NaN included.
  * An infinity in V that it sees makes that output the infinity; where its weight rounds to 0, the
  * infinity or NaN.

@@ -5,8 +5,8 @@
 // positions; query head hq of token j sees position t <= len - n + j of KV head hq / g:
 //   out[j, hq] = sum_t softmax_t(scale * q[j, hq] . K_t) V_t
 // One pass over the tiles with a running reference m and sum l per query: p_t = 2^(s_t - m),
-// O += p V, l += p; m moves only when a row's maximum exceeds it by more than 2^8 (O and l are then
-// scaled).
+// O += p V, l += p (for binary16 all times 2^7); m moves only when a row's maximum exceeds it by
+// more than 2^8 (O and l are then scaled).
 //
 // Design.
 //  * A unit is one row, KV head and block of up to 128 query vectors: 128 / g tokens times the g
@@ -75,6 +75,13 @@ constexpr uint32_t kPgSmem = (kSlotsK + kSlotsV) * kStepBytes + kPgQBytes + 256 
                              kRowThreads * 16 + kOddWords * 4 + 16 + 1024;
 constexpr int kTable = kPgQBytes / 4;  // entries of the rows' prefix sums, in Q's place at first
 constexpr float kPgGrow = 8.f;  // a row's reference moves for maxima above it by 2^this
+// Weights, sums and outputs are held times 2^this (it cancels in the end). binary16's steps end at
+// 2^-24 and its range at 2^16: with 7, weights reach 2^15 at most, and those down to 2^-32 of the
+// reference's are kept. (With 0 it was 2^-25: 131072 positions of that weight beside one of the
+// reference's lost 0.4 % of the output.) bfloat16 has fp32's range.
+template <typename T>
+constexpr float kPgLift = std::is_same<T, __half>::value ? 7.f : 0.f;
+static_assert(kPgGrow + kPgLift<__half> < 16.f, "binary16's range");
 
 // The list's weights: of a tile, and what a unit costs besides (its start, end and merge).
 // Measured, before the merge took its present form, on one row of 8192 positions (64 tiles x 8
@@ -679,9 +686,9 @@ __device__ __noinline__ RowsEnd run_rows(float scale_log2, uint32_t bars, uint32
                 }
             }
             // the weights, rounded to the storage type; their sum is taken before that (rounding
-            // to nearest leaves no bias)
+            // to nearest leaves no bias, but where binary16 has no values any more: see kPgLift)
             if (!first_tile) p_free = mbar_done(bars + 8 * kBarO, (it - 1) & 1);
-            const float nref = m == -INFINITY ? 0.f : -m;
+            const float nref = m == -INFINITY ? 0.f : kPgLift<T> - m;
             const Pair cs2(scale_log2, scale_log2), ref2(nref, nref);
             Pair sum[4] = {Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f), Pair(0.f, 0.f)};
 #pragma unroll
