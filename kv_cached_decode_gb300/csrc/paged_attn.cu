@@ -769,7 +769,7 @@ __device__ __forceinline__ uint2 pack4(const float4& o, float inv) {
 // sees positions below lim0 + y / group; ml: the copies' sums; to: the partial of a piece, or null.
 // The row threads, behind a barrier; ends before one. (To look through every tile of V before its
 // product, as scan_hidden does, took 2 % more for 32 rows to 16384, 9 % for 8 rows of 5 tokens and
-// 30 % for the mixed batch; this 0 to 1 %, and 3.7 times as long for 32 rows that hold infinities.)
+// 30 % for the mixed batch; this nothing, and 4.2 times as long for 32 rows that hold infinities.)
 template <typename T, int REP>
 __device__ __noinline__ void odd_of_copies(const PagedParams& p, int32_t* odd, const float2* ml,
                                            int b, int h, int live, int lo, int hi, int lim0,
@@ -780,7 +780,7 @@ __device__ __noinline__ void odd_of_copies(const PagedParams& p, int32_t* odd, c
     rows_sync();
     const int32_t* pages = p.table + b * p.table_stride;
     const uint8_t* v = p.v + h * p.v_sh + (tid & 7) * 16;
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 2;
 #pragma unroll 1
     for (int at = lo + (tid >> 3); at < hi; at += kAhead * (kRowThreads / 8)) {
         int page[kAhead];
