@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const PagedApp
     __shared__ uint64_t s_freq[32];
     if (threadIdx.x < 32) s_freq[threadIdx.x] = p.turns.freq[threadIdx.x];
     pdl_wait();
+    const int first = p.starts[0], end = min(p.starts[p.batch], p.n_tokens);
     __syncthreads();
     // lengths after the call, and the rows that do not fit
     for (int64_t b = (int64_t)blockIdx.x * kPaThreads + threadIdx.x; b < p.batch;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kPaThreads) paged_append_kernel(const PagedApp
     const int t = (int)(wid / p.hgroups);
     const uint32_t hg = (uint32_t)(wid % p.hgroups);
     const int lane = threadIdx.x & 31, ch = lane & 7;
-    if (t < p.n_tokens) {  // warp-uniform
+    if (t >= first && t < end) {  // (warp-uniform; tokens of no row are not read)
         // this lane's heads are h0, h0 + 4, ..: those of K, of V and of q
         const int hk = p.hk, h0 = (int)(hg * p.iters) * 4 + (lane >> 3);
         const int last = min(2 * p.hk + p.hq, (int)((hg + 1) * p.iters) * 4);
