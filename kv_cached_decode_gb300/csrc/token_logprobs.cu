@@ -221,14 +221,16 @@ struct Sums {
     }
     __device__ __forceinline__ void raise_to(float m) {
         if (!(m > a.m)) return;
-        if (a.m > -INFINITY) {
-            settle();
-            const float y = (a.m - m) * c, f = exp2f(y), s = a.n + a.rest;
-            a.rest = s * f;
-            a.ent = f > 0.f ? f * fmaf(y, s, a.ent) : 0.f;
-        }
-        a.n = 0.f;
+        settle();
+        // (as add_one: sums by a reference lack its lo; y is -inf where there are none yet)
+        float y = (a.m - m) * c;
+        const float s = a.n + a.rest;
         set_reference(m);
+        y -= lo;
+        const float f = exp2f(y);
+        a.rest = s * f;
+        a.ent = f > 0.f ? f * fmaf(y, s, a.ent) : 0.f;
+        a.n = 0.f;
     }
     __device__ __forceinline__ void add_one(float x) {
         if (x == a.m) {
