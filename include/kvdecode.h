@@ -558,7 +558,8 @@ typedef enum kvd_rope_scaling {
  *   RAMP : s_i = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1), where pair(r) = rot_dim *
  *          ln(N / (2 pi r)) / (2 ln base) turns r times over N positions, a = max(0,
  *          floor(pair(high))), b = min(rot_dim - 1, ceil(pair(low)))
- * Frequencies are formed in 64 bits, angles are exact modulo a turn to position * 2^-53. */
+ * Frequencies are formed in 64 bits; up to a turn per position, angles are exact modulo a turn to
+ * position * 2^-53. */
 typedef struct kvd_rope_spec {
     float base;             /* > 0 (RAMP: > 1)                                            */
     int32_t rot_dim;        /* dims 0 .. rot_dim-1 turn, the others are copied: 16, 32,   */
@@ -673,8 +674,8 @@ kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32
  *            bytes, under the rules of the other attention calls
  * Q.K^T and P.V run on the tensor cores with fp32 accumulation. Weights are rounded to the storage
  * type before they meet V, as kvd_window_attn's, and their sum is taken before that; KVD_F16 drops
- * weights below 2^-32 of the largest so far. What a token does
- * not see does not reach its outputs, whatever the pages hold there, infinities and NaN included.
+ * weights below 2^-32 of the largest so far. What a token does not see does not reach its outputs,
+ * whatever the pages hold there, infinities and NaN included.
  * An infinity in V that it sees makes that output the infinity; where its weight rounds to 0, the
  * infinity or NaN.
  * The same call gives the same bits on every run; how a row is split depends on the whole batch.
@@ -683,9 +684,9 @@ kvd_status kvd_paged_append(kvd_dtype dtype, const kvd_paged_cache *cache, int32
  * Device errors: lens[b] outside [n_b, capacity] or n_b > max_new -> KVD_ERR_LEN_OVERFLOW, the
  * row's outputs are left as they are (all rows' where overlapping stretches of `starts` make more
  * tiles than 32 bits count); KVD_ERR_TIMEOUT: a bounded wait gave up; a page outside [0, n_pages)
- * -> KVD_ERR_BAD_INDEX, its positions count as rows of zeros. KVD_ERR_UNSUPPORTED: more tiles than 32 bits count, with rows
- * as long as the table allows (n_kv_heads * (n_tokens * n_heads / n_kv_heads / 128 + batch) units
- * of up to page_size * table_width / 128 tiles: above about 8e8).
+ * -> KVD_ERR_BAD_INDEX, its positions count as rows of zeros. KVD_ERR_UNSUPPORTED: more tiles than
+ * 32 bits count, with rows as long as the table allows (n_kv_heads * (n_tokens * n_heads /
+ * n_kv_heads / 128 + batch) units of up to page_size * table_width / 128 tiles: above about 8e8).
  */
 kvd_status kvd_paged_attn(kvd_dtype dtype, const kvd_paged_cache *cache, int32_t n_tokens,
                           int32_t max_new, const kvd_token_rows *q, const int32_t *starts,
@@ -823,7 +824,7 @@ kvd_status kvd_sample_filtered(const float *logits, int64_t row_stride, int32_t 
  * entropy, lse : device fp32 [rows] or NULL
  * top_id, top_logprob : device int32 / fp32 [rows, n_top], 0 <= n_top <= KVD_MAX_TOP, or NULL
  * Sums are fp32 relative to the largest logit, whose weight is counted apart, so a log probability
- * near 0 keeps its relative precision. A NaN counts as -inf. With +inf logits those ids alone have
+ * near 0 keeps its relative precision (weights below 2^-126 of the largest count as 0). A NaN counts as -inf. With +inf logits those ids alone have
  * mass. Ids with logit -inf are never listed (slots left over: -1, -inf). A row without any logit
  * above -inf has Z = -inf, entropy 0, logprob -inf. The same bits on every run.
  * Device errors: a NaN logit -> KVD_ERR_NAN; a token outside [-1, vocab) -> KVD_ERR_BAD_TOKEN

@@ -883,9 +883,10 @@ def kvd_paged_attn(q, cache: PagedCache, out, workspace, starts, lens, max_new: 
     T = q.shape[0]
     _check(load_library().kvd_paged_attn(
         _dtype_code(q), _cache_on(cache, dev, q.dtype), T,
-        max(T, 1) if max_new is None else max_new, ctypes.byref(rq), _at(starts, _I32, (B + 1,), "starts", dev),
-        _at(lens, _I32, (B,), "lens", dev), scale, ws, ws_bytes, flags,
-        _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)), "kvd_paged_attn")
+        max(T, 1) if max_new is None else max_new, ctypes.byref(rq),
+        _at(starts, _I32, (B + 1,), "starts", dev), _at(lens, _I32, (B,), "lens", dev), scale, ws,
+        ws_bytes, flags, _at(dev_err, _I32, None, "dev_err", dev), _on(stream, dev)),
+        "kvd_paged_attn")
 
 
 _LOGIT_TYPES = {torch.float16: KVD_F16, torch.bfloat16: KVD_BF16, torch.float32: KVD_F32}

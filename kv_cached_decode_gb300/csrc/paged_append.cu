@@ -8,13 +8,14 @@
 //
 // Design. Rows of 128 bytes are read and written once: HBM bounds prompts, the launch single
 // tokens. A warp takes the heads of one token (or a share of them when tokens are few), four rows
-// at a time, eight lanes a row, so a token's row, page and angles are found once. The row comes
-// from a search over `starts`, 32 probes a step; rows, lengths and pages that do not fit are
-// flagged and skipped.
+// at a time, eight lanes a row, so a token's row, page and angles are found once. Its rows are on
+// their way meanwhile, if some row of the batch holds the token. Which one comes from a search over
+// `starts`, 32 probes a step; rows, lengths and pages that do not fit are flagged and skipped.
 //
 // Measured (in a graph): 64 tokens x 40 heads 3.5 us, a launch and four loads that need one
-// another (row, length, page, rows); 6 rows of up to 2000 tokens x 28 heads 14.2 us, 4.5 TB/s of
-// what is read and written: one wave of warps, so the loads and the stores hardly overlap.
+// another (row, length, page, rows); 6 rows of up to 2000 tokens x 28 heads 16.6 us from cold
+// buffers, 3.9 TB/s of what is read and written (14.3 with buffers that the second-level cache
+// holds in part): one wave of warps, so the loads and the stores hardly overlap.
 #include <algorithm>
 
 #include "kvd_paged.cuh"

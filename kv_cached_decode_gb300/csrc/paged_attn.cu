@@ -14,7 +14,8 @@
 //    run on the fifth-generation tensor cores: S = Q.K^T (M 128, N 128, K 64) and O += P.V
 //    (M 128, N 64, K 128); scores, outputs and P (as the A operand) in tensor memory, Q, K and V in
 //    128-byte-swizzled shared memory. Tiles are 128 positions: with 64, and so twice the hand-offs
-//    between the roles, a chunk of 512 tokens over 16384 took 104 us instead of 98.
+//    between the roles, a chunk of 512 tokens over 16384 took 104 us instead of 98 (measured before
+//    the loop lost its spilled registers, which brought the latter to 73).
 //  * Six warps: four hold the rows (thread t: tensor-memory lane t), one issues the products, one
 //    copies K and V through two and three slots. A page that holds less than a tile is a TMA box of
 //    its own, a lane of the copying warp per page; page numbers are read a tile ahead. Boxes from
@@ -34,10 +35,11 @@
 //
 // Measured (in a graph, caches warm where they fit; a copy runs at 6.8 TB/s, a large product at
 // 1928 TFLOP/s):
-//   1 row x 8192 positions, 32/8 heads         12.1 us   the launch, the list and the merge
-//   32 rows to 16384, 32/8 heads                125 us   6.4 TB/s
+//   1 row x 8192 positions, 32/8 heads         12.3 us   the launch, the list and the merge; 64
+//                                                        tiles: 13.9 at 61, 62 and 63, see kUnit
+//   32 rows to 16384, 32/8 heads                126 us   6.4 TB/s
 //   8 rows x 5 tokens over up to 4095            32 us   4.0 TB/s
-//   a chunk of 512 over 16384, 32/8 heads        73 us   930 TFLOP/s: the row warps' chain of
+//   a chunk of 512 over 16384, 32/8 heads        72 us   940 TFLOP/s: the row warps' chain of
 //                                                        loads, maxima, exponentials and
 //                                                        hand-offs, 2200 cycles a tile
 //   30 rows, two with chunks of 1000 at 8000     98 us   the same
@@ -84,11 +86,13 @@ constexpr float kPgLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 static_assert(kPgGrow + kPgLift<__half> < 16.f, "binary16's range");
 
 // The list's weights: of a tile, and what a unit costs besides (its start, end and merge).
-// Measured, before the merge took its present form, on one row of 8192 positions (64 tiles x 8
-// heads) and on a mixed batch: a unit as 3, 4, 5 and 6 tiles 15.4, 13.6, 15.3, 15.3 us and 101.9,
-// 101.5, 102.3, 103.3; tiles of few vectors lighter by 1/6 than the others 14.2 and 104.2, heavier
-// by 1/5 15.3 and 105.3. A cut at least 20 from a unit's ends: 17.3 us for the row (5: no change);
-// a least share of 15, 25, 30: 15.7, 15.1, 16.7.
+// Measured on one row of 61, 62, 63 and 64 tiles x 8 heads and on a mixed batch: 13.9, 13.9, 13.9,
+// 12.5 us and 98.2 (shares of 20 fit units of 4 n tiles, and no block has more than 4 then; of
+// other units some block has 6). A unit as 3, 5 and 6 tiles instead of 4: 12.7, 13.7, 13.9, 14.2
+// and 98.1; 13.9, 13.9, 12.2, 14.0 and 98.6; 13.8, 13.9, 13.8, 14.1 and 98.8. A cut at least 20
+// from a unit's ends: 15.5, 15.8, 15.7, 16.3 and 98.4; at least 5: 12.7, 12.0, 12.5, 12.5 and 98.2.
+// A least share of 15, 25, 30: 13.9, 13.3, 14.0, 14.5; 13.7, 14.4, 15.1, 13.9; 15.6, 15.6, 16.3,
+// 15.9 (the mixed batch 98.2 with each).
 constexpr uint32_t kWeight = 5, kUnit = 20;
 constexpr int kShort = 2;           // see copies_of
 constexpr uint32_t kSnap = 12;      // no cut this close to a unit's ends

@@ -14,8 +14,9 @@
 // stored. A launch with few tokens spreads a token's heads over several warps.
 //
 // Measured (in a graph): 16 tokens x 24 heads 2.5 us, a launch's time; 4 x 4096 tokens x 24 heads
-// 15.7 us, 6.4 TB/s of what is read and written (a copy: 6.8). Addresses are formed once per token:
-// with all of a row's strides multiplied for each row it was 18.7 us, bound by instructions.
+// 18.3 us from cold buffers, 5.5 TB/s of what is read and written (a copy: 6.8), 15.6 with buffers
+// that the second-level cache holds in part. Addresses are formed once per token: with all of a
+// row's strides multiplied for each row the latter was 18.7 us, bound by instructions.
 #include <cmath>
 #include <cstring>
 

@@ -19,7 +19,7 @@ def _gpu():
 
 
 def sink(rows, hq, hk, dtype, at, score):
-    """Position `at` of every row has this score, the others 0; V is 0 there and near 1 elsewhere."""
+    """Position `at` of every row has this score, the others 0; V is 0 there, near 1 elsewhere."""
     b = Batch(rows, hq, hk, 64, dtype, seed=1)
     b.q.fill_(1.0)
     for row, (_, length) in enumerate(rows):
@@ -36,9 +36,9 @@ def sink(rows, hq, hk, dtype, at, score):
 @pytest.mark.parametrize("rows,at", [([(1, 131072)], 0), ([(1, 100000), (40, 30000)], 3),
                                      ([(30, 65536)], 40000), ([(5, 20000), (1, 777)], 700)])
 def test_a_long_rest_keeps_its_weight(rows, at, score, dtype):
-    """A weight of 2^(s - m) is held in 16 bits. binary16 has steps of 2^-24 at its lower end, so half
-    a step is lost of 2^7 times the weight at most: 2^-32 of the reference's. (That is the bound's
-    absolute term, 2^-25 of the form's `low` less 7 bits.)"""
+    """A weight of 2^(s - m) is held in 16 bits. binary16 has steps of 2^-24 at its lower end, so
+    half a step is lost of 2^7 times the weight at most: 2^-32 of the reference's. (That is the
+    bound's absolute term, 2^-25 of the form's `low` less 7 bits.)"""
     b = sink(rows, 4, 1, dtype, at, score)
     out = b.attend()
     table = b.table.cpu()
