@@ -773,8 +773,8 @@ __device__ __forceinline__ uint2 pack4(const float4& o, float inv) {
 // sees positions below lim0 + y / group; ml: the copies' sums; to: the partial of a piece, or null.
 // The row threads, behind a barrier; ends before one. (To look through every tile of V before its
 // product, as scan_hidden does, took 2 % more for 32 rows to 16384, 9 % for 8 rows of 5 tokens and
-// 30 % for the mixed batch; this nothing, and 4.2 times as long for 32 rows that hold infinities.)
-// The copying and the MMA warp wait meanwhile, for a second at most; it takes 40 ns a position, and a
+// 30 % for the mixed batch; this nothing, and 4.2 times as long for 32 rows with infinities.) The
+// copying and the MMA warp wait meanwhile, for a second at most; it takes 40 ns a position, and a
 // pool of 280 GB gives a block pieces of 4 million positions.
 template <typename T, int REP>
 __device__ __noinline__ void odd_of_copies(const PagedParams& p, int32_t* odd, const float2* ml,
